@@ -19,10 +19,12 @@ from . import _build
 
 F32, BF16 = 0, 1
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_SCRATCH_LIMIT = 0, 1, 2, 3, 4
-DEV_ERR_SLOT_OOB, DEV_ERR_TIMEOUT, DEV_ERR_SEQLENS = 1, 2, 4
+DEV_ERR_SLOT_OOB, DEV_ERR_TIMEOUT, DEV_ERR_SEQLENS, DEV_ERR_BLOCKS = 1, 2, 4, 8
+SCALE_F32, SCALE_E8M0 = 0, 1
 (K_DECODE, K_SPEC_VERIFY, K_SLOT_COPY, K_SLOT_ZERO, K_SPEC_COMMIT, K_PREFILL, K_COMMIT_INDEX,
- K_STATE_PACK, K_GATED_RMSNORM, K_KDA_DECODE, K_KDA_VERIFY, K_KDA_PREFILL, K_MIXED) = range(13)
-K_COUNT = 13
+ K_STATE_PACK, K_GATED_RMSNORM, K_KDA_DECODE, K_KDA_VERIFY, K_KDA_PREFILL, K_MIXED, K_SSM_DECODE,
+ K_SSM_PREFILL, K_ADD_RMSNORM, K_BATCH_MAPS) = range(17)
+K_COUNT = 17
 
 _DT_CODE = {torch.float32: F32, torch.bfloat16: BF16}
 
@@ -52,11 +54,17 @@ class CParams(ctypes.Structure):
                 ("dt_bias", ctypes.c_void_p)]
 
 
+class CSsmParams(ctypes.Structure):
+    _fields_ = [("conv_w", ctypes.c_void_p), ("conv_bias", ctypes.c_void_p), ("A_log", ctypes.c_void_p),
+                ("dt_bias", ctypes.c_void_p), ("D", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 _PD = ctypes.POINTER(CDims)
 _PP = ctypes.POINTER(CParams)
+_PS = ctypes.POINTER(CSsmParams)
 
 EXPORTS = {
     "gdn_decode_step": ([_PD, CPool, _PP, _P, _I32, _P, _P, _P, _P, _P, _P], _I32),
@@ -82,6 +90,13 @@ EXPORTS = {
     "gdn_state_pack": ([_PD, CPool, _P, _I32, _P, ctypes.c_size_t, _P, _P], _I32),
     "gdn_state_unpack": ([_PD, _P, ctypes.c_size_t, CPool, _P, _I32, _P, _P], _I32),
     "gdn_gated_rmsnorm": ([_PD, _P, _P, _P, ctypes.c_float, _I64, _P, _P], _I32),
+    "gdn_ssm_decode_step": ([_PD, CPool, _PS, _P, _I32, _P, _P, _P, _P, _P], _I32),
+    "gdn_ssm_prefill_workspace_size": ([_PD, _I32, _I64], ctypes.c_size_t),
+    "gdn_ssm_prefill": ([_PD, CPool, CPool, _PS, _P, _P, _P, _I32, _I64, _P, _I32, _I32, _P, _P, _P, _P,
+                         ctypes.c_size_t, _P, _P], _I32),
+    "gdn_add_rmsnorm": ([_I32, _I32, _P, _P, _P, ctypes.c_float, _I64, _I32, _P, _P, _P, _I32, _I32, _P], _I32),
+    "gdn_batch_maps": ([_P, _P, _I32, _I32, _P, _I32, _P, _I32, _P, _P, _P, _P, _I32, _P, _P, _P, _I64, _P, _P],
+                       _I32),
     "gdn_selftest_wait_timeout": ([_P, _P], _I32),
     "gdn_status_string": ([_I32], ctypes.c_char_p),
     "gdn_launch_count": ([_I32], ctypes.c_uint64),
@@ -239,6 +254,48 @@ class LayerParams:
             cached = (key, CParams(*key))
             self.__dict__["_c"] = cached
         return cached[1]
+
+
+@dataclass
+class SsmParams:
+    """Parameters of a selective state space layer (fp32); conv_bias and D may be None."""
+
+    conv_w: torch.Tensor             # [C][W]
+    conv_bias: torch.Tensor | None   # [C]
+    A_log: torch.Tensor              # [HV]
+    dt_bias: torch.Tensor            # [HV]
+    D: torch.Tensor | None           # [HV]
+
+    def c(self) -> CSsmParams:
+        key = (self.conv_w.data_ptr(), _ptr(self.conv_bias), self.A_log.data_ptr(), self.dt_bias.data_ptr(),
+               _ptr(self.D))
+        cached = self.__dict__.get("_c")
+        if cached is None or cached[0] != key:
+            cached = (key, CSsmParams(*key))
+            self.__dict__["_c"] = cached
+        return cached[1]
+
+
+def _require(fn: str, what: str, t, dtype, shape):
+    """Raise unless t is a contiguous tensor of the dtype and shape on the current device."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise GdnError(fn, ERR_INVALID_ARG, f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                                            f"got {t.dtype} {tuple(t.shape)}, strides {t.stride()}")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise GdnError(fn, ERR_INVALID_ARG, f"{what} is on {t.device}, not on the current CUDA device")
+
+
+def _require_ssm(fn: str, dims: Dims, pool: StatePool, params: SsmParams):
+    C, W, hv = dims.channels, dims.conv_width, dims.hv
+    _require(fn, "pool.ssm", pool.ssm, torch.float32, (pool.num_slots, hv, dims.dv, dims.dk))
+    _require(fn, "pool.conv", pool.conv, dims.conv_dtype, (pool.num_slots, W - 1, C))
+    _require(fn, "conv_w", params.conv_w, torch.float32, (C, W))
+    _require(fn, "A_log", params.A_log, torch.float32, (hv,))
+    _require(fn, "dt_bias", params.dt_bias, torch.float32, (hv,))
+    if params.conv_bias is not None:
+        _require(fn, "conv_bias", params.conv_bias, torch.float32, (C,))
+    if params.D is not None:
+        _require(fn, "D", params.D, torch.float32, (hv,))
 
 
 # ---------------------------------------------------------------- entry points
@@ -481,6 +538,131 @@ def gated_rmsnorm(dims: Dims, o, z, weight, eps: float = 1e-6, y=None, stream=No
                              int(o.shape[0]), _ptr(y), _stream(stream))
     _check("gdn_gated_rmsnorm", st)
     return y
+
+
+def ssm_decode_step(dims: Dims, pool: StatePool, params: SsmParams, slot_ids, qkv, a, out, dev_err=None,
+                    stream=None):
+    """Selective state space decode: one token per request, state and conv
+    history updated in place; qkv [B][C] ordered q | k | v (the family's C, B,
+    x), a [B][hv] time-step logits, out [B][hv][dv]."""
+    fn, L = "gdn_ssm_decode_step", load()
+    B = int(slot_ids.shape[0])
+    _require_ssm(fn, dims, pool, params)
+    _require(fn, "slot_ids", slot_ids, torch.int32, (B,))
+    _require(fn, "qkv", qkv, dims.act_dtype, (B, dims.channels))
+    _require(fn, "a", a, dims.act_dtype, (B, dims.hv))
+    _require(fn, "out", out, dims.act_dtype, (B, dims.hv, dims.dv))
+    cd, cp = dims.c(), params.c()
+    st = L.gdn_ssm_decode_step(ctypes.byref(cd), pool.c(), ctypes.byref(cp), _ptr(slot_ids), B, _ptr(qkv), _ptr(a),
+                               _ptr(out), _ptr(dev_err), _stream(stream))
+    _check(fn, st)
+
+
+def ssm_prefill_workspace_size(dims: Dims, n_seq: int, total_tokens: int) -> int:
+    cd = dims.c()
+    return int(load().gdn_ssm_prefill_workspace_size(ctypes.byref(cd), int(n_seq), int(total_tokens)))
+
+
+def ssm_prefill(dims: Dims, pool: StatePool, ckpt: StatePool | None, params: SsmParams, slot_ids, cu_seqlens,
+                start_pos, total_tokens: int, ckpt_ids, ckpt_block: int, qkv, a, out, workspace, dev_err=None,
+                stream=None):
+    """Selective state space prefill: chunk_prefill's contract with every token
+    the step of ssm_decode_step.  ckpt and ckpt_ids may be None (no
+    checkpoints); workspace: ssm_prefill_workspace_size bytes."""
+    fn, L = "gdn_ssm_prefill", load()
+    n_seq, total = int(slot_ids.shape[0]), int(total_tokens)
+    max_ckpt = int(ckpt_ids.shape[1]) if ckpt_ids is not None and ckpt_ids.dim() == 2 else 0
+    _require_ssm(fn, dims, pool, params)
+    if max_ckpt:
+        if ckpt is None:
+            raise GdnError(fn, ERR_INVALID_ARG, "ckpt_ids without a checkpoint pool")
+        _require(fn, "ckpt.ssm", ckpt.ssm, torch.float32, (ckpt.num_slots, dims.hv, dims.dv, dims.dk))
+        _require(fn, "ckpt.conv", ckpt.conv, dims.conv_dtype, (ckpt.num_slots, dims.conv_width - 1, dims.channels))
+        _require(fn, "ckpt_ids", ckpt_ids, torch.int32, (n_seq, max_ckpt))
+    _require(fn, "slot_ids", slot_ids, torch.int32, (n_seq,))
+    _require(fn, "cu_seqlens", cu_seqlens, torch.int32, (n_seq + 1,))
+    _require(fn, "start_pos", start_pos, torch.int64, (n_seq,))
+    _require(fn, "qkv", qkv, dims.act_dtype, (total, dims.channels))
+    _require(fn, "a", a, dims.act_dtype, (total, dims.hv))
+    _require(fn, "out", out, dims.act_dtype, (total, dims.hv, dims.dv))
+    if workspace is not None:
+        _require(fn, "workspace", workspace, workspace.dtype, workspace.shape)
+    cd, cp = dims.c(), params.c()
+    ck = ckpt.c() if ckpt is not None else CPool(None, None, 0)
+    st = L.gdn_ssm_prefill(ctypes.byref(cd), pool.c(), ck, ctypes.byref(cp), _ptr(slot_ids), _ptr(cu_seqlens),
+                           _ptr(start_pos), n_seq, total, _ptr(ckpt_ids) if max_ckpt else None, max_ckpt,
+                           int(ckpt_block), _ptr(qkv), _ptr(a), _ptr(out), _ptr(workspace),
+                           _nbytes(workspace) if workspace is not None else 0, _ptr(dev_err), _stream(stream))
+    _check(fn, st)
+
+
+def add_rmsnorm(x, residual, weight, eps: float = 1e-6, y=None, q8=None, scales=None, group: int = 0, stream=None):
+    """h = x + residual (residual updated in place, or None), y = RMS norm of
+    the rows of h times weight, into y (x's dtype) and/or q8 (float8_e4m3fn)
+    with scales [rows][d / group] (float32, or uint8 / float8_e8m0fnu for
+    power-of-two scales; group 0: one per row).  Returns (y, q8, scales); y is
+    created when neither y nor q8 is given."""
+    fn, L = "gdn_add_rmsnorm", load()
+    if x.dtype not in _DT_CODE or x.dim() < 1 or (residual is not None and residual.dtype not in _DT_CODE):
+        raise GdnError(fn, ERR_INVALID_ARG, "x and residual must be float32 or bfloat16")
+    shape, d = tuple(x.shape), int(x.shape[-1])
+    rows = x.numel() // d if d else 0
+    _require(fn, "x", x, x.dtype, shape)
+    if residual is not None:
+        _require(fn, "residual", residual, residual.dtype, shape)
+    _require(fn, "weight", weight, torch.float32, (d,))
+    if y is None and q8 is None:
+        y = torch.empty_like(x)
+    if y is not None:
+        _require(fn, "y", y, x.dtype, shape)
+    scale_type = SCALE_F32
+    if q8 is not None:
+        if group < 0 or (group and d % group):
+            raise GdnError(fn, ERR_INVALID_ARG, f"group {group} does not divide {d}")
+        _require(fn, "q8", q8, torch.float8_e4m3fn, shape)
+        if scales is None:
+            scales = torch.empty(shape[:-1] + (d // (group or d),), dtype=torch.float32, device=x.device)
+        if scales.dtype != torch.float32:
+            scale_type = SCALE_E8M0
+            if scales.dtype not in (torch.uint8, torch.float8_e8m0fnu):
+                raise GdnError(fn, ERR_INVALID_ARG, f"scales of {scales.dtype}")
+        _require(fn, "scales", scales, scales.dtype, shape[:-1] + (d // (group or d),))
+    st = L.gdn_add_rmsnorm(_DT_CODE[x.dtype], _DT_CODE[residual.dtype] if residual is not None else _DT_CODE[x.dtype],
+                           _ptr(x), _ptr(residual), _ptr(weight), float(eps), rows, d, _ptr(y), _ptr(q8),
+                           _ptr(scales), int(group), scale_type, _stream(stream))
+    _check(fn, st)
+    return y, q8, scales
+
+
+def batch_maps(new_lens, start_pos, block: int, block_table, free_ids, n_free, cu_seqlens, ckpt_ids=None,
+               seq_ids=None, positions=None, slot_map=None, n_free_out=None, dev_err=None, stream=None):
+    """Packed offsets, block tables, checkpoint table and per-row maps of a
+    batch from its lengths, on the device (see gdn_batch_maps).  n_free [1]
+    is updated in place unless n_free_out is given; seq_ids, positions and
+    slot_map (all of one length, the rows' capacity) may be None."""
+    fn, L = "gdn_batch_maps", load()
+    n_seq = int(new_lens.shape[0])
+    i32, i64 = torch.int32, torch.int64
+    rows = next((int(t.shape[0]) for t in (seq_ids, positions, slot_map) if t is not None), 2**31 - 1)
+    if n_free_out is None:
+        n_free_out = n_free
+    for what, t, dt, shape in (("new_lens", new_lens, i32, (n_seq,)), ("start_pos", start_pos, i64, (n_seq,)),
+                               ("block_table", block_table, i32, (n_seq, block_table.shape[-1])),
+                               ("free_ids", free_ids, i32, (free_ids.numel(),)), ("n_free", n_free, i32, (1,)),
+                               ("n_free_out", n_free_out, i32, (1,)), ("cu_seqlens", cu_seqlens, i32, (n_seq + 1,))):
+        _require(fn, what, t, dt, shape)
+    max_ckpt = 0
+    if ckpt_ids is not None:
+        max_ckpt = int(ckpt_ids.shape[-1])
+        _require(fn, "ckpt_ids", ckpt_ids, i32, (n_seq, max_ckpt))
+    for what, t, dt in (("seq_ids", seq_ids, i32), ("positions", positions, i64), ("slot_map", slot_map, i64)):
+        if t is not None:
+            _require(fn, what, t, dt, (rows,))
+    st = L.gdn_batch_maps(_ptr(new_lens), _ptr(start_pos), n_seq, int(block), _ptr(block_table),
+                          int(block_table.shape[-1]), _ptr(free_ids), free_ids.numel(), _ptr(n_free),
+                          _ptr(n_free_out), _ptr(cu_seqlens), _ptr(ckpt_ids), max_ckpt, _ptr(seq_ids),
+                          _ptr(positions), _ptr(slot_map), rows, _ptr(dev_err), _stream(stream))
+    _check(fn, st)
 
 
 def launch_count(kernel: int) -> int:

@@ -1,0 +1,223 @@
+// Maps of a packed batch built on the device from the requests' lengths
+// (TokenSpeed Qwen3.5 page, "Scheduler dual" and "Ciclo de vida de slots"):
+// packed offsets, block tables filled from a free list, checkpoint tables and
+// per-row maps, so that a step whose lengths are known only on the device
+// (accepted drafts) needs no host round trip.
+//
+// Latency bound: a few KB in and 20 bytes per row out.  One launch of one
+// cluster.  Every CTA scans all lengths itself (at most 8192, in shared
+// memory), so no CTA waits for another's results: an entry of a new block is
+// recomputed from the scan wherever it is needed instead of being read back
+// from the table.  The rows are spread over the cluster's threads, each
+// finding its request by a binary search in the offsets.  The cluster
+// barrier stands only between the last read of *n_free and its update, which
+// may be in place.
+#include "gdn_common.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kCluster = 8;   // CTAs
+constexpr int kMaxSeq = 8192;
+
+struct MapsArgs {
+  const int32_t* new_lens;
+  const int64_t* start_pos;
+  int32_t n_seq, shift;  // block = 1 << shift
+  int32_t* block_table;
+  int32_t max_blocks;
+  const int32_t* free_ids;
+  int32_t free_cap;
+  const int32_t* n_free;
+  int32_t* n_free_out;
+  int32_t* cu_seqlens;
+  int32_t* ckpt_ids;
+  int32_t max_ckpt;
+  int32_t* seq_ids;
+  int64_t* positions;
+  int64_t* slot_map;
+  int64_t max_tokens;
+  uint32_t* err;
+};
+
+// inclusive scan of one value per thread; `total` is the CTA's sum
+__device__ __forceinline__ int64_t scan_cta(int64_t v, int64_t* warp_sums, int64_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  if (lane == 31) warp_sums[warp] = v;
+  __syncthreads();
+  int64_t s = warp_sums[lane];  // kWarps == 32
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += u;
+  }
+  const int64_t before = warp ? __shfl_sync(0xffffffffu, s, warp - 1) : 0;
+  total = __shfl_sync(0xffffffffu, s, 31);
+  __syncthreads();  // warp_sums may be written again
+  return v + before;
+}
+static_assert(kWarps == 32, "scan_cta reads one warp sum per lane");
+
+__global__ void __launch_bounds__(kThreads) batch_maps_kernel(const MapsArgs a) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  __shared__ int64_t warp_sums[kWarps];
+  const auto s_cu = GDN_SV(reinterpret_cast<int32_t*>(smem_raw), a.n_seq + 1);           // offsets
+  const auto s_base = GDN_SV(reinterpret_cast<int32_t*>(smem_raw) + a.n_seq + 1, a.n_seq);  // new blocks before
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, rank = (int)cluster_ctarank();
+  const auto new_lens = GDN_GV(a.new_lens, a.n_seq);
+  const auto start_pos = GDN_GV(a.start_pos, a.n_seq);
+  const auto table = GDN_GV(a.block_table, (long long)a.n_seq * a.max_blocks);
+  const auto free_ids = GDN_GV(a.free_ids, a.free_cap);
+  const auto cu = GDN_GV(a.cu_seqlens, a.n_seq + 1);
+  const int64_t blk = (int64_t)1 << a.shift;
+  int64_t n_free = *a.n_free;
+  n_free = n_free < 0 ? 0 : n_free > a.free_cap ? a.free_cap : n_free;
+  uint32_t bad = 0;
+  // offsets and new blocks, kThreads requests at a time
+  int64_t carry_t = 0, carry_b = 0;
+  for (int r0 = 0; r0 < a.n_seq; r0 += kThreads) {
+    const int r = r0 + tid;
+    int64_t len = 0, p0 = 0;
+    if (r < a.n_seq) {
+      len = new_lens[r];
+      p0 = start_pos[r];
+      if (p0 < 0 || len < 0 || p0 > ((int64_t)a.max_blocks << a.shift) - len) {
+        bad |= GDN_DEV_ERR_SEQLENS;
+        len = 0;
+        p0 = 0;
+      }
+    }
+    int64_t total;
+    int64_t end = carry_t + scan_cta(len, warp_sums, total);
+    int64_t begin = end - len;
+    if (end > a.max_tokens) {
+      bad |= GDN_DEV_ERR_SEQLENS;
+      end = a.max_tokens;
+      begin = begin < end ? begin : end;
+    }
+    carry_t += total;
+    const int64_t nb = (p0 + (end - begin) + blk - 1) / blk - (p0 + blk - 1) / blk;
+    int64_t total_b;
+    const int64_t after = carry_b + scan_cta(nb, warp_sums, total_b);
+    carry_b += total_b;
+    if (r < a.n_seq) {
+      s_cu[r] = (int32_t)begin;
+      s_base[r] = (int32_t)min(after - nb, (int64_t)0x7fffffff);  // past any free list
+      if (r == a.n_seq - 1) s_cu[a.n_seq] = (int32_t)end;
+    }
+  }
+  if (a.n_seq == 0 && tid == 0) s_cu[0] = 0;
+  __syncthreads();
+  const int gt = rank * kThreads + tid, gn = kCluster * kThreads;
+  // the id of new block j (0-based among this step's), -1: none left
+  auto fresh = [&](int64_t j) -> int32_t { return j < n_free ? free_ids[n_free - 1 - j] : -1; };
+  for (int r = gt; r < a.n_seq + 1; r += gn) cu[r] = s_cu[r];
+  // table entries of the new blocks and the checkpoints, one warp per request
+  for (int r = gt >> 5; r < a.n_seq; r += gn >> 5) {
+    const int lane = tid & 31;
+    const int64_t len = s_cu[r + 1] - s_cu[r];
+    int64_t p0 = start_pos[r];
+    if (p0 < 0 || p0 > ((int64_t)a.max_blocks << a.shift)) p0 = 0;  // a request that counts as 0 tokens
+    const int64_t have = (p0 + blk - 1) >> a.shift, need = (p0 + len + blk - 1) >> a.shift;
+    const int64_t base = s_base[r];
+    for (int64_t i = have + lane; i < need; i += 32) {
+      const int32_t id = fresh(base + i - have);
+      if (id < 0) bad |= GDN_DEV_ERR_BLOCKS;
+      table[(size_t)r * a.max_blocks + i] = id;
+    }
+    const int64_t first = p0 >> a.shift, done = (p0 + len) >> a.shift;  // blocks completed: first .. done - 1
+    for (int64_t k = lane; k < a.max_ckpt; k += 32) {
+      const int64_t i = first + k;
+      int32_t id = -1;
+      if (i < done && len > 0) id = i >= have ? fresh(base + i - have) : table[(size_t)r * a.max_blocks + i];
+      GDN_GV(a.ckpt_ids, (long long)a.n_seq * a.max_ckpt)[(size_t)r * a.max_ckpt + k] = id < 0 ? -1 : id;
+    }
+  }
+  // the packed rows
+  if (a.seq_ids || a.positions || a.slot_map) {
+    const int64_t rows = s_cu[a.n_seq];
+    for (int64_t t = gt; t < a.max_tokens; t += gn) {
+      int32_t seq = -1;
+      int64_t pos = 0, slot = -1;
+      if (t < rows) {
+        int lo = 0, hi = a.n_seq;  // the last request whose offset is <= t
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (s_cu[mid] <= t) lo = mid; else hi = mid;
+        }
+        seq = lo;
+        const int64_t p0 = start_pos[lo];
+        pos = p0 + (t - s_cu[lo]);
+        if (a.slot_map) {
+          const int64_t have = (p0 + blk - 1) >> a.shift, i = pos >> a.shift;
+          const int32_t id = i >= have ? fresh(s_base[lo] + i - have) : table[(size_t)lo * a.max_blocks + i];
+          if (id < 0) bad |= i >= have ? GDN_DEV_ERR_BLOCKS : GDN_DEV_ERR_SLOT_OOB;
+          else slot = ((int64_t)id << a.shift) + (pos & (blk - 1));
+        }
+      }
+      if (a.seq_ids) GDN_GV(a.seq_ids, a.max_tokens)[t] = seq;
+      if (a.positions) GDN_GV(a.positions, a.max_tokens)[t] = pos;
+      if (a.slot_map) GDN_GV(a.slot_map, a.max_tokens)[t] = slot;
+    }
+  }
+  if (bad) report(a.err, bad);
+  // every CTA has read *n_free: it may be replaced
+  cluster_arrive_release();
+  cluster_wait_acquire();
+  if (gt == 0) *a.n_free_out = (int32_t)(n_free > carry_b ? n_free - carry_b : 0);
+}
+
+}  // namespace
+}  // namespace gdn
+
+extern "C" gdn_status gdn_batch_maps(const int32_t* new_lens, const int64_t* start_pos, int32_t n_seq, int32_t block,
+                                     int32_t* block_table, int32_t max_blocks, const int32_t* free_ids,
+                                     int32_t free_cap, const int32_t* n_free, int32_t* n_free_out,
+                                     int32_t* cu_seqlens, int32_t* ckpt_ids, int32_t max_ckpt, int32_t* seq_ids,
+                                     int64_t* positions, int64_t* slot_map, int64_t max_tokens, uint32_t* dev_err,
+                                     void* stream) {
+  using namespace gdn;
+  if (n_seq < 0 || max_blocks < 0 || free_cap < 0 || max_ckpt < 0 || max_tokens < 0) return GDN_ERR_INVALID_ARG;
+  if (block <= 0 || (block & (block - 1))) return GDN_ERR_INVALID_ARG;
+  if (!n_free || !n_free_out || !cu_seqlens || (free_cap > 0 && !free_ids)) return GDN_ERR_INVALID_ARG;
+  if (n_seq > 0 && (!new_lens || !start_pos || (max_blocks > 0 && !block_table) || (max_ckpt > 0 && !ckpt_ids)))
+    return GDN_ERR_INVALID_ARG;
+  if (n_seq > kMaxSeq || max_tokens > 2147483647LL) return GDN_ERR_UNSUPPORTED;
+  MapsArgs m = {};
+  m.new_lens = new_lens;
+  m.start_pos = start_pos;
+  m.n_seq = n_seq;
+  while ((1 << m.shift) < block) ++m.shift;
+  m.block_table = block_table;
+  m.max_blocks = max_blocks;
+  m.free_ids = free_ids;
+  m.free_cap = free_cap;
+  m.n_free = n_free;
+  m.n_free_out = n_free_out;
+  m.cu_seqlens = cu_seqlens;
+  m.ckpt_ids = ckpt_ids;
+  m.max_ckpt = max_ckpt;
+  m.seq_ids = seq_ids;
+  m.positions = positions;
+  m.slot_map = slot_map;
+  m.max_tokens = max_tokens;
+  m.err = dev_err;
+  const size_t smem = (2 * (size_t)n_seq + 1) * sizeof(int32_t);
+  cudaError_t e = cudaFuncSetAttribute(batch_maps_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (2 * kMaxSeq + 1) * (int)sizeof(int32_t));
+  if (e == cudaSuccess)
+    e = launch_pdl(batch_maps_kernel, dim3(kCluster), dim3(kThreads), smem, reinterpret_cast<cudaStream_t>(stream),
+                   dim3(kCluster), m);
+  if (e != cudaSuccess) return GDN_ERR_CUDA;
+  count_launch(GDN_K_BATCH_MAPS);
+  return GDN_OK;
+}

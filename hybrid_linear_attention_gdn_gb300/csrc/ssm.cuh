@@ -1,0 +1,48 @@
+// Selective state space step: pieces shared by its kernels.
+#pragma once
+#include "gdn_common.cuh"
+
+namespace gdn {
+namespace ssm {
+
+constexpr int kMaxW = 8;
+
+// dt = softplus(a + dt_bias) and the log decay -exp(A_log) dt of a token
+struct Gate {
+  float dt, g;
+};
+__device__ __forceinline__ Gate gate(float A_log, float dt_bias, float a) {
+  Gate r;
+  r.dt = softplus_f(a + dt_bias);
+  r.g = -expf(A_log) * r.dt;
+  return r;
+}
+
+struct PrefillArgs {
+  float* ssm;
+  const void* conv;
+  int32_t num_slots;
+  float* ck_ssm;
+  int32_t ck_num_slots;
+  const float* conv_w;
+  const float* conv_bias;
+  const float* A_log;
+  const float* dt_bias;
+  const float* D;
+  const int32_t* slot_ids;
+  const int32_t* cu_seqlens;
+  const int64_t* start_pos;
+  int32_t n_seq;
+  int64_t total;
+  const int32_t* ckpt_ids;
+  int32_t max_ckpt;
+  int32_t ckpt_block;
+  const void* qkv;
+  const void* a;
+  void* out;
+  uint32_t* err;
+  int32_t hk, hv, dk, dv, W, C, G;
+};
+
+}  // namespace ssm
+}  // namespace gdn

@@ -68,6 +68,7 @@ typedef enum {
 #define GDN_DEV_ERR_SLOT_OOB 1u /* a slot id (or accept length) out of range   */
 #define GDN_DEV_ERR_TIMEOUT 2u  /* a bounded inter-CTA wait gave up            */
 #define GDN_DEV_ERR_SEQLENS 4u  /* prefill: cu_seqlens / start_pos inconsistent */
+#define GDN_DEV_ERR_BLOCKS 8u   /* batch maps: the free list ran out           */
 
 typedef struct {
   int32_t hk;         /* QK heads                                   */
@@ -398,6 +399,129 @@ gdn_status gdn_gated_rmsnorm(const gdn_dims* dims, const void* o, const void* z,
                              void* stream);
 
 /*
+ * Selective state space layers.  The pages name the family only (TokenSpeed
+ * Qwen3.5 page, "Prefix cache para arquitecturas GDN/Mamba"); the step is the
+ * published selective state space recurrence with one decay per head (Gu &
+ * Dao, "Mamba", 2023; Dao & Gu, "Transformers are SSMs", ICML 2024) over the
+ * same slot pool, conv history and head layout as gdn_decode_step:
+ *   y = SiLU(conv1d(history, x) + conv_bias);  q,k,v = split(y)
+ *   dt = softplus(a + dt_bias);  alpha = exp(-exp(A_log) * dt)
+ *   S <- alpha S + dt k v^T;  o = S^T q + D v          (updated S)
+ * In that family's words q is C, k is B, v is x, hk the groups, dk the state
+ * size and dv the head size.  q and k are not normalised or scaled.  Slots
+ * are those of every other call: gdn_slot_copy, gdn_slot_zero,
+ * gdn_state_pack and gdn_state_unpack apply unchanged.
+ */
+typedef struct {
+  const float* conv_w;    /* [C][conv_width]             */
+  const float* conv_bias; /* [C], NULL: no bias          */
+  const float* A_log;     /* [hv]                        */
+  const float* dt_bias;   /* [hv]                        */
+  const float* D;         /* [hv], NULL: no skip term    */
+} gdn_ssm_params;
+
+/*
+ * State space decode: one token per request, the state and conv history
+ * updated in place in the working slot.  Arguments as for gdn_decode_step
+ * (slot_ids distinct; a [B][hv] holds the time-step logits) without b.
+ * hv / hk * dv above 8192 returns GDN_ERR_UNSUPPORTED.  B = 0 is a no-op.
+ */
+gdn_status gdn_ssm_decode_step(const gdn_dims* dims, gdn_pool pool, const gdn_ssm_params* params,
+                               const int32_t* slot_ids, int32_t B, const void* qkv, const void* a,
+                               void* out, uint32_t* dev_err, void* stream);
+
+/*
+ * State space prefill: the contract of gdn_chunk_prefill (packed sequences
+ * from any start position, block-aligned checkpoints of SSM state and conv
+ * history, final state into the working slot, rows outside the sequences not
+ * written) with every token the step above.  fp32 accuracy of states and
+ * checkpoints.  A zero decay (a = +inf gives dt = +inf) is not finite here:
+ * the state takes dt k v^T as it is.
+ *   workspace: >= gdn_ssm_prefill_workspace_size(...) bytes, 256-aligned
+ *   (may be NULL where that is 0); nothing in it needs to be zero, and
+ *   nothing is kept in it between calls.
+ */
+size_t gdn_ssm_prefill_workspace_size(const gdn_dims* dims, int32_t n_seq, int64_t total_tokens);
+gdn_status gdn_ssm_prefill(const gdn_dims* dims, gdn_pool pool, gdn_pool ckpt,
+                           const gdn_ssm_params* params, const int32_t* slot_ids,
+                           const int32_t* cu_seqlens, const int64_t* start_pos, int32_t n_seq,
+                           int64_t total_tokens, const int32_t* ckpt_ids, int32_t max_ckpt,
+                           int32_t ckpt_block, const void* qkv, const void* a, void* out,
+                           void* workspace, size_t workspace_bytes, uint32_t* dev_err, void* stream);
+
+/*
+ * Residual addition and RMS norm between the layers, with an 8-bit output
+ * for the next projection.  Not written on the pages; the published
+ * pre-norm block.  For every row:
+ *   h = x + residual;  residual <- h (rounded to its type)
+ *   y = h / sqrt(mean(h^2) + eps) * weight
+ * The norm is taken of the unrounded fp32 h.  Without a residual h = x.
+ *   x [n_rows][d] (act_dtype); residual [n_rows][d] (res_dtype), read and
+ *   written, or NULL; weight [d] fp32; y [n_rows][d] (act_dtype) or NULL
+ *   (y may be x: in place)
+ *   q8 [n_rows][d] e4m3 or NULL (then scales is not used); at least one of y
+ *   and q8.  scales [n_rows][d / group] with one scale per `group`
+ *   consecutive values of a row; group 0: one per row, else 32, 64, 128 or
+ *   256, dividing d:
+ *     GDN_SCALE_F32   float: max|y| / 448 (at least 2^-126), or 1 where every y
+                     is 0
+ *     GDN_SCALE_E8M0  uint8: 2^(byte - 127), the smallest power of two
+ *                     (at least 2^-127) that is >= max|y| / 448; 127 where
+ *                     every y is 0
+ *   q8 = y / scale rounded to nearest even, at most +-448.  A NaN among a
+ *   group's y makes its scale NaN (byte 255) and every q8 of the group NaN.
+ * d at most 32768, else GDN_ERR_UNSUPPORTED; n_rows = 0 launches nothing.
+ * No alignment beyond the element types' own is required; 16-byte aligned
+ * tensors with d a multiple of 8 take vector accesses.
+ */
+#define GDN_SCALE_F32 0
+#define GDN_SCALE_E8M0 1
+gdn_status gdn_add_rmsnorm(int32_t act_dtype, int32_t res_dtype, const void* x, void* residual,
+                           const float* weight, float eps, int64_t n_rows, int32_t d, void* y,
+                           void* q8, void* scales, int32_t group, int32_t scale_type, void* stream);
+
+/*
+ * Maps of a packed batch, built on the device from the requests' lengths
+ * (TokenSpeed Qwen3.5 page, "Scheduler dual": a request holds block indices
+ * and a state slot; "Ciclo de vida de slots": checkpoints are block-aligned).
+ * Request r appends new_lens[r] tokens at positions start_pos[r] ..; it holds
+ * ceil(start_pos / block) blocks, listed in order in block_table[r], and gets
+ * the blocks it lacks from the top of a stack of free block ids.  A block id
+ * stands for the block's KV page and for the checkpoint slot of the state at
+ * its end.  For prefill and mixed calls on the same batch:
+ *   cu_seqlens [n_seq+1]   packed row offsets
+ *   ckpt_ids [n_seq][max_ckpt]  the checkpoint slots of the blocks that this
+ *                 step completes, in the order gdn_chunk_prefill reads them
+ *                 (ckpt_block = block), else -1; max_ckpt may be 0
+ * and for the attention layers, per packed row t < max_tokens:
+ *   seq_ids [max_tokens]   request, or -1 behind the last row
+ *   positions [max_tokens] int64 position, or 0
+ *   slot_map [max_tokens]  int64 block id * block + position % block, or -1
+ * (each of the three may be NULL).
+ *   new_lens [n_seq] int32, start_pos [n_seq] int64
+ *   block_table [n_seq][max_blocks] int32: entries of new blocks written
+ *   free_ids [free_cap] int32, *n_free of them free (entry n_free - 1 first);
+ *   new blocks go to the requests in order; *n_free_out = what is left
+ *   (n_free_out may be n_free; free_ids is not written)
+ * Problems, each reported in *dev_err:
+ *   GDN_DEV_ERR_SEQLENS  a negative length or start, or more blocks than
+ *                 max_blocks: the request counts as 0 tokens; rows beyond
+ *                 max_tokens: the offsets stop at max_tokens
+ *   GDN_DEV_ERR_BLOCKS   no free block left: that entry, its rows' slots and
+ *                 its checkpoint are -1
+ *   GDN_DEV_ERR_SLOT_OOB a held entry is negative: its rows' slots are -1
+ * block a positive power of two; n_seq at most 8192 and max_tokens at most
+ * 2^31 - 1, else GDN_ERR_UNSUPPORTED.  n_seq = 0 writes cu_seqlens[0],
+ * *n_free_out and the rows' padding.
+ */
+gdn_status gdn_batch_maps(const int32_t* new_lens, const int64_t* start_pos, int32_t n_seq,
+                          int32_t block, int32_t* block_table, int32_t max_blocks,
+                          const int32_t* free_ids, int32_t free_cap, const int32_t* n_free,
+                          int32_t* n_free_out, int32_t* cu_seqlens, int32_t* ckpt_ids,
+                          int32_t max_ckpt, int32_t* seq_ids, int64_t* positions,
+                          int64_t* slot_map, int64_t max_tokens, uint32_t* dev_err, void* stream);
+
+/*
  * Self-test of the device-side failure path: one CTA waits on a barrier phase
  * that nothing completes; the bounded wait gives up after the library's wait
  * limit (1 s), GDN_DEV_ERR_TIMEOUT is OR-ed into *dev_err (device, required)
@@ -425,7 +549,11 @@ const char* gdn_status_string(int32_t status);
 #define GDN_K_KDA_VERIFY 10
 #define GDN_K_KDA_PREFILL 11 /* the recurrence and its conv-history kernel */
 #define GDN_K_MIXED 12       /* the single-launch mixed step */
-#define GDN_K_COUNT 13
+#define GDN_K_SSM_DECODE 13
+#define GDN_K_SSM_PREFILL 14
+#define GDN_K_ADD_RMSNORM 15
+#define GDN_K_BATCH_MAPS 16
+#define GDN_K_COUNT 17
 uint64_t gdn_launch_count(int32_t kernel);
 void gdn_launch_count_reset(void);
 
