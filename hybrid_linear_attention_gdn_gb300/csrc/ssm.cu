@@ -7,8 +7,11 @@
 // Here: the decode step, and the token recurrence of the prefill for the
 // shapes that its chunked form does not take.
 #include "ssm.cuh"
+#include "ssm_chunk.cuh"
 #include "decode_tma.cuh"  // sm_count
 #include "prefill_tc.cuh"  // conv_history_launch
+
+#include <cstring>
 
 namespace gdn {
 namespace {
@@ -441,7 +444,7 @@ extern "C" gdn_status gdn_ssm_decode_step(const gdn_dims* dims, gdn_pool pool, c
 
 extern "C" size_t gdn_ssm_prefill_workspace_size(const gdn_dims* dims, int32_t n_seq, int64_t total_tokens) {
   if (gdn::check_dims(dims) != GDN_OK || total_tokens <= 0 || n_seq <= 0) return 0;
-  return 0;
+  return gdn::ssm_chunk_shape(*dims) ? gdn::ssm_chunk_workspace(*dims, n_seq, total_tokens) : 0;
 }
 
 extern "C" gdn_status gdn_ssm_prefill(const gdn_dims* dims, gdn_pool pool, gdn_pool ckpt,
@@ -497,7 +500,12 @@ extern "C" gdn_status gdn_ssm_prefill(const gdn_dims* dims, gdn_pool pool, gdn_p
   p.G = dims->hv / dims->hk;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaErrorInvalidValue;
-  switch (dims->dk) {
+  // GDN_SSM_PREFILL_PATH=recurrent (read on every call) forces the recurrence
+  const char* path = std::getenv("GDN_SSM_PREFILL_PATH");
+  const bool chunked = !(path && !std::strcmp(path, "recurrent")) &&
+                       ssm_chunk_supported(*dims, n_seq, total_tokens, qkv, out, *params);
+  if (chunked) e = ssm_chunk_launch(p, *dims, workspace, s);
+  else switch (dims->dk) {
     case 16: e = dispatch_recurrent<16, 2>(p, dims->act_dtype, dims->conv_dtype, s); break;
     case 64: e = dispatch_recurrent<64, 4>(p, dims->act_dtype, dims->conv_dtype, s); break;
     case 128: e = dispatch_recurrent<128, 8>(p, dims->act_dtype, dims->conv_dtype, s); break;
