@@ -17,19 +17,22 @@
 // chain kernel (128 V channels = one head of 128 or two of 64; sequence or
 //   segment of one): walks its chunks in order, V rows in the tensor core's
 //   M = 128 rows.  Per chunk, with S^T [dv][dk] in registers between chunks:
-//     O1^T = S^T Q^T         tf32, S^T the A operand in TMEM
-//     O2^T = V^T P^T         tf32, V^T the A operand in TMEM; two heads'
-//                            P^T side by side (N = 128), each head's rows
-//                            taken from its own half
-//     dS^T = (V w)^T K       fp16 in two halves per operand (22 bits), three
-//                            products, w_j = e^{b_last - b_j} dt_j
+//     O1^T = S^T Q^T         S^T the A operand in TMEM
+//     O2^T = V^T P^T         V^T the A operand in TMEM; two heads' P^T side
+//                            by side (N = 128), each head's rows taken from
+//                            its own half
+//     dS^T = (V w)^T K       w_j = e^{b_last - b_j} dt_j
 //     S^T <- e^{b_last} S^T + dS^T   fp32 on the CUDA cores, rounded to
 //                            nearest: the tensor core's truncating
 //                            accumulation never touches the long-lived state
-//   Roundings: the two output products' operands to tf32 (2^-12 of their
-//   terms, a tenth of the bf16 output's own 2^-9); the state's operands to
-//   22 bits after a power-of-two scaling per chunk, by the largest |k| and
-//   the largest |v w|, so that any input range keeps them.
+//   All operands are fp16 (kind::f16, four times the measured rate of
+//   kind::tf32 at the same 11 bits) after exact power-of-two scalings that
+//   keep any input range: by the largest |q|, |k|, |v| and |v w| of a chunk,
+//   and by upper bounds of |P| and |S|.  A bound may be loose by 2^14: fp16
+//   keeps 11 bits over 29 binades.  Roundings: the output products' operands
+//   to 11 bits (a relative 2^-12 of their terms, against 2^-9 of the bf16
+//   output); the state's operands to two halves each, 22 bits, in three
+//   products.
 // The work per 64 x 128 V values is bound by the instructions of the
 // elementwise steps (conv + SiLU, P, operand conversion), not by the products
 // or by memory.
@@ -64,32 +67,25 @@ constexpr int kRawRows = kC + 3;
 // Sequence n's chunks occupy the slots from cu[n] / 64 + 2 n on: a sequence of
 // len tokens touches at most len / 64 + 2 chunks, so the ranges are disjoint
 // without a scan.  Its segments likewise: from that / seg_chunks + n on.
-// One record per (chunk slot, group):
+// One record per (chunk slot, group), of fp16 operands in the tensor core's
+// 128-byte swizzled layout:
 struct __align__(1024) Record {
-  uint8_t q[4 * 64 * 128];    // q [token][dk] tf32, K-major swizzled, 32-column blocks of 8 KB
-  uint8_t kh[128 * 128];      // k^T [dk][token] fp16, K-major swizzled: high halves
-  uint8_t kl[128 * 128];      //   low halves
-  uint8_t g[64 * 256];        // G [i][j] fp32, row i's 16-byte pieces p at p ^ (i & 7)
+  uint8_t q[2 * 64 * 128];  // q 2^qe [token][dk], 64-column blocks of 8 KB
+  uint8_t kh[128 * 128];    // k^T 2^ke [dk][token]: high halves
+  uint8_t kl[128 * 128];    //   low halves
+  uint8_t g[64 * 128];      // G 2^(qe + ke - 22) [i][j]
+  int32_t qe, ke;
 };
-constexpr uint32_t kQBytes = sizeof(Record::q), kKBytes = 2 * sizeof(Record::kh), kGBytes = sizeof(Record::g);
+constexpr uint32_t kQKBytes = offsetof(Record, g), kGBytes = sizeof(Record::g), kGMBytes = kGBytes + 16;
 
 struct ChunkArgs {
   PrefillArgs p;
   Record* rec;       // [chunk slots][hk]
-  float* kscale;     // [chunk slots][hk]: 2^-e of the stored k
   float* seg_state;  // [segment slots][hv][dv][dk]
   float* seg_decay;  // [segment slots][hv]
   int32_t n_chunks, n_segs;  // slots
   int32_t seg_chunks;
 };
-
-__device__ __forceinline__ uint32_t f32_off(int r, int c, uint32_t blk) {
-  return (uint32_t)(c >> 5) * blk + (uint32_t)(r >> 3) * 1024u + (uint32_t)(r & 7) * 128u +
-         (uint32_t)((((c & 31) >> 2) ^ (r & 7)) << 4) + (uint32_t)(c & 3) * 4u;
-}
-__device__ __forceinline__ uint32_t g_off(int i, int c) {  // c a multiple of 4
-  return (uint32_t)i * 256u + (uint32_t)(((c >> 2) ^ (i & 7)) << 4);
-}
 
 struct Seq {
   int64_t t0, len, p0, p1;
@@ -161,16 +157,17 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
 // features of q and k, G = Q K^T
 // ---------------------------------------------------------------------------
 // One CTA per (chunk slot, group), 256 threads: a channel pair and half of
-// the chunk's tokens each.  HBM bound: 67 x 512 bytes in, 80 KB out.  q and k
+// the chunk's tokens each.  HBM bound: 67 x 512 bytes in, 56 KB out.  q and k
 // stand one above the other as one 128-row operand, so that one product of
-// M = 128 gives G in its upper half; k's place then takes its fp16 halves.
+// M = 128 gives G in its upper half.
 constexpr int kFT = 256;
 struct __align__(1024) FeatSmem {
-  uint8_t qk[4 * 128 * 128];  // [q; k] tf32, K-major swizzled, 32-column blocks of 16 KB; then in
-                              // the k halves of the blocks: kh rows 0.., 64.., kl rows 0.., 64..
+  uint8_t qk[2 * 128 * 128];  // [q; k] [token][dk], 64-column blocks of 16 KB
+  uint8_t kt[2 * 128 * 128];  // kh, kl
   uint8_t g[kGBytes];
+  __align__(16) int32_t meta[4];  // qe, ke
   uint64_t bar;
-  uint32_t kmax, tmem_base;
+  uint32_t qkmax[2], tmem_base;
 };
 
 __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
@@ -195,7 +192,7 @@ __global__ void __launch_bounds__(kFT, 2) ssm_features_kernel(const ChunkArgs a)
   if (c < 0 || c >= s.nch) return;
   if (warp == 0) umma::tmem_alloc(&S.tmem_base, 64);
   if (tid == 0) {
-    S.kmax = 0;
+    S.qkmax[0] = S.qkmax[1] = 0;
     mbar_init(&S.bar, 1);
     fence_mbar_init();
   }
@@ -256,39 +253,67 @@ __global__ void __launch_bounds__(kFT, 2) ssm_features_kernel(const ChunkArgs a)
     for (int t = 0; t < 32; ++t)
       if (m0 + t < 0 || m0 + t >= s.len) y[t] = make_float2(0.f, 0.f);
   }
-  if (!isq) {
+#pragma unroll
+  for (int t = 0; t < 32; ++t) {
+    const float u = fabsf(y[t].x), v = fabsf(y[t].y);  // the finite ones
+    mx = fmaxf(mx, fmaxf(u <= 3.4e38f ? u : 0.f, v <= 3.4e38f ? v : 0.f));
+  }
+  __syncthreads();  // S.qkmax cleared
+  {
+    const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
+    if (lane == 0) atomicMax(&S.qkmax[isq ? 0 : 1], m);
+  }
+  __syncthreads();
+  {
+    const float f = exp2_int(scale_exp(S.qkmax[isq ? 0 : 1]));
+    const int R0 = (isq ? 0 : kC) + 32 * half;
 #pragma unroll
     for (int t = 0; t < 32; ++t) {
-      const float u = fabsf(y[t].x), v = fabsf(y[t].y);  // the finite ones
-      mx = fmaxf(mx, fmaxf(u <= 3.4e38f ? u : 0.f, v <= 3.4e38f ? v : 0.f));
+      y[t] = mul2(y[t], make_float2(f, f));
+      tile_at<__half2>(S.qk, sizeof(S.qk), umma::sw128_off(R0 + t, 2 * cp, 128 * 128)) = __floats2half2_rn(y[t].x, y[t].y);
     }
   }
-  const int R0 = (isq ? 0 : kC) + 32 * half;
-#pragma unroll
-  for (int t = 0; t < 32; ++t)
-    tile_at<float2>(S.qk, sizeof(S.qk), f32_off(R0 + t, 2 * cp, 128 * 128)) =
-        make_float2(umma::tf32_round(y[t].x), umma::tf32_round(y[t].y));
   umma::fence_proxy_async();
   umma::fence_before();
-  __syncthreads();  // the tile written, S.kmax cleared
+  __syncthreads();  // [q; k] written
   umma::fence_after();
   const uint32_t tmem = S.tmem_base;
+  const int qe = scale_exp(S.qkmax[0]), ke = scale_exp(S.qkmax[1]);
+  const int64_t ri = cslot * p.hk + hq;
+  Record& rec = a.rec[ri];
+  [[maybe_unused]] const bool rec_ok = GDN_SPAN_G(ri, 1, (long long)a.n_chunks * p.hk);
   if (tid == 0) {
     const uint64_t dq = umma::desc(smem_addr(S.qk), 16, 1024);
-    constexpr uint32_t ID = umma::idesc_tf32(128, kC, false, false);
+    constexpr uint32_t ID = umma::idesc_f16(128, kC, false, false);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
+    for (int k = 0; k < 8; ++k) {
       const uint32_t ko = (k >> 2) * 16384 + (k & 3) * 32;
-      umma::mma_tf32(tmem, umma::adv(dq, ko), umma::adv(dq, ko + 8192), ID, k > 0);
+      umma::mma_bf16(tmem, umma::adv(dq, ko), umma::adv(dq, ko + 8192), ID, k > 0);
     }
     umma::commit(&S.bar);
+    S.meta[0] = qe;
+    S.meta[1] = ke;
   }
   if (!isq) {
-    const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
-    if (lane == 0) atomicMax(&S.kmax, m);
+#pragma unroll
+    for (int t8 = 0; t8 < 4; ++t8) {
+      uint32_t h0[4], l0[4], h1[4], l1[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 u = y[8 * t8 + 2 * i], v = y[8 * t8 + 2 * i + 1];
+        split2(u.x, v.x, h0[i], l0[i]);
+        split2(u.y, v.y, h1[i], l1[i]);
+      }
+      const uint32_t o0 = umma::sw128_off(2 * cp, 32 * half + 8 * t8, 0),
+                     o1 = umma::sw128_off(2 * cp + 1, 32 * half + 8 * t8, 0);
+      tile_at<uint4>(S.kt, sizeof(S.kt), o0) = make_uint4(h0[0], h0[1], h0[2], h0[3]);
+      tile_at<uint4>(S.kt, sizeof(S.kt), o0 + 16384) = make_uint4(l0[0], l0[1], l0[2], l0[3]);
+      tile_at<uint4>(S.kt, sizeof(S.kt), o1) = make_uint4(h1[0], h1[1], h1[2], h1[3]);
+      tile_at<uint4>(S.kt, sizeof(S.kt), o1 + 16384) = make_uint4(l1[0], l1[1], l1[2], l1[3]);
+    }
   }
   const bool late = !mbar_wait(&S.bar, 0);
-  if (__syncthreads_or(late)) {  // also: S.kmax complete
+  if (__syncthreads_or(late)) {
     if (tid == 0) {
       report(p.err, GDN_DEV_ERR_TIMEOUT);
       mbar_wait(&S.bar, 0);
@@ -298,53 +323,33 @@ __global__ void __launch_bounds__(kFT, 2) ssm_features_kernel(const ChunkArgs a)
     const int i = 32 * (warp & 3) + lane;
     float v[32];
     umma::tmem_ld32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 32 * half, v);
+    // |v| <= 128 2^15 2^15: times 2^-22 it fits fp16
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-      tile_at<float4>(S.g, sizeof(S.g), g_off(i, 32 * half + 4 * q)) =
-          make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-  } else {
-    const int e = scale_exp(S.kmax);
-    const float f = exp2_int(e);
-    // row r of a half's tile: in k's part of block (r >> 6), of block 2 + (r >> 6) for the low halves
-    auto place = [](int r, int tok) {
-      return (uint32_t)(r >> 6) * 16384u + 8192u + umma::sw128_off(r & 63, tok, 0);
-    };
+    for (int q = 0; q < 4; ++q) {
+      uint32_t h[4];
 #pragma unroll
-    for (int t8 = 0; t8 < 4; ++t8) {
-      uint32_t h0[4], l0[4], h1[4], l1[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 u = y[8 * t8 + 2 * i], v = y[8 * t8 + 2 * i + 1];
-        split2(u.x * f, v.x * f, h0[i], l0[i]);
-        split2(u.y * f, v.y * f, h1[i], l1[i]);
+      for (int e = 0; e < 4; ++e) {
+        const __half2 x = __floats2half2_rn(v[8 * q + 2 * e] * 0x1p-22f, v[8 * q + 2 * e + 1] * 0x1p-22f);
+        h[e] = *reinterpret_cast<const uint32_t*>(&x);
       }
-      const uint32_t o0 = place(2 * cp, 32 * half + 8 * t8), o1 = place(2 * cp + 1, 32 * half + 8 * t8);
-      tile_at<uint4>(S.qk, sizeof(S.qk), o0) = make_uint4(h0[0], h0[1], h0[2], h0[3]);
-      tile_at<uint4>(S.qk, sizeof(S.qk), o0 + 32768) = make_uint4(l0[0], l0[1], l0[2], l0[3]);
-      tile_at<uint4>(S.qk, sizeof(S.qk), o1) = make_uint4(h1[0], h1[1], h1[2], h1[3]);
-      tile_at<uint4>(S.qk, sizeof(S.qk), o1 + 32768) = make_uint4(l1[0], l1[1], l1[2], l1[3]);
+      tile_at<uint4>(S.g, sizeof(S.g), umma::sw128_off(i, 32 * half + 8 * q, 0)) = make_uint4(h[0], h[1], h[2], h[3]);
     }
-    if (tid == 64) GDN_GV(a.kscale, (long long)a.n_chunks * p.hk)[cslot * p.hk + hq] = exp2_int(-e);
   }
   umma::fence_proxy_async();
   umma::fence_before();
   __syncthreads();
-  if (tid == 0) {
-    const int64_t ri = cslot * p.hk + hq;
-    if (GDN_SPAN_G(ri, 1, (long long)a.n_chunks * p.hk)) {
-      Record& r = a.rec[ri];
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        bulk_s2g(r.q + b * 8192, S.qk + b * 16384, 8192);
-        bulk_s2g(r.kh + b * 8192, S.qk + b * 16384 + 8192, 8192);  // kh, then kl
-      }
-      bulk_s2g(r.g, S.g, kGBytes);
-      bulk_commit();
-      bulk_wait_all();
-    }
+  if (tid == 0 && rec_ok) {
+    bulk_s2g(rec.q, S.qk, 8192);
+    bulk_s2g(rec.q + 8192, S.qk + 16384, 8192);
+    bulk_s2g(rec.kh, S.kt, 32768);  // and kl
+    bulk_s2g(rec.g, S.g, kGMBytes);  // and qe, ke
+    bulk_commit();
+    bulk_wait_all();
   }
   if (warp == 0) umma::tmem_dealloc(tmem, 64);
 }
+static_assert(offsetof(FeatSmem, meta) == offsetof(FeatSmem, g) + kGBytes && offsetof(Record, qe) == offsetof(Record, g) + kGBytes,
+              "G and its exponents leave and arrive as one piece");
 
 // ---------------------------------------------------------------------------
 // the chain
@@ -363,43 +368,88 @@ constexpr int kThreads = kCompute + 128;
 constexpr int kComputeRegs = 104, kIssuerRegs = 64;
 static_assert(kCompute * kComputeRegs + 128 * kIssuerRegs <= kThreads * 96, "no more than the launch's registers");
 
-// TMEM columns
-constexpr uint32_t TM_S = 0;     // S^T (operand), then dS^T
+// TMEM columns (fp16 operands hold two values per column)
+constexpr uint32_t TM_DS = 0;    // dS^T [dv rows][dk]
 constexpr uint32_t TM_O1 = 128;  // [dv rows][64 tokens]
 constexpr uint32_t TM_O2 = 192;  // [dv rows][64 tokens of each head]
-constexpr uint32_t TM_V = 320;   // V^T tf32 [dv rows][64 tokens]
-constexpr uint32_t TM_WH = 384;  // (V w)^T fp16 pairs: high halves, 32 columns
-constexpr uint32_t TM_WL = 416;  //   low halves
+constexpr uint32_t TM_S = 320;   // S^T fp16 [dv rows][dk], 64 columns
+constexpr uint32_t TM_V = 384;   // V^T fp16 [dv rows][64 tokens], 32 columns
+constexpr uint32_t TM_WH = 416;  // (V w)^T fp16: high halves, 32 columns
+constexpr uint32_t TM_WL = 448;  //   low halves
 constexpr uint32_t TM_COLS = 512;
 
 template <int NH>
 struct __align__(1024) ChainSmem {
-  uint8_t q[kQBytes];
-  uint8_t k[kKBytes];
-  uint8_t pt[2][2 * NH * 64 * 128];  // P [head, i][j] tf32: two 32-column blocks
-  uint8_t g[2][kGBytes];
+  uint8_t qk[2][kQKBytes];         // q, kh, kl
+  uint8_t pt[2][NH * 64 * 128];    // P 2^pe [head, i][j]
+  struct __align__(1024) Gm {
+    uint8_t g[kGBytes];
+    int32_t meta[4];               // qe, ke
+  } g[2];
   __nv_bfloat16 raw[2][kRawRows][128];
   __align__(128) __nv_bfloat16 ot[kC][128];
   // per chunk (mod 4) and head
   __align__(16) float b2[4][NH][kC];  // b log2(e)
   float eb[4][NH][kC];                // e^b
   float dt[4][NH][kC];
+  float v[4][NH][kC];                 // e^{b' - b} dt, b' at the end of the token's 16-token block
   float w[4][NH][kC];                 // e^{b_last - b} dt
   float dec[4][NH];                   // e^{b_last}
-  uint32_t vmax[3];                   // largest |V w| of a chunk (mod 3), float bits
-  uint32_t vfin;                      //   the same over finite values, where that is not finite
-  uint64_t x_bar[2], g_bar[2], q_bar, k_bar, ready, o1_bar, mma_bar;
+  float dtm[4][NH];                   // the largest dt
+  uint32_t vmax[3][2];                // largest |V w|, |V| of a chunk (mod 3), float bits
+  uint32_t vfin[2];                   //   the same over finite values, where one is not
+  uint64_t x_bar[2], g_bar[2], qk_bar[2], ready, mma_bar;
+  uint32_t smax;                      // largest |S| entering the segment
   uint32_t tmem_base;
   int seq;
 };
 
-// 8 consecutive columns of this thread's TMEM lane, written
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8], int line = __builtin_LINE()) {
+// 8 or 16 consecutive columns of this thread's TMEM lane, written; done after
+// tmem_wait_st()
+__device__ __forceinline__ void tmem_put8(uint32_t taddr, const uint32_t (&v)[8], int line = __builtin_LINE()) {
   if (!umma::tmem_ok(taddr, 8, true, line)) return;
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(v[0]),
                "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
-  asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ void tmem_put16(uint32_t taddr, const uint32_t (&v)[16], int line = __builtin_LINE()) {
+  if (!umma::tmem_ok(taddr, 16, true, line)) return;
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(
+          taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+// two runs of 16 columns read at once
+__device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, float (&va)[16], float (&vb)[16],
+                                            int line = __builtin_LINE()) {
+  if (!umma::tmem_ok(ta, 16, true, line) || !umma::tmem_ok(tb, 16, true, line)) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) va[i] = vb[i] = 0.f;
+    return;
+  }
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, "
+      "[%33];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=f"(va[0]), "=f"(va[1]), "=f"(va[2]), "=f"(va[3]), "=f"(va[4]), "=f"(va[5]), "=f"(va[6]), "=f"(va[7]),
+        "=f"(va[8]), "=f"(va[9]), "=f"(va[10]), "=f"(va[11]), "=f"(va[12]), "=f"(va[13]), "=f"(va[14]), "=f"(va[15]),
+        "=f"(vb[0]), "=f"(vb[1]), "=f"(vb[2]), "=f"(vb[3]), "=f"(vb[4]), "=f"(vb[5]), "=f"(vb[6]), "=f"(vb[7]),
+        "=f"(vb[8]), "=f"(vb[9]), "=f"(vb[10]), "=f"(vb[11]), "=f"(vb[12]), "=f"(vb[13]), "=f"(vb[14]), "=f"(vb[15])
+      : "r"(ta), "r"(tb)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t half2_bits(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
 }
 // D (TMEM) (+)= A B with A in TMEM (fp16 pairs: K = 16 is 8 columns from
 // tmem_a) and B from a shared-memory descriptor, kind::f16
@@ -451,30 +501,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.x_bar[i], 1);
       mbar_init(&S.g_bar[i], 1);
+      mbar_init(&S.qk_bar[i], 1);
     }
-    mbar_init(&S.q_bar, 1);
-    mbar_init(&S.k_bar, 1);
     mbar_init(&S.ready, kCompute / 32);
-    mbar_init(&S.o1_bar, 1);
     mbar_init(&S.mma_bar, 1);
-    S.vmax[0] = S.vmax[1] = S.vmax[2] = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) S.vmax[i][0] = S.vmax[i][1] = 0;
+    S.smax = 0;
     fence_mbar_init();
   }
   umma::fence_before();
   __syncthreads();
   umma::fence_after();
   const uint32_t tmem = S.tmem_base;
-  constexpr uint32_t kPBlk = NH * 64 * 128;
-  static_assert(TM_O1 == TM_S + kDK && TM_O2 == TM_O1 + kC && TM_V == TM_O2 + 2 * kC && TM_WH == TM_V + kC &&
-                    TM_WL == TM_WH + kC / 2 && TM_WL + kC / 2 <= TM_COLS,
+  static_assert(TM_O1 == TM_DS + kDK && TM_O2 == TM_O1 + kC && TM_S == TM_O2 + 2 * kC && TM_V == TM_S + kDK / 2 &&
+                    TM_WH == TM_V + kC / 2 && TM_WL == TM_WH + kC / 2 && TM_WL + kC / 2 <= TM_COLS,
                 "TMEM regions");
 
   if (warp >= kCompute / 32) {
     // ------------------------------------------------------------------ issuer
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kIssuerRegs));
     if (warp == kCompute / 32) {
-    constexpr uint32_t ID_O1 = umma::idesc_tf32(128, kC, false, false);
-    constexpr uint32_t ID_O2 = umma::idesc_tf32(128, NH * kC, false, false);
+    constexpr uint32_t ID_O1 = umma::idesc_f16(128, kC, false, false);
+    constexpr uint32_t ID_O2 = umma::idesc_f16(128, NH * kC, false, false);
     constexpr uint32_t ID_S = umma::idesc_f16(128, kDK, false, false);
     const int64_t rec0 = (s.first + c_begin) * p.hk + hq;
     auto bulk = [&](void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -482,53 +531,58 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (GDN_GBYTES(src, bytes, a.rec, (long long)a.n_chunks * p.hk * sizeof(Record)) && GDN_SBYTES(dst, bytes, S))
         bulk_g2s(dst, src, bytes, bar);
     };
-    // raw V rows and G of the segment's chunk i (lane 0)
-    auto load_x = [&](int i) {
+    // raw V rows, and G with its exponents, of the segment's chunk i (lane 0)
+    auto load_xg = [&](int i) {
       const int32_t row0 = (int32_t)(s.t0 + (P0 + (int64_t)i * kC - 3 - s.p0));  // may be < 0: zeros
       mbar_arrive_expect_tx(&S.x_bar[i & 1], (uint32_t)sizeof(S.raw[0]));
       if (GDN_SPAN_G(2 * p.hk * kDK + tile * 128, 128, p.C) && GDN_SBYTES(&S.raw[i & 1][0][0], sizeof(S.raw[0]), S))
         tma_load_2d(&S.raw[i & 1][0][0], &xmap, 2 * p.hk * kDK + tile * 128, row0, &S.x_bar[i & 1]);
+      bulk(&S.g[i & 1], a.rec[rec0 + (int64_t)i * p.hk].g, kGMBytes, &S.g_bar[i & 1]);
     };
-    auto load_g = [&](int i) { bulk(S.g[i & 1], a.rec[rec0 + (int64_t)i * p.hk].g, kGBytes, &S.g_bar[i & 1]); };
-    auto load_q = [&](int i) { bulk(S.q, a.rec[rec0 + (int64_t)i * p.hk].q, kQBytes, &S.q_bar); };
-    auto load_k = [&](int i) { bulk(S.k, a.rec[rec0 + (int64_t)i * p.hk].kh, kKBytes, &S.k_bar); };
-    int n_xg = 0, n_q = 0, n_k = 0, n_o1 = 0, n_mma = 0;  // issued
+    // q and k (the state alone needs only k)
+    constexpr uint32_t kSkip = STATE ? sizeof(Record::q) : 0;
+    auto load_qk = [&](int i) {
+      bulk(S.qk[i & 1] + kSkip, a.rec[rec0 + (int64_t)i * p.hk].q + kSkip, kQKBytes - kSkip, &S.qk_bar[i & 1]);
+    };
+    int n_xg = 0, n_qk = 0, n_mma = 0;  // issued
     if (lane == 0) {
-      for (; n_xg < 2 && n_xg < nit; ++n_xg) {
-        load_x(n_xg);
-        if (!STATE) load_g(n_xg);
-      }
-      load_k(0);
-      n_k = 1;
-      if (!STATE) {
-        load_q(0);
-        n_q = 1;
-      }
+      for (; n_xg < 2 && n_xg < nit; ++n_xg) load_xg(n_xg);
+      for (; n_qk < 2 && n_qk < nit; ++n_qk) load_qk(n_qk);
     }
     bool ok = true;
-    const uint64_t dq = umma::desc(smem_addr(S.q), 16, 1024);
-    const uint64_t dh = umma::desc(smem_addr(S.k), 16, 1024), dl = umma::adv(dh, sizeof(Record::kh));
     // pass i: chunk i's operands are in place (and chunk i - 1's output staged)
     for (int i = 0; i < nit + (STATE ? 0 : 1) && ok; ++i) {
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(&S.ready, i & 1)))) break;
       umma::fence_after();
-      const uint32_t par = i & 1;
       if (lane == 0 && i < nit) {
         if (i + 2 < nit) {  // chunk i's raw rows and G have been read
-          load_x(i + 2);
-          if (!STATE) load_g(i + 2);
+          load_xg(i + 2);
           n_xg = i + 3;
         }
-        if (!STATE) {
-          // O1^T = S^T Q^T
-          if ((ok = mbar_wait(&S.q_bar, par))) {
+        if ((ok = mbar_wait(&S.qk_bar[i & 1], (i >> 1) & 1))) {
+          umma::fence_after();
+          const uint64_t dq = umma::desc(smem_addr(S.qk[i & 1]), 16, 1024);
+          const uint64_t dh = umma::adv(dq, offsetof(Record, kh)), dl = umma::adv(dq, offsetof(Record, kl));
+          if (!STATE) {
+            // O1^T = S^T Q^T, O2^T = V^T P^T
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              umma::mma_tf32_ta(tmem + TM_O1, tmem + TM_S + 8 * k, umma::adv(dq, (k >> 2) * 8192 + (k & 3) * 32),
-                                ID_O1, k > 0);
-            umma::commit(&S.o1_bar);
-            ++n_o1;
+            for (int k = 0; k < 8; ++k)
+              mma_f16_ta(tmem + TM_O1, tmem + TM_S + 8 * k, umma::adv(dq, (k >> 2) * 8192 + (k & 3) * 32), ID_O1, k > 0);
+            const uint64_t dp = umma::desc(smem_addr(S.pt[i & 1]), 16, 1024);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_f16_ta(tmem + TM_O2, tmem + TM_V + 8 * k, umma::adv(dp, 32 * k), ID_O2, k > 0);
           }
+          // dS^T = (V w)^T K, small products first
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_f16_ta(tmem + TM_DS, tmem + TM_WL + 8 * k, umma::adv(dh, 32 * k), ID_S, k > 0);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_f16_ta(tmem + TM_DS, tmem + TM_WH + 8 * k, umma::adv(dl, 32 * k), ID_S, true);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_f16_ta(tmem + TM_DS, tmem + TM_WH + 8 * k, umma::adv(dh, 32 * k), ID_S, true);
         }
       }
       if constexpr (!STATE) {
@@ -552,38 +606,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (lane == 0 && i < nit && ok) {
-        if (!STATE) {
-          // O2^T = V^T P^T
-          const uint64_t dp = umma::desc(smem_addr(S.pt[par]), 16, 1024);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            umma::mma_tf32_ta(tmem + TM_O2, tmem + TM_V + 8 * k, umma::adv(dp, (k >> 2) * kPBlk + (k & 3) * 32),
-                              ID_O2, k > 0);
-          // dS^T takes the place of S^T once O1's product has read it
-          if ((ok = mbar_wait(&S.o1_bar, par)) && i + 1 < nit) {
-            load_q(i + 1);
-            ++n_q;
-          }
-        }
-        if (ok && (ok = mbar_wait(&S.k_bar, par))) {
-          umma::fence_after();
-          // dS^T = (V w)^T K, small products first
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_f16_ta(tmem + TM_S, tmem + TM_WL + 8 * k, umma::adv(dh, 32 * k), ID_S, k > 0);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_f16_ta(tmem + TM_S, tmem + TM_WH + 8 * k, umma::adv(dl, 32 * k), ID_S, true);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_f16_ta(tmem + TM_S, tmem + TM_WH + 8 * k, umma::adv(dh, 32 * k), ID_S, true);
-          bulk_wait_read();  // the staging may be written once this chunk's products are known to be done
-          umma::commit(&S.mma_bar);
-          ++n_mma;
-          if ((ok = mbar_wait(&S.mma_bar, par)) && i + 1 < nit) {
-            load_k(i + 1);
-            ++n_k;
-          }
+        bulk_wait_read();  // the staging may be written once this chunk's products are known to be done
+        umma::commit(&S.mma_bar);
+        ++n_mma;
+        if ((ok = mbar_wait(&S.mma_bar, i & 1)) && i + 2 < nit) {
+          load_qk(i + 2);
+          n_qk = i + 3;
         }
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -594,11 +622,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         report(p.err, GDN_DEV_ERR_TIMEOUT);
         for (int k = max(0, n_xg - 2); k < n_xg; ++k) {
           mbar_wait(&S.x_bar[k & 1], (k >> 1) & 1);
-          if (!STATE) mbar_wait(&S.g_bar[k & 1], (k >> 1) & 1);
+          mbar_wait(&S.g_bar[k & 1], (k >> 1) & 1);
         }
-        if (n_q) mbar_wait(&S.q_bar, (n_q - 1) & 1);
-        if (n_k) mbar_wait(&S.k_bar, (n_k - 1) & 1);
-        if (n_o1) mbar_wait(&S.o1_bar, (n_o1 - 1) & 1);
+        for (int k = max(0, n_qk - 2); k < n_qk; ++k) mbar_wait(&S.qk_bar[k & 1], (k >> 1) & 1);
         if (n_mma) mbar_wait(&S.mma_bar, (n_mma - 1) & 1);
       }
       bulk_wait_all();
@@ -652,18 +678,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       b[1] += __shfl_sync(0xffffffffu, b[0], 31);
       const float back = __shfl_sync(0xffffffffu, suf[1], 0), all = back + __shfl_sync(0xffffffffu, suf[0], 0);
+      float m = fmaxf(dt[0], dt[1]);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       const float nx = __shfl_down_sync(0xffffffffu, suf[0], 1), ny = __shfl_down_sync(0xffffffffu, suf[1], 1);
       suf[0] = (lane < 31 ? nx : 0.f) + back;
       suf[1] = lane < 31 ? ny : 0.f;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int t = 32 * e + lane;
-        S.b2[buf][ghl][t] = b[e] * 1.4426950408889634f;
+        const float b2 = b[e] * 1.4426950408889634f;
+        S.b2[buf][ghl][t] = b2;
+        S.v[buf][ghl][t] = ex2(__shfl_sync(0xffffffffu, b2, lane | 15) - b2) * dt[e];
         S.eb[buf][ghl][t] = expf(b[e]);
         S.dt[buf][ghl][t] = dt[e];
         S.w[buf][ghl][t] = expf(suf[e]) * dt[e];
       }
-      if (lane == 0) S.dec[buf][ghl] = expf(all);
+      if (lane == 0) {
+        S.dec[buf][ghl] = expf(all);
+        S.dtm[buf][ghl] = m;
+      }
     };
     if (gate_warp) {
       gate_load(0);
@@ -707,6 +741,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    if (!STATE) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const uint32_t u = __float_as_uint(st[i]) & 0x7fffffffu;
+        m = max(m, u < 0x7f800000u ? u : 0u);  // the finite ones
+      }
+      m = __reduce_max_sync(0xffffffffu, m);
+      if (lane == 0) atomicMax(&S.smax, m);
+    }
     const float4 w4 = vec_at<const float4>(GDN_GV(p.conv_w, (long long)p.C * 4), (size_t)ch * 4);
     const float bias = p.conv_bias ? GDN_GV(p.conv_bias, p.C)[ch] : 0.f;
     // P's rows of this thread: row pr of the heads' 64 NH, PC columns from pc;
@@ -715,26 +759,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int pr = NH == 2 ? lrow : (lrow & 63), pi = pr & 63, ph = pr >> 6;
     const int pc = 16 * qq + (NH == 2 ? 0 : 8 * (lrow >> 6));
     const float skip = p.D ? GDN_GV(p.D, p.hv)[h0 + ph] : 0.f;
+    [[maybe_unused]] const float skip2 = p.D && NH == 2 ? GDN_GV(p.D, p.hv)[h0 + (ph ^ 1)] : 0.f;
     if (!STATE) {
 #pragma unroll
-      for (int c4 = 0; c4 < PC / 4; ++c4) {
-        tile_at<float4>(S.pt[0], sizeof(S.pt[0]), f32_off(pr, pc + 4 * c4, kPBlk)) = make_float4(0.f, 0.f, 0.f, 0.f);
-        tile_at<float4>(S.pt[1], sizeof(S.pt[1]), f32_off(pr, pc + 4 * c4, kPBlk)) = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int c4 = 0; c4 < PC / 8; ++c4) {
+        tile_at<uint4>(S.pt[0], sizeof(S.pt[0]), umma::sw128_off(pr, pc + 8 * c4, 0)) = make_uint4(0u, 0u, 0u, 0u);
+        tile_at<uint4>(S.pt[1], sizeof(S.pt[1]), umma::sw128_off(pr, pc + 8 * c4, 0)) = make_uint4(0u, 0u, 0u, 0u);
       }
     }
+    // chunks until the next block boundary, and the boundary's index
     const int kpc = p.ckpt_block / kC;
-    const int q0 = (int)((s.p0 / kC) % kpc);
-    auto ckpt_slot = [&](int c) -> int32_t {  // checkpoint slot at the end of the sequence's chunk c, -1: none
-      if (c == s.nch - 1 && s.p1 % kC) return -1;
-      const int q = q0 + c + 1;
-      if (q % kpc) return -1;
-      const int idx = q / kpc - 1;
-      if (idx >= p.max_ckpt) return -1;
-      const int32_t id = GDN_GV(p.ckpt_ids, (long long)p.n_seq * p.max_ckpt)[(size_t)n * p.max_ckpt + idx];
-      return slot_class(id, p.ck_num_slots) == 0 ? id : -1;
-    };
+    int to_ckpt = kpc - 1 - (int)((P0 / kC) % kpc);
+    int64_t ck_idx = P0 / p.ckpt_block - s.p0 / p.ckpt_block;
 
     bool bad = false;
+    int qe = 0, ke = 0, pe = 0;  // scale exponents of the next chunk's q, k and P
     float y[16];  // V of the next chunk: channel lrow, tokens 16 qq ..
     auto weights = [&](int i, float (&x)[16]) {  // V w
       const auto ws = GDN_SV(&S.w[i & 3][hl][0], kC);
@@ -786,79 +825,134 @@ __global__ void __launch_bounds__(kThreads, 1)
       {
         float x[16];
         weights(i, x);
-        uint32_t m = 0;
+        uint32_t m = 0, mv = 0;
 #pragma unroll
-        for (int t = 0; t < 16; ++t) m = max(m, __float_as_uint(x[t]) & 0x7fffffffu);
+        for (int t = 0; t < 16; ++t) {
+          m = max(m, __float_as_uint(x[t]) & 0x7fffffffu);
+          if (!STATE) mv = max(mv, __float_as_uint(y[t]) & 0x7fffffffu);
+        }
         m = __reduce_max_sync(0xffffffffu, m);
-        if (lane == 0) atomicMax(&S.vmax[i % 3], m);
+        if (!STATE) mv = __reduce_max_sync(0xffffffffu, mv);
+        if (lane == 0) {
+          atomicMax(&S.vmax[i % 3][0], m);
+          if (!STATE) atomicMax(&S.vmax[i % 3][1], mv);
+        }
       }
+      if (!mbar_wait(&S.g_bar[i & 1], (i >> 1) & 1)) bad = true;
+      qe = S.g[i & 1].meta[0];
+      ke = S.g[i & 1].meta[1];
       if constexpr (!STATE) {
-        if (!mbar_wait(&S.g_bar[i & 1], (i >> 1) & 1)) bad = true;
+        // |P| <= 128 max|q| max|k| max dt + |D| < 2^(37 - qe - ke) max dt + |D|
+        const int buf = i & 3;
+        const float g1 = exp2_int(max(-126, min(127, 37 - qe - ke)));
+        pe = scale_exp(__float_as_uint(fmaf(g1, S.dtm[buf][ph], fabsf(skip))));
+        if constexpr (NH == 2)  // one scale for both heads
+          pe = min(pe, scale_exp(__float_as_uint(fmaf(g1, S.dtm[buf][ph ^ 1], fabsf(skip2)))));
         if (pc <= pi) {
-          const int buf = i & 3;
-          const float bi = S.b2[buf][ph][pi];
+          // P_ij = G_ij u_i v_j: both factors taken at the end b' of j's
+          // 16-token block, u_i = e^{b_i - b'} at most 1 below the diagonal
+          // blocks; on them it is large where the block decays, and beyond
+          // 2^80 the differences are taken one by one
+          const float bi = S.b2[buf][ph][pi], be = S.b2[buf][ph][GDN_S(pc | 15, kC)];
+          const bool diag = (pi >> 4) == qq;
+          const float pscale = exp2_int(max(-126, min(127, 22 - qe - ke + pe)));
+          const float u = ex2(bi - be) * pscale;
+          float e[PC];
 #pragma unroll
-          for (int c4 = 0; c4 < PC / 4; ++c4) {
-            const int j = pc + 4 * c4;
-            const float4 gv = tile_at<float4>(S.g[i & 1], sizeof(S.g[0]), g_off(pi, j));
-            const float4 bj = *reinterpret_cast<const float4*>(&S.b2[buf][ph][GDN_S(j, kC - 3)]);
-            const float4 dj = *reinterpret_cast<const float4*>(&S.dt[buf][ph][j]);
-            float e[4] = {bi - bj.x, bi - bj.y, bi - bj.z, bi - bj.w};
-            const float gd[4] = {gv.x * dj.x, gv.y * dj.y, gv.z * dj.z, gv.w * dj.w};
+          for (int c8 = 0; c8 < PC / 8; ++c8) {
+            const uint4 g4 = tile_at<uint4>(S.g[i & 1].g, kGBytes, umma::sw128_off(pi, pc + 8 * c8, 0));
+            const float4 va = *reinterpret_cast<const float4*>(&S.v[buf][ph][GDN_S(pc + 8 * c8, kC - 7)]);
+            const float4 vb = *reinterpret_cast<const float4*>(&S.v[buf][ph][pc + 8 * c8 + 4]);
+            const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w};
+            const float vv[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              float x;
-              asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(x) : "f"(e[k]));
-              x *= gd[k];
-              if (j + k == pi) x += skip;
-              e[k] = j + k <= pi ? umma::tf32_round(x) : 0.f;
+              const float2 g2 = __half22float2(*reinterpret_cast<const __half2*>(&gw[k]));
+              e[8 * c8 + 2 * k] = g2.x * (u * vv[2 * k]);
+              e[8 * c8 + 2 * k + 1] = g2.y * (u * vv[2 * k + 1]);
             }
-            tile_at<float4>(S.pt[i & 1], sizeof(S.pt[0]), f32_off(pr, j, kPBlk)) = make_float4(e[0], e[1], e[2], e[3]);
           }
+          if (diag) {
+            const float sk = skip * exp2_int(pe);
+            if (S.b2[buf][ph][pc & ~15] - be > 80.f) {
+#pragma unroll 1
+              for (int k = 0; k < PC; ++k) {
+                const int j = pc + k;
+                const float g = __half2float(tile_at<__half>(S.g[i & 1].g, kGBytes, umma::sw128_off(pi, j, 0)));
+                const float x = j > pi ? 0.f : g * (ex2(bi - S.b2[buf][ph][GDN_S(j, kC)]) * S.dt[buf][ph][j] * pscale);
+#pragma unroll
+                for (int q = 0; q < PC; ++q)
+                  if (q == k) e[q] = x;
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < PC; ++k) {
+              const int j = pc + k;
+              e[k] = j < pi ? e[k] : j == pi ? e[k] + sk : 0.f;
+            }
+          }
+#pragma unroll
+          for (int c8 = 0; c8 < PC / 8; ++c8)
+            tile_at<uint4>(S.pt[i & 1], sizeof(S.pt[0]), umma::sw128_off(pr, pc + 8 * c8, 0)) =
+                make_uint4(half2_bits(e[8 * c8], e[8 * c8 + 1]), half2_bits(e[8 * c8 + 2], e[8 * c8 + 3]),
+                           half2_bits(e[8 * c8 + 4], e[8 * c8 + 5]), half2_bits(e[8 * c8 + 6], e[8 * c8 + 7]));
         }
       }
       if (gate_warp && i + 1 < nit && i > 0) gates(i + 1);
-      if (tid == 0) S.vmax[(i + 1) % 3] = 0;
+      if (tid == 0) S.vmax[(i + 1) % 3][0] = S.vmax[(i + 1) % 3][1] = 0;
     };
-    int ve = 0;  // scale exponent of the (V w) operand in TMEM
-    // chunk i's operands into TMEM (its vmax complete): S^T, V^T, (V w)^T
+    float s_bound = 0.f;  // >= |S|
+    // of the operands in TMEM: factors that take the products back
+    float ds_f = 0.f, o1_f = 0.f, o2_f = 0.f;
+    // chunk i's operands into TMEM (its maxima complete): S^T, V^T, (V w)^T
     auto operands = [&](int i) {
-      if constexpr (!STATE) {
-        float r[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) r[e] = umma::tf32_round(st[e]);
-        umma::tmem_st32(tlane + TM_S + 32 * qq, r);
-        float v[16];
-#pragma unroll
-        for (int t = 0; t < 16; ++t) v[t] = umma::tf32_round(y[t]);
-        umma::tmem_st16(tlane + TM_V + 16 * qq, v);
-      }
       float x[16];
       weights(i, x);
-      uint32_t m = S.vmax[i % 3];
-      if (m >= 0x7f800000u) {
-        // infinite or NaN values among V w: the scale of the finite ones
+      uint32_t m = S.vmax[i % 3][0], mv = S.vmax[i % 3][1];
+      if (max(m, mv) >= 0x7f800000u) {
+        // infinite or NaN values among them: the scales of the finite ones
         named_sync(1, kCompute);
-        if (tid == 0) S.vfin = 0;
+        if (tid == 0) S.vfin[0] = S.vfin[1] = 0;
         named_sync(1, kCompute);
-        m = 0;
+        m = mv = 0;
 #pragma unroll
         for (int t = 0; t < 16; ++t) {
-          const uint32_t u = __float_as_uint(x[t]) & 0x7fffffffu;
+          const uint32_t u = __float_as_uint(x[t]) & 0x7fffffffu, v = __float_as_uint(y[t]) & 0x7fffffffu;
           m = max(m, u < 0x7f800000u ? u : 0u);
+          mv = max(mv, v < 0x7f800000u ? v : 0u);
         }
-        atomicMax(&S.vfin, m);
+        atomicMax(&S.vfin[0], m);
+        atomicMax(&S.vfin[1], mv);
         named_sync(1, kCompute);
-        m = S.vfin;
+        m = S.vfin[0];
+        mv = S.vfin[1];
       }
-      ve = scale_exp(m);
+      const int ve = scale_exp(m);
+      __syncwarp();
+      if constexpr (!STATE) {
+        const int se = scale_exp(__float_as_uint(s_bound)), vse = scale_exp(mv);
+        const float fs = exp2_int(se), fv = exp2_int(vse);
+        uint32_t r[16], v[8];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) r[e] = half2_bits(st[2 * e] * fs, st[2 * e + 1] * fs);
+        tmem_put16(tlane + TM_S + 16 * qq, r);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) v[t] = half2_bits(y[2 * t] * fv, y[2 * t + 1] * fv);
+        tmem_put8(tlane + TM_V + 8 * qq, v);
+        o1_f = exp2_int(-se) * exp2_int(-qe);
+        o2_f = exp2_int(-vse) * exp2_int(-pe);
+      }
       const float f = exp2_int(ve);
       uint32_t hi[8], lo[8];
 #pragma unroll
       for (int t = 0; t < 8; ++t) split2(x[2 * t] * f, x[2 * t + 1] * f, hi[t], lo[t]);
-      __syncwarp();
-      tmem_st8(tlane + TM_WH + 8 * qq, hi);
-      tmem_st8(tlane + TM_WL + 8 * qq, lo);
+      tmem_put8(tlane + TM_WH + 8 * qq, hi);
+      tmem_put8(tlane + TM_WL + 8 * qq, lo);
+      ds_f = exp2_int(-ve) * exp2_int(-ke);
+      // |S| after the chunk: 64 terms of at most max|V w| max|k|
+      const float dm = NH == 2 ? fmaxf(S.dec[i & 3][0], S.dec[i & 3][NH - 1]) : S.dec[i & 3][0];
+      s_bound = fmaf(s_bound, dm, 64.f * __uint_as_float(m) * exp2_int(max(-126, min(127, 15 - ke))));
+      tmem_wait_st();
     };
     auto publish = [&]() {
       umma::fence_proxy_async();
@@ -871,28 +965,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     features(0);
     int i = 0;
     if (!named_sync_or(1, kCompute, bad)) {
+      s_bound = __uint_as_float(S.smax);
       operands(0);
       publish();
       for (; i < nit; ++i) {
         if (i + 1 < nit) features(i + 1);
-        const float kscale = GDN_GV(a.kscale, (long long)a.n_chunks * p.hk)[(s.first + c_begin + i) * p.hk + hq];
         if (named_sync_or(1, kCompute, bad)) break;
         if (!mbar_wait(&S.mma_bar, i & 1)) bad = true;
         __syncwarp();
         umma::fence_after();
         const int buf = i & 3;
         {
-          const float dec = S.dec[buf][hl], f = exp2_int(-ve);
+          const float dec = S.dec[buf][hl];
           seg_dec *= dec;
           float d[32];
-          umma::tmem_ld32(tlane + TM_S + 32 * qq, d);
+          umma::tmem_ld32(tlane + TM_DS + 32 * qq, d);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) st[e] = fmaf(st[e], dec, d[e] * kscale * f);
+          for (int e = 0; e < 32; ++e) st[e] = fmaf(st[e], dec, d[e] * ds_f);
         }
         if constexpr (!STATE) {
           float o1[16], o2[16];
-          umma::tmem_ld16(tlane + TM_O1 + 16 * qq, o1);
-          umma::tmem_ld16(tlane + TM_O2 + (NH == 2 ? hl * kC : 0) + 16 * qq, o2);
+          tmem_ld16x2(tlane + TM_O1 + 16 * qq, tlane + TM_O2 + (NH == 2 ? hl * kC : 0) + 16 * qq, o1, o2);
           const auto ot = GDN_SV(&S.ot[0][0], kC * 128);
 #pragma unroll
           for (int t4 = 0; t4 < 4; ++t4) {
@@ -900,14 +993,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float ev[4] = {e.x, e.y, e.z, e.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              ot[(16 * qq + 4 * t4 + k) * 128 + lrow] = __float2bfloat16_rn(fmaf(o1[4 * t4 + k], ev[k], o2[4 * t4 + k]));
+              ot[(16 * qq + 4 * t4 + k) * 128 + lrow] =
+                  __float2bfloat16_rn(fmaf(o1[4 * t4 + k] * o1_f, ev[k], o2[4 * t4 + k] * o2_f));
           }
-          const int32_t cid = ckpt_slot(c_begin + i);
-          if (cid >= 0) {
-            const auto K = GDN_GV(p.ck_ssm, p.ck_num_slots * slot_n) + ((size_t)cid * slot_n + tile_off);
+          // the block boundary at this chunk's end (a sequence that ends
+          // inside the chunk does not reach it)
+          if (to_ckpt-- == 0) {
+            to_ckpt = kpc - 1;
+            if (ck_idx < p.max_ckpt && P0 + (int64_t)(i + 1) * kC <= s.p1) {
+              const int32_t cid = GDN_GV(p.ckpt_ids, (long long)p.n_seq * p.max_ckpt)[(size_t)n * p.max_ckpt + ck_idx];
+              if (slot_class(cid, p.ck_num_slots) == 0) {
+                const auto K = GDN_GV(p.ck_ssm, p.ck_num_slots * slot_n) + ((size_t)cid * slot_n + tile_off);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              vec_at<float4>(K, 4 * e) = make_float4(st[4 * e], st[4 * e + 1], st[4 * e + 2], st[4 * e + 3]);
+                for (int e = 0; e < 8; ++e)
+                  vec_at<float4>(K, 4 * e) = make_float4(st[4 * e], st[4 * e + 1], st[4 * e + 2], st[4 * e + 3]);
+              }
+            }
+            ++ck_idx;
           }
         }
         if (i + 1 < nit) operands(i + 1);
@@ -955,7 +1057,7 @@ __global__ void __launch_bounds__(256) ssm_check_kernel(const PrefillArgs p) {
 }
 
 struct Layout {
-  size_t rec, kscale, state, decay, total;
+  size_t rec, state, decay, total;
   int64_t n_chunks, n_segs;
   int32_t seg_chunks;
 };
@@ -970,7 +1072,6 @@ Layout layout(const gdn_dims& d, int32_t n_seq, int64_t total) {
   l.n_segs = l.n_chunks / l.seg_chunks + n_seq;
   size_t off = 0;
   l.rec = off; off += sizeof(Record) * (size_t)l.n_chunks * d.hk;
-  l.kscale = off; off += up256(sizeof(float) * (size_t)l.n_chunks * d.hk);
   l.state = off;
   if (l.seg_chunks < l.n_chunks) {
     off += sizeof(float) * (size_t)l.n_segs * d.hv * d.dv * d.dk;
@@ -1019,7 +1120,6 @@ cudaError_t ssm_chunk_launch(const ssm::PrefillArgs& p, const gdn_dims& d, void*
   a.p = p;
   uint8_t* const ws = reinterpret_cast<uint8_t*>(((uintptr_t)workspace + 1023) & ~(uintptr_t)1023);
   a.rec = reinterpret_cast<Record*>(ws + l.rec);
-  a.kscale = reinterpret_cast<float*>(ws + l.kscale);
   a.seg_state = reinterpret_cast<float*>(ws + l.state);
   a.seg_decay = reinterpret_cast<float*>(ws + l.decay);
   a.n_chunks = (int32_t)l.n_chunks;
