@@ -27,8 +27,8 @@
 //                            accumulation never touches the long-lived state
 //   All operands are fp16 (kind::f16, four times the measured rate of
 //   kind::tf32 at the same 11 bits) after exact power-of-two scalings that
-//   keep any input range: by the largest |q|, |k|, |v| and |v w| of a chunk,
-//   and by upper bounds of |P| and |S|.  A bound may be loose by 2^14: fp16
+//   keep any input range: by the largest |q|, |k| and |v| of a chunk, and by
+//   upper bounds of |v w|, |P| and |S|.  A bound may be loose by 2^14: fp16
 //   keeps 11 bits over 29 binades.  Roundings: the output products' operands
 //   to 11 bits (a relative 2^-12 of their terms, against 2^-9 of the bf16
 //   output); the state's operands to two halves each, 22 bits, in three
@@ -396,8 +396,8 @@ struct __align__(1024) ChainSmem {
   float w[4][NH][kC];                 // e^{b_last - b} dt
   float dec[4][NH];                   // e^{b_last}
   float dtm[4][NH];                   // the largest dt
-  uint32_t vmax[3][2];                // largest |V w|, |V| of a chunk (mod 3), float bits
-  uint32_t vfin[2];                   //   the same over finite values, where one is not
+  uint32_t vmax[3];                   // largest |V| of a chunk (mod 3), float bits
+  uint32_t vfin;                      //   the same over finite values, where one is not
   uint64_t x_bar[2], g_bar[2], qk_bar[2], ready, mma_bar;
   uint32_t smax;                      // largest |S| entering the segment
   uint32_t tmem_base;
@@ -470,6 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ssm_chain_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap xmap,
                      const __grid_constant__ CUtensorMap omap) {
   constexpr int DV = 128 / NH;
+  constexpr int kBarAll = kCompute + 32 * NH;  // the compute and gate warps' barrier
   using SM = ChainSmem<NH>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   SM& S = *reinterpret_cast<SM*>(smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023));
@@ -506,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&S.ready, kCompute / 32);
     mbar_init(&S.mma_bar, 1);
 #pragma unroll
-    for (int i = 0; i < 3; ++i) S.vmax[i][0] = S.vmax[i][1] = 0;
+    for (int i = 0; i < 3; ++i) S.vmax[i] = 0;
     S.smax = 0;
     fence_mbar_init();
   }
@@ -522,113 +523,184 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------ issuer
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kIssuerRegs));
     if (warp == kCompute / 32) {
-    constexpr uint32_t ID_O1 = umma::idesc_f16(128, kC, false, false);
-    constexpr uint32_t ID_O2 = umma::idesc_f16(128, NH * kC, false, false);
-    constexpr uint32_t ID_S = umma::idesc_f16(128, kDK, false, false);
-    const int64_t rec0 = (s.first + c_begin) * p.hk + hq;
-    auto bulk = [&](void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-      mbar_arrive_expect_tx(bar, bytes);
-      if (GDN_GBYTES(src, bytes, a.rec, (long long)a.n_chunks * p.hk * sizeof(Record)) && GDN_SBYTES(dst, bytes, S))
-        bulk_g2s(dst, src, bytes, bar);
-    };
-    // raw V rows, and G with its exponents, of the segment's chunk i (lane 0)
-    auto load_xg = [&](int i) {
-      const int32_t row0 = (int32_t)(s.t0 + (P0 + (int64_t)i * kC - 3 - s.p0));  // may be < 0: zeros
-      mbar_arrive_expect_tx(&S.x_bar[i & 1], (uint32_t)sizeof(S.raw[0]));
-      if (GDN_SPAN_G(2 * p.hk * kDK + tile * 128, 128, p.C) && GDN_SBYTES(&S.raw[i & 1][0][0], sizeof(S.raw[0]), S))
-        tma_load_2d(&S.raw[i & 1][0][0], &xmap, 2 * p.hk * kDK + tile * 128, row0, &S.x_bar[i & 1]);
-      bulk(&S.g[i & 1], a.rec[rec0 + (int64_t)i * p.hk].g, kGMBytes, &S.g_bar[i & 1]);
-    };
-    // q and k (the state alone needs only k)
-    constexpr uint32_t kSkip = STATE ? sizeof(Record::q) : 0;
-    auto load_qk = [&](int i) {
-      bulk(S.qk[i & 1] + kSkip, a.rec[rec0 + (int64_t)i * p.hk].q + kSkip, kQKBytes - kSkip, &S.qk_bar[i & 1]);
-    };
-    int n_xg = 0, n_qk = 0, n_mma = 0;  // issued
-    if (lane == 0) {
-      for (; n_xg < 2 && n_xg < nit; ++n_xg) load_xg(n_xg);
-      for (; n_qk < 2 && n_qk < nit; ++n_qk) load_qk(n_qk);
-    }
-    bool ok = true;
-    // pass i: chunk i's operands are in place (and chunk i - 1's output staged)
-    for (int i = 0; i < nit + (STATE ? 0 : 1) && ok; ++i) {
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&S.ready, i & 1)))) break;
-      umma::fence_after();
-      if (lane == 0 && i < nit) {
-        if (i + 2 < nit) {  // chunk i's raw rows and G have been read
-          load_xg(i + 2);
-          n_xg = i + 3;
-        }
-        if ((ok = mbar_wait(&S.qk_bar[i & 1], (i >> 1) & 1))) {
-          umma::fence_after();
-          const uint64_t dq = umma::desc(smem_addr(S.qk[i & 1]), 16, 1024);
-          const uint64_t dh = umma::adv(dq, offsetof(Record, kh)), dl = umma::adv(dq, offsetof(Record, kl));
-          if (!STATE) {
-            // O1^T = S^T Q^T, O2^T = V^T P^T
+      constexpr uint32_t ID_O1 = umma::idesc_f16(128, kC, false, false);
+      constexpr uint32_t ID_O2 = umma::idesc_f16(128, NH * kC, false, false);
+      constexpr uint32_t ID_S = umma::idesc_f16(128, kDK, false, false);
+      const int64_t rec0 = (s.first + c_begin) * p.hk + hq;
+      auto bulk = [&](void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+        mbar_arrive_expect_tx(bar, bytes);
+        if (GDN_GBYTES(src, bytes, a.rec, (long long)a.n_chunks * p.hk * sizeof(Record)) && GDN_SBYTES(dst, bytes, S))
+          bulk_g2s(dst, src, bytes, bar);
+      };
+      // raw V rows, and G with its exponents, of the segment's chunk i (lane 0)
+      auto load_xg = [&](int i) {
+        const int32_t row0 = (int32_t)(s.t0 + (P0 + (int64_t)i * kC - 3 - s.p0));  // may be < 0: zeros
+        mbar_arrive_expect_tx(&S.x_bar[i & 1], (uint32_t)sizeof(S.raw[0]));
+        if (GDN_SPAN_G(2 * p.hk * kDK + tile * 128, 128, p.C) && GDN_SBYTES(&S.raw[i & 1][0][0], sizeof(S.raw[0]), S))
+          tma_load_2d(&S.raw[i & 1][0][0], &xmap, 2 * p.hk * kDK + tile * 128, row0, &S.x_bar[i & 1]);
+        bulk(&S.g[i & 1], a.rec[rec0 + (int64_t)i * p.hk].g, kGMBytes, &S.g_bar[i & 1]);
+      };
+      // q and k (the state alone needs only k)
+      constexpr uint32_t kSkip = STATE ? sizeof(Record::q) : 0;
+      auto load_qk = [&](int i) {
+        bulk(S.qk[i & 1] + kSkip, a.rec[rec0 + (int64_t)i * p.hk].q + kSkip, kQKBytes - kSkip, &S.qk_bar[i & 1]);
+      };
+      int n_xg = 0, n_qk = 0, n_mma = 0;  // issued
+      if (lane == 0) {
+        for (; n_xg < 2 && n_xg < nit; ++n_xg) load_xg(n_xg);
+        for (; n_qk < 2 && n_qk < nit; ++n_qk) load_qk(n_qk);
+      }
+      bool ok = true;
+      // pass i: chunk i's operands are in place (and chunk i - 1's output staged)
+      for (int i = 0; i < nit + (STATE ? 0 : 1) && ok; ++i) {
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&S.ready, i & 1)))) break;
+        umma::fence_after();
+        if (lane == 0 && i < nit) {
+          if (i + 2 < nit) {  // chunk i's raw rows and G have been read
+            load_xg(i + 2);
+            n_xg = i + 3;
+          }
+          if ((ok = mbar_wait(&S.qk_bar[i & 1], (i >> 1) & 1))) {
+            umma::fence_after();
+            const uint64_t dq = umma::desc(smem_addr(S.qk[i & 1]), 16, 1024);
+            const uint64_t dh = umma::adv(dq, offsetof(Record, kh)), dl = umma::adv(dq, offsetof(Record, kl));
+            if (!STATE) {
+              // O1^T = S^T Q^T, O2^T = V^T P^T
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_f16_ta(tmem + TM_O1, tmem + TM_S + 8 * k, umma::adv(dq, (k >> 2) * 8192 + (k & 3) * 32), ID_O1, k > 0);
-            const uint64_t dp = umma::desc(smem_addr(S.pt[i & 1]), 16, 1024);
+              for (int k = 0; k < 8; ++k)
+                mma_f16_ta(tmem + TM_O1, tmem + TM_S + 8 * k, umma::adv(dq, (k >> 2) * 8192 + (k & 3) * 32), ID_O1, k > 0);
+              const uint64_t dp = umma::desc(smem_addr(S.pt[i & 1]), 16, 1024);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_f16_ta(tmem + TM_O2, tmem + TM_V + 8 * k, umma::adv(dp, 32 * k), ID_O2, k > 0);
+            }
+            // dS^T = (V w)^T K, small products first
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_f16_ta(tmem + TM_O2, tmem + TM_V + 8 * k, umma::adv(dp, 32 * k), ID_O2, k > 0);
+              mma_f16_ta(tmem + TM_DS, tmem + TM_WL + 8 * k, umma::adv(dh, 32 * k), ID_S, k > 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_f16_ta(tmem + TM_DS, tmem + TM_WH + 8 * k, umma::adv(dl, 32 * k), ID_S, true);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_f16_ta(tmem + TM_DS, tmem + TM_WH + 8 * k, umma::adv(dh, 32 * k), ID_S, true);
           }
-          // dS^T = (V w)^T K, small products first
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_f16_ta(tmem + TM_DS, tmem + TM_WL + 8 * k, umma::adv(dh, 32 * k), ID_S, k > 0);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_f16_ta(tmem + TM_DS, tmem + TM_WH + 8 * k, umma::adv(dl, 32 * k), ID_S, true);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_f16_ta(tmem + TM_DS, tmem + TM_WH + 8 * k, umma::adv(dh, 32 * k), ID_S, true);
         }
-      }
-      if constexpr (!STATE) {
-        // chunk i - 1's staged output
-        if (i > 0) {
-          const int64_t P = P0 + (int64_t)(i - 1) * kC;
-          const int tlo = (int)max((int64_t)0, s.p0 - P), thi = (int)min((int64_t)kC, s.p1 - P);
-          if (tlo == 0 && thi == kC) {
-            if (lane == 0 && GDN_SPAN_G(s.t0 + (P - s.p0), kC, p.total)) {
-              tma_store_2d(&omap, &S.ot[0][0], tile * 128, (int32_t)(s.t0 + (P - s.p0)));
-              bulk_commit();
+        if constexpr (!STATE) {
+          // chunk i - 1's staged output
+          if (i > 0) {
+            const int64_t P = P0 + (int64_t)(i - 1) * kC;
+            const int tlo = (int)max((int64_t)0, s.p0 - P), thi = (int)min((int64_t)kC, s.p1 - P);
+            if (tlo == 0 && thi == kC) {
+              if (lane == 0 && GDN_SPAN_G(s.t0 + (P - s.p0), kC, p.total)) {
+                tma_store_2d(&omap, &S.ot[0][0], tile * 128, (int32_t)(s.t0 + (P - s.p0)));
+                bulk_commit();
+              }
+            } else {
+              const auto ot = GDN_SV(&S.ot[0][0], kC * 128);
+              const auto out = GDN_GV(reinterpret_cast<__nv_bfloat16*>(p.out), p.total * p.hv * DV);
+              for (int r = tlo + (lane >> 4); r < thi; r += 2)
+                vec_at<uint4>(out, ((s.t0 + P - s.p0 + r) * p.hv) * DV + tile * 128 + 8 * (lane & 15)) =
+                    vec_at<const uint4>(ot, r * 128 + 8 * (lane & 15));
+              __syncwarp();
             }
-          } else {
-            const auto ot = GDN_SV(&S.ot[0][0], kC * 128);
-            const auto out = GDN_GV(reinterpret_cast<__nv_bfloat16*>(p.out), p.total * p.hv * DV);
-            for (int r = tlo + (lane >> 4); r < thi; r += 2)
-              vec_at<uint4>(out, ((s.t0 + P - s.p0 + r) * p.hv) * DV + tile * 128 + 8 * (lane & 15)) =
-                  vec_at<const uint4>(ot, r * 128 + 8 * (lane & 15));
-            __syncwarp();
           }
         }
+        if (lane == 0 && i < nit && ok) {
+          bulk_wait_read();  // the staging may be written once this chunk's products are known to be done
+          umma::commit(&S.mma_bar);
+          ++n_mma;
+          if ((ok = mbar_wait(&S.mma_bar, i & 1)) && i + 2 < nit) {
+            load_qk(i + 2);
+            n_qk = i + 3;
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
       }
-      if (lane == 0 && i < nit && ok) {
-        bulk_wait_read();  // the staging may be written once this chunk's products are known to be done
-        umma::commit(&S.mma_bar);
-        ++n_mma;
-        if ((ok = mbar_wait(&S.mma_bar, i & 1)) && i + 2 < nit) {
-          load_qk(i + 2);
-          n_qk = i + 3;
+      if (lane == 0) {
+        if (!ok) {
+          // a wait expired: let what is in flight land before the memory goes
+          report(p.err, GDN_DEV_ERR_TIMEOUT);
+          for (int k = max(0, n_xg - 2); k < n_xg; ++k) {
+            mbar_wait(&S.x_bar[k & 1], (k >> 1) & 1);
+            mbar_wait(&S.g_bar[k & 1], (k >> 1) & 1);
+          }
+          for (int k = max(0, n_qk - 2); k < n_qk; ++k) mbar_wait(&S.qk_bar[k & 1], (k >> 1) & 1);
+          if (n_mma) mbar_wait(&S.mma_bar, (n_mma - 1) & 1);
+        }
+        bulk_wait_all();
+      }
+    } else if (warp <= kCompute / 32 + NH) {
+      // gates, one warp per head, two chunks ahead of the products; two tokens
+      // per lane, their logits loaded one chunk earlier still
+      const int ghl = warp - kCompute / 32 - 1, gh = h0 + ghl;
+      const auto gate_a = GDN_GV(reinterpret_cast<const __nv_bfloat16*>(p.a), p.total * p.hv);
+      float ga[2] = {0.f, 0.f};
+      auto gate_load = [&](int i) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int64_t m = P0 + (int64_t)i * kC + 32 * e + lane - s.p0;
+          ga[e] = i < nit && m >= 0 && m < s.len ? __bfloat162float(gate_a[(s.t0 + m) * p.hv + gh]) : 0.f;
+        }
+      };
+      const float A_log = GDN_GV(p.A_log, p.hv)[gh], dtb = GDN_GV(p.dt_bias, p.hv)[gh];
+      auto gates = [&](int i) {
+        const int buf = i & 3;
+        float dt[2], b[2], suf[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int64_t m = P0 + (int64_t)i * kC + 32 * e + lane - s.p0;
+          const bool in = m >= 0 && m < s.len;
+          const Gate t = gate(A_log, dtb, ga[e]);
+          dt[e] = in ? t.dt : 0.f;
+          b[e] = suf[e] = in ? floor_log_decay(t.g) : 0.f;
+        }
+        gate_load(i + 1);
+        // sums from the front and from the back: b_last - b_j is a sum of its
+        // own, exact to its own size whatever b_last is
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float u = __shfl_up_sync(0xffffffffu, b[e], o), v = __shfl_down_sync(0xffffffffu, suf[e], o);
+            if (lane >= o) b[e] += u;
+            if (lane + o < 32) suf[e] += v;
+          }
+        }
+        b[1] += __shfl_sync(0xffffffffu, b[0], 31);
+        const float back = __shfl_sync(0xffffffffu, suf[1], 0), all = back + __shfl_sync(0xffffffffu, suf[0], 0);
+        float m = fmaxf(dt[0], dt[1]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float nx = __shfl_down_sync(0xffffffffu, suf[0], 1), ny = __shfl_down_sync(0xffffffffu, suf[1], 1);
+        suf[0] = (lane < 31 ? nx : 0.f) + back;
+        suf[1] = lane < 31 ? ny : 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int t = 32 * e + lane;
+          const float b2 = b[e] * 1.4426950408889634f;
+          S.b2[buf][ghl][t] = b2;
+          S.v[buf][ghl][t] = ex2(__shfl_sync(0xffffffffu, b2, lane | 15) - b2) * dt[e];
+          S.eb[buf][ghl][t] = expf(b[e]);
+          S.dt[buf][ghl][t] = dt[e];
+          S.w[buf][ghl][t] = expf(suf[e]) * dt[e];
+        }
+        if (lane == 0) {
+          S.dec[buf][ghl] = expf(all);
+          S.dtm[buf][ghl] = m;
+        }
+      };
+      gate_load(0);
+      gates(0);
+      if (nit > 1) gates(1);
+      named_sync(1, kBarAll);
+      if (!named_sync_or(1, kBarAll, false)) {
+        for (int i = 0; i < nit; ++i) {
+          if (i + 2 < nit) gates(i + 2);
+          if (named_sync_or(1, kBarAll, false)) break;
         }
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-    }
-    if (lane == 0) {
-      if (!ok) {
-        // a wait expired: let what is in flight land before the memory goes
-        report(p.err, GDN_DEV_ERR_TIMEOUT);
-        for (int k = max(0, n_xg - 2); k < n_xg; ++k) {
-          mbar_wait(&S.x_bar[k & 1], (k >> 1) & 1);
-          mbar_wait(&S.g_bar[k & 1], (k >> 1) & 1);
-        }
-        for (int k = max(0, n_qk - 2); k < n_qk; ++k) mbar_wait(&S.qk_bar[k & 1], (k >> 1) & 1);
-        if (n_mma) mbar_wait(&S.mma_bar, (n_mma - 1) & 1);
-      }
-      bulk_wait_all();
-    }
+      named_sync_or(1, kBarAll, false);
     }
   } else {
     // ----------------------------------------------------------------- compute
@@ -638,72 +710,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int hl = lrow / DV;                 // this row's head within the tile
     const uint32_t tlane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const int ch = 2 * p.hk * kDK + tile * 128 + lrow;
-
-    // gates: warps 8 and 10, which have no part in P; two tokens per lane,
-    // their logits loaded one chunk ahead
-    const bool gate_warp = warp == 8 || (NH == 2 && warp == 10);
-    const int gh = h0 + (warp == 10 ? NH - 1 : 0), ghl = gh - h0;
-    const auto gate_a = GDN_GV(reinterpret_cast<const __nv_bfloat16*>(p.a), p.total * p.hv);
-    float ga[2] = {0.f, 0.f};
-    auto gate_load = [&](int i) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int64_t m = P0 + (int64_t)i * kC + 32 * e + lane - s.p0;
-        ga[e] = i < nit && m >= 0 && m < s.len ? __bfloat162float(gate_a[(s.t0 + m) * p.hv + gh]) : 0.f;
-      }
-    };
-    const float A_log = GDN_GV(p.A_log, p.hv)[gh], dtb = GDN_GV(p.dt_bias, p.hv)[gh];
-    auto gates = [&](int i) {
-      const int buf = i & 3;
-      float dt[2], b[2], suf[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int64_t m = P0 + (int64_t)i * kC + 32 * e + lane - s.p0;
-        const bool in = m >= 0 && m < s.len;
-        const Gate t = gate(A_log, dtb, ga[e]);
-        dt[e] = in ? t.dt : 0.f;
-        b[e] = suf[e] = in ? floor_log_decay(t.g) : 0.f;
-      }
-      gate_load(i + 1);
-      // sums from the front and from the back: b_last - b_j is a sum of its
-      // own, exact to its own size whatever b_last is
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float u = __shfl_up_sync(0xffffffffu, b[e], o), v = __shfl_down_sync(0xffffffffu, suf[e], o);
-          if (lane >= o) b[e] += u;
-          if (lane + o < 32) suf[e] += v;
-        }
-      }
-      b[1] += __shfl_sync(0xffffffffu, b[0], 31);
-      const float back = __shfl_sync(0xffffffffu, suf[1], 0), all = back + __shfl_sync(0xffffffffu, suf[0], 0);
-      float m = fmaxf(dt[0], dt[1]);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float nx = __shfl_down_sync(0xffffffffu, suf[0], 1), ny = __shfl_down_sync(0xffffffffu, suf[1], 1);
-      suf[0] = (lane < 31 ? nx : 0.f) + back;
-      suf[1] = lane < 31 ? ny : 0.f;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int t = 32 * e + lane;
-        const float b2 = b[e] * 1.4426950408889634f;
-        S.b2[buf][ghl][t] = b2;
-        S.v[buf][ghl][t] = ex2(__shfl_sync(0xffffffffu, b2, lane | 15) - b2) * dt[e];
-        S.eb[buf][ghl][t] = expf(b[e]);
-        S.dt[buf][ghl][t] = dt[e];
-        S.w[buf][ghl][t] = expf(suf[e]) * dt[e];
-      }
-      if (lane == 0) {
-        S.dec[buf][ghl] = expf(all);
-        S.dtm[buf][ghl] = m;
-      }
-    };
-    if (gate_warp) {
-      gate_load(0);
-      gates(0);
-      if (nit > 1) gates(1);
-    }
 
     // the state entering the segment, S^T row lrow, columns 32 qq ..
     float st[32];
@@ -800,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             S.raw[i & 1][GDN_S((int)(pos - (P - 3)), kRawRows)][tid] =
                 hist[(size_t)(3 - (s.p0 - pos)) * p.C + 2 * p.hk * kDK + tile * 128 + tid];
         umma::fence_proxy_async();  // before a later chunk's copy into these rows
-        named_sync(1, kCompute);
+        named_sync(2, kCompute);
       }
       {
         const auto xs = GDN_SV(&S.raw[i & 1][0][0], kRawRows * 128) + (16 * qq * 128 + lrow);
@@ -823,20 +829,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (16 * qq + t < tlo || 16 * qq + t >= thi) y[t] = 0.f;
       }
       {
-        float x[16];
-        weights(i, x);
-        uint32_t m = 0, mv = 0;
+        uint32_t m = 0;
 #pragma unroll
-        for (int t = 0; t < 16; ++t) {
-          m = max(m, __float_as_uint(x[t]) & 0x7fffffffu);
-          if (!STATE) mv = max(mv, __float_as_uint(y[t]) & 0x7fffffffu);
-        }
+        for (int t = 0; t < 16; ++t) m = max(m, __float_as_uint(y[t]) & 0x7fffffffu);
         m = __reduce_max_sync(0xffffffffu, m);
-        if (!STATE) mv = __reduce_max_sync(0xffffffffu, mv);
-        if (lane == 0) {
-          atomicMax(&S.vmax[i % 3][0], m);
-          if (!STATE) atomicMax(&S.vmax[i % 3][1], mv);
-        }
+        if (lane == 0) atomicMax(&S.vmax[i % 3], m);
       }
       if (!mbar_wait(&S.g_bar[i & 1], (i >> 1) & 1)) bad = true;
       qe = S.g[i & 1].meta[0];
@@ -898,8 +895,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                            half2_bits(e[8 * c8 + 4], e[8 * c8 + 5]), half2_bits(e[8 * c8 + 6], e[8 * c8 + 7]));
         }
       }
-      if (gate_warp && i + 1 < nit && i > 0) gates(i + 1);
-      if (tid == 0) S.vmax[(i + 1) % 3][0] = S.vmax[(i + 1) % 3][1] = 0;
+      if (tid == 0) S.vmax[(i + 1) % 3] = 0;
     };
     float s_bound = 0.f;  // >= |S|
     // of the operands in TMEM: factors that take the products back
@@ -908,29 +904,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto operands = [&](int i) {
       float x[16];
       weights(i, x);
-      uint32_t m = S.vmax[i % 3][0], mv = S.vmax[i % 3][1];
-      if (max(m, mv) >= 0x7f800000u) {
-        // infinite or NaN values among them: the scales of the finite ones
-        named_sync(1, kCompute);
-        if (tid == 0) S.vfin[0] = S.vfin[1] = 0;
-        named_sync(1, kCompute);
-        m = mv = 0;
+      uint32_t m = S.vmax[i % 3];
+      if (m >= 0x7f800000u) {
+        // infinite or NaN values among V: the scale of the finite ones
+        named_sync(2, kCompute);
+        if (tid == 0) S.vfin = 0;
+        named_sync(2, kCompute);
+        m = 0;
 #pragma unroll
         for (int t = 0; t < 16; ++t) {
-          const uint32_t u = __float_as_uint(x[t]) & 0x7fffffffu, v = __float_as_uint(y[t]) & 0x7fffffffu;
+          const uint32_t u = __float_as_uint(y[t]) & 0x7fffffffu;
           m = max(m, u < 0x7f800000u ? u : 0u);
-          mv = max(mv, v < 0x7f800000u ? v : 0u);
         }
-        atomicMax(&S.vfin[0], m);
-        atomicMax(&S.vfin[1], mv);
-        named_sync(1, kCompute);
-        m = S.vfin[0];
-        mv = S.vfin[1];
+        atomicMax(&S.vfin, m);
+        named_sync(2, kCompute);
+        m = S.vfin;
       }
-      const int ve = scale_exp(m);
+      // |V w| <= max|V| max dt, for both heads
+      const float dtm = NH == 2 ? fmaxf(S.dtm[i & 3][0], S.dtm[i & 3][NH - 1]) : S.dtm[i & 3][0];
+      const float vw = __uint_as_float(m) * dtm;
+      const int ve = scale_exp(__float_as_uint(vw));
       __syncwarp();
       if constexpr (!STATE) {
-        const int se = scale_exp(__float_as_uint(s_bound)), vse = scale_exp(mv);
+        const int se = scale_exp(__float_as_uint(s_bound)), vse = scale_exp(m);
         const float fs = exp2_int(se), fv = exp2_int(vse);
         uint32_t r[16], v[8];
 #pragma unroll
@@ -951,7 +947,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ds_f = exp2_int(-ve) * exp2_int(-ke);
       // |S| after the chunk: 64 terms of at most max|V w| max|k|
       const float dm = NH == 2 ? fmaxf(S.dec[i & 3][0], S.dec[i & 3][NH - 1]) : S.dec[i & 3][0];
-      s_bound = fmaf(s_bound, dm, 64.f * __uint_as_float(m) * exp2_int(max(-126, min(127, 15 - ke))));
+      s_bound = fmaf(s_bound, dm, 64.f * vw * exp2_int(max(-126, min(127, 15 - ke))));
       tmem_wait_st();
     };
     auto publish = [&]() {
@@ -961,16 +957,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&S.ready);
     };
 
-    named_sync(1, kCompute);  // the first gates
+    named_sync(1, kBarAll);  // the first gates
     features(0);
     int i = 0;
-    if (!named_sync_or(1, kCompute, bad)) {
+    if (!named_sync_or(1, kBarAll, bad)) {
       s_bound = __uint_as_float(S.smax);
       operands(0);
       publish();
       for (; i < nit; ++i) {
         if (i + 1 < nit) features(i + 1);
-        if (named_sync_or(1, kCompute, bad)) break;
+        if (named_sync_or(1, kBarAll, bad)) break;
         if (!mbar_wait(&S.mma_bar, i & 1)) bad = true;
         __syncwarp();
         umma::fence_after();
@@ -1016,7 +1012,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (i + 1 < nit || !STATE) publish();
       }
     }
-    bad = named_sync_or(1, kCompute, bad);
+    bad = named_sync_or(1, kBarAll, bad);
     if (i == nit && !bad) {
       if (STATE) {
         const auto L = segs + ((seg_first + seg) * slot_n + (int64_t)tile_off);
