@@ -145,10 +145,10 @@ __device__ __forceinline__ int scale_exp(uint32_t m_bits) {
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 // two values as fp16 high halves and the low halves that remain
-__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
-  const __half2 h = __floats2half2_rn(x, y);
-  const float2 f = __half22float2(h);
-  const __half2 l = __floats2half2_rn(x - f.x, y - f.y);
+__device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x.x, x.y);
+  const float2 r = fma2(__half22float2(h), make_float2(-1.f, -1.f), x);
+  const __half2 l = __floats2half2_rn(r.x, r.y);
   hi = *reinterpret_cast<const uint32_t*>(&h);
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
@@ -301,8 +301,8 @@ __global__ void __launch_bounds__(kFT, 2) ssm_features_kernel(const ChunkArgs a)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 u = y[8 * t8 + 2 * i], v = y[8 * t8 + 2 * i + 1];
-        split2(u.x, v.x, h0[i], l0[i]);
-        split2(u.y, v.y, h1[i], l1[i]);
+        split2(make_float2(u.x, v.x), h0[i], l0[i]);
+        split2(make_float2(u.y, v.y), h1[i], l1[i]);
       }
       const uint32_t o0 = umma::sw128_off(2 * cp, 32 * half + 8 * t8, 0),
                      o1 = umma::sw128_off(2 * cp + 1, 32 * half + 8 * t8, 0);
@@ -354,13 +354,18 @@ static_assert(offsetof(FeatSmem, meta) == offsetof(FeatSmem, g) + kGBytes && off
 // ---------------------------------------------------------------------------
 // the chain
 // ---------------------------------------------------------------------------
-// Sixteen warps do the elementwise work; a seventeenth (the issuer, in a
-// warpgroup of its own whose registers go to the others) issues every copy and
-// product, because a thread that issues products is held up about as long as
-// they run.  While the tensor core runs chunk c's products,
-// the sixteen warps compute chunk c + 1's V (kept in registers) and P (the
-// other of two buffers) and the gates of chunk c + 2; then they take chunk
-// c's results and put chunk c + 1's operands in their place.
+// Twenty warps, with no barrier among them after the start, only mbarriers:
+//   0..15    compute: while the tensor core runs chunk i's products, V (kept
+//            in registers) and P (the other of two buffers) of chunk i + 1;
+//            then chunk i's results out of TMEM, the state, and chunk i + 1's
+//            operands in their place
+//   16       issuer: every product and the copies of q and k (a thread that
+//            issues products is held up about as long as they run), and the
+//            output stores
+//   17, 18   gates and scales of one head each
+//   19       loader: the copies of raw V rows and G, the three rows before a
+//            sequence from the conv history, and the largest raw input
+// The last four give their registers to the compute warps.
 constexpr int kCompute = 512;
 constexpr int kThreads = kCompute + 128;
 // Registers per thread after the split of the launch's 640 x 96: the compute
@@ -378,6 +383,19 @@ constexpr uint32_t TM_WH = 416;  // (V w)^T fp16: high halves, 32 columns
 constexpr uint32_t TM_WL = 448;  //   low halves
 constexpr uint32_t TM_COLS = 512;
 
+// Per chunk and head: e^{b_last}; with V 2^ve, (V w) 2^we, P 2^pe, q 2^qe,
+// k 2^ke the operands, the factors that take the products back and forth.
+struct __align__(16) Scales {
+  float dec;    // e^{b_last}
+  float ds;     // 2^-(we + ke)
+  float o2;     // 2^-(ve + pe)
+  float q;      // 2^-qe
+  float grow;   // bound of what the chunk adds to |S|
+  float v;      // 2^-ve
+  float p;      // 2^(22 - qe - ke + pe): from the stored G to P 2^pe
+  float skip;   // D 2^pe
+};
+
 template <int NH>
 struct __align__(1024) ChainSmem {
   uint8_t qk[2][kQKBytes];         // q, kh, kl
@@ -393,13 +411,16 @@ struct __align__(1024) ChainSmem {
   float eb[4][NH][kC];                // e^b
   float dt[4][NH][kC];
   float v[4][NH][kC];                 // e^{b' - b} dt, b' at the end of the token's 16-token block
-  float w[4][NH][kC];                 // e^{b_last - b} dt
-  float dec[4][NH];                   // e^{b_last}
-  float dtm[4][NH];                   // the largest dt
-  uint32_t vmax[3];                   // largest |V| of a chunk (mod 3), float bits
-  uint32_t vfin;                      //   the same over finite values, where one is not
-  uint64_t x_bar[2], g_bar[2], qk_bar[2], ready, mma_bar;
-  uint32_t smax;                      // largest |S| entering the segment
+  float w[4][NH][kC];                 // e^{b_last - b} dt 2^(we - ve)
+  Scales sc[4][NH];
+  float xmax[2];                      // largest raw input of a chunk (mod 2)
+  float vgain, vbias;                 // |V| <= vgain xmax + vbias
+  uint32_t smax[NH];                  // largest |S| entering the segment, float bits
+  uint64_t x_bar[2], g_bar[2], qk_bar[2];  // copies landed
+  uint64_t hx[2];                     // xmax known, history rows in place
+  uint64_t gx[2];                     // gates and scales known
+  uint64_t used[2];                   // raw rows and G read
+  uint64_t ready, mma_bar;            // operands in place; products done
   uint32_t tmem_base;
   int seq;
 };
@@ -470,7 +491,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     ssm_chain_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap xmap,
                      const __grid_constant__ CUtensorMap omap) {
   constexpr int DV = 128 / NH;
-  constexpr int kBarAll = kCompute + 32 * NH;  // the compute and gate warps' barrier
   using SM = ChainSmem<NH>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   SM& S = *reinterpret_cast<SM*>(smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023));
@@ -503,12 +523,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.x_bar[i], 1);
       mbar_init(&S.g_bar[i], 1);
       mbar_init(&S.qk_bar[i], 1);
+      mbar_init(&S.hx[i], 1);
+      mbar_init(&S.gx[i], NH);
+      mbar_init(&S.used[i], kCompute / 32);
     }
     mbar_init(&S.ready, kCompute / 32);
     mbar_init(&S.mma_bar, 1);
 #pragma unroll
-    for (int i = 0; i < 3; ++i) S.vmax[i] = 0;
-    S.smax = 0;
+    for (int i = 0; i < NH; ++i) S.smax[i] = 0;
     fence_mbar_init();
   }
   umma::fence_before();
@@ -519,6 +541,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     TM_WH == TM_V + kC / 2 && TM_WL == TM_WH + kC / 2 && TM_WL + kC / 2 <= TM_COLS,
                 "TMEM regions");
 
+  const int64_t rec0 = (s.first + c_begin) * p.hk + hq;
+  auto bulk = [&](void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    mbar_arrive_expect_tx(bar, bytes);
+    if (GDN_GBYTES(src, bytes, a.rec, (long long)a.n_chunks * p.hk * sizeof(Record)) && GDN_SBYTES(dst, bytes, S))
+      bulk_g2s(dst, src, bytes, bar);
+  };
   if (warp >= kCompute / 32) {
     // ------------------------------------------------------------------ issuer
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kIssuerRegs));
@@ -526,28 +554,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t ID_O1 = umma::idesc_f16(128, kC, false, false);
       constexpr uint32_t ID_O2 = umma::idesc_f16(128, NH * kC, false, false);
       constexpr uint32_t ID_S = umma::idesc_f16(128, kDK, false, false);
-      const int64_t rec0 = (s.first + c_begin) * p.hk + hq;
-      auto bulk = [&](void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-        mbar_arrive_expect_tx(bar, bytes);
-        if (GDN_GBYTES(src, bytes, a.rec, (long long)a.n_chunks * p.hk * sizeof(Record)) && GDN_SBYTES(dst, bytes, S))
-          bulk_g2s(dst, src, bytes, bar);
-      };
-      // raw V rows, and G with its exponents, of the segment's chunk i (lane 0)
-      auto load_xg = [&](int i) {
-        const int32_t row0 = (int32_t)(s.t0 + (P0 + (int64_t)i * kC - 3 - s.p0));  // may be < 0: zeros
-        mbar_arrive_expect_tx(&S.x_bar[i & 1], (uint32_t)sizeof(S.raw[0]));
-        if (GDN_SPAN_G(2 * p.hk * kDK + tile * 128, 128, p.C) && GDN_SBYTES(&S.raw[i & 1][0][0], sizeof(S.raw[0]), S))
-          tma_load_2d(&S.raw[i & 1][0][0], &xmap, 2 * p.hk * kDK + tile * 128, row0, &S.x_bar[i & 1]);
-        bulk(&S.g[i & 1], a.rec[rec0 + (int64_t)i * p.hk].g, kGMBytes, &S.g_bar[i & 1]);
-      };
       // q and k (the state alone needs only k)
       constexpr uint32_t kSkip = STATE ? sizeof(Record::q) : 0;
       auto load_qk = [&](int i) {
         bulk(S.qk[i & 1] + kSkip, a.rec[rec0 + (int64_t)i * p.hk].q + kSkip, kQKBytes - kSkip, &S.qk_bar[i & 1]);
       };
-      int n_xg = 0, n_qk = 0, n_mma = 0;  // issued
+      int n_qk = 0, n_mma = 0;  // issued
       if (lane == 0) {
-        for (; n_xg < 2 && n_xg < nit; ++n_xg) load_xg(n_xg);
         for (; n_qk < 2 && n_qk < nit; ++n_qk) load_qk(n_qk);
       }
       bool ok = true;
@@ -556,10 +569,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&S.ready, i & 1)))) break;
         umma::fence_after();
         if (lane == 0 && i < nit) {
-          if (i + 2 < nit) {  // chunk i's raw rows and G have been read
-            load_xg(i + 2);
-            n_xg = i + 3;
-          }
           if ((ok = mbar_wait(&S.qk_bar[i & 1], (i >> 1) & 1))) {
             umma::fence_after();
             const uint64_t dq = umma::desc(smem_addr(S.qk[i & 1]), 16, 1024);
@@ -618,25 +627,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __shfl_sync(0xffffffffu, ok, 0);
       }
       if (lane == 0) {
-        if (!ok) {
-          // a wait expired: let what is in flight land before the memory goes
-          report(p.err, GDN_DEV_ERR_TIMEOUT);
-          for (int k = max(0, n_xg - 2); k < n_xg; ++k) {
-            mbar_wait(&S.x_bar[k & 1], (k >> 1) & 1);
-            mbar_wait(&S.g_bar[k & 1], (k >> 1) & 1);
-          }
-          for (int k = max(0, n_qk - 2); k < n_qk; ++k) mbar_wait(&S.qk_bar[k & 1], (k >> 1) & 1);
-          if (n_mma) mbar_wait(&S.mma_bar, (n_mma - 1) & 1);
-        }
+        if (!ok) report(p.err, GDN_DEV_ERR_TIMEOUT);
+        // what is in flight lands before the memory goes (at once, unless a wait expired)
+        for (int k = max(0, n_qk - 2); k < n_qk; ++k) mbar_wait(&S.qk_bar[k & 1], (k >> 1) & 1);
+        if (n_mma) mbar_wait(&S.mma_bar, (n_mma - 1) & 1);
         bulk_wait_all();
       }
     } else if (warp <= kCompute / 32 + NH) {
-      // gates, one warp per head, two chunks ahead of the products; two tokens
-      // per lane, their logits loaded one chunk earlier still
-      const int ghl = warp - kCompute / 32 - 1, gh = h0 + ghl;
+      // ----------------------------------------------------------------- gates
+      // two tokens per lane, their logits loaded one chunk ahead
+      const int hh = warp - kCompute / 32 - 1, gh = h0 + hh;
       const auto gate_a = GDN_GV(reinterpret_cast<const __nv_bfloat16*>(p.a), p.total * p.hv);
-      float ga[2] = {0.f, 0.f};
-      auto gate_load = [&](int i) {
+      auto gate_load = [&](int i, float (&ga)[2]) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int64_t m = P0 + (int64_t)i * kC + 32 * e + lane - s.p0;
@@ -644,8 +646,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       const float A_log = GDN_GV(p.A_log, p.hv)[gh], dtb = GDN_GV(p.dt_bias, p.hv)[gh];
-      auto gates = [&](int i) {
-        const int buf = i & 3;
+      const float D = p.D ? GDN_GV(p.D, p.hv)[gh] : 0.f;
+      float ga[2];
+      gate_load(0, ga);
+      bool ok = true;
+      for (int i = 0; i < nit && ok; ++i) {
         float dt[2], b[2], suf[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -655,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           dt[e] = in ? t.dt : 0.f;
           b[e] = suf[e] = in ? floor_log_decay(t.g) : 0.f;
         }
-        gate_load(i + 1);
+        gate_load(i + 1, ga);
         // sums from the front and from the back: b_last - b_j is a sum of its
         // own, exact to its own size whatever b_last is
 #pragma unroll
@@ -669,38 +674,141 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         b[1] += __shfl_sync(0xffffffffu, b[0], 31);
         const float back = __shfl_sync(0xffffffffu, suf[1], 0), all = back + __shfl_sync(0xffffffffu, suf[0], 0);
-        float m = fmaxf(dt[0], dt[1]);
+        float dtm = fmaxf(dt[0], dt[1]);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int o = 16; o; o >>= 1) dtm = fmaxf(dtm, __shfl_xor_sync(0xffffffffu, dtm, o));
         const float nx = __shfl_down_sync(0xffffffffu, suf[0], 1), ny = __shfl_down_sync(0xffffffffu, suf[1], 1);
         suf[0] = (lane < 31 ? nx : 0.f) + back;
         suf[1] = lane < 31 ? ny : 0.f;
+        float vj[2], wj[2], eb[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          wj[e] = expf(suf[e]) * dt[e];
+          eb[e] = expf(b[e]);
+          b[e] *= 1.4426950408889634f;
+          vj[e] = ex2(__shfl_sync(0xffffffffu, b[e], lane | 15) - b[e]) * dt[e];
+        }
+        // Chunk i's raw rows and G have landed: chunk i - 2's were read by
+        // every compute warp, whose chunk i - 4 was done before that, so the
+        // slot of chunk i - 4 may be written.
+        const bool in_time = mbar_wait(&S.hx[i & 1], (i >> 1) & 1) && mbar_wait(&S.g_bar[i & 1], (i >> 1) & 1);
+        if (!(ok = __all_sync(0xffffffffu, in_time))) break;
+        const int buf = i & 3, qe = S.g[i & 1].meta[0], ke = S.g[i & 1].meta[1];
+        // |V| <= vb, |V w| <= vb max dt,
+        // |P| <= 128 max|q| max|k| max dt + |D| < 2^(37 - qe - ke) max dt + |D|
+        const float vb = fmaf(S.vgain, S.xmax[i & 1], S.vbias);
+        const float gb = exp2_int(max(-126, min(127, 37 - qe - ke)));
+        const int ve = scale_exp(__float_as_uint(vb)), we = scale_exp(__float_as_uint(vb * dtm));
+        const int pe = scale_exp(__float_as_uint(fmaf(gb, dtm, fabsf(D))));
+        const float fw = exp2_int(max(-126, min(127, we - ve)));
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int t = 32 * e + lane;
-          const float b2 = b[e] * 1.4426950408889634f;
-          S.b2[buf][ghl][t] = b2;
-          S.v[buf][ghl][t] = ex2(__shfl_sync(0xffffffffu, b2, lane | 15) - b2) * dt[e];
-          S.eb[buf][ghl][t] = expf(b[e]);
-          S.dt[buf][ghl][t] = dt[e];
-          S.w[buf][ghl][t] = expf(suf[e]) * dt[e];
+          S.b2[buf][hh][t] = b[e];
+          S.v[buf][hh][t] = vj[e];
+          S.eb[buf][hh][t] = eb[e];
+          S.dt[buf][hh][t] = dt[e];
+          S.w[buf][hh][t] = wj[e] * fw;
         }
         if (lane == 0) {
-          S.dec[buf][ghl] = expf(all);
-          S.dtm[buf][ghl] = m;
+          Scales& c = S.sc[buf][hh];
+          c.dec = expf(all);
+          c.ds = exp2_int(-we) * exp2_int(-ke);
+          c.o2 = exp2_int(-ve) * exp2_int(-pe);
+          c.q = exp2_int(-qe);
+          c.grow = 64.f * (vb * dtm) * exp2_int(max(-126, min(127, 15 - ke)));
+          c.v = exp2_int(-ve);
+          c.p = exp2_int(max(-126, min(127, 22 - qe - ke + pe)));
+          c.skip = D * exp2_int(pe);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.gx[i & 1]);
+      }
+      if (!ok && lane == 0) report(p.err, GDN_DEV_ERR_TIMEOUT);
+    } else if (warp == kThreads / 32 - 1) {
+      // ---------------------------------------------------------------- loader
+      auto load_xg = [&](int i) {
+        const int32_t row0 = (int32_t)(s.t0 + (P0 + (int64_t)i * kC - 3 - s.p0));  // may be < 0: zeros
+        mbar_arrive_expect_tx(&S.x_bar[i & 1], (uint32_t)sizeof(S.raw[0]));
+        if (GDN_SPAN_G(2 * p.hk * kDK + tile * 128, 128, p.C) && GDN_SBYTES(&S.raw[i & 1][0][0], sizeof(S.raw[0]), S))
+          tma_load_2d(&S.raw[i & 1][0][0], &xmap, 2 * p.hk * kDK + tile * 128, row0, &S.x_bar[i & 1]);
+        bulk(&S.g[i & 1], a.rec[rec0 + (int64_t)i * p.hk].g, kGMBytes, &S.g_bar[i & 1]);
       };
-      gate_load(0);
-      gates(0);
-      if (nit > 1) gates(1);
-      named_sync(1, kBarAll);
-      if (!named_sync_or(1, kBarAll, false)) {
-        for (int i = 0; i < nit; ++i) {
-          if (i + 2 < nit) gates(i + 2);
-          if (named_sync_or(1, kBarAll, false)) break;
+      int n = 0;  // issued
+      if (lane == 0)
+        for (; n < 2 && n < nit; ++n) load_xg(n);
+      n = min(2, nit);
+      {
+        // |V| <= |conv| <= max over the channels of sum |w| times the largest
+        // raw input, plus the largest |bias|
+        const auto cw = GDN_GV(p.conv_w, (long long)p.C * 4);
+        float gain = 0.f, bmax = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int ch = 2 * p.hk * kDK + tile * 128 + 32 * k + lane;
+          const float4 w = vec_at<const float4>(cw, (size_t)ch * 4);
+          gain = fmaxf(gain, fabsf(w.x) + fabsf(w.y) + fabsf(w.z) + fabsf(w.w));
+          if (p.conv_bias) bmax = fmaxf(bmax, fabsf(GDN_GV(p.conv_bias, p.C)[ch]));
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+          gain = fmaxf(gain, __shfl_xor_sync(0xffffffffu, gain, o));
+          bmax = fmaxf(bmax, __shfl_xor_sync(0xffffffffu, bmax, o));
+        }
+        if (lane == 0) {
+          S.vgain = gain;
+          S.vbias = bmax;
         }
       }
-      named_sync_or(1, kBarAll, false);
+      bool ok = true;
+      for (int i = 0; i < nit && ok; ++i) {
+        if (i >= 2) {
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&S.used[i & 1], ((i - 2) >> 1) & 1)))) break;
+          if (lane == 0) load_xg(i);
+          n = i + 1;
+        }
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&S.x_bar[i & 1], (i >> 1) & 1)))) break;
+        const int64_t P = P0 + (int64_t)i * kC;
+        if (P - 3 < s.p0) {
+          // the up to 3 rows just before the sequence come from the history
+          const int64_t lo = max(P - 3, s.p0 - 3), hi = min(P + kC, s.p0);
+          const auto hist = GDN_GV(reinterpret_cast<const __nv_bfloat16*>(p.conv), (long long)p.num_slots * 3 * p.C) +
+                            (size_t)s.slot * 3 * p.C;
+          for (int64_t pos = lo; pos < hi; ++pos)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              S.raw[i & 1][GDN_S((int)(pos - (P - 3)), kRawRows)][32 * k + lane] =
+                  hist[(size_t)(3 - (s.p0 - pos)) * p.C + 2 * p.hk * kDK + tile * 128 + 32 * k + lane];
+          umma::fence_proxy_async();  // before a later chunk's copy into these rows
+          __syncwarp();
+        }
+        // the largest finite |raw input|: bf16 magnitudes order as integers
+        const auto rows = GDN_SV(reinterpret_cast<const uint4*>(&S.raw[i & 1][0][0]), kRawRows * 16);
+        uint32_t m = 0;
+#pragma unroll 4
+        for (int e = lane; e < kRawRows * 16; e += 32) {
+          const uint4 u = rows[e];
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t h = w[k] & 0x7fff0000u, l = w[k] << 16 & 0x7fff0000u;
+            m = max(m, max(h < 0x7f800000u ? h : 0u, l < 0x7f800000u ? l : 0u));
+          }
+        }
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == 0) {
+          S.xmax[i & 1] = __uint_as_float(m);
+          mbar_arrive(&S.hx[i & 1]);
+        }
+        __syncwarp();
+      }
+      if (lane == 0) {
+        if (!ok) report(p.err, GDN_DEV_ERR_TIMEOUT);
+        for (int k = max(0, n - 2); k < n; ++k) {  // as the issuer
+          mbar_wait(&S.x_bar[k & 1], (k >> 1) & 1);
+          mbar_wait(&S.g_bar[k & 1], (k >> 1) & 1);
+        }
+      }
     }
   } else {
     // ----------------------------------------------------------------- compute
@@ -712,12 +820,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ch = 2 * p.hk * kDK + tile * 128 + lrow;
 
     // the state entering the segment, S^T row lrow, columns 32 qq ..
-    float st[32];
+    float2 st[16];
     float seg_dec = 1.f;
     const size_t tile_off = ((size_t)tile * 128 + lrow) * kDK + 32 * qq;  // within one slot's [hv][dv][dk]
     const long long slot_n = (long long)p.hv * DV * kDK;
     const auto segs = GDN_GV(a.seg_state, a.n_segs * slot_n);
     const auto pool = GDN_GV(p.ssm, p.num_slots * slot_n) + ((size_t)s.slot * slot_n + tile_off);
+    auto put = [&](const auto& to) {  // the state to its place in a slot
+#pragma unroll
+      for (int e = 0; e < 8; ++e) vec_at<float4>(to, 4 * e) = join4(st[2 * e], st[2 * e + 1]);
+    };
     {
       // One segment: from the slot.  Several: the first launch starts the
       // first segment from the slot and keeps a copy, at the last segment's
@@ -730,7 +842,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           v = STATE || n_seg == 1 ? vec_at<const float4>(pool, 4 * i) : vec_at<const float4>(keep, 4 * i);
           if (STATE) vec_at<float4>(keep, 4 * i) = v;
         }
-        st[4 * i] = v.x; st[4 * i + 1] = v.y; st[4 * i + 2] = v.z; st[4 * i + 3] = v.w;
+        st[2 * i] = lo2(v);
+        st[2 * i + 1] = hi2(v);
       }
       if (!STATE) {
         for (int k = 0; k < seg; ++k) {
@@ -739,10 +852,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const float4 v = vec_at<const float4>(L, 4 * i);
-            st[4 * i] = fmaf(d, st[4 * i], v.x);
-            st[4 * i + 1] = fmaf(d, st[4 * i + 1], v.y);
-            st[4 * i + 2] = fmaf(d, st[4 * i + 2], v.z);
-            st[4 * i + 3] = fmaf(d, st[4 * i + 3], v.w);
+            st[2 * i] = fma2(make_float2(d, d), st[2 * i], lo2(v));
+            st[2 * i + 1] = fma2(make_float2(d, d), st[2 * i + 1], hi2(v));
           }
         }
       }
@@ -750,12 +861,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!STATE) {
       uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const uint32_t u = __float_as_uint(st[i]) & 0x7fffffffu;
-        m = max(m, u < 0x7f800000u ? u : 0u);  // the finite ones
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t u = __float_as_uint(st[i].x) & 0x7fffffffu, v = __float_as_uint(st[i].y) & 0x7fffffffu;
+        m = max(m, max(u < 0x7f800000u ? u : 0u, v < 0x7f800000u ? v : 0u));  // the finite ones
       }
       m = __reduce_max_sync(0xffffffffu, m);
-      if (lane == 0) atomicMax(&S.smax, m);
+      if (lane == 0) atomicMax(&S.smax[hl], m);  // a warp's rows are of one head
     }
     const float4 w4 = vec_at<const float4>(GDN_GV(p.conv_w, (long long)p.C * 4), (size_t)ch * 4);
     const float bias = p.conv_bias ? GDN_GV(p.conv_bias, p.C)[ch] : 0.f;
@@ -764,13 +875,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int PC = 8 * NH;
     const int pr = NH == 2 ? lrow : (lrow & 63), pi = pr & 63, ph = pr >> 6;
     const int pc = 16 * qq + (NH == 2 ? 0 : 8 * (lrow >> 6));
-    const float skip = p.D ? GDN_GV(p.D, p.hv)[h0 + ph] : 0.f;
-    [[maybe_unused]] const float skip2 = p.D && NH == 2 ? GDN_GV(p.D, p.hv)[h0 + (ph ^ 1)] : 0.f;
     if (!STATE) {
 #pragma unroll
-      for (int c4 = 0; c4 < PC / 8; ++c4) {
-        tile_at<uint4>(S.pt[0], sizeof(S.pt[0]), umma::sw128_off(pr, pc + 8 * c4, 0)) = make_uint4(0u, 0u, 0u, 0u);
-        tile_at<uint4>(S.pt[1], sizeof(S.pt[1]), umma::sw128_off(pr, pc + 8 * c4, 0)) = make_uint4(0u, 0u, 0u, 0u);
+      for (int c8 = 0; c8 < PC / 8; ++c8) {
+        tile_at<uint4>(S.pt[0], sizeof(S.pt[0]), umma::sw128_off(pr, pc + 8 * c8, 0)) = make_uint4(0u, 0u, 0u, 0u);
+        tile_at<uint4>(S.pt[1], sizeof(S.pt[1]), umma::sw128_off(pr, pc + 8 * c8, 0)) = make_uint4(0u, 0u, 0u, 0u);
       }
     }
     // chunks until the next block boundary, and the boundary's index
@@ -778,99 +887,68 @@ __global__ void __launch_bounds__(kThreads, 1)
     int to_ckpt = kpc - 1 - (int)((P0 / kC) % kpc);
     int64_t ck_idx = P0 / p.ckpt_block - s.p0 / p.ckpt_block;
 
-    bool bad = false;
-    int qe = 0, ke = 0, pe = 0;  // scale exponents of the next chunk's q, k and P
-    float y[16];  // V of the next chunk: channel lrow, tokens 16 qq ..
-    auto weights = [&](int i, float (&x)[16]) {  // V w
-      const auto ws = GDN_SV(&S.w[i & 3][hl][0], kC);
-#pragma unroll
-      for (int t4 = 0; t4 < 4; ++t4) {
-        const float4 v = vec_at<const float4>(ws, 16 * qq + 4 * t4);
-        x[4 * t4] = y[4 * t4] * v.x;
-        x[4 * t4 + 1] = y[4 * t4 + 1] * v.y;
-        x[4 * t4 + 2] = y[4 * t4 + 2] * v.z;
-        x[4 * t4 + 3] = y[4 * t4 + 3] * v.w;
-      }
-    };
-    // V and P of the segment's chunk i, the largest |V w|, the gates ahead
-    auto features = [&](int i) {
-      const int64_t P = P0 + (int64_t)i * kC;
-      if (!mbar_wait(&S.x_bar[i & 1], (i >> 1) & 1)) bad = true;
-      if (P - 3 < s.p0) {
-        // the up to 3 rows just before the sequence come from the history
-        const int64_t lo = max(P - 3, s.p0 - 3), hi = min(P + kC, s.p0);
-        const auto hist = GDN_GV(reinterpret_cast<const __nv_bfloat16*>(p.conv), (long long)p.num_slots * 3 * p.C) +
-                          (size_t)s.slot * 3 * p.C;
-        for (int64_t pos = lo; pos < hi; ++pos)
-          if (tid < 128)
-            S.raw[i & 1][GDN_S((int)(pos - (P - 3)), kRawRows)][tid] =
-                hist[(size_t)(3 - (s.p0 - pos)) * p.C + 2 * p.hk * kDK + tile * 128 + tid];
-        umma::fence_proxy_async();  // before a later chunk's copy into these rows
-        named_sync(2, kCompute);
-      }
+    float2 y[8];  // V 2^ve of the next chunk: channel lrow, tokens 16 qq ..
+    // V and P of the segment's chunk i; false if a wait expired
+    auto features = [&](int i) -> bool {
+      const uint32_t par = (i >> 1) & 1;
+      if (!mbar_wait(&S.gx[i & 1], par) || !mbar_wait(&S.x_bar[i & 1], par) || !mbar_wait(&S.g_bar[i & 1], par))
+        return false;
+      const int buf = i & 3;
       {
-        const auto xs = GDN_SV(&S.raw[i & 1][0][0], kRawRows * 128) + (16 * qq * 128 + lrow);
-        float x[19];
+        const auto xs = GDN_SV(reinterpret_cast<const uint16_t*>(&S.raw[i & 1][0][0]), kRawRows * 128) +
+                        (16 * qq * 128 + lrow);
+        uint32_t x[19];
 #pragma unroll
-        for (int r = 0; r < 19; ++r) x[r] = __bfloat162float(xs[r * 128]);
+        for (int r = 0; r < 19; ++r) x[r] = xs[r * 128];
+        auto pair = [&](int r) {  // rows r, r + 1 in fp32
+          return make_float2(__uint_as_float(x[r] << 16), __uint_as_float(x[r + 1] << 16));
+        };
+        // SiLU(v) 2^ve = v / (2^-ve + 2^-ve e^-v)
+        const float cv = S.sc[buf][hl].v;
 #pragma unroll
-        for (int t = 0; t < 16; ++t) {
-          float acc = fmaf(w4.x, x[t], bias);
-          acc = fmaf(w4.y, x[t + 1], acc);
-          acc = fmaf(w4.z, x[t + 2], acc);
-          acc = fmaf(w4.w, x[t + 3], acc);
-          y[t] = silu_acc(acc);
+        for (int t = 0; t < 8; ++t) {
+          float2 v = fma2(make_float2(w4.x, w4.x), pair(2 * t), make_float2(bias, bias));
+          v = fma2(make_float2(w4.y, w4.y), pair(2 * t + 1), v);
+          v = fma2(make_float2(w4.z, w4.z), pair(2 * t + 2), v);
+          v = fma2(make_float2(w4.w, w4.w), pair(2 * t + 3), v);
+          const float2 e = mul2(v, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+          const float2 d = fma2(make_float2(ex2(e.x), ex2(e.y)), make_float2(cv, cv), make_float2(cv, cv));
+          y[t] = make_float2(__fdividef(v.x, d.x), __fdividef(v.y, d.y));
         }
       }
+      const int64_t P = P0 + (int64_t)i * kC;
       if (P < s.p0 || P + kC > s.p1) {  // tokens outside the sequence
         const int tlo = (int)max((int64_t)0, s.p0 - P), thi = (int)min((int64_t)kC, s.p1 - P);
 #pragma unroll
-        for (int t = 0; t < 16; ++t)
-          if (16 * qq + t < tlo || 16 * qq + t >= thi) y[t] = 0.f;
+        for (int t = 0; t < 8; ++t) {
+          if (16 * qq + 2 * t < tlo || 16 * qq + 2 * t >= thi) y[t].x = 0.f;
+          if (16 * qq + 2 * t + 1 < tlo || 16 * qq + 2 * t + 1 >= thi) y[t].y = 0.f;
+        }
       }
-      {
-        uint32_t m = 0;
-#pragma unroll
-        for (int t = 0; t < 16; ++t) m = max(m, __float_as_uint(y[t]) & 0x7fffffffu);
-        m = __reduce_max_sync(0xffffffffu, m);
-        if (lane == 0) atomicMax(&S.vmax[i % 3], m);
-      }
-      if (!mbar_wait(&S.g_bar[i & 1], (i >> 1) & 1)) bad = true;
-      qe = S.g[i & 1].meta[0];
-      ke = S.g[i & 1].meta[1];
       if constexpr (!STATE) {
-        // |P| <= 128 max|q| max|k| max dt + |D| < 2^(37 - qe - ke) max dt + |D|
-        const int buf = i & 3;
-        const float g1 = exp2_int(max(-126, min(127, 37 - qe - ke)));
-        pe = scale_exp(__float_as_uint(fmaf(g1, S.dtm[buf][ph], fabsf(skip))));
-        if constexpr (NH == 2)  // one scale for both heads
-          pe = min(pe, scale_exp(__float_as_uint(fmaf(g1, S.dtm[buf][ph ^ 1], fabsf(skip2)))));
         if (pc <= pi) {
           // P_ij = G_ij u_i v_j: both factors taken at the end b' of j's
           // 16-token block, u_i = e^{b_i - b'} at most 1 below the diagonal
           // blocks; on them it is large where the block decays, and beyond
           // 2^80 the differences are taken one by one
           const float bi = S.b2[buf][ph][pi], be = S.b2[buf][ph][GDN_S(pc | 15, kC)];
-          const bool diag = (pi >> 4) == qq;
-          const float pscale = exp2_int(max(-126, min(127, 22 - qe - ke + pe)));
+          const float pscale = S.sc[buf][ph].p;
           const float u = ex2(bi - be) * pscale;
-          float e[PC];
+          float2 e[PC / 2];
 #pragma unroll
           for (int c8 = 0; c8 < PC / 8; ++c8) {
             const uint4 g4 = tile_at<uint4>(S.g[i & 1].g, kGBytes, umma::sw128_off(pi, pc + 8 * c8, 0));
             const float4 va = *reinterpret_cast<const float4*>(&S.v[buf][ph][GDN_S(pc + 8 * c8, kC - 7)]);
             const float4 vb = *reinterpret_cast<const float4*>(&S.v[buf][ph][pc + 8 * c8 + 4]);
             const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w};
-            const float vv[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
+            const float2 vv[4] = {lo2(va), hi2(va), lo2(vb), hi2(vb)};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 g2 = __half22float2(*reinterpret_cast<const __half2*>(&gw[k]));
-              e[8 * c8 + 2 * k] = g2.x * (u * vv[2 * k]);
-              e[8 * c8 + 2 * k + 1] = g2.y * (u * vv[2 * k + 1]);
-            }
+            for (int k = 0; k < 4; ++k)
+              e[4 * c8 + k] = mul2(__half22float2(*reinterpret_cast<const __half2*>(&gw[k])),
+                                   mul2(vv[k], make_float2(u, u)));
           }
-          if (diag) {
-            const float sk = skip * exp2_int(pe);
+          if ((pi >> 4) == qq) {
+            const float sk = S.sc[buf][ph].skip;
             if (S.b2[buf][ph][pc & ~15] - be > 80.f) {
 #pragma unroll 1
               for (int k = 0; k < PC; ++k) {
@@ -878,76 +956,58 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float g = __half2float(tile_at<__half>(S.g[i & 1].g, kGBytes, umma::sw128_off(pi, j, 0)));
                 const float x = j > pi ? 0.f : g * (ex2(bi - S.b2[buf][ph][GDN_S(j, kC)]) * S.dt[buf][ph][j] * pscale);
 #pragma unroll
-                for (int q = 0; q < PC; ++q)
-                  if (q == k) e[q] = x;
+                for (int q = 0; q < PC / 2; ++q) {
+                  if (2 * q == k) e[q].x = x;
+                  if (2 * q + 1 == k) e[q].y = x;
+                }
               }
             }
 #pragma unroll
-            for (int k = 0; k < PC; ++k) {
-              const int j = pc + k;
-              e[k] = j < pi ? e[k] : j == pi ? e[k] + sk : 0.f;
+            for (int k = 0; k < PC / 2; ++k) {
+              const int j = pc + 2 * k;
+              e[k].x = j < pi ? e[k].x : j == pi ? e[k].x + sk : 0.f;
+              e[k].y = j + 1 < pi ? e[k].y : j + 1 == pi ? e[k].y + sk : 0.f;
             }
           }
 #pragma unroll
           for (int c8 = 0; c8 < PC / 8; ++c8)
             tile_at<uint4>(S.pt[i & 1], sizeof(S.pt[0]), umma::sw128_off(pr, pc + 8 * c8, 0)) =
-                make_uint4(half2_bits(e[8 * c8], e[8 * c8 + 1]), half2_bits(e[8 * c8 + 2], e[8 * c8 + 3]),
-                           half2_bits(e[8 * c8 + 4], e[8 * c8 + 5]), half2_bits(e[8 * c8 + 6], e[8 * c8 + 7]));
+                make_uint4(half2_bits(e[4 * c8].x, e[4 * c8].y), half2_bits(e[4 * c8 + 1].x, e[4 * c8 + 1].y),
+                           half2_bits(e[4 * c8 + 2].x, e[4 * c8 + 2].y), half2_bits(e[4 * c8 + 3].x, e[4 * c8 + 3].y));
         }
       }
-      if (tid == 0) S.vmax[(i + 1) % 3] = 0;
-    };
-    float s_bound = 0.f;  // >= |S|
-    // of the operands in TMEM: factors that take the products back
-    float ds_f = 0.f, o1_f = 0.f, o2_f = 0.f;
-    // chunk i's operands into TMEM (its maxima complete): S^T, V^T, (V w)^T
-    auto operands = [&](int i) {
-      float x[16];
-      weights(i, x);
-      uint32_t m = S.vmax[i % 3];
-      if (m >= 0x7f800000u) {
-        // infinite or NaN values among V: the scale of the finite ones
-        named_sync(2, kCompute);
-        if (tid == 0) S.vfin = 0;
-        named_sync(2, kCompute);
-        m = 0;
-#pragma unroll
-        for (int t = 0; t < 16; ++t) {
-          const uint32_t u = __float_as_uint(y[t]) & 0x7fffffffu;
-          m = max(m, u < 0x7f800000u ? u : 0u);
-        }
-        atomicMax(&S.vfin, m);
-        named_sync(2, kCompute);
-        m = S.vfin;
-      }
-      // |V w| <= max|V| max dt, for both heads
-      const float dtm = NH == 2 ? fmaxf(S.dtm[i & 3][0], S.dtm[i & 3][NH - 1]) : S.dtm[i & 3][0];
-      const float vw = __uint_as_float(m) * dtm;
-      const int ve = scale_exp(__float_as_uint(vw));
       __syncwarp();
+      if (lane == 0) mbar_arrive(&S.used[i & 1]);
+      return true;
+    };
+    float s_bound = 0.f, s_back = 0.f;  // >= |S|; 2^-e of the S^T operand
+    // chunk i's operands into TMEM: S^T, V^T, (V w)^T
+    auto operands = [&](int i) {
       if constexpr (!STATE) {
-        const int se = scale_exp(__float_as_uint(s_bound)), vse = scale_exp(m);
-        const float fs = exp2_int(se), fv = exp2_int(vse);
+        const int se = scale_exp(__float_as_uint(s_bound));
+        const float fs = exp2_int(se);
+        s_back = exp2_int(-se);
         uint32_t r[16], v[8];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) r[e] = half2_bits(st[2 * e] * fs, st[2 * e + 1] * fs);
+        for (int e = 0; e < 16; ++e) {
+          const float2 x = mul2(st[e], make_float2(fs, fs));
+          r[e] = half2_bits(x.x, x.y);
+        }
         tmem_put16(tlane + TM_S + 16 * qq, r);
 #pragma unroll
-        for (int t = 0; t < 8; ++t) v[t] = half2_bits(y[2 * t] * fv, y[2 * t + 1] * fv);
+        for (int t = 0; t < 8; ++t) v[t] = half2_bits(y[t].x, y[t].y);
         tmem_put8(tlane + TM_V + 8 * qq, v);
-        o1_f = exp2_int(-se) * exp2_int(-qe);
-        o2_f = exp2_int(-vse) * exp2_int(-pe);
       }
-      const float f = exp2_int(ve);
+      const auto ws = GDN_SV(&S.w[i & 3][hl][0], kC);
       uint32_t hi[8], lo[8];
 #pragma unroll
-      for (int t = 0; t < 8; ++t) split2(x[2 * t] * f, x[2 * t + 1] * f, hi[t], lo[t]);
+      for (int t4 = 0; t4 < 4; ++t4) {
+        const float4 w = vec_at<const float4>(ws, 16 * qq + 4 * t4);
+        split2(mul2(y[2 * t4], lo2(w)), hi[2 * t4], lo[2 * t4]);
+        split2(mul2(y[2 * t4 + 1], hi2(w)), hi[2 * t4 + 1], lo[2 * t4 + 1]);
+      }
       tmem_put8(tlane + TM_WH + 8 * qq, hi);
       tmem_put8(tlane + TM_WL + 8 * qq, lo);
-      ds_f = exp2_int(-ve) * exp2_int(-ke);
-      // |S| after the chunk: 64 terms of at most max|V w| max|k|
-      const float dm = NH == 2 ? fmaxf(S.dec[i & 3][0], S.dec[i & 3][NH - 1]) : S.dec[i & 3][0];
-      s_bound = fmaf(s_bound, dm, 64.f * vw * exp2_int(max(-126, min(127, 15 - ke))));
       tmem_wait_st();
     };
     auto publish = [&]() {
@@ -957,40 +1017,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&S.ready);
     };
 
-    named_sync(1, kBarAll);  // the first gates
-    features(0);
-    int i = 0;
-    if (!named_sync_or(1, kBarAll, bad)) {
-      s_bound = __uint_as_float(S.smax);
+    named_sync(1, kCompute);  // smax complete
+    bool ok = features(0);
+    if ((ok = __all_sync(0xffffffffu, ok))) {
+      s_bound = __uint_as_float(S.smax[hl]);
       operands(0);
       publish();
-      for (; i < nit; ++i) {
-        if (i + 1 < nit) features(i + 1);
-        if (named_sync_or(1, kBarAll, bad)) break;
-        if (!mbar_wait(&S.mma_bar, i & 1)) bad = true;
-        __syncwarp();
+      for (int i = 0; i < nit; ++i) {
+        if (i + 1 < nit) ok = features(i + 1);
+        ok = ok && mbar_wait(&S.mma_bar, i & 1);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
         umma::fence_after();
         const int buf = i & 3;
+        const Scales& sc = S.sc[buf][hl];
+        const float4 sa = *reinterpret_cast<const float4*>(&sc.dec);  // dec, ds, o2, q
+        s_bound = fmaf(s_bound, sa.x, sc.grow);
         {
-          const float dec = S.dec[buf][hl];
-          seg_dec *= dec;
+          seg_dec *= sa.x;
           float d[32];
           umma::tmem_ld32(tlane + TM_DS + 32 * qq, d);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) st[e] = fmaf(st[e], dec, d[e] * ds_f);
+          for (int e = 0; e < 16; ++e)
+            st[e] = fma2(st[e], make_float2(sa.x, sa.x), mul2(make_float2(d[2 * e], d[2 * e + 1]), make_float2(sa.y, sa.y)));
         }
         if constexpr (!STATE) {
           float o1[16], o2[16];
           tmem_ld16x2(tlane + TM_O1 + 16 * qq, tlane + TM_O2 + (NH == 2 ? hl * kC : 0) + 16 * qq, o1, o2);
-          const auto ot = GDN_SV(&S.ot[0][0], kC * 128);
+          const float f1 = s_back * sa.w;
+          const auto ot = GDN_SV(&S.ot[0][0], kC * 128) + (16 * qq * 128 + lrow);
 #pragma unroll
           for (int t4 = 0; t4 < 4; ++t4) {
             const float4 e = *reinterpret_cast<const float4*>(&S.eb[buf][hl][GDN_S(16 * qq + 4 * t4, kC - 3)]);
-            const float ev[4] = {e.x, e.y, e.z, e.w};
+            const float2 ev[2] = {lo2(e), hi2(e)};
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              ot[(16 * qq + 4 * t4 + k) * 128 + lrow] =
-                  __float2bfloat16_rn(fmaf(o1[4 * t4 + k] * o1_f, ev[k], o2[4 * t4 + k] * o2_f));
+            for (int k = 0; k < 2; ++k) {
+              const int t = 4 * t4 + 2 * k;
+              const float2 o = fma2(mul2(make_float2(o1[t], o1[t + 1]), make_float2(f1, f1)), ev[k],
+                                    mul2(make_float2(o2[t], o2[t + 1]), make_float2(sa.z, sa.z)));
+              const __nv_bfloat162 h = __floats2bfloat162_rn(o.x, o.y);
+              ot[t * 128] = h.x;
+              ot[(t + 1) * 128] = h.y;
+            }
           }
           // the block boundary at this chunk's end (a sequence that ends
           // inside the chunk does not reach it)
@@ -998,12 +1065,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             to_ckpt = kpc - 1;
             if (ck_idx < p.max_ckpt && P0 + (int64_t)(i + 1) * kC <= s.p1) {
               const int32_t cid = GDN_GV(p.ckpt_ids, (long long)p.n_seq * p.max_ckpt)[(size_t)n * p.max_ckpt + ck_idx];
-              if (slot_class(cid, p.ck_num_slots) == 0) {
-                const auto K = GDN_GV(p.ck_ssm, p.ck_num_slots * slot_n) + ((size_t)cid * slot_n + tile_off);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  vec_at<float4>(K, 4 * e) = make_float4(st[4 * e], st[4 * e + 1], st[4 * e + 2], st[4 * e + 3]);
-              }
+              if (slot_class(cid, p.ck_num_slots) == 0)
+                put(GDN_GV(p.ck_ssm, p.ck_num_slots * slot_n) + ((size_t)cid * slot_n + tile_off));
             }
             ++ck_idx;
           }
@@ -1012,22 +1075,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (i + 1 < nit || !STATE) publish();
       }
     }
-    bad = named_sync_or(1, kBarAll, bad);
-    if (i == nit && !bad) {
-      if (STATE) {
-        const auto L = segs + ((seg_first + seg) * slot_n + (int64_t)tile_off);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          vec_at<float4>(L, 4 * e) = make_float4(st[4 * e], st[4 * e + 1], st[4 * e + 2], st[4 * e + 3]);
-        if (qq == 0 && lrow % DV == 0)
-          GDN_GV(a.seg_decay, (long long)a.n_segs * p.hv)[(seg_first + seg) * p.hv + h0 + hl] = seg_dec;
-      } else if (seg == n_seg - 1) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          vec_at<float4>(pool, 4 * e) = make_float4(st[4 * e], st[4 * e + 1], st[4 * e + 2], st[4 * e + 3]);
-      }
-    } else if (tid == 0) {
-      report(p.err, GDN_DEV_ERR_TIMEOUT);
+    if (!ok) {
+      if (lane == 0) report(p.err, GDN_DEV_ERR_TIMEOUT);
+    } else if (STATE) {
+      put(segs + ((seg_first + seg) * slot_n + (int64_t)tile_off));
+      if (qq == 0 && lrow % DV == 0)
+        GDN_GV(a.seg_decay, (long long)a.n_segs * p.hv)[(seg_first + seg) * p.hv + h0 + hl] = seg_dec;
+    } else if (seg == n_seg - 1) {
+      put(pool);
     }
   }
   umma::fence_before();
