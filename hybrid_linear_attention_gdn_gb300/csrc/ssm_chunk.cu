@@ -420,7 +420,9 @@ struct __align__(1024) ChainSmem {
   uint64_t hx[2];                     // xmax known, history rows in place
   uint64_t gx[2];                     // gates and scales known
   uint64_t used[2];                   // raw rows and G read
-  uint64_t ready, mma_bar;            // operands in place; products done
+  uint64_t ready;                     // operands in place
+  uint64_t ds_bar, o_bar;             // dS^T done; all products done
+  uint64_t o_full, o_free;            // output staged; staging read
   uint32_t tmem_base;
   int seq;
 };
@@ -528,7 +530,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.used[i], kCompute / 32);
     }
     mbar_init(&S.ready, kCompute / 32);
-    mbar_init(&S.mma_bar, 1);
+    mbar_init(&S.ds_bar, 1);
+    mbar_init(&S.o_bar, 1);
+    mbar_init(&S.o_full, kCompute / 32);
+    mbar_init(&S.o_free, 1);
 #pragma unroll
     for (int i = 0; i < NH; ++i) S.smax[i] = 0;
     fence_mbar_init();
@@ -564,73 +569,74 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (; n_qk < 2 && n_qk < nit; ++n_qk) load_qk(n_qk);
       }
       bool ok = true;
-      // pass i: chunk i's operands are in place (and chunk i - 1's output staged)
-      for (int i = 0; i < nit + (STATE ? 0 : 1) && ok; ++i) {
+      // chunk i's staged output, the whole warp
+      auto store = [&](int i) -> bool {
+        if (!__all_sync(0xffffffffu, mbar_wait(&S.o_full, i & 1))) return false;
+        const int64_t P = P0 + (int64_t)i * kC;
+        const int tlo = (int)max((int64_t)0, s.p0 - P), thi = (int)min((int64_t)kC, s.p1 - P);
+        if (tlo == 0 && thi == kC) {
+          if (lane == 0 && GDN_SPAN_G(s.t0 + (P - s.p0), kC, p.total)) {
+            tma_store_2d(&omap, &S.ot[0][0], tile * 128, (int32_t)(s.t0 + (P - s.p0)));
+            bulk_commit();
+            bulk_wait_read();
+          }
+        } else {
+          const auto ot = GDN_SV(&S.ot[0][0], kC * 128);
+          const auto out = GDN_GV(reinterpret_cast<__nv_bfloat16*>(p.out), p.total * p.hv * DV);
+          for (int r = tlo + (lane >> 4); r < thi; r += 2)
+            vec_at<uint4>(out, ((s.t0 + P - s.p0 + r) * p.hv) * DV + tile * 128 + 8 * (lane & 15)) =
+                vec_at<const uint4>(ot, r * 128 + 8 * (lane & 15));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.o_free);
+        return true;
+      };
+      // pass i: chunk i's operands are in place
+      for (int i = 0; i < nit && ok; ++i) {
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&S.ready, i & 1)))) break;
-        umma::fence_after();
-        if (lane == 0 && i < nit) {
-          if ((ok = mbar_wait(&S.qk_bar[i & 1], (i >> 1) & 1))) {
-            umma::fence_after();
-            const uint64_t dq = umma::desc(smem_addr(S.qk[i & 1]), 16, 1024);
-            const uint64_t dh = umma::adv(dq, offsetof(Record, kh)), dl = umma::adv(dq, offsetof(Record, kl));
-            if (!STATE) {
-              // O1^T = S^T Q^T, O2^T = V^T P^T
+        if (lane == 0 && (ok = mbar_wait(&S.qk_bar[i & 1], (i >> 1) & 1))) {
+          umma::fence_after();
+          const uint64_t dq = umma::desc(smem_addr(S.qk[i & 1]), 16, 1024);
+          const uint64_t dh = umma::adv(dq, offsetof(Record, kh)), dl = umma::adv(dq, offsetof(Record, kl));
+          // dS^T = (V w)^T K, small products first; on it the next state waits
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                mma_f16_ta(tmem + TM_O1, tmem + TM_S + 8 * k, umma::adv(dq, (k >> 2) * 8192 + (k & 3) * 32), ID_O1, k > 0);
-              const uint64_t dp = umma::desc(smem_addr(S.pt[i & 1]), 16, 1024);
+          for (int k = 0; k < 4; ++k)
+            mma_f16_ta(tmem + TM_DS, tmem + TM_WL + 8 * k, umma::adv(dh, 32 * k), ID_S, k > 0);
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_f16_ta(tmem + TM_O2, tmem + TM_V + 8 * k, umma::adv(dp, 32 * k), ID_O2, k > 0);
-            }
-            // dS^T = (V w)^T K, small products first
+          for (int k = 0; k < 4; ++k)
+            mma_f16_ta(tmem + TM_DS, tmem + TM_WH + 8 * k, umma::adv(dl, 32 * k), ID_S, true);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_f16_ta(tmem + TM_DS, tmem + TM_WH + 8 * k, umma::adv(dh, 32 * k), ID_S, true);
+          umma::commit(&S.ds_bar);
+          if (!STATE) {
+            // O1^T = S^T Q^T, O2^T = V^T P^T
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_f16_ta(tmem + TM_O1, tmem + TM_S + 8 * k, umma::adv(dq, (k >> 2) * 8192 + (k & 3) * 32), ID_O1,
+                         k > 0);
+            const uint64_t dp = umma::desc(smem_addr(S.pt[i & 1]), 16, 1024);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_f16_ta(tmem + TM_DS, tmem + TM_WL + 8 * k, umma::adv(dh, 32 * k), ID_S, k > 0);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_f16_ta(tmem + TM_DS, tmem + TM_WH + 8 * k, umma::adv(dl, 32 * k), ID_S, true);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_f16_ta(tmem + TM_DS, tmem + TM_WH + 8 * k, umma::adv(dh, 32 * k), ID_S, true);
+              mma_f16_ta(tmem + TM_O2, tmem + TM_V + 8 * k, umma::adv(dp, 32 * k), ID_O2, k > 0);
           }
-        }
-        if constexpr (!STATE) {
-          // chunk i - 1's staged output
-          if (i > 0) {
-            const int64_t P = P0 + (int64_t)(i - 1) * kC;
-            const int tlo = (int)max((int64_t)0, s.p0 - P), thi = (int)min((int64_t)kC, s.p1 - P);
-            if (tlo == 0 && thi == kC) {
-              if (lane == 0 && GDN_SPAN_G(s.t0 + (P - s.p0), kC, p.total)) {
-                tma_store_2d(&omap, &S.ot[0][0], tile * 128, (int32_t)(s.t0 + (P - s.p0)));
-                bulk_commit();
-              }
-            } else {
-              const auto ot = GDN_SV(&S.ot[0][0], kC * 128);
-              const auto out = GDN_GV(reinterpret_cast<__nv_bfloat16*>(p.out), p.total * p.hv * DV);
-              for (int r = tlo + (lane >> 4); r < thi; r += 2)
-                vec_at<uint4>(out, ((s.t0 + P - s.p0 + r) * p.hv) * DV + tile * 128 + 8 * (lane & 15)) =
-                    vec_at<const uint4>(ot, r * 128 + 8 * (lane & 15));
-              __syncwarp();
-            }
-          }
-        }
-        if (lane == 0 && i < nit && ok) {
-          bulk_wait_read();  // the staging may be written once this chunk's products are known to be done
-          umma::commit(&S.mma_bar);
+          umma::commit(&S.o_bar);
           ++n_mma;
-          if ((ok = mbar_wait(&S.mma_bar, i & 1)) && i + 2 < nit) {
-            load_qk(i + 2);
-            n_qk = i + 3;
-          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!STATE && ok && i > 0) ok = store(i - 1);
+        if (lane == 0 && ok && (ok = mbar_wait(&S.o_bar, i & 1)) && i + 2 < nit) {
+          load_qk(i + 2);
+          n_qk = i + 3;
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
       }
+      if (!STATE && ok) ok = store(nit - 1);
       if (lane == 0) {
         if (!ok) report(p.err, GDN_DEV_ERR_TIMEOUT);
         // what is in flight lands before the memory goes (at once, unless a wait expired)
         for (int k = max(0, n_qk - 2); k < n_qk; ++k) mbar_wait(&S.qk_bar[k & 1], (k >> 1) & 1);
-        if (n_mma) mbar_wait(&S.mma_bar, (n_mma - 1) & 1);
+        if (n_mma) mbar_wait(&S.o_bar, (n_mma - 1) & 1);
         bulk_wait_all();
       }
     } else if (warp <= kCompute / 32 + NH) {
@@ -782,17 +788,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma::fence_proxy_async();  // before a later chunk's copy into these rows
           __syncwarp();
         }
-        // the largest finite |raw input|: bf16 magnitudes order as integers
+        // the largest finite |raw input|
         const auto rows = GDN_SV(reinterpret_cast<const uint4*>(&S.raw[i & 1][0][0]), kRawRows * 16);
-        uint32_t m = 0;
-#pragma unroll 4
+        __nv_bfloat162 mx[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll 8
         for (int e = lane; e < kRawRows * 16; e += 32) {
           const uint4 u = rows[e];
           const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint32_t h = w[k] & 0x7fff0000u, l = w[k] << 16 & 0x7fff0000u;
-            m = max(m, max(h < 0x7f800000u ? h : 0u, l < 0x7f800000u ? l : 0u));
+            const uint32_t v = w[k] & 0x7fff7fffu;
+            mx[k] = __hmax2(mx[k], *reinterpret_cast<const __nv_bfloat162*>(&v));  // a NaN is passed over
+          }
+        }
+        const float2 m01 = __bfloat1622float2(__hmax2(__hmax2(mx[0], mx[1]), __hmax2(mx[2], mx[3])));
+        uint32_t m = __float_as_uint(fmaxf(m01.x, m01.y));
+        if (__any_sync(0xffffffffu, m >= 0x7f800000u)) {  // infinities: without them
+          m = 0;
+          for (int e = lane; e < kRawRows * 128; e += 32) {
+            const uint32_t v = __float_as_uint(__bfloat162float(S.raw[i & 1][e / 128][e % 128])) & 0x7fffffffu;
+            m = max(m, v < 0x7f800000u ? v : 0u);
           }
         }
         m = __reduce_max_sync(0xffffffffu, m);
@@ -885,7 +902,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // chunks until the next block boundary, and the boundary's index
     const int kpc = p.ckpt_block / kC;
     int to_ckpt = kpc - 1 - (int)((P0 / kC) % kpc);
-    int64_t ck_idx = P0 / p.ckpt_block - s.p0 / p.ckpt_block;
+    int ck_idx = (int)min((int64_t)p.max_ckpt, P0 / p.ckpt_block - s.p0 / p.ckpt_block);
+    // the sequence's tokens, counted from the segment's first chunk
+    const int first = (int)(s.p0 - P0), last = (int)min((int64_t)nit * kC, s.p1 - P0);
 
     float2 y[8];  // V 2^ve of the next chunk: channel lrow, tokens 16 qq ..
     // V and P of the segment's chunk i; false if a wait expired
@@ -916,13 +935,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           y[t] = make_float2(__fdividef(v.x, d.x), __fdividef(v.y, d.y));
         }
       }
-      const int64_t P = P0 + (int64_t)i * kC;
-      if (P < s.p0 || P + kC > s.p1) {  // tokens outside the sequence
-        const int tlo = (int)max((int64_t)0, s.p0 - P), thi = (int)min((int64_t)kC, s.p1 - P);
+      const int tlo = first - i * kC - 16 * qq, thi = last - i * kC - 16 * qq;
+      if (tlo > 0 || thi < 16) {  // tokens outside the sequence
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
-          if (16 * qq + 2 * t < tlo || 16 * qq + 2 * t >= thi) y[t].x = 0.f;
-          if (16 * qq + 2 * t + 1 < tlo || 16 * qq + 2 * t + 1 >= thi) y[t].y = 0.f;
+          if (2 * t < tlo || 2 * t >= thi) y[t].x = 0.f;
+          if (2 * t + 1 < tlo || 2 * t + 1 >= thi) y[t].y = 0.f;
         }
       }
       if constexpr (!STATE) {
@@ -976,28 +994,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                            half2_bits(e[4 * c8 + 2].x, e[4 * c8 + 2].y), half2_bits(e[4 * c8 + 3].x, e[4 * c8 + 3].y));
         }
       }
+      umma::fence_proxy_async();  // P
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.used[i & 1]);
       return true;
     };
-    float s_bound = 0.f, s_back = 0.f;  // >= |S|; 2^-e of the S^T operand
-    // chunk i's operands into TMEM: S^T, V^T, (V w)^T
-    auto operands = [&](int i) {
-      if constexpr (!STATE) {
-        const int se = scale_exp(__float_as_uint(s_bound));
-        const float fs = exp2_int(se);
-        s_back = exp2_int(-se);
-        uint32_t r[16], v[8];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float2 x = mul2(st[e], make_float2(fs, fs));
-          r[e] = half2_bits(x.x, x.y);
-        }
-        tmem_put16(tlane + TM_S + 16 * qq, r);
-#pragma unroll
-        for (int t = 0; t < 8; ++t) v[t] = half2_bits(y[t].x, y[t].y);
-        tmem_put8(tlane + TM_V + 8 * qq, v);
-      }
+    // chunk i's V and V w to their operands
+    auto put_v = [&](int i) {
       const auto ws = GDN_SV(&S.w[i & 3][hl][0], kC);
       uint32_t hi[8], lo[8];
 #pragma unroll
@@ -1008,71 +1011,113 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tmem_put8(tlane + TM_WH + 8 * qq, hi);
       tmem_put8(tlane + TM_WL + 8 * qq, lo);
-      tmem_wait_st();
+      if (!STATE) {
+        uint32_t v[8];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) v[t] = half2_bits(y[t].x, y[t].y);
+        tmem_put8(tlane + TM_V + 8 * qq, v);
+      }
     };
-    auto publish = [&]() {
-      umma::fence_proxy_async();
+    float s_bound = 0.f, s_back = 0.f;  // >= |S|; 2^-e of the S^T operand
+    auto put_s = [&]() {
+      if constexpr (!STATE) {
+        const int se = scale_exp(__float_as_uint(s_bound));
+        const float fs = exp2_int(se);
+        s_back = exp2_int(-se);
+        uint32_t r[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float2 x = mul2(st[e], make_float2(fs, fs));
+          r[e] = half2_bits(x.x, x.y);
+        }
+        tmem_put16(tlane + TM_S + 16 * qq, r);
+      }
+    };
+    auto publish = [&](uint64_t* bar) {
       umma::fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.ready);
+      if (lane == 0) mbar_arrive(bar);
     };
 
     named_sync(1, kCompute);  // smax complete
-    bool ok = features(0);
-    if ((ok = __all_sync(0xffffffffu, ok))) {
-      s_bound = __uint_as_float(S.smax[hl]);
-      operands(0);
-      publish();
-      for (int i = 0; i < nit; ++i) {
-        if (i + 1 < nit) ok = features(i + 1);
-        ok = ok && mbar_wait(&S.mma_bar, i & 1);
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+    s_bound = __uint_as_float(S.smax[hl]);
+    bool ok = true;
+    if ((ok = __all_sync(0xffffffffu, features(0)))) {
+      put_v(0);
+      put_s();
+      tmem_wait_st();
+      publish(&S.ready);
+    }
+    // pass i: chunk i + 1's features, chunk i's results, chunk i + 1's operands
+#pragma unroll 1
+    for (int i = 0; i < nit && ok; ++i) {
+      const bool more = i + 1 < nit;
+      if (more) {
+        if (!(ok = __all_sync(0xffffffffu, features(i + 1)))) break;
+      }
+      [[maybe_unused]] float f1, f2;
+      {
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&S.ds_bar, i & 1)))) break;
         umma::fence_after();
-        const int buf = i & 3;
-        const Scales& sc = S.sc[buf][hl];
+        const Scales& sc = S.sc[i & 3][hl];
         const float4 sa = *reinterpret_cast<const float4*>(&sc.dec);  // dec, ds, o2, q
+        f1 = s_back * sa.w;
+        f2 = sa.z;
         s_bound = fmaf(s_bound, sa.x, sc.grow);
-        {
-          seg_dec *= sa.x;
-          float d[32];
-          umma::tmem_ld32(tlane + TM_DS + 32 * qq, d);
+        seg_dec *= sa.x;
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            st[e] = fma2(st[e], make_float2(sa.x, sa.x), mul2(make_float2(d[2 * e], d[2 * e + 1]), make_float2(sa.y, sa.y)));
+        for (int k = 0; k < 2; ++k) {
+          float d[16];
+          umma::tmem_ld16(tlane + TM_DS + 32 * qq + 16 * k, d);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            st[8 * k + e] = fma2(st[8 * k + e], make_float2(sa.x, sa.x),
+                                 mul2(make_float2(d[2 * e], d[2 * e + 1]), make_float2(sa.y, sa.y)));
         }
-        if constexpr (!STATE) {
-          float o1[16], o2[16];
-          tmem_ld16x2(tlane + TM_O1 + 16 * qq, tlane + TM_O2 + (NH == 2 ? hl * kC : 0) + 16 * qq, o1, o2);
-          const float f1 = s_back * sa.w;
-          const auto ot = GDN_SV(&S.ot[0][0], kC * 128) + (16 * qq * 128 + lrow);
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&S.o_bar, i & 1)))) break;
+        umma::fence_after();
+      }
+      if (more) {
+        put_v(i + 1);
+        put_s();
+      }
+      [[maybe_unused]] float o1[16], o2[16];
+      if (!STATE)
+        tmem_ld16x2(tlane + TM_O1 + 16 * qq, tlane + TM_O2 + (NH == 2 ? hl * kC : 0) + 16 * qq, o1, o2);
+      if (more) {
+        tmem_wait_st();
+        publish(&S.ready);
+      }
+      if constexpr (!STATE) {
+        if (i > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&S.o_free, (i - 1) & 1)))) break;
+        const auto ot = GDN_SV(&S.ot[0][0], kC * 128) + (16 * qq * 128 + lrow);
 #pragma unroll
-          for (int t4 = 0; t4 < 4; ++t4) {
-            const float4 e = *reinterpret_cast<const float4*>(&S.eb[buf][hl][GDN_S(16 * qq + 4 * t4, kC - 3)]);
-            const float2 ev[2] = {lo2(e), hi2(e)};
+        for (int t4 = 0; t4 < 4; ++t4) {
+          const float4 e = *reinterpret_cast<const float4*>(&S.eb[i & 3][hl][GDN_S(16 * qq + 4 * t4, kC - 3)]);
+          const float2 ev[2] = {lo2(e), hi2(e)};
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int t = 4 * t4 + 2 * k;
-              const float2 o = fma2(mul2(make_float2(o1[t], o1[t + 1]), make_float2(f1, f1)), ev[k],
-                                    mul2(make_float2(o2[t], o2[t + 1]), make_float2(sa.z, sa.z)));
-              const __nv_bfloat162 h = __floats2bfloat162_rn(o.x, o.y);
-              ot[t * 128] = h.x;
-              ot[(t + 1) * 128] = h.y;
-            }
+          for (int k = 0; k < 2; ++k) {
+            const int t = 4 * t4 + 2 * k;
+            const float2 o = fma2(mul2(make_float2(o1[t], o1[t + 1]), make_float2(f1, f1)), ev[k],
+                                  mul2(make_float2(o2[t], o2[t + 1]), make_float2(f2, f2)));
+            const __nv_bfloat162 h = __floats2bfloat162_rn(o.x, o.y);
+            ot[t * 128] = h.x;
+            ot[(t + 1) * 128] = h.y;
           }
-          // the block boundary at this chunk's end (a sequence that ends
-          // inside the chunk does not reach it)
-          if (to_ckpt-- == 0) {
-            to_ckpt = kpc - 1;
-            if (ck_idx < p.max_ckpt && P0 + (int64_t)(i + 1) * kC <= s.p1) {
-              const int32_t cid = GDN_GV(p.ckpt_ids, (long long)p.n_seq * p.max_ckpt)[(size_t)n * p.max_ckpt + ck_idx];
-              if (slot_class(cid, p.ck_num_slots) == 0)
-                put(GDN_GV(p.ck_ssm, p.ck_num_slots * slot_n) + ((size_t)cid * slot_n + tile_off));
-            }
+        }
+        umma::fence_proxy_async();
+        publish(&S.o_full);
+        // the block boundary at this chunk's end (a sequence that ends inside
+        // the chunk does not reach it)
+        if (to_ckpt-- == 0) {
+          to_ckpt = kpc - 1;
+          if (ck_idx < p.max_ckpt && (i + 1) * kC <= last) {
+            const int32_t cid = GDN_GV(p.ckpt_ids, (long long)p.n_seq * p.max_ckpt)[(size_t)n * p.max_ckpt + ck_idx];
+            if (slot_class(cid, p.ck_num_slots) == 0)
+              put(GDN_GV(p.ck_ssm, p.ck_num_slots * slot_n) + ((size_t)cid * slot_n + tile_off));
             ++ck_idx;
           }
         }
-        if (i + 1 < nit) operands(i + 1);
-        if (i + 1 < nit || !STATE) publish();
       }
     }
     if (!ok) {
