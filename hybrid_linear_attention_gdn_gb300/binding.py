@@ -174,9 +174,20 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+# torch.cuda.current_stream().cuda_stream without building a Stream object,
+# which is most of a small call's host time, where torch offers it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _current_stream() -> int:
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -276,26 +287,39 @@ class SsmParams:
         return cached[1]
 
 
-def _require(fn: str, what: str, t, dtype, shape):
-    """Raise unless t is a contiguous tensor of the dtype and shape on the current device."""
+def _require(fn: str, what: str, t, dtype, shape, device: int):
+    """Raise unless t is a contiguous tensor of the dtype and shape on the CUDA
+    device (the current one)."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device:
+        return
     if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
         raise GdnError(fn, ERR_INVALID_ARG, f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
                                             f"got {t.dtype} {tuple(t.shape)}, strides {t.stride()}")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
-        raise GdnError(fn, ERR_INVALID_ARG, f"{what} is on {t.device}, not on the current CUDA device")
+    raise GdnError(fn, ERR_INVALID_ARG, f"{what} is on {t.device}, not on the current CUDA device")
 
 
-def _require_ssm(fn: str, dims: Dims, pool: StatePool, params: SsmParams):
-    C, W, hv = dims.channels, dims.conv_width, dims.hv
-    _require(fn, "pool.ssm", pool.ssm, torch.float32, (pool.num_slots, hv, dims.dv, dims.dk))
-    _require(fn, "pool.conv", pool.conv, dims.conv_dtype, (pool.num_slots, W - 1, C))
-    _require(fn, "conv_w", params.conv_w, torch.float32, (C, W))
-    _require(fn, "A_log", params.A_log, torch.float32, (hv,))
-    _require(fn, "dt_bias", params.dt_bias, torch.float32, (hv,))
+def _device() -> int:
+    """The current CUDA device (-2 without one: no tensor is on it)."""
+    if torch.cuda.is_initialized() or torch.cuda.is_available():
+        return torch.cuda.current_device()
+    return -2
+
+
+def _require_pool(fn: str, what: str, dims: Dims, pool: StatePool, device: int):
+    n = pool.num_slots
+    _require(fn, what + ".ssm", pool.ssm, torch.float32, (n, dims.hv, dims.dv, dims.dk), device)
+    _require(fn, what + ".conv", pool.conv, dims.conv_dtype, (n, dims.conv_width - 1, dims.channels), device)
+
+
+def _require_ssm(fn: str, dims: Dims, params: SsmParams, device: int):
+    C, hv = dims.channels, dims.hv
+    _require(fn, "conv_w", params.conv_w, torch.float32, (C, dims.conv_width), device)
+    _require(fn, "A_log", params.A_log, torch.float32, (hv,), device)
+    _require(fn, "dt_bias", params.dt_bias, torch.float32, (hv,), device)
     if params.conv_bias is not None:
-        _require(fn, "conv_bias", params.conv_bias, torch.float32, (C,))
+        _require(fn, "conv_bias", params.conv_bias, torch.float32, (C,), device)
     if params.D is not None:
-        _require(fn, "D", params.D, torch.float32, (hv,))
+        _require(fn, "D", params.D, torch.float32, (hv,), device)
 
 
 # ---------------------------------------------------------------- entry points
@@ -546,12 +570,13 @@ def ssm_decode_step(dims: Dims, pool: StatePool, params: SsmParams, slot_ids, qk
     history updated in place; qkv [B][C] ordered q | k | v (the family's C, B,
     x), a [B][hv] time-step logits, out [B][hv][dv]."""
     fn, L = "gdn_ssm_decode_step", load()
-    B = int(slot_ids.shape[0])
-    _require_ssm(fn, dims, pool, params)
-    _require(fn, "slot_ids", slot_ids, torch.int32, (B,))
-    _require(fn, "qkv", qkv, dims.act_dtype, (B, dims.channels))
-    _require(fn, "a", a, dims.act_dtype, (B, dims.hv))
-    _require(fn, "out", out, dims.act_dtype, (B, dims.hv, dims.dv))
+    B, dev, act = slot_ids.shape[0], _device(), dims.act_dtype
+    _require_pool(fn, "pool", dims, pool, dev)
+    _require_ssm(fn, dims, params, dev)
+    _require(fn, "slot_ids", slot_ids, torch.int32, (B,), dev)
+    _require(fn, "qkv", qkv, act, (B, dims.channels), dev)
+    _require(fn, "a", a, act, (B, dims.hv), dev)
+    _require(fn, "out", out, act, (B, dims.hv, dims.dv), dev)
     cd, cp = dims.c(), params.c()
     st = L.gdn_ssm_decode_step(ctypes.byref(cd), pool.c(), ctypes.byref(cp), _ptr(slot_ids), B, _ptr(qkv), _ptr(a),
                                _ptr(out), _ptr(dev_err), _stream(stream))
@@ -570,23 +595,23 @@ def ssm_prefill(dims: Dims, pool: StatePool, ckpt: StatePool | None, params: Ssm
     the step of ssm_decode_step.  ckpt and ckpt_ids may be None (no
     checkpoints); workspace: ssm_prefill_workspace_size bytes."""
     fn, L = "gdn_ssm_prefill", load()
-    n_seq, total = int(slot_ids.shape[0]), int(total_tokens)
+    n_seq, total, dev, act = slot_ids.shape[0], int(total_tokens), _device(), dims.act_dtype
     max_ckpt = int(ckpt_ids.shape[1]) if ckpt_ids is not None and ckpt_ids.dim() == 2 else 0
-    _require_ssm(fn, dims, pool, params)
+    _require_pool(fn, "pool", dims, pool, dev)
+    _require_ssm(fn, dims, params, dev)
     if max_ckpt:
         if ckpt is None:
             raise GdnError(fn, ERR_INVALID_ARG, "ckpt_ids without a checkpoint pool")
-        _require(fn, "ckpt.ssm", ckpt.ssm, torch.float32, (ckpt.num_slots, dims.hv, dims.dv, dims.dk))
-        _require(fn, "ckpt.conv", ckpt.conv, dims.conv_dtype, (ckpt.num_slots, dims.conv_width - 1, dims.channels))
-        _require(fn, "ckpt_ids", ckpt_ids, torch.int32, (n_seq, max_ckpt))
-    _require(fn, "slot_ids", slot_ids, torch.int32, (n_seq,))
-    _require(fn, "cu_seqlens", cu_seqlens, torch.int32, (n_seq + 1,))
-    _require(fn, "start_pos", start_pos, torch.int64, (n_seq,))
-    _require(fn, "qkv", qkv, dims.act_dtype, (total, dims.channels))
-    _require(fn, "a", a, dims.act_dtype, (total, dims.hv))
-    _require(fn, "out", out, dims.act_dtype, (total, dims.hv, dims.dv))
+        _require_pool(fn, "ckpt", dims, ckpt, dev)
+        _require(fn, "ckpt_ids", ckpt_ids, torch.int32, (n_seq, max_ckpt), dev)
+    _require(fn, "slot_ids", slot_ids, torch.int32, (n_seq,), dev)
+    _require(fn, "cu_seqlens", cu_seqlens, torch.int32, (n_seq + 1,), dev)
+    _require(fn, "start_pos", start_pos, torch.int64, (n_seq,), dev)
+    _require(fn, "qkv", qkv, act, (total, dims.channels), dev)
+    _require(fn, "a", a, act, (total, dims.hv), dev)
+    _require(fn, "out", out, act, (total, dims.hv, dims.dv), dev)
     if workspace is not None:
-        _require(fn, "workspace", workspace, workspace.dtype, workspace.shape)
+        _require(fn, "workspace", workspace, workspace.dtype, workspace.shape, dev)
     cd, cp = dims.c(), params.c()
     ck = ckpt.c() if ckpt is not None else CPool(None, None, 0)
     st = L.gdn_ssm_prefill(ctypes.byref(cd), pool.c(), ck, ctypes.byref(cp), _ptr(slot_ids), _ptr(cu_seqlens),
@@ -605,28 +630,29 @@ def add_rmsnorm(x, residual, weight, eps: float = 1e-6, y=None, q8=None, scales=
     fn, L = "gdn_add_rmsnorm", load()
     if x.dtype not in _DT_CODE or x.dim() < 1 or (residual is not None and residual.dtype not in _DT_CODE):
         raise GdnError(fn, ERR_INVALID_ARG, "x and residual must be float32 or bfloat16")
-    shape, d = tuple(x.shape), int(x.shape[-1])
+    shape, dev = x.shape, _device()
+    d = shape[-1]
     rows = x.numel() // d if d else 0
-    _require(fn, "x", x, x.dtype, shape)
+    _require(fn, "x", x, x.dtype, shape, dev)
     if residual is not None:
-        _require(fn, "residual", residual, residual.dtype, shape)
-    _require(fn, "weight", weight, torch.float32, (d,))
+        _require(fn, "residual", residual, residual.dtype, shape, dev)
+    _require(fn, "weight", weight, torch.float32, (d,), dev)
     if y is None and q8 is None:
         y = torch.empty_like(x)
     if y is not None:
-        _require(fn, "y", y, x.dtype, shape)
+        _require(fn, "y", y, x.dtype, shape, dev)
     scale_type = SCALE_F32
     if q8 is not None:
         if group < 0 or (group and d % group):
             raise GdnError(fn, ERR_INVALID_ARG, f"group {group} does not divide {d}")
-        _require(fn, "q8", q8, torch.float8_e4m3fn, shape)
+        _require(fn, "q8", q8, torch.float8_e4m3fn, shape, dev)
         if scales is None:
-            scales = torch.empty(shape[:-1] + (d // (group or d),), dtype=torch.float32, device=x.device)
+            scales = torch.empty((*shape[:-1], d // (group or d)), dtype=torch.float32, device=x.device)
         if scales.dtype != torch.float32:
             scale_type = SCALE_E8M0
             if scales.dtype not in (torch.uint8, torch.float8_e8m0fnu):
                 raise GdnError(fn, ERR_INVALID_ARG, f"scales of {scales.dtype}")
-        _require(fn, "scales", scales, scales.dtype, shape[:-1] + (d // (group or d),))
+        _require(fn, "scales", scales, scales.dtype, (*shape[:-1], d // (group or d)), dev)
     st = L.gdn_add_rmsnorm(_DT_CODE[x.dtype], _DT_CODE[residual.dtype] if residual is not None else _DT_CODE[x.dtype],
                            _ptr(x), _ptr(residual), _ptr(weight), float(eps), rows, d, _ptr(y), _ptr(q8),
                            _ptr(scales), int(group), scale_type, _stream(stream))
@@ -641,23 +667,27 @@ def batch_maps(new_lens, start_pos, block: int, block_table, free_ids, n_free, c
     is updated in place unless n_free_out is given; seq_ids, positions and
     slot_map (all of one length, the rows' capacity) may be None."""
     fn, L = "gdn_batch_maps", load()
-    n_seq = int(new_lens.shape[0])
-    i32, i64 = torch.int32, torch.int64
+    n_seq, dev, i32, i64 = new_lens.shape[0], _device(), torch.int32, torch.int64
     rows = next((int(t.shape[0]) for t in (seq_ids, positions, slot_map) if t is not None), 2**31 - 1)
     if n_free_out is None:
         n_free_out = n_free
-    for what, t, dt, shape in (("new_lens", new_lens, i32, (n_seq,)), ("start_pos", start_pos, i64, (n_seq,)),
-                               ("block_table", block_table, i32, (n_seq, block_table.shape[-1])),
-                               ("free_ids", free_ids, i32, (free_ids.numel(),)), ("n_free", n_free, i32, (1,)),
-                               ("n_free_out", n_free_out, i32, (1,)), ("cu_seqlens", cu_seqlens, i32, (n_seq + 1,))):
-        _require(fn, what, t, dt, shape)
+    _require(fn, "new_lens", new_lens, i32, (n_seq,), dev)
+    _require(fn, "start_pos", start_pos, i64, (n_seq,), dev)
+    _require(fn, "block_table", block_table, i32, (n_seq, block_table.shape[-1]), dev)
+    _require(fn, "free_ids", free_ids, i32, (free_ids.numel(),), dev)
+    _require(fn, "n_free", n_free, i32, (1,), dev)
+    _require(fn, "n_free_out", n_free_out, i32, (1,), dev)
+    _require(fn, "cu_seqlens", cu_seqlens, i32, (n_seq + 1,), dev)
     max_ckpt = 0
     if ckpt_ids is not None:
         max_ckpt = int(ckpt_ids.shape[-1])
-        _require(fn, "ckpt_ids", ckpt_ids, i32, (n_seq, max_ckpt))
-    for what, t, dt in (("seq_ids", seq_ids, i32), ("positions", positions, i64), ("slot_map", slot_map, i64)):
-        if t is not None:
-            _require(fn, what, t, dt, (rows,))
+        _require(fn, "ckpt_ids", ckpt_ids, i32, (n_seq, max_ckpt), dev)
+    if seq_ids is not None:
+        _require(fn, "seq_ids", seq_ids, i32, (rows,), dev)
+    if positions is not None:
+        _require(fn, "positions", positions, i64, (rows,), dev)
+    if slot_map is not None:
+        _require(fn, "slot_map", slot_map, i64, (rows,), dev)
     st = L.gdn_batch_maps(_ptr(new_lens), _ptr(start_pos), n_seq, int(block), _ptr(block_table),
                           int(block_table.shape[-1]), _ptr(free_ids), free_ids.numel(), _ptr(n_free),
                           _ptr(n_free_out), _ptr(cu_seqlens), _ptr(ckpt_ids), max_ckpt, _ptr(seq_ids),

@@ -504,15 +504,18 @@ extern "C" gdn_status gdn_ssm_prefill(const gdn_dims* dims, gdn_pool pool, gdn_p
   const char* path = std::getenv("GDN_SSM_PREFILL_PATH");
   const bool chunked = !(path && !std::strcmp(path, "recurrent")) &&
                        ssm_chunk_supported(*dims, n_seq, total_tokens, qkv, out, *params);
-  if (chunked) e = ssm_chunk_launch(p, *dims, workspace, s);
-  else switch (dims->dk) {
-    case 16: e = dispatch_recurrent<16, 2>(p, dims->act_dtype, dims->conv_dtype, s); break;
-    case 64: e = dispatch_recurrent<64, 4>(p, dims->act_dtype, dims->conv_dtype, s); break;
-    case 128: e = dispatch_recurrent<128, 8>(p, dims->act_dtype, dims->conv_dtype, s); break;
+  if (chunked) {
+    e = ssm_chunk_launch(p, *dims, ckpt.conv, workspace, s);
+  } else {
+    switch (dims->dk) {
+      case 16: e = dispatch_recurrent<16, 2>(p, dims->act_dtype, dims->conv_dtype, s); break;
+      case 64: e = dispatch_recurrent<64, 4>(p, dims->act_dtype, dims->conv_dtype, s); break;
+      case 128: e = dispatch_recurrent<128, 8>(p, dims->act_dtype, dims->conv_dtype, s); break;
+    }
+    if (e == cudaSuccess)
+      e = conv_history_launch(*dims, pool, ckpt, slot_ids, cu_seqlens, start_pos, n_seq, total_tokens, ckpt_ids,
+                              max_ckpt, ckpt_block, qkv, dev_err, s);
   }
-  if (e == cudaSuccess)
-    e = conv_history_launch(*dims, pool, ckpt, slot_ids, cu_seqlens, start_pos, n_seq, total_tokens, ckpt_ids,
-                            max_ckpt, ckpt_block, qkv, dev_err, s);
   if (e != cudaSuccess) return GDN_ERR_CUDA;
   count_launch(GDN_K_SSM_PREFILL);
   return GDN_OK;

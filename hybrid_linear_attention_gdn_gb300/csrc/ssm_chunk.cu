@@ -47,6 +47,7 @@
 #include "ssm.cuh"
 #include "ssm_chunk.cuh"
 #include "decode_tma.cuh"  // sm_count
+#include "prefill_history.cuh"
 #include "tma.cuh"
 #include "umma.cuh"
 
@@ -80,11 +81,14 @@ constexpr uint32_t kQKBytes = offsetof(Record, g), kGBytes = sizeof(Record::g), 
 
 struct ChunkArgs {
   PrefillArgs p;
-  Record* rec;       // [chunk slots][hk]
-  float* seg_state;  // [segment slots][hv][dv][dk]
-  float* seg_decay;  // [segment slots][hv]
+  Record* rec;           // [chunk slots][hk]
+  __nv_bfloat16* vhist;  // [n_seq][3][hv dv]: the V channels' conv history before the call
+  float* seg_state;      // [segment slots][hv][dv][dk]
+  float* seg_decay;      // [segment slots][hv]
   int32_t n_chunks, n_segs;  // slots
   int32_t seg_chunks;
+  int32_t hist_blocks, hist_groups;  // the history work items: sequences x channel blocks
+  pfx::PrefillArgs hist;
 };
 
 struct Seq {
@@ -176,6 +180,34 @@ __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t by
                : "memory");
 }
 
+// Sequence n, by hk CTAs of which this is number `part`: errors reported, an
+// unusable slot's rows zeroed, and the V channels' conv history kept aside,
+// so that the chain launch may both start chains from it and replace it.
+__device__ __forceinline__ void sequence_block(const ChunkArgs& a, const int n, const int part) {
+  const PrefillArgs& p = a.p;
+  Seq s;
+  bool bad;
+  const bool some = load_seq(p, n, s, bad);
+  const int cls = slot_class(s.slot, p.num_slots);
+  if (part == 0 && threadIdx.x == 0) {
+    if (bad) report(p.err, GDN_DEV_ERR_SEQLENS);
+    else if (cls == 2) report(p.err, GDN_DEV_ERR_SLOT_OOB);
+  }
+  if (!some) return;
+  const int64_t row = (int64_t)p.hv * p.dv / 8, step = (int64_t)p.hk * kFT;  // 16-byte pieces
+  const int64_t first = (int64_t)part * kFT + threadIdx.x;
+  if (cls) {
+    const auto out = GDN_GV(reinterpret_cast<uint4*>(p.out), p.total * row);
+    for (int64_t e = first; e < s.len * row; e += step) out[s.t0 * row + e] = make_uint4(0u, 0u, 0u, 0u);
+    return;
+  }
+  const auto hist = GDN_GV(reinterpret_cast<const __nv_bfloat16*>(p.conv), (long long)p.num_slots * 3 * p.C) +
+                    (size_t)s.slot * 3 * p.C;
+  const auto to = GDN_GV(reinterpret_cast<uint4*>(a.vhist), (long long)p.n_seq * 3 * row);
+  for (int64_t e = first; e < 3 * row; e += step)
+    to[(int64_t)n * 3 * row + e] = vec_at<const uint4>(hist, e / row * p.C + 2 * p.hk * kDK + e % row * 8);
+}
+
 __global__ void __launch_bounds__(kFT, 2) ssm_features_kernel(const ChunkArgs a) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   FeatSmem& S = *reinterpret_cast<FeatSmem*>(smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023));
@@ -184,6 +216,11 @@ __global__ void __launch_bounds__(kFT, 2) ssm_features_kernel(const ChunkArgs a)
   const int hq = blockIdx.y;
   const int64_t cslot = blockIdx.x;
   pdl_wait();
+  pdl_trigger();
+  if (cslot >= a.n_chunks) {
+    sequence_block(a, (int)(cslot - a.n_chunks), hq);
+    return;
+  }
   const int n = find_seq(p, cslot, 1, false);
   Seq s;
   bool bad;
@@ -500,15 +537,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tile = blockIdx.x, h0 = tile * NH, hq = h0 / p.G;
   pdl_wait();
+  pdl_trigger();
+  if (!STATE && (int)blockIdx.y >= a.n_segs) {
+    // the conv histories of checkpoints and final states: after the chains,
+    // on the SMs that they leave free
+    const int item = ((int)blockIdx.y - a.n_segs) * (int)gridDim.x + (int)blockIdx.x;
+    if (item < p.n_seq * a.hist_blocks)
+      for (int grp = 0; grp < a.hist_groups; ++grp)
+        pfx::history_channel<__nv_bfloat16, __nv_bfloat16>(a.hist, item / a.hist_blocks, grp,
+                                                           item % a.hist_blocks * kThreads + tid);
+    return;
+  }
   if (warp == 0) {
     const int f = find_seq(p, blockIdx.y, a.seg_chunks, true);
     if (lane == 0) S.seq = f;
   }
   __syncthreads();
-  const int n = S.seq;
+  const int n = S.seq, seq_n = n;
   Seq s;
   bool bad_seq;
-  // inconsistent, empty and padded sequences: ssm_check_kernel's
+  // inconsistent, empty and padded sequences: the features kernel's
   if (!load_seq(p, n, s, bad_seq) || slot_class(s.slot, p.num_slots)) return;
   const int64_t seg_first = s.first / a.seg_chunks + n;
   const int seg = (int)(blockIdx.y - seg_first);
@@ -778,13 +826,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (P - 3 < s.p0) {
           // the up to 3 rows just before the sequence come from the history
           const int64_t lo = max(P - 3, s.p0 - 3), hi = min(P + kC, s.p0);
-          const auto hist = GDN_GV(reinterpret_cast<const __nv_bfloat16*>(p.conv), (long long)p.num_slots * 3 * p.C) +
-                            (size_t)s.slot * 3 * p.C;
+          const int64_t row = (int64_t)p.hv * DV;
+          const auto hist = GDN_GV((const __nv_bfloat16*)a.vhist, (long long)p.n_seq * 3 * row) + (size_t)seq_n * 3 * row;
           for (int64_t pos = lo; pos < hi; ++pos)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               S.raw[i & 1][GDN_S((int)(pos - (P - 3)), kRawRows)][32 * k + lane] =
-                  hist[(size_t)(3 - (s.p0 - pos)) * p.C + 2 * p.hk * kDK + tile * 128 + 32 * k + lane];
+                  hist[(3 - (s.p0 - pos)) * row + tile * 128 + 32 * k + lane];
           umma::fence_proxy_async();  // before a later chunk's copy into these rows
           __syncwarp();
         }
@@ -1135,39 +1183,38 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) umma::tmem_dealloc(tmem, TM_COLS);
 }
 
-// Inconsistent sequences reported, unusable slots' rows zeroed (grid: sequences).
-__global__ void __launch_bounds__(256) ssm_check_kernel(const PrefillArgs p) {
-  pdl_wait();
-  pdl_trigger();
-  const int n = blockIdx.x;
-  Seq s;
-  bool bad;
-  const bool some = load_seq(p, n, s, bad);
-  if (bad && threadIdx.x == 0) report(p.err, GDN_DEV_ERR_SEQLENS);
-  const int cls = slot_class(s.slot, p.num_slots);
-  if (!bad && cls == 2 && threadIdx.x == 0) report(p.err, GDN_DEV_ERR_SLOT_OOB);
-  if (!some || !cls) return;
-  const auto out = GDN_GV(reinterpret_cast<uint4*>(p.out), p.total * p.hv * p.dv / 8);
-  const int64_t row = (int64_t)p.hv * p.dv / 8;
-  for (int64_t e = threadIdx.x; e < s.len * row; e += blockDim.x) out[s.t0 * row + e] = make_uint4(0u, 0u, 0u, 0u);
-}
-
 struct Layout {
-  size_t rec, state, decay, total;
+  size_t rec, vhist, state, decay, total;
   int64_t n_chunks, n_segs;
   int32_t seg_chunks;
 };
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// Chunks per segment.  The lengths are on the device: the rule sees their sum.
+//  * Enough chains for the SMs (sequences x tiles >= 96): whole sequences.  The
+//    state pass costs about half as much again, and cutting only those longer
+//    than the mean measured no gain (7 ragged sequences of the 8-group layer
+//    186 us whole, 193 us cut; 4 x 8192 501 and 510 us).
+//  * Fewer: as many segments as fill the SMs, at most kMaxSegs per sequence
+//    of the mean length (a segment reads all its predecessors' states), and
+//    not below kMinSeg chunks.
+constexpr int64_t kMinSeg = 8, kMaxSegs = 16;
+int64_t seg_chunks(int64_t tiles, int64_t n_seq, int64_t total) {
+  const int64_t chunks = (total + kC - 1) / kC, mean = (chunks + n_seq - 1) / n_seq;
+  if (tiles * n_seq >= 96) return 1 << 30;
+  const int64_t fill = (tiles * chunks + sm_count() - 1) / sm_count();
+  return max(max(fill + 1, kMinSeg), (mean + kMaxSegs - 1) / kMaxSegs);
+}
+
 Layout layout(const gdn_dims& d, int32_t n_seq, int64_t total) {
   Layout l;
   l.n_chunks = total / kC + 2 * (int64_t)n_seq;
   const int64_t tiles = (int64_t)d.hv * d.dv / 128;
-  l.seg_chunks = 1 << 30;
-  (void)tiles;
+  l.seg_chunks = (int32_t)seg_chunks(tiles, n_seq, total);
   l.n_segs = l.n_chunks / l.seg_chunks + n_seq;
   size_t off = 0;
   l.rec = off; off += sizeof(Record) * (size_t)l.n_chunks * d.hk;
+  l.vhist = off; off += up256(sizeof(__nv_bfloat16) * 3 * (size_t)n_seq * d.hv * d.dv);
   l.state = off;
   if (l.seg_chunks < l.n_chunks) {
     off += sizeof(float) * (size_t)l.n_segs * d.hv * d.dv * d.dk;
@@ -1179,20 +1226,25 @@ Layout layout(const gdn_dims& d, int32_t n_seq, int64_t total) {
   return l;
 }
 
+// grid rows of the chain launch that hold the history work items
+int64_t hist_blocks(int64_t C) { return (C + kThreads - 1) / kThreads; }
+int64_t hist_rows(int64_t n_seq, int64_t C, int64_t tiles) { return (n_seq * hist_blocks(C) + tiles - 1) / tiles; }
+
 template <int NH>
 cudaError_t launch_chain(const ChunkArgs& a, const Layout& l, const CUtensorMap& xmap, const CUtensorMap& omap,
                          cudaStream_t s) {
   const size_t smem = sizeof(ChainSmem<NH>) + 1024;
-  const dim3 grid((unsigned)(a.p.hv / NH), (unsigned)l.n_segs);
+  const unsigned tiles = (unsigned)(a.p.hv / NH);
+  const dim3 grid(tiles, (unsigned)l.n_segs), all(tiles, (unsigned)(l.n_segs + hist_rows(a.p.n_seq, a.p.C, tiles)));
   cudaError_t e;
   if (l.seg_chunks < l.n_chunks) {
     auto k = ssm_chain_kernel<NH, true>;
     if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
-    if ((e = launch_plain(k, grid, dim3(kThreads), smem, s, dim3(1), a, xmap, omap)) != cudaSuccess) return e;
+    if ((e = launch_pdl(k, grid, dim3(kThreads), smem, s, dim3(1), a, xmap, omap)) != cudaSuccess) return e;
   }
   auto k = ssm_chain_kernel<NH, false>;
   if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
-  return launch_plain(k, grid, dim3(kThreads), smem, s, dim3(1), a, xmap, omap);
+  return launch_pdl(k, all, dim3(kThreads), smem, s, dim3(1), a, xmap, omap);
 }
 
 }  // namespace
@@ -1204,23 +1256,53 @@ bool ssm_chunk_shape(const gdn_dims& d) {
 
 bool ssm_chunk_supported(const gdn_dims& d, int32_t n_seq, int64_t total, const void* qkv, const void* out,
                          const gdn_ssm_params& p) {
-  return ssm_chunk_shape(d) && total > 0 && layout(d, n_seq, total).n_segs <= 65535 && d.hk <= 65535 &&
+  const int64_t tiles = (int64_t)d.hv * d.dv / 128;
+  return ssm_chunk_shape(d) && total > 0 && d.hk <= 65535 &&
+         layout(d, n_seq, total).n_segs + hist_rows(n_seq, channels(d), tiles) <= 65535 &&
          aligned(qkv, 16) && aligned(out, 16) && aligned(p.conv_w, 16);
 }
 
 size_t ssm_chunk_workspace(const gdn_dims& d, int32_t n_seq, int64_t total) { return layout(d, n_seq, total).total; }
 
-cudaError_t ssm_chunk_launch(const ssm::PrefillArgs& p, const gdn_dims& d, void* workspace, cudaStream_t s) {
+cudaError_t ssm_chunk_launch(const ssm::PrefillArgs& p, const gdn_dims& d, void* ck_conv, void* workspace,
+                             cudaStream_t s) {
   const Layout l = layout(d, p.n_seq, p.total);
   ChunkArgs a = {};
   a.p = p;
   uint8_t* const ws = reinterpret_cast<uint8_t*>(((uintptr_t)workspace + 1023) & ~(uintptr_t)1023);
   a.rec = reinterpret_cast<Record*>(ws + l.rec);
+  a.vhist = reinterpret_cast<__nv_bfloat16*>(ws + l.vhist);
   a.seg_state = reinterpret_cast<float*>(ws + l.state);
   a.seg_decay = reinterpret_cast<float*>(ws + l.decay);
   a.n_chunks = (int32_t)l.n_chunks;
   a.n_segs = (int32_t)l.n_segs;
   a.seg_chunks = l.seg_chunks;
+  a.hist_blocks = (int32_t)hist_blocks(p.C);
+  a.hist_groups = p.max_ckpt > pfx::kCkGroup ? (p.max_ckpt + pfx::kCkGroup - 1) / pfx::kCkGroup : 1;
+  pfx::PrefillArgs& h = a.hist;
+  h.ssm = p.ssm;
+  h.conv = const_cast<void*>(p.conv);
+  h.num_slots = p.num_slots;
+  h.ck_ssm = p.ck_ssm;
+  h.ck_conv = ck_conv;
+  h.ck_num_slots = p.ck_num_slots;
+  h.slot_ids = p.slot_ids;
+  h.cu_seqlens = p.cu_seqlens;
+  h.start_pos = p.start_pos;
+  h.n_seq = p.n_seq;
+  h.total = p.total;
+  h.ckpt_ids = p.ckpt_ids;
+  h.max_ckpt = p.max_ckpt;
+  h.ckpt_block = p.ckpt_block;
+  h.qkv = p.qkv;
+  h.err = p.err;
+  h.hk = p.hk;
+  h.hv = p.hv;
+  h.dk = p.dk;
+  h.dv = p.dv;
+  h.W = p.W;
+  h.C = p.C;
+  h.G = p.G;
   CUtensorMap xmap, omap;
   cudaError_t e;
   if ((e = tensor_map_2d(&xmap, p.qkv, p.total, p.C, 2, 128, kRawRows, CU_TENSOR_MAP_SWIZZLE_NONE)) != cudaSuccess)
@@ -1232,10 +1314,8 @@ cudaError_t ssm_chunk_launch(const ssm::PrefillArgs& p, const gdn_dims& d, void*
   if ((e = cudaFuncSetAttribute(ssm_features_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
       cudaSuccess)
     return e;
-  if ((e = launch_plain(ssm_features_kernel, dim3((unsigned)l.n_chunks, (unsigned)p.hk), dim3(kFT), smem, s, dim3(1),
-                        a)) != cudaSuccess)
-    return e;
-  if ((e = launch_plain(ssm_check_kernel, dim3((unsigned)p.n_seq), dim3(256), 0, s, dim3(1), p)) != cudaSuccess)
+  if ((e = launch_pdl(ssm_features_kernel, dim3((unsigned)(l.n_chunks + p.n_seq), (unsigned)p.hk), dim3(kFT), smem, s,
+                      dim3(1), a)) != cudaSuccess)
     return e;
   return p.dv == 64 ? launch_chain<2>(a, l, xmap, omap, s) : launch_chain<1>(a, l, xmap, omap, s);
 }

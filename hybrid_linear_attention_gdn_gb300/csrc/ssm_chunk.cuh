@@ -8,5 +8,7 @@ bool ssm_chunk_shape(const gdn_dims& d);
 bool ssm_chunk_supported(const gdn_dims& d, int32_t n_seq, int64_t total, const void* qkv, const void* out,
                          const gdn_ssm_params& p);
 size_t ssm_chunk_workspace(const gdn_dims& d, int32_t n_seq, int64_t total);
-cudaError_t ssm_chunk_launch(const ssm::PrefillArgs& p, const gdn_dims& d, void* workspace, cudaStream_t s);
+// the whole prefill: outputs, states, checkpoints and conv histories
+cudaError_t ssm_chunk_launch(const ssm::PrefillArgs& p, const gdn_dims& d, void* ck_conv, void* workspace,
+                             cudaStream_t s);
 }  // namespace gdn
