@@ -460,6 +460,7 @@ struct __align__(1024) ChainSmem {
   uint64_t ready;                     // operands in place
   uint64_t ds_bar, o_bar;             // dS^T done; all products done
   uint64_t o_full, o_free;            // output staged; staging read
+  uint64_t s_used;                    // the state's way through S.qk is free
   uint32_t tmem_base;
   int seq;
 };
@@ -501,6 +502,12 @@ __device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, float (&va
         "=f"(vb[8]), "=f"(vb[9]), "=f"(vb[10]), "=f"(vb[11]), "=f"(vb[12]), "=f"(vb[13]), "=f"(vb[14]), "=f"(vb[15])
       : "r"(ta), "r"(tb)
       : "memory");
+}
+// 32 bytes to a 32-byte aligned place
+__device__ __forceinline__ void st_global32(float* to, float4 a, float4 b) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(to), "f"(a.x), "f"(a.y), "f"(a.z), "f"(a.w),
+               "f"(b.x), "f"(b.y), "f"(b.z), "f"(b.w)
+               : "memory");
 }
 __device__ __forceinline__ uint32_t half2_bits(float x, float y) {
   const __half2 h = __floats2half2_rn(x, y);
@@ -582,6 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&S.o_bar, 1);
     mbar_init(&S.o_full, kCompute / 32);
     mbar_init(&S.o_free, 1);
+    mbar_init(&S.s_used, kCompute / 32);
 #pragma unroll
     for (int i = 0; i < NH; ++i) S.smax[i] = 0;
     fence_mbar_init();
@@ -613,10 +621,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         bulk(S.qk[i & 1] + kSkip, a.rec[rec0 + (int64_t)i * p.hk].q + kSkip, kQKBytes - kSkip, &S.qk_bar[i & 1]);
       };
       int n_qk = 0, n_mma = 0;  // issued
-      if (lane == 0) {
+      bool ok = __all_sync(0xffffffffu, mbar_wait(&S.s_used, 0));
+      if (ok && lane == 0) {
         for (; n_qk < 2 && n_qk < nit; ++n_qk) load_qk(n_qk);
       }
-      bool ok = true;
       // chunk i's staged output, the whole warp
       auto store = [&](int i) -> bool {
         if (!__all_sync(0xffffffffu, mbar_wait(&S.o_full, i & 1))) return false;
@@ -887,41 +895,72 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the state entering the segment, S^T row lrow, columns 32 qq ..
     float2 st[16];
     float seg_dec = 1.f;
-    const size_t tile_off = ((size_t)tile * 128 + lrow) * kDK + 32 * qq;  // within one slot's [hv][dv][dk]
-    const long long slot_n = (long long)p.hv * DV * kDK;
+    const long long slot_n = (long long)p.hv * DV * kDK;  // a slot's state, [hv][dv][dk]
     const auto segs = GDN_GV(a.seg_state, a.n_segs * slot_n);
-    const auto pool = GDN_GV(p.ssm, p.num_slots * slot_n) + ((size_t)s.slot * slot_n + tile_off);
-    auto put = [&](const auto& to) {  // the state to its place in a slot
+    // A state tile goes to and from global memory in whole rows (one per
+    // warp-wide access of 16-byte pieces) and through S.qk, which is free
+    // before the first chunk's operands arrive and after the last product, to
+    // the threads' quarter rows: piece p of row r at p ^ (r & 7).  (Quarter
+    // rows straight from global memory took 4,000 cycles a tile: 32 lines per
+    // access.)
+    constexpr unsigned kTile = 128 * kDK * 4;
+    static_assert(kTile <= sizeof(S.qk), "the state tile's way through shared memory");
+    uint8_t* const tile_smem = &S.qk[0][0];
+    const size_t tile0 = (size_t)tile * 128 * kDK;
+    auto piece_off = [](int r, int p) { return (uint32_t)r * 512u + (uint32_t)((p ^ (r & 7)) << 4); };
+    auto save = [&](const auto& to) {  // the state to `to` (the tile's place), all compute warps
 #pragma unroll
-      for (int e = 0; e < 8; ++e) vec_at<float4>(to, 4 * e) = join4(st[2 * e], st[2 * e + 1]);
+      for (int e = 0; e < 8; ++e)
+        tile_at<float4>(tile_smem, kTile, piece_off(lrow, 8 * qq + e)) = join4(st[2 * e], st[2 * e + 1]);
+      named_sync(1, kCompute);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        vec_at<float4>(to, ((warp + 16 * j) * 32 + lane) * 4) =
+            tile_at<float4>(tile_smem, kTile, piece_off(warp + 16 * j, lane));
     };
     {
       // One segment: from the slot.  Several: the first launch starts the
       // first segment from the slot and keeps a copy, at the last segment's
       // otherwise unused place, for the second launch; the others from zero.
-      const auto keep = segs + (n_seg > 1 ? (seg_first + n_seg - 1) * slot_n + (int64_t)tile_off : 0);
+      const auto slot = GDN_GV(p.ssm, p.num_slots * slot_n) + ((size_t)s.slot * slot_n + tile0);
+      const auto keep = segs + (n_seg > 1 ? (seg_first + n_seg - 1) * slot_n + (int64_t)tile0 : 0);
+      float4 v[8];  // piece `lane` of rows warp, warp + 16, ..
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (seg == 0) {
-          v = STATE || n_seg == 1 ? vec_at<const float4>(pool, 4 * i) : vec_at<const float4>(keep, 4 * i);
-          if (STATE) vec_at<float4>(keep, 4 * i) = v;
-        }
-        st[2 * i] = lo2(v);
-        st[2 * i + 1] = hi2(v);
+      for (int j = 0; j < 8; ++j) {
+        const int at = ((warp + 16 * j) * 32 + lane) * 4;
+        v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (seg == 0 || !STATE) v[j] = STATE || n_seg == 1 ? vec_at<const float4>(slot, at) : vec_at<const float4>(keep, at);
+        if (STATE && seg == 0) vec_at<float4>(keep, at) = v[j];
       }
       if (!STATE) {
         for (int k = 0; k < seg; ++k) {
-          const auto L = segs + ((seg_first + k) * slot_n + (int64_t)tile_off);
-          const float d = k ? GDN_GV(a.seg_decay, (long long)a.n_segs * p.hv)[(seg_first + k) * p.hv + h0 + hl] : 0.f;
+          const auto L = segs + ((seg_first + k) * slot_n + (int64_t)tile0);
+          const auto dec = GDN_GV(a.seg_decay, (long long)a.n_segs * p.hv) + ((seg_first + k) * p.hv + h0);
+          // the first segment's state holds the slot's already
+          const float d0 = k ? dec[0] : 0.f, d1 = k ? dec[NH - 1] : 0.f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 v = vec_at<const float4>(L, 4 * i);
-            st[2 * i] = fma2(make_float2(d, d), st[2 * i], lo2(v));
-            st[2 * i + 1] = fma2(make_float2(d, d), st[2 * i + 1], hi2(v));
+          for (int j = 0; j < 8; ++j) {
+            const float4 x = vec_at<const float4>(L, ((warp + 16 * j) * 32 + lane) * 4);
+            const float d = j < 4 ? d0 : d1;  // rows 64 .. are the second of two heads
+            v[j].x = fmaf(d, v[j].x, x.x);
+            v[j].y = fmaf(d, v[j].y, x.y);
+            v[j].z = fmaf(d, v[j].z, x.z);
+            v[j].w = fmaf(d, v[j].w, x.w);
           }
         }
       }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) tile_at<float4>(tile_smem, kTile, piece_off(warp + 16 * j, lane)) = v[j];
+      named_sync(1, kCompute);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float4 x = tile_at<float4>(tile_smem, kTile, piece_off(lrow, 8 * qq + e));
+        st[2 * e] = lo2(x);
+        st[2 * e + 1] = hi2(x);
+      }
+      umma::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.s_used);
     }
     if (!STATE) {
       uint32_t m = 0;
@@ -1161,21 +1200,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           to_ckpt = kpc - 1;
           if (ck_idx < p.max_ckpt && (i + 1) * kC <= last) {
             const int32_t cid = GDN_GV(p.ckpt_ids, (long long)p.n_seq * p.max_ckpt)[(size_t)n * p.max_ckpt + ck_idx];
-            if (slot_class(cid, p.ck_num_slots) == 0)
-              put(GDN_GV(p.ck_ssm, p.ck_num_slots * slot_n) + ((size_t)cid * slot_n + tile_off));
+            if (slot_class(cid, p.ck_num_slots) == 0) {
+              // quarter rows, 32 bytes per access where the pool's alignment allows
+              const auto to = GDN_GV(p.ck_ssm, p.ck_num_slots * slot_n) +
+                              ((size_t)cid * slot_n + ((size_t)tile * 128 + lrow) * kDK + 32 * qq);
+              if (((uintptr_t)p.ck_ssm & 31) == 0) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  st_global32(to.at(8 * e, 8), join4(st[4 * e], st[4 * e + 1]), join4(st[4 * e + 2], st[4 * e + 3]));
+              } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) vec_at<float4>(to, 4 * e) = join4(st[2 * e], st[2 * e + 1]);
+              }
+            }
             ++ck_idx;
           }
         }
       }
     }
-    if (!ok) {
-      if (lane == 0) report(p.err, GDN_DEV_ERR_TIMEOUT);
+    if (named_sync_or(1, kCompute, !ok)) {
+      if (tid == 0) report(p.err, GDN_DEV_ERR_TIMEOUT);
     } else if (STATE) {
-      put(segs + ((seg_first + seg) * slot_n + (int64_t)tile_off));
+      save(segs + ((seg_first + seg) * slot_n + (int64_t)tile0));
       if (qq == 0 && lrow % DV == 0)
         GDN_GV(a.seg_decay, (long long)a.n_segs * p.hv)[(seg_first + seg) * p.hv + h0 + hl] = seg_dec;
     } else if (seg == n_seg - 1) {
-      put(pool);
+      save(GDN_GV(p.ssm, p.num_slots * slot_n) + ((size_t)s.slot * slot_n + tile0));
     }
   }
   umma::fence_before();
