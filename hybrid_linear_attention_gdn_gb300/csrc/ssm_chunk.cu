@@ -558,23 +558,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     const int f = find_seq(p, blockIdx.y, a.seg_chunks, true);
     if (lane == 0) S.seq = f;
-  }
-  __syncthreads();
-  const int n = S.seq, seq_n = n;
-  Seq s;
-  bool bad_seq;
-  // inconsistent, empty and padded sequences: the features kernel's
-  if (!load_seq(p, n, s, bad_seq) || slot_class(s.slot, p.num_slots)) return;
-  const int64_t seg_first = s.first / a.seg_chunks + n;
-  const int seg = (int)(blockIdx.y - seg_first);
-  const int n_seg = (s.nch + a.seg_chunks - 1) / a.seg_chunks;
-  if (seg < 0 || seg >= n_seg || (STATE && seg == n_seg - 1)) return;
-  const int c_begin = seg * a.seg_chunks, c_end = min(s.nch, c_begin + a.seg_chunks);
-  const int nit = c_end - c_begin;
-  const int64_t P0 = (s.p0 / kC + c_begin) * kC;  // the first chunk's first position
-
-  if (warp == 0) umma::tmem_alloc(&S.tmem_base, TM_COLS);
-  if (tid == 0) {
+  } else if (warp == 1) {
+    umma::tmem_alloc(&S.tmem_base, TM_COLS);
+  } else if (tid == 64) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.x_bar[i], 1);
@@ -597,6 +583,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   umma::fence_before();
   __syncthreads();
   umma::fence_after();
+  const int n = S.seq, seq_n = n;
+  Seq s;
+  bool bad_seq;
+  // inconsistent, empty and padded sequences are the features kernel's
+  bool active = load_seq(p, n, s, bad_seq) && !slot_class(s.slot, p.num_slots);
+  const int64_t seg_first = active ? s.first / a.seg_chunks + n : 0;
+  const int seg = (int)(blockIdx.y - seg_first);
+  const int n_seg = active ? (s.nch + a.seg_chunks - 1) / a.seg_chunks : 0;
+  active = active && seg >= 0 && seg < n_seg && !(STATE && seg == n_seg - 1);
+  if (!active) {
+    __syncthreads();
+    if (warp == 1) umma::tmem_dealloc(S.tmem_base, TM_COLS);
+    return;
+  }
+  const int c_begin = seg * a.seg_chunks, c_end = min(s.nch, c_begin + a.seg_chunks);
+  const int nit = c_end - c_begin;
+  const int64_t P0 = (s.p0 / kC + c_begin) * kC;  // the first chunk's first position
   const uint32_t tmem = S.tmem_base;
   static_assert(TM_O1 == TM_DS + kDK && TM_O2 == TM_O1 + kC && TM_S == TM_O2 + 2 * kC && TM_V == TM_S + kDK / 2 &&
                     TM_WH == TM_V + kC / 2 && TM_WL == TM_WH + kC / 2 && TM_WL + kC / 2 <= TM_COLS,
@@ -639,6 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           const auto ot = GDN_SV(&S.ot[0][0], kC * 128);
           const auto out = GDN_GV(reinterpret_cast<__nv_bfloat16*>(p.out), p.total * p.hv * DV);
+#pragma unroll 4
           for (int r = tlo + (lane >> 4); r < thi; r += 2)
             vec_at<uint4>(out, ((s.t0 + P - s.p0 + r) * p.hv) * DV + tile * 128 + 8 * (lane & 15)) =
                 vec_at<const uint4>(ot, r * 128 + 8 * (lane & 15));
@@ -800,6 +804,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0)
         for (; n < 2 && n < nit; ++n) load_xg(n);
       n = min(2, nit);
+      // the up to 3 rows just before the sequence, from the conv history
+      __nv_bfloat16 hrow[3][4];
+      if (P0 - 3 < s.p0) {
+        const int64_t row = (int64_t)p.hv * DV;
+        const auto hist = GDN_GV((const __nv_bfloat16*)a.vhist, (long long)p.n_seq * 3 * row) + (size_t)seq_n * 3 * row;
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) hrow[j][k] = hist[j * row + tile * 128 + 32 * k + lane];
+      }
       {
         // |V| <= |conv| <= max over the channels of sum |w| times the largest
         // raw input, plus the largest |bias|
@@ -832,15 +846,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&S.x_bar[i & 1], (i >> 1) & 1)))) break;
         const int64_t P = P0 + (int64_t)i * kC;
         if (P - 3 < s.p0) {
-          // the up to 3 rows just before the sequence come from the history
-          const int64_t lo = max(P - 3, s.p0 - 3), hi = min(P + kC, s.p0);
-          const int64_t row = (int64_t)p.hv * DV;
-          const auto hist = GDN_GV((const __nv_bfloat16*)a.vhist, (long long)p.n_seq * 3 * row) + (size_t)seq_n * 3 * row;
-          for (int64_t pos = lo; pos < hi; ++pos)
+          // history row j is position p0 - 3 + j, raw row r position P - 3 + r
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              S.raw[i & 1][GDN_S((int)(pos - (P - 3)), kRawRows)][32 * k + lane] =
-                  hist[(3 - (s.p0 - pos)) * row + tile * 128 + 32 * k + lane];
+          for (int j = 0; j < 3; ++j) {
+            const int64_t r = s.p0 - P + j;
+            if (r >= 0 && r < kRawRows)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) S.raw[i & 1][GDN_S((int)r, kRawRows)][32 * k + lane] = hrow[j][k];
+          }
           umma::fence_proxy_async();  // before a later chunk's copy into these rows
           __syncwarp();
         }
@@ -1230,7 +1243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   umma::fence_before();
   __syncthreads();
-  if (warp == 0) umma::tmem_dealloc(tmem, TM_COLS);
+  if (warp == 1) umma::tmem_dealloc(tmem, TM_COLS);
 }
 
 struct Layout {
