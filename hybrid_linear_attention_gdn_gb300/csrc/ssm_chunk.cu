@@ -86,7 +86,7 @@ struct ChunkArgs {
   float* seg_state;      // [segment slots][hv][dv][dk]
   float* seg_decay;      // [segment slots][hv]
   int32_t n_chunks, n_segs;  // slots
-  int32_t seg_chunks;
+  int32_t seg_chunks, feat_chunks;
   int32_t hist_blocks, hist_groups;  // the history work items: sequences x channel blocks
   pfx::PrefillArgs hist;
 };
@@ -160,18 +160,24 @@ __device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
 // ---------------------------------------------------------------------------
 // features of q and k, G = Q K^T
 // ---------------------------------------------------------------------------
-// One CTA per (chunk slot, group), 256 threads: a channel pair and half of
-// the chunk's tokens each.  HBM bound: 67 x 512 bytes in, 56 KB out.  q and k
-// stand one above the other as one 128-row operand, so that one product of
-// M = 128 gives G in its upper half.
+// A CTA of 256 threads walks feat_chunks consecutive chunk slots of one group;
+// a thread has a channel pair and half of the chunk's tokens.  HBM bound: 67 x
+// 512 bytes in, 56 KB out.  The next chunk's raw rows arrive by TMA while the
+// last ones' features, already in registers, are worked on.  q and k stand
+// one above the other as one 128-row operand, so that one product of M = 128
+// gives G in its upper half.
 constexpr int kFT = 256;
 struct __align__(1024) FeatSmem {
   uint8_t qk[2 * 128 * 128];  // [q; k] [token][dk], 64-column blocks of 16 KB
   uint8_t kt[2 * 128 * 128];  // kh, kl
   uint8_t g[kGBytes];
   __align__(16) int32_t meta[4];  // qe, ke
-  uint64_t bar;
-  uint32_t qkmax[2], tmem_base;
+  __align__(128) __nv_bfloat16 raw[2][kRawRows][128];  // q, k
+  Seq seq;        // of the chunk whose raw rows are in raw or on their way
+  int64_t chunk;  // its slot and its number in the sequence; slot -1: no more
+  int32_t c;
+  uint64_t raw_bar, bar;
+  uint32_t qkmax[2][2], tmem_base;  // by parity; q, k
 };
 
 __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
@@ -208,37 +214,64 @@ __device__ __forceinline__ void sequence_block(const ChunkArgs& a, const int n, 
     to[(int64_t)n * 3 * row + e] = vec_at<const uint4>(hist, e / row * p.C + 2 * p.hk * kDK + e % row * 8);
 }
 
-__global__ void __launch_bounds__(kFT, 2) ssm_features_kernel(const ChunkArgs a) {
+__global__ void __launch_bounds__(kFT, 2)
+    ssm_features_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap xmap) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   FeatSmem& S = *reinterpret_cast<FeatSmem*>(smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023));
   const PrefillArgs& p = a.p;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hq = blockIdx.y;
-  const int64_t cslot = blockIdx.x;
+  const int64_t slot0 = (int64_t)blockIdx.x * a.feat_chunks, slot1 = min(slot0 + a.feat_chunks, (int64_t)a.n_chunks);
   pdl_wait();
   pdl_trigger();
-  if (cslot >= a.n_chunks) {
-    sequence_block(a, (int)(cslot - a.n_chunks), hq);
+  if (slot0 >= a.n_chunks) {
+    sequence_block(a, (int)(blockIdx.x - (a.n_chunks + a.feat_chunks - 1) / a.feat_chunks), hq);
     return;
   }
-  const int n = find_seq(p, cslot, 1, false);
-  Seq s;
-  bool bad;
-  if (!load_seq(p, n, s, bad) || slot_class(s.slot, p.num_slots)) return;
-  const int64_t c = cslot - s.first;
-  if (c < 0 || c >= s.nch) return;
-  if (warp == 0) umma::tmem_alloc(&S.tmem_base, 64);
-  if (tid == 0) {
-    S.qkmax[0] = S.qkmax[1] = 0;
-    mbar_init(&S.bar, 1);
-    fence_mbar_init();
+  // warp 0: the next chunk in [from, slot1) that a usable sequence has, its
+  // raw rows on their way
+  auto next = [&](int64_t from) {
+    Seq s;
+    bool bad;
+    int64_t at = -1;
+    int c = 0;
+    for (int64_t k = from; k < slot1; ++k) {
+      const int n = find_seq(p, k, 1, false);
+      if (!load_seq(p, n, s, bad) || slot_class(s.slot, p.num_slots)) continue;
+      if (k - s.first < 0 || k - s.first >= s.nch) continue;
+      at = k;
+      c = (int)(k - s.first);
+      break;
+    }
+    if (lane == 0) {
+      S.seq = s;
+      S.chunk = at;
+      S.c = c;
+      if (at >= 0) {
+        const int32_t row0 = (int32_t)(s.t0 + ((s.p0 / kC + c) * kC - 3 - s.p0));  // may be < 0: zeros
+        mbar_arrive_expect_tx(&S.raw_bar, (uint32_t)sizeof(S.raw));
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          if (GDN_SPAN_G((hq + q * p.hk) * kDK, kDK, p.C) && GDN_SBYTES(&S.raw[q][0][0], sizeof(S.raw[0]), S))
+            tma_load_2d(&S.raw[q][0][0], &xmap, (hq + q * p.hk) * kDK, row0, &S.raw_bar);
+      }
+    }
+  };
+  if (warp == 1) umma::tmem_alloc(&S.tmem_base, 64);
+  if (warp == 0) {
+    if (lane == 0) {
+      mbar_init(&S.raw_bar, 1);
+      mbar_init(&S.bar, 1);
+      S.qkmax[0][0] = S.qkmax[0][1] = S.qkmax[1][0] = S.qkmax[1][1] = 0;
+      fence_mbar_init();
+    }
+    __syncwarp();
+    next(slot0);
   }
-  const int64_t P = (s.p0 / kC + c) * kC;  // the chunk's first position
   const int cp = tid & 63;                 // channel pair of the part
   const bool isq = (tid & 64) == 0;        // warps 0, 1, 4, 5
   const int half = tid >> 7;               // tokens 32 half ..
   const int ch = (isq ? hq : p.hk + hq) * kDK + 2 * cp;
-  const auto qkv = GDN_GV(reinterpret_cast<const __nv_bfloat16*>(p.qkv), p.total * p.C);
   const auto cw = GDN_GV(p.conv_w, (long long)p.C * 4);
   const float4 w0 = vec_at<const float4>(cw, (size_t)ch * 4), w1 = vec_at<const float4>(cw, (size_t)ch * 4 + 4);
   float2 bias = make_float2(0.f, 0.f);
@@ -246,144 +279,162 @@ __global__ void __launch_bounds__(kFT, 2) ssm_features_kernel(const ChunkArgs a)
     const auto cb = GDN_GV(p.conv_bias, p.C);
     bias = make_float2(cb[ch], cb[ch + 1]);
   }
-  // raw rows from 3 before the thread's first token: of the sequence, of the
-  // history (up to 3 before the sequence), zeros elsewhere
-  const int64_t m0 = P + 32 * half - s.p0;  // the first token's index in the sequence
-  const bool full = m0 >= 3 && m0 + 32 <= s.len;
-  __nv_bfloat162 xr[35];
-  if (full) {
-    const auto src = qkv + (s.t0 + m0 - 3) * p.C + ch;
-#pragma unroll
-    for (int r = 0; r < 35; ++r) xr[r] = vec_at<const __nv_bfloat162>(src, (size_t)r * p.C);
-  } else {
-    const auto hist = GDN_GV(reinterpret_cast<const __nv_bfloat16*>(p.conv), (long long)p.num_slots * 3 * p.C) +
-                      (size_t)s.slot * 3 * p.C;
-#pragma unroll
-    for (int r = 0; r < 35; ++r) {
-      const int64_t m = m0 - 3 + r;
-      xr[r] = __floats2bfloat162_rn(0.f, 0.f);
-      if (m >= 0 && m < s.len) xr[r] = vec_at<const __nv_bfloat162>(qkv, (s.t0 + m) * p.C + ch);
-      else if (m < 0 && m >= -3) xr[r] = vec_at<const __nv_bfloat162>(hist, (size_t)(3 + m) * p.C + ch);
-    }
-  }
-  float2 y[32];
-  float mx = 0.f;
-  {
-    const float2 v0 = make_float2(w0.x, w1.x), v1 = make_float2(w0.y, w1.y), v2 = make_float2(w0.z, w1.z),
-                 v3 = make_float2(w0.w, w1.w);
-    float2 x0 = __bfloat1622float2(xr[0]), x1 = __bfloat1622float2(xr[1]), x2 = __bfloat1622float2(xr[2]);
-#pragma unroll
-    for (int t = 0; t < 32; ++t) {
-      const float2 x3 = __bfloat1622float2(xr[t + 3]);
-      float2 acc = fma2(v0, x0, bias);
-      acc = fma2(v1, x1, acc);
-      acc = fma2(v2, x2, acc);
-      acc = fma2(v3, x3, acc);
-      y[t] = make_float2(silu_acc(acc.x), silu_acc(acc.y));
-      x0 = x1;
-      x1 = x2;
-      x2 = x3;
-    }
-  }
-  if (!full) {
-#pragma unroll
-    for (int t = 0; t < 32; ++t)
-      if (m0 + t < 0 || m0 + t >= s.len) y[t] = make_float2(0.f, 0.f);
-  }
-#pragma unroll
-  for (int t = 0; t < 32; ++t) {
-    const float u = fabsf(y[t].x), v = fabsf(y[t].y);  // the finite ones
-    mx = fmaxf(mx, fmaxf(u <= 3.4e38f ? u : 0.f, v <= 3.4e38f ? v : 0.f));
-  }
-  __syncthreads();  // S.qkmax cleared
-  {
-    const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
-    if (lane == 0) atomicMax(&S.qkmax[isq ? 0 : 1], m);
-  }
-  __syncthreads();
-  {
-    const float f = exp2_int(scale_exp(S.qkmax[isq ? 0 : 1]));
-    const int R0 = (isq ? 0 : kC) + 32 * half;
-#pragma unroll
-    for (int t = 0; t < 32; ++t) {
-      y[t] = mul2(y[t], make_float2(f, f));
-      tile_at<__half2>(S.qk, sizeof(S.qk), umma::sw128_off(R0 + t, 2 * cp, 128 * 128)) = __floats2half2_rn(y[t].x, y[t].y);
-    }
-  }
-  umma::fence_proxy_async();
   umma::fence_before();
-  __syncthreads();  // [q; k] written
+  __syncthreads();
   umma::fence_after();
   const uint32_t tmem = S.tmem_base;
-  const int qe = scale_exp(S.qkmax[0]), ke = scale_exp(S.qkmax[1]);
-  const int64_t ri = cslot * p.hk + hq;
-  Record& rec = a.rec[ri];
-  [[maybe_unused]] const bool rec_ok = GDN_SPAN_G(ri, 1, (long long)a.n_chunks * p.hk);
-  if (tid == 0) {
-    const uint64_t dq = umma::desc(smem_addr(S.qk), 16, 1024);
-    constexpr uint32_t ID = umma::idesc_f16(128, kC, false, false);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t ko = (k >> 2) * 16384 + (k & 3) * 32;
-      umma::mma_bf16(tmem, umma::adv(dq, ko), umma::adv(dq, ko + 8192), ID, k > 0);
-    }
-    umma::commit(&S.bar);
-    S.meta[0] = qe;
-    S.meta[1] = ke;
-  }
-  if (!isq) {
-#pragma unroll
-    for (int t8 = 0; t8 < 4; ++t8) {
-      uint32_t h0[4], l0[4], h1[4], l1[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 u = y[8 * t8 + 2 * i], v = y[8 * t8 + 2 * i + 1];
-        split2(make_float2(u.x, v.x), h0[i], l0[i]);
-        split2(make_float2(u.y, v.y), h1[i], l1[i]);
+  bool failed = false;
+  uint32_t par = 0;
+#pragma unroll 1
+  for (int it = 0;; ++it) {
+    const int64_t cslot = S.chunk;
+    if (cslot < 0) break;
+    par = it & 1;
+    // the first token of this thread in the sequence's tokens (may be < 0), and their number
+    const int64_t m0 = (S.seq.p0 / kC + S.c) * kC + 32 * half - S.seq.p0;
+    const int tlo = (int)max((int64_t)-64, -m0), thi = (int)min((int64_t)64, S.seq.len - m0);  // valid: [tlo, thi)
+    const bool late = !mbar_wait(&S.raw_bar, par);
+    const int64_t c0 = m0 - 32 * half;  // the chunk's first token
+    if (c0 < 3) {
+      // up to 3 rows before the sequence, from the history
+      const auto hist = GDN_GV(reinterpret_cast<const __nv_bfloat16*>(p.conv), (long long)p.num_slots * 3 * p.C) +
+                        (size_t)S.seq.slot * 3 * p.C;
+      for (int e = tid; e < 2 * 3 * 128; e += kFT) {
+        const int q = e / (3 * 128), j = e / 128 % 3, cc = e % 128;  // history row j: token j - 3
+        const int64_t r = j - c0;
+        if (r >= 0 && r < kRawRows)
+          S.raw[q][GDN_S((int)r, kRawRows)][cc] = hist[(size_t)j * p.C + (hq + q * p.hk) * kDK + cc];
       }
-      const uint32_t o0 = umma::sw128_off(2 * cp, 32 * half + 8 * t8, 0),
-                     o1 = umma::sw128_off(2 * cp + 1, 32 * half + 8 * t8, 0);
-      tile_at<uint4>(S.kt, sizeof(S.kt), o0) = make_uint4(h0[0], h0[1], h0[2], h0[3]);
-      tile_at<uint4>(S.kt, sizeof(S.kt), o0 + 16384) = make_uint4(l0[0], l0[1], l0[2], l0[3]);
-      tile_at<uint4>(S.kt, sizeof(S.kt), o1) = make_uint4(h1[0], h1[1], h1[2], h1[3]);
-      tile_at<uint4>(S.kt, sizeof(S.kt), o1 + 16384) = make_uint4(l1[0], l1[1], l1[2], l1[3]);
+      umma::fence_proxy_async();  // before the next chunk's copy into these rows
     }
-  }
-  const bool late = !mbar_wait(&S.bar, 0);
-  if (__syncthreads_or(late)) {
-    if (tid == 0) {
-      report(p.err, GDN_DEV_ERR_TIMEOUT);
-      mbar_wait(&S.bar, 0);
+    if ((failed = __syncthreads_or(late))) break;
+    float2 y[32];
+    float mx = 0.f;
+    {
+      const auto src = GDN_SV(reinterpret_cast<const __nv_bfloat162*>(&S.raw[isq ? 0 : 1][0][0]), kRawRows * 64) +
+                       (32 * half * 64 + cp);
+      const float2 v0 = make_float2(w0.x, w1.x), v1 = make_float2(w0.y, w1.y), v2 = make_float2(w0.z, w1.z),
+                   v3 = make_float2(w0.w, w1.w);
+      float2 x0 = __bfloat1622float2(src[0]), x1 = __bfloat1622float2(src[64]), x2 = __bfloat1622float2(src[128]);
+#pragma unroll
+      for (int t = 0; t < 32; ++t) {
+        const float2 x3 = __bfloat1622float2(src[(t + 3) * 64]);
+        float2 acc = fma2(v0, x0, bias);
+        acc = fma2(v1, x1, acc);
+        acc = fma2(v2, x2, acc);
+        acc = fma2(v3, x3, acc);
+        y[t] = make_float2(silu_acc(acc.x), silu_acc(acc.y));
+        x0 = x1;
+        x1 = x2;
+        x2 = x3;
+      }
     }
-  } else if (isq) {
+    if (tlo > 0 || thi < 32) {
+#pragma unroll
+      for (int t = 0; t < 32; ++t)
+        if (t < tlo || t >= thi) y[t] = make_float2(0.f, 0.f);
+    }
+#pragma unroll
+    for (int t = 0; t < 32; ++t) {
+      const float u = fabsf(y[t].x), v = fabsf(y[t].y);  // the finite ones
+      mx = fmaxf(mx, fmaxf(u <= 3.4e38f ? u : 0.f, v <= 3.4e38f ? v : 0.f));
+    }
+    {
+      const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
+      if (lane == 0) atomicMax(&S.qkmax[par][isq ? 0 : 1], m);
+    }
+    if (tid == 0) bulk_wait_read();  // the last chunk's record has left
+    __syncthreads();  // the maxima complete, the raw rows read, the tiles free
+    const int qe = scale_exp(S.qkmax[par][0]), ke = scale_exp(S.qkmax[par][1]);
+    if (tid == 0) S.qkmax[par ^ 1][0] = S.qkmax[par ^ 1][1] = 0;
+    {
+      const float f = exp2_int(isq ? qe : ke);
+      const int R0 = (isq ? 0 : kC) + 32 * half;
+#pragma unroll
+      for (int t = 0; t < 32; ++t) {
+        y[t] = mul2(y[t], make_float2(f, f));
+        tile_at<__half2>(S.qk, sizeof(S.qk), umma::sw128_off(R0 + t, 2 * cp, 128 * 128)) = __floats2half2_rn(y[t].x, y[t].y);
+      }
+    }
+    umma::fence_proxy_async();
+    umma::fence_before();
+    __syncthreads();  // [q; k] written
     umma::fence_after();
-    const int i = 32 * (warp & 3) + lane;
-    float v[32];
-    umma::tmem_ld32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 32 * half, v);
-    // |v| <= 128 2^15 2^15: times 2^-22 it fits fp16
+    const int64_t ri = cslot * p.hk + hq;
+    Record& rec = a.rec[ri];
+    [[maybe_unused]] const bool rec_ok = GDN_SPAN_G(ri, 1, (long long)a.n_chunks * p.hk);
+    if (tid == 0) {
+      const uint64_t dq = umma::desc(smem_addr(S.qk), 16, 1024);
+      constexpr uint32_t ID = umma::idesc_f16(128, kC, false, false);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t h[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const __half2 x = __floats2half2_rn(v[8 * q + 2 * e] * 0x1p-22f, v[8 * q + 2 * e + 1] * 0x1p-22f);
-        h[e] = *reinterpret_cast<const uint32_t*>(&x);
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t ko = (k >> 2) * 16384 + (k & 3) * 32;
+        umma::mma_bf16(tmem, umma::adv(dq, ko), umma::adv(dq, ko + 8192), ID, k > 0);
       }
-      tile_at<uint4>(S.g, sizeof(S.g), umma::sw128_off(i, 32 * half + 8 * q, 0)) = make_uint4(h[0], h[1], h[2], h[3]);
+      umma::commit(&S.bar);
+      S.meta[0] = qe;
+      S.meta[1] = ke;
+    }
+    __syncwarp();
+    if (warp == 0) next(cslot + 1);
+    if (!isq) {
+#pragma unroll
+      for (int t8 = 0; t8 < 4; ++t8) {
+        uint32_t h0[4], l0[4], h1[4], l1[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 u = y[8 * t8 + 2 * i], v = y[8 * t8 + 2 * i + 1];
+          split2(make_float2(u.x, v.x), h0[i], l0[i]);
+          split2(make_float2(u.y, v.y), h1[i], l1[i]);
+        }
+        const uint32_t o0 = umma::sw128_off(2 * cp, 32 * half + 8 * t8, 0),
+                       o1 = umma::sw128_off(2 * cp + 1, 32 * half + 8 * t8, 0);
+        tile_at<uint4>(S.kt, sizeof(S.kt), o0) = make_uint4(h0[0], h0[1], h0[2], h0[3]);
+        tile_at<uint4>(S.kt, sizeof(S.kt), o0 + 16384) = make_uint4(l0[0], l0[1], l0[2], l0[3]);
+        tile_at<uint4>(S.kt, sizeof(S.kt), o1) = make_uint4(h1[0], h1[1], h1[2], h1[3]);
+        tile_at<uint4>(S.kt, sizeof(S.kt), o1 + 16384) = make_uint4(l1[0], l1[1], l1[2], l1[3]);
+      }
+    }
+    if ((failed = __syncthreads_or(!mbar_wait(&S.bar, par)))) break;
+    if (isq) {
+      umma::fence_after();
+      const int i = 32 * (warp & 3) + lane;
+      float v[32];
+      umma::tmem_ld32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 32 * half, v);
+      // |v| <= 128 2^15 2^15: times 2^-22 it fits fp16
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __half2 x = __floats2half2_rn(v[8 * q + 2 * e] * 0x1p-22f, v[8 * q + 2 * e + 1] * 0x1p-22f);
+          h[e] = *reinterpret_cast<const uint32_t*>(&x);
+        }
+        tile_at<uint4>(S.g, sizeof(S.g), umma::sw128_off(i, 32 * half + 8 * q, 0)) = make_uint4(h[0], h[1], h[2], h[3]);
+      }
+    }
+    umma::fence_proxy_async();
+    umma::fence_before();
+    __syncthreads();
+    if (tid == 0 && rec_ok) {
+      bulk_s2g(rec.q, S.qk, 8192);
+      bulk_s2g(rec.q + 8192, S.qk + 16384, 8192);
+      bulk_s2g(rec.kh, S.kt, 32768);  // and kl
+      bulk_s2g(rec.g, S.g, kGMBytes);  // and qe, ke
+      bulk_commit();
     }
   }
-  umma::fence_proxy_async();
+  if (failed && tid == 0) {
+    // let what is in flight land before the memory goes
+    report(p.err, GDN_DEV_ERR_TIMEOUT);
+    mbar_wait(&S.raw_bar, par);
+    mbar_wait(&S.raw_bar, par ^ 1);
+    mbar_wait(&S.bar, par);
+  }
+  if (tid == 0) bulk_wait_all();
   umma::fence_before();
   __syncthreads();
-  if (tid == 0 && rec_ok) {
-    bulk_s2g(rec.q, S.qk, 8192);
-    bulk_s2g(rec.q + 8192, S.qk + 16384, 8192);
-    bulk_s2g(rec.kh, S.kt, 32768);  // and kl
-    bulk_s2g(rec.g, S.g, kGMBytes);  // and qe, ke
-    bulk_commit();
-    bulk_wait_all();
-  }
-  if (warp == 0) umma::tmem_dealloc(tmem, 64);
+  if (warp == 1) umma::tmem_dealloc(tmem, 64);
 }
 static_assert(offsetof(FeatSmem, meta) == offsetof(FeatSmem, g) + kGBytes && offsetof(Record, qe) == offsetof(Record, g) + kGBytes,
               "G and its exponents leave and arrive as one piece");
@@ -1340,6 +1391,9 @@ cudaError_t ssm_chunk_launch(const ssm::PrefillArgs& p, const gdn_dims& d, void*
   a.n_chunks = (int32_t)l.n_chunks;
   a.n_segs = (int32_t)l.n_segs;
   a.seg_chunks = l.seg_chunks;
+  // the features' walks: one wave of two CTAs per SM, so that all but a
+  // walk's first chunk find their raw rows waiting
+  a.feat_chunks = (int32_t)((l.n_chunks * p.hk + 2 * sm_count() - 1) / (2 * sm_count()));
   a.hist_blocks = (int32_t)hist_blocks(p.C);
   a.hist_groups = p.max_ckpt > pfx::kCkGroup ? (p.max_ckpt + pfx::kCkGroup - 1) / pfx::kCkGroup : 1;
   pfx::PrefillArgs& h = a.hist;
@@ -1377,8 +1431,9 @@ cudaError_t ssm_chunk_launch(const ssm::PrefillArgs& p, const gdn_dims& d, void*
   if ((e = cudaFuncSetAttribute(ssm_features_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
       cudaSuccess)
     return e;
-  if ((e = launch_pdl(ssm_features_kernel, dim3((unsigned)(l.n_chunks + p.n_seq), (unsigned)p.hk), dim3(kFT), smem, s,
-                      dim3(1), a)) != cudaSuccess)
+  const unsigned walks = (unsigned)((l.n_chunks + a.feat_chunks - 1) / a.feat_chunks);
+  if ((e = launch_pdl(ssm_features_kernel, dim3(walks + (unsigned)p.n_seq, (unsigned)p.hk), dim3(kFT), smem, s, dim3(1),
+                      a, xmap)) != cudaSuccess)
     return e;
   return p.dv == 64 ? launch_chain<2>(a, l, xmap, omap, s) : launch_chain<1>(a, l, xmap, omap, s);
 }
