@@ -442,24 +442,27 @@ static_assert(offsetof(FeatSmem, meta) == offsetof(FeatSmem, g) + kGBytes && off
 // ---------------------------------------------------------------------------
 // the chain
 // ---------------------------------------------------------------------------
-// Twenty warps, with no barrier among them after the start, only mbarriers:
-//   0..15    compute: while the tensor core runs chunk i's products, V (kept
-//            in registers) and P (the other of two buffers) of chunk i + 1;
-//            then chunk i's results out of TMEM, the state, and chunk i + 1's
-//            operands in their place
-//   16       issuer: every product and the copies of q and k (a thread that
-//            issues products is held up about as long as they run), and the
-//            output stores
-//   17, 18   gates and scales of one head each
-//   19       loader: the copies of raw V rows and G, the three rows before a
+// Twenty-four warps, with no barrier among them after the start, only
+// mbarriers:
+//   0..15    compute: while the tensor core runs chunk i's products, V of chunk
+//            i + 1 (kept in registers); then the state, chunk i + 1's operands
+//            in place of chunk i's, and chunk i's output to its rows
+//   16..19   P of chunk i + 1, the other of two buffers
+//   20       issuer: every product and the copies of q and k (a thread that
+//            issues products is held up about as long as they run)
+//   21, 22   gates and scales of one head each
+//   23       loader: the copies of raw V rows and G, the three rows before a
 //            sequence from the conv history, and the largest raw input
-// The last four give their registers to the compute warps.
-constexpr int kCompute = 512;
-constexpr int kThreads = kCompute + 128;
-// Registers per thread after the split of the launch's 640 x 96: the compute
-// warps' state, V and temporaries against the issuer's few.
-constexpr int kComputeRegs = 104, kIssuerRegs = 64;
-static_assert(kCompute * kComputeRegs + 128 * kIssuerRegs <= kThreads * 96, "no more than the launch's registers");
+// What bounds a chunk is the one-after-the-other of a compute warp's steps,
+// not the products: leaving out half of dS^T's changed nothing.
+constexpr int kCompute = 512, kAux = 128;  // threads
+constexpr int kIssuer = (kCompute + kAux) / 32, kLoader = kIssuer + 3;
+constexpr int kThreads = 32 * (kLoader + 1);
+// Registers per thread after the split of the launch's 768 x 80.  Spills cost
+// more here than elsewhere: shared memory leaves little of the L1 cache.
+constexpr int kComputeRegs = 96, kAuxRegs = 48, kHelpRegs = 48;
+static_assert(kCompute * kComputeRegs + kAux * kAuxRegs + 128 * kHelpRegs <= kThreads * 80,
+              "no more than the launch's registers");
 
 // TMEM columns (fp16 operands hold two values per column)
 constexpr uint32_t TM_DS = 0;    // dS^T [dv rows][dk]
@@ -484,6 +487,17 @@ struct __align__(16) Scales {
   float skip;   // D 2^pe
 };
 
+// What a CTA walks: kept in shared memory, so that no role holds what another
+// needs in registers.  Tokens are counted from the sequence's first.
+struct Chain {
+  int64_t rec0, seg0;  // record of the first chunk (and the tile's group); the sequence's first segment slot
+  int32_t nit;         // chunks; 0: nothing to do
+  int32_t m0;          // the first chunk's first token (-63 .. in a first segment)
+  int32_t len, t0;     // tokens of the sequence; its first packed row
+  int32_t n, slot, seg, n_seg;
+  int32_t to_ckpt, ck_idx;  // chunks before the one that ends at the next block boundary; that boundary's index
+};
+
 template <int NH>
 struct __align__(1024) ChainSmem {
   uint8_t qk[2][kQKBytes];         // q, kh, kl
@@ -493,7 +507,6 @@ struct __align__(1024) ChainSmem {
     int32_t meta[4];               // qe, ke
   } g[2];
   __nv_bfloat16 raw[2][kRawRows][128];
-  __align__(128) __nv_bfloat16 ot[kC][128];
   // per chunk (mod 4) and head
   __align__(16) float b2[4][NH][kC];  // b log2(e)
   float eb[4][NH][kC];                // e^b
@@ -510,10 +523,9 @@ struct __align__(1024) ChainSmem {
   uint64_t used[2];                   // raw rows and G read
   uint64_t ready;                     // operands in place
   uint64_t ds_bar, o_bar;             // dS^T done; all products done
-  uint64_t o_full, o_free;            // output staged; staging read
   uint64_t s_used;                    // the state's way through S.qk is free
   uint32_t tmem_base;
-  int seq;
+  Chain ch;
 };
 
 // 8 or 16 consecutive columns of this thread's TMEM lane, written; done after
@@ -585,9 +597,9 @@ __device__ __forceinline__ void mma_f16_ta(uint32_t tmem_d, uint32_t tmem_a, uin
 // STATE: the segment's state alone (every segment but a sequence's last).
 template <int NH, bool STATE>
 __global__ void __launch_bounds__(kThreads, 1)
-    ssm_chain_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap xmap,
-                     const __grid_constant__ CUtensorMap omap) {
+    ssm_chain_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap xmap) {
   constexpr int DV = 128 / NH;
+  constexpr int kPart = (kCompute + (STATE ? 0 : kAux)) / 32;  // warps that take part in a chunk
   using SM = ChainSmem<NH>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   SM& S = *reinterpret_cast<SM*>(smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023));
@@ -607,8 +619,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   if (warp == 0) {
-    const int f = find_seq(p, blockIdx.y, a.seg_chunks, true);
-    if (lane == 0) S.seq = f;
+    // inconsistent, empty and padded sequences are the features kernel's
+    const int n = find_seq(p, blockIdx.y, a.seg_chunks, true);
+    Seq s;
+    bool bad;
+    Chain c = {};
+    if (load_seq(p, n, s, bad) && !slot_class(s.slot, p.num_slots)) {
+      c.seg0 = s.first / a.seg_chunks + n;
+      c.seg = (int)(blockIdx.y - c.seg0);
+      c.n_seg = (s.nch + a.seg_chunks - 1) / a.seg_chunks;
+      if (c.seg >= 0 && c.seg < c.n_seg && !(STATE && c.seg == c.n_seg - 1)) {
+        const int first = c.seg * a.seg_chunks;  // chunk of the sequence
+        const int64_t P = s.p0 / kC + first;     // and absolute
+        const int kpc = p.ckpt_block / kC;
+        c.nit = min(s.nch - first, a.seg_chunks);
+        c.rec0 = (s.first + first) * p.hk + hq;
+        c.m0 = first * kC - (int)(s.p0 % kC);
+        c.len = (int)s.len;
+        c.t0 = (int)s.t0;
+        c.n = n;
+        c.slot = s.slot;
+        c.to_ckpt = kpc - 1 - (int)(P % kpc);
+        c.ck_idx = (int)min((int64_t)p.max_ckpt, P / kpc - s.p0 / p.ckpt_block);
+      }
+    }
+    if (lane == 0) S.ch = c;
   } else if (warp == 1) {
     umma::tmem_alloc(&S.tmem_base, TM_COLS);
   } else if (tid == 64) {
@@ -619,13 +654,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.qk_bar[i], 1);
       mbar_init(&S.hx[i], 1);
       mbar_init(&S.gx[i], NH);
-      mbar_init(&S.used[i], kCompute / 32);
+      mbar_init(&S.used[i], kPart);
     }
-    mbar_init(&S.ready, kCompute / 32);
+    mbar_init(&S.ready, kPart);
     mbar_init(&S.ds_bar, 1);
     mbar_init(&S.o_bar, 1);
-    mbar_init(&S.o_full, kCompute / 32);
-    mbar_init(&S.o_free, 1);
     mbar_init(&S.s_used, kCompute / 32);
 #pragma unroll
     for (int i = 0; i < NH; ++i) S.smax[i] = 0;
@@ -634,74 +667,38 @@ __global__ void __launch_bounds__(kThreads, 1)
   umma::fence_before();
   __syncthreads();
   umma::fence_after();
-  const int n = S.seq, seq_n = n;
-  Seq s;
-  bool bad_seq;
-  // inconsistent, empty and padded sequences are the features kernel's
-  bool active = load_seq(p, n, s, bad_seq) && !slot_class(s.slot, p.num_slots);
-  const int64_t seg_first = active ? s.first / a.seg_chunks + n : 0;
-  const int seg = (int)(blockIdx.y - seg_first);
-  const int n_seg = active ? (s.nch + a.seg_chunks - 1) / a.seg_chunks : 0;
-  active = active && seg >= 0 && seg < n_seg && !(STATE && seg == n_seg - 1);
-  if (!active) {
-    __syncthreads();
+  const int nit = S.ch.nit;
+  if (nit == 0) {
     if (warp == 1) umma::tmem_dealloc(S.tmem_base, TM_COLS);
     return;
   }
-  const int c_begin = seg * a.seg_chunks, c_end = min(s.nch, c_begin + a.seg_chunks);
-  const int nit = c_end - c_begin;
-  const int64_t P0 = (s.p0 / kC + c_begin) * kC;  // the first chunk's first position
   const uint32_t tmem = S.tmem_base;
   static_assert(TM_O1 == TM_DS + kDK && TM_O2 == TM_O1 + kC && TM_S == TM_O2 + 2 * kC && TM_V == TM_S + kDK / 2 &&
                     TM_WH == TM_V + kC / 2 && TM_WL == TM_WH + kC / 2 && TM_WL + kC / 2 <= TM_COLS,
                 "TMEM regions");
 
-  const int64_t rec0 = (s.first + c_begin) * p.hk + hq;
   auto bulk = [&](void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
     mbar_arrive_expect_tx(bar, bytes);
     if (GDN_GBYTES(src, bytes, a.rec, (long long)a.n_chunks * p.hk * sizeof(Record)) && GDN_SBYTES(dst, bytes, S))
       bulk_g2s(dst, src, bytes, bar);
   };
-  if (warp >= kCompute / 32) {
+  if (warp >= kIssuer) {
     // ------------------------------------------------------------------ issuer
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kIssuerRegs));
-    if (warp == kCompute / 32) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kHelpRegs));
+    if (warp == kIssuer) {
       constexpr uint32_t ID_O1 = umma::idesc_f16(128, kC, false, false);
       constexpr uint32_t ID_O2 = umma::idesc_f16(128, NH * kC, false, false);
       constexpr uint32_t ID_S = umma::idesc_f16(128, kDK, false, false);
       // q and k (the state alone needs only k)
       constexpr uint32_t kSkip = STATE ? sizeof(Record::q) : 0;
       auto load_qk = [&](int i) {
-        bulk(S.qk[i & 1] + kSkip, a.rec[rec0 + (int64_t)i * p.hk].q + kSkip, kQKBytes - kSkip, &S.qk_bar[i & 1]);
+        bulk(S.qk[i & 1] + kSkip, a.rec[S.ch.rec0 + (int64_t)i * p.hk].q + kSkip, kQKBytes - kSkip, &S.qk_bar[i & 1]);
       };
       int n_qk = 0, n_mma = 0;  // issued
       bool ok = __all_sync(0xffffffffu, mbar_wait(&S.s_used, 0));
       if (ok && lane == 0) {
         for (; n_qk < 2 && n_qk < nit; ++n_qk) load_qk(n_qk);
       }
-      // chunk i's staged output, the whole warp
-      auto store = [&](int i) -> bool {
-        if (!__all_sync(0xffffffffu, mbar_wait(&S.o_full, i & 1))) return false;
-        const int64_t P = P0 + (int64_t)i * kC;
-        const int tlo = (int)max((int64_t)0, s.p0 - P), thi = (int)min((int64_t)kC, s.p1 - P);
-        if (tlo == 0 && thi == kC) {
-          if (lane == 0 && GDN_SPAN_G(s.t0 + (P - s.p0), kC, p.total)) {
-            tma_store_2d(&omap, &S.ot[0][0], tile * 128, (int32_t)(s.t0 + (P - s.p0)));
-            bulk_commit();
-            bulk_wait_read();
-          }
-        } else {
-          const auto ot = GDN_SV(&S.ot[0][0], kC * 128);
-          const auto out = GDN_GV(reinterpret_cast<__nv_bfloat16*>(p.out), p.total * p.hv * DV);
-#pragma unroll 4
-          for (int r = tlo + (lane >> 4); r < thi; r += 2)
-            vec_at<uint4>(out, ((s.t0 + P - s.p0 + r) * p.hv) * DV + tile * 128 + 8 * (lane & 15)) =
-                vec_at<const uint4>(ot, r * 128 + 8 * (lane & 15));
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.o_free);
-        return true;
-      };
       // pass i: chunk i's operands are in place
       for (int i = 0; i < nit && ok; ++i) {
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&S.ready, i & 1)))) break;
@@ -735,31 +732,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++n_mma;
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!STATE && ok && i > 0) ok = store(i - 1);
         if (lane == 0 && ok && (ok = mbar_wait(&S.o_bar, i & 1)) && i + 2 < nit) {
           load_qk(i + 2);
           n_qk = i + 3;
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
       }
-      if (!STATE && ok) ok = store(nit - 1);
       if (lane == 0) {
         if (!ok) report(p.err, GDN_DEV_ERR_TIMEOUT);
         // what is in flight lands before the memory goes (at once, unless a wait expired)
         for (int k = max(0, n_qk - 2); k < n_qk; ++k) mbar_wait(&S.qk_bar[k & 1], (k >> 1) & 1);
         if (n_mma) mbar_wait(&S.o_bar, (n_mma - 1) & 1);
-        bulk_wait_all();
       }
-    } else if (warp <= kCompute / 32 + NH) {
+    } else if (warp <= kIssuer + NH) {
       // ----------------------------------------------------------------- gates
       // two tokens per lane, their logits loaded one chunk ahead
-      const int hh = warp - kCompute / 32 - 1, gh = h0 + hh;
+      const int hh = warp - kIssuer - 1, gh = h0 + hh;
       const auto gate_a = GDN_GV(reinterpret_cast<const __nv_bfloat16*>(p.a), p.total * p.hv);
+      const int m0 = S.ch.m0, len = S.ch.len;
       auto gate_load = [&](int i, float (&ga)[2]) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int64_t m = P0 + (int64_t)i * kC + 32 * e + lane - s.p0;
-          ga[e] = i < nit && m >= 0 && m < s.len ? __bfloat162float(gate_a[(s.t0 + m) * p.hv + gh]) : 0.f;
+          const int m = m0 + i * kC + 32 * e + lane;
+          ga[e] = i < nit && (unsigned)m < (unsigned)len
+                      ? __bfloat162float(gate_a[(long long)(S.ch.t0 + m) * p.hv + gh])
+                      : 0.f;
         }
       };
       const float A_log = GDN_GV(p.A_log, p.hv)[gh], dtb = GDN_GV(p.dt_bias, p.hv)[gh];
@@ -771,8 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float dt[2], b[2], suf[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int64_t m = P0 + (int64_t)i * kC + 32 * e + lane - s.p0;
-          const bool in = m >= 0 && m < s.len;
+          const bool in = (unsigned)(m0 + i * kC + 32 * e + lane) < (unsigned)len;
           const Gate t = gate(A_log, dtb, ga[e]);
           dt[e] = in ? t.dt : 0.f;
           b[e] = suf[e] = in ? floor_log_decay(t.g) : 0.f;
@@ -842,14 +838,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&S.gx[i & 1]);
       }
       if (!ok && lane == 0) report(p.err, GDN_DEV_ERR_TIMEOUT);
-    } else if (warp == kThreads / 32 - 1) {
+    } else if (warp == kLoader) {
       // ---------------------------------------------------------------- loader
       auto load_xg = [&](int i) {
-        const int32_t row0 = (int32_t)(s.t0 + (P0 + (int64_t)i * kC - 3 - s.p0));  // may be < 0: zeros
+        const int32_t row0 = S.ch.t0 + S.ch.m0 + i * kC - 3;  // may be < 0: zeros
         mbar_arrive_expect_tx(&S.x_bar[i & 1], (uint32_t)sizeof(S.raw[0]));
         if (GDN_SPAN_G(2 * p.hk * kDK + tile * 128, 128, p.C) && GDN_SBYTES(&S.raw[i & 1][0][0], sizeof(S.raw[0]), S))
           tma_load_2d(&S.raw[i & 1][0][0], &xmap, 2 * p.hk * kDK + tile * 128, row0, &S.x_bar[i & 1]);
-        bulk(&S.g[i & 1], a.rec[rec0 + (int64_t)i * p.hk].g, kGMBytes, &S.g_bar[i & 1]);
+        bulk(&S.g[i & 1], a.rec[S.ch.rec0 + (int64_t)i * p.hk].g, kGMBytes, &S.g_bar[i & 1]);
       };
       int n = 0;  // issued
       if (lane == 0)
@@ -857,9 +853,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       n = min(2, nit);
       // the up to 3 rows just before the sequence, from the conv history
       __nv_bfloat16 hrow[3][4];
-      if (P0 - 3 < s.p0) {
+      if (S.ch.m0 < 3) {
         const int64_t row = (int64_t)p.hv * DV;
-        const auto hist = GDN_GV((const __nv_bfloat16*)a.vhist, (long long)p.n_seq * 3 * row) + (size_t)seq_n * 3 * row;
+        const auto hist = GDN_GV((const __nv_bfloat16*)a.vhist, (long long)p.n_seq * 3 * row) + (size_t)S.ch.n * 3 * row;
 #pragma unroll
         for (int j = 0; j < 3; ++j)
 #pragma unroll
@@ -895,15 +891,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           n = i + 1;
         }
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&S.x_bar[i & 1], (i >> 1) & 1)))) break;
-        const int64_t P = P0 + (int64_t)i * kC;
-        if (P - 3 < s.p0) {
-          // history row j is position p0 - 3 + j, raw row r position P - 3 + r
+        const int m0 = S.ch.m0 + i * kC;
+        if (m0 < 3) {
+          // history row j is token j - 3, raw row r token m - 3 + r
 #pragma unroll
           for (int j = 0; j < 3; ++j) {
-            const int64_t r = s.p0 - P + j;
+            const int r = j - m0;
             if (r >= 0 && r < kRawRows)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) S.raw[i & 1][GDN_S((int)r, kRawRows)][32 * k + lane] = hrow[j][k];
+              for (int k = 0; k < 4; ++k) S.raw[i & 1][GDN_S(r, kRawRows)][32 * k + lane] = hrow[j][k];
           }
           umma::fence_proxy_async();  // before a later chunk's copy into these rows
           __syncwarp();
@@ -947,6 +943,94 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+  } else if (warp >= kCompute / 32) {
+    // --------------------------------------------------------------------- aux
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kAuxRegs));
+    if constexpr (!STATE) {
+      // thread: row pr of the heads' 64 NH, in every 16-token block the PC
+      // columns from pc0; what lies above the diagonal stays zero
+      const int row = tid - kCompute;
+      constexpr int PC = 8 * NH;
+      const int pr = NH == 2 ? row : (row & 63), pi = pr & 63, ph = pr >> 6;
+      const int pc0 = NH == 2 ? 0 : 8 * (row >> 6);
+      const int wlo = pi & 32;  // the warp's rows: wlo .. wlo + 31 of a head
+#pragma unroll
+      for (int k = 0; k < 4 * PC / 8; ++k) {
+        const uint32_t at = umma::sw128_off(pr, 16 * (k % 4) + pc0 + 8 * (k / 4), 0);
+        tile_at<uint4>(S.pt[0], sizeof(S.pt[0]), at) = make_uint4(0u, 0u, 0u, 0u);
+        tile_at<uint4>(S.pt[1], sizeof(S.pt[1]), at) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      // P of the segment's chunk i; false if a wait expired
+      auto put_p = [&](int i) -> bool {
+        const uint32_t par = (i >> 1) & 1;
+        if (!mbar_wait(&S.gx[i & 1], par) || !mbar_wait(&S.g_bar[i & 1], par)) return false;
+        const int buf = i & 3;
+#pragma unroll 1
+        for (int J = 0; 16 * J < wlo + 32; ++J) {
+          const int pc = 16 * J + pc0;
+          // P_ij = G_ij u_i v_j: both factors taken at the end b' of j's
+          // 16-token block, u_i = e^{b_i - b'} at most 1 below the diagonal
+          // blocks; on them it is large where the block decays, and beyond
+          // 2^80 the differences are taken one by one
+          const float bi = S.b2[buf][ph][pi], be = S.b2[buf][ph][GDN_S(pc | 15, kC)];
+          const float pscale = S.sc[buf][ph].p;
+          const float u = ex2(bi - be) * pscale;
+          float2 e[PC / 2];
+#pragma unroll
+          for (int c8 = 0; c8 < PC / 8; ++c8) {
+            const uint4 g4 = tile_at<uint4>(S.g[i & 1].g, kGBytes, umma::sw128_off(pi, pc + 8 * c8, 0));
+            const float4 va = *reinterpret_cast<const float4*>(&S.v[buf][ph][GDN_S(pc + 8 * c8, kC - 7)]);
+            const float4 vb = *reinterpret_cast<const float4*>(&S.v[buf][ph][pc + 8 * c8 + 4]);
+            const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w};
+            const float2 vv[4] = {lo2(va), hi2(va), lo2(vb), hi2(vb)};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              e[4 * c8 + k] = mul2(__half22float2(*reinterpret_cast<const __half2*>(&gw[k])),
+                                   mul2(vv[k], make_float2(u, u)));
+          }
+          if (16 * J >= wlo) {  // the warp holds a diagonal block
+            const float sk = S.sc[buf][ph].skip;
+            if (__any_sync(0xffffffffu, S.b2[buf][ph][pc & ~15] - be > 80.f)) {
+#pragma unroll 1
+              for (int k = 0; k < PC; ++k) {
+                const int j = pc + k;
+                const float g = __half2float(tile_at<__half>(S.g[i & 1].g, kGBytes, umma::sw128_off(pi, j, 0)));
+                const float x = j > pi ? 0.f : g * (ex2(bi - S.b2[buf][ph][GDN_S(j, kC)]) * S.dt[buf][ph][j] * pscale);
+#pragma unroll
+                for (int q = 0; q < PC / 2; ++q) {
+                  if (2 * q == k) e[q].x = x;
+                  if (2 * q + 1 == k) e[q].y = x;
+                }
+              }
+            }
+            const int dj = pi - pc;  // the diagonal's column
+#pragma unroll
+            for (int k = 0; k < PC / 2; ++k) {
+              e[k].x = 2 * k < dj ? e[k].x : 2 * k == dj ? e[k].x + sk : 0.f;
+              e[k].y = 2 * k + 1 < dj ? e[k].y : 2 * k + 1 == dj ? e[k].y + sk : 0.f;
+            }
+          }
+#pragma unroll
+          for (int c8 = 0; c8 < PC / 8; ++c8)
+            tile_at<uint4>(S.pt[i & 1], sizeof(S.pt[0]), umma::sw128_off(pr, pc + 8 * c8, 0)) =
+                make_uint4(half2_bits(e[4 * c8].x, e[4 * c8].y), half2_bits(e[4 * c8 + 1].x, e[4 * c8 + 1].y),
+                           half2_bits(e[4 * c8 + 2].x, e[4 * c8 + 2].y), half2_bits(e[4 * c8 + 3].x, e[4 * c8 + 3].y));
+        }
+        umma::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.used[i & 1]);
+        return true;
+      };
+      bool ok = true;
+#pragma unroll 1
+      for (int i = 0; i < nit; ++i) {
+        // the products of chunk i - 1 are done before the next pass writes the
+        // buffer that they read
+        if (!(ok = __all_sync(0xffffffffu, put_p(i) && (i == 0 || mbar_wait(&S.o_bar, (i - 1) & 1))))) break;
+        if (lane == 0) mbar_arrive(&S.ready);
+      }
+      if (!ok && lane == 0) report(p.err, GDN_DEV_ERR_TIMEOUT);
+    }
   } else {
     // ----------------------------------------------------------------- compute
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kComputeRegs));
@@ -986,20 +1070,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       // One segment: from the slot.  Several: the first launch starts the
       // first segment from the slot and keeps a copy, at the last segment's
       // otherwise unused place, for the second launch; the others from zero.
-      const auto slot = GDN_GV(p.ssm, p.num_slots * slot_n) + ((size_t)s.slot * slot_n + tile0);
-      const auto keep = segs + (n_seg > 1 ? (seg_first + n_seg - 1) * slot_n + (int64_t)tile0 : 0);
+      const auto slot = GDN_GV(p.ssm, p.num_slots * slot_n) + ((size_t)S.ch.slot * slot_n + tile0);
+      const int seg = S.ch.seg, n_seg = S.ch.n_seg;
+      const int64_t seg0 = S.ch.seg0;
+      const auto keep = segs + (n_seg > 1 ? (seg0 + n_seg - 1) * slot_n + (int64_t)tile0 : 0);
       float4 v[8];  // piece `lane` of rows warp, warp + 16, ..
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int at = ((warp + 16 * j) * 32 + lane) * 4;
         v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (seg == 0 || !STATE) v[j] = STATE || n_seg == 1 ? vec_at<const float4>(slot, at) : vec_at<const float4>(keep, at);
+        if (seg == 0) v[j] = STATE || n_seg == 1 ? vec_at<const float4>(slot, at) : vec_at<const float4>(keep, at);
         if (STATE && seg == 0) vec_at<float4>(keep, at) = v[j];
       }
       if (!STATE) {
         for (int k = 0; k < seg; ++k) {
-          const auto L = segs + ((seg_first + k) * slot_n + (int64_t)tile0);
-          const auto dec = GDN_GV(a.seg_decay, (long long)a.n_segs * p.hv) + ((seg_first + k) * p.hv + h0);
+          const auto L = segs + ((seg0 + k) * slot_n + (int64_t)tile0);
+          const auto dec = GDN_GV(a.seg_decay, (long long)a.n_segs * p.hv) + ((seg0 + k) * p.hv + h0);
           // the first segment's state holds the slot's already
           const float d0 = k ? dec[0] : 0.f, d1 = k ? dec[NH - 1] : 0.f;
 #pragma unroll
@@ -1038,31 +1124,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const float4 w4 = vec_at<const float4>(GDN_GV(p.conv_w, (long long)p.C * 4), (size_t)ch * 4);
     const float bias = p.conv_bias ? GDN_GV(p.conv_bias, p.C)[ch] : 0.f;
-    // P's rows of this thread: row pr of the heads' 64 NH, PC columns from pc;
-    // what lies above the diagonal stays zero
-    constexpr int PC = 8 * NH;
-    const int pr = NH == 2 ? lrow : (lrow & 63), pi = pr & 63, ph = pr >> 6;
-    const int pc = 16 * qq + (NH == 2 ? 0 : 8 * (lrow >> 6));
-    if (!STATE) {
-#pragma unroll
-      for (int c8 = 0; c8 < PC / 8; ++c8) {
-        tile_at<uint4>(S.pt[0], sizeof(S.pt[0]), umma::sw128_off(pr, pc + 8 * c8, 0)) = make_uint4(0u, 0u, 0u, 0u);
-        tile_at<uint4>(S.pt[1], sizeof(S.pt[1]), umma::sw128_off(pr, pc + 8 * c8, 0)) = make_uint4(0u, 0u, 0u, 0u);
-      }
-    }
     // chunks until the next block boundary, and the boundary's index
-    const int kpc = p.ckpt_block / kC;
-    int to_ckpt = kpc - 1 - (int)((P0 / kC) % kpc);
-    int ck_idx = (int)min((int64_t)p.max_ckpt, P0 / p.ckpt_block - s.p0 / p.ckpt_block);
+    int to_ckpt = S.ch.to_ckpt, ck_idx = S.ch.ck_idx;
     // the sequence's tokens, counted from the segment's first chunk
-    const int first = (int)(s.p0 - P0), last = (int)min((int64_t)nit * kC, s.p1 - P0);
+    const int first = -S.ch.m0, last = min(nit * kC, S.ch.len - S.ch.m0);
 
     float2 y[8];  // V 2^ve of the next chunk: channel lrow, tokens 16 qq ..
-    // V and P of the segment's chunk i; false if a wait expired
+    // V of the segment's chunk i; false if a wait expired
     auto features = [&](int i) -> bool {
       const uint32_t par = (i >> 1) & 1;
-      if (!mbar_wait(&S.gx[i & 1], par) || !mbar_wait(&S.x_bar[i & 1], par) || !mbar_wait(&S.g_bar[i & 1], par))
-        return false;
+      if (!mbar_wait(&S.gx[i & 1], par) || !mbar_wait(&S.x_bar[i & 1], par)) return false;
       const int buf = i & 3;
       {
         const auto xs = GDN_SV(reinterpret_cast<const uint16_t*>(&S.raw[i & 1][0][0]), kRawRows * 128) +
@@ -1094,58 +1165,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (2 * t + 1 < tlo || 2 * t + 1 >= thi) y[t].y = 0.f;
         }
       }
-      if constexpr (!STATE) {
-        if (pc <= pi) {
-          // P_ij = G_ij u_i v_j: both factors taken at the end b' of j's
-          // 16-token block, u_i = e^{b_i - b'} at most 1 below the diagonal
-          // blocks; on them it is large where the block decays, and beyond
-          // 2^80 the differences are taken one by one
-          const float bi = S.b2[buf][ph][pi], be = S.b2[buf][ph][GDN_S(pc | 15, kC)];
-          const float pscale = S.sc[buf][ph].p;
-          const float u = ex2(bi - be) * pscale;
-          float2 e[PC / 2];
-#pragma unroll
-          for (int c8 = 0; c8 < PC / 8; ++c8) {
-            const uint4 g4 = tile_at<uint4>(S.g[i & 1].g, kGBytes, umma::sw128_off(pi, pc + 8 * c8, 0));
-            const float4 va = *reinterpret_cast<const float4*>(&S.v[buf][ph][GDN_S(pc + 8 * c8, kC - 7)]);
-            const float4 vb = *reinterpret_cast<const float4*>(&S.v[buf][ph][pc + 8 * c8 + 4]);
-            const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w};
-            const float2 vv[4] = {lo2(va), hi2(va), lo2(vb), hi2(vb)};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              e[4 * c8 + k] = mul2(__half22float2(*reinterpret_cast<const __half2*>(&gw[k])),
-                                   mul2(vv[k], make_float2(u, u)));
-          }
-          if ((pi >> 4) == qq) {
-            const float sk = S.sc[buf][ph].skip;
-            if (S.b2[buf][ph][pc & ~15] - be > 80.f) {
-#pragma unroll 1
-              for (int k = 0; k < PC; ++k) {
-                const int j = pc + k;
-                const float g = __half2float(tile_at<__half>(S.g[i & 1].g, kGBytes, umma::sw128_off(pi, j, 0)));
-                const float x = j > pi ? 0.f : g * (ex2(bi - S.b2[buf][ph][GDN_S(j, kC)]) * S.dt[buf][ph][j] * pscale);
-#pragma unroll
-                for (int q = 0; q < PC / 2; ++q) {
-                  if (2 * q == k) e[q].x = x;
-                  if (2 * q + 1 == k) e[q].y = x;
-                }
-              }
-            }
-#pragma unroll
-            for (int k = 0; k < PC / 2; ++k) {
-              const int j = pc + 2 * k;
-              e[k].x = j < pi ? e[k].x : j == pi ? e[k].x + sk : 0.f;
-              e[k].y = j + 1 < pi ? e[k].y : j + 1 == pi ? e[k].y + sk : 0.f;
-            }
-          }
-#pragma unroll
-          for (int c8 = 0; c8 < PC / 8; ++c8)
-            tile_at<uint4>(S.pt[i & 1], sizeof(S.pt[0]), umma::sw128_off(pr, pc + 8 * c8, 0)) =
-                make_uint4(half2_bits(e[4 * c8].x, e[4 * c8].y), half2_bits(e[4 * c8 + 1].x, e[4 * c8 + 1].y),
-                           half2_bits(e[4 * c8 + 2].x, e[4 * c8 + 2].y), half2_bits(e[4 * c8 + 3].x, e[4 * c8 + 3].y));
-        }
-      }
-      umma::fence_proxy_async();  // P
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.used[i & 1]);
       return true;
@@ -1190,6 +1209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(bar);
     };
 
+    const auto out = GDN_GV(reinterpret_cast<__nv_bfloat16*>(p.out), p.total * p.hv * DV);
     named_sync(1, kCompute);  // smax complete
     s_bound = __uint_as_float(S.smax[hl]);
     bool ok = true;
@@ -1199,35 +1219,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_wait_st();
       publish(&S.ready);
     }
-    // pass i: chunk i + 1's features, chunk i's results, chunk i + 1's operands
+    // pass i: chunk i + 1's V, the state after chunk i, chunk i + 1's operands
 #pragma unroll 1
     for (int i = 0; i < nit && ok; ++i) {
       const bool more = i + 1 < nit;
-      if (more) {
-        if (!(ok = __all_sync(0xffffffffu, features(i + 1)))) break;
-      }
-      [[maybe_unused]] float f1, f2;
-      {
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&S.ds_bar, i & 1)))) break;
-        umma::fence_after();
-        const Scales& sc = S.sc[i & 3][hl];
-        const float4 sa = *reinterpret_cast<const float4*>(&sc.dec);  // dec, ds, o2, q
-        f1 = s_back * sa.w;
-        f2 = sa.z;
-        s_bound = fmaf(s_bound, sa.x, sc.grow);
-        seg_dec *= sa.x;
+      if (more && !(ok = __all_sync(0xffffffffu, features(i + 1)))) break;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&S.ds_bar, i & 1)))) break;
+      umma::fence_after();
+      const Scales& sc = S.sc[i & 3][hl];
+      const float4 sa = *reinterpret_cast<const float4*>(&sc.dec);  // dec, ds, o2, q
+      [[maybe_unused]] const float f1 = s_back * sa.w, f2 = sa.z;
+      s_bound = fmaf(s_bound, sa.x, sc.grow);
+      seg_dec *= sa.x;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float d[16];
-          umma::tmem_ld16(tlane + TM_DS + 32 * qq + 16 * k, d);
+      for (int k = 0; k < 2; ++k) {
+        float d[16];
+        umma::tmem_ld16(tlane + TM_DS + 32 * qq + 16 * k, d);
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            st[8 * k + e] = fma2(st[8 * k + e], make_float2(sa.x, sa.x),
-                                 mul2(make_float2(d[2 * e], d[2 * e + 1]), make_float2(sa.y, sa.y)));
-        }
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&S.o_bar, i & 1)))) break;
-        umma::fence_after();
+        for (int e = 0; e < 8; ++e)
+          st[8 * k + e] = fma2(st[8 * k + e], make_float2(sa.x, sa.x),
+                               mul2(make_float2(d[2 * e], d[2 * e + 1]), make_float2(sa.y, sa.y)));
       }
+      // the products of chunk i are done: their operands may go
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&S.o_bar, i & 1)))) break;
+      umma::fence_after();
       if (more) {
         put_v(i + 1);
         put_s();
@@ -1240,8 +1255,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         publish(&S.ready);
       }
       if constexpr (!STATE) {
-        if (i > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&S.o_free, (i - 1) & 1)))) break;
-        const auto ot = GDN_SV(&S.ot[0][0], kC * 128) + (16 * qq * 128 + lrow);
+        // a warp's 32 channels of a token are 64 consecutive bytes
+        const int tlo = first - i * kC - 16 * qq, thi = last - i * kC - 16 * qq;  // tokens of the sequence
+        const long long ld = (long long)p.hv * DV;
+        const long long at = (S.ch.t0 + S.ch.m0 + i * kC + 16 * qq) * ld + tile * 128 + lrow;  // may be < 0
+        __nv_bfloat16 ob[16];
 #pragma unroll
         for (int t4 = 0; t4 < 4; ++t4) {
           const float4 e = *reinterpret_cast<const float4*>(&S.eb[i & 3][hl][GDN_S(16 * qq + 4 * t4, kC - 3)]);
@@ -1252,18 +1270,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float2 o = fma2(mul2(make_float2(o1[t], o1[t + 1]), make_float2(f1, f1)), ev[k],
                                   mul2(make_float2(o2[t], o2[t + 1]), make_float2(f2, f2)));
             const __nv_bfloat162 h = __floats2bfloat162_rn(o.x, o.y);
-            ot[t * 128] = h.x;
-            ot[(t + 1) * 128] = h.y;
+            ob[t] = h.x;
+            ob[t + 1] = h.y;
           }
         }
-        umma::fence_proxy_async();
-        publish(&S.o_full);
+        if (tlo <= 0 && thi >= 16) {
+#pragma unroll
+          for (int t = 0; t < 16; ++t) out[at + t * ld] = ob[t];
+        } else {
+#pragma unroll
+          for (int t = 0; t < 16; ++t)
+            if (t >= tlo && t < thi) out[at + t * ld] = ob[t];
+        }
         // the block boundary at this chunk's end (a sequence that ends inside
         // the chunk does not reach it)
         if (to_ckpt-- == 0) {
-          to_ckpt = kpc - 1;
+          to_ckpt = p.ckpt_block / kC - 1;
           if (ck_idx < p.max_ckpt && (i + 1) * kC <= last) {
-            const int32_t cid = GDN_GV(p.ckpt_ids, (long long)p.n_seq * p.max_ckpt)[(size_t)n * p.max_ckpt + ck_idx];
+            const int32_t cid = GDN_GV(p.ckpt_ids, (long long)p.n_seq * p.max_ckpt)[(size_t)S.ch.n * p.max_ckpt + ck_idx];
             if (slot_class(cid, p.ck_num_slots) == 0) {
               // quarter rows, 32 bytes per access where the pool's alignment allows
               const auto to = GDN_GV(p.ck_ssm, p.ck_num_slots * slot_n) +
@@ -1285,11 +1309,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (named_sync_or(1, kCompute, !ok)) {
       if (tid == 0) report(p.err, GDN_DEV_ERR_TIMEOUT);
     } else if (STATE) {
-      save(segs + ((seg_first + seg) * slot_n + (int64_t)tile0));
+      save(segs + ((S.ch.seg0 + S.ch.seg) * slot_n + (int64_t)tile0));
       if (qq == 0 && lrow % DV == 0)
-        GDN_GV(a.seg_decay, (long long)a.n_segs * p.hv)[(seg_first + seg) * p.hv + h0 + hl] = seg_dec;
-    } else if (seg == n_seg - 1) {
-      save(GDN_GV(p.ssm, p.num_slots * slot_n) + ((size_t)s.slot * slot_n + tile0));
+        GDN_GV(a.seg_decay, (long long)a.n_segs * p.hv)[(S.ch.seg0 + S.ch.seg) * p.hv + h0 + hl] = seg_dec;
+    } else if (S.ch.seg == S.ch.n_seg - 1) {
+      save(GDN_GV(p.ssm, p.num_slots * slot_n) + ((size_t)S.ch.slot * slot_n + tile0));
     }
   }
   umma::fence_before();
@@ -1345,7 +1369,7 @@ int64_t hist_blocks(int64_t C) { return (C + kThreads - 1) / kThreads; }
 int64_t hist_rows(int64_t n_seq, int64_t C, int64_t tiles) { return (n_seq * hist_blocks(C) + tiles - 1) / tiles; }
 
 template <int NH>
-cudaError_t launch_chain(const ChunkArgs& a, const Layout& l, const CUtensorMap& xmap, const CUtensorMap& omap,
+cudaError_t launch_chain(const ChunkArgs& a, const Layout& l, const CUtensorMap& xmap,
                          cudaStream_t s) {
   const size_t smem = sizeof(ChainSmem<NH>) + 1024;
   const unsigned tiles = (unsigned)(a.p.hv / NH);
@@ -1354,11 +1378,11 @@ cudaError_t launch_chain(const ChunkArgs& a, const Layout& l, const CUtensorMap&
   if (l.seg_chunks < l.n_chunks) {
     auto k = ssm_chain_kernel<NH, true>;
     if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
-    if ((e = launch_pdl(k, grid, dim3(kThreads), smem, s, dim3(1), a, xmap, omap)) != cudaSuccess) return e;
+    if ((e = launch_pdl(k, grid, dim3(kThreads), smem, s, dim3(1), a, xmap)) != cudaSuccess) return e;
   }
   auto k = ssm_chain_kernel<NH, false>;
   if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
-  return launch_pdl(k, all, dim3(kThreads), smem, s, dim3(1), a, xmap, omap);
+  return launch_pdl(k, all, dim3(kThreads), smem, s, dim3(1), a, xmap);
 }
 
 }  // namespace
@@ -1420,12 +1444,9 @@ cudaError_t ssm_chunk_launch(const ssm::PrefillArgs& p, const gdn_dims& d, void*
   h.W = p.W;
   h.C = p.C;
   h.G = p.G;
-  CUtensorMap xmap, omap;
+  CUtensorMap xmap;
   cudaError_t e;
   if ((e = tensor_map_2d(&xmap, p.qkv, p.total, p.C, 2, 128, kRawRows, CU_TENSOR_MAP_SWIZZLE_NONE)) != cudaSuccess)
-    return e;
-  if ((e = tensor_map_2d(&omap, p.out, p.total, (int64_t)p.hv * p.dv, 2, 128, kC, CU_TENSOR_MAP_SWIZZLE_NONE)) !=
-      cudaSuccess)
     return e;
   const size_t smem = sizeof(FeatSmem) + 1024;
   if ((e = cudaFuncSetAttribute(ssm_features_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
@@ -1435,7 +1456,7 @@ cudaError_t ssm_chunk_launch(const ssm::PrefillArgs& p, const gdn_dims& d, void*
   if ((e = launch_pdl(ssm_features_kernel, dim3(walks + (unsigned)p.n_seq, (unsigned)p.hk), dim3(kFT), smem, s, dim3(1),
                       a, xmap)) != cudaSuccess)
     return e;
-  return p.dv == 64 ? launch_chain<2>(a, l, xmap, omap, s) : launch_chain<1>(a, l, xmap, omap, s);
+  return p.dv == 64 ? launch_chain<2>(a, l, xmap, s) : launch_chain<1>(a, l, xmap, s);
 }
 
 }  // namespace gdn
