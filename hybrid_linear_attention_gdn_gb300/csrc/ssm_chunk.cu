@@ -464,6 +464,13 @@ constexpr int kComputeRegs = 96, kAuxRegs = 48, kHelpRegs = 48;
 static_assert(kCompute * kComputeRegs + kAux * kAuxRegs + 128 * kHelpRegs <= kThreads * 80,
               "no more than the launch's registers");
 
+// Raw V rows and G of up to kRing chunks are on their way or being read (with
+// two, 4 x 8192 tokens took 452 us, not 446: copy, largest input and
+// scales then follow one another within a chunk); gates in twice as many slots.
+constexpr int kRing = 3, kSlots = 2 * kRing;
+__device__ __forceinline__ int ring(int i) { return i % kRing; }
+__device__ __forceinline__ uint32_t phase(int i) { return i / kRing & 1; }
+
 // TMEM columns (fp16 operands hold two values per column)
 constexpr uint32_t TM_DS = 0;    // dS^T [dv rows][dk]
 constexpr uint32_t TM_O1 = 128;  // [dv rows][64 tokens]
@@ -505,22 +512,22 @@ struct __align__(1024) ChainSmem {
   struct __align__(1024) Gm {
     uint8_t g[kGBytes];
     int32_t meta[4];               // qe, ke
-  } g[2];
-  __nv_bfloat16 raw[2][kRawRows][128];
-  // per chunk (mod 4) and head
-  __align__(16) float b2[4][NH][kC];  // b log2(e)
-  float eb[4][NH][kC];                // e^b
-  float dt[4][NH][kC];
-  float v[4][NH][kC];                 // e^{b' - b} dt, b' at the end of the token's 16-token block
-  float w[4][NH][kC];                 // e^{b_last - b} dt 2^(we - ve)
-  Scales sc[4][NH];
-  float xmax[2];                      // largest raw input of a chunk (mod 2)
+  } g[kRing];
+  __nv_bfloat16 raw[kRing][kRawRows][128];
+  // per chunk (mod kSlots) and head
+  __align__(16) float b2[kSlots][NH][kC];  // b log2(e)
+  float eb[kSlots][NH][kC];                // e^b
+  float dt[kSlots][NH][kC];
+  float v[kSlots][NH][kC];                 // e^{b' - b} dt, b' at the end of the token's 16-token block
+  float w[kSlots][NH][kC];                 // e^{b_last - b} dt 2^(we - ve)
+  Scales sc[kSlots][NH];
+  float xmax[kRing];                  // largest raw input of a chunk
   float vgain, vbias;                 // |V| <= vgain xmax + vbias
   uint32_t smax[NH];                  // largest |S| entering the segment, float bits
-  uint64_t x_bar[2], g_bar[2], qk_bar[2];  // copies landed
-  uint64_t hx[2];                     // xmax known, history rows in place
-  uint64_t gx[2];                     // gates and scales known
-  uint64_t used[2];                   // raw rows and G read
+  uint64_t x_bar[kRing], g_bar[kRing], qk_bar[2];  // copies landed
+  uint64_t hx[kRing];                 // xmax known, history rows in place
+  uint64_t gx[kRing];                 // gates and scales known
+  uint64_t used[kRing];               // raw rows and G read
   uint64_t ready;                     // operands in place
   uint64_t ds_bar, o_bar;             // dS^T done; all products done
   uint64_t s_used;                    // the state's way through S.qk is free
@@ -648,14 +655,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     umma::tmem_alloc(&S.tmem_base, TM_COLS);
   } else if (tid == 64) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kRing; ++i) {
       mbar_init(&S.x_bar[i], 1);
       mbar_init(&S.g_bar[i], 1);
-      mbar_init(&S.qk_bar[i], 1);
       mbar_init(&S.hx[i], 1);
       mbar_init(&S.gx[i], NH);
       mbar_init(&S.used[i], kPart);
     }
+    mbar_init(&S.qk_bar[0], 1);
+    mbar_init(&S.qk_bar[1], 1);
     mbar_init(&S.ready, kPart);
     mbar_init(&S.ds_bar, 1);
     mbar_init(&S.o_bar, 1);
@@ -801,15 +809,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           b[e] *= 1.4426950408889634f;
           vj[e] = ex2(__shfl_sync(0xffffffffu, b[e], lane | 15) - b[e]) * dt[e];
         }
-        // Chunk i's raw rows and G have landed: chunk i - 2's were read by
-        // every compute warp, whose chunk i - 4 was done before that, so the
-        // slot of chunk i - 4 may be written.
-        const bool in_time = mbar_wait(&S.hx[i & 1], (i >> 1) & 1) && mbar_wait(&S.g_bar[i & 1], (i >> 1) & 1);
+        // Chunk i's raw rows and G have landed: chunk i - 3's were read by
+        // every compute warp, whose chunk i - 5 was done before that, so the
+        // slot of chunk i - 6 may be written.
+        const bool in_time = mbar_wait(&S.hx[ring(i)], phase(i)) && mbar_wait(&S.g_bar[ring(i)], phase(i));
         if (!(ok = __all_sync(0xffffffffu, in_time))) break;
-        const int buf = i & 3, qe = S.g[i & 1].meta[0], ke = S.g[i & 1].meta[1];
+        const int buf = i % kSlots, qe = S.g[ring(i)].meta[0], ke = S.g[ring(i)].meta[1];
         // |V| <= vb, |V w| <= vb max dt,
         // |P| <= 128 max|q| max|k| max dt + |D| < 2^(37 - qe - ke) max dt + |D|
-        const float vb = fmaf(S.vgain, S.xmax[i & 1], S.vbias);
+        const float vb = fmaf(S.vgain, S.xmax[ring(i)], S.vbias);
         const float gb = exp2_int(max(-126, min(127, 37 - qe - ke)));
         const int ve = scale_exp(__float_as_uint(vb)), we = scale_exp(__float_as_uint(vb * dtm));
         const int pe = scale_exp(__float_as_uint(fmaf(gb, dtm, fabsf(D))));
@@ -835,22 +843,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           c.skip = D * exp2_int(pe);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.gx[i & 1]);
+        if (lane == 0) mbar_arrive(&S.gx[ring(i)]);
       }
       if (!ok && lane == 0) report(p.err, GDN_DEV_ERR_TIMEOUT);
     } else if (warp == kLoader) {
       // ---------------------------------------------------------------- loader
       auto load_xg = [&](int i) {
         const int32_t row0 = S.ch.t0 + S.ch.m0 + i * kC - 3;  // may be < 0: zeros
-        mbar_arrive_expect_tx(&S.x_bar[i & 1], (uint32_t)sizeof(S.raw[0]));
-        if (GDN_SPAN_G(2 * p.hk * kDK + tile * 128, 128, p.C) && GDN_SBYTES(&S.raw[i & 1][0][0], sizeof(S.raw[0]), S))
-          tma_load_2d(&S.raw[i & 1][0][0], &xmap, 2 * p.hk * kDK + tile * 128, row0, &S.x_bar[i & 1]);
-        bulk(&S.g[i & 1], a.rec[S.ch.rec0 + (int64_t)i * p.hk].g, kGMBytes, &S.g_bar[i & 1]);
+        mbar_arrive_expect_tx(&S.x_bar[ring(i)], (uint32_t)sizeof(S.raw[0]));
+        if (GDN_SPAN_G(2 * p.hk * kDK + tile * 128, 128, p.C) && GDN_SBYTES(&S.raw[ring(i)][0][0], sizeof(S.raw[0]), S))
+          tma_load_2d(&S.raw[ring(i)][0][0], &xmap, 2 * p.hk * kDK + tile * 128, row0, &S.x_bar[ring(i)]);
+        bulk(&S.g[ring(i)], a.rec[S.ch.rec0 + (int64_t)i * p.hk].g, kGMBytes, &S.g_bar[ring(i)]);
       };
       int n = 0;  // issued
       if (lane == 0)
-        for (; n < 2 && n < nit; ++n) load_xg(n);
-      n = min(2, nit);
+        for (; n < kRing && n < nit; ++n) load_xg(n);
+      n = min(kRing, nit);
       // the up to 3 rows just before the sequence, from the conv history
       __nv_bfloat16 hrow[3][4];
       if (S.ch.m0 < 3) {
@@ -885,27 +893,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       bool ok = true;
       for (int i = 0; i < nit && ok; ++i) {
-        if (i >= 2) {
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&S.used[i & 1], ((i - 2) >> 1) & 1)))) break;
+        if (i >= kRing) {
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&S.used[ring(i)], phase(i - kRing))))) break;
           if (lane == 0) load_xg(i);
           n = i + 1;
         }
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&S.x_bar[i & 1], (i >> 1) & 1)))) break;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&S.x_bar[ring(i)], phase(i))))) break;
         const int m0 = S.ch.m0 + i * kC;
-        if (m0 < 3) {
-          // history row j is token j - 3, raw row r token m - 3 + r
+        const auto rows = GDN_SV(reinterpret_cast<uint4*>(&S.raw[ring(i)][0][0]), kRawRows * 16);
+        if (m0 < 3 || S.ch.len - m0 < kC) {
+          // What stands around the sequence in the packed rows is not its
+          // business: zeros, or it would count among the largest inputs.
+          for (int e = lane; e < kRawRows * 16; e += 32)
+            if ((unsigned)(m0 + e / 16) >= (unsigned)S.ch.len + 3) rows[e] = make_uint4(0u, 0u, 0u, 0u);
+          __syncwarp();
+          // history row j is token j - 3, raw row r token m0 - 3 + r
 #pragma unroll
           for (int j = 0; j < 3; ++j) {
             const int r = j - m0;
             if (r >= 0 && r < kRawRows)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) S.raw[i & 1][GDN_S(r, kRawRows)][32 * k + lane] = hrow[j][k];
+              for (int k = 0; k < 4; ++k) S.raw[ring(i)][GDN_S(r, kRawRows)][32 * k + lane] = hrow[j][k];
           }
           umma::fence_proxy_async();  // before a later chunk's copy into these rows
           __syncwarp();
         }
         // the largest finite |raw input|
-        const auto rows = GDN_SV(reinterpret_cast<const uint4*>(&S.raw[i & 1][0][0]), kRawRows * 16);
         __nv_bfloat162 mx[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) mx[k] = __floats2bfloat162_rn(0.f, 0.f);
@@ -924,22 +937,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (__any_sync(0xffffffffu, m >= 0x7f800000u)) {  // infinities: without them
           m = 0;
           for (int e = lane; e < kRawRows * 128; e += 32) {
-            const uint32_t v = __float_as_uint(__bfloat162float(S.raw[i & 1][e / 128][e % 128])) & 0x7fffffffu;
+            const uint32_t v = __float_as_uint(__bfloat162float(S.raw[ring(i)][e / 128][e % 128])) & 0x7fffffffu;
             m = max(m, v < 0x7f800000u ? v : 0u);
           }
         }
         m = __reduce_max_sync(0xffffffffu, m);
         if (lane == 0) {
-          S.xmax[i & 1] = __uint_as_float(m);
-          mbar_arrive(&S.hx[i & 1]);
+          S.xmax[ring(i)] = __uint_as_float(m);
+          mbar_arrive(&S.hx[ring(i)]);
         }
         __syncwarp();
       }
       if (lane == 0) {
         if (!ok) report(p.err, GDN_DEV_ERR_TIMEOUT);
-        for (int k = max(0, n - 2); k < n; ++k) {  // as the issuer
-          mbar_wait(&S.x_bar[k & 1], (k >> 1) & 1);
-          mbar_wait(&S.g_bar[k & 1], (k >> 1) & 1);
+        for (int k = max(0, n - kRing); k < n; ++k) {  // as the issuer
+          mbar_wait(&S.x_bar[ring(k)], phase(k));
+          mbar_wait(&S.g_bar[ring(k)], phase(k));
         }
       }
     }
@@ -962,9 +975,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // P of the segment's chunk i; false if a wait expired
       auto put_p = [&](int i) -> bool {
-        const uint32_t par = (i >> 1) & 1;
-        if (!mbar_wait(&S.gx[i & 1], par) || !mbar_wait(&S.g_bar[i & 1], par)) return false;
-        const int buf = i & 3;
+        const uint32_t par = phase(i);
+        if (!mbar_wait(&S.gx[ring(i)], par) || !mbar_wait(&S.g_bar[ring(i)], par)) return false;
+        const int buf = i % kSlots;
 #pragma unroll 1
         for (int J = 0; 16 * J < wlo + 32; ++J) {
           const int pc = 16 * J + pc0;
@@ -978,7 +991,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float2 e[PC / 2];
 #pragma unroll
           for (int c8 = 0; c8 < PC / 8; ++c8) {
-            const uint4 g4 = tile_at<uint4>(S.g[i & 1].g, kGBytes, umma::sw128_off(pi, pc + 8 * c8, 0));
+            const uint4 g4 = tile_at<uint4>(S.g[ring(i)].g, kGBytes, umma::sw128_off(pi, pc + 8 * c8, 0));
             const float4 va = *reinterpret_cast<const float4*>(&S.v[buf][ph][GDN_S(pc + 8 * c8, kC - 7)]);
             const float4 vb = *reinterpret_cast<const float4*>(&S.v[buf][ph][pc + 8 * c8 + 4]);
             const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w};
@@ -994,7 +1007,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
               for (int k = 0; k < PC; ++k) {
                 const int j = pc + k;
-                const float g = __half2float(tile_at<__half>(S.g[i & 1].g, kGBytes, umma::sw128_off(pi, j, 0)));
+                const float g = __half2float(tile_at<__half>(S.g[ring(i)].g, kGBytes, umma::sw128_off(pi, j, 0)));
                 const float x = j > pi ? 0.f : g * (ex2(bi - S.b2[buf][ph][GDN_S(j, kC)]) * S.dt[buf][ph][j] * pscale);
 #pragma unroll
                 for (int q = 0; q < PC / 2; ++q) {
@@ -1018,7 +1031,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         umma::fence_proxy_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.used[i & 1]);
+        if (lane == 0) mbar_arrive(&S.used[ring(i)]);
         return true;
       };
       bool ok = true;
@@ -1132,11 +1145,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     float2 y[8];  // V 2^ve of the next chunk: channel lrow, tokens 16 qq ..
     // V of the segment's chunk i; false if a wait expired
     auto features = [&](int i) -> bool {
-      const uint32_t par = (i >> 1) & 1;
-      if (!mbar_wait(&S.gx[i & 1], par) || !mbar_wait(&S.x_bar[i & 1], par)) return false;
-      const int buf = i & 3;
+      const uint32_t par = phase(i);
+      if (!mbar_wait(&S.gx[ring(i)], par) || !mbar_wait(&S.x_bar[ring(i)], par)) return false;
+      const int buf = i % kSlots;
       {
-        const auto xs = GDN_SV(reinterpret_cast<const uint16_t*>(&S.raw[i & 1][0][0]), kRawRows * 128) +
+        const auto xs = GDN_SV(reinterpret_cast<const uint16_t*>(&S.raw[ring(i)][0][0]), kRawRows * 128) +
                         (16 * qq * 128 + lrow);
         uint32_t x[19];
 #pragma unroll
@@ -1166,12 +1179,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.used[i & 1]);
+      if (lane == 0) mbar_arrive(&S.used[ring(i)]);
       return true;
     };
     // chunk i's V and V w to their operands
     auto put_v = [&](int i) {
-      const auto ws = GDN_SV(&S.w[i & 3][hl][0], kC);
+      const auto ws = GDN_SV(&S.w[i % kSlots][hl][0], kC);
       uint32_t hi[8], lo[8];
 #pragma unroll
       for (int t4 = 0; t4 < 4; ++t4) {
@@ -1226,7 +1239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (more && !(ok = __all_sync(0xffffffffu, features(i + 1)))) break;
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(&S.ds_bar, i & 1)))) break;
       umma::fence_after();
-      const Scales& sc = S.sc[i & 3][hl];
+      const Scales& sc = S.sc[i % kSlots][hl];
       const float4 sa = *reinterpret_cast<const float4*>(&sc.dec);  // dec, ds, o2, q
       [[maybe_unused]] const float f1 = s_back * sa.w, f2 = sa.z;
       s_bound = fmaf(s_bound, sa.x, sc.grow);
@@ -1262,7 +1275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __nv_bfloat16 ob[16];
 #pragma unroll
         for (int t4 = 0; t4 < 4; ++t4) {
-          const float4 e = *reinterpret_cast<const float4*>(&S.eb[i & 3][hl][GDN_S(16 * qq + 4 * t4, kC - 3)]);
+          const float4 e = *reinterpret_cast<const float4*>(&S.eb[i % kSlots][hl][GDN_S(16 * qq + 4 * t4, kC - 3)]);
           const float2 ev[2] = {lo2(e), hi2(e)};
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
