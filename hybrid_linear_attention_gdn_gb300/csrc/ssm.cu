@@ -64,6 +64,8 @@ __device__ __forceinline__ int reduce_rows(float (&o)[UN], bool& writer) {
 // ---------------------------------------------------------------------------
 // decode
 // ---------------------------------------------------------------------------
+// The split form, for few requests and for shapes that the persistent form
+// (ssm_ring.cu) does not take.
 // HBM bound: the state is read and written once (8 dk bytes per row), all
 // else is about 1 % of it.  A cluster of `cs` CTAs takes one request and one
 // QK head hq: the G dv state rows of the V heads that read hq are split
@@ -73,25 +75,9 @@ __device__ __forceinline__ int reduce_rows(float (&o)[UN], bool& writer) {
 // every CTA reaches long before the first has streamed its rows.  Each warp
 // holds UN accesses of rows in flight, the first batch requested before the
 // features are computed; several CTAs per SM cover one another's prologues.
-struct DecodeArgs {
-  float* ssm;
-  void* conv;
-  int32_t num_slots;
-  const float* conv_w;
-  const float* conv_bias;
-  const float* A_log;
-  const float* dt_bias;
-  const float* D;
-  const int32_t* slot_ids;
-  int32_t B;
-  const void* qkv;
-  const void* a;
-  void* out;
-  uint32_t* err;
-  int32_t hk, hv, dv, W, C, G;
-  int32_t cs, rpc;  // CTAs per (request, QK head); rows per CTA
-};
-
+// 64 heads of 64 in 8 groups, graph of calls: 1 / 4 / 24 requests 5.0 / 8.2 /
+// 21.4 us (0.12 / 0.30 / 0.69 of the copy bandwidth); 32 heads of 64 in one
+// group, 64 / 256 requests 29.8 / 98 us (0.66 / 0.81).
 template <int DK, int UN, typename Tact, typename Tconv>
 __global__ void __launch_bounds__(kThreads, 3) ssm_decode_kernel(const DecodeArgs a) {
   using M = Rows<DK>;
@@ -420,22 +406,46 @@ extern "C" gdn_status gdn_ssm_decode_step(const gdn_dims* dims, gdn_pool pool, c
   d.W = dims->conv_width;
   d.C = (int32_t)channels(*dims);
   d.G = dims->hv / dims->hk;
-  // split a group's rows over up to 8 CTAs while the grid is short of four
-  // CTAs per SM and each still has a batch of rows, and whatever the grid to
-  // at most 1024 rows per CTA (its share of shared memory)
-  const int batch = dims->dk == 128 ? 64 : 128;
-  d.cs = 1;
-  while (d.cs < 8 && (rows > 1024LL * d.cs ||
-                      ((int64_t)B * d.hk * d.cs < 4LL * sm_count() && rows >= 2LL * batch * d.cs)))
-    d.cs *= 2;
+  // Split a group's rows over 1 to 8 CTAs (at most 1024 rows each, their
+  // share of shared memory): the fewest rounds of 3 CTAs per SM times a CTA's
+  // rows and its prologue, which costs about as much as 128 rows of dk = 128.
+  // Clusters of 8 find room for an eighth less.  64 heads of 64 in 8 groups,
+  // us: 8 requests 10.8 in 4 parts (this rule), 14.0 in 8, 11.3 in 2; 16
+  // requests 16.0 in 2, 19.5 in 4; 64 requests 55.9 in 2, 61.9 whole.
+  const int64_t groups = (int64_t)B * d.hk, prologue = 16384 / dims->dk;
+  int64_t best = INT64_MAX;
+  for (int cs = 1; cs <= 8; cs *= 2) {
+    const int64_t room = 3LL * sm_count() * (cs == 8 ? 7 : 8) / 8, per = (rows + cs - 1) / cs;
+    const int64_t cost = (groups * cs + room - 1) / room * (per + prologue);
+    if (per <= 1024 && cost <= best) {
+      best = cost;
+      d.cs = cs;
+    }
+  }
   d.rpc = (int32_t)((rows + d.cs - 1) / d.cs);
   if ((int64_t)d.hk * d.cs > 2147483647LL) return GDN_ERR_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaErrorInvalidValue;
-  switch (dims->dk) {
-    case 16: e = dispatch_decode<16, 4>(d, dims->act_dtype, dims->conv_dtype, s); break;
-    case 64: e = dispatch_decode<64, 8>(d, dims->act_dtype, dims->conv_dtype, s); break;
-    case 128: e = dispatch_decode<128, 8>(d, dims->act_dtype, dims->conv_dtype, s); break;
+  // The persistent form where a round of one group per SM is well filled:
+  // from 0.4 of the first (64 heads of 64 in 8 groups: 4 requests, 0.21, 9.4
+  // us, split 8.2; 8 requests 10.0, split 10.9), from 0.7 of the last of
+  // several (24 requests, 0.63: 22.1, split 21.4; 40 requests, 0.70: 34.0,
+  // split 35.0; 64 requests, 0.84: 47.9, split 56.3).
+  // GDN_SSM_DECODE_PATH=ring or split (read on every call) forces one.
+  const int64_t rounds = (groups + sm_count() - 1) / sm_count(), full = rounds * sm_count();
+  bool ring = decode_ring_supported(*dims, B, qkv, *params) && groups * 10 >= full * (rounds == 1 ? 4 : 7);
+  if (const char* path = std::getenv("GDN_SSM_DECODE_PATH")) {
+    if (!std::strcmp(path, "split")) ring = false;
+    if (!std::strcmp(path, "ring")) ring = decode_ring_supported(*dims, B, qkv, *params);
+  }
+  if (ring) {
+    e = decode_ring_launch(d, dims->act_dtype, dims->conv_dtype, s);
+  } else {
+    switch (dims->dk) {
+      case 16: e = dispatch_decode<16, 4>(d, dims->act_dtype, dims->conv_dtype, s); break;
+      case 64: e = dispatch_decode<64, 8>(d, dims->act_dtype, dims->conv_dtype, s); break;
+      case 128: e = dispatch_decode<128, 8>(d, dims->act_dtype, dims->conv_dtype, s); break;
+    }
   }
   if (e != cudaSuccess) return GDN_ERR_CUDA;
   count_launch(GDN_K_SSM_DECODE);

@@ -18,6 +18,29 @@ __device__ __forceinline__ Gate gate(float A_log, float dt_bias, float a) {
   return r;
 }
 
+struct DecodeArgs {
+  float* ssm;
+  void* conv;
+  int32_t num_slots;
+  const float* conv_w;
+  const float* conv_bias;
+  const float* A_log;
+  const float* dt_bias;
+  const float* D;
+  const int32_t* slot_ids;
+  int32_t B;
+  const void* qkv;
+  const void* a;
+  void* out;
+  uint32_t* err;
+  int32_t hk, hv, dv, W, C, G;
+  int32_t cs, rpc;  // CTAs per (request, QK head); rows per CTA
+};
+
+// the persistent form for large batches (ssm_ring.cu)
+bool decode_ring_supported(const gdn_dims& d, int32_t B, const void* qkv, const gdn_ssm_params& p);
+cudaError_t decode_ring_launch(const DecodeArgs& a, int act, int cv, cudaStream_t s);
+
 struct PrefillArgs {
   float* ssm;
   const void* conv;
