@@ -353,7 +353,8 @@ __global__ void __launch_bounds__(kFT, 2)
 #pragma unroll
       for (int t = 0; t < 32; ++t) {
         y[t] = mul2(y[t], make_float2(f, f));
-        tile_at<__half2>(S.qk, sizeof(S.qk), umma::sw128_off(R0 + t, 2 * cp, 128 * 128)) = __floats2half2_rn(y[t].x, y[t].y);
+        tile_at<__half2>(S.qk, sizeof(S.qk), umma::sw128_off(R0 + t, 2 * cp, 128 * 128)) =
+            __floats2half2_rn(y[t].x, y[t].y);
       }
     }
     umma::fence_proxy_async();
@@ -436,7 +437,8 @@ __global__ void __launch_bounds__(kFT, 2)
   __syncthreads();
   if (warp == 1) umma::tmem_dealloc(tmem, 64);
 }
-static_assert(offsetof(FeatSmem, meta) == offsetof(FeatSmem, g) + kGBytes && offsetof(Record, qe) == offsetof(Record, g) + kGBytes,
+static_assert(offsetof(FeatSmem, meta) == offsetof(FeatSmem, g) + kGBytes &&
+                  offsetof(Record, qe) == offsetof(Record, g) + kGBytes,
               "G and its exponents leave and arrive as one piece");
 
 // ---------------------------------------------------------------------------
@@ -863,7 +865,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       __nv_bfloat16 hrow[3][4];
       if (S.ch.m0 < 3) {
         const int64_t row = (int64_t)p.hv * DV;
-        const auto hist = GDN_GV((const __nv_bfloat16*)a.vhist, (long long)p.n_seq * 3 * row) + (size_t)S.ch.n * 3 * row;
+        const auto hist =
+            GDN_GV((const __nv_bfloat16*)a.vhist, (long long)p.n_seq * 3 * row) + (size_t)S.ch.n * 3 * row;
 #pragma unroll
         for (int j = 0; j < 3; ++j)
 #pragma unroll
@@ -1300,7 +1303,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (to_ckpt-- == 0) {
           to_ckpt = p.ckpt_block / kC - 1;
           if (ck_idx < p.max_ckpt && (i + 1) * kC <= last) {
-            const int32_t cid = GDN_GV(p.ckpt_ids, (long long)p.n_seq * p.max_ckpt)[(size_t)S.ch.n * p.max_ckpt + ck_idx];
+            const int32_t cid =
+                GDN_GV(p.ckpt_ids, (long long)p.n_seq * p.max_ckpt)[(size_t)S.ch.n * p.max_ckpt + ck_idx];
             if (slot_class(cid, p.ck_num_slots) == 0) {
               // quarter rows, 32 bytes per access where the pool's alignment allows
               const auto to = GDN_GV(p.ck_ssm, p.ck_num_slots * slot_n) +

@@ -99,7 +99,8 @@ __global__ void __launch_bounds__(kThr, 1) ssm_decode_ring_kernel(const DecodeAr
     usable = 0;
     for (int k = 0; k < 2 * kCW; ++k) {
       if (k % kCW == warp && (m[k / kCW] >> lane & 1))
-        S.order[GDN_S(usable + __popc(m[k / kCW] & ((1u << lane) - 1)), kMaxListed)] = (uint16_t)(k / kCW * kCons + tid);
+        S.order[GDN_S(usable + __popc(m[k / kCW] & ((1u << lane) - 1)), kMaxListed)] =
+            (uint16_t)(k / kCW * kCons + tid);
       usable += S.count[k];
     }
     __syncthreads();
@@ -125,7 +126,8 @@ __global__ void __launch_bounds__(kThr, 1) ssm_decode_ring_kernel(const DecodeAr
         auto& B = S.bundle[bb];
         auto g2s = [&](void* dst, const void* src, uint32_t bytes, [[maybe_unused]] const void* base,
                        [[maybe_unused]] long long extent) {
-          if (GDN_GBYTES(src, bytes, base, extent) && GDN_SBYTES(dst, bytes, S)) bulk_g2s(dst, src, bytes, &S.bfull[bb]);
+          if (GDN_GBYTES(src, bytes, base, extent) && GDN_SBYTES(dst, bytes, S))
+            bulk_g2s(dst, src, bytes, &S.bfull[bb]);
         };
         const Tconv* hist = reinterpret_cast<const Tconv*>(a.conv) + (size_t)slot * (kW - 1) * a.C;
         const Tact* x = reinterpret_cast<const Tact*>(a.qkv) + (size_t)r * a.C;
@@ -154,7 +156,8 @@ __global__ void __launch_bounds__(kThr, 1) ssm_decode_ring_kernel(const DecodeAr
       if (!ok || *abort_flag) {  // let what was issued land before the memory goes away
         *abort_flag = 1;
         report(a.err, GDN_DEV_ERR_TIMEOUT);
-        for (uint32_t m = n > (uint32_t)STAGES ? n - STAGES : 0; m < n; ++m) mbar_wait(&S.full[m % STAGES], (m / STAGES) & 1);
+        for (uint32_t m = n > (uint32_t)STAGES ? n - STAGES : 0; m < n; ++m)
+          mbar_wait(&S.full[m % STAGES], (m / STAGES) & 1);
         for (uint32_t m = vk > 2 ? vk - 2 : 0; m < vk; ++m) mbar_wait(&S.bfull[m & 1], (m >> 1) & 1);
       }
     }

@@ -10,8 +10,8 @@ from test_gpu_debug_bounds import _child, debug_lib  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
-FILES = ["test_gpu_ssm.py", "test_gpu_ssm_paths.py", "test_gpu_ssm_decode_paths.py", "test_gpu_add_rmsnorm.py", "test_gpu_batch_maps.py",
-         "test_gpu_serving_step.py"]
+FILES = ["test_gpu_ssm.py", "test_gpu_ssm_paths.py", "test_gpu_ssm_decode_paths.py", "test_gpu_add_rmsnorm.py",
+         "test_gpu_batch_maps.py", "test_gpu_serving_step.py"]
 
 
 def test_state_space_norm_and_maps_under_the_checked_build(debug_lib):  # noqa: F811

@@ -34,7 +34,8 @@ class Loop:
         dev = lambda t: t.cuda()
         self.w_norm = dev(1 + 0.1 * torch.randn(D, generator=g))
         self.w_gate = dev(1 + 0.1 * torch.randn(sh.dv, generator=g))
-        self.proj = dev((torch.randn((D, sh.channels + sh.hv + sh.hv * sh.dv), generator=g) / D ** 0.5).to(sh.act_dtype))
+        cols = sh.channels + sh.hv + sh.hv * sh.dv
+        self.proj = dev((torch.randn((D, cols), generator=g) / D ** 0.5).to(sh.act_dtype))
         self.back = dev((torch.randn((sh.hv * sh.dv, D), generator=g) / (sh.hv * sh.dv) ** 0.5).to(sh.act_dtype))
         n_ids = n_seq * MAX_BLOCKS
         self.ck, self.ock = st.ckpt_pool(n_ids)
@@ -132,7 +133,8 @@ def test_prefix_resumed_from_its_checkpoint(cuda, name):
     L.x.copy_(torch.randn((190, D), generator=st.gen))
     L.step(False)
     qkv, a, whole = L.qkv, L.a, L.out.clone()
-    gdn.slot_copy(st.dims, L.ck, st.pool, L.table[0, 1:2].contiguous(), torch.tensor([2], dtype=torch.int32, device="cuda"))
+    gdn.slot_copy(st.dims, L.ck, st.pool, L.table[0, 1:2].contiguous(),
+                  torch.tensor([2], dtype=torch.int32, device="cuda"))
     out = torch.empty((62, sh.hv, sh.dv), dtype=sh.act_dtype, device="cuda")
     size = gdn.ssm_prefill_workspace_size(st.dims, 1, 62)
     gdn.ssm_prefill(st.dims, st.pool, None, st.params, torch.tensor([2], dtype=torch.int32, device="cuda"),
@@ -176,4 +178,5 @@ def test_captured_decode_loop(cuda, name):
         for k in ("out", "h", "q8", "sc", "cu", "table", "n_free", "starts", "slot", "pos", "ckpt", "err"):
             assert torch.equal(getattr(one, k).view(torch.uint8), getattr(two, k).view(torch.uint8)), (t, k)
         assert torch.equal(one.st.pool.ssm, two.st.pool.ssm)
-    assert int(one.err.item()) == 0 and (one.table[:, 1] >= 0).all() and int(one.n_free.item()) == n * MAX_BLOCKS - 2 * n
+    assert int(one.err.item()) == 0 and (one.table[:, 1] >= 0).all()
+    assert int(one.n_free.item()) == n * MAX_BLOCKS - 2 * n
