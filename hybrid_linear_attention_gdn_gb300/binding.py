@@ -298,6 +298,12 @@ def _require(fn: str, what: str, t, dtype, shape, device: int):
     raise GdnError(fn, ERR_INVALID_ARG, f"{what} is on {t.device}, not on the current CUDA device")
 
 
+def _require_err(fn: str, t, device: int):
+    if t is not None and (t.element_size() != 4 or not t.numel() or t.get_device() != device):
+        raise GdnError(fn, ERR_INVALID_ARG, f"dev_err must be a 32-bit word on the current CUDA device, got {t.dtype} "
+                                            f"{tuple(t.shape)} on {t.device}")
+
+
 def _device() -> int:
     """The current CUDA device (-2 without one: no tensor is on it)."""
     if torch.cuda.is_initialized() or torch.cuda.is_available():
@@ -577,6 +583,7 @@ def ssm_decode_step(dims: Dims, pool: StatePool, params: SsmParams, slot_ids, qk
     _require(fn, "qkv", qkv, act, (B, dims.channels), dev)
     _require(fn, "a", a, act, (B, dims.hv), dev)
     _require(fn, "out", out, act, (B, dims.hv, dims.dv), dev)
+    _require_err(fn, dev_err, dev)
     cd, cp = dims.c(), params.c()
     st = L.gdn_ssm_decode_step(ctypes.byref(cd), pool.c(), ctypes.byref(cp), _ptr(slot_ids), B, _ptr(qkv), _ptr(a),
                                _ptr(out), _ptr(dev_err), _stream(stream))
@@ -612,6 +619,7 @@ def ssm_prefill(dims: Dims, pool: StatePool, ckpt: StatePool | None, params: Ssm
     _require(fn, "out", out, act, (total, dims.hv, dims.dv), dev)
     if workspace is not None:
         _require(fn, "workspace", workspace, workspace.dtype, workspace.shape, dev)
+    _require_err(fn, dev_err, dev)
     cd, cp = dims.c(), params.c()
     ck = ckpt.c() if ckpt is not None else CPool(None, None, 0)
     st = L.gdn_ssm_prefill(ctypes.byref(cd), pool.c(), ck, ctypes.byref(cp), _ptr(slot_ids), _ptr(cu_seqlens),
@@ -688,6 +696,7 @@ def batch_maps(new_lens, start_pos, block: int, block_table, free_ids, n_free, c
         _require(fn, "positions", positions, i64, (rows,), dev)
     if slot_map is not None:
         _require(fn, "slot_map", slot_map, i64, (rows,), dev)
+    _require_err(fn, dev_err, dev)
     st = L.gdn_batch_maps(_ptr(new_lens), _ptr(start_pos), n_seq, int(block), _ptr(block_table),
                           int(block_table.shape[-1]), _ptr(free_ids), free_ids.numel(), _ptr(n_free),
                           _ptr(n_free_out), _ptr(cu_seqlens), _ptr(ckpt_ids), max_ckpt, _ptr(seq_ids),

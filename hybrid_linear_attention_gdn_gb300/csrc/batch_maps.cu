@@ -12,7 +12,7 @@
 // finding its request by a binary search in the offsets.  The cluster
 // barrier stands only between the last read of *n_free and its update, which
 // may be in place.
-#include "gdn_common.cuh"
+#include "ssm.cuh"  // allow_smem
 
 namespace gdn {
 namespace {
@@ -212,8 +212,7 @@ extern "C" gdn_status gdn_batch_maps(const int32_t* new_lens, const int64_t* sta
   m.max_tokens = max_tokens;
   m.err = dev_err;
   const size_t smem = (2 * (size_t)n_seq + 1) * sizeof(int32_t);
-  cudaError_t e = cudaFuncSetAttribute(batch_maps_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (2 * kMaxSeq + 1) * (int)sizeof(int32_t));
+  cudaError_t e = ssm::allow_smem<batch_maps_kernel>((2 * kMaxSeq + 1) * sizeof(int32_t));
   if (e == cudaSuccess)
     e = launch_pdl(batch_maps_kernel, dim3(kCluster), dim3(kThreads), smem, reinterpret_cast<cudaStream_t>(stream),
                    dim3(kCluster), m);

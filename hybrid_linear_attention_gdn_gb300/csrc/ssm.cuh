@@ -18,6 +18,20 @@ __device__ __forceinline__ Gate gate(float A_log, float dt_bias, float a) {
   return r;
 }
 
+// Kernel K's dynamic shared memory limit, raised on its first launch on a
+// device (`bytes` the same on every call).
+template <auto K>
+cudaError_t allow_smem(size_t bytes) {
+  static bool done[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const bool known = dev >= 0 && dev < 64;
+  if (known && done[dev]) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (known && e == cudaSuccess) done[dev] = true;
+  return e;
+}
+
 struct DecodeArgs {
   float* ssm;
   void* conv;

@@ -1393,12 +1393,12 @@ cudaError_t launch_chain(const ChunkArgs& a, const Layout& l, const CUtensorMap&
   const dim3 grid(tiles, (unsigned)l.n_segs), all(tiles, (unsigned)(l.n_segs + hist_rows(a.p.n_seq, a.p.C, tiles)));
   cudaError_t e;
   if (l.seg_chunks < l.n_chunks) {
-    auto k = ssm_chain_kernel<NH, true>;
-    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+    constexpr auto k = ssm_chain_kernel<NH, true>;
+    if ((e = ssm::allow_smem<k>(smem)) != cudaSuccess) return e;
     if ((e = launch_pdl(k, grid, dim3(kThreads), smem, s, dim3(1), a, xmap)) != cudaSuccess) return e;
   }
-  auto k = ssm_chain_kernel<NH, false>;
-  if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+  constexpr auto k = ssm_chain_kernel<NH, false>;
+  if ((e = ssm::allow_smem<k>(smem)) != cudaSuccess) return e;
   return launch_pdl(k, all, dim3(kThreads), smem, s, dim3(1), a, xmap);
 }
 
@@ -1466,9 +1466,7 @@ cudaError_t ssm_chunk_launch(const ssm::PrefillArgs& p, const gdn_dims& d, void*
   if ((e = tensor_map_2d(&xmap, p.qkv, p.total, p.C, 2, 128, kRawRows, CU_TENSOR_MAP_SWIZZLE_NONE)) != cudaSuccess)
     return e;
   const size_t smem = sizeof(FeatSmem) + 1024;
-  if ((e = cudaFuncSetAttribute(ssm_features_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
-      cudaSuccess)
-    return e;
+  if ((e = ssm::allow_smem<ssm_features_kernel>(smem)) != cudaSuccess) return e;
   const unsigned walks = (unsigned)((l.n_chunks + a.feat_chunks - 1) / a.feat_chunks);
   if ((e = launch_pdl(ssm_features_kernel, dim3(walks + (unsigned)p.n_seq, (unsigned)p.hk), dim3(kFT), smem, s, dim3(1),
                       a, xmap)) != cudaSuccess)

@@ -300,8 +300,8 @@ cudaError_t launch(const DecodeArgs& a, cudaStream_t s) {
   static_assert(sizeof(B) % 16 == 0 && offsetof(B, x) % 16 == 0 && offsetof(B, w) % 16 == 0 &&
                     offsetof(B, bias) % 16 == 0 && offsetof(SM, bundle) % 16 == 0 && offsetof(SM, qk) % 16 == 0,
                 "copies and vectors start 16-byte aligned");
-  auto k = ssm_decode_ring_kernel<Tact, Tconv, STAGES>;
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SM));
+  constexpr auto k = ssm_decode_ring_kernel<Tact, Tconv, STAGES>;
+  const cudaError_t e = allow_smem<k>(sizeof(SM));
   if (e != cudaSuccess) return e;
   const int items = a.B * a.hk, sms = sm_count();
   return launch_pdl(k, dim3((unsigned)(items < sms ? items : sms)), dim3(kThr), sizeof(SM), s, dim3(1), a);

@@ -220,3 +220,34 @@ def test_no_tokens(cuda):
     gdn.ssm_decode_step(st.dims, st.pool, st.params, _i32([]), e(0, sh.channels), e(0, sh.hv), e(0, sh.hv, sh.dv))
     torch.cuda.synchronize()
     assert torch.equal(st.pool.ssm, before[0]) and torch.equal(st.pool.conv, before[1])
+
+
+def test_refusals_next_to_a_gpu(cuda):
+    """Host tensors, short or missing workspaces and wrong error words are
+    refused before anything is launched."""
+    sh = shape("wide")
+    st = SsmSetup(sh, seed=43)
+    qkv, a = (t.cuda() for t in st.tokens(100))
+    out = torch.empty((100, sh.hv, sh.dv), dtype=sh.act_dtype, device="cuda")
+    size = gdn.ssm_prefill_workspace_size(st.dims, 1, 100)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    sp = torch.tensor([0], device="cuda")
+    good = dict(ids=_i32([1]), cu=_i32([0, 100]), sp=sp, ck=None, ck_ids=None, block=64, qkv=qkv, a=a, out=out, ws=ws,
+                err=_i32([0]))
+    before, n0 = st.pool.ssm.clone(), binding.launch_counts()
+    for bad in (dict(ids=torch.tensor([1], dtype=torch.int32)), dict(cu=_i32([0, 100]).cpu()), dict(sp=sp.cpu()),
+                dict(sp=sp.int()), dict(ws=None), dict(ws=ws[:-1]), dict(ws=ws[1:]), dict(ws=ws.cpu()), dict(block=0),
+                dict(block=96), dict(err=torch.zeros(1, dtype=torch.int32)), dict(err=sp), dict(qkv=qkv.cpu()),
+                dict(out=out.transpose(1, 2)), dict(a=a[:99]), dict(ck_ids=_i32([[0]]))):
+        k = {**good, **bad}
+        with pytest.raises(gdn.GdnError) as e:
+            gdn.ssm_prefill(st.dims, st.pool, k["ck"], st.params, k["ids"], k["cu"], k["sp"], 100, k["ck_ids"],
+                            k["block"], k["qkv"], k["a"], k["out"], k["ws"], k["err"])
+        assert e.value.status == binding.ERR_INVALID_ARG, bad
+    with pytest.raises(gdn.GdnError):
+        gdn.ssm_decode_step(st.dims, st.pool, st.params, _i32([1]), qkv[:1], a[:1], out[:1], good["err"].cpu())
+    with pytest.raises(gdn.GdnError):
+        gdn.ssm_decode_step(st.dims, st.pool, SsmParams(*(getattr(st.params, k).cpu() for k in
+                                                          ("conv_w", "conv_bias", "A_log", "dt_bias", "D"))),
+                            _i32([1]), qkv[:1], a[:1], out[:1])
+    assert binding.launch_counts() == n0 and torch.equal(st.pool.ssm, before)
