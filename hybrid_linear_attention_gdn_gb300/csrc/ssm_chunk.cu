@@ -12,7 +12,7 @@
 //
 // features kernel (chunk, group): conv1d + SiLU of the group's q and k
 //   channels once instead of once per head, and G = Q K^T, written in the
-//   chain kernel's operand layouts (80 KB per chunk and group, read back
+//   chain kernel's operand layouts (56 KB per chunk and group, read back
 //   through L2 by the heads of the group, whose chains run side by side).
 // chain kernel (128 V channels = one head of 128 or two of 64; sequence or
 //   segment of one): walks its chunks in order, V rows in the tensor core's
@@ -35,7 +35,11 @@
 //   products.
 // The work per 64 x 128 V values is bound by the instructions of the
 // elementwise steps (conv + SiLU, P, operand conversion), not by the products
-// or by memory.
+// (tensor pipe 24 % busy) or by memory.  Measured, 64 heads of 64 in 8 groups:
+// 4 x 8192 tokens 446 us (features 84, chain 362: 2.8 us per chunk; 112 us of
+// memory traffic), seven ragged sequences of 3,968 tokens 140 us, 37 tokens 21
+// us in a graph; 32 heads in one group, 1 x 8192 tokens 100 us (features 10,
+// states of 8 segments 36, chains 54).
 //
 // Segments: where sequences times V tiles are too few for the SMs, each
 // sequence is cut into segments of seg_chunks chunks.  A first launch walks
@@ -161,8 +165,10 @@ __device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
 // features of q and k, G = Q K^T
 // ---------------------------------------------------------------------------
 // A CTA of 256 threads walks feat_chunks consecutive chunk slots of one group;
-// a thread has a channel pair and half of the chunk's tokens.  HBM bound: 67 x
-// 512 bytes in, 56 KB out.  The next chunk's raw rows arrive by TMA while the
+// a thread has a channel pair and half of the chunk's tokens.  67 x 512 bytes
+// in, 56 KB out: 84 us for 4 x 8192 tokens of 8 groups, 0.65 of the copy
+// bandwidth (issue slots 43 % busy; one chunk per CTA, its rows not requested
+// ahead, took 108).  The next chunk's raw rows arrive by TMA while the
 // last ones' features, already in registers, are worked on.  q and k stand
 // one above the other as one 128-row operand, so that one product of M = 128
 // gives G in its upper half.
@@ -455,13 +461,18 @@ static_assert(offsetof(FeatSmem, meta) == offsetof(FeatSmem, g) + kGBytes &&
 //   21, 22   gates and scales of one head each
 //   23       loader: the copies of raw V rows and G, the three rows before a
 //            sequence from the conv history, and the largest raw input
-// What bounds a chunk is the one-after-the-other of a compute warp's steps,
-// not the products: leaving out half of dS^T's changed nothing.
+// What bounds a chunk is instruction issue: 3,400 instructions per scheduler
+// and chunk, 75 % of its slots.  It is not the products: leaving out half of
+// dS^T's changed nothing.  With P in the compute warps 4 x 8192 tokens took 468
+// us instead of 446.
 constexpr int kCompute = 512, kAux = 128;  // threads
 constexpr int kIssuer = (kCompute + kAux) / 32, kLoader = kIssuer + 3;
 constexpr int kThreads = 32 * (kLoader + 1);
 // Registers per thread after the split of the launch's 768 x 80.  Spills cost
-// more here than elsewhere: shared memory leaves little of the L1 cache.
+// more here than elsewhere: shared memory leaves little of the L1 cache (96 /
+// 56 / 40, with 64 bytes of the issuer's and the loader's spilled, 521 us for
+// 4 x 8192 tokens; 88 / 64 / 64, with the compute warps', 445, but 4 % slower
+// on the ragged sequences).
 constexpr int kComputeRegs = 96, kAuxRegs = 48, kHelpRegs = 48;
 static_assert(kCompute * kComputeRegs + kAux * kAuxRegs + 128 * kHelpRegs <= kThreads * 80,
               "no more than the launch's registers");
