@@ -18,8 +18,11 @@
 // with loads in flight on every SM.  The same code with element accesses
 // takes any alignment and any d.
 //
-// Measured: 32768 rows of 4096, bf16 with an fp32 residual, y and q8: 248 us,
-// 1.04 of the copy bandwidth (1.75 GB); 64 rows 3.5 us in a graph of calls.
+// Measured: 32768 rows of 4096, bf16 with an fp32 residual, y and q8: 256 us,
+// 1.00 of the copy bandwidth (1.75 GB), with a bf16 residual 208 us (0.86);
+// 64 rows 3.6 us in a graph of calls.  With the rare exact path inlined they
+// took 280 and 248 us, its registers costing a CTA per SM; at 4 or 6 CTAs of
+// 256 threads instead of 5, 255 and 223 or 306 and 207.
 #include "gdn_common.cuh"
 
 #include <cuda_fp8.h>
@@ -40,74 +43,150 @@ struct NormArgs {
   int32_t group, scale_type;
 };
 
-// 8 consecutive elements from p[0], as fp32; VEC: p is 16-byte aligned and
-// all 8 exist, else the first n of them (the others 0)
-template <bool VEC, typename T, typename VT>
-__device__ __forceinline__ void load8(float (&f)[8], const VT& p, int64_t at, int n) {
-  if constexpr (!VEC) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = i < n ? to_f32(p[at + i]) : 0.f;
-  } else if constexpr (sizeof(T) == 4) {
-    const float4 u = vec_at<const float4>(p, at), v = vec_at<const float4>(p, at + 4);
-    f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w;
-    f[4] = v.x; f[5] = v.y; f[6] = v.z; f[7] = v.w;
-  } else {
-    const uint4 u = vec_at<const uint4>(p, at);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
-      f[2 * i] = v.x;
-      f[2 * i + 1] = v.y;
-    }
+// 8 consecutive elements as they are stored
+template <typename T>
+struct Vec8 {
+  uint32_t w[2 * sizeof(T)];
+  __device__ __forceinline__ float2 pair(int i) const {  // elements 2 i, 2 i + 1
+    if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
-}
-template <bool VEC, typename T, typename VT>
-__device__ __forceinline__ void store8(const float (&f)[8], const VT& p, int64_t at, int n) {
-  if constexpr (!VEC) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[at + i] = from_f32<T>(f[i]);
-  } else if constexpr (sizeof(T) == 4) {
-    vec_at<float4>(p, at) = make_float4(f[0], f[1], f[2], f[3]);
-    vec_at<float4>(p, at + 4) = make_float4(f[4], f[5], f[6], f[7]);
-  } else {
-    uint4 u;
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+  __device__ __forceinline__ void put(int i, float2 x) {  // rounded to nearest even
+    if constexpr (sizeof(T) == 4) {
+      w[2 * i] = __float_as_uint(x.x);
+      w[2 * i + 1] = __float_as_uint(x.y);
+    } else {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
       w[i] = *reinterpret_cast<const uint32_t*>(&b);
     }
-    u.x = w[0]; u.y = w[1]; u.z = w[2]; u.w = w[3];
-    vec_at<uint4>(p, at) = u;
+  }
+};
+// from p[at]; VEC: p + at is 16-byte aligned and all 8 exist, else the first
+// n of them (the others 0)
+template <bool VEC, typename T, typename VT>
+__device__ __forceinline__ void load8(Vec8<T>& f, const VT& p, int64_t at, int n) {
+  if constexpr (VEC) {
+    constexpr int kPer = 16 / sizeof(T);  // elements of a 16-byte access
+#pragma unroll
+    for (int i = 0; i < 8 / kPer; ++i) {
+      const uint4 u = vec_at<const uint4>(p, at + i * kPer);
+      f.w[4 * i] = u.x; f.w[4 * i + 1] = u.y; f.w[4 * i + 2] = u.z; f.w[4 * i + 3] = u.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      f.put(i, make_float2(2 * i < n ? to_f32(p[at + 2 * i]) : 0.f, 2 * i + 1 < n ? to_f32(p[at + 2 * i + 1]) : 0.f));
+  }
+}
+template <bool VEC, typename T, typename VT>
+__device__ __forceinline__ void store8(const Vec8<T>& f, const VT& p, int64_t at, int n) {
+  if constexpr (VEC) {
+    constexpr int kPer = 16 / sizeof(T);
+#pragma unroll
+    for (int i = 0; i < 8 / kPer; ++i)
+      vec_at<uint4>(p, at + i * kPer) = make_uint4(f.w[4 * i], f.w[4 * i + 1], f.w[4 * i + 2], f.w[4 * i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = f.pair(i);
+      if (2 * i < n) p[at + 2 * i] = from_f32<T>(x.x);
+      if (2 * i + 1 < n) p[at + 2 * i + 1] = from_f32<T>(x.y);
+    }
   }
 }
 
-// the larger of two magnitudes, NaN if either is (fmaxf would drop it)
-__device__ __forceinline__ float amax2(float a, float b) { return (a > b || a != a) ? a : b; }
+// a magnitude's bits: their order is that of the values, with NaN above all
+__device__ __forceinline__ uint32_t mag(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 add2(float2 x, float2 y) { return fma2(x, both(1.f), y); }
+__device__ __forceinline__ float2 sub2(float2 x, float2 y) { return fma2(y, both(-1.f), x); }
+__device__ __forceinline__ uint32_t e4m3x2(float2 x) {
+  return __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+}
 
-// the scale of a group whose largest |y| is m, stored at index `at`; returns
+// q8 is the e4m3 value nearest to y / scale before either was rounded.  The
+// norm cancels from that quotient: it is 448 (h w) / max|h w|.  y times the
+// scale's reciprocal is within 8 fp32 steps of it, so where 2^-20 more and
+// 2^-20 less round to the same e4m3 value, that is it; else (some thirty
+// values in a million) the quotient is taken exactly: from p = h w and the
+// error e of that and of h, and those of the group's largest, m and me.  (The
+// product alone put some ten values in a million on the wrong side.)
+// 448 (p + e) / (m + me): the value in fp32 towards zero, its last bit set
+// where something is left, so that rounding to e4m3 is the only rounding
+__device__ __forceinline__ float quotient(float p, float e, float m, float me, float im) {
+  const float t = p * im, r = fmaf(-t, m, p) + fmaf(-t, me, e), dt = r * im * 448.f;
+  const float z = fmaf(448.f, t, dt), rest = fmaf(448.f, t, -z) + dt;
+  const uint32_t u = __float_as_uint(z);
+  if (rest == 0.f) return z;
+  return __uint_as_float((u - ((u ^ __float_as_uint(rest)) >> 31)) | 1u);
+}
+
+// Four pairs of a vector: the sums h, what their rounding lost, the weights.
+struct Four {
+  float2 h[4];
+  uint32_t lost[4];
+  float2 g[4];
+  float i2;
+  __device__ __forceinline__ float2 product(int i) const { return mul2(mul2(h[i], both(i2)), g[i]); }  // h w
+  // what the roundings of the sum and of the product p left
+  __device__ __forceinline__ float2 error(int i, float2 p) const {
+    const float2 e = make_float2(__uint_as_float(lost[i] << 16), __uint_as_float(lost[i] & 0xffff0000u));
+    return fma2(mul2(e, both(i2)), g[i], fma2(mul2(h[i], both(i2)), g[i], mul2(p, both(-1.f))));
+  }
+  // the error of the largest, |h w| = m: of several the largest in its direction
+  __device__ __forceinline__ float error_of(uint32_t m, float me) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 p = product(i);
+      if (mag(p.x) != m && mag(p.y) != m) continue;
+      const float2 e = error(i, p);
+      if (mag(p.x) == m) me = fmaxf(me, p.x < 0.f ? -e.x : e.x);
+      if (mag(p.y) == m) me = fmaxf(me, p.y < 0.f ? -e.y : e.y);
+    }
+    return me;
+  }
+};
+constexpr float kNone = -3.4e38f;  // no error yet
+
+// The exact values of a vector, by all lanes of a warp; gl: lanes of a group
+// that find me themselves, or 0.  Not inlined: it is rare, and what it needs
+// would take registers (and with them CTAs) from every row.
+__device__ __noinline__ uint2 exact_q8(const Four f, uint32_t mu, float me, int gl) {
+  if (gl) {
+    me = f.error_of(mu, kNone);
+    for (int o = 1; o < gl; o <<= 1) me = fmaxf(me, __shfl_xor_sync(0xffffffffu, me, o));
+  }
+  const float m = __uint_as_float(mu), im = 1.f / m;
+  uint32_t q[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = f.product(i), e = f.error(i, p);
+    q[i >> 1] |= e4m3x2(make_float2(quotient(p.x, e.x, m, me, im), quotient(p.y, e.y, m, me, im))) << (16 * (i & 1));
+  }
+  return make_uint2(q[0], q[1]);
+}
+
+// the scale of a group whose largest |y| is top, stored at index `at`; returns
 // 1 / scale (0 only for an infinite scale).  e4m3's largest value is 448.
-__device__ __forceinline__ float put_scale(const NormArgs& a, float m, int64_t at, int64_t n_scales, bool store) {
+__device__ __forceinline__ float put_scale(const NormArgs& a, float top, int64_t at, int64_t n_scales, bool store) {
   if (a.scale_type == GDN_SCALE_F32) {
     // at least 2^-126: a smaller scale's reciprocal could overflow
-    float s = m == 0.f ? 1.f : m / 448.f;
+    float s = top == 0.f ? 1.f : top * (1.f / 448.f);
     s = s < 1.17549435e-38f ? 1.17549435e-38f : s;
     if (store) GDN_GV(reinterpret_cast<float*>(a.scales), n_scales)[at] = s;
-    return 1.f / s;
+    return __fdividef(1.f, s);
   }
-  // byte b stands for 2^(b - 127): the smallest with 448 * 2^(b - 127) >= m
+  // byte b stands for 2^(b - 127): the smallest with 448 * 2^(b - 127) >= top
   int b = 127;
-  if (m != m) {
+  if (top != top) {
     b = 255;
-  } else if (m > 0.f) {
-    const float s = m / 448.f;
+  } else if (top > 0.f) {
+    const float s = top / 448.f;
     const uint32_t u = __float_as_uint(s);
     // the exponent, rounded up; byte 0 is the subnormal 2^-127
     b = u > 0x400000u ? (int)(u >> 23) + ((u & 0x7fffffu) ? 1 : 0) : 0;
-    // the division may have rounded down onto a power of two below m / 448
-    if (b < 254 && b > 0 && 448.f * __uint_as_float((uint32_t)b << 23) < m) ++b;
+    // the division may have rounded down onto a power of two below top / 448
+    if (b < 254 && b > 0 && 448.f * __uint_as_float((uint32_t)b << 23) < top) ++b;
     b = b > 254 ? 254 : b;
   }
   if (store) GDN_GV(reinterpret_cast<uint8_t*>(a.scales), n_scales)[at] = (uint8_t)b;
@@ -117,10 +196,10 @@ __device__ __forceinline__ float put_scale(const NormArgs& a, float m, int64_t a
 }
 
 // TPR threads per row, ROWS rows per CTA
-template <typename Tact, typename Tres, int TPR, int ROWS, int V, bool VEC>
-__global__ void __launch_bounds__(TPR* ROWS) add_rmsnorm_kernel(const NormArgs a) {
+template <typename Tact, typename Tres, int TPR, int ROWS, int V, bool VEC, bool ROWSCALE>
+__global__ void __launch_bounds__(TPR* ROWS, TPR* ROWS >= 1024 ? 1 : 1280 / (TPR * ROWS)) add_rmsnorm_kernel(const NormArgs a) {
   constexpr int kRowWarps = TPR / 32;
-  __shared__ float red[ROWS][32];
+  __shared__ uint32_t red[ROWS][32];
   pdl_wait();
   pdl_trigger();
   const int t = threadIdx.x % TPR, rloc = threadIdx.x / TPR, lane = threadIdx.x & 31;
@@ -130,118 +209,179 @@ __global__ void __launch_bounds__(TPR* ROWS) add_rmsnorm_kernel(const NormArgs a
   const auto x = GDN_GV(reinterpret_cast<const Tact*>(a.x), n);
   const auto res = GDN_GV(reinterpret_cast<Tres*>(a.residual), n);
   const auto w = GDN_GV(a.weight, a.d);
-  float h[V][8];
-  float ss = 0.f;
-  if (live) {
-    float r[V][8];
+  float2 h[V][4];      // x + residual
+  uint32_t lost[V][4];  // what its rounding lost, as bf16 pairs
+  {
+    Vec8<Tact> xv[V];
+    Vec8<Tres> rv[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = 8 * (v * TPR + t);
-      if (c < a.d) {
-        load8<VEC, Tact>(h[v], x, base + c, a.d - c);
-        if (a.residual) load8<VEC, Tres>(r[v], res, base + c, a.d - c);
+#pragma unroll
+      for (auto& u : xv[v].w) u = 0u;
+#pragma unroll
+      for (auto& u : rv[v].w) u = 0u;
+      if (live && c < a.d) {
+        load8<VEC>(xv[v], x, base + c, a.d - c);
+        if (a.residual) load8<VEC>(rv[v], res, base + c, a.d - c);
       }
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = 8 * (v * TPR + t);
-      if (c < a.d) {
-        if (a.residual) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) h[v][i] += r[v][i];
-          store8<VEC, Tres>(h[v], res, base + c, a.d - c);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(h[v][i], h[v][i], ss);
+      for (int i = 0; i < 4; ++i) {
+        const float2 xi = xv[v].pair(i), ri = rv[v].pair(i), s = add2(xi, ri), b = sub2(s, xi);
+        const float2 e = add2(sub2(xi, sub2(s, b)), sub2(ri, b));
+        const __nv_bfloat162 eb = __floats2bfloat162_rn(e.x, e.y);
+        h[v][i] = s;
+        lost[v][i] = *reinterpret_cast<const uint32_t*>(&eb);
+        rv[v].put(i, s);
       }
+      if (a.residual && live && c < a.d) store8<VEC>(rv[v], res, base + c, a.d - c);
     }
   }
+  float2 ss2 = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  if (kRowWarps > 1) {
-    if (lane == 0) red[rloc][t >> 5] = ss;
-    __syncthreads();
-    ss = lane < kRowWarps ? red[rloc][lane] : 0.f;
+  for (int v = 0; v < V; ++v)
 #pragma unroll
-    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  }
-  const float inv = 1.f / sqrtf(ss / (float)a.d + a.eps);
-  float top = 0.f;  // the row's largest |y| (one scale per row)
-  if (live) {
+    for (int i = 0; i < 4; ++i) ss2 = fma2(h[v][i], h[v][i], ss2);
+  // over the row's threads
+  auto row_all = [&](auto m, auto join) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = 8 * (v * TPR + t);
-      if (c < a.d) {
-        float g[8];
-        load8<VEC, float>(g, w, c, a.d - c);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          h[v][i] = h[v][i] * inv * g[i];
-          top = amax2(fabsf(h[v][i]), top);
-        }
-        if (a.y) store8<VEC, Tact>(h[v], GDN_GV(reinterpret_cast<Tact*>(a.y), n), base + c, a.d - c);
-      }
-    }
-  }
-  if (!a.q8) return;
-  const int64_t per_row = a.group ? a.d / a.group : 1, n_scales = a.n_rows * per_row;
-  float scale_inv = 0.f;
-  if (a.group == 0) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = amax2(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (kRowWarps > 1) {
+    for (int o = 16; o; o >>= 1) m = join(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if constexpr (kRowWarps > 1) {
+      auto* const part = reinterpret_cast<decltype(m)*>(red[rloc]);
       __syncthreads();  // red has been read
-      if (lane == 0) red[rloc][t >> 5] = top;
+      if (lane == 0) part[t >> 5] = m;
       __syncthreads();
-      top = lane < kRowWarps ? red[rloc][lane] : 0.f;
+      m = part[lane % kRowWarps];
 #pragma unroll
-      for (int o = 16; o; o >>= 1) top = amax2(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int o = kRowWarps / 2; o; o >>= 1) m = join(m, __shfl_xor_sync(0xffffffffu, m, o));
     }
-    if (live) scale_inv = put_scale(a, top, row, n_scales, t == 0);
+    return m;
+  };
+  const float ss = row_all(ss2.x + ss2.y, [](float p, float q) { return p + q; });
+  const float inv = 1.f / sqrtf(ss / (float)a.d + a.eps);
+  // inv = i2 c2 with a power of two i2, so that h i2 w neither overflows nor
+  // vanishes before it is scaled
+  const uint32_t ib = __float_as_uint(inv);
+  const bool normal = inv > 1.17549435e-38f && inv < 3.4e38f;
+  const float i2 = normal ? __uint_as_float(ib & 0x7f800000u) : inv;
+  const float c2 = normal ? __uint_as_float((ib & 0x7fffffu) | 0x3f800000u) : 1.f;
+  auto four = [&](int v, const Vec8<float>& g) {
+    Four f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f.h[i] = h[v][i];
+      f.lost[i] = lost[v][i];
+      f.g[i] = g.pair(i);
+    }
+    f.i2 = i2;
+    return f;
+  };
+  const int64_t per_row = a.group ? a.d / a.group : 1, n_scales = a.n_rows * per_row;
+  uint32_t top = 0;  // the row's largest |h w| (one scale per row)
+  float row_inv = 0.f;
+  // f(v, the vector's column, its four pairs) for this thread's vectors
+  auto vectors = [&](auto f) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = 8 * (v * TPR + t);
+      if (live && c < a.d) {
+        Vec8<float> g;
+        load8<VEC>(g, w, c, a.d - c);
+        f(v, c, four(v, g));
+      }
+    }
+  };
+  if constexpr (ROWSCALE) {
+    vectors([&](int, int, const Four& f) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = max(top, max(mag(f.product(i).x), mag(f.product(i).y)));
+    });
+    top = row_all(top, [](uint32_t p, uint32_t q) { return max(p, q); });
+    if (live) row_inv = put_scale(a, __uint_as_float(top) * c2, row, n_scales, t == 0);
   }
   const auto q8 = GDN_GV(a.q8, n);
   const int gl = a.group / 8;  // lanes of a group
+  auto put_q8 = [&](int c, uint2 q) {
+    if constexpr (VEC) {
+      vec_at<uint2>(q8, base + c) = q;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < a.d - c) q8[base + c + i] = (uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
+    }
+  };
+  uint32_t open = 0;  // one scale per row: the vectors whose values are still to be taken exactly
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int c = 8 * (v * TPR + t);
     const bool in = live && c < a.d;
-    float inv_s = scale_inv;
-    if (a.group) {
-      float m = 0.f;
-      if (in) {
+    Vec8<float> g = {};
+    if (in) load8<VEC>(g, w, c, a.d - c);
+    const Four f = four(v, g);
+    float2 p[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = amax2(fabsf(h[v][i]), m);
-      }
+    for (int i = 0; i < 4; ++i) p[i] = f.product(i);
+    if (a.y && in) {
+      Vec8<Tact> y;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float u = __shfl_xor_sync(0xffffffffu, m, o);
-        if (o < gl) m = amax2(m, u);
-      }
-      if (in) inv_s = put_scale(a, m, row * per_row + c / a.group, n_scales, t % gl == 0);
+      for (int i = 0; i < 4; ++i) y.put(i, mul2(p[i], both(c2)));
+      store8<VEC>(y, GDN_GV(reinterpret_cast<Tact*>(a.y), n), base + c, a.d - c);
     }
-    if (!in) continue;
-    uint32_t q[2] = {0u, 0u};
+    if (!a.q8) continue;
+    uint32_t mu = top;
+    float inv_s = row_inv;
+    if constexpr (!ROWSCALE) {
+      mu = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mu = max(mu, max(mag(p[i].x), mag(p[i].y)));
+      for (int o = 1; o < gl; o <<= 1) mu = max(mu, __shfl_xor_sync(0xffffffffu, mu, o));
+      if (in) inv_s = put_scale(a, __uint_as_float(mu) * c2, row * per_row + c / a.group, n_scales, t % gl == 0);
+    }
+    const float m = __uint_as_float(mu), k = c2 * inv_s;
+    // (within these the quotient's pieces neither overflow nor vanish)
+    const bool exact = in && a.scale_type == GDN_SCALE_F32 && m > 1e-24f && m < 1e24f;
+    const float2 lo = both(exact ? k * (1.f - 0x1p-20f) : k), hi = both(exact ? k * (1.f + 0x1p-20f) : k);
+    uint32_t q[2] = {0u, 0u}, differ = 0u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 p = make_float2(h[v][2 * i] * inv_s, h[v][2 * i + 1] * inv_s);
-      const uint32_t b = __nv_cvt_float2_to_fp8x2(p, __NV_SATFINITE, __NV_E4M3);
+      const uint32_t b = e4m3x2(mul2(p[i], lo));
       q[i >> 1] |= b << (16 * (i & 1));
+      differ |= b ^ e4m3x2(mul2(p[i], hi));
     }
-    if constexpr (VEC) {
-      vec_at<uint2>(q8, base + c) = make_uint2(q[0], q[1]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < a.d - c) q8[base + c + i] = (uint8_t)(q[i >> 2] >> (8 * (i & 3)));
+    if constexpr (ROWSCALE) {
+      open |= differ ? 1u << v : 0u;
+    } else if (__any_sync(0xffffffffu, differ)) {
+      const uint2 z = exact_q8(f, mu, 0.f, gl);
+      if (differ) {
+        q[0] = z.x;
+        q[1] = z.y;
+      }
     }
+    if (in) put_q8(c, make_uint2(q[0], q[1]));
+  }
+  if constexpr (ROWSCALE) {
+    if (!__syncthreads_or(open)) return;
+    float me = kNone;
+    vectors([&](int, int, const Four& f) { me = f.error_of(top, me); });
+    me = row_all(me, [](float p, float q) { return fmaxf(p, q); });
+    vectors([&](int v, int c, const Four& f) {
+      if (open >> v & 1) put_q8(c, exact_q8(f, top, me, 0));
+    });
   }
 }
 
 template <typename Tact, typename Tres, int TPR, int ROWS, int V>
 cudaError_t launch_norm(const NormArgs& a, bool vec, cudaStream_t s) {
   const dim3 grid((unsigned)((a.n_rows + ROWS - 1) / ROWS)), block(TPR * ROWS);
-  return vec ? launch_pdl(add_rmsnorm_kernel<Tact, Tres, TPR, ROWS, V, true>, grid, block, 0, s, dim3(1), a)
-             : launch_pdl(add_rmsnorm_kernel<Tact, Tres, TPR, ROWS, V, false>, grid, block, 0, s, dim3(1), a);
+  if (a.q8 && a.group == 0)
+    return vec ? launch_pdl(add_rmsnorm_kernel<Tact, Tres, TPR, ROWS, V, true, true>, grid, block, 0, s, dim3(1), a)
+               : launch_pdl(add_rmsnorm_kernel<Tact, Tres, TPR, ROWS, V, false, true>, grid, block, 0, s, dim3(1), a);
+  return vec ? launch_pdl(add_rmsnorm_kernel<Tact, Tres, TPR, ROWS, V, true, false>, grid, block, 0, s, dim3(1), a)
+             : launch_pdl(add_rmsnorm_kernel<Tact, Tres, TPR, ROWS, V, false, false>, grid, block, 0, s, dim3(1), a);
 }
 
 template <typename Tact, typename Tres>

@@ -468,7 +468,9 @@ gdn_status gdn_ssm_prefill(const gdn_dims* dims, gdn_pool pool, gdn_pool ckpt,
  *     GDN_SCALE_E8M0  uint8: 2^(byte - 127), the smallest power of two
  *                     (at least 2^-127) that is >= max|y| / 448; 127 where
  *                     every y is 0
- *   q8 = y / scale rounded to nearest even, at most +-448.  A NaN among a
+ *   q8 = y / scale rounded to nearest even, at most +-448; with an fp32 scale
+ *   that is the exact quotient's nearest value, whatever y's and the scale's
+ *   own roundings (for a largest |y| between 1e-23 and 1e23).  A NaN among a
  *   group's y makes its scale NaN (byte 255) and every q8 of the group NaN.
  * d at most 32768, else GDN_ERR_UNSUPPORTED; n_rows = 0 launches nothing.
  * No alignment beyond the element types' own is required; 16-byte aligned

@@ -134,3 +134,45 @@ def test_rows_of_higher_rank_and_none(cuda):
     assert y.shape == (2, 3, 64) and q8 is None and s is None
     e = gdn.add_rmsnorm(x[:0].cuda(), r[:0].cuda(), w.cuda())[0]
     assert e.shape == (0, 64)
+
+
+def _e4m3(z):
+    """float64 to the nearest e4m3 value, ties to even, at most 448."""
+    m = z.abs().clamp(max=448.0)
+    step = torch.exp2(torch.floor(torch.log2(m.clamp(min=2.0 ** -6))) - 3)
+    return torch.sign(z) * (torch.round(m / step) * step).clamp(max=448.0)
+
+
+@pytest.mark.parametrize("group", [0, 32, 128])
+@pytest.mark.parametrize("act,res", [(BF16, BF16), (BF16, F32), (F32, F32), (BF16, None)])
+def test_q8_is_the_nearest_to_the_exact_quotient(cuda, act, res, group):
+    """The only rounding between y / scale and q8 is q8's: the kernel's
+    quotient is within 2^-40 of the exact one, so that of 2 million values in
+    float64 not one is expected on the other side of a midpoint."""
+    for rows, d in ((512, 4096), (64, 256), (40, 16384)) + (((9, 1001),) if group == 0 else ()):
+        x, r, w = _case(rows, d, act, res, 12 + d)
+        x[1] = x[0]  # equal rows, and in one of them equal largest values
+        x[2, ::2] = x[2, 0]
+        h = x.cuda().double() + (r.cuda().double() if r is not None else 0)
+        p = h * w.cuda().double()
+        gs = group or d
+        top = p.reshape(rows, -1, gs).abs().amax(-1, keepdim=True)
+        z = (448 * p.reshape(rows, -1, gs) / top).reshape(rows, d)
+        q = torch.empty((rows, d), dtype=torch.float8_e4m3fn, device="cuda")
+        gdn.add_rmsnorm(x.cuda(), r.cuda() if r is not None else None, w.cuda(), 1e-6, q8=q, group=group)
+        assert torch.equal(q.double(), _e4m3(z))
+
+
+def test_q8_at_midpoints(cuda):
+    """Quotients that are midpoints go to the even neighbour, in normal and
+    subnormal range; a step of the input's last bit decides beside them."""
+    top = 448.0
+    mid = torch.tensor([17 / 16, 19 / 16, 208.0 + 8, 224 + 16, 2.0 ** -7 * 1.25, 2.0 ** -10, 3 * 2.0 ** -10, 5 * 2.0 ** -10])
+    vals = torch.cat([mid, mid * (1 + 2.0 ** -23), mid * (1 - 2.0 ** -24), -mid])
+    x = torch.zeros(2, 64)
+    x[0, :32], x[1, :32] = vals, vals.flip(0)
+    x[:, 40] = top
+    q = torch.empty((2, 64), dtype=torch.float8_e4m3fn, device="cuda")
+    for group in (0, 64):
+        gdn.add_rmsnorm(x.cuda(), None, torch.ones(64).cuda(), 1e-6, q8=q, group=group)
+        assert torch.equal(q.cpu().double(), _e4m3(x.double()))
