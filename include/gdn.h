@@ -464,7 +464,7 @@ gdn_status gdn_ssm_prefill(const gdn_dims* dims, gdn_pool pool, gdn_pool ckpt,
  *   consecutive values of a row; group 0: one per row, else 32, 64, 128 or
  *   256, dividing d:
  *     GDN_SCALE_F32   float: max|y| / 448 (at least 2^-126), or 1 where every y
-                     is 0
+ *                     is 0
  *     GDN_SCALE_E8M0  uint8: 2^(byte - 127), the smallest power of two
  *                     (at least 2^-127) that is >= max|y| / 448; 127 where
  *                     every y is 0
