@@ -435,7 +435,9 @@ gdn_status gdn_ssm_decode_step(const gdn_dims* dims, gdn_pool pool, const gdn_ss
  * from any start position, block-aligned checkpoints of SSM state and conv
  * history, final state into the working slot, rows outside the sequences not
  * written) with every token the step above.  fp32 accuracy of states and
- * checkpoints.  A zero decay (a = +inf gives dt = +inf) is not finite here:
+ * checkpoints.  A NaN or an infinity among a sequence's inputs reaches its
+ * outputs and state from that 64-token block of positions on, nothing before
+ * it and no other sequence.  A zero decay (a = +inf gives dt = +inf) is not finite here:
  * the state takes dt k v^T as it is.
  *   workspace: >= gdn_ssm_prefill_workspace_size(...) bytes, 256-aligned
  *   (may be NULL where that is 0); nothing in it needs to be zero, and
