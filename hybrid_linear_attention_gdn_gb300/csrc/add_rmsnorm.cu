@@ -18,11 +18,12 @@
 // with loads in flight on every SM.  The same code with element accesses
 // takes any alignment and any d.
 //
-// Measured: 32768 rows of 4096, bf16 with an fp32 residual, y and q8: 256 us,
-// 1.00 of the copy bandwidth (1.75 GB), with a bf16 residual 208 us (0.86);
-// 64 rows 3.6 us in a graph of calls.  With the rare exact path inlined they
-// took 280 and 248 us, its registers costing a CTA per SM; at 4 or 6 CTAs of
-// 256 threads instead of 5, 255 and 223 or 306 and 207.
+// Measured: 32768 rows of 4096, bf16 with an fp32 residual, y and q8, a scale
+// per row 250 us, 1.03 of the copy bandwidth (1.75 GB), per 128 values 260; with
+// a bf16 residual 203 and 209 (0.88, 0.85); 64 rows 3.6 us in a graph of calls.
+// With the rare exact path inlined 280 and 248 us per 128 values: its registers
+// cost a CTA per SM.  4 or 6 CTAs of 256 threads instead of 5: 258 and 221, or
+// 306 and 207.
 #include "gdn_common.cuh"
 
 #include <cuda_fp8.h>
@@ -121,6 +122,13 @@ __device__ __forceinline__ float quotient(float p, float e, float m, float me, f
   return __uint_as_float((u - ((u ^ __float_as_uint(rest)) >> 31)) | 1u);
 }
 
+__device__ __forceinline__ float2 unpack(uint32_t bf16x2) {
+  return make_float2(__uint_as_float(bf16x2 << 16), __uint_as_float(bf16x2 & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t pack(float2 x) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
 // Four pairs of a vector: the sums h, what their rounding lost, the weights.
 struct Four {
   float2 h[4];
@@ -130,8 +138,7 @@ struct Four {
   __device__ __forceinline__ float2 product(int i) const { return mul2(mul2(h[i], both(i2)), g[i]); }  // h w
   // what the roundings of the sum and of the product p left
   __device__ __forceinline__ float2 error(int i, float2 p) const {
-    const float2 e = make_float2(__uint_as_float(lost[i] << 16), __uint_as_float(lost[i] & 0xffff0000u));
-    return fma2(mul2(e, both(i2)), g[i], fma2(mul2(h[i], both(i2)), g[i], mul2(p, both(-1.f))));
+    return fma2(mul2(unpack(lost[i]), both(i2)), g[i], fma2(mul2(h[i], both(i2)), g[i], mul2(p, both(-1.f))));
   }
   // the error of the largest, |h w| = m: of several the largest in its direction
   __device__ __forceinline__ float error_of(uint32_t m, float me) const {
@@ -148,19 +155,33 @@ struct Four {
 };
 constexpr float kNone = -3.4e38f;  // no error yet
 
-// The exact values of a vector, by all lanes of a warp; gl: lanes of a group
-// that find me themselves, or 0.  Not inlined: it is rare, and what it needs
-// would take registers (and with them CTAs) from every row.
-__device__ __noinline__ uint2 exact_q8(const Four f, uint32_t mu, float me, int gl) {
-  if (gl) {
-    me = f.error_of(mu, kNone);
-    for (int o = 1; o < gl; o <<= 1) me = fmaxf(me, __shfl_xor_sync(0xffffffffu, me, o));
-  }
+// The exact values of a vector, by all lanes of a warp; gl: lanes of a group,
+// which find me together.  Not inlined: it is rare, and what it needs would
+// take registers (and with them CTAs) from every row.
+__device__ __noinline__ uint2 exact_q8(const Four f, uint32_t mu, int gl) {
+  float me = f.error_of(mu, kNone);
+  for (int o = 1; o < gl; o <<= 1) me = fmaxf(me, __shfl_xor_sync(0xffffffffu, me, o));
   const float m = __uint_as_float(mu), im = 1.f / m;
   uint32_t q[2] = {0u, 0u};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 p = f.product(i), e = f.error(i, p);
+    q[i >> 1] |= e4m3x2(make_float2(quotient(p.x, e.x, m, me, im), quotient(p.y, e.y, m, me, im))) << (16 * (i & 1));
+  }
+  return make_uint2(q[0], q[1]);
+}
+
+// the same where p = h w and its errors are at hand, and me known
+struct FourP {
+  float2 p[4];
+  uint32_t e[4];
+};
+__device__ __noinline__ uint2 exact_q8_of(const FourP f, float m, float me) {
+  const float im = 1.f / m;
+  uint32_t q[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = f.p[i], e = unpack(f.e[i]);
     q[i >> 1] |= e4m3x2(make_float2(quotient(p.x, e.x, m, me, im), quotient(p.y, e.y, m, me, im))) << (16 * (i & 1));
   }
   return make_uint2(q[0], q[1]);
@@ -197,9 +218,10 @@ __device__ __forceinline__ float put_scale(const NormArgs& a, float top, int64_t
 
 // TPR threads per row, ROWS rows per CTA
 template <typename Tact, typename Tres, int TPR, int ROWS, int V, bool VEC, bool ROWSCALE>
-__global__ void __launch_bounds__(TPR* ROWS, TPR* ROWS >= 1024 ? 1 : 1280 / (TPR * ROWS)) add_rmsnorm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(TPR* ROWS, TPR* ROWS >= 1024 ? 1 : 1280 / (TPR * ROWS))
+    add_rmsnorm_kernel(const NormArgs a) {
   constexpr int kRowWarps = TPR / 32;
-  __shared__ uint32_t red[ROWS][32];
+  __shared__ uint64_t red[ROWS][32];
   pdl_wait();
   pdl_trigger();
   const int t = threadIdx.x % TPR, rloc = threadIdx.x / TPR, lane = threadIdx.x & 31;
@@ -232,10 +254,8 @@ __global__ void __launch_bounds__(TPR* ROWS, TPR* ROWS >= 1024 ? 1 : 1280 / (TPR
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 xi = xv[v].pair(i), ri = rv[v].pair(i), s = add2(xi, ri), b = sub2(s, xi);
-        const float2 e = add2(sub2(xi, sub2(s, b)), sub2(ri, b));
-        const __nv_bfloat162 eb = __floats2bfloat162_rn(e.x, e.y);
         h[v][i] = s;
-        lost[v][i] = *reinterpret_cast<const uint32_t*>(&eb);
+        lost[v][i] = pack(add2(sub2(xi, sub2(s, b)), sub2(ri, b)));
         rv[v].put(i, s);
       }
       if (a.residual && live && c < a.d) store8<VEC>(rv[v], res, base + c, a.d - c);
@@ -280,28 +300,47 @@ __global__ void __launch_bounds__(TPR* ROWS, TPR* ROWS >= 1024 ? 1 : 1280 / (TPR
     f.i2 = i2;
     return f;
   };
-  const int64_t per_row = a.group ? a.d / a.group : 1, n_scales = a.n_rows * per_row;
-  uint32_t top = 0;  // the row's largest |h w| (one scale per row)
-  float row_inv = 0.f;
-  // f(v, the vector's column, its four pairs) for this thread's vectors
-  auto vectors = [&](auto f) {
+  const int64_t per_row = ROWSCALE ? 1 : a.group ? a.d / a.group : 1, n_scales = a.n_rows * per_row;
+  // One scale per row: p = h w in place of h and its error in place of what h
+  // lost, y, and the row's largest |p| with its error (of several as large,
+  // the largest in its direction): one maximum of both.
+  float row_m = 0.f, row_me = 0.f, row_inv = 0.f;
+  if constexpr (ROWSCALE) {
+    uint32_t top = 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = 8 * (v * TPR + t);
       if (live && c < a.d) {
         Vec8<float> g;
+        Vec8<Tact> y;
         load8<VEC>(g, w, c, a.d - c);
-        f(v, c, four(v, g));
+        const Four f = four(v, g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 p = f.product(i);
+          lost[v][i] = pack(f.error(i, p));
+          h[v][i] = p;
+          y.put(i, mul2(p, both(c2)));
+          top = max(top, max(mag(p.x), mag(p.y)));
+        }
+        if (a.y) store8<VEC>(y, GDN_GV(reinterpret_cast<Tact*>(a.y), n), base + c, a.d - c);
       }
     }
-  };
-  if constexpr (ROWSCALE) {
-    vectors([&](int, int, const Four& f) {
+    float me = kNone;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) top = max(top, max(mag(f.product(i).x), mag(f.product(i).y)));
-    });
-    top = row_all(top, [](uint32_t p, uint32_t q) { return max(p, q); });
-    if (live) row_inv = put_scale(a, __uint_as_float(top) * c2, row, n_scales, t == 0);
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 p = h[v][i], e = unpack(lost[v][i]);
+        if (mag(p.x) == top) me = fmaxf(me, p.x < 0.f ? -e.x : e.x);
+        if (mag(p.y) == top) me = fmaxf(me, p.y < 0.f ? -e.y : e.y);
+      }
+    const uint32_t eb = __float_as_uint(me), order = eb ^ (eb >> 31 ? 0xffffffffu : 0x80000000u);
+    const uint64_t key = row_all((uint64_t)top << 32 | order, [](uint64_t p, uint64_t q) { return p > q ? p : q; });
+    const uint32_t ob = (uint32_t)key;
+    row_m = __uint_as_float((uint32_t)(key >> 32));
+    row_me = __uint_as_float(ob ^ (ob >> 31 ? 0x80000000u : 0xffffffffu));
+    if (live) row_inv = put_scale(a, row_m * c2, row, n_scales, t == 0);
   }
   const auto q8 = GDN_GV(a.q8, n);
   const int gl = a.group / 8;  // lanes of a group
@@ -314,34 +353,36 @@ __global__ void __launch_bounds__(TPR* ROWS, TPR* ROWS >= 1024 ? 1 : 1280 / (TPR
         if (i < a.d - c) q8[base + c + i] = (uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
     }
   };
-  uint32_t open = 0;  // one scale per row: the vectors whose values are still to be taken exactly
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int c = 8 * (v * TPR + t);
     const bool in = live && c < a.d;
     Vec8<float> g = {};
-    if (in) load8<VEC>(g, w, c, a.d - c);
-    const Four f = four(v, g);
     float2 p[4];
+    float m = row_m, inv_s = row_inv;
+    if constexpr (ROWSCALE) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = f.product(i);
-    if (a.y && in) {
-      Vec8<Tact> y;
+      for (int i = 0; i < 4; ++i) p[i] = h[v][i];
+    } else {
+      if (in) load8<VEC>(g, w, c, a.d - c);
+      const Four f = four(v, g);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y.put(i, mul2(p[i], both(c2)));
-      store8<VEC>(y, GDN_GV(reinterpret_cast<Tact*>(a.y), n), base + c, a.d - c);
-    }
-    if (!a.q8) continue;
-    uint32_t mu = top;
-    float inv_s = row_inv;
-    if constexpr (!ROWSCALE) {
-      mu = 0;
+      for (int i = 0; i < 4; ++i) p[i] = f.product(i);
+      if (a.y && in) {
+        Vec8<Tact> y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y.put(i, mul2(p[i], both(c2)));
+        store8<VEC>(y, GDN_GV(reinterpret_cast<Tact*>(a.y), n), base + c, a.d - c);
+      }
+      if (!a.q8) continue;
+      uint32_t mu = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) mu = max(mu, max(mag(p[i].x), mag(p[i].y)));
       for (int o = 1; o < gl; o <<= 1) mu = max(mu, __shfl_xor_sync(0xffffffffu, mu, o));
-      if (in) inv_s = put_scale(a, __uint_as_float(mu) * c2, row * per_row + c / a.group, n_scales, t % gl == 0);
+      m = __uint_as_float(mu);
+      if (in) inv_s = put_scale(a, m * c2, row * per_row + c / a.group, n_scales, t % gl == 0);
     }
-    const float m = __uint_as_float(mu), k = c2 * inv_s;
+    const float k = c2 * inv_s;
     // (within these the quotient's pieces neither overflow nor vanish)
     const bool exact = in && a.scale_type == GDN_SCALE_F32 && m > 1e-24f && m < 1e24f;
     const float2 lo = both(exact ? k * (1.f - 0x1p-20f) : k), hi = both(exact ? k * (1.f + 0x1p-20f) : k);
@@ -352,25 +393,25 @@ __global__ void __launch_bounds__(TPR* ROWS, TPR* ROWS >= 1024 ? 1 : 1280 / (TPR
       q[i >> 1] |= b << (16 * (i & 1));
       differ |= b ^ e4m3x2(mul2(p[i], hi));
     }
-    if constexpr (ROWSCALE) {
-      open |= differ ? 1u << v : 0u;
-    } else if (__any_sync(0xffffffffu, differ)) {
-      const uint2 z = exact_q8(f, mu, 0.f, gl);
+    if (__any_sync(0xffffffffu, differ)) {
+      uint2 z;
+      if constexpr (ROWSCALE) {
+        FourP f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f.p[i] = p[i];
+          f.e[i] = lost[v][i];
+        }
+        z = exact_q8_of(f, m, row_me);
+      } else {
+        z = exact_q8(four(v, g), __float_as_uint(m), gl);
+      }
       if (differ) {
         q[0] = z.x;
         q[1] = z.y;
       }
     }
     if (in) put_q8(c, make_uint2(q[0], q[1]));
-  }
-  if constexpr (ROWSCALE) {
-    if (!__syncthreads_or(open)) return;
-    float me = kNone;
-    vectors([&](int, int, const Four& f) { me = f.error_of(top, me); });
-    me = row_all(me, [](float p, float q) { return fmaxf(p, q); });
-    vectors([&](int v, int c, const Four& f) {
-      if (open >> v & 1) put_q8(c, exact_q8(f, top, me, 0));
-    });
   }
 }
 

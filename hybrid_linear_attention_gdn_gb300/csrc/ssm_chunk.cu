@@ -987,10 +987,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tile_at<uint4>(S.pt[0], sizeof(S.pt[0]), at) = make_uint4(0u, 0u, 0u, 0u);
         tile_at<uint4>(S.pt[1], sizeof(S.pt[1]), at) = make_uint4(0u, 0u, 0u, 0u);
       }
-      // P of the segment's chunk i; false if a wait expired
+      // P of the segment's chunk i; false (for the whole warp) if a wait expired
       auto put_p = [&](int i) -> bool {
         const uint32_t par = phase(i);
-        if (!mbar_wait(&S.gx[ring(i)], par) || !mbar_wait(&S.g_bar[ring(i)], par)) return false;
+        if (!__all_sync(0xffffffffu, mbar_wait(&S.gx[ring(i)], par) && mbar_wait(&S.g_bar[ring(i)], par))) return false;
         const int buf = i % kSlots;
 #pragma unroll 1
         for (int J = 0; 16 * J < wlo + 32; ++J) {
@@ -1157,10 +1157,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int first = -S.ch.m0, last = min(nit * kC, S.ch.len - S.ch.m0);
 
     float2 y[8];  // V 2^ve of the next chunk: channel lrow, tokens 16 qq ..
-    // V of the segment's chunk i; false if a wait expired
+    // V of the segment's chunk i; false (for the whole warp) if a wait expired
     auto features = [&](int i) -> bool {
       const uint32_t par = phase(i);
-      if (!mbar_wait(&S.gx[ring(i)], par) || !mbar_wait(&S.x_bar[ring(i)], par)) return false;
+      if (!__all_sync(0xffffffffu, mbar_wait(&S.gx[ring(i)], par) && mbar_wait(&S.x_bar[ring(i)], par))) return false;
       const int buf = i % kSlots;
       {
         const auto xs = GDN_SV(reinterpret_cast<const uint16_t*>(&S.raw[ring(i)][0][0]), kRawRows * 128) +

@@ -206,7 +206,8 @@ __global__ void __launch_bounds__(kThr, 1) ssm_decode_ring_kernel(const DecodeAr
           gd[e] = a.D ? GDN_GV(a.D, a.hv)[h] : 0.f;
         }
       }
-      ok = ok && mbar_wait(&S.bfull[bb], (vk >> 1) & 1);
+      // (a warp gives up as one: nothing below may find part of it gone)
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(&S.bfull[bb], (vk >> 1) & 1));
       const auto& B = S.bundle[bb];
       Tconv h1, h2, h3;
       auto feature = [&](int i0) -> float {
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(kThr, 1) ssm_decode_ring_kernel(const DecodeAr
       const auto dst = state + ((size_t)slot * a.hv + (size_t)hq * a.G) * a.dv * kDK;
       for (int c = 0; c < rows / kRows; ++c, ++n) {
         const int st = n % STAGES;
-        if (!(ok = ok && mbar_wait(&S.full[st], (n / STAGES) & 1))) break;
+        if (!(ok = __all_sync(0xffffffffu, ok && mbar_wait(&S.full[st], (n / STAGES) & 1)))) break;
         const int row = GDN_S(c * kRows + rloc, kMaxRows);
         const float* src = S.ring[GDN_S(st, STAGES)] + GDN_S(rloc, kRows) * kDK;
         float4 s[4];

@@ -441,7 +441,8 @@ gdn_status gdn_ssm_decode_step(const gdn_dims* dims, gdn_pool pool, const gdn_ss
  * the state takes dt k v^T as it is.
  *   workspace: >= gdn_ssm_prefill_workspace_size(...) bytes, 256-aligned
  *   (may be NULL where that is 0); nothing in it needs to be zero, and
- *   nothing is kept in it between calls.
+ *   nothing is kept in it between calls, but calls that run at once (on two
+ *   streams, or in two graphs that are replayed at once) need one each.
  */
 size_t gdn_ssm_prefill_workspace_size(const gdn_dims* dims, int32_t n_seq, int64_t total_tokens);
 gdn_status gdn_ssm_prefill(const gdn_dims* dims, gdn_pool pool, gdn_pool ckpt,

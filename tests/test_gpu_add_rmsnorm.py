@@ -103,7 +103,8 @@ def test_odd_sizes_and_unaligned(cuda, act, d):
     yd, q, s = gdn.add_rmsnorm(off(x), rd, off(w), 1e-5, y=off(x), q8=q)
     assert torch.equal(rd.cpu(), (x.float() + r.float()).to(act))
     mag = (x.double().abs() + r.double().abs()) / h.abs().clamp(min=1e-30)
-    assert ((yd.cpu().double() - y).abs() <= y.abs() * (torch.finfo(act).eps / 2 + 4e-6 + mag * 2.0 ** -24) + 1e-12).all()
+    half = torch.finfo(act).eps / 2
+    assert ((yd.cpu().double() - y).abs() <= y.abs() * (half + 4e-6 + mag * 2.0 ** -24) + 1e-12).all()
     _check_q8(q.cpu(), s.cpu(), y, d)
 
 
@@ -167,7 +168,8 @@ def test_q8_at_midpoints(cuda):
     """Quotients that are midpoints go to the even neighbour, in normal and
     subnormal range; a step of the input's last bit decides beside them."""
     top = 448.0
-    mid = torch.tensor([17 / 16, 19 / 16, 208.0 + 8, 224 + 16, 2.0 ** -7 * 1.25, 2.0 ** -10, 3 * 2.0 ** -10, 5 * 2.0 ** -10])
+    mid = torch.tensor([17 / 16, 19 / 16, 208.0 + 8, 224 + 16, 2.0 ** -7 * 1.25, 2.0 ** -10, 3 * 2.0 ** -10,
+                        5 * 2.0 ** -10])
     vals = torch.cat([mid, mid * (1 + 2.0 ** -23), mid * (1 - 2.0 ** -24), -mid])
     x = torch.zeros(2, 64)
     x[0, :32], x[1, :32] = vals, vals.flip(0)
