@@ -185,9 +185,10 @@ def _current_stream() -> int:
     return _raw_stream(torch.cuda.current_device())
 
 
-def _stream(stream) -> int | None:
+def _stream(stream, device: int | None = None) -> int | None:
+    """The stream's handle; device: the current one where the caller has it."""
     if stream is None:
-        return _current_stream()
+        return _current_stream() if device is None or _raw_stream is None else _raw_stream(device)
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -304,11 +305,15 @@ def _require_err(fn: str, t, device: int):
                                             f"{tuple(t.shape)} on {t.device}")
 
 
+# torch.cuda.current_device() without its lazy initialisation, where offered
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _device() -> int:
     """The current CUDA device (-2 without one: no tensor is on it)."""
-    if torch.cuda.is_initialized() or torch.cuda.is_available():
-        return torch.cuda.current_device()
-    return -2
+    if torch.cuda.is_initialized():
+        return _get_device() if _get_device is not None else torch.cuda.current_device()
+    return torch.cuda.current_device() if torch.cuda.is_available() else -2
 
 
 def _require_pool(fn: str, what: str, dims: Dims, pool: StatePool, device: int):
@@ -586,7 +591,7 @@ def ssm_decode_step(dims: Dims, pool: StatePool, params: SsmParams, slot_ids, qk
     _require_err(fn, dev_err, dev)
     cd, cp = dims.c(), params.c()
     st = L.gdn_ssm_decode_step(ctypes.byref(cd), pool.c(), ctypes.byref(cp), _ptr(slot_ids), B, _ptr(qkv), _ptr(a),
-                               _ptr(out), _ptr(dev_err), _stream(stream))
+                               _ptr(out), _ptr(dev_err), _stream(stream, dev))
     _check(fn, st)
 
 
@@ -625,7 +630,7 @@ def ssm_prefill(dims: Dims, pool: StatePool, ckpt: StatePool | None, params: Ssm
     st = L.gdn_ssm_prefill(ctypes.byref(cd), pool.c(), ck, ctypes.byref(cp), _ptr(slot_ids), _ptr(cu_seqlens),
                            _ptr(start_pos), n_seq, total, _ptr(ckpt_ids) if max_ckpt else None, max_ckpt,
                            int(ckpt_block), _ptr(qkv), _ptr(a), _ptr(out), _ptr(workspace),
-                           _nbytes(workspace) if workspace is not None else 0, _ptr(dev_err), _stream(stream))
+                           _nbytes(workspace) if workspace is not None else 0, _ptr(dev_err), _stream(stream, dev))
     _check(fn, st)
 
 
@@ -663,7 +668,7 @@ def add_rmsnorm(x, residual, weight, eps: float = 1e-6, y=None, q8=None, scales=
         _require(fn, "scales", scales, scales.dtype, (*shape[:-1], d // (group or d)), dev)
     st = L.gdn_add_rmsnorm(_DT_CODE[x.dtype], _DT_CODE[residual.dtype] if residual is not None else _DT_CODE[x.dtype],
                            _ptr(x), _ptr(residual), _ptr(weight), float(eps), rows, d, _ptr(y), _ptr(q8),
-                           _ptr(scales), int(group), scale_type, _stream(stream))
+                           _ptr(scales), int(group), scale_type, _stream(stream, dev))
     _check(fn, st)
     return y, q8, scales
 
@@ -700,7 +705,7 @@ def batch_maps(new_lens, start_pos, block: int, block_table, free_ids, n_free, c
     st = L.gdn_batch_maps(_ptr(new_lens), _ptr(start_pos), n_seq, int(block), _ptr(block_table),
                           int(block_table.shape[-1]), _ptr(free_ids), free_ids.numel(), _ptr(n_free),
                           _ptr(n_free_out), _ptr(cu_seqlens), _ptr(ckpt_ids), max_ckpt, _ptr(seq_ids),
-                          _ptr(positions), _ptr(slot_map), rows, _ptr(dev_err), _stream(stream))
+                          _ptr(positions), _ptr(slot_map), rows, _ptr(dev_err), _stream(stream, dev))
     _check(fn, st)
 
 

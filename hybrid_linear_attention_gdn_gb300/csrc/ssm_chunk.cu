@@ -1359,8 +1359,9 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 // Chunks per segment.  The lengths are on the device: the rule sees their sum.
 //  * Enough chains for the SMs (sequences x tiles >= 96): whole sequences.  The
 //    state pass costs about half as much again, and cutting only those longer
-//    than the mean measured no gain (7 ragged sequences of the 8-group layer
-//    186 us whole, 193 us cut; 4 x 8192 501 and 510 us).
+//    than the mean gains on some mixes and loses on others (8-group layer: 7
+//    ragged sequences 143 us whole, 138 cut; 8 others 129 and 155; 8 x 1000
+//    tokens 151 and 159; 4 x 8192 449 and 458).
 //  * Fewer: as many segments as fill the SMs, at most kMaxSegs per sequence
 //    of the mean length (a segment reads all its predecessors' states), and
 //    not below kMinSeg chunks.
