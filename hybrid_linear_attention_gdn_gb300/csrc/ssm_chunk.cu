@@ -36,10 +36,10 @@
 // The work per 64 x 128 V values is bound by the instructions of the
 // elementwise steps (conv + SiLU, P, operand conversion), not by the products
 // (tensor pipe 24 % busy) or by memory.  Measured, 64 heads of 64 in 8 groups:
-// 4 x 8192 tokens 446 us (features 84, chain 362: 2.8 us per chunk; 112 us of
-// memory traffic), seven ragged sequences of 3,968 tokens 140 us, 37 tokens 21
-// us in a graph; 32 heads in one group, 1 x 8192 tokens 100 us (features 10,
-// states of 8 segments 36, chains 54).
+// 4 x 8192 tokens 417 us (features 84, chain 333: 2.6 us per chunk; 112 us of
+// memory traffic), seven ragged sequences of 3,968 tokens 139 us, 37 tokens 21
+// us in a graph; 32 heads in one group, 1 x 8192 tokens 97 us (features 10,
+// states of 8 segments 35, chains 52).
 //
 // Segments: where sequences times V tiles are too few for the SMs, each
 // sequence is cut into segments of seg_chunks chunks.  A first launch walks
@@ -462,24 +462,24 @@ static_assert(offsetof(FeatSmem, meta) == offsetof(FeatSmem, g) + kGBytes &&
 //   23       loader: the copies of raw V rows and G, the three rows before a
 //            sequence from the conv history, and the largest raw input
 // What bounds a chunk is instruction issue: 3,400 instructions per scheduler
-// and chunk, 75 % of its slots.  It is not the products: leaving out half of
-// dS^T's changed nothing.  With P in the compute warps 4 x 8192 tokens took 468
-// us instead of 446.
+// and chunk, 80 % of its slots.  It is not the products: leaving out half of
+// dS^T's changed nothing.  4 x 8192 tokens: P in the compute warps cost 21 us
+// more; without P at all (wrong) it would be 25 us less.
 constexpr int kCompute = 512, kAux = 128;  // threads
 constexpr int kIssuer = (kCompute + kAux) / 32, kLoader = kIssuer + 3;
 constexpr int kThreads = 32 * (kLoader + 1);
 // Registers per thread after the split of the launch's 768 x 80.  Spills cost
-// more here than elsewhere: shared memory leaves little of the L1 cache (96 /
-// 56 / 40, with 64 bytes of the issuer's and the loader's spilled, 521 us for
-// 4 x 8192 tokens; 88 / 64 / 64, with the compute warps', 445, but 4 % slower
-// on the ragged sequences).
+// more here than elsewhere: shared memory leaves little of the L1 cache (4 x
+// 8192 tokens 422 us with this split, 528 with 96 / 56 / 40 and 64 bytes of the
+// issuer's and the loader's spilled, 436 with 96 / 40 / 56, 450 with 88 / 64 /
+// 64 and the compute warps' spilled).
 constexpr int kComputeRegs = 96, kAuxRegs = 48, kHelpRegs = 48;
 static_assert(kCompute * kComputeRegs + kAux * kAuxRegs + 128 * kHelpRegs <= kThreads * 80,
               "no more than the launch's registers");
 
-// Raw V rows and G of up to kRing chunks are on their way or being read (with
-// two, 4 x 8192 tokens took 452 us, not 446: copy, largest input and
-// scales then follow one another within a chunk); gates in twice as many slots.
+// Raw V rows and G of up to kRing chunks are on their way or being read (two
+// cost 6 us of 4 x 8192 tokens: copy, largest input and scales then follow one
+// another within a chunk); gates in twice as many slots.
 constexpr int kRing = 3, kSlots = 2 * kRing;
 __device__ __forceinline__ int ring(int i) { return i % kRing; }
 __device__ __forceinline__ uint32_t phase(int i) { return i / kRing & 1; }
@@ -908,8 +908,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int i = 0; i < nit && ok; ++i) {
         // the next chunk's copies go out before this one's rows are looked at
-        // (waited for in its own pass, a copy and the maximum one after the
-        // other took as long as a chunk: 446 us for 4 x 8192 tokens, not 423)
+        // (in one pass, a copy and the maximum one after the other took as
+        // long as a chunk and cost 23 us of 4 x 8192 tokens)
         if (i + 1 >= kRing && i + 1 < nit) {
           if (!(ok = __all_sync(0xffffffffu, mbar_wait(&S.used[ring(i + 1)], phase(i + 1 - kRing))))) break;
           if (lane == 0) load_xg(i + 1);
@@ -1155,9 +1155,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float4 w4 = vec_at<const float4>(GDN_GV(p.conv_w, (long long)p.C * 4), (size_t)ch * 4);
     const float bias = p.conv_bias ? GDN_GV(p.conv_bias, p.C)[ch] : 0.f;
     // chunks until the next block boundary, and the boundary's index
-    int to_ckpt = S.ch.to_ckpt, ck_idx = S.ch.ck_idx;
-    // the sequence's tokens, counted from the segment's first chunk
-    const int first = -S.ch.m0, last = min(nit * kC, S.ch.len - S.ch.m0);
+    int next_ckpt = S.ch.to_ckpt;  // the chunk that ends at the next block boundary
+    // the sequence's tokens among the 16 from token `at` of the segment's chunks on: [lo, hi)
+    auto inside = [&](int at, int& lo, int& hi) {
+      lo = -S.ch.m0 - at;
+      hi = min(S.ch.nit * kC, S.ch.len - S.ch.m0) - at;
+    };
 
     float2 y[8];  // V 2^ve of the next chunk: channel lrow, tokens 16 qq ..
     // V of the segment's chunk i; false (for the whole warp) if a wait expired
@@ -1187,7 +1190,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           y[t] = make_float2(__fdividef(v.x, d.x), __fdividef(v.y, d.y));
         }
       }
-      const int tlo = first - i * kC - 16 * qq, thi = last - i * kC - 16 * qq;
+      int tlo, thi;
+      inside(i * kC + 16 * qq, tlo, thi);
       if (tlo > 0 || thi < 16) {  // tokens outside the sequence
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
@@ -1286,7 +1290,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if constexpr (!STATE) {
         // a warp's 32 channels of a token are 64 consecutive bytes
-        const int tlo = first - i * kC - 16 * qq, thi = last - i * kC - 16 * qq;  // tokens of the sequence
+        int tlo, thi;
+        inside(i * kC + 16 * qq, tlo, thi);
         const long long ld = (long long)p.hv * DV;
         const long long at = (S.ch.t0 + S.ch.m0 + i * kC + 16 * qq) * ld + tile * 128 + lrow;  // may be < 0
         __nv_bfloat16 ob[16];
@@ -1314,9 +1319,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // the block boundary at this chunk's end (a sequence that ends inside
         // the chunk does not reach it)
-        if (to_ckpt-- == 0) {
-          to_ckpt = p.ckpt_block / kC - 1;
-          if (ck_idx < p.max_ckpt && (i + 1) * kC <= last) {
+        if (i == next_ckpt) {
+          const int kpc = p.ckpt_block / kC, ck_idx = S.ch.ck_idx + (i - S.ch.to_ckpt) / kpc;
+          next_ckpt += kpc;
+          if (ck_idx < p.max_ckpt && (i + 1) * kC <= S.ch.len - S.ch.m0) {
             const int32_t cid =
                 GDN_GV(p.ckpt_ids, (long long)p.n_seq * p.max_ckpt)[(size_t)S.ch.n * p.max_ckpt + ck_idx];
             if (slot_class(cid, p.ck_num_slots) == 0) {
@@ -1332,7 +1338,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int e = 0; e < 8; ++e) vec_at<float4>(to, 4 * e) = join4(st[2 * e], st[2 * e + 1]);
               }
             }
-            ++ck_idx;
           }
         }
       }
