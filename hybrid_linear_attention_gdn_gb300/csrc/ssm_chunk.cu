@@ -462,7 +462,7 @@ static_assert(offsetof(FeatSmem, meta) == offsetof(FeatSmem, g) + kGBytes &&
 //   23       loader: the copies of raw V rows and G, the three rows before a
 //            sequence from the conv history, and the largest raw input
 // What bounds a chunk is instruction issue: 3,400 instructions per scheduler
-// and chunk, 80 % of its slots.  It is not the products: leaving out half of
+// and chunk, 70 to 80 % of its slots.  It is not the products: leaving out half of
 // dS^T's changed nothing.  4 x 8192 tokens: P in the compute warps cost 21 us
 // more; without P at all (wrong) it would be 25 us less.
 constexpr int kCompute = 512, kAux = 128;  // threads
