@@ -206,13 +206,26 @@ cudaError_t dispatch_decode(const DecodeArgs& a, int act, int cv, cudaStream_t s
 // features and gates are computed into shared memory, then every warp walks
 // the window's tokens on its rows.  Bound by the latency of a token's chain
 // (update, dot product, transposed reduction), not by memory.  Measured: 513
-// tokens of 32 heads of 64 x 128 312 us, 0.6 us a token (396 before a window's
-// inputs were requested a window ahead); 233 tokens of the smallest layer 64
-// us.  The checkpoint test taken out of the token loop and unrolling it by 2
-// to 8 changed nothing or cost up to 9 %.
+// tokens of 32 heads of 64 x 128 244 us, 0.48 us a token (84 us more without a
+// window's inputs requested a window ahead, 26 more with eight taps for a conv
+// of four); 233 tokens of the smallest layer 51 us.  The checkpoint test taken
+// out of the token loop and unrolling it by 2 to 8 changed nothing or cost up
+// to 9 %.
 constexpr int kTW = 16;
 
-template <int DK, int UN, typename Tact, typename Tconv>
+// SiLU to some 3 units in the last place: e^-x as 2^(-x log2 e) with what the
+// product lost put back, and an approximate quotient (with the library's
+// exponential and division 513 tokens of 32 heads of 64 x 128 took 286 us, not
+// 244)
+__device__ __forceinline__ float silu_3ulp(float x) {
+  const float c = fminf(fmaxf(x, -87.f), 87.f);  // e^87 is finite
+  const float t = c * -1.44269504f, lost = fmaf(c, -1.92596299e-8f, fmaf(c, -1.44269504f, -t));
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(e) : "f"(t));
+  return __fdividef(x, 1.f + fmaf(e, lost * 0.693147181f, e));
+}
+
+template <int DK, int UN, int TAPS, typename Tact, typename Tconv>
 __global__ void __launch_bounds__(kThreads) ssm_recurrent_kernel(const PrefillArgs a, const int parts) {
   using M = Rows<DK>;
   constexpr int kWarpRows = UN * M::RPW, R = kWarps * kWarpRows, NCH = 2 * DK + R;
@@ -255,10 +268,10 @@ __global__ void __launch_bounds__(kThreads) ssm_recurrent_kernel(const PrefillAr
   for (int u = 0; u < UN; ++u)
     s[u] = row + u * M::RPW < nrows ? vec_at<const float4>(S, (size_t)(row + u * M::RPW) * DK + 4 * seg)
                                     : make_float4(0.f, 0.f, 0.f, 0.f);
-  // this thread's channels: weights and history right-aligned in kMaxW taps
-  float w[kCPT][kMaxW], win[kCPT][kMaxW - 1], bias[kCPT];
+  // this thread's channels: weights and history right-aligned in TAPS taps
+  float w[kCPT][TAPS], win[kCPT][TAPS - 1], bias[kCPT];
   int ch[kCPT];
-  const int lead = kMaxW - a.W;
+  const int lead = TAPS - a.W;
   const auto hist = GDN_GV(reinterpret_cast<const Tconv*>(a.conv), (long long)a.num_slots * (a.W - 1) * a.C) +
                     (size_t)slot * (a.W - 1) * a.C;
   const auto conv_w = GDN_GV(a.conv_w, (long long)a.C * a.W);
@@ -272,9 +285,9 @@ __global__ void __launch_bounds__(kThreads) ssm_recurrent_kernel(const PrefillAr
     if (ch[ci] < 0) continue;
     bias[ci] = a.conv_bias ? GDN_GV(a.conv_bias, a.C)[ch[ci]] : 0.f;
 #pragma unroll
-    for (int j = 0; j < kMaxW; ++j) w[ci][j] = j >= lead ? conv_w[(size_t)ch[ci] * a.W + (j - lead)] : 0.f;
+    for (int j = 0; j < TAPS; ++j) w[ci][j] = j >= lead ? conv_w[(size_t)ch[ci] * a.W + (j - lead)] : 0.f;
 #pragma unroll
-    for (int j = 0; j < kMaxW - 1; ++j) win[ci][j] = j >= lead ? to_f32(hist[(size_t)(j - lead) * a.C + ch[ci]]) : 0.f;
+    for (int j = 0; j < TAPS - 1; ++j) win[ci][j] = j >= lead ? to_f32(hist[(size_t)(j - lead) * a.C + ch[ci]]) : 0.f;
   }
   const float A_log = GDN_GV(a.A_log, a.hv)[h], dtb = GDN_GV(a.dt_bias, a.hv)[h];
   const float D = a.D ? GDN_GV(a.D, a.hv)[h] : 0.f;
@@ -288,7 +301,7 @@ __global__ void __launch_bounds__(kThreads) ssm_recurrent_kernel(const PrefillAr
     for (int ci = 0; ci < kCPT; ++ci)
 #pragma unroll
       for (int t = 0; t < kTW; ++t)
-        if (ch[ci] >= 0 && w0 + t < len) xv[ci][t] = qkv[(size_t)(t0 + w0 + t) * a.C + ch[ci]];
+        xv[ci][t] = ch[ci] >= 0 && w0 + t < len ? qkv[(size_t)(t0 + w0 + t) * a.C + ch[ci]] : from_f32<Tact>(0.f);
     if (tid < kTW && w0 + tid < len) ga = gate_a[(size_t)(t0 + w0 + tid) * a.hv + h];
   };
   request(0);
@@ -301,15 +314,14 @@ __global__ void __launch_bounds__(kThreads) ssm_recurrent_kernel(const PrefillAr
       for (int t = 0; t < kTW; ++t) {
         float acc = bias[ci];
 #pragma unroll
-        for (int j = 0; j < kMaxW - 1; ++j) acc = fmaf(w[ci][j], j < lead ? 0.f : win[ci][j], acc);
+        for (int j = 0; j < TAPS - 1; ++j) acc = fmaf(w[ci][j], win[ci][j], acc);
         const float x = to_f32(xv[ci][t]);
-        acc = fmaf(w[ci][kMaxW - 1], x, acc);
-        if (t < nt) {
-          sy[t * NCH + tid + ci * kThreads] = silu_f(acc);
+        acc = fmaf(w[ci][TAPS - 1], x, acc);
+        sy[t * NCH + tid + ci * kThreads] = silu_3ulp(acc);
+        // (past the end, in a last window, nothing reads these)
 #pragma unroll
-          for (int j = 0; j < kMaxW - 2; ++j) win[ci][j] = win[ci][j + 1];
-          win[ci][kMaxW - 2] = x;
-        }
+        for (int j = 0; j < TAPS - 2; ++j) win[ci][j] = win[ci][j + 1];
+        win[ci][TAPS - 2] = x;
       }
     }
     if (tid < nt) {
@@ -365,18 +377,21 @@ __global__ void __launch_bounds__(kThreads) ssm_recurrent_kernel(const PrefillAr
     if (row + u * M::RPW < nrows) vec_at<float4>(S, (size_t)(row + u * M::RPW) * DK + 4 * seg) = s[u];
 }
 
-template <int DK, int UN>
-cudaError_t dispatch_recurrent(const PrefillArgs& a, int act, int cv, cudaStream_t s) {
+template <int DK, int UN, int TAPS>
+cudaError_t launch_recurrent(const PrefillArgs& a, int act, int cv, cudaStream_t s) {
   constexpr int R = kWarps * UN * Rows<DK>::RPW;
   const int parts = (a.dv + R - 1) / R;
-  const dim3 grid((unsigned)(a.hv * parts), (unsigned)a.n_seq);
+  const dim3 grid((unsigned)(a.hv * parts), (unsigned)a.n_seq), block(kThreads);
+  using B = __nv_bfloat16;
   if (act == GDN_F32)
-    return launch_plain(ssm_recurrent_kernel<DK, UN, float, float>, grid, dim3(kThreads), 0, s, dim3(1), a, parts);
+    return launch_plain(ssm_recurrent_kernel<DK, UN, TAPS, float, float>, grid, block, 0, s, dim3(1), a, parts);
   if (cv == GDN_BF16)
-    return launch_plain(ssm_recurrent_kernel<DK, UN, __nv_bfloat16, __nv_bfloat16>, grid, dim3(kThreads), 0, s,
-                        dim3(1), a, parts);
-  return launch_plain(ssm_recurrent_kernel<DK, UN, __nv_bfloat16, float>, grid, dim3(kThreads), 0, s, dim3(1), a,
-                      parts);
+    return launch_plain(ssm_recurrent_kernel<DK, UN, TAPS, B, B>, grid, block, 0, s, dim3(1), a, parts);
+  return launch_plain(ssm_recurrent_kernel<DK, UN, TAPS, B, float>, grid, block, 0, s, dim3(1), a, parts);
+}
+template <int DK, int UN>
+cudaError_t dispatch_recurrent(const PrefillArgs& a, int act, int cv, cudaStream_t s) {
+  return a.W <= 4 ? launch_recurrent<DK, UN, 4>(a, act, cv, s) : launch_recurrent<DK, UN, kMaxW>(a, act, cv, s);
 }
 
 gdn_status check_params(const gdn_ssm_params* p) {
