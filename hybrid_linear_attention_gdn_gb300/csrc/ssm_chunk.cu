@@ -1370,13 +1370,16 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 //    than the mean gains on some mixes and loses on others (8-group layer: 7
 //    ragged sequences 143 us whole, 138 cut; 8 others 129 and 155; 8 x 1000
 //    tokens 151 and 159; 4 x 8192 449 and 458).
-//  * Fewer: as many segments as fill the SMs, at most kMaxSegs per sequence
+//  * Few chunks in all (16, or 24 of several sequences): whole too, since the
+//    state pass costs more than it shortens (1 x 700 tokens 62 us cut, 47 whole;
+//    2 x 700 64 and 51; but 1 x 1500 65 and 85).
+//  * Fewer chains: as many segments as fill the SMs, at most kMaxSegs per sequence
 //    of the mean length (a segment reads all its predecessors' states), and
 //    not below kMinSeg chunks.
 constexpr int64_t kMinSeg = 8, kMaxSegs = 16;
 int64_t seg_chunks(int64_t tiles, int64_t n_seq, int64_t total) {
   const int64_t chunks = (total + kC - 1) / kC, mean = (chunks + n_seq - 1) / n_seq;
-  if (tiles * n_seq >= 96) return 1 << 30;
+  if (tiles * n_seq >= 96 || chunks <= (n_seq > 1 ? 24 : 16)) return 1 << 30;
   const int64_t fill = (tiles * chunks + sm_count() - 1) / sm_count();
   return max(max(fill + 1, kMinSeg), (mean + kMaxSegs - 1) / kMaxSegs);
 }
