@@ -1,0 +1,106 @@
+"""The state space prefill over the range of its inputs: saturated SiLU,
+queries or keys that are zero, values at the top of fp32, heads of very
+different sizes.  Each head is compared at its own size; tolerances as in the
+other state space tests unless derived here.
+"""
+import numpy as np
+import pytest
+import torch
+
+import hybrid_linear_attention_gdn_gb300 as gdn
+from hybrid_linear_attention_gdn_gb300 import synth
+from oracle import state_space
+from helpers import assert_out_close, out_tol
+from ssm_helpers import SsmSetup, f64, shape
+from test_gpu_ssm import _check_states
+
+pytestmark = pytest.mark.gpu
+
+IDS, LENS, STARTS = [4, 1], [100, 130], [33, 64]
+
+
+def _i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def _call(st, qkv, a, ids=IDS, lens=LENS, starts=STARTS):
+    """One prefill and its recurrence: both outputs."""
+    sh, total = st.shape, sum(lens)
+    cu = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    out = torch.full((total, sh.hv, sh.dv), 7.0, dtype=sh.act_dtype, device="cuda")
+    size = gdn.ssm_prefill_workspace_size(st.dims, len(lens), total)
+    ws = torch.full((size,), 0xff, dtype=torch.uint8, device="cuda") if size else None
+    gdn.ssm_prefill(st.dims, st.pool, None, st.params, _i32(ids), _i32(cu), torch.tensor(starts, device="cuda"), total,
+                    None, 64, qkv.cuda(), a.cuda(), out, ws)
+    ref = state_space.prefill(st.od, st.opool, None, st.oparams, ids, cu, starts, None, 64, f64(qkv), f64(a))
+    return out, ref
+
+
+def _check_heads(st, out, ref):
+    for h in range(st.shape.hv):
+        assert_out_close(out[:, h], ref[:, h], st.shape.dv, out_tol(st.shape), row_floor_rms=True)
+    _check_states(st, st.pool, st.opool)
+
+
+def _silu(x, qk=0.0):
+    """SiLU as the token recurrence takes it: a layer whose output is D v (and
+    S q with queries and keys of SiLU(qk))."""
+    hv = 64
+    sh = synth.LayerShape("silu", 1, hv, 16, 16, 2, 1, "f32", "f32")
+    st = SsmSetup(sh, seed=70, bias=False)
+    st.params.conv_w[:] = torch.tensor([0.0, 1.0], device="cuda")
+    st.params.D[:] = 1.0
+    st.pool.conv.zero_(), st.pool.ssm.zero_()
+    T = x.numel() // (hv * 16)
+    qkv = torch.cat([torch.full((T, 2 * 16), qk), x.reshape(T, hv * 16)], 1).cuda()
+    out = torch.empty((T, hv, 16), device="cuda")
+    gdn.ssm_prefill(st.dims, st.pool, None, st.params, _i32([0]), _i32([0, T]), torch.tensor([0], device="cuda"), T, None,
+                    64, qkv, torch.zeros((T, hv), device="cuda"), out, None)
+    return out.cpu().reshape(-1)
+
+
+def test_silu_of_the_recurrence(cuda):
+    """From -3e38 to 3e38.  For x >= -87 the exponential's 2 units in the last
+    place and half a one for each of its correction, the sum, the product and
+    the quotient's 2: 5.5 <= 6 units of at most 2^-23; below, where the
+    exponential leaves the normal range, what is lost is at most 90 2^-126."""
+    big = torch.logspace(2, 38.4, 4096, dtype=torch.float64)
+    x = torch.cat([torch.linspace(-110, 110, 57344, dtype=torch.float64), -big, big]).float()
+    got = _silu(x).double()
+    xd = x.double()
+    ref = xd / (1 + torch.exp(-xd))
+    assert torch.isfinite(got).all()
+    assert ((got - ref).abs() <= 6 * 2.0 ** -23 * ref.abs() + 90 * 2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+def test_silu_of_the_recurrence_not_finite(cuda, value):
+    """As in the decode step: infinity, NaN, NaN.  With keys of 0 the state
+    takes infinity times 0, so that every output is NaN."""
+    x = torch.full((1024,), value)
+    assert torch.isnan(_silu(x)).all()
+    got = _silu(x, qk=1.0)
+    assert (got == float("inf")).all() if value > 0 else torch.isnan(got).all()
+
+
+@pytest.mark.parametrize("name", ["tiny", "dk64", "wide_conv", "ragged_dv"])
+@pytest.mark.parametrize("value", [-1e30, -1e37])
+def test_saturated_channels(cuda, name, value):
+    """Channels whose conv sums are far below zero: features of 0."""
+    st = SsmSetup(shape(name), seed=71)
+    st.params.conv_w.abs_()
+    st.oparams.conv_w[:] = f64(st.params.conv_w)
+    qkv, a = st.tokens(sum(LENS))
+    qkv[:, ::3] = value
+    _check_heads(st, *_call(st, qkv, a))
+
+
+@pytest.mark.parametrize("scale", [1e-6, 1e6])
+@pytest.mark.parametrize("name", ["tiny", "dk64", "wide_conv"])
+def test_recurrence_small_and_large_inputs(cuda, name, scale):
+    st = SsmSetup(shape(name), seed=72, bias=False)
+    qkv, a = st.tokens(sum(LENS))
+    st.pool.conv *= scale
+    st.pool.ssm *= scale * scale
+    st.opool.conv[:], st.opool.ssm[:] = f64(st.pool.conv), f64(st.pool.ssm)  # the rounded products
+    _check_heads(st, *_call(st, (qkv.float() * scale).to(qkv.dtype), a))
