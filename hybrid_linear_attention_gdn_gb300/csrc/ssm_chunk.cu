@@ -143,10 +143,13 @@ __device__ __forceinline__ float silu_acc(float y) { return __fdividef(y, 1.f + 
 
 // The power of two 2^e that takes a largest magnitude m to [2^14, 2^15), as
 // an exponent: fp16's high halves stay finite and the low halves keep 11 more
-// bits of everything down to 2^-28 of m.  0 for m = 0, infinite or NaN.
+// bits of everything down to 2^-28 of m.  At most 100, which is also what a
+// largest magnitude of 0 gets: operands that are all zero must not count as
+// large where a bound is taken from their scales.  0 for an infinite m or NaN.
 __device__ __forceinline__ int scale_exp(uint32_t m_bits) {
   const int ex = (int)(m_bits >> 23);
-  if (ex == 0 || ex == 255) return 0;
+  if (ex == 0) return 100;
+  if (ex == 255) return 0;
   const int e = 14 - (ex - 127);
   return e > 100 ? 100 : e;
 }
@@ -829,12 +832,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = __all_sync(0xffffffffu, in_time))) break;
         const int buf = i % kSlots, qe = S.g[ring(i)].meta[0], ke = S.g[ring(i)].meta[1];
         // |V| <= vb, |V w| <= vb max dt,
-        // |P| <= 128 max|q| max|k| max dt + |D| < 2^(37 - qe - ke) max dt + |D|
+        // |P| <= 128 max|q| max|k| max dt + |D| < 2^(37 - qe - ke) max dt + |D|,
+        // each of the two below 2^(14 - pe)
         const float vb = fmaf(S.vgain, S.xmax[ring(i)], S.vbias);
-        const float gb = exp2_int(max(-126, min(127, 37 - qe - ke)));
-        const int ve = scale_exp(__float_as_uint(vb)), we = scale_exp(__float_as_uint(vb * dtm));
-        const int pe = scale_exp(__float_as_uint(fmaf(gb, dtm, fabsf(D))));
-        const float fw = exp2_int(max(-126, min(127, we - ve)));
+        const int ve = scale_exp(__float_as_uint(vb));
+        const int we = max(ve - 126, min(ve + 126, scale_exp(__float_as_uint(vb * dtm))));
+        const int pe =
+            max(-126, min(scale_exp(__float_as_uint(dtm)) - (37 - qe - ke), scale_exp(__float_as_uint(fabsf(D)))) - 1);
+        const float fw = exp2_int(we - ve);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int t = 32 * e + lane;

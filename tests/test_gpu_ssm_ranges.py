@@ -104,3 +104,37 @@ def test_recurrence_small_and_large_inputs(cuda, name, scale):
     st.pool.ssm *= scale * scale
     st.opool.conv[:], st.opool.ssm[:] = f64(st.pool.conv), f64(st.pool.ssm)  # the rounded products
     _check_heads(st, *_call(st, (qkv.float() * scale).to(qkv.dtype), a))
+
+
+@pytest.mark.parametrize("zero", ["q", "k", "qk"])
+@pytest.mark.parametrize("name", ["wide", "square"])
+def test_zero_queries_and_keys(cuda, name, zero):
+    """Where q.k is zero throughout, D v is all that P holds: it keeps its
+    bits at any dt and for skips from 0.01 to 5."""
+    st = SsmSetup(shape(name), seed=73, decay=(0.1, 3.0))
+    n = st.shape.hk * st.shape.dk
+    cols = slice(0 if "q" in zero else n, 2 * n if "k" in zero else n)
+    for p in (st.params, st.oparams):
+        p.conv_bias[cols] = 0.0
+        p.A_log[:] = -7.0  # a state that fp32 still holds at the end
+    for p in (st.pool, st.opool):
+        p.conv[:, :, cols] = 0.0
+    st.params.D[:] = torch.tensor([0.1, 0.5, 0.01, 5.0] * (st.shape.hv // 4))
+    st.oparams.D[:] = f64(st.params.D)
+    qkv, a = st.tokens(sum(LENS))
+    qkv[:, cols] = 0.0
+    _check_heads(st, *_call(st, qkv, a))
+
+
+@pytest.mark.parametrize("name", ["wide", "square"])
+def test_zero_everything(cuda, name):
+    """No inputs, no bias, no skip term: the state decays, every output is 0."""
+    st = SsmSetup(shape(name), seed=74, bias=False, skip=False)
+    st.params.A_log[:] = -7.0
+    st.oparams.A_log[:] = -7.0
+    st.pool.conv.zero_()
+    st.opool.conv[:] = 0.0
+    qkv, a = st.tokens(sum(LENS))
+    out, ref = _call(st, torch.zeros_like(qkv), a)
+    assert (out == 0).all() and (ref == 0).all()
+    _check_states(st, st.pool, st.opool)
