@@ -537,8 +537,8 @@ struct __align__(1024) ChainSmem {
   float v[kSlots][NH][kC];                 // e^{b' - b} dt, b' at the end of the token's 16-token block
   float w[kSlots][NH][kC];                 // e^{b_last - b} dt 2^(we - ve)
   Scales sc[kSlots][NH];
-  float xmax[kRing];                  // largest raw input of a chunk
-  float vgain, vbias;                 // |V| <= vgain xmax + vbias
+  float xmax[kRing][NH];              // largest raw input of a chunk, of a head
+  float vgain[NH], vbias[NH];         // |V| <= vgain xmax + vbias
   uint32_t smax[NH];                  // largest |S| entering the segment, float bits
   uint64_t x_bar[kRing], g_bar[kRing], qk_bar[2];  // copies landed
   uint64_t hx[kRing];                 // xmax known, history rows in place
@@ -834,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // |V| <= vb, |V w| <= vb max dt,
         // |P| <= 128 max|q| max|k| max dt + |D| < 2^(37 - qe - ke) max dt + |D|,
         // each of the two below 2^(14 - pe)
-        const float vb = fmaf(S.vgain, S.xmax[ring(i)], S.vbias);
+        const float vb = fmaf(S.vgain[hh], S.xmax[ring(i)][hh], S.vbias[hh]);
         const int ve = scale_exp(__float_as_uint(vb));
         const int we = max(ve - 126, min(ve + 126, scale_exp(__float_as_uint(vb * dtm))));
         const int pe =
@@ -889,25 +889,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 4; ++k) hrow[j][k] = hist[j * row + tile * 128 + 32 * k + lane];
       }
       {
-        // |V| <= |conv| <= max over the channels of sum |w| times the largest
-        // raw input, plus the largest |bias|
+        // |V| <= |conv| <= max over a head's channels of sum |w| times the
+        // largest raw input, plus the largest |bias|
         const auto cw = GDN_GV(p.conv_w, (long long)p.C * 4);
-        float gain = 0.f, bmax = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int ch = 2 * p.hk * kDK + tile * 128 + 32 * k + lane;
-          const float4 w = vec_at<const float4>(cw, (size_t)ch * 4);
-          gain = fmaxf(gain, fabsf(w.x) + fabsf(w.y) + fabsf(w.z) + fabsf(w.w));
-          if (p.conv_bias) bmax = fmaxf(bmax, fabsf(GDN_GV(p.conv_bias, p.C)[ch]));
-        }
+        for (int hh = 0; hh < NH; ++hh) {
+          float gain = 0.f, bmax = 0.f;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) {
-          gain = fmaxf(gain, __shfl_xor_sync(0xffffffffu, gain, o));
-          bmax = fmaxf(bmax, __shfl_xor_sync(0xffffffffu, bmax, o));
-        }
-        if (lane == 0) {
-          S.vgain = gain;
-          S.vbias = bmax;
+          for (int k = hh * (DV / 32); k < (hh + 1) * (DV / 32); ++k) {
+            const int ch = 2 * p.hk * kDK + tile * 128 + 32 * k + lane;
+            const float4 w = vec_at<const float4>(cw, (size_t)ch * 4);
+            gain = fmaxf(gain, fabsf(w.x) + fabsf(w.y) + fabsf(w.z) + fabsf(w.w));
+            if (p.conv_bias) bmax = fmaxf(bmax, fabsf(GDN_GV(p.conv_bias, p.C)[ch]));
+          }
+#pragma unroll
+          for (int o = 16; o; o >>= 1) {
+            gain = fmaxf(gain, __shfl_xor_sync(0xffffffffu, gain, o));
+            bmax = fmaxf(bmax, __shfl_xor_sync(0xffffffffu, bmax, o));
+          }
+          if (lane == 0) {
+            S.vgain[hh] = gain;
+            S.vbias[hh] = bmax;
+          }
         }
       }
       bool ok = true;
@@ -940,7 +943,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma::fence_proxy_async();  // before a later chunk's copy into these rows
           __syncwarp();
         }
-        // the largest finite |raw input|
+        // the largest finite |raw input| of each head: its channels are those
+        // of the lanes whose 16-byte pieces (lane mod 16) are its own
         __nv_bfloat162 mx[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) mx[k] = __floats2bfloat162_rn(0.f, 0.f);
@@ -958,16 +962,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t m = __float_as_uint(fmaxf(m01.x, m01.y));
         if (__any_sync(0xffffffffu, m >= 0x7f800000u)) {  // infinities: without them
           m = 0;
-          for (int e = lane; e < kRawRows * 128; e += 32) {
-            const uint32_t v = __float_as_uint(__bfloat162float(S.raw[ring(i)][e / 128][e % 128])) & 0x7fffffffu;
-            m = max(m, v < 0x7f800000u ? v : 0u);
-          }
+          for (int e = lane; e < kRawRows * 16; e += 32)
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k) {
+              const float x = __bfloat162float(S.raw[ring(i)][e / 16][e % 16 * 8 + k]);
+              const uint32_t v = __float_as_uint(x) & 0x7fffffffu;
+              m = max(m, v < 0x7f800000u ? v : 0u);
+            }
         }
-        m = __reduce_max_sync(0xffffffffu, m);
-        if (lane == 0) {
-          S.xmax[ring(i)] = __uint_as_float(m);
-          mbar_arrive(&S.hx[ring(i)]);
+#pragma unroll
+        for (int hh = 0; hh < NH; ++hh) {
+          const uint32_t mh = __reduce_max_sync(0xffffffffu, NH == 1 || (lane >> 3 & 1) == hh ? m : 0u);
+          if (lane == 0) S.xmax[ring(i)][hh] = __uint_as_float(mh);
         }
+        if (lane == 0) mbar_arrive(&S.hx[ring(i)]);
         __syncwarp();
       }
       if (lane == 0) {

@@ -138,3 +138,21 @@ def test_zero_everything(cuda, name):
     out, ref = _call(st, torch.zeros_like(qkv), a)
     assert (out == 0).all() and (ref == 0).all()
     _check_states(st, st.pool, st.opool)
+
+
+@pytest.mark.parametrize("big,small", [(1.0, 1e-12), (1e6, 1e-6), (1e20, 1.0), (1.0, 0.0)])
+def test_heads_of_different_sizes(cuda, big, small):
+    """Neighbouring heads that share a tile's products: each keeps its bits,
+    whatever the other's size."""
+    st = SsmSetup(shape("wide"), seed=76, bias=False)
+    sh = st.shape
+    c = 2 * sh.hk * sh.dk
+    qkv, a = st.tokens(sum(LENS))
+    for h in range(sh.hv):
+        f = big if h % 2 else small
+        cols = slice(c + h * sh.dv, c + (h + 1) * sh.dv)
+        qkv[:, cols] = (qkv[:, cols].float() * f).to(qkv.dtype)
+        st.pool.conv[:, :, cols] *= f
+        st.pool.ssm[:, h] *= f
+    st.opool.conv[:], st.opool.ssm[:] = f64(st.pool.conv), f64(st.pool.ssm)
+    _check_heads(st, *_call(st, qkv, a))
