@@ -26,10 +26,14 @@
 //                            nearest: the tensor core's truncating
 //                            accumulation never touches the long-lived state
 //   All operands are fp16 (kind::f16, four times the measured rate of
-//   kind::tf32 at the same 11 bits) after exact power-of-two scalings that
-//   keep any input range: by the largest |q|, |k| and |v| of a chunk, and by
-//   upper bounds of |v w|, |P| and |S|.  A bound may be loose by 2^14: fp16
-//   keeps 11 bits over 29 binades.  Roundings: the output products' operands
+//   kind::tf32 at the same 11 bits) after exact power-of-two scalings: by the
+//   largest |q| and |k| of a chunk and group, the largest |v| of a chunk and
+//   head, and by upper bounds of |v w|, |P| and |S| of a head.  A bound may be
+//   loose by 2^14: fp16 keeps 11 bits over 29 binades.  So inputs of any size
+//   do (tests from 1e-12 to 1e36), relative to the largest of their operand:
+//   what is 2^-29 of it or less loses bits.  Where the product of two
+//   operands' largest magnitudes passes fp32 the result may be infinite though
+//   the largest do not meet.  Roundings: the output products' operands
 //   to 11 bits (a relative 2^-12 of their terms, against 2^-9 of the bf16
 //   output); the state's operands to two halves each, 22 bits, in three
 //   products.
@@ -153,6 +157,7 @@ __device__ __forceinline__ int scale_exp(uint32_t m_bits) {
   const int e = 14 - (ex - 127);
   return e > 100 ? 100 : e;
 }
+constexpr float kLargest = 3.40282347e38f;  // of fp32
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 // two values as fp16 high halves and the low halves that remain
@@ -346,7 +351,7 @@ __global__ void __launch_bounds__(kFT, 2)
 #pragma unroll
     for (int t = 0; t < 32; ++t) {
       const float u = fabsf(y[t].x), v = fabsf(y[t].y);  // the finite ones
-      mx = fmaxf(mx, fmaxf(u <= 3.4e38f ? u : 0.f, v <= 3.4e38f ? v : 0.f));
+      mx = fmaxf(mx, fmaxf(u <= kLargest ? u : 0.f, v <= kLargest ? v : 0.f));
     }
     {
       const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
@@ -811,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         b[1] += __shfl_sync(0xffffffffu, b[0], 31);
         const float back = __shfl_sync(0xffffffffu, suf[1], 0), all = back + __shfl_sync(0xffffffffu, suf[0], 0);
-        float dtm = fmaxf(dt[0], dt[1]);
+        float dtm = fmaxf(dt[0] <= kLargest ? dt[0] : 0.f, dt[1] <= kLargest ? dt[1] : 0.f);  // the finite ones
 #pragma unroll
         for (int o = 16; o; o >>= 1) dtm = fmaxf(dtm, __shfl_xor_sync(0xffffffffu, dtm, o));
         const float nx = __shfl_down_sync(0xffffffffu, suf[0], 1), ny = __shfl_down_sync(0xffffffffu, suf[1], 1);
@@ -833,10 +838,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int buf = i % kSlots, qe = S.g[ring(i)].meta[0], ke = S.g[ring(i)].meta[1];
         // |V| <= vb, |V w| <= vb max dt,
         // |P| <= 128 max|q| max|k| max dt + |D| < 2^(37 - qe - ke) max dt + |D|,
-        // each of the two below 2^(14 - pe)
-        const float vb = fmaf(S.vgain[hh], S.xmax[ring(i)][hh], S.vbias[hh]);
+        // each of the two below 2^(14 - pe).  A bound that passes the largest
+        // fp32 value is that value: what is finite is no larger.
+        const float vb = fminf(fmaf(S.vgain[hh], S.xmax[ring(i)][hh], S.vbias[hh]), kLargest);
+        const float wb = fminf(vb * dtm, kLargest);
         const int ve = scale_exp(__float_as_uint(vb));
-        const int we = max(ve - 126, min(ve + 126, scale_exp(__float_as_uint(vb * dtm))));
+        const int we = max(ve - 126, min(ve + 126, scale_exp(__float_as_uint(wb))));
         const int pe =
             max(-126, min(scale_exp(__float_as_uint(dtm)) - (37 - qe - ke), scale_exp(__float_as_uint(fabsf(D)))) - 1);
         const float fw = exp2_int(we - ve);
@@ -855,7 +862,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           c.ds = exp2_int(-we) * exp2_int(-ke);
           c.o2 = exp2_int(-ve) * exp2_int(-pe);
           c.q = exp2_int(-qe);
-          c.grow = 64.f * (vb * dtm) * exp2_int(max(-126, min(127, 15 - ke)));
+          // 64 max|V w| max|k|, in two steps: neither factor overflows alone
+          c.grow = wb * exp2_int((21 - ke) / 2) * exp2_int(21 - ke - (21 - ke) / 2);
           c.v = exp2_int(-ve);
           c.p = exp2_int(max(-126, min(127, 22 - qe - ke + pe)));
           c.skip = D * exp2_int(pe);
@@ -1276,7 +1284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Scales& sc = S.sc[i % kSlots][hl];
       const float4 sa = *reinterpret_cast<const float4*>(&sc.dec);  // dec, ds, o2, q
       [[maybe_unused]] const float f1 = s_back * sa.w, f2 = sa.z;
-      s_bound = fmaf(s_bound, sa.x, sc.grow);
+      s_bound = fminf(fmaf(s_bound, sa.x, sc.grow), kLargest);
       seg_dec *= sa.x;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {

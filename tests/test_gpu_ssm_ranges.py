@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import hybrid_linear_attention_gdn_gb300 as gdn
+import oracle
 from hybrid_linear_attention_gdn_gb300 import synth
 from oracle import state_space
 from helpers import assert_out_close, out_tol
@@ -156,3 +157,67 @@ def test_heads_of_different_sizes(cuda, big, small):
         st.pool.ssm[:, h] *= f
     st.opool.conv[:], st.opool.ssm[:] = f64(st.pool.conv), f64(st.pool.ssm)
     _check_heads(st, *_call(st, qkv, a))
+
+
+def _sum_of_terms(st, opool, qkv, a, h, ch):
+    """The readouts of head h's channel ch with every term's magnitude."""
+    p, sh, n, rows, out = st.oparams, st.shape, st.shape.hk * st.shape.dk, f64(qkv), []
+    hq, vc = h // (sh.hv // sh.hk), 2 * n + h * sh.dv + ch
+    cols = [hq * sh.dk + np.arange(sh.dk), n + hq * sh.dk + np.arange(sh.dk), np.array([vc])]
+    dt = np.logaddexp(0.0, f64(a)[:, h] + p.dt_bias[h])
+    for slot, lo, hi in zip(IDS, [0, LENS[0]], [LENS[0], sum(LENS)]):
+        x = np.concatenate([opool.conv[slot], rows[lo:hi]])
+        y = [sum(p.conv_w[c, j] * x[j:len(x) - sh.w + 1 + j, c] for j in range(sh.w)) + p.conv_bias[c] for c in cols]
+        q, k, v = (np.abs(f / (1 + np.exp(-f))) for f in y)
+        s = np.abs(opool.ssm[slot, h, ch])
+        for t in range(hi - lo):
+            s = np.exp(-np.exp(p.A_log[h]) * dt[lo + t]) * s + dt[lo + t] * v[t] * k[t]
+            out.append(s @ q[t] + (0.0 if p.D is None else abs(p.D[h]) * v[t, 0]))
+    return np.array(out)
+
+
+@pytest.mark.parametrize("wide_bound", [False, True])
+@pytest.mark.parametrize("scale", [1e30, 1e34, 1e36])
+@pytest.mark.parametrize("name", ["wide", "square"])
+def test_values_at_the_top_of_the_range(cuda, name, scale, wide_bound):
+    """A channel of head 0 with raw values up to some 1e36: bounds of |V| and
+    |S| pass the largest fp32 value, V, the state and the outputs do not.
+    wide_bound: another channel's taps are large, so that the bound of |V|
+    (largest tap sum times largest input) overflows by itself.
+
+    Head 0's rows are that one channel, not the dv of which a row's bound
+    takes the norm.  Its elements: q, k, G, P, V (or q and S) are rounded to
+    11 bits, 2^-12 of every term each, and the sum to bf16, 2^-8."""
+    st = SsmSetup(shape(name), seed=75, skip=not wide_bound)
+    c, ch = 2 * st.shape.hk * st.shape.dk, 5
+    if wide_bound:
+        st.params.conv_w[c + 2] = 60.0
+        st.oparams.conv_w[c + 2] = 60.0
+    qkv, a = st.tokens(sum(LENS))
+    qkv[:, c + ch] = (qkv[:, c + ch].float() * scale).to(qkv.dtype)
+    before = oracle.Pool(st.opool.ssm.copy(), st.opool.conv.copy())
+    with np.errstate(over="ignore"):
+        out, ref = _call(st, qkv, a)
+        terms = _sum_of_terms(st, before, qkv, a, 0, ch)
+    assert torch.isfinite(out).all()
+    got, want = f64(out[:, 0, ch]), ref[:, 0, ch]
+    assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 5.1 * 2.0 ** -12 * terms).all()
+    for h in range(1, st.shape.hv):
+        assert_out_close(out[:, h], ref[:, h], st.shape.dv, out_tol(st.shape), row_floor_rms=True)
+    _check_states(st, st.pool, st.opool)
+
+
+@pytest.mark.parametrize("name", ["wide", "square"])
+def test_rows_before_an_infinite_step(cuda, name):
+    """An infinite dt: the rows before it, in its own block of 64 too, keep
+    their values; from it on its head is not finite."""
+    st = SsmSetup(shape(name), seed=77, decay=(0.1, 1.0))
+    qkv, a = st.tokens(100)
+    a[50, 2] = float("inf")
+    with np.errstate(all="ignore"):
+        out, ref = _call(st, qkv, a, [3], [100], [0])
+    heads = [h for h in range(st.shape.hv) if h != 2]
+    for h, end in [(2, 50)] + [(h, 100) for h in heads]:
+        assert_out_close(out[:end, h], ref[:end, h], st.shape.dv, out_tol(st.shape), row_floor_rms=True)
+    assert not torch.isfinite(out[50:, 2]).any()
+    assert not torch.isfinite(st.pool.ssm[3, 2]).any() and torch.isfinite(st.pool.ssm[3, heads]).all()
