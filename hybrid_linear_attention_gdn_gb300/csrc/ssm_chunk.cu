@@ -34,7 +34,7 @@
 //   what is 2^-29 of it or less loses bits.  Where the product of two
 //   operands' largest magnitudes passes fp32 the result may be infinite though
 //   the largest do not meet.  Roundings: the output products' operands
-//   to 11 bits (a relative 2^-12 of their terms, against 2^-9 of the bf16
+//   to 11 bits (at most 2^-11 of their terms, against 2^-8 of the bf16
 //   output); the state's operands to two halves each, 22 bits, in three
 //   products.
 // The work per 64 x 128 V values is bound by the instructions of the
