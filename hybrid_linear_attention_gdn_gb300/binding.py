@@ -604,11 +604,16 @@ def ssm_prefill(dims: Dims, pool: StatePool, ckpt: StatePool | None, params: Ssm
                 start_pos, total_tokens: int, ckpt_ids, ckpt_block: int, qkv, a, out, workspace, dev_err=None,
                 stream=None):
     """Selective state space prefill: chunk_prefill's contract with every token
-    the step of ssm_decode_step.  ckpt and ckpt_ids may be None (no
-    checkpoints); workspace: ssm_prefill_workspace_size bytes."""
+    the step of ssm_decode_step.  ckpt and ckpt_ids [n_seq][max_ckpt] may be
+    None (no checkpoints); workspace: ssm_prefill_workspace_size bytes."""
     fn, L = "gdn_ssm_prefill", load()
     n_seq, total, dev, act = slot_ids.shape[0], int(total_tokens), _device(), dims.act_dtype
-    max_ckpt = int(ckpt_ids.shape[1]) if ckpt_ids is not None and ckpt_ids.dim() == 2 else 0
+    max_ckpt = 0
+    if ckpt_ids is not None:
+        if ckpt_ids.dim() != 2 or ckpt_ids.shape[0] != n_seq:
+            raise GdnError(fn, ERR_INVALID_ARG, f"ckpt_ids must be of shape ({n_seq}, max_ckpt), got "
+                                                f"{tuple(ckpt_ids.shape)}")
+        max_ckpt = int(ckpt_ids.shape[1])
     _require_pool(fn, "pool", dims, pool, dev)
     _require_ssm(fn, dims, params, dev)
     if max_ckpt:
