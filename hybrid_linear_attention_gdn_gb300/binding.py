@@ -650,7 +650,9 @@ def add_rmsnorm(x, residual, weight, eps: float = 1e-6, y=None, q8=None, scales=
         raise GdnError(fn, ERR_INVALID_ARG, "x and residual must be float32 or bfloat16")
     shape, dev = x.shape, _device()
     d = shape[-1]
-    rows = x.numel() // d if d else 0
+    if d == 0:
+        raise GdnError(fn, ERR_INVALID_ARG, f"rows of no values: x is {tuple(shape)}")
+    rows = x.numel() // d
     _require(fn, "x", x, x.dtype, shape, dev)
     if residual is not None:
         _require(fn, "residual", residual, residual.dtype, shape, dev)

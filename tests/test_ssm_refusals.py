@@ -47,3 +47,17 @@ def test_checkpoint_table_of_its_shape(cuda):
     ck = _prefill_with(st, lambda t: t, "cuda")
     assert (ck.ssm[0] != -5).all() and (ck.ssm[1] == -5).all()
     _prefill_with(st, lambda t: t[:, :0], "cuda")  # room for none
+
+
+@pytest.mark.parametrize("group", [0, 32])
+@pytest.mark.parametrize("device", ["cpu", pytest.param("cuda", marks=pytest.mark.gpu)])
+def test_norm_of_rows_of_nothing(device, group):
+    """Rows of no values have no norm; with an 8-bit output the scales' shape
+    divided by zero."""
+    if device == "cuda" and not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    e = lambda *s, dt=torch.float32: torch.zeros(s, device=device).to(dt)
+    for kw in ({}, dict(q8=e(3, 0, dt=torch.float8_e4m3fn), group=group)):
+        with pytest.raises(gdn.GdnError, match="no values") as err:
+            gdn.add_rmsnorm(e(3, 0), None, e(0), **kw)
+        assert err.value.status == binding.ERR_INVALID_ARG
