@@ -140,6 +140,7 @@ __global__ void __launch_bounds__(kThreads) batch_maps_kernel(const MapsArgs a) 
       const int64_t i = first + k;
       int32_t id = -1;
       if (i < done && len > 0) id = i >= have ? fresh(base + i - have) : table[(size_t)r * a.max_blocks + i];
+      if (i < done && len > 0 && i < have && id < 0) bad |= GDN_DEV_ERR_SLOT_OOB;
       GDN_GV(a.ckpt_ids, (long long)a.n_seq * a.max_ckpt)[(size_t)r * a.max_ckpt + k] = id < 0 ? -1 : id;
     }
   }

@@ -514,7 +514,8 @@ gdn_status gdn_add_rmsnorm(int32_t act_dtype, int32_t res_dtype, const void* x, 
  *                 max_tokens: the offsets stop at max_tokens
  *   GDN_DEV_ERR_BLOCKS   no free block left: that entry, its rows' slots and
  *                 its checkpoint are -1
- *   GDN_DEV_ERR_SLOT_OOB a held entry is negative: its rows' slots are -1
+ *   GDN_DEV_ERR_SLOT_OOB a held entry that a new row or a checkpoint needs is
+ *                 negative: its rows' slots and its checkpoint are -1
  * block a positive power of two; n_seq at most 8192 and max_tokens at most
  * 2^31 - 1, else GDN_ERR_UNSUPPORTED.  n_seq = 0 writes cu_seqlens[0],
  * *n_free_out and the rows' padding.
