@@ -73,9 +73,15 @@ constexpr int kDK = 128;  // state size
 constexpr int kRawRows = kC + 3;
 
 // ---- workspace ----------------------------------------------------------------
-// Sequence n's chunks occupy the slots from cu[n] / 64 + 2 n on: a sequence of
-// len tokens touches at most len / 64 + 2 chunks, so the ranges are disjoint
-// without a scan.  Its segments likewise: from that / seg_chunks + n on.
+// Sequence n's chunks occupy the slots from first_slot(cu[n], n) on.  A sequence
+// of len tokens touches at most min(len / 64 + 2, len) chunks, and both of the
+// numbers whose smaller one first_slot is grow by at least that much: the
+// ranges are disjoint without a scan, and no more than one slot per token.
+// Its segments likewise: from that / seg_chunks + n on.
+__host__ __device__ __forceinline__ int64_t first_slot(int64_t tokens, int64_t n) {
+  const int64_t by_chunk = tokens / kC + 2 * n;
+  return by_chunk < tokens ? by_chunk : tokens;
+}
 // One record per (chunk slot, group), of fp16 operands in the tensor core's
 // 128-byte swizzled layout:
 struct __align__(1024) Record {
@@ -116,13 +122,12 @@ __device__ __forceinline__ bool load_seq(const PrefillArgs& a, int n, Seq& s, bo
   bad = s.t0 < 0 || s.len < 0 || s.t0 + s.len > a.total || s.p0 < 0;
   if (bad) return false;
   s.nch = s.len ? (int)((s.p1 + kC - 1) / kC - s.p0 / kC) : 0;
-  s.first = s.t0 / kC + 2 * (int64_t)n;
+  s.first = first_slot(s.t0, n);
   return s.len > 0;
 }
-// The last sequence whose first slot (first(n) = (cu[n] / 64 + 2 n) / div + n
-// (div > 1) or cu[n] / 64 + 2 n (div 1)) is at most `slot`: one warp, 32
-// candidates at a time.  Offsets outside [0, total] end the search early,
-// never outside the array.
+// The last sequence whose first chunk slot, or segment slot (segs: chunk slot /
+// div + n), is at most `slot`: one warp, 32 candidates at a time.  Offsets
+// outside [0, total] end the search early, never outside the array.
 __device__ __forceinline__ int find_seq(const PrefillArgs& a, int64_t slot, int div, bool segs) {
   const auto cu = GDN_GV(a.cu_seqlens, a.n_seq + 1);
   const int lane = threadIdx.x & 31;
@@ -132,7 +137,7 @@ __device__ __forceinline__ int find_seq(const PrefillArgs& a, int64_t slot, int 
     const int i = lane * step;
     bool le = false;
     if (i < n) {
-      const int64_t c = (int64_t)cu[lo + i] / kC + 2 * (int64_t)(lo + i);
+      const int64_t c = first_slot(cu[lo + i], lo + i);
       le = (segs ? c / div + (lo + i) : c) <= slot;
     }
     const uint32_t m = __ballot_sync(0xffffffffu, le);
@@ -1407,7 +1412,7 @@ int64_t seg_chunks(int64_t tiles, int64_t n_seq, int64_t total) {
 
 Layout layout(const gdn_dims& d, int32_t n_seq, int64_t total) {
   Layout l;
-  l.n_chunks = total / kC + 2 * (int64_t)n_seq;
+  l.n_chunks = first_slot(total, n_seq);
   const int64_t tiles = (int64_t)d.hv * d.dv / 128;
   l.seg_chunks = (int32_t)seg_chunks(tiles, n_seq, total);
   l.n_segs = l.n_chunks / l.seg_chunks + n_seq;

@@ -440,6 +440,11 @@ gdn_status gdn_ssm_decode_step(const gdn_dims* dims, gdn_pool pool, const gdn_ss
  * it and no other sequence.  A zero decay (a = +inf gives dt = +inf) is not finite here:
  * the state takes dt k v^T as it is.
  *   workspace: >= gdn_ssm_prefill_workspace_size(...) bytes, 256-aligned
+ *   (57 KB per group and 64-token chunk of positions that a sequence touches,
+ *   counted as min(total_tokens / 64 + 2 n_seq, total_tokens) chunks: 252 MB
+ *   for 512 sequences of one token, 8 groups and 64 heads of 64; and where
+ *   sequences are cut
+ *   into segments a state per segment)
  *   (may be NULL where that is 0); nothing in it needs to be zero, and
  *   nothing is kept in it between calls, but calls that run at once (on two
  *   streams, or in two graphs that are replayed at once) need one each.
