@@ -19,16 +19,18 @@ __device__ __forceinline__ Gate gate(float A_log, float dt_bias, float a) {
 }
 
 // Kernel K's dynamic shared memory limit, raised on its first launch on a
-// device (`bytes` the same on every call).
+// device (`bytes` the same on every call).  Threads that come first together
+// each raise it.
 template <auto K>
 cudaError_t allow_smem(size_t bytes) {
-  static bool done[64] = {false};
+  static std::atomic<bool> done[64];
   int dev = 0;
-  cudaGetDevice(&dev);
+  const cudaError_t d = cudaGetDevice(&dev);
+  if (d != cudaSuccess) return d;
   const bool known = dev >= 0 && dev < 64;
-  if (known && done[dev]) return cudaSuccess;
+  if (known && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
   const cudaError_t e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (known && e == cudaSuccess) done[dev] = true;
+  if (known && e == cudaSuccess) done[dev].store(true, std::memory_order_release);
   return e;
 }
 
