@@ -424,7 +424,8 @@ typedef struct {
  * State space decode: one token per request, the state and conv history
  * updated in place in the working slot.  Arguments as for gdn_decode_step
  * (slot_ids distinct; a [B][hv] holds the time-step logits) without b.
- * hv / hk * dv above 8192 returns GDN_ERR_UNSUPPORTED.  B = 0 is a no-op.
+ * hv / hk * dv above 8192 or B above 65535 returns GDN_ERR_UNSUPPORTED.
+ * B = 0 is a no-op.
  */
 gdn_status gdn_ssm_decode_step(const gdn_dims* dims, gdn_pool pool, const gdn_ssm_params* params,
                                const int32_t* slot_ids, int32_t B, const void* qkv, const void* a,
@@ -438,13 +439,16 @@ gdn_status gdn_ssm_decode_step(const gdn_dims* dims, gdn_pool pool, const gdn_ss
  * checkpoints.  A NaN or an infinity among a sequence's inputs reaches its
  * outputs and state from that 64-token block of positions on, nothing before
  * it and no other sequence.  A zero decay (a = +inf gives dt = +inf) is not finite here:
- * the state takes dt k v^T as it is.
+ * the state takes dt k v^T as it is.  Above 65535 sequences, 2^31 - 1 tokens
+ * or 262140 checkpoints per sequence: GDN_ERR_UNSUPPORTED.  dk = 128, dv 64
+ * or 128, hv / hk * dv a multiple of 128, width 4, all bf16, 16-byte aligned
+ * qkv, out and conv_w take 64-token chunks on the tensor cores; every other
+ * form walks the tokens one after another (0.2 to 0.5 us each).
  *   workspace: >= gdn_ssm_prefill_workspace_size(...) bytes, 256-aligned
  *   (57 KB per group and 64-token chunk of positions that a sequence touches,
  *   counted as min(total_tokens / 64 + 2 n_seq, total_tokens) chunks: 252 MB
- *   for 512 sequences of one token, 8 groups and 64 heads of 64; and where
- *   sequences are cut
- *   into segments a state per segment)
+ *   for 512 sequences of one token, 8 groups and 64 heads of 64; and a state
+ *   per segment where sequences are cut)
  *   (may be NULL where that is 0); nothing in it needs to be zero, and
  *   nothing is kept in it between calls, but calls that run at once (on two
  *   streams, or in two graphs that are replayed at once) need one each.
@@ -464,6 +468,9 @@ gdn_status gdn_ssm_prefill(const gdn_dims* dims, gdn_pool pool, gdn_pool ckpt,
  *   h = x + residual;  residual <- h (rounded to its type)
  *   y = h / sqrt(mean(h^2) + eps) * weight
  * The norm is taken of the unrounded fp32 h.  Without a residual h = x.
+ * The sum of squares is held in fp32: a row whose squares sum past 3.4e38
+ * (values of some 1e17 to 1e19, by d) gets y = 0, and one whose squares all
+ * vanish beside eps = 0 (values below some 1e-20) infinities and NaN.
  *   x [n_rows][d] (act_dtype); residual [n_rows][d] (res_dtype), read and
  *   written, or NULL; weight [d] fp32; y [n_rows][d] (act_dtype) or NULL
  *   (y may be x: in place)
