@@ -28,22 +28,21 @@
 //   All operands are fp16 (kind::f16, four times the measured rate of
 //   kind::tf32 at the same 11 bits) after exact power-of-two scalings: by the
 //   largest |q| and |k| of a chunk and group, the largest |v| of a chunk and
-//   head, and by upper bounds of |v w|, |P| and |S| of a head.  A bound may be
-//   loose by 2^14: fp16 keeps 11 bits over 29 binades.  So inputs of any size
-//   do (tests from 1e-12 to 1e36), relative to the largest of their operand:
-//   what is 2^-29 of it or less loses bits.  Where the product of two
-//   operands' largest magnitudes passes fp32 the result may be infinite though
-//   the largest do not meet.  Roundings: the output products' operands
-//   to 11 bits (at most 2^-11 of their terms, against 2^-8 of the bf16
-//   output); the state's operands to two halves each, 22 bits, in three
-//   products.
+//   head, and by upper bounds of |v w|, |P| and |S| of a head.  fp16 keeps 11
+//   bits over 29 binades below the largest value or its bound (a bound may be
+//   loose by 2^14), so inputs of any size do (tests from 1e-12 to 1e36), and
+//   what is smaller yet than its chunk's largest loses bits.  Where the product
+//   of two operands' largest magnitudes passes fp32 the result may be infinite
+//   though the largest do not meet.  Roundings: the output products' operands
+//   to 11 bits (at most 2^-11 of their terms, against 2^-8 of the bf16 output);
+//   the state's operands to two halves each, 22 bits, in three products.
 // The work per 64 x 128 V values is bound by the instructions of the
 // elementwise steps (conv + SiLU, P, operand conversion), not by the products
 // (tensor pipe 24 % busy) or by memory.  Measured, 64 heads of 64 in 8 groups:
-// 4 x 8192 tokens 417 us (features 84, chain 333: 2.6 us per chunk; 112 us of
-// memory traffic), seven ragged sequences of 3,968 tokens 139 us, 37 tokens 21
+// 4 x 8192 tokens 418 us (features 85, chain 333: 2.6 us per chunk; 112 us of
+// memory traffic), seven ragged sequences of 3,968 tokens 141 us, 37 tokens 20
 // us in a graph; 32 heads in one group, 1 x 8192 tokens 97 us (features 10,
-// states of 8 segments 35, chains 52).
+// states of 8 segments 33, chains 54).
 //
 // Segments: where sequences times V tiles are too few for the SMs, each
 // sequence is cut into segments of seg_chunks chunks.  A first launch walks
@@ -1392,13 +1391,14 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Chunks per segment.  The lengths are on the device: the rule sees their sum.
 //  * Enough chains for the SMs (sequences x tiles >= 96): whole sequences.  The
-//    state pass costs about half as much again, and cutting only those longer
-//    than the mean gains on some mixes and loses on others (8-group layer: 7
-//    ragged sequences 143 us whole, 138 cut; 8 others 129 and 155; 8 x 1000
-//    tokens 151 and 159; 4 x 8192 449 and 458).
+//    state pass costs about half as much again (8-group layer, in a graph,
+//    whole and cut: 7 ragged sequences 126 and 134 us; 8 others of up to 1,931
+//    tokens 187 and 194; 8 x 1000 135 and 142; 3 x 8192 401 and 552; 4 x 8192
+//    417 and 668).
 //  * Few chunks in all (16, or 24 of several sequences): whole too, since the
-//    state pass costs more than it shortens (1 x 700 tokens 62 us cut, 47 whole;
-//    2 x 700 64 and 51; but 1 x 1500 65 and 85).
+//    state pass costs more than it shortens (1 x 700 tokens 43 us whole, 58
+//    cut; 1 x 1024 57 and 61; 1 x 1088 59 and 60; 1 x 1500 78 and 61; 2 x 768
+//    48 and 60; 2 x 1000 60 and 62: two sequences break even near 32 chunks).
 //  * Fewer chains: as many segments as fill the SMs, at most kMaxSegs per sequence
 //    of the mean length (a segment reads all its predecessors' states), and
 //    not below kMinSeg chunks.
