@@ -112,11 +112,17 @@ __device__ __forceinline__ uint32_t e4m3x2(float2 x) {
 // values in a million) the quotient is taken exactly: from p = h w and the
 // error e of that and of h, and those of the group's largest, m and me.  (The
 // product alone put some ten values in a million on the wrong side.)
-// 448 (p + e) / (m + me): the value in fp32 towards zero, its last bit set
-// where something is left, so that rounding to e4m3 is the only rounding
+// 448 (p + e) / (m + me): the fp32 value nearest to it, moved off a half of an
+// e4m3 step to the side of what is left, so that rounding to e4m3 is the only
+// rounding.  What is left is 448 p - z m and the errors' part.  On a half z has
+// five significant bits: the product's two pieces and z m cancel exactly, so
+// that where h w lost nothing (e = me = 0, as with 16-bit h and w) a quotient
+// that is the half stays on it.  (The remainder of the division instead, z and
+// t both rounded, moved those off to either side.)
 __device__ __forceinline__ float quotient(float p, float e, float m, float me, float im) {
-  const float t = p * im, r = fmaf(-t, m, p) + fmaf(-t, me, e), dt = r * im * 448.f;
-  const float z = fmaf(448.f, t, dt), rest = fmaf(448.f, t, -z) + dt;
+  const float t = p * im, r = fmaf(-t, m, p) + fmaf(-t, me, e);
+  const float z = fmaf(448.f, t, r * im * 448.f), a = __fmul_rn(448.f, p);
+  const float rest = (fmaf(-z, m, a) + fmaf(448.f, p, -a)) + fmaf(448.f, e, -__fmul_rn(z, me));
   const uint32_t u = __float_as_uint(z);
   if (rest == 0.f) return z;
   return __uint_as_float((u - ((u ^ __float_as_uint(rest)) >> 31)) | 1u);

@@ -485,8 +485,11 @@ gdn_status gdn_ssm_prefill(const gdn_dims* dims, gdn_pool pool, gdn_pool ckpt,
  *                     every y is 0
  *   q8 = y / scale rounded to nearest even, at most +-448; with an fp32 scale
  *   that is the exact quotient's nearest value, whatever y's and the scale's
- *   own roundings (for a largest |y| between 1e-23 and 1e23).  A NaN among a
- *   group's y makes its scale NaN (byte 255) and every q8 of the group NaN.
+ *   own roundings (for a largest |y| between 1e-23 and 1e23; a quotient half
+ *   way between two values goes to the even one where h and h * weight are
+ *   exact in fp32, as with 16-bit h and weight, elsewhere to either).  A NaN
+ *   among a group's y makes its scale NaN (byte 255) and every q8 of the group
+ *   NaN.
  * d at most 32768, else GDN_ERR_UNSUPPORTED; n_rows = 0 launches nothing.
  * No alignment beyond the element types' own is required; 16-byte aligned
  * tensors with d a multiple of 8 take vector accesses.

@@ -1,5 +1,5 @@
-"""The state space prefill's range, segment and workspace tests and the maps'
-errors under the bounds-checked build."""
+"""The state space prefill's range, segment and workspace tests, the maps'
+errors and the norm's halves under the bounds-checked build."""
 import os
 import re
 
@@ -10,7 +10,7 @@ from test_gpu_debug_bounds import _child, debug_lib  # noqa: F401
 pytestmark = pytest.mark.gpu
 
 FILES = ["test_gpu_ssm_ranges.py", "test_gpu_ssm_segments.py", "test_ssm_workspace.py", "test_ssm_refusals.py",
-         "test_gpu_batch_maps_errors.py"]
+         "test_gpu_batch_maps_errors.py", "test_gpu_add_rmsnorm_ties.py"]
 
 
 def test_ranges_and_segments_under_the_checked_build(debug_lib):  # noqa: F811
