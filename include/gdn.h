@@ -435,15 +435,18 @@ gdn_status gdn_ssm_decode_step(const gdn_dims* dims, gdn_pool pool, const gdn_ss
  * State space prefill: the contract of gdn_chunk_prefill (packed sequences
  * from any start position, block-aligned checkpoints of SSM state and conv
  * history, final state into the working slot, rows outside the sequences not
- * written) with every token the step above.  fp32 accuracy of states and
- * checkpoints.  A NaN or an infinity among a sequence's inputs reaches its
- * outputs and state from that 64-token block of positions on, nothing before
- * it and no other sequence.  A zero decay (a = +inf gives dt = +inf) is not finite here:
- * the state takes dt k v^T as it is.  Above 65535 sequences, 2^31 - 1 tokens
- * or 262140 checkpoints per sequence: GDN_ERR_UNSUPPORTED.  dk = 128, dv 64
- * or 128, hv / hk * dv a multiple of 128, width 4, all bf16, 16-byte aligned
- * qkv, out and conv_w take 64-token chunks on the tensor cores; every other
- * form walks the tokens one after another (0.2 to 0.5 us each).
+ * written) with every token the step above.
+ * dk = 128, dv 64 or 128, hv / hk * dv a multiple of 128, width 4, all bf16,
+ * 16-byte aligned qkv, out and conv_w take 64-token blocks of positions on the
+ * tensor cores; every other form walks the tokens one after another (0.2 to
+ * 0.5 us each).  States and checkpoints have fp32's accuracy, in the block
+ * form against the largest dt |k| |v| of a head's block (what is 2^-37 of it or
+ * less is lost); its outputs have 11-bit operands (2^-11 of every term).
+ * A NaN or an infinity among a sequence's inputs reaches its outputs and state
+ * from that 64-token block of positions on, nothing before it and no other
+ * sequence.  A zero decay (a = +inf gives dt = +inf) is not finite here: the
+ * state takes dt k v^T as it is.  Above 65535 sequences, 2^31 - 1 tokens or
+ * 262140 checkpoints per sequence: GDN_ERR_UNSUPPORTED.
  *   workspace: >= gdn_ssm_prefill_workspace_size(...) bytes, 256-aligned
  *   (57 KB per group and 64-token chunk of positions that a sequence touches,
  *   counted as min(total_tokens / 64 + 2 n_seq, total_tokens) chunks: 252 MB
