@@ -820,9 +820,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         b[1] += __shfl_sync(0xffffffffu, b[0], 31);
         const float back = __shfl_sync(0xffffffffu, suf[1], 0), all = back + __shfl_sync(0xffffffffu, suf[0], 0);
-        float dtm = fmaxf(dt[0] <= kLargest ? dt[0] : 0.f, dt[1] <= kLargest ? dt[1] : 0.f);  // the finite ones
-#pragma unroll
-        for (int o = 16; o; o >>= 1) dtm = fmaxf(dtm, __shfl_xor_sync(0xffffffffu, dtm, o));
         const float nx = __shfl_down_sync(0xffffffffu, suf[0], 1), ny = __shfl_down_sync(0xffffffffu, suf[1], 1);
         suf[0] = (lane < 31 ? nx : 0.f) + back;
         suf[1] = lane < 31 ? ny : 0.f;
@@ -834,18 +831,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           b[e] *= 1.4426950408889634f;
           vj[e] = ex2(__shfl_sync(0xffffffffu, b[e], lane | 15) - b[e]) * dt[e];
         }
+        // the largest finite dt and weight (a weight only decays from its dt:
+        // where the decay is strong, the state holds what the last tokens
+        // gave, however small beside the largest dt)
+        auto largest = [](float x, float y) {
+          const float m = fmaxf(x <= kLargest ? x : 0.f, y <= kLargest ? y : 0.f);
+          return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+        };
+        const float dtm = largest(dt[0], dt[1]), wm = largest(wj[0], wj[1]);
         // Chunk i's raw rows and G have landed: chunk i - 3's were read by
         // every compute warp, whose chunk i - 5 was done before that, so the
         // slot of chunk i - 6 may be written.
         const bool in_time = mbar_wait(&S.hx[ring(i)], phase(i)) && mbar_wait(&S.g_bar[ring(i)], phase(i));
         if (!(ok = __all_sync(0xffffffffu, in_time))) break;
         const int buf = i % kSlots, qe = S.g[ring(i)].meta[0], ke = S.g[ring(i)].meta[1];
-        // |V| <= vb, |V w| <= vb max dt,
+        // |V| <= vb, |V w| <= vb max w,
         // |P| <= 128 max|q| max|k| max dt + |D| < 2^(37 - qe - ke) max dt + |D|,
         // each of the two below 2^(14 - pe).  A bound that passes the largest
         // fp32 value is that value: what is finite is no larger.
         const float vb = fminf(fmaf(S.vgain[hh], S.xmax[ring(i)][hh], S.vbias[hh]), kLargest);
-        const float wb = fminf(vb * dtm, kLargest);
+        const float wb = fminf(vb * wm, kLargest);
         const int ve = scale_exp(__float_as_uint(vb));
         const int we = max(ve - 126, min(ve + 126, scale_exp(__float_as_uint(wb))));
         const int pe =

@@ -440,8 +440,9 @@ gdn_status gdn_ssm_decode_step(const gdn_dims* dims, gdn_pool pool, const gdn_ss
  * 16-byte aligned qkv, out and conv_w take 64-token blocks of positions on the
  * tensor cores; every other form walks the tokens one after another (0.2 to
  * 0.5 us each).  States and checkpoints have fp32's accuracy, in the block
- * form against the largest dt |k| |v| of a head's block (what is 2^-37 of it or
- * less is lost); its outputs have 11-bit operands (2^-11 of every term).
+ * form against max |k| max |v| max (dt, decayed to the block's end) of a head's
+ * block (what is 2^-37 of that or less is lost); its outputs have 11-bit
+ * operands (2^-11 of every term).
  * A NaN or an infinity among a sequence's inputs reaches its outputs and state
  * from that 64-token block of positions on, nothing before it and no other
  * sequence.  A zero decay (a = +inf gives dt = +inf) is not finite here: the

@@ -221,3 +221,22 @@ def test_rows_before_an_infinite_step(cuda, name):
         assert_out_close(out[:end, h], ref[:end, h], st.shape.dv, out_tol(st.shape), row_floor_rms=True)
     assert not torch.isfinite(out[50:, 2]).any()
     assert not torch.isfinite(st.pool.ssm[3, 2]).any() and torch.isfinite(st.pool.ssm[3, heads]).all()
+
+
+@pytest.mark.parametrize("name", ["wide", "square"])
+@pytest.mark.parametrize("T", [64, 150])
+def test_small_steps_after_a_strong_decay(cuda, name, T):
+    """Heads that forget within a token, with time steps between 1e-5 and 60
+    in a block: the state is what the last, small steps gave."""
+    st = SsmSetup(shape(name), seed=78)
+    for p in (st.params, st.oparams):
+        p.A_log[::2] = 30.0
+        p.dt_bias[:] = 0.0
+    qkv, a = st.tokens(T)
+    a[:] = torch.where(torch.rand(a.shape, generator=st.gen) < 0.2, 60.0, -2.0 + a.float()).to(a.dtype)
+    a[-6:] = -11.0
+    out, ref = _call(st, qkv, a, [3], [T], [0])
+    # (the few rows of large steps hold a head's norm, where bf16's rounding
+    # alone may reach 2^-8: the whole tensor, not head by head)
+    assert_out_close(out, ref, st.shape.dv, out_tol(st.shape), row_floor_rms=True)
+    _check_states(st, st.pool, st.opool)
