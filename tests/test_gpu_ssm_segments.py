@@ -158,3 +158,42 @@ def test_prompt_in_pieces_equals_whole(cuda, name):
     # 43 chunks and five joins: 569 roundings of 2^-24
     assert max_rel_l2(f64(st.pool.ssm), st.opool.ssm, sh.dv * sh.dk) <= 569 * 2.0 ** -24
     assert conv_bits_equal(st.pool.conv, st.opool.conv)
+
+
+def test_cut_call_captured_and_replayed(cuda):
+    """A cut prefill, its checkpoints in free slots of the working pool, and a
+    decode step behind it in one graph, replayed on new inputs: the eager
+    calls' results, with a workspace that holds what the last replay left."""
+    sh, lens = shape("wide", num_slots=24), [1100, 600]
+    T = sum(lens)
+    assert _cut(sh, 2, T)
+    st, ref = SsmSetup(sh, seed=86), SsmSetup(sh, seed=86)
+    start = st.pool.ssm.clone(), st.pool.conv.clone()
+    ids, cu, sp = _i32([1, 4]), _i32([0, lens[0], T]), torch.tensor([0, 30], device="cuda")
+    table = _i32([[5, 6, 7, 8, 9, 10, 11, 12], [13, 14, 15, 16, -1, -1, -1, -1]])
+    qkv, a = (t.cuda() for t in st.tokens(T))
+
+    def step(s, ws, out, tok):
+        gdn.ssm_prefill(s.dims, s.pool, s.pool, s.params, ids, cu, sp, T, table, 128, qkv, a, out, ws)
+        gdn.ssm_decode_step(s.dims, s.pool, s.params, ids, qkv[:2], a[:2], tok)
+
+    size = gdn.ssm_prefill_workspace_size(st.dims, 2, T)
+    ws = [torch.full((size,), 0xff, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    out = [torch.zeros((T, sh.hv, sh.dv), dtype=sh.act_dtype, device="cuda") for _ in range(2)]
+    tok = [torch.zeros((2, sh.hv, sh.dv), dtype=sh.act_dtype, device="cuda") for _ in range(2)]
+    step(ref, ws[1], out[1], tok[1])  # loads the kernels
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        step(st, ws[0], out[0], tok[0])
+    for seed in range(3):
+        gen = torch.Generator().manual_seed(seed)
+        qkv.copy_(torch.randn(qkv.shape, generator=gen))
+        for s in (st, ref):
+            s.pool.ssm.copy_(start[0]), s.pool.conv.copy_(start[1])
+        g.replay()
+        step(ref, ws[1], out[1], tok[1])
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], out[1]) and torch.equal(tok[0], tok[1])
+        assert torch.equal(st.pool.ssm, ref.pool.ssm) and torch.equal(st.pool.conv, ref.pool.conv)
+        assert torch.equal(st.pool.ssm[[0, 2, 3, 17]], start[0][[0, 2, 3, 17]])  # no other slot
