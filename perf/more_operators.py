@@ -255,9 +255,8 @@ def _handles(gdn, s):
         s["ws"] = torch.empty(max(size, 16), dtype=torch.uint8, device=DEV)
     if s["op"] in ("branch", "compact"):
         s["cache"] = gdn.PagePlanes(s["planes"])
-        size = gdn.block_release_workspace_size(s["blocks"]) if s["op"] == "branch" \
-            else gdn.block_compact_workspace_size(s["blocks"])
-        s["ws"] = torch.empty(max(size, 16), dtype=torch.uint8, device=DEV)
+    if s["op"] == "compact":
+        s["ws"] = torch.empty(gdn.block_compact_workspace_size(s["blocks"]), dtype=torch.uint8, device=DEV)
     s["ready"] = True
 
 
@@ -299,7 +298,7 @@ def _own_call(s):
         gdn.page_copy(s["cache"], s["copy_src"], s["copy_dst"])
         s["child_table"].copy_(s["table"][-s["n"]:])
         gdn.block_release(s["dst_rows"], s["lens"], s["none"], s["block"], s["table"], s["refs"], s["free"],
-                          s["n_free"], s["ws"])
+                          s["n_free"])
     else:
         gdn.block_compact(s["table"], s["refs"], s["free"], s["n_free"], s["move_src"], s["move_dst"], s["n_moves"],
                           s["ws"], table_out=s["table_out"], refs_out=s["refs_out"], free_out=s["free_out"])
