@@ -9,5 +9,8 @@ from .binding import (  # noqa: F401
     slot_zero, BoundsError, debug_bounds, debug_bounds_take, selftest_bounds,
     DEV_ERR_BLOCKS, DEV_ERR_SEQLENS, K_ADD_RMSNORM, K_BATCH_MAPS, K_SSM_DECODE, K_SSM_PREFILL, SCALE_E8M0, SCALE_F32,
     SsmParams, add_rmsnorm, batch_maps, ssm_decode_step, ssm_prefill, ssm_prefill_workspace_size,
+    K_BLOCK_COMPACT, K_BLOCK_FORK, K_BLOCK_RELEASE, K_LIN_DECODE, K_LIN_PREFILL, K_PAGE_COPY, K_QK_NORM_ROPE,
+    PagePlanes, block_compact, block_compact_workspace_size, block_fork, block_release, lin_decode_step, lin_prefill,
+    lin_prefill_workspace_size, page_copy, qk_norm_rope,
     spec_commit, spec_commit_index, spec_verify, state_pack, state_record_bytes, state_unpack,
 )

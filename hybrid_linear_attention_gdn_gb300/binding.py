@@ -23,8 +23,9 @@ DEV_ERR_SLOT_OOB, DEV_ERR_TIMEOUT, DEV_ERR_SEQLENS, DEV_ERR_BLOCKS = 1, 2, 4, 8
 SCALE_F32, SCALE_E8M0 = 0, 1
 (K_DECODE, K_SPEC_VERIFY, K_SLOT_COPY, K_SLOT_ZERO, K_SPEC_COMMIT, K_PREFILL, K_COMMIT_INDEX,
  K_STATE_PACK, K_GATED_RMSNORM, K_KDA_DECODE, K_KDA_VERIFY, K_KDA_PREFILL, K_MIXED, K_SSM_DECODE,
- K_SSM_PREFILL, K_ADD_RMSNORM, K_BATCH_MAPS) = range(17)
-K_COUNT = 17
+ K_SSM_PREFILL, K_ADD_RMSNORM, K_BATCH_MAPS, K_LIN_DECODE, K_LIN_PREFILL, K_QK_NORM_ROPE, K_PAGE_COPY,
+ K_BLOCK_FORK, K_BLOCK_RELEASE, K_BLOCK_COMPACT) = range(24)
+K_COUNT = 24
 
 _DT_CODE = {torch.float32: F32, torch.bfloat16: BF16}
 
@@ -57,6 +58,14 @@ class CParams(ctypes.Structure):
 class CSsmParams(ctypes.Structure):
     _fields_ = [("conv_w", ctypes.c_void_p), ("conv_bias", ctypes.c_void_p), ("A_log", ctypes.c_void_p),
                 ("dt_bias", ctypes.c_void_p), ("D", ctypes.c_void_p)]
+
+
+class CRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class CPages(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("page", ctypes.c_int64), ("row", ctypes.c_int64), ("head", ctypes.c_int64)]
 
 
 _P = ctypes.c_void_p
@@ -97,6 +106,18 @@ EXPORTS = {
     "gdn_add_rmsnorm": ([_I32, _I32, _P, _P, _P, ctypes.c_float, _I64, _I32, _P, _P, _P, _I32, _I32, _P], _I32),
     "gdn_batch_maps": ([_P, _P, _I32, _I32, _P, _I32, _P, _I32, _P, _P, _P, _P, _I32, _P, _P, _P, _I64, _P, _P],
                        _I32),
+    "gdn_lin_decode_step": ([_PD, CPool, _P, ctypes.c_float, _P, _I32, _P, _P, _P, _P], _I32),
+    "gdn_lin_prefill_workspace_size": ([_PD, _I32, _I64], ctypes.c_size_t),
+    "gdn_lin_prefill": ([_PD, CPool, CPool, _P, ctypes.c_float, _P, _P, _P, _I32, _I64, _P, _I32, _I32, _P, _P, _P,
+                         ctypes.c_size_t, _P, _P], _I32),
+    "gdn_qk_norm_rope": ([_I32, _I32, _I32, _I32, _I32, _I32, _I64, CRows, CRows, CRows, _P, _P, ctypes.c_float, _P,
+                          _I64, _I32, _I32, _P, CRows, CRows, CPages, CPages, _I32, _I32, _P, _P, _P], _I32),
+    "gdn_block_fork": ([_P, _P, _P, _I32, _I32, _P, _I32, _I32, _P, _I32, _P, _I32, _P, _P, _P, _P, _P, _P], _I32),
+    "gdn_block_release": ([_P, _P, _P, _I32, _I32, _P, _I32, _I32, _P, _I32, _P, _I32, _P, _P, _P, _P], _I32),
+    "gdn_block_compact_workspace_size": ([_I32], ctypes.c_size_t),
+    "gdn_block_compact": ([_P, _P, _I64, _P, _P, _I32, _P, _P, _I32, _P, _P, _P, _I32, _P, _P, ctypes.c_size_t, _P, _P],
+                          _I32),
+    "gdn_page_copy": ([_P, _I32, _I64, _I64, _I32, _P, _P, _I32, _P, _P], _I32),
     "gdn_selftest_wait_timeout": ([_P, _P], _I32),
     "gdn_status_string": ([_I32], ctypes.c_char_p),
     "gdn_launch_count": ([_I32], ctypes.c_uint64),
@@ -228,17 +249,18 @@ class Dims:
 
 @dataclass
 class StatePool:
-    """Device pool: ssm [N][HV][DV][DK] fp32, conv [N][W-1][C]."""
+    """Device pool: ssm [N][HV][DV][DK] fp32, conv [N][W-1][C] (None: no conv
+    history, conv_width 1)."""
 
     ssm: torch.Tensor
-    conv: torch.Tensor
+    conv: torch.Tensor | None = None
 
     @property
     def num_slots(self) -> int:
         return self.ssm.shape[0]
 
     def c(self) -> CPool:
-        key = (self.ssm.data_ptr(), self.conv.data_ptr(), self.ssm.shape[0])
+        key = (self.ssm.data_ptr(), self.conv.data_ptr() if self.conv is not None else None, self.ssm.shape[0])
         cached = self.__dict__.get("_c")
         if cached is None or cached[0] != key:
             cached = (key, CPool(*key))
@@ -248,6 +270,8 @@ class StatePool:
     @staticmethod
     def empty(dims: Dims, num_slots: int, device="cuda") -> "StatePool":
         ssm = torch.empty((num_slots, dims.hv, dims.dv, dims.dk), dtype=torch.float32, device=device)
+        if dims.conv_width == 1:
+            return StatePool(ssm)
         conv = torch.empty((num_slots, dims.conv_width - 1, dims.channels), dtype=dims.conv_dtype,
                            device=device)
         return StatePool(ssm, conv)
@@ -319,6 +343,10 @@ def _device() -> int:
 def _require_pool(fn: str, what: str, dims: Dims, pool: StatePool, device: int):
     n = pool.num_slots
     _require(fn, what + ".ssm", pool.ssm, torch.float32, (n, dims.hv, dims.dv, dims.dk), device)
+    if pool.conv is None and dims.conv_width == 1:
+        return
+    if pool.conv is None:
+        raise GdnError(fn, ERR_INVALID_ARG, f"{what} has no conv history, conv_width {dims.conv_width} needs one")
     _require(fn, what + ".conv", pool.conv, dims.conv_dtype, (n, dims.conv_width - 1, dims.channels), device)
 
 
@@ -713,6 +741,285 @@ def batch_maps(new_lens, start_pos, block: int, block_table, free_ids, n_free, c
                           int(block_table.shape[-1]), _ptr(free_ids), free_ids.numel(), _ptr(n_free),
                           _ptr(n_free_out), _ptr(cu_seqlens), _ptr(ckpt_ids), max_ckpt, _ptr(seq_ids),
                           _ptr(positions), _ptr(slot_map), rows, _ptr(dev_err), _stream(stream, dev))
+    _check(fn, st)
+
+
+def _require_ckpt(fn: str, dims: Dims, ckpt, ckpt_ids, n_seq: int, device: int) -> int:
+    """The columns of the checkpoint table (0 without one), checked."""
+    if ckpt_ids is None:
+        return 0
+    if ckpt_ids.dim() != 2 or ckpt_ids.shape[0] != n_seq:
+        raise GdnError(fn, ERR_INVALID_ARG, f"ckpt_ids must be of shape ({n_seq}, max_ckpt), got "
+                                            f"{tuple(ckpt_ids.shape)}")
+    max_ckpt = int(ckpt_ids.shape[1])
+    if max_ckpt:
+        if ckpt is None:
+            raise GdnError(fn, ERR_INVALID_ARG, "ckpt_ids without a checkpoint pool")
+        _require_pool(fn, "ckpt", dims, ckpt, device)
+        _require(fn, "ckpt_ids", ckpt_ids, torch.int32, (n_seq, max_ckpt), device)
+    return max_ckpt
+
+
+def lin_decode_step(dims: Dims, pool: StatePool, log_decay, slot_ids, qkv, out, scale: float = 1.0, dev_err=None,
+                    stream=None):
+    """Linear attention with a fixed decay per head, one token per request:
+    S <- exp(log_decay) S + k v^T in place, out = scale S^T q; dims.conv_width
+    1, log_decay [hv] fp32, qkv [B][C] ordered q | k | v, out [B][hv][dv]."""
+    fn, L = "gdn_lin_decode_step", load()
+    B, dev, act = slot_ids.shape[0], _device(), dims.act_dtype
+    _require_pool(fn, "pool", dims, pool, dev)
+    _require(fn, "log_decay", log_decay, torch.float32, (dims.hv,), dev)
+    _require(fn, "slot_ids", slot_ids, torch.int32, (B,), dev)
+    _require(fn, "qkv", qkv, act, (B, dims.channels), dev)
+    _require(fn, "out", out, act, (B, dims.hv, dims.dv), dev)
+    _require_err(fn, dev_err, dev)
+    st = L.gdn_lin_decode_step(ctypes.byref(dims.c()), pool.c(), _ptr(log_decay), float(scale), _ptr(slot_ids), B,
+                               _ptr(qkv), _ptr(out), _ptr(dev_err), _stream(stream, dev))
+    _check(fn, st)
+
+
+def lin_prefill_workspace_size(dims: Dims, n_seq: int, total_tokens: int) -> int:
+    return int(load().gdn_lin_prefill_workspace_size(ctypes.byref(dims.c()), int(n_seq), int(total_tokens)))
+
+
+def lin_prefill(dims: Dims, pool: StatePool, ckpt: StatePool | None, log_decay, slot_ids, cu_seqlens, start_pos,
+                total_tokens: int, ckpt_ids, ckpt_block: int, qkv, out, workspace, scale: float = 1.0, dev_err=None,
+                stream=None):
+    """Its prefill: chunk_prefill's contract with every token the step of
+    lin_decode_step.  ckpt and ckpt_ids [n_seq][max_ckpt] may be None (no
+    checkpoints); workspace: lin_prefill_workspace_size bytes (None where 0)."""
+    fn, L = "gdn_lin_prefill", load()
+    n_seq, total, dev, act = slot_ids.shape[0], int(total_tokens), _device(), dims.act_dtype
+    _require_pool(fn, "pool", dims, pool, dev)
+    max_ckpt = _require_ckpt(fn, dims, ckpt, ckpt_ids, n_seq, dev)
+    _require(fn, "log_decay", log_decay, torch.float32, (dims.hv,), dev)
+    _require(fn, "slot_ids", slot_ids, torch.int32, (n_seq,), dev)
+    _require(fn, "cu_seqlens", cu_seqlens, torch.int32, (n_seq + 1,), dev)
+    _require(fn, "start_pos", start_pos, torch.int64, (n_seq,), dev)
+    _require(fn, "qkv", qkv, act, (total, dims.channels), dev)
+    _require(fn, "out", out, act, (total, dims.hv, dims.dv), dev)
+    if workspace is not None:
+        _require(fn, "workspace", workspace, workspace.dtype, workspace.shape, dev)
+    _require_err(fn, dev_err, dev)
+    ck = ckpt.c() if ckpt is not None else CPool(None, None, 0)
+    st = L.gdn_lin_prefill(ctypes.byref(dims.c()), pool.c(), ck, _ptr(log_decay), float(scale), _ptr(slot_ids),
+                           _ptr(cu_seqlens), _ptr(start_pos), n_seq, total, _ptr(ckpt_ids) if max_ckpt else None,
+                           max_ckpt, int(ckpt_block), _ptr(qkv), _ptr(out), _ptr(workspace),
+                           _nbytes(workspace) if workspace is not None else 0, _ptr(dev_err), _stream(stream, dev))
+    _check(fn, st)
+
+
+def _rows(fn: str, what: str, t, dtype, shape, device: int) -> CRows:
+    """t [rows][heads][width] as gdn_rows: any strides, a head's values consecutive."""
+    if t is None:
+        return CRows(None, 0, 0)
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise GdnError(fn, ERR_INVALID_ARG, f"{what} must be a {dtype} tensor of shape {tuple(shape)} with consecutive "
+                                            f"head values, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}")
+    if t.get_device() != device:
+        raise GdnError(fn, ERR_INVALID_ARG, f"{what} is on {t.device}, not on the current CUDA device")
+    return CRows(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _overlap(t) -> bool:
+    """Whether different elements of t may share memory."""
+    need = 1
+    for size, stride in sorted(((n, s) for n, s in zip(t.shape, t.stride()) if n > 1), key=lambda p: p[1]):
+        if stride < need:
+            return True
+        need = stride * size
+    return False
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float = 1e-6, interleaved: bool = False,
+                 q_out=None, k_out=None, v=None, k_cache=None, v_cache=None, slot_map=None, dev_err=None, stream=None):
+    """RMS norm per head (weights [d] fp32; None: no norm), rotation by
+    position (cos_sin [max_pos][rot] fp32, cosines first) of q [rows][hq][d]
+    and k [rows][hk][d], and with a slot_map [rows] the write of k and v
+    [rows][hv][dv] to k_cache and v_cache [pages][block][heads][width] (see
+    gdn_qk_norm_rope).  All may be views of any strides with consecutive head
+    values (permute a cache that is kept by heads).  q_out defaults to q, k_out
+    to k without a cache (in place); with one, k is written to k_out only where
+    that is given.  q or k may be None.  Returns (q_out, k_out)."""
+    fn, L = "gdn_qk_norm_rope", load()
+    x = q if q is not None else k
+    if x is None or x.dim() != 3 or x.dtype not in _DT_CODE or (k is not None and k.dim() != 3):
+        raise GdnError(fn, ERR_INVALID_ARG, "q and k must be float32 or bfloat16 tensors [rows][heads][d]")
+    act, dev, (rows, _, d) = x.dtype, _device(), x.shape
+    hq, hk = (0 if t is None else int(t.shape[1]) for t in (q, k))
+    if cos_sin.dim() != 2:
+        raise GdnError(fn, ERR_INVALID_ARG, f"cos_sin must be of shape (max_pos, rot), got {tuple(cos_sin.shape)}")
+    if q_out is None:
+        q_out = q
+    if k_out is None and slot_map is None:
+        k_out = k
+    a = [_rows(fn, "q", q, act, (rows, hq, d), dev), _rows(fn, "k", k, act, (rows, hk, d), dev)]
+    o = [_rows(fn, "q_out", q_out, act, (rows, hq, d), dev), _rows(fn, "k_out", k_out, act, (rows, hk, d), dev)]
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _require(fn, name, w, torch.float32, (d,), dev)
+    _require(fn, "cos_sin", cos_sin, torch.float32, cos_sin.shape, dev)
+    _require(fn, "positions", positions, torch.int64, (rows,), dev)
+    cv, pages, pages_n, block, hv, dv = CRows(None, 0, 0), [CPages(None, 0, 0, 0)] * 2, 0, 1, 0, 0
+    if slot_map is not None:
+        _require(fn, "slot_map", slot_map, torch.int64, (rows,), dev)
+        if k is None or k_cache is None or (v is None) != (v_cache is None):
+            raise GdnError(fn, ERR_INVALID_ARG, "a slot_map needs k and k_cache, and v with v_cache")
+        if v is not None:
+            if v.dim() != 3:
+                raise GdnError(fn, ERR_INVALID_ARG, f"v must be of shape (rows, hv, dv), got {tuple(v.shape)}")
+            hv, dv = int(v.shape[1]), int(v.shape[2])
+            cv = _rows(fn, "v", v, act, (rows, hv, dv), dev)
+        pages = []
+        for name, t, h, w in (("k_cache", k_cache, hk, d), ("v_cache", v_cache, hv, dv)):
+            if t is None:
+                pages.append(CPages(None, 0, 0, 0))
+                continue
+            want = (k_cache.shape[0], k_cache.shape[1], h, w)
+            if t.dtype != act or t.dim() != 4 or tuple(t.shape) != want or (w > 1 and t.stride(3) != 1) or _overlap(t):
+                raise GdnError(fn, ERR_INVALID_ARG, f"{name} must be a {act} tensor of shape {want} with consecutive "
+                                                    f"head values, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}")
+            if t.get_device() != dev:
+                raise GdnError(fn, ERR_INVALID_ARG, f"{name} is on {t.device}, not on the current CUDA device")
+            pages.append(CPages(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2)))
+        pages_n, block = int(k_cache.shape[0]), int(k_cache.shape[1])
+    elif k_cache is not None or v_cache is not None:
+        raise GdnError(fn, ERR_INVALID_ARG, "a cache without a slot_map")
+    for name, t in (("q_out", q_out), ("k_out", k_out)):
+        if t is not None and _overlap(t):
+            raise GdnError(fn, ERR_INVALID_ARG, f"{name}'s rows overlap: strides {t.stride()}")
+    _require_err(fn, dev_err, dev)
+    st = L.gdn_qk_norm_rope(_DT_CODE[act], hq, hk, int(d), hv, dv, int(rows), a[0], a[1], cv, _ptr(q_weight),
+                            _ptr(k_weight), float(eps), _ptr(cos_sin), int(cos_sin.shape[0]), int(cos_sin.shape[1]),
+                            int(bool(interleaved)), _ptr(positions), o[0], o[1], pages[0], pages[1], pages_n, block,
+                            _ptr(slot_map), _ptr(dev_err), _stream(stream, dev))
+    _check(fn, st)
+    return q_out, k_out
+
+
+def _require_blocks(fn: str, block_table, refs, free_ids, n_free, device: int):
+    i32 = torch.int32
+    if block_table.dim() != 2:
+        raise GdnError(fn, ERR_INVALID_ARG, f"block_table must be of shape (rows, max_blocks), got "
+                                            f"{tuple(block_table.shape)}")
+    _require(fn, "block_table", block_table, i32, block_table.shape, device)
+    _require(fn, "refs", refs, i32, (refs.numel(),), device)
+    _require(fn, "free_ids", free_ids, i32, (free_ids.numel(),), device)
+    _require(fn, "n_free", n_free, i32, (1,), device)
+
+
+def block_fork(src_rows, dst_rows, lens, block: int, block_table, refs, free_ids, n_free, copy_src, copy_dst,
+               n_free_out=None, dev_err=None, stream=None):
+    """Row dst_rows[i] of the block table becomes a branch of row src_rows[i],
+    which holds lens[i] tokens: whole blocks shared (refs counts their further
+    holders), a partly filled last one new from the stack, with the pages to
+    copy in copy_src and copy_dst [n] (see gdn_block_fork)."""
+    fn, L, dev, i32 = "gdn_block_fork", load(), _device(), torch.int32
+    n = src_rows.shape[0]
+    if n_free_out is None:
+        n_free_out = n_free
+    _require_blocks(fn, block_table, refs, free_ids, n_free, dev)
+    _require(fn, "src_rows", src_rows, i32, (n,), dev)
+    _require(fn, "dst_rows", dst_rows, i32, (n,), dev)
+    _require(fn, "lens", lens, torch.int64, (n,), dev)
+    _require(fn, "n_free_out", n_free_out, i32, (1,), dev)
+    _require(fn, "copy_src", copy_src, i32, (n,), dev)
+    _require(fn, "copy_dst", copy_dst, i32, (n,), dev)
+    _require_err(fn, dev_err, dev)
+    st = L.gdn_block_fork(_ptr(src_rows), _ptr(dst_rows), _ptr(lens), n, int(block), _ptr(block_table),
+                          block_table.shape[0], block_table.shape[1], _ptr(refs), refs.numel(), _ptr(free_ids),
+                          free_ids.numel(), _ptr(n_free), _ptr(n_free_out), _ptr(copy_src), _ptr(copy_dst),
+                          _ptr(dev_err), _stream(stream, dev))
+    _check(fn, st)
+
+
+def block_release(rows, old_lens, new_lens, block: int, block_table, refs, free_ids, n_free, n_free_out=None,
+                  dev_err=None, stream=None):
+    """Row rows[i] goes from old_lens[i] to new_lens[i] tokens (0: done): its
+    blocks behind that lose a holder, and those without one go onto the stack,
+    by id (see gdn_block_release).  free_ids and refs are updated in place."""
+    fn, L, dev, i32 = "gdn_block_release", load(), _device(), torch.int32
+    n = rows.shape[0]
+    if n_free_out is None:
+        n_free_out = n_free
+    _require_blocks(fn, block_table, refs, free_ids, n_free, dev)
+    _require(fn, "rows", rows, i32, (n,), dev)
+    _require(fn, "old_lens", old_lens, torch.int64, (n,), dev)
+    _require(fn, "new_lens", new_lens, torch.int64, (n,), dev)
+    _require(fn, "n_free_out", n_free_out, i32, (1,), dev)
+    _require_err(fn, dev_err, dev)
+    st = L.gdn_block_release(_ptr(rows), _ptr(old_lens), _ptr(new_lens), n, int(block), _ptr(block_table),
+                             block_table.shape[0], block_table.shape[1], _ptr(refs), refs.numel(), _ptr(free_ids),
+                             free_ids.numel(), _ptr(n_free), _ptr(n_free_out), _ptr(dev_err), _stream(stream, dev))
+    _check(fn, st)
+
+
+def block_compact_workspace_size(num_blocks: int) -> int:
+    return int(load().gdn_block_compact_workspace_size(int(num_blocks)))
+
+
+def block_compact(block_table, refs, free_ids, n_free, move_src, move_dst, n_moves, workspace, table_out=None,
+                  refs_out=None, free_out=None, dev_err=None, stream=None):
+    """The blocks in use move to the lowest ids: move_src, move_dst
+    [max_moves] name the pages to copy, n_moves [1] how many; table, counts and
+    stack follow, in place unless outputs are given (see gdn_block_compact)."""
+    fn, L, dev, i32 = "gdn_block_compact", load(), _device(), torch.int32
+    _require_blocks(fn, block_table, refs, free_ids, n_free, dev)
+    table_out = block_table if table_out is None else table_out
+    refs_out = refs if refs_out is None else refs_out
+    free_out = free_ids if free_out is None else free_out
+    _require(fn, "table_out", table_out, i32, block_table.shape, dev)
+    _require(fn, "refs_out", refs_out, i32, refs.shape, dev)
+    _require(fn, "free_out", free_out, i32, free_ids.shape, dev)
+    _require(fn, "move_src", move_src, i32, (move_src.numel(),), dev)
+    _require(fn, "move_dst", move_dst, i32, (move_src.numel(),), dev)
+    _require(fn, "n_moves", n_moves, i32, (1,), dev)
+    _require(fn, "workspace", workspace, workspace.dtype, workspace.shape, dev)
+    _require_err(fn, dev_err, dev)
+    st = L.gdn_block_compact(_ptr(block_table), _ptr(table_out), block_table.numel(), _ptr(refs), _ptr(refs_out),
+                             refs.numel(), _ptr(free_ids), _ptr(free_out), free_ids.numel(), _ptr(n_free),
+                             _ptr(move_src), _ptr(move_dst), move_src.numel(), _ptr(n_moves), _ptr(workspace),
+                             _nbytes(workspace), _ptr(dev_err), _stream(stream, dev))
+    _check(fn, st)
+
+
+class PagePlanes:
+    """The planes of a paged cache (one layer's keys, its values, the next
+    layer's, ...): tensors [num_pages][...] of one shape and one page stride,
+    each page's bytes consecutive.  Holds the tensors and the device array of
+    their addresses; make it once, before any stream capture."""
+
+    def __init__(self, planes):
+        self.planes = list(planes)
+        fn = "PagePlanes"
+        if not self.planes:
+            raise GdnError(fn, ERR_INVALID_ARG, "no planes")
+        t0 = self.planes[0]
+        for t in self.planes:
+            if t.device != t0.device or t.dtype != t0.dtype or t.shape != t0.shape or t.stride() != t0.stride():
+                raise GdnError(fn, ERR_INVALID_ARG, "planes must be of one shape, type, stride and device")
+        if t0.dim() < 2 or not t0[:1].is_contiguous() or t0.get_device() < 0 or t0[:1].numel() == 0:
+            raise GdnError(fn, ERR_INVALID_ARG, f"planes must be CUDA tensors [pages][...] with consecutive pages, got "
+                                                f"{tuple(t0.shape)}, strides {t0.stride()} on {t0.device}")
+        self.num_pages, esz = int(t0.shape[0]), t0.element_size()
+        self.page_bytes = t0[0].numel() * esz
+        self.page_stride = t0.stride(0) * esz if self.num_pages > 1 else self.page_bytes
+        if any(t.data_ptr() % 16 for t in self.planes):
+            raise GdnError(fn, ERR_INVALID_ARG, "planes must be 16-byte aligned")
+        self.addresses = torch.tensor([t.data_ptr() for t in self.planes], dtype=torch.int64, device=t0.device)
+
+
+def page_copy(planes: PagePlanes, src_ids, dst_ids, dev_err=None, stream=None):
+    """Page dst_ids[i] <- page src_ids[i] of every plane; pairs with a -1 are
+    skipped (see gdn_page_copy)."""
+    fn, L, dev = "gdn_page_copy", load(), _device()
+    n = src_ids.shape[0]
+    _require(fn, "planes", planes.addresses, torch.int64, (len(planes.planes),), dev)
+    _require(fn, "src_ids", src_ids, torch.int32, (n,), dev)
+    _require(fn, "dst_ids", dst_ids, torch.int32, (n,), dev)
+    _require_err(fn, dev_err, dev)
+    st = L.gdn_page_copy(_ptr(planes.addresses), len(planes.planes), planes.page_bytes, planes.page_stride,
+                         planes.num_pages, _ptr(src_ids), _ptr(dst_ids), n, _ptr(dev_err), _stream(stream, dev))
     _check(fn, st)
 
 

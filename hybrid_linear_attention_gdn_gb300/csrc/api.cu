@@ -24,6 +24,12 @@ void register_bounds_reader(const char* unit, BoundsReader r) {
 }
 
 gdn_status check_dims(const gdn_dims* d) {
+  const gdn_status st = check_dims_state(d);
+  if (st != GDN_OK) return st;
+  return d->conv_width < 2 ? GDN_ERR_UNSUPPORTED : GDN_OK;
+}
+
+gdn_status check_dims_state(const gdn_dims* d) {
   if (!d) return GDN_ERR_INVALID_ARG;
   if (d->hk <= 0 || d->hv <= 0 || d->dk <= 0 || d->dv <= 0 || d->conv_width <= 0)
     return GDN_ERR_INVALID_ARG;
@@ -32,7 +38,7 @@ gdn_status check_dims(const gdn_dims* d) {
   if (d->conv_dtype != GDN_F32 && d->conv_dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
   if (d->dk != 16 && d->dk != 64 && d->dk != 128) return GDN_ERR_UNSUPPORTED;
   if (d->dv > 256) return GDN_ERR_UNSUPPORTED;
-  if (d->conv_width < 2 || d->conv_width > 8) return GDN_ERR_UNSUPPORTED;
+  if (d->conv_width > 8) return GDN_ERR_UNSUPPORTED;
   if (d->act_dtype == GDN_F32 && d->conv_dtype == GDN_BF16) return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
 }
@@ -40,7 +46,7 @@ gdn_status check_dims(const gdn_dims* d) {
 gdn_status check_pool(const gdn_dims& d, const gdn_pool& p) {
   if (p.num_slots < 0) return GDN_ERR_INVALID_ARG;
   if (p.num_slots == 0) return GDN_OK;
-  if (!p.ssm || !p.conv) return GDN_ERR_INVALID_ARG;
+  if (!p.ssm || (d.conv_width > 1 && !p.conv)) return GDN_ERR_INVALID_ARG;
   if (!aligned(p.ssm, 16) || !aligned(p.conv, 16)) return GDN_ERR_INVALID_ARG;
   return GDN_OK;
 }

@@ -445,6 +445,8 @@ const int g_bounds_registered = (register_bounds_reader(GDN_TU, read_bounds_word
 
 // Host-side validation shared by every entry point.
 gdn_status check_dims(const gdn_dims* d);
+// the same for calls that work without a conv history too (conv_width 1)
+gdn_status check_dims_state(const gdn_dims* d);
 gdn_status check_pool(const gdn_dims& d, const gdn_pool& p);
 inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 

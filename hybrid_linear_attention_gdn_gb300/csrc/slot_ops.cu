@@ -118,7 +118,7 @@ gdn_status launch_slot_op(int mode, const gdn_dims* dims, const gdn_pool* src,
                           const gdn_pool& dst, const int32_t* src_ids,
                           const int32_t* dst_ids, const int32_t* accept_len,
                           int32_t T, int32_t n, uint32_t* dev_err, void* stream) {
-  gdn_status st = check_dims(dims);
+  gdn_status st = check_dims_state(dims);
   if (st != GDN_OK) return st;
   if (n < 0) return GDN_ERR_INVALID_ARG;
   if (n == 0) return GDN_OK;
@@ -167,7 +167,7 @@ gdn_status launch_slot_op(int mode, const gdn_dims* dims, const gdn_pool* src,
 gdn_status launch_state_xfer(bool pack, const gdn_dims* dims, const gdn_pool& pool,
                              const int32_t* ids, int32_t n, const void* staging,
                              size_t staging_bytes, uint32_t* dev_err, void* stream) {
-  gdn_status st = check_dims(dims);
+  gdn_status st = check_dims_state(dims);
   if (st != GDN_OK) return st;
   if (n < 0) return GDN_ERR_INVALID_ARG;
   if (n == 0) return GDN_OK;
@@ -293,7 +293,7 @@ extern "C" gdn_status gdn_spec_commit_index(const int32_t* spec_ids, const int32
 }
 
 extern "C" size_t gdn_state_record_bytes(const gdn_dims* dims) {
-  if (gdn::check_dims(dims) != GDN_OK) return 0;
+  if (gdn::check_dims_state(dims) != GDN_OK) return 0;
   return gdn::ssm_slot_bytes(*dims) + gdn::conv_slot_bytes(*dims);
 }
 

@@ -75,7 +75,8 @@ typedef struct {
   int32_t hv;         /* V heads, a multiple of hk                  */
   int32_t dk;         /* key/query head dim: 16, 64 or 128          */
   int32_t dv;         /* value head dim: 1..256                     */
-  int32_t conv_width; /* conv1d width W: 2..8                       */
+  int32_t conv_width; /* conv1d width W: 2..8; 1: no conv history
+                         (gdn_lin_*, slot and record calls only)    */
   int32_t act_dtype;  /* GDN_F32 or GDN_BF16: qkv, a, b and outputs */
   int32_t conv_dtype; /* GDN_F32 or GDN_BF16: the conv history      */
 } gdn_dims;
@@ -547,6 +548,184 @@ gdn_status gdn_batch_maps(const int32_t* new_lens, const int64_t* start_pos, int
                           int64_t* slot_map, int64_t max_tokens, uint32_t* dev_err, void* stream);
 
 /*
+ * Linear attention with a fixed decay per head.  Not written on the pages; the
+ * published step (Sun et al., "Retentive Network", 2023; Qin et al.,
+ * "Lightning Attention-2", 2024) over the same slots and head layout as
+ * gdn_decode_step:
+ *   S <- lambda S + k v^T;  o = scale S^T q  (updated S);  lambda = exp(log_decay)
+ * There is no conv, gate or normalisation: dims->conv_width is 1 and the
+ * pools hold no conv history (pool.conv may be NULL).  gdn_slot_copy,
+ * gdn_slot_zero, gdn_spec_commit, gdn_state_pack and gdn_state_unpack take
+ * such dims and pools as well.
+ *   log_decay [hv] float: natural logarithm of each head's decay, <= 0
+ *   (-INFINITY: nothing is kept from one token to the next)
+ *
+ * Decode: one token per request, the state updated in place.
+ *   slot_ids [B] int32, distinct; qkv [B][C], out [B][hv][dv] (act_dtype)
+ * B above 65535: GDN_ERR_UNSUPPORTED; B = 0 is a no-op.
+ */
+gdn_status gdn_lin_decode_step(const gdn_dims* dims, gdn_pool pool, const float* log_decay,
+                               float scale, const int32_t* slot_ids, int32_t B, const void* qkv,
+                               void* out, uint32_t* dev_err, void* stream);
+
+/*
+ * Its prefill: the contract of gdn_chunk_prefill (packed sequences from any
+ * start position, block-aligned checkpoints of the state, final state into the
+ * working slot, rows outside the sequences not written) with every token the
+ * step above.  A checkpoint id outside the pool is skipped and sets
+ * GDN_DEV_ERR_SLOT_OOB.  Above 16384 sequences, 2^31 - 1 tokens or 65535
+ * segments: GDN_ERR_UNSUPPORTED.
+ *   workspace: >= gdn_lin_prefill_workspace_size(...) bytes, 256-aligned (may
+ *   be NULL where that is 0); nothing in it needs to be zero, and nothing is
+ *   kept in it between calls, but calls that run at once (on two streams, or
+ *   in two graphs that are replayed at once) need one each.
+ */
+size_t gdn_lin_prefill_workspace_size(const gdn_dims* dims, int32_t n_seq, int64_t total_tokens);
+gdn_status gdn_lin_prefill(const gdn_dims* dims, gdn_pool pool, gdn_pool ckpt, const float* log_decay,
+                           float scale, const int32_t* slot_ids, const int32_t* cu_seqlens,
+                           const int64_t* start_pos, int32_t n_seq, int64_t total_tokens,
+                           const int32_t* ckpt_ids, int32_t max_ckpt, int32_t ckpt_block,
+                           const void* qkv, void* out, void* workspace, size_t workspace_bytes,
+                           uint32_t* dev_err, void* stream);
+
+/*
+ * Norms of queries and keys per head, rotation by position, and the write of
+ * keys and values to their cache pages, in one pass: what a full-attention
+ * layer (or a linear one whose q and k are rotated) does between its
+ * projection and its attention.  Not written on the pages; the published
+ * blocks (Henry et al., "Query-Key Normalization", 2020; Su et al.,
+ * "RoFormer", 2021).  For every row r and head:
+ *   y = x / sqrt(mean(x^2) + eps) * weight       (weight NULL: y = x)
+ *   pairs (a, b) of y's first `rot` values -> (a c - b s, b c + a s),
+ *   c = cos_sin[positions[r]][i], s = cos_sin[positions[r]][rot / 2 + i],
+ *   pair i = (i, i + rot / 2), or (2 i, 2 i + 1) with interleaved = 1
+ * Tensors are described by their strides in elements (gdn_rows: element
+ * [row][head][0] at row * r + head * h; gdn_pages: [page][row][head][0]), so
+ * that q, k and v may be parts of one projection and a cache may be laid out
+ * by rows or by heads; a head's values are consecutive.
+ *   q [n_rows][hq][d], k [n_rows][hk][d], v [n_rows][hv][dv] (act_dtype)
+ *   q_out, k_out as q, k: each may be its input (same strides); any other
+ *   overlap is undefined
+ *   positions [n_rows] int64; cos_sin [max_pos][rot] float, its cosines first
+ *   slot_map [n_rows] int64 (see gdn_batch_maps) or NULL: row r's k and v also
+ *   go to row slot % block of page slot / block of k_cache and v_cache
+ *   [num_pages][block][...]; slot -1: they do not.  With a slot_map k_out may
+ *   be absent (data NULL), and hv may be 0 (v and v_cache are not used then).
+ *   Slots other than -1 must be distinct (precondition).
+ * Everything is computed in fp32 and rounded once.  The sum of squares is held
+ * in fp32 (values beyond some 1e18 give zeros, as in gdn_add_rmsnorm).
+ * A position outside [0, max_pos) makes the row's outputs zeros, writes nothing
+ * to the cache and sets GDN_DEV_ERR_SEQLENS; a slot outside the cache is
+ * skipped and sets GDN_DEV_ERR_SLOT_OOB.
+ * rot even, 0 <= rot <= d; block a positive power of two; d or dv above 1024:
+ * GDN_ERR_UNSUPPORTED.  n_rows = 0 launches nothing.
+ */
+typedef struct {
+  void* data;   /* element [0][0][0]            */
+  int64_t row;  /* elements from a row to the next  */
+  int64_t head; /* elements from a head to the next */
+} gdn_rows;
+typedef struct {
+  void* data;
+  int64_t page, row, head;
+} gdn_pages;
+gdn_status gdn_qk_norm_rope(int32_t act_dtype, int32_t hq, int32_t hk, int32_t d, int32_t hv, int32_t dv,
+                            int64_t n_rows, gdn_rows q, gdn_rows k, gdn_rows v, const float* q_weight,
+                            const float* k_weight, float eps, const float* cos_sin, int64_t max_pos,
+                            int32_t rot, int32_t interleaved, const int64_t* positions, gdn_rows q_out,
+                            gdn_rows k_out, gdn_pages k_cache, gdn_pages v_cache, int32_t num_pages,
+                            int32_t block, const int64_t* slot_map, uint32_t* dev_err, void* stream);
+
+/*
+ * Blocks after gdn_batch_maps has handed them out (TokenSpeed Qwen3.5 page,
+ * "Scheduler dual": requests hold block indices; "Ciclo de vida de slots": a
+ * shared prefix is kept once).  `block_table` [n_rows][max_blocks] and the
+ * stack free_ids / n_free are those of gdn_batch_maps; refs [num_blocks] int32
+ * counts a block's holders beyond the first, so that a block fresh from the
+ * stack (0) needs no entry of its own.  All results are independent of the
+ * order in which threads run.  Row id -1 is padding; another one outside
+ * [0, n_rows) is skipped and sets GDN_DEV_ERR_SLOT_OOB.  n_free_out may be
+ * n_free.  block a positive power of two.
+ *
+ * Fork: row dst_rows[i] becomes a branch of row src_rows[i], which holds
+ * lens[i] tokens: the whole blocks are shared (one more holder each), and
+ * where the last one is partly filled the branch gets a block of its own from
+ * the stack, in the order of i, and copy_src[i], copy_dst[i] name the pages to
+ * copy (else both are -1; see gdn_page_copy).  The entries behind a branch's
+ * blocks are left as they were.  One row may be the source of several
+ * branches; the destinations must be distinct and no sources (precondition).
+ *   GDN_DEV_ERR_SEQLENS   lens[i] negative or beyond max_blocks: skipped
+ *   GDN_DEV_ERR_BLOCKS    no free block left: that entry and its pair are -1
+ *   GDN_DEV_ERR_SLOT_OOB  a held entry or a free id outside [0, num_blocks),
+ *                 that entry is -1; a row that is its own branch, skipped
+ */
+gdn_status gdn_block_fork(const int32_t* src_rows, const int32_t* dst_rows, const int64_t* lens, int32_t n,
+                          int32_t block, int32_t* block_table, int32_t n_rows, int32_t max_blocks,
+                          int32_t* refs, int32_t num_blocks, const int32_t* free_ids, int32_t free_cap,
+                          const int32_t* n_free, int32_t* n_free_out, int32_t* copy_src, int32_t* copy_dst,
+                          uint32_t* dev_err, void* stream);
+
+/*
+ * Release: row rows[i] goes from old_lens[i] tokens to new_lens[i] (0: the
+ * request is done).  The blocks that it no longer needs lose a holder, its
+ * entries for them become -1, and the blocks that nobody holds any more go
+ * onto the stack in ascending order of their ids.  Rows distinct
+ * (precondition).  What is kept may end inside a block that other rows share:
+ * fork such a row before appending to it.
+ *   GDN_DEV_ERR_SEQLENS   new_lens[i] not in [0, old_lens[i]], or old_lens[i]
+ *                 beyond max_blocks: the row is skipped
+ *   GDN_DEV_ERR_SLOT_OOB  an entry outside [0, num_blocks) (skipped), or a block
+ *                 given up more often than it was held (it goes onto the stack
+ *                 once)
+ *   GDN_DEV_ERR_BLOCKS    more free blocks than free_cap: the highest are lost
+ */
+gdn_status gdn_block_release(const int32_t* rows, const int64_t* old_lens, const int64_t* new_lens, int32_t n,
+                             int32_t block, int32_t* block_table, int32_t n_rows, int32_t max_blocks,
+                             int32_t* refs, int32_t num_blocks, int32_t* free_ids, int32_t free_cap,
+                             const int32_t* n_free, int32_t* n_free_out, uint32_t* dev_err, void* stream);
+
+/*
+ * Compact: with F blocks on the stack, the num_blocks - F others (in use) move
+ * to the ids below num_blocks - F.  The k-th highest block in use above that
+ * border goes to the k-th lowest free id below it: move_src[k], move_dst[k],
+ * for k < *n_moves <= max_moves (pairs behind are -1); fewer than needed where
+ * max_moves is smaller.  Table entries and reference counts follow; the free
+ * ids are put back with the lowest on top.  Entries outside [0, num_blocks)
+ * stay as they are.  The caller copies the pages (gdn_page_copy) and whatever
+ * else goes by block id (gdn_slot_copy for checkpoints) before any of them is
+ * used.
+ *   table_out, refs_out, free_out: each may be its input (in place), or not:
+ *   then the input is kept and the output written whole (free_out: free_cap
+ *   entries; those behind the stack's top as they were)
+ *   workspace: gdn_block_compact_workspace_size(num_blocks) bytes, 256-aligned,
+ *   of one call at a time
+ *   GDN_DEV_ERR_BLOCKS    *n_free outside [0, min(free_cap, num_blocks)]
+ *   GDN_DEV_ERR_SLOT_OOB  an id on the stack outside [0, num_blocks) or twice on it
+ *   in both cases nothing moves (*n_moves = 0, outputs are the inputs)
+ */
+size_t gdn_block_compact_workspace_size(int32_t num_blocks);
+gdn_status gdn_block_compact(const int32_t* block_table, int32_t* table_out, int64_t n_entries,
+                             const int32_t* refs, int32_t* refs_out, int32_t num_blocks,
+                             const int32_t* free_ids, int32_t* free_out, int32_t free_cap,
+                             const int32_t* n_free, int32_t* move_src, int32_t* move_dst, int32_t max_moves,
+                             int32_t* n_moves, void* workspace, size_t workspace_bytes, uint32_t* dev_err,
+                             void* stream);
+
+/*
+ * Page copies: page dst_ids[i] <- page src_ids[i] of every plane (a plane: one
+ * layer's keys, say), bit for bit.
+ *   planes [n_planes] device array of the planes' base addresses, each of
+ *   num_pages pages of page_bytes, page_stride bytes apart (both multiples of
+ *   16, else GDN_ERR_UNSUPPORTED; bases 16-byte aligned)
+ *   src_ids, dst_ids [n]: a pair with a -1 is skipped; one with another id
+ *   outside [0, num_pages) is skipped and sets GDN_DEV_ERR_SLOT_OOB.
+ *   Destinations must be distinct and no sources (precondition).
+ */
+gdn_status gdn_page_copy(void* const* planes, int32_t n_planes, int64_t page_bytes, int64_t page_stride,
+                         int32_t num_pages, const int32_t* src_ids, const int32_t* dst_ids, int32_t n,
+                         uint32_t* dev_err, void* stream);
+
+/*
  * Self-test of the device-side failure path: one CTA waits on a barrier phase
  * that nothing completes; the bounded wait gives up after the library's wait
  * limit (1 s), GDN_DEV_ERR_TIMEOUT is OR-ed into *dev_err (device, required)
@@ -578,7 +757,14 @@ const char* gdn_status_string(int32_t status);
 #define GDN_K_SSM_PREFILL 14
 #define GDN_K_ADD_RMSNORM 15
 #define GDN_K_BATCH_MAPS 16
-#define GDN_K_COUNT 17
+#define GDN_K_LIN_DECODE 17
+#define GDN_K_LIN_PREFILL 18
+#define GDN_K_QK_NORM_ROPE 19
+#define GDN_K_PAGE_COPY 20
+#define GDN_K_BLOCK_FORK 21
+#define GDN_K_BLOCK_RELEASE 22
+#define GDN_K_BLOCK_COMPACT 23
+#define GDN_K_COUNT 24
 uint64_t gdn_launch_count(int32_t kernel);
 void gdn_launch_count_reset(void);
 
