@@ -102,23 +102,26 @@ __device__ __forceinline__ bool find_segment(const PrefillArgs& a, const int64_t
   return true;
 }
 
-// lambda^n (n >= 0), the exponent and the exponential in double: exact to a
-// rounding of fp32 whatever n.  lambda^0 is 1 for every decay, -inf too.
+// lambda^n (n >= 0).  The rounding of the exponent (2^-24 of it) is the same
+// part of every power: what a state still remembers has exponents of a few
+// units in sum, however many powers were multiplied.  lambda^0 is 1 for every
+// decay, -inf too.
 __device__ __forceinline__ float power(float log_decay, int64_t n) {
-  return n == 0 ? 1.f : (float)exp((double)log_decay * (double)n);
+  return n == 0 ? 1.f : expf(log_decay * (float)n);
 }
 
-// A decay as two floats.  A state that remembers 2,000 tokens has been
-// multiplied by lambda as often: its rounding to one float alone (2^-25) would
-// put it off by 6e-5.
+// A decay as the sum of two floats.  A state that remembers 2,000 tokens has
+// been multiplied by lambda as often: its rounding to one float (2^-25) would
+// put it off by 6e-5.  As 1 + expm1(log_decay) the error is 2^-24 of the small
+// part; a decay that forgets within two tokens needs no second part.
 struct Decay {
   float hi, lo;
 };
 __device__ __forceinline__ Decay decay_of(float log_decay) {
-  const double l = exp((double)log_decay);
   Decay d;
-  d.hi = (float)l;
-  d.lo = (float)(l - (double)d.hi);
+  const bool slow = log_decay > -0.5f;
+  d.hi = slow ? 1.f : expf(log_decay);
+  d.lo = slow ? expm1f(log_decay) : 0.f;
   return d;
 }
 // lambda s + v k
