@@ -22,7 +22,7 @@ LIB_DEBUG = os.path.join(PKG, "libgdn_debug.so")
 
 SOURCES = ["api.cu", "slot_ops.cu", "decode.cu", "decode_tma.cu", "verify_tma.cu", "prefill.cu", "prefill_tc.cu",
            "prefill_tc32.cu", "epilogue.cu", "kda_chunk.cu", "kda_tc32.cu", "ssm.cu", "ssm_ring.cu",
-           "ssm_chunk.cu", "add_rmsnorm.cu", "batch_maps.cu", "lin.cu", "qk_norm_rope.cu", "pages.cu"]
+           "ssm_chunk.cu", "add_rmsnorm.cu", "batch_maps.cu", "lin.cu", "lin_chunk.cu", "qk_norm_rope.cu", "pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
          "--expt-relaxed-constexpr"]

@@ -457,8 +457,13 @@ extern "C" gdn_status gdn_lin_prefill(const gdn_dims* dims, gdn_pool pool, gdn_p
   a.n_segs = (int32_t)segs;
   a.seg_state = need > 0 ? reinterpret_cast<float*>(workspace) : nullptr;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = dims->act_dtype == GDN_BF16 ? recurrent_dispatch<__nv_bfloat16>(a, s)
-                                                    : recurrent_dispatch<float>(a, s);
+  cudaError_t e;
+  // GDN_LIN_PREFILL_PATH=recurrent (read on every call) forces the recurrence
+  const char* path = std::getenv("GDN_LIN_PREFILL_PATH");
+  if (lin::chunk_supported(*dims, total_tokens, qkv, out) && !(path && !std::strcmp(path, "recurrent")))
+    e = lin::chunk_launch(a, s);
+  else
+    e = dims->act_dtype == GDN_BF16 ? recurrent_dispatch<__nv_bfloat16>(a, s) : recurrent_dispatch<float>(a, s);
   if (e != cudaSuccess) return GDN_ERR_CUDA;
   count_launch(GDN_K_LIN_PREFILL);
   return GDN_OK;
