@@ -11,21 +11,27 @@
 // in fp32 between chunks.  Per chunk, all accumulators in TMEM:
 //   G    = Q K^T                    Q and K as they lie in memory
 //   dS^T = (V w)^T K                w_j = lambda^(L - 1 - j); A = V w, in parts
-//   O1^T = S^T Q^T                  A = S^T in TMEM, two parts
-//   O2^T = V^T P^T                  A = V; B = P, its two parts side by side
+//   O1^T = S^T Q^T                  A = S^T in TMEM, in parts
+//   O2^T = V^T P^T                  A = V; P = G with its decays, in parts
 // dS does not need S, so only an elementwise update per chunk is left of the
 // recurrence, and the tensor core always has another chunk's work.
 //
-// Roundings.  q, k and v are bf16 already and enter G, dS and O2 exactly.
-// V w is split into three bf16 parts (24 bits: the fp32 product itself), so that
-// states keep fp32's accuracy; P and S^T, which only outputs see, into two (16
-// bits, off by at most 2^-17 of each term, against the output's own 2^-9).
-// Parts of 8 bits keep fp32's range, so no scaling is needed; values from
-// 3.39e38 on become infinite.
+// Roundings.  q, k and v are bf16 already and enter G, dS and O2 exactly.  V w
+// is split into three bf16 parts (24 bits: the fp32 product itself), so that
+// states and checkpoints keep fp32's accuracy; P and S^T, which only outputs
+// see, into two (16 bits, off by at most 2^-16 of a term, against the output's
+// own 2^-8; with one part each the outputs were 2.4e-3 off instead of 1.7e-3).
+// bf16 parts keep fp32's range, so no scaling is needed; values from 3.39e38 on
+// become infinite.
 //
-// 20 warps by role: 8 hold S (2 per 32 V channels, 64 dk columns each), 4 write
-// outputs, 3 compute P (in blocks of 32 x 32; one of four lies above the
-// diagonal), 4 scale and split V, one issues the products.
+// A product of K = 16 takes some 59 cycles with N = 64 and 67 to 73 with N = 128
+// (measured; M = 64 no less than M = 128), 2,800 a chunk, and both operands from
+// shared memory take all its bandwidth: two parts of V w therefore go through
+// registers to TMEM, whose 512 columns are all in use.
+//
+// 17 warps by role (of 20): 8 hold S (2 per 32 V channels, 64 dk columns each), 4
+// make P from G and write outputs (one of them issues the copies), 4 scale and
+// split V, one issues the products.
 #include "lin.cuh"
 
 #include "decode_tma.cuh"  // sm_count
@@ -39,24 +45,28 @@ namespace {
 
 constexpr int kD = 128;  // dk = dv
 constexpr int kStages = 3;
-constexpr int kStateWarps = 8, kOutWarp = 8, kAuxWarp = 12, kIssuer = 16;
+constexpr int kStateWarps = 8, kOutWarp = 8, kSplitWarp = 12, kIssuer = 16;
 constexpr int kThreads = 20 * 32;
 constexpr int kStateThreads = kStateWarps * 32;
-// Registers per thread, by warpgroup; 640 x 96 at launch is what there is.
-constexpr int kStateRegs = 136, kOutRegs = 72, kAuxRegs = 64;
-static_assert(2 * kStateRegs + kOutRegs + 2 * kAuxRegs <= 5 * 96, "the launch's registers");
+// Registers per thread, by warpgroup (state, state, output, split, issuer);
+// 640 x 96 at launch is what there is.
+constexpr int kStateRegs = 136, kOutRegs = 88, kSplitRegs = 72, kRestRegs = 48;
+static_assert(2 * kStateRegs + kOutRegs + kSplitRegs + kRestRegs <= 5 * 96, "the launch's registers");
 
-// TMEM columns
-constexpr uint32_t TM_G = 0, TM_DS = 64, TM_O1 = 192, TM_O2 = 256, TM_SH = 384, TM_SL = 448, TM_COLS = 512;
+// TMEM columns.  G (M = 64) is in the first 16 lanes of each warp's 32; S^T and
+// V w are two parts each.
+constexpr uint32_t TM_G = 0, TM_DS = 64, TM_O1 = 192, TM_O2 = 256, TM_S = 320, TM_VW = 448, TM_COLS = 512;
 
+// 64-column blocks of 128-byte rows, 16-byte piece c of row r at c ^ (r & 7)
 struct __align__(1024) Stage {
-  uint8_t qk[2][128 * 128];  // 64-column blocks: rows 0..63 q, 64..127 k
-  uint8_t v[2][64 * 128];    // 64-column blocks
+  uint8_t qk[2][128 * 128];  // rows 0..63 q, 64..127 k
+  uint8_t v[2][64 * 128];
 };
 struct __align__(1024) ChunkSmem {
   Stage st[kStages];
-  uint8_t vw[3][2 * 64 * 128];  // V w: its three parts
-  uint8_t p[2][128 * 128];      // P [t][j] by the chunk's parity: rows 0..63 hi, 64..127 lo
+  uint8_t p[2][2][64 * 128];    // P [t][j], by the chunk's parity: its two parts
+  uint8_t o[2][64 * 128];       // outputs [t][dv], 64-column blocks
+  uint8_t vw[2][64 * 128];      // V w's third part [j][dv], 64-column blocks
   float pw[kC + 1];             // lambda^n
   float ps[kC + 1];             // scale lambda^n
   Segment seg;
@@ -66,11 +76,11 @@ struct __align__(1024) ChunkSmem {
   uint32_t tmem_base;
 };
 // The state tile's way between global memory and the threads' rows: 64 KB from
-// the last stage on, free before chunk kStages - 1 is loaded and V w first
-// written, and after the last product.
+// the last stage on, free before chunk kStages - 1 is loaded and P first
+// written, and after the last product (which no output has left by then).
 constexpr unsigned kTile = kD * kD * 4;
 static_assert(sizeof(ChunkSmem) + 1024 <= 232448, "shared memory of a CTA");
-static_assert(offsetof(ChunkSmem, p) - offsetof(ChunkSmem, st) - (kStages - 1) * sizeof(Stage) >= kTile, "state tile");
+static_assert(offsetof(ChunkSmem, vw) - offsetof(ChunkSmem, st) - (kStages - 1) * sizeof(Stage) >= kTile, "state tile");
 
 // hi: x rounded to bf16, packed in pairs; x: what is left of it, exactly
 __device__ __forceinline__ uint32_t take_bf16(float2& x) {
@@ -79,11 +89,77 @@ __device__ __forceinline__ uint32_t take_bf16(float2& x) {
   x = fma2(make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)), make_float2(-1.f, -1.f), x);
   return hi;
 }
-// x as two bf16 parts, packed in pairs
-__device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
-  hi = take_bf16(x);
-  const __nv_bfloat162 l = __floats2bfloat162_rn(x.x, x.y);
-  lo = *reinterpret_cast<const uint32_t*>(&l);
+__device__ __forceinline__ uint32_t bf16_pair(float2 x) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Four 8 x 8 matrices of 16-bit values, transposed: lane 8 i + r names row r of
+// matrix i; the thread gets (rows 2 (lane % 4), + 1; column lane / 4) of each.
+__device__ __forceinline__ void ldmatrix4_t(uint32_t at, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void stmatrix4_t(uint32_t at, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(at), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+__device__ __forceinline__ void stmatrix4(uint32_t at, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(at), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+// 16 lanes (of `half`: the warp's first or last) x 16 columns: register 2 m + g
+// of a thread is lane lane / 4 + 8 g, column 4 m + lane % 4
+__device__ __forceinline__ void tmem_put_frag(uint32_t taddr, int half, const uint32_t (&v)[8],
+                                              int line = __builtin_LINE()) {
+  if (!umma::tmem_ok(taddr, 16, true, line)) return;
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(
+          taddr + ((uint32_t)(16 * half) << 16)),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+      : "memory");
+}
+// the warp's first 16 lanes x 32 columns: register 4 m + 2 g + e of a thread is
+// lane lane / 4 + 8 g, column 8 m + 2 (lane % 4) + e
+__device__ __forceinline__ void tmem_get_frag(uint32_t taddr, float (&v)[16], int line = __builtin_LINE()) {
+  if (!umma::tmem_ok(taddr, 32, true, line)) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 0.f;
+    return;
+  }
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+// 16 lanes x 32 columns of two regions: register 4 m + 2 g + e of a thread is
+// lane lane / 4 + 8 g, column 8 m + 2 (lane % 4) + e
+__device__ __forceinline__ void tmem_get_frag2(uint32_t ta, uint32_t tb, int half, float (&va)[16], float (&vb)[16],
+                                               int line = __builtin_LINE()) {
+  if (!umma::tmem_ok(ta, 32, true, line) || !umma::tmem_ok(tb, 32, true, line)) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) va[i] = vb[i] = 0.f;
+    return;
+  }
+  const uint32_t off = (uint32_t)(16 * half) << 16;
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, "
+      "[%33];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=f"(va[0]), "=f"(va[1]), "=f"(va[2]), "=f"(va[3]), "=f"(va[4]), "=f"(va[5]), "=f"(va[6]), "=f"(va[7]),
+        "=f"(va[8]), "=f"(va[9]), "=f"(va[10]), "=f"(va[11]), "=f"(va[12]), "=f"(va[13]), "=f"(va[14]), "=f"(va[15]),
+        "=f"(vb[0]), "=f"(vb[1]), "=f"(vb[2]), "=f"(vb[3]), "=f"(vb[4]), "=f"(vb[5]), "=f"(vb[6]), "=f"(vb[7]),
+        "=f"(vb[8]), "=f"(vb[9]), "=f"(vb[10]), "=f"(vb[11]), "=f"(vb[12]), "=f"(vb[13]), "=f"(vb[14]), "=f"(vb[15])
+      : "r"(ta + off), "r"(tb + off)
+      : "memory");
 }
 
 // 16 TMEM columns of packed values, written; complete after tmem_wait_st()
@@ -94,25 +170,6 @@ __device__ __forceinline__ void tmem_put16(uint32_t taddr, const uint32_t (&v)[1
           taddr),
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
-}
-// three runs of 8 columns read at once
-__device__ __forceinline__ void tmem_ld8x3(uint32_t ta, uint32_t tb, uint32_t tc, float (&va)[8], float (&vb)[8],
-                                           float (&vc)[8], int line = __builtin_LINE()) {
-  if (!umma::tmem_ok(ta, 8, true, line) || !umma::tmem_ok(tb, 8, true, line) || !umma::tmem_ok(tc, 8, true, line)) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) va[i] = vb[i] = vc[i] = 0.f;
-    return;
-  }
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%24];\n"
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%25];\n"
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16,%17,%18,%19,%20,%21,%22,%23}, [%26];\n"
-      "tcgen05.wait::ld.sync.aligned;\n"
-      : "=f"(va[0]), "=f"(va[1]), "=f"(va[2]), "=f"(va[3]), "=f"(va[4]), "=f"(va[5]), "=f"(va[6]), "=f"(va[7]),
-        "=f"(vb[0]), "=f"(vb[1]), "=f"(vb[2]), "=f"(vb[3]), "=f"(vb[4]), "=f"(vb[5]), "=f"(vb[6]), "=f"(vb[7]),
-        "=f"(vc[0]), "=f"(vc[1]), "=f"(vc[2]), "=f"(vc[3]), "=f"(vc[4]), "=f"(vc[5]), "=f"(vc[6]), "=f"(vc[7])
-      : "r"(ta), "r"(tb), "r"(tc)
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
@@ -164,7 +221,8 @@ __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity) {
 // segment but a sequence's last).
 template <bool STATE>
 __global__ void __launch_bounds__(kThreads, 1)
-    lin_chunk_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap xmap) {
+    lin_chunk_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap xmap,
+                     const __grid_constant__ CUtensorMap omap) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   ChunkSmem& S = *reinterpret_cast<ChunkSmem*>(smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023));
   const int tid = threadIdx.x, lane = tid & 31;
@@ -178,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.empty[i], 1);
     }
     mbar_init(&S.g_full, 1);
-    mbar_init(&S.aux_full, STATE ? 4 : 4 + 3);
+    mbar_init(&S.aux_full, STATE ? 4 : 4 + 4);
     mbar_init(&S.ds_full, 1);
     mbar_init(&S.ds_empty, kStateWarps);
     mbar_init(&S.s_full, kStateWarps);
@@ -226,29 +284,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto from = [&](int i) { return i ? m0 - head + (int64_t)i * kC : m0; };
   auto count = [&](int i) { return (int)(min(m1, m0 - head + (int64_t)(i + 1) * kC) - from(i)); };
 
-  if (warp >= kAuxWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kAuxRegs));
-    const int quarter = warp & 3, half = (warp - kAuxWarp) >> 2;
+  if (warp >= kIssuer) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRestRegs));
     if (warp == kIssuer) {
       // ---------------------------------------------------------------- issuer
       // Order per chunk i: dS(i), G(i + 1), O2(i), O1(i): whatever the other
       // warps make of one product has two more products' time.
-      constexpr uint32_t ID_64 = umma::idesc_bf16(128, kC, false, false);  // G, O1
-      constexpr uint32_t ID_DS = umma::idesc_bf16(128, kD, true, true);
-      constexpr uint32_t ID_O2 = umma::idesc_bf16(128, 2 * kC, true, false);
+      constexpr uint32_t ID_G = umma::idesc_bf16(64, kC, false, false);
+      constexpr uint32_t ID_O1 = umma::idesc_bf16(128, kC, false, false);
+      constexpr uint32_t ID_DS = umma::idesc_bf16(128, kD, false, true);   // V w in TMEM
+      constexpr uint32_t ID_DS3 = umma::idesc_bf16(128, kD, true, true);  // in shared memory
+      constexpr uint32_t ID_O2 = umma::idesc_bf16(128, kC, true, false);
       const uint32_t lead = lane == 0;
       const uint64_t dq0 = umma::desc(smem_addr(S.st[0].qk[0]), 16, 1024);            // q as rows, k 8 KB on
       const uint64_t dk0 = umma::desc(smem_addr(S.st[0].qk[0]) + 8192, 16384, 1024);  // k as columns
       const uint64_t dv0 = umma::desc(smem_addr(S.st[0].v[0]), 8192, 1024);
+      const uint64_t dp0 = umma::desc(smem_addr(S.p[0][0]), 16, 1024);
       const uint64_t dvw = umma::desc(smem_addr(S.vw[0]), 8192, 1024);
-      const uint64_t dp0 = umma::desc(smem_addr(S.p[0]), 16, 1024);
       bool ok = true;
       auto issue_g = [&](int s) {
         const uint64_t d = umma::adv(dq0, s * (uint32_t)sizeof(Stage));
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const uint32_t at = (k >> 2) * 16384 + (k & 3) * 32;
-          mma_ss(lead, tmem + TM_G, umma::adv(d, at), umma::adv(d, 8192 + at), ID_64, k > 0);
+          mma_ss(lead, tmem + TM_G, umma::adv(d, at), umma::adv(d, 8192 + at), ID_G, k > 0);
         }
         commit(lead, &S.g_full);
       };
@@ -269,11 +328,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         {
           const uint64_t dk = umma::adv(dk0, at);
 #pragma unroll
-          for (int part = 2; part >= 0; --part)
+          for (int k = 0; k < 4; ++k)
+            mma_ss(lead, tmem + TM_DS, umma::adv(dvw, 2048 * k), umma::adv(dk, 2048 * k), ID_DS3, k > 0);
+#pragma unroll
+          for (int part = 1; part >= 0; --part)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_ss(lead, tmem + TM_DS, umma::adv(dvw, part * 16384 + 2048 * k), umma::adv(dk, 2048 * k), ID_DS,
-                     part < 2 || k > 0);
+              mma_ts(lead, tmem + TM_DS, tmem + TM_VW + 32 * part + 8 * k, umma::adv(dk, 2048 * k), ID_DS, true);
           commit(lead, &S.ds_full);
           if (STATE) commit(lead, &S.empty[s]);
         }
@@ -285,14 +346,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!STATE) {
-          // O2^T = V^T P^T, both parts of P side by side
+          // O2^T = V^T P^T
           if (i > 0 && !(ok = wait_all(&S.o_empty, (i - 1) & 1))) break;
           umma::fence_after();
           {
             const uint64_t dv = umma::adv(dv0, at), dp = umma::adv(dp0, (i & 1) * (uint32_t)sizeof(S.p[0]));
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ss(lead, tmem + TM_O2, umma::adv(dv, 2048 * k), umma::adv(dp, 32 * k), ID_O2, k > 0);
+            for (int part = 1; part >= 0; --part)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_ss(lead, tmem + TM_O2, umma::adv(dv, 2048 * k), umma::adv(dp, part * 8192 + 32 * k), ID_O2,
+                       part == 0 || k > 0);
           }
           // O1^T = S^T Q^T
           if (!(ok = wait_all(&S.s_full, i & 1))) break;
@@ -303,8 +367,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int part = 1; part >= 0; --part)
 #pragma unroll
               for (int k = 0; k < 8; ++k)
-                mma_ts(lead, tmem + TM_O1, tmem + (part ? TM_SL : TM_SH) + 8 * k,
-                       umma::adv(dq, (k >> 2) * 16384 + (k & 3) * 32), ID_64, part == 0 || k > 0);
+                mma_ts(lead, tmem + TM_O1, tmem + TM_S + 64 * part + 8 * k,
+                       umma::adv(dq, (k >> 2) * 16384 + (k & 3) * 32), ID_O1, part == 0 || k > 0);
             commit(lead, &S.o_full);
           }
         }
@@ -315,108 +379,94 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the products in flight end before their memory is used otherwise
       commit(lead, &S.drained);
       wait_all(&S.drained, 0);
-    } else if (quarter >= 2) {
-      // ------------------------------------------------------------- V w, split
-      // A thread has 8 of the tile's 1024 16-byte pieces, of four rows.
-      const int ct = ((quarter - 2) * 2 + half) * 32 + lane;  // 0 .. 127
-      bool ok = wait_all(&S.init, 0);                         // the state tile has left vw
-      for (int i = 0; i < nit && ok; ++i) {
-        Stage& st = S.st[i % kStages];
-        const int L = count(i);
-        if (!(ok = wait_all(&S.full[i % kStages], (i / kStages) & 1))) break;
-        if (L < kC) {
-          // rows behind the chunk are others' values: zeros, or a NaN among
-          // them would reach this chunk's products
+    }
+    __syncwarp();
+  } else if (warp >= kSplitWarp) {
+    // --------------------------------------------------------------- V w, split
+    // V channels 32 quarter .. + 31 of every token, transposed on the way to
+    // TMEM.  A thread's tokens are 8 m + 2 (lane % 4), + 1 (m = 0 .. 7).
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kSplitRegs));
+    const int quarter = warp & 3, j0 = 2 * (lane & 3);
+    const uint32_t tlane = tmem + ((uint32_t)(32 * quarter) << 16);
+    float2 w[8];
+#pragma unroll
+    for (int m = 0; m < 8; ++m) w[m] = make_float2(S.pw[kC - 1 - 8 * m - j0], S.pw[kC - 2 - 8 * m - j0]);
+    bool ok = true;
+    for (int i = 0; i < nit && ok; ++i) {
+      Stage& st = S.st[i % kStages];
+      const int L = count(i);
+      ok = wait_all(&S.full[i % kStages], (i / kStages) & 1);
+      if (L < kC) {
+        if (named_sync_or(2, 128, !ok)) ok = false;
+        if (!ok) break;
+        // rows behind the chunk are others' values: zeros, or a NaN among them
+        // would reach this chunk's products
 #pragma unroll 1
-          for (int e = ct; e < (kC - L) * 8; e += 128) {
-            const uint32_t at = (uint32_t)(L + e / 8) * 128u + (e % 8) * 16u;
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              tile_at<uint4>(st.v[b], sizeof(st.v[b]), at) = make_uint4(0, 0, 0, 0);
-              tile_at<uint4>(st.qk[b], sizeof(st.qk[b]), 8192 + at) = make_uint4(0, 0, 0, 0);
-            }
-          }
-          umma::fence_proxy_async();
-          named_sync(2, 128);
-        }
-        if (i > 0 && !(ok = wait_all(&S.ds_full, (i - 1) & 1))) break;  // vw was read
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int row = (e & 3) * 16 + ct / 8;
-          const uint32_t at = (uint32_t)row * 128u + (ct & 7) * 16u;
-          const float w = row < L ? S.pw[L - 1 - row] : 0.f;
-          const uint4 u = tile_at<const uint4>(st.v[e >> 2], sizeof(st.v[0]), at);
-          const uint32_t x[4] = {u.x, u.y, u.z, u.w};
-          uint32_t r[3][4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float2 y = mul2(make_float2(__uint_as_float(x[k] << 16), __uint_as_float(x[k] & 0xffff0000u)),
-                            make_float2(w, w));
-            r[0][k] = take_bf16(y);
-            r[1][k] = take_bf16(y);
-            const __nv_bfloat162 l = __floats2bfloat162_rn(y.x, y.y);
-            r[2][k] = *reinterpret_cast<const uint32_t*>(&l);
-          }
-#pragma unroll
-          for (int q = 0; q < 3; ++q)
-            tile_at<uint4>(S.vw[q], sizeof(S.vw[0]), (e >> 2) * 8192u + at) = make_uint4(r[q][0], r[q][1], r[q][2], r[q][3]);
-        }
-        umma::fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.aux_full);
-      }
-      if (!ok && lane == 0) report(a.err, GDN_DEV_ERR_TIMEOUT);
-    } else if (!STATE) {
-      // ---------------------------------------------------------------------- P
-      // token row t, columns 32 half .. + 31
-      const int t = 32 * quarter + lane, j0 = 32 * half;
-      const uint32_t tlane = tmem + ((uint32_t)(32 * quarter) << 16);
-      if (quarter == 0) {  // the block above the diagonal: zeros, once
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t at = umma::sw128_off(t, 32 + 8 * c, 0);
+        for (int e = tid - kSplitWarp * 32; e < (kC - L) * 8; e += 128) {
+          const uint32_t at = (uint32_t)(L + e / 8) * 128u + (e % 8) * 16u;
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            tile_at<uint4>(S.p[b], sizeof(S.p[0]), at) = make_uint4(0, 0, 0, 0);
-            tile_at<uint4>(S.p[b], sizeof(S.p[0]), 8192 + at) = make_uint4(0, 0, 0, 0);
+            tile_at<uint4>(st.v[b], sizeof(st.v[b]), at) = make_uint4(0, 0, 0, 0);
+            tile_at<uint4>(st.qk[b], sizeof(st.qk[b]), 8192 + at) = make_uint4(0, 0, 0, 0);
           }
         }
+        umma::fence_proxy_async();
+        named_sync(2, 128);
       }
-      bool ok = true;
-      for (int i = 0; i < nit && ok; ++i) {
-        if (!(ok = wait_all(&S.g_full, i & 1))) break;
-        umma::fence_after();
-        // G(i)'s commit covers the products before it, O2(i - 2) among them: P's
-        // buffer is free
-        uint8_t* const pt = S.p[i & 1];
-        {
+      if (!ok) break;
+      if (i > 0 && !(ok = wait_all(&S.ds_full, (i - 1) & 1))) break;  // the operand was read
+      umma::fence_after();
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        // matrices of 8 tokens x 8 channels: lane / 8 = 2 (token group) + channel group
+        const int c = (4 * quarter + 2 * half + (lane >> 3 & 1));  // 16-byte piece of the 128 channels
+        const int r8 = lane & 7;
+        const uint32_t row = smem_addr(st.v[c >> 3]) + (uint32_t)(8 * (lane >> 4) + r8) * 128u + (((c & 7) ^ r8) << 4);
+        const uint32_t to = smem_addr(S.vw[c >> 3]) + (row - smem_addr(st.v[c >> 3]));
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            float g[16];
-            umma::tmem_ld16(tlane + TM_G + j0 + 16 * q, g);
+        for (int th = 0; th < 2; ++th) {  // 32 tokens
+          float2 x[8];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint32_t hi[4], lo[4];
+          for (int m = 0; m < 4; m += 2) {
+            uint32_t r[4];
+            ldmatrix4_t(row + (4 * th + m) * 1024u, r);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int e = 8 * c + 2 * k;
-                const int d = t - j0 - 16 * q - e;  // t - j
-                split2(make_float2(d >= 0 ? g[e] * S.ps[max(d, 0)] : 0.f, d >= 1 ? g[e + 1] * S.ps[max(d - 1, 0)] : 0.f),
-                       hi[k], lo[k]);
-              }
-              const uint32_t at = umma::sw128_off(t, j0 + 16 * q + 8 * c, 0);
-              tile_at<uint4>(pt, sizeof(S.p[0]), at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-              tile_at<uint4>(pt, sizeof(S.p[0]), 8192 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            for (int k = 0; k < 4; ++k)
+              x[2 * m + k] = make_float2(__uint_as_float(r[k] << 16), __uint_as_float(r[k] & 0xffff0000u));
+          }
+          if (L == kC) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = mul2(x[k], w[4 * th + k / 2]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int j = 8 * (4 * th + k / 2) + j0;
+              x[k] = make_float2(j < L ? x[k].x * S.pw[max(L - 1 - j, 0)] : 0.f,
+                                 j + 1 < L ? x[k].y * S.pw[max(L - 2 - j, 0)] : 0.f);
             }
           }
-          umma::fence_proxy_async();
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            uint32_t r[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) r[k] = take_bf16(x[k]);
+            tmem_put_frag(tlane + TM_VW + 32 * part + 16 * th, half, r);
+          }
+#pragma unroll
+          for (int m = 0; m < 4; m += 2) {
+            const uint32_t r[4] = {bf16_pair(x[2 * m]), bf16_pair(x[2 * m + 1]), bf16_pair(x[2 * m + 2]),
+                                   bf16_pair(x[2 * m + 3])};
+            stmatrix4_t(to + (4 * th + m) * 1024u, r);
+          }
         }
-        umma::fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.aux_full);
       }
-      if (!ok && lane == 0) report(a.err, GDN_DEV_ERR_TIMEOUT);
+      umma::fence_proxy_async();
+      tmem_wait_st();
+      umma::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.aux_full);
     }
+    if (!ok && lane == 0) report(a.err, GDN_DEV_ERR_TIMEOUT);
   } else if (warp >= kOutWarp) {
     // ------------------------------------------------------------------ outputs
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOutRegs));
@@ -453,41 +503,130 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; n_load < nit && ok; ++i)
           if ((ok = wait_all(&S.empty[i % kStages], (i / kStages) & 1))) load();
     } else {
+      // V channels 32 quarter .. + 31, transposed on the way to shared memory; a
+      // thread's tokens are 8 m + 2 (lane % 4), + 1
       const int quarter = warp & 3;
       const uint32_t tlane = tmem + ((uint32_t)(32 * quarter) << 16);
-      const auto out = GDN_GV(reinterpret_cast<__nv_bfloat16*>(a.out), a.total * ld);
-      for (int i = 0; i < nit && ok; ++i) {
-        const int L = count(i);
-        const int64_t at = (S.seg.t0 + from(i)) * ld + (int64_t)h * kD + 32 * quarter + lane;
-        if (!(ok = wait_all(&S.o_full, i & 1))) break;
-        umma::fence_after();
-        if (loader && n_load < nit) load();
-        __nv_bfloat162 o[kC / 2];
+      float2 f[8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          float o1[8], oh[8], ol[8];
-          tmem_ld8x3(tlane + TM_O1 + 8 * c, tlane + TM_O2 + 8 * c, tlane + TM_O2 + kC + 8 * c, o1, oh, ol);
+      for (int m = 0; m < 8; ++m) f[m] = make_float2(S.ps[8 * m + 2 * (lane & 3) + 1], S.ps[8 * m + 2 * (lane & 3) + 2]);
+      const auto out = GDN_GV(reinterpret_cast<uint4*>(a.out), a.total * ld / 8);
+      // P: rows 16 quarter .. + 15 (G's first 16 lanes of the quarter); a thread's
+      // rows are lane / 4, + 8 and its columns 8 m + 2 (lane % 4), + 1
+      const int pr = 16 * quarter + (lane >> 2), pc = 2 * (lane & 3);
+      // matrices of 8 rows x 8 columns: lane / 8 = 2 (column group) + row group
+      const uint32_t prow = (uint32_t)(16 * quarter + (lane & 15)) * 128u, pc8 = lane >> 4;
+      auto put_p = [&](int i) {
+        // G(i)'s commit covers the products before it, O2(i - 2) among them: P's
+        // buffer is free
+        const uint32_t pt = smem_addr(S.p[i & 1][0]) + prow;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = make_float2(S.ps[8 * c + 2 * e + 1], S.ps[8 * c + 2 * e + 2]);
-            o[4 * c + e] = __floats2bfloat162_rn(fmaf(f.x, o1[2 * e], oh[2 * e] + ol[2 * e]),
-                                                 fmaf(f.y, o1[2 * e + 1], oh[2 * e + 1] + ol[2 * e + 1]));
+        for (int cols = 0; cols < 2; ++cols) {  // 32 columns
+          if (cols == 1 && quarter < 2) break;  // above the diagonal: zeros since the start
+          float g[16];
+          tmem_get_frag(tlane + TM_G + 32 * cols, g);
+#pragma unroll
+          for (int m = 0; m < 4; m += 2) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {  // column group m + k / 2, row group k % 2
+              const int d = pr + 8 * (k & 1) - pc - 8 * (4 * cols + m + k / 2), e = 4 * (m + k / 2) + 2 * (k & 1);  // d: t - j
+              float2 x = make_float2(d >= 0 ? g[e] * S.ps[max(d, 0)] : 0.f, d >= 1 ? g[e + 1] * S.ps[max(d - 1, 0)] : 0.f);
+              hi[k] = take_bf16(x);
+              lo[k] = bf16_pair(x);
+            }
+            const uint32_t c = 4 * cols + m + pc8, to = pt + ((c ^ (lane & 7)) << 4);
+            stmatrix4(to, hi);
+            stmatrix4(to + 8192u, lo);
           }
         }
+        umma::fence_proxy_async();
         umma::fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.o_empty);
-        // a warp's 32 channels of a token are 64 consecutive bytes
-        __nv_bfloat16* const to = &out[at];
-        if (L == kC) {
+        if (lane == 0) mbar_arrive(&S.aux_full);
+      };
+      if (ok) ok = wait_all(&S.init, 0);  // the state tile has left p
+      if (ok && quarter < 2) {            // columns 32 .. of rows 0 .. 31: zeros, once
 #pragma unroll
-          for (int t = 0; t < kC; ++t) to[t * ld] = t & 1 ? o[t / 2].y : o[t / 2].x;
-        } else {
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int t = 0; t < kC; ++t)
-            if (t < L) to[t * ld] = t & 1 ? o[t / 2].y : o[t / 2].x;
-        }
+          for (int b = 0; b < 2; ++b)
+            tile_at<uint4>(S.p[b][lane >> 4], sizeof(S.p[0][0]), umma::sw128_off(16 * quarter + (lane & 15), 32 + 8 * c, 0)) =
+                make_uint4(0, 0, 0, 0);
       }
+      if (ok && (ok = wait_all(&S.g_full, 0))) {
+        umma::fence_after();
+        put_p(0);
+      }
+      for (int i = 0; i < nit && ok; ++i) {
+        const int L = count(i);
+        uint8_t* const ot = S.o[0];
+        if (i + 1 < nit) {
+          if ((ok = wait_all(&S.g_full, (i + 1) & 1))) {
+            umma::fence_after();
+            put_p(i + 1);
+          }
+        }
+        ok = ok && wait_all(&S.o_full, i & 1);
+        umma::fence_after();
+        if (loader && ok) {
+          if (n_load < nit) load();
+          if (lane == 0) bulk_wait_read();  // the last chunk's outputs have left their buffer
+        }
+        if (named_sync_or(3, 128, !ok)) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          // matrices of 8 tokens x 8 channels: lane / 8 = 2 (token group) + channel group
+          const int c = 4 * quarter + 2 * half + (lane >> 3 & 1), r8 = lane & 7;
+          const uint32_t row = smem_addr(ot) + (c >> 3) * 8192u + (uint32_t)(8 * (lane >> 4) + r8) * 128u + (((c & 7) ^ r8) << 4);
+#pragma unroll
+          for (int cols = 0; cols < 2; ++cols) {
+            float o1[16], o2[16];
+            tmem_get_frag2(tlane + TM_O1 + 32 * cols, tlane + TM_O2 + 32 * cols, half, o1, o2);
+            if (half == 1 && cols == 1) {
+              umma::fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&S.o_empty);
+            }
+#pragma unroll
+            for (int m = 0; m < 4; m += 2) {
+              uint32_t r[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int e = 4 * m + 2 * k;
+                r[k] = bf16_pair(fma2(f[4 * cols + m + k / 2], make_float2(o1[e], o1[e + 1]), make_float2(o2[e], o2[e + 1])));
+              }
+              stmatrix4_t(row + (4 * cols + m) * 1024u, r);
+            }
+          }
+        }
+        const int64_t t0 = S.seg.t0 + from(i);
+        if (L == kC) {
+          umma::fence_proxy_async();
+          named_sync(3, 128);
+          if (loader && lane == 0) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+              if (GDN_SPAN_G((int64_t)h * kD + 64 * b, 64, ld) && GDN_SPAN_G(t0, kC, a.total))
+                tma_store_2d(&omap, ot + 8192 * b, (int32_t)((int64_t)h * kD + 64 * b), (int32_t)t0);
+          }
+        } else {  // rows behind the chunk belong to others
+          named_sync(3, 128);
+#pragma unroll 1
+          for (int e = tid - kOutWarp * 32; e < L * 16; e += 128) {
+            const int t = e / 16, c = e % 16;
+            out[((t0 + t) * ld + (int64_t)h * kD) / 8 + c] =
+                tile_at<uint4>(ot, sizeof(S.o), (c >> 3) * 8192u + t * 128u + (((c & 7) ^ (t & 7)) << 4));
+          }
+        }
+        if (loader && lane == 0) bulk_commit();
+        __syncwarp();
+      }
+      if (loader && lane == 0) bulk_wait_all();
+      __syncwarp();
     }
     if (!ok && lane == 0) report(a.err, GDN_DEV_ERR_TIMEOUT);
     if (loader)  // what is in flight lands before the memory goes (at once, unless a wait expired)
@@ -506,39 +645,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto piece = [](int r, int p) { return (uint32_t)r * 512u + (uint32_t)((p ^ (r & 7)) << 4); };
     float2 st[32];
     {
-      float4 v[16];  // piece `lane` of rows warp, warp + 8, ..
-#pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-      auto place = [&](int j) { return own + ((warp + 8 * j) * 32 + lane) * 4; };
       const int seg = S.seg.seg, n_seg = S.seg.n_seg;
-      if (seg == 0) {
-        const bool kept = !STATE && n_seg > 1;
-        const auto src = kept ? GDN_GV((const float*)a.seg_state, a.n_segs * slot_n) + (S.seg.seg0 + n_seg - 1) * slot_n
-                              : GDN_GV((const float*)a.ssm, a.num_slots * slot_n) + S.seg.slot * slot_n;
+      const float dec = power(GDN_GV(a.log_decay, a.hv)[h], (int64_t)a.seg_chunks * kC);
+#pragma unroll 1
+      for (int part = 0; part < 2; ++part) {
+        float4 v[8];  // piece `lane` of rows warp + 64 part, + 8, ..
+        auto place = [&](int j) { return own + ((warp + 8 * j + 64 * part) * 32 + lane) * 4; };
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = vec_at<const float4>(src, place(j));
-        if (STATE) {
-          const auto keep = segs + (S.seg.seg0 + n_seg - 1) * slot_n;
+        for (int j = 0; j < 8; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (seg == 0) {
+          const bool kept = !STATE && n_seg > 1;
+          const auto src = kept ? GDN_GV((const float*)a.seg_state, a.n_segs * slot_n) + (S.seg.seg0 + n_seg - 1) * slot_n
+                                : GDN_GV((const float*)a.ssm, a.num_slots * slot_n) + S.seg.slot * slot_n;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) vec_at<float4>(keep, place(j)) = v[j];
-        }
-      } else if (!STATE) {
-        const float dec = power(GDN_GV(a.log_decay, a.hv)[h], (int64_t)a.seg_chunks * kC);
-        for (int k = 0; k < seg; ++k) {
-          const float d = k ? dec : 0.f;  // the first segment's state holds the slot's already
-          const auto from_seg = segs + (S.seg.seg0 + k) * slot_n;
+          for (int j = 0; j < 8; ++j) v[j] = vec_at<const float4>(src, place(j));
+          if (STATE) {
+            const auto keep = segs + (S.seg.seg0 + n_seg - 1) * slot_n;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float4 x = vec_at<const float4>(from_seg, place(j));
-            v[j].x = fmaf(d, v[j].x, x.x);
-            v[j].y = fmaf(d, v[j].y, x.y);
-            v[j].z = fmaf(d, v[j].z, x.z);
-            v[j].w = fmaf(d, v[j].w, x.w);
+            for (int j = 0; j < 8; ++j) vec_at<float4>(keep, place(j)) = v[j];
+          }
+        } else if (!STATE) {
+          for (int k = 0; k < seg; ++k) {
+            const float d = k ? dec : 0.f;  // the first segment's state holds the slot's already
+            const auto from_seg = segs + (S.seg.seg0 + k) * slot_n;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float4 x = vec_at<const float4>(from_seg, place(j));
+              v[j].x = fmaf(d, v[j].x, x.x);
+              v[j].y = fmaf(d, v[j].y, x.y);
+              v[j].z = fmaf(d, v[j].z, x.z);
+              v[j].w = fmaf(d, v[j].w, x.w);
+            }
           }
         }
-      }
 #pragma unroll
-      for (int j = 0; j < 16; ++j) tile_at<float4>(tile, kTile, piece(warp + 8 * j, lane)) = v[j];
+        for (int j = 0; j < 8; ++j) tile_at<float4>(tile, kTile, piece(warp + 8 * j + 64 * part, lane)) = v[j];
+      }
       named_sync(1, kStateThreads);
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
@@ -555,9 +697,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int q = 0; q < 2; ++q) {
         uint32_t hi[16], lo[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) split2(st[16 * q + e], hi[e], lo[e]);
-        tmem_put16(tlane + TM_SH + 32 * half + 16 * q, hi);
-        tmem_put16(tlane + TM_SL + 32 * half + 16 * q, lo);
+        for (int e = 0; e < 16; ++e) {
+          float2 x = st[16 * q + e];
+          hi[e] = take_bf16(x);
+          lo[e] = bf16_pair(x);
+        }
+        tmem_put16(tlane + TM_S + 32 * half + 16 * q, hi);
+        tmem_put16(tlane + TM_S + 64 + 32 * half + 16 * q, lo);
       }
       tmem_wait_st();
       umma::fence_before();
@@ -640,19 +786,21 @@ bool chunk_supported(const gdn_dims& d, int64_t total, const void* qkv, const vo
 }
 
 cudaError_t chunk_launch(const PrefillArgs& a, cudaStream_t s) {
-  CUtensorMap xmap;
+  CUtensorMap xmap, omap;
   cudaError_t e = tensor_map_2d(&xmap, a.qkv, a.total, a.C, 2, 64, kC, CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
+  if ((e = tensor_map_2d(&omap, a.out, a.total, (int64_t)a.hv * kD, 2, 64, kC, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess)
+    return e;
   const size_t smem = sizeof(ChunkSmem) + 1024;
   const dim3 grid(a.hv, a.n_segs);
   if (a.seg_state) {
     constexpr auto k = lin_chunk_kernel<true>;
     if ((e = ssm::allow_smem<k>(smem)) != cudaSuccess) return e;
-    if ((e = launch_pdl(k, grid, dim3(kThreads), smem, s, dim3(1), a, xmap)) != cudaSuccess) return e;
+    if ((e = launch_pdl(k, grid, dim3(kThreads), smem, s, dim3(1), a, xmap, omap)) != cudaSuccess) return e;
   }
   constexpr auto k = lin_chunk_kernel<false>;
   if ((e = ssm::allow_smem<k>(smem)) != cudaSuccess) return e;
-  return launch_pdl(k, grid, dim3(kThreads), smem, s, dim3(1), a, xmap);
+  return launch_pdl(k, grid, dim3(kThreads), smem, s, dim3(1), a, xmap, omap);
 }
 
 }  // namespace lin
