@@ -174,36 +174,27 @@ __device__ __forceinline__ void tmem_put16(uint32_t taddr, const uint32_t (&v)[1
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
-// Products issued by a whole converged warp, of which the thread with `lead`
-// set does it: descriptors and addresses that are the same for the warp stay in
-// its uniform registers, where the instruction wants them.  (Issued by one
-// thread alone, each product took some 100 cycles to assemble.)
+// Products with a constant accumulate flag, issued in runs by one thread inside
+// one branch of a converged warp: 48 cycles each with N = 64, where a predicate
+// per product took 59 and a loop over the whole issue code by a single thread
+// some 100.
 // D (TMEM) (+)= A B, both by descriptor
-__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       bool accumulate, int line = __builtin_LINE()) {
+template <bool ACC>
+__device__ __forceinline__ void mma_ss(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       int line = __builtin_LINE()) {
   if (!umma::tmem_ok(tmem_d, umma::idesc_n(idesc), false, line)) return;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead)
-      : "memory");
+  asm volatile("tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, %4;\n" ::"r"(tmem_d), "l"(a), "l"(b), "r"(idesc),
+               "n"((int)ACC)
+               : "memory");
 }
 // the same with A in TMEM (K = 16 values in 8 columns)
-__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t idesc,
-                                       bool accumulate, int line = __builtin_LINE()) {
+template <bool ACC>
+__device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t idesc,
+                                       int line = __builtin_LINE()) {
   if (!umma::tmem_ok(tmem_d, umma::idesc_n(idesc), false, line) || !umma::tmem_ok(tmem_a, 8, false, line)) return;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead)
-      : "memory");
-}
-__device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
-  asm volatile(
-      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
-      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_addr(bar)),
-      "r"(lead)
-      : "memory");
+  asm volatile("tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, %4;\n" ::"r"(tmem_d), "r"(tmem_a), "l"(b),
+               "r"(idesc), "n"((int)ACC)
+               : "memory");
 }
 
 __device__ __forceinline__ void st_global32(float* to, float4 a, float4 b) {
@@ -295,7 +286,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t ID_DS = umma::idesc_bf16(128, kD, false, true);   // V w in TMEM
       constexpr uint32_t ID_DS3 = umma::idesc_bf16(128, kD, true, true);  // in shared memory
       constexpr uint32_t ID_O2 = umma::idesc_bf16(128, kC, true, false);
-      const uint32_t lead = lane == 0;
       const uint64_t dq0 = umma::desc(smem_addr(S.st[0].qk[0]), 16, 1024);            // q as rows, k 8 KB on
       const uint64_t dk0 = umma::desc(smem_addr(S.st[0].qk[0]) + 8192, 16384, 1024);  // k as columns
       const uint64_t dv0 = umma::desc(smem_addr(S.st[0].v[0]), 8192, 1024);
@@ -304,12 +294,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       auto issue_g = [&](int s) {
         const uint64_t d = umma::adv(dq0, s * (uint32_t)sizeof(Stage));
+        if (lane == 0) {
+          mma_ss<false>(tmem + TM_G, d, umma::adv(d, 8192), ID_G);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t at = (k >> 2) * 16384 + (k & 3) * 32;
-          mma_ss(lead, tmem + TM_G, umma::adv(d, at), umma::adv(d, 8192 + at), ID_G, k > 0);
+          for (int k = 1; k < 8; ++k) {
+            const uint32_t at = (k >> 2) * 16384 + (k & 3) * 32;
+            mma_ss<true>(tmem + TM_G, umma::adv(d, at), umma::adv(d, 8192 + at), ID_G);
+          }
+          umma::commit(&S.g_full);
         }
-        commit(lead, &S.g_full);
+        __syncwarp();
       };
       if ((ok = wait_all(&S.full[0], 0)) && !STATE) {
         umma::fence_after();
@@ -325,19 +319,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait_all(&S.aux_full, i & 1) && (i == 0 || wait_all(&S.ds_empty, (i - 1) & 1));
         if (!ok) break;
         umma::fence_after();
-        {
+        if (lane == 0) {
           const uint64_t dk = umma::adv(dk0, at);
+          mma_ss<false>(tmem + TM_DS, dvw, dk, ID_DS3);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_ss(lead, tmem + TM_DS, umma::adv(dvw, 2048 * k), umma::adv(dk, 2048 * k), ID_DS3, k > 0);
+          for (int k = 1; k < 4; ++k) mma_ss<true>(tmem + TM_DS, umma::adv(dvw, 2048 * k), umma::adv(dk, 2048 * k), ID_DS3);
 #pragma unroll
           for (int part = 1; part >= 0; --part)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_ts(lead, tmem + TM_DS, tmem + TM_VW + 32 * part + 8 * k, umma::adv(dk, 2048 * k), ID_DS, true);
-          commit(lead, &S.ds_full);
-          if (STATE) commit(lead, &S.empty[s]);
+              mma_ts<true>(tmem + TM_DS, tmem + TM_VW + 32 * part + 8 * k, umma::adv(dk, 2048 * k), ID_DS);
+          umma::commit(&S.ds_full);
+          if (STATE) umma::commit(&S.empty[s]);
         }
+        __syncwarp();
         if (i + 1 < nit) {
           if (!(ok = wait_all(&S.full[s1], s1_par))) break;
           if (!STATE) {
@@ -349,35 +344,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           // O2^T = V^T P^T
           if (i > 0 && !(ok = wait_all(&S.o_empty, (i - 1) & 1))) break;
           umma::fence_after();
-          {
+          if (lane == 0) {
             const uint64_t dv = umma::adv(dv0, at), dp = umma::adv(dp0, (i & 1) * (uint32_t)sizeof(S.p[0]));
+            mma_ss<false>(tmem + TM_O2, dv, umma::adv(dp, 8192), ID_O2);
 #pragma unroll
-            for (int part = 1; part >= 0; --part)
+            for (int k = 1; k < 4; ++k)
+              mma_ss<true>(tmem + TM_O2, umma::adv(dv, 2048 * k), umma::adv(dp, 8192 + 32 * k), ID_O2);
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_ss(lead, tmem + TM_O2, umma::adv(dv, 2048 * k), umma::adv(dp, part * 8192 + 32 * k), ID_O2,
-                       part == 0 || k > 0);
+            for (int k = 0; k < 4; ++k) mma_ss<true>(tmem + TM_O2, umma::adv(dv, 2048 * k), umma::adv(dp, 32 * k), ID_O2);
           }
+          __syncwarp();
           // O1^T = S^T Q^T
           if (!(ok = wait_all(&S.s_full, i & 1))) break;
           umma::fence_after();
-          {
+          if (lane == 0) {
             const uint64_t dq = umma::adv(dq0, at);
+            mma_ts<false>(tmem + TM_O1, tmem + TM_S + 64, dq, ID_O1);
 #pragma unroll
-            for (int part = 1; part >= 0; --part)
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                mma_ts(lead, tmem + TM_O1, tmem + TM_S + 64 * part + 8 * k,
-                       umma::adv(dq, (k >> 2) * 16384 + (k & 3) * 32), ID_O1, part == 0 || k > 0);
-            commit(lead, &S.o_full);
+            for (int k = 1; k < 16; ++k)
+              mma_ts<true>(tmem + TM_O1, tmem + TM_S + (k < 8 ? 64 : 0) + 8 * (k & 7),
+                           umma::adv(dq, (k >> 2 & 1) * 16384 + (k & 3) * 32), ID_O1);
+            umma::commit(&S.o_full);
           }
+          __syncwarp();
         }
         s = s1;
         s_par = s1_par;
       }
       if (!ok && lane == 0) report(a.err, GDN_DEV_ERR_TIMEOUT);
       // the products in flight end before their memory is used otherwise
-      commit(lead, &S.drained);
+      if (lane == 0) umma::commit(&S.drained);
+      __syncwarp();
       wait_all(&S.drained, 0);
     }
     __syncwarp();
