@@ -29,9 +29,11 @@
 // shared memory take all its bandwidth: two parts of V w therefore go through
 // registers to TMEM, whose 512 columns are all in use.
 //
-// 17 warps by role (of 20): 8 hold S (2 per 32 V channels, 64 dk columns each), 4
+// 18 warps by role (of 20): 8 hold S (2 per 32 V channels, 64 dk columns each), 4
 // make P from G and write outputs (one of them issues the copies), 4 scale and
-// split V, one issues the products.
+// split V, and two issue the products: dS and O1, and G and O2.  The tensor core
+// takes a product about when the one before it is done, so that one issuer's
+// waits for the other warps left it idle a third of the time.
 #include "lin.cuh"
 
 #include "decode_tma.cuh"  // sm_count
@@ -45,7 +47,7 @@ namespace {
 
 constexpr int kD = 128;  // dk = dv
 constexpr int kStages = 3;
-constexpr int kStateWarps = 8, kOutWarp = 8, kSplitWarp = 12, kIssuer = 16;
+constexpr int kStateWarps = 8, kOutWarp = 8, kSplitWarp = 12, kIssuer = 16;  // 16: dS, O1; 17: G, O2
 constexpr int kThreads = 20 * 32;
 constexpr int kStateThreads = kStateWarps * 32;
 // Registers per thread, by warpgroup (state, state, output, split, issuer);
@@ -67,12 +69,15 @@ struct __align__(1024) ChunkSmem {
   uint8_t p[2][2][64 * 128];    // P [t][j], by the chunk's parity: its two parts
   uint8_t o[2][64 * 128];       // outputs [t][dv], 64-column blocks
   uint8_t vw[2][64 * 128];      // V w's third part [j][dv], 64-column blocks
+  uint8_t ck[kStateWarps][32 * 64];  // a state warp's rows on their way to a checkpoint, 16 columns
   float pw[kC + 1];             // lambda^n
   float ps[kC + 1];             // scale lambda^n
   Segment seg;
   int some;
   uint64_t full[kStages], empty[kStages];
-  uint64_t g_full, aux_full, ds_full, ds_empty, s_full, o_full, o_empty, init, drained;
+  // ds_go: V w is there, the last dS has been read; o1_go: S is there, the last
+  // outputs have been read; o2_go: the latter
+  uint64_t g_full, p_full, ds_go, ds_full, o1_go, o2_go, o_full, init, drained;
   uint32_t tmem_base;
 };
 // The state tile's way between global memory and the threads' rows: 64 KB from
@@ -197,12 +202,6 @@ __device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_
                : "memory");
 }
 
-__device__ __forceinline__ void st_global32(float* to, float4 a, float4 b) {
-  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(to), "f"(a.x), "f"(a.y), "f"(a.z), "f"(a.w),
-               "f"(b.x), "f"(b.y), "f"(b.z), "f"(b.w)
-               : "memory");
-}
-
 // wait of a whole warp
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity));
@@ -227,14 +226,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.empty[i], 1);
     }
     mbar_init(&S.g_full, 1);
-    mbar_init(&S.aux_full, STATE ? 4 : 4 + 4);
+    mbar_init(&S.p_full, 4 + 4);
+    mbar_init(&S.ds_go, 4 + kStateWarps);
     mbar_init(&S.ds_full, 1);
-    mbar_init(&S.ds_empty, kStateWarps);
-    mbar_init(&S.s_full, kStateWarps);
-    mbar_init(&S.o_full, 1);
-    mbar_init(&S.o_empty, 4);
+    mbar_init(&S.o1_go, kStateWarps + 4);
+    mbar_init(&S.o2_go, 4);
+    mbar_init(&S.o_full, 2);
     mbar_init(&S.init, kStateWarps);
-    mbar_init(&S.drained, 1);
+    mbar_init(&S.drained, STATE ? 1 : 2);
     fence_mbar_init();
   }
   pdl_wait();
@@ -277,47 +276,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= kIssuer) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRestRegs));
+    const uint64_t dq0 = umma::desc(smem_addr(S.st[0].qk[0]), 16, 1024);  // q as rows, k 8 KB on
+    bool ok = true;
+    int s = 0, s_par = 0;  // a chunk's stage and its phase
+    auto next = [&]() {
+      if (++s == kStages) {
+        s = 0;
+        s_par ^= 1;
+      }
+    };
     if (warp == kIssuer) {
-      // ---------------------------------------------------------------- issuer
-      // Order per chunk i: dS(i), G(i + 1), O2(i), O1(i): whatever the other
-      // warps make of one product has two more products' time.
-      constexpr uint32_t ID_G = umma::idesc_bf16(64, kC, false, false);
-      constexpr uint32_t ID_O1 = umma::idesc_bf16(128, kC, false, false);
+      // ------------------------------------------------------- issuer of dS, O1
       constexpr uint32_t ID_DS = umma::idesc_bf16(128, kD, false, true);   // V w in TMEM
       constexpr uint32_t ID_DS3 = umma::idesc_bf16(128, kD, true, true);  // in shared memory
-      constexpr uint32_t ID_O2 = umma::idesc_bf16(128, kC, true, false);
-      const uint64_t dq0 = umma::desc(smem_addr(S.st[0].qk[0]), 16, 1024);            // q as rows, k 8 KB on
+      constexpr uint32_t ID_O1 = umma::idesc_bf16(128, kC, false, false);
       const uint64_t dk0 = umma::desc(smem_addr(S.st[0].qk[0]) + 8192, 16384, 1024);  // k as columns
-      const uint64_t dv0 = umma::desc(smem_addr(S.st[0].v[0]), 8192, 1024);
-      const uint64_t dp0 = umma::desc(smem_addr(S.p[0][0]), 16, 1024);
       const uint64_t dvw = umma::desc(smem_addr(S.vw[0]), 8192, 1024);
-      bool ok = true;
-      auto issue_g = [&](int s) {
-        const uint64_t d = umma::adv(dq0, s * (uint32_t)sizeof(Stage));
-        if (lane == 0) {
-          mma_ss<false>(tmem + TM_G, d, umma::adv(d, 8192), ID_G);
-#pragma unroll
-          for (int k = 1; k < 8; ++k) {
-            const uint32_t at = (k >> 2) * 16384 + (k & 3) * 32;
-            mma_ss<true>(tmem + TM_G, umma::adv(d, at), umma::adv(d, 8192 + at), ID_G);
-          }
-          umma::commit(&S.g_full);
-        }
-        __syncwarp();
-      };
-      if ((ok = wait_all(&S.full[0], 0)) && !STATE) {
-        umma::fence_after();
-        issue_g(0);
-      }
-      int s = 0, s_par = 0;  // chunk i's stage and its phase
 #pragma unroll 1
-      for (int i = 0; i < nit && ok; ++i) {
+      for (int i = 0; i < nit; ++i, next()) {
         const uint32_t at = s * (uint32_t)sizeof(Stage);
-        const int s1 = s + 1 == kStages ? 0 : s + 1, s1_par = s1 ? s_par : s_par ^ 1;
-        // dS^T = (V w)^T K, the small parts first.  V w and P of this chunk are
-        // there (so G's columns have been read, too).
-        ok = wait_all(&S.aux_full, i & 1) && (i == 0 || wait_all(&S.ds_empty, (i - 1) & 1));
-        if (!ok) break;
+        // dS^T = (V w)^T K, the small parts first (whoever split V has seen the
+        // chunk's copies land)
+        if (!(ok = wait_all(&S.ds_go, i & 1))) break;
         umma::fence_after();
         if (lane == 0) {
           const uint64_t dk = umma::adv(dk0, at);
@@ -333,29 +313,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (STATE) umma::commit(&S.empty[s]);
         }
         __syncwarp();
-        if (i + 1 < nit) {
-          if (!(ok = wait_all(&S.full[s1], s1_par))) break;
-          if (!STATE) {
-            umma::fence_after();
-            issue_g(s1);
-          }
-        }
         if (!STATE) {
-          // O2^T = V^T P^T
-          if (i > 0 && !(ok = wait_all(&S.o_empty, (i - 1) & 1))) break;
-          umma::fence_after();
-          if (lane == 0) {
-            const uint64_t dv = umma::adv(dv0, at), dp = umma::adv(dp0, (i & 1) * (uint32_t)sizeof(S.p[0]));
-            mma_ss<false>(tmem + TM_O2, dv, umma::adv(dp, 8192), ID_O2);
-#pragma unroll
-            for (int k = 1; k < 4; ++k)
-              mma_ss<true>(tmem + TM_O2, umma::adv(dv, 2048 * k), umma::adv(dp, 8192 + 32 * k), ID_O2);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mma_ss<true>(tmem + TM_O2, umma::adv(dv, 2048 * k), umma::adv(dp, 32 * k), ID_O2);
-          }
-          __syncwarp();
           // O1^T = S^T Q^T
-          if (!(ok = wait_all(&S.s_full, i & 1))) break;
+          if (!(ok = wait_all(&S.o1_go, i & 1))) break;
           umma::fence_after();
           if (lane == 0) {
             const uint64_t dq = umma::adv(dq0, at);
@@ -368,16 +328,61 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
-        s = s1;
-        s_par = s1_par;
       }
+    } else if (!STATE && warp == kIssuer + 1) {
+      // -------------------------------------------------------- issuer of G, O2
+      constexpr uint32_t ID_G = umma::idesc_bf16(64, kC, false, false);
+      constexpr uint32_t ID_O2 = umma::idesc_bf16(128, kC, true, false);
+      const uint64_t dv0 = umma::desc(smem_addr(S.st[0].v[0]), 8192, 1024);
+      const uint64_t dp0 = umma::desc(smem_addr(S.p[0][0]), 16, 1024);
+      uint32_t at = 0;  // the stage of the chunk whose G is next
+      auto issue_g = [&]() -> bool {
+        if (!wait_all(&S.full[s], s_par)) return false;
+        umma::fence_after();
+        at = s * (uint32_t)sizeof(Stage);
+        if (lane == 0) {
+          const uint64_t d = umma::adv(dq0, at);
+          mma_ss<false>(tmem + TM_G, d, umma::adv(d, 8192), ID_G);
+#pragma unroll
+          for (int k = 1; k < 8; ++k) {
+            const uint32_t o = (k >> 2) * 16384 + (k & 3) * 32;
+            mma_ss<true>(tmem + TM_G, umma::adv(d, o), umma::adv(d, 8192 + o), ID_G);
+          }
+          umma::commit(&S.g_full);
+        }
+        __syncwarp();
+        next();
+        return true;
+      };
+      ok = issue_g();
+#pragma unroll 1
+      for (int i = 0; i < nit && ok; ++i) {
+        const uint64_t dv = umma::adv(dv0, at), dp = umma::adv(dp0, (i & 1) * (uint32_t)sizeof(S.p[0]));
+        // P of this chunk is there (G's columns have been read), its V is clean
+        if (!(ok = wait_all(&S.p_full, i & 1))) break;
+        if (i + 1 < nit && !(ok = issue_g())) break;
+        // O2^T = V^T P^T
+        if (!(ok = wait_all(&S.o2_go, i & 1))) break;
+        umma::fence_after();
+        if (lane == 0) {
+          mma_ss<false>(tmem + TM_O2, dv, umma::adv(dp, 8192), ID_O2);
+#pragma unroll
+          for (int k = 1; k < 4; ++k)
+            mma_ss<true>(tmem + TM_O2, umma::adv(dv, 2048 * k), umma::adv(dp, 8192 + 32 * k), ID_O2);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma_ss<true>(tmem + TM_O2, umma::adv(dv, 2048 * k), umma::adv(dp, 32 * k), ID_O2);
+          umma::commit(&S.o_full);
+        }
+        __syncwarp();
+      }
+    }
+    if (warp == kIssuer || (!STATE && warp == kIssuer + 1)) {
       if (!ok && lane == 0) report(a.err, GDN_DEV_ERR_TIMEOUT);
       // the products in flight end before their memory is used otherwise
       if (lane == 0) umma::commit(&S.drained);
       __syncwarp();
       wait_all(&S.drained, 0);
     }
-    __syncwarp();
   } else if (warp >= kSplitWarp) {
     // --------------------------------------------------------------- V w, split
     // V channels 32 quarter .. + 31 of every token, transposed on the way to
@@ -461,7 +466,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_wait_st();
       umma::fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.aux_full);
+      if (lane == 0) mbar_arrive(&S.ds_go);
+      if (!STATE) {
+        // after G(i), so that p_full's phases do not mix: G(i) is issued once
+        // P(i - 1) is there
+        if (!(ok = wait_all(&S.g_full, i & 1))) break;
+        if (lane == 0) mbar_arrive(&S.p_full);
+      }
     }
     if (!ok && lane == 0) report(a.err, GDN_DEV_ERR_TIMEOUT);
   } else if (warp >= kOutWarp) {
@@ -540,8 +551,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma::fence_proxy_async();
         umma::fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.aux_full);
+        if (lane == 0) mbar_arrive(&S.p_full);
       };
+      if (lane == 0) {  // nothing to read yet
+        mbar_arrive(&S.o1_go);
+        mbar_arrive(&S.o2_go);
+      }
       if (ok) ok = wait_all(&S.init, 0);  // the state tile has left p
       if (ok && quarter < 2) {            // columns 32 .. of rows 0 .. 31: zeros, once
 #pragma unroll
@@ -586,7 +601,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (half == 1 && cols == 1) {
               umma::fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(&S.o_empty);
+              if (lane == 0) {
+                mbar_arrive(&S.o1_go);
+                mbar_arrive(&S.o2_go);
+              }
             }
 #pragma unroll
             for (int m = 0; m < 4; m += 2) {
@@ -705,9 +723,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_wait_st();
       umma::fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.s_full);
+      if (lane == 0) mbar_arrive(&S.o1_go);
     };
     if (!STATE) put_s();
+    if (lane == 0) mbar_arrive(&S.ds_go);  // no dS to read yet
     bool ok = true;
 #pragma unroll 1
     for (int i = 0; i < nit && ok; ++i) {
@@ -725,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       umma::fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.ds_empty);
+      if (lane == 0) mbar_arrive(&S.ds_go);
       if (!STATE) {
         if (i + 1 < nit) {
           if (!(ok = wait_all(&S.o_full, i & 1))) break;  // the operand was read
@@ -741,14 +760,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int cls = slot_class(id, a.ck_num_slots);
             if (cls == 2 && tid == 0) report(a.err, GDN_DEV_ERR_SLOT_OOB);
             if (cls == 0) {
-              const auto to = GDN_GV(a.ck_ssm, a.ck_num_slots * slot_n) + (id * slot_n + own + row * kD + 64 * half);
-              if (((uintptr_t)a.ck_ssm & 31) == 0) {
+              // 16 columns at a time through the warp's 2 KB, so that 64 bytes
+              // of a row leave together (32 bytes from each lane's own row
+              // took 5,000 cycles)
+              const auto to = GDN_GV(a.ck_ssm, a.ck_num_slots * slot_n) + (id * slot_n + own + (row - lane) * kD + 64 * half);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  st_global32(to.at(8 * e, 8), join4(st[4 * e], st[4 * e + 1]), join4(st[4 * e + 2], st[4 * e + 3]));
-              } else {
+              for (int q = 0; q < 4; ++q) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) vec_at<float4>(to, 4 * e) = join4(st[2 * e], st[2 * e + 1]);
+                for (int e = 0; e < 4; ++e)
+                  tile_at<float4>(S.ck[warp], sizeof(S.ck[0]), (uint32_t)lane * 64u + ((e ^ (lane >> 1 & 3)) << 4)) =
+                      join4(st[8 * q + 2 * e], st[8 * q + 2 * e + 1]);
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const int r = 8 * j + lane / 4;
+                  vec_at<float4>(to, r * kD + 16 * q + 4 * (lane & 3)) =
+                      tile_at<float4>(S.ck[warp], sizeof(S.ck[0]), (uint32_t)r * 64u + (((lane & 3) ^ (r >> 1 & 3)) << 4));
+                }
+                __syncwarp();
               }
             }
           }
