@@ -21,8 +21,7 @@
 // states and checkpoints keep fp32's accuracy; P and S^T, which only outputs
 // see, into two (16 bits, off by at most 2^-16 of a term, against the output's
 // own 2^-8; with one part each the outputs were 2.4e-3 off instead of 1.7e-3).
-// bf16 parts keep fp32's range, so no scaling is needed; values from 3.39e38 on
-// become infinite.
+// bf16 parts keep fp32's range, so no scaling is needed.
 //
 // A product of K = 16 takes some 59 cycles with N = 64 and 67 to 73 with N = 128
 // (measured; M = 64 no less than M = 128), 2,800 a chunk, and both operands from
@@ -52,7 +51,7 @@ constexpr int kThreads = 20 * 32;
 constexpr int kStateThreads = kStateWarps * 32;
 // Registers per thread, by warpgroup (state, state, output, split, issuer);
 // 640 x 96 at launch is what there is.
-constexpr int kStateRegs = 136, kOutRegs = 88, kSplitRegs = 72, kRestRegs = 48;
+constexpr int kStateRegs = 136, kOutRegs = 80, kSplitRegs = 80, kRestRegs = 48;
 static_assert(2 * kStateRegs + kOutRegs + kSplitRegs + kRestRegs <= 5 * 96, "the launch's registers");
 
 // TMEM columns.  G (M = 64) is in the first 16 lanes of each warp's 32; S^T and
@@ -75,9 +74,10 @@ struct __align__(1024) ChunkSmem {
   Segment seg;
   int some;
   uint64_t full[kStages], empty[kStages];
-  // ds_go: V w is there, the last dS has been read; o1_go: S is there, the last
-  // outputs have been read; o2_go: the latter
-  uint64_t g_full, p_full, ds_go, ds_full, o1_go, o2_go, o_full, init, drained;
+  // dsa_go: V w of the chunk's first 32 tokens is there, the last dS has been
+  // read; dsb_go: that of its last 32; dsa_done: the former's products are done;
+  // o1_go: S is there, the last outputs have been read; o2_go: the latter
+  uint64_t g_full, p_full, dsa_go, dsb_go, dsa_done, ds_full, o1_go, o2_go, o_full, init, drained;
   uint32_t tmem_base;
 };
 // The state tile's way between global memory and the threads' rows: 64 KB from
@@ -87,12 +87,12 @@ constexpr unsigned kTile = kD * kD * 4;
 static_assert(sizeof(ChunkSmem) + 1024 <= 232448, "shared memory of a CTA");
 static_assert(offsetof(ChunkSmem, vw) - offsetof(ChunkSmem, st) - (kStages - 1) * sizeof(Stage) >= kTile, "state tile");
 
-// hi: x rounded to bf16, packed in pairs; x: what is left of it, exactly
+// The leading 8 bits of both values as bf16, packed in pairs; x: what is left
+// of it, exactly.  Three parts hold all of an fp32 value's 24 bits.
 __device__ __forceinline__ uint32_t take_bf16(float2& x) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
-  const uint32_t hi = *reinterpret_cast<const uint32_t*>(&h);
-  x = fma2(make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)), make_float2(-1.f, -1.f), x);
-  return hi;
+  const uint32_t u = __float_as_uint(x.x), v = __float_as_uint(x.y);
+  x = fma2(make_float2(__uint_as_float(u & 0xffff0000u), __uint_as_float(v & 0xffff0000u)), make_float2(-1.f, -1.f), x);
+  return __byte_perm(u, v, 0x7632);
 }
 __device__ __forceinline__ uint32_t bf16_pair(float2 x) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
@@ -227,7 +227,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&S.g_full, 1);
     mbar_init(&S.p_full, 4 + 4);
-    mbar_init(&S.ds_go, 4 + kStateWarps);
+    mbar_init(&S.dsa_go, 4 + kStateWarps);
+    mbar_init(&S.dsb_go, 4);
+    mbar_init(&S.dsa_done, 1);
     mbar_init(&S.ds_full, 1);
     mbar_init(&S.o1_go, kStateWarps + 4);
     mbar_init(&S.o2_go, 4);
@@ -297,22 +299,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t at = s * (uint32_t)sizeof(Stage);
         // dS^T = (V w)^T K, the small parts first (whoever split V has seen the
         // chunk's copies land)
-        if (!(ok = wait_all(&S.ds_go, i & 1))) break;
-        umma::fence_after();
-        if (lane == 0) {
-          const uint64_t dk = umma::adv(dk0, at);
-          mma_ss<false>(tmem + TM_DS, dvw, dk, ID_DS3);
+        const uint64_t dk = umma::adv(dk0, at);
 #pragma unroll
-          for (int k = 1; k < 4; ++k) mma_ss<true>(tmem + TM_DS, umma::adv(dvw, 2048 * k), umma::adv(dk, 2048 * k), ID_DS3);
+        for (int th = 0; th < 2; ++th) {  // 32 tokens, whose V w may be replaced under the others' products
+          if (!(ok = wait_all(th ? &S.dsb_go : &S.dsa_go, i & 1))) break;
+          umma::fence_after();
+          if (lane == 0) {
 #pragma unroll
-          for (int part = 1; part >= 0; --part)
+            for (int k = 2 * th; k < 2 * th + 2; ++k) {
+              if (k == 0) mma_ss<false>(tmem + TM_DS, dvw, dk, ID_DS3);
+              else mma_ss<true>(tmem + TM_DS, umma::adv(dvw, 2048 * k), umma::adv(dk, 2048 * k), ID_DS3);
+            }
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ts<true>(tmem + TM_DS, tmem + TM_VW + 32 * part + 8 * k, umma::adv(dk, 2048 * k), ID_DS);
-          umma::commit(&S.ds_full);
-          if (STATE) umma::commit(&S.empty[s]);
+            for (int part = 1; part >= 0; --part)
+#pragma unroll
+              for (int k = 2 * th; k < 2 * th + 2; ++k)
+                mma_ts<true>(tmem + TM_DS, tmem + TM_VW + 32 * part + 8 * k, umma::adv(dk, 2048 * k), ID_DS);
+            umma::commit(th ? &S.ds_full : &S.dsa_done);
+            if (STATE && th) umma::commit(&S.empty[s]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        if (!ok) break;
         if (!STATE) {
           // O1^T = S^T Q^T
           if (!(ok = wait_all(&S.o1_go, i & 1))) break;
@@ -416,17 +424,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         named_sync(2, 128);
       }
       if (!ok) break;
-      if (i > 0 && !(ok = wait_all(&S.ds_full, (i - 1) & 1))) break;  // the operand was read
-      umma::fence_after();
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        // matrices of 8 tokens x 8 channels: lane / 8 = 2 (token group) + channel group
-        const int c = (4 * quarter + 2 * half + (lane >> 3 & 1));  // 16-byte piece of the 128 channels
-        const int r8 = lane & 7;
-        const uint32_t row = smem_addr(st.v[c >> 3]) + (uint32_t)(8 * (lane >> 4) + r8) * 128u + (((c & 7) ^ r8) << 4);
-        const uint32_t to = smem_addr(S.vw[c >> 3]) + (row - smem_addr(st.v[c >> 3]));
 #pragma unroll
-        for (int th = 0; th < 2; ++th) {  // 32 tokens
+      for (int th = 0; th < 2; ++th) {  // 32 tokens
+        // the operand was read by the last chunk's products
+        if (i > 0 && !(ok = wait_all(th ? &S.ds_full : &S.dsa_done, (i - 1) & 1))) break;
+        umma::fence_after();
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          // matrices of 8 tokens x 8 channels: lane / 8 = 2 (token group) + channel group
+          const int c = 4 * quarter + 2 * half + (lane >> 3 & 1);  // 16-byte piece of the 128 channels
+          const int r8 = lane & 7;
+          const uint32_t off = (c >> 3) * 8192u + (uint32_t)(8 * (lane >> 4) + r8) * 128u + (((c & 7) ^ r8) << 4);
+          const uint32_t row = smem_addr(st.v[0]) + off, to = smem_addr(S.vw[0]) + off;
           float2 x[8];
 #pragma unroll
           for (int m = 0; m < 4; m += 2) {
@@ -456,17 +465,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int m = 0; m < 4; m += 2) {
-            const uint32_t r[4] = {bf16_pair(x[2 * m]), bf16_pair(x[2 * m + 1]), bf16_pair(x[2 * m + 2]),
-                                   bf16_pair(x[2 * m + 3])};
+            uint32_t r[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) r[k] = take_bf16(x[2 * m + k]);
             stmatrix4_t(to + (4 * th + m) * 1024u, r);
           }
         }
+        umma::fence_proxy_async();
+        tmem_wait_st();
+        umma::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(th ? &S.dsb_go : &S.dsa_go);
       }
-      umma::fence_proxy_async();
-      tmem_wait_st();
-      umma::fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.ds_go);
+      if (!ok) break;
       if (!STATE) {
         // after G(i), so that p_full's phases do not mix: G(i) is issued once
         // P(i - 1) is there
@@ -726,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&S.o1_go);
     };
     if (!STATE) put_s();
-    if (lane == 0) mbar_arrive(&S.ds_go);  // no dS to read yet
+    if (lane == 0) mbar_arrive(&S.dsa_go);  // no dS to read yet
     bool ok = true;
 #pragma unroll 1
     for (int i = 0; i < nit && ok; ++i) {
@@ -744,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       umma::fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.ds_go);
+      if (lane == 0) mbar_arrive(&S.dsa_go);
       if (!STATE) {
         if (i + 1 < nit) {
           if (!(ok = wait_all(&S.o_full, i & 1))) break;  // the operand was read
