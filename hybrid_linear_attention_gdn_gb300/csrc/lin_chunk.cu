@@ -51,7 +51,7 @@ constexpr int kThreads = 20 * 32;
 constexpr int kStateThreads = kStateWarps * 32;
 // Registers per thread, by warpgroup (state, state, output, split, issuer);
 // 640 x 96 at launch is what there is.
-constexpr int kStateRegs = 136, kOutRegs = 80, kSplitRegs = 80, kRestRegs = 48;
+constexpr int kStateRegs = 136, kOutRegs = 72, kSplitRegs = 72, kRestRegs = 64;
 static_assert(2 * kStateRegs + kOutRegs + kSplitRegs + kRestRegs <= 5 * 96, "the launch's registers");
 
 // TMEM columns.  G (M = 64) is in the first 16 lanes of each warp's 32; S^T and
@@ -69,8 +69,10 @@ struct __align__(1024) ChunkSmem {
   uint8_t o[2][64 * 128];       // outputs [t][dv], 64-column blocks
   uint8_t vw[2][64 * 128];      // V w's third part [j][dv], 64-column blocks
   uint8_t ck[kStateWarps][32 * 64];  // a state warp's rows on their way to a checkpoint, 16 columns
-  float pw[kC + 1];             // lambda^n
-  float ps[kC + 1];             // scale lambda^n
+  __align__(16) float w[2 * kC];  // lambda^(63 - j), zeros from 64 on
+  float ps[kC];                 // scale lambda^n
+  float pt[kC];                 // scale lambda^(n + 1)
+  float dec[kC + 1];            // lambda^n
   Segment seg;
   int some;
   uint64_t full[kStages], empty[kStages];
@@ -128,19 +130,18 @@ __device__ __forceinline__ void tmem_put_frag(uint32_t taddr, int half, const ui
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
       : "memory");
 }
-// the warp's first 16 lanes x 32 columns: register 4 m + 2 g + e of a thread is
+// the warp's first 16 lanes x 16 columns: register 4 m + 2 g + e of a thread is
 // lane lane / 4 + 8 g, column 8 m + 2 (lane % 4) + e
-__device__ __forceinline__ void tmem_get_frag(uint32_t taddr, float (&v)[16], int line = __builtin_LINE()) {
-  if (!umma::tmem_ok(taddr, 32, true, line)) {
+__device__ __forceinline__ void tmem_get_frag(uint32_t taddr, float (&v)[8], int line = __builtin_LINE()) {
+  if (!umma::tmem_ok(taddr, 16, true, line)) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0.f;
+    for (int i = 0; i < 8; ++i) v[i] = 0.f;
     return;
   }
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
       "tcgen05.wait::ld.sync.aligned;\n"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
       : "r"(taddr)
       : "memory");
 }
@@ -248,11 +249,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       S.some = some && !(STATE && (s.seg == s.n_seg - 1 || s.padded));
     }
   }
-  if (tid >= 96 && tid < 96 + kC + 1) {
+  if (tid >= 96 && tid < 96 + 2 * kC) {
     const int n = tid - 96;
-    const float p = power(GDN_GV(a.log_decay, a.hv)[h], n);
-    S.pw[n] = p;
-    S.ps[n] = p * a.scale;
+    const float ld_h = GDN_GV(a.log_decay, a.hv)[h], x = n <= kC ? power(ld_h, n) : 0.f;
+    if (n <= kC) S.dec[n] = x;
+    S.w[n < kC ? kC - 1 - n : n] = n < kC ? x : 0.f;
+    if (n < kC) S.ps[n] = x * a.scale;
+    if (n >= 1 && n <= kC) S.pt[n - 1] = x * a.scale;
   }
   umma::fence_before();
   __syncthreads();
@@ -398,9 +401,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kSplitRegs));
     const int quarter = warp & 3, j0 = 2 * (lane & 3);
     const uint32_t tlane = tmem + ((uint32_t)(32 * quarter) << 16);
-    float2 w[8];
-#pragma unroll
-    for (int m = 0; m < 8; ++m) w[m] = make_float2(S.pw[kC - 1 - 8 * m - j0], S.pw[kC - 2 - 8 * m - j0]);
     bool ok = true;
     for (int i = 0; i < nit && ok; ++i) {
       Stage& st = S.st[i % kStages];
@@ -424,37 +424,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         named_sync(2, 128);
       }
       if (!ok) break;
-#pragma unroll
+      const float* const wl = &S.w[kC - L + j0];  // of tokens j0, ..
+#pragma unroll 1
       for (int th = 0; th < 2; ++th) {  // 32 tokens
         // the operand was read by the last chunk's products
         if (i > 0 && !(ok = wait_all(th ? &S.ds_full : &S.dsa_done, (i - 1) & 1))) break;
         umma::fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           // matrices of 8 tokens x 8 channels: lane / 8 = 2 (token group) + channel group
           const int c = 4 * quarter + 2 * half + (lane >> 3 & 1);  // 16-byte piece of the 128 channels
           const int r8 = lane & 7;
-          const uint32_t off = (c >> 3) * 8192u + (uint32_t)(8 * (lane >> 4) + r8) * 128u + (((c & 7) ^ r8) << 4);
+          const uint32_t off = (c >> 3) * 8192u + (uint32_t)(32 * th + 8 * (lane >> 4) + r8) * 128u + (((c & 7) ^ r8) << 4);
           const uint32_t row = smem_addr(st.v[0]) + off, to = smem_addr(S.vw[0]) + off;
           float2 x[8];
 #pragma unroll
           for (int m = 0; m < 4; m += 2) {
             uint32_t r[4];
-            ldmatrix4_t(row + (4 * th + m) * 1024u, r);
+            ldmatrix4_t(row + m * 1024u, r);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               x[2 * m + k] = make_float2(__uint_as_float(r[k] << 16), __uint_as_float(r[k] & 0xffff0000u));
           }
-          if (L == kC) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = mul2(x[k], w[4 * th + k / 2]);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int j = 8 * (4 * th + k / 2) + j0;
-              x[k] = make_float2(j < L ? x[k].x * S.pw[max(L - 1 - j, 0)] : 0.f,
-                                 j + 1 < L ? x[k].y * S.pw[max(L - 2 - j, 0)] : 0.f);
-            }
+          for (int m = 0; m < 4; ++m) {
+            const float2 w = make_float2(wl[32 * th + 8 * m], wl[32 * th + 8 * m + 1]);
+            x[2 * m] = mul2(x[2 * m], w);
+            x[2 * m + 1] = mul2(x[2 * m + 1], w);
           }
 #pragma unroll
           for (int part = 0; part < 2; ++part) {
@@ -468,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t r[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) r[k] = take_bf16(x[2 * m + k]);
-            stmatrix4_t(to + (4 * th + m) * 1024u, r);
+            stmatrix4_t(to + m * 1024u, r);
           }
         }
         umma::fence_proxy_async();
@@ -526,9 +522,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // thread's tokens are 8 m + 2 (lane % 4), + 1
       const int quarter = warp & 3;
       const uint32_t tlane = tmem + ((uint32_t)(32 * quarter) << 16);
-      float2 f[8];
-#pragma unroll
-      for (int m = 0; m < 8; ++m) f[m] = make_float2(S.ps[8 * m + 2 * (lane & 3) + 1], S.ps[8 * m + 2 * (lane & 3) + 2]);
       const auto out = GDN_GV(reinterpret_cast<uint4*>(a.out), a.total * ld / 8);
       // P: rows 16 quarter .. + 15 (G's first 16 lanes of the quarter); a thread's
       // rows are lane / 4, + 8 and its columns 8 m + 2 (lane % 4), + 1
@@ -539,25 +532,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         // G(i)'s commit covers the products before it, O2(i - 2) among them: P's
         // buffer is free
         const uint32_t pt = smem_addr(S.p[i & 1][0]) + prow;
+#pragma unroll 1
+        for (int c = 0; c <= quarter; ++c) {  // 16 columns; those behind lie above the diagonal
+          float g[8];
+          tmem_get_frag(tlane + TM_G + 16 * c, g);
+          const int d0 = pr - pc - 16 * c;  // t - j
+          uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int cols = 0; cols < 2; ++cols) {  // 32 columns
-          if (cols == 1 && quarter < 2) break;  // above the diagonal: zeros since the start
-          float g[16];
-          tmem_get_frag(tlane + TM_G + 32 * cols, g);
-#pragma unroll
-          for (int m = 0; m < 4; m += 2) {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {  // column group m + k / 2, row group k % 2
-              const int d = pr + 8 * (k & 1) - pc - 8 * (4 * cols + m + k / 2), e = 4 * (m + k / 2) + 2 * (k & 1);  // d: t - j
-              float2 x = make_float2(d >= 0 ? g[e] * S.ps[max(d, 0)] : 0.f, d >= 1 ? g[e + 1] * S.ps[max(d - 1, 0)] : 0.f);
-              hi[k] = take_bf16(x);
-              lo[k] = bf16_pair(x);
-            }
-            const uint32_t c = 4 * cols + m + pc8, to = pt + ((c ^ (lane & 7)) << 4);
-            stmatrix4(to, hi);
-            stmatrix4(to + 8192u, lo);
+          for (int k = 0; k < 4; ++k) {  // column group k / 2, row group k % 2
+            const int d = d0 + 8 * (k & 1) - 8 * (k >> 1), e = 4 * (k >> 1) + 2 * (k & 1);
+            float2 x = make_float2(d >= 0 ? g[e] * S.ps[max(d, 0)] : 0.f, d >= 1 ? g[e + 1] * S.ps[max(d - 1, 0)] : 0.f);
+            hi[k] = take_bf16(x);
+            lo[k] = bf16_pair(x);
           }
+          const uint32_t to = pt + (((2 * c + pc8) ^ (lane & 7)) << 4);
+          stmatrix4(to, hi);
+          stmatrix4(to + 8192u, lo);
         }
         umma::fence_proxy_async();
         umma::fence_before();
@@ -569,14 +559,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&S.o2_go);
       }
       if (ok) ok = wait_all(&S.init, 0);  // the state tile has left p
-      if (ok && quarter < 2) {            // columns 32 .. of rows 0 .. 31: zeros, once
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
+      if (ok)  // columns 16 (quarter + 1) .. of its rows: zeros, once
+        for (int c = 2 * quarter + 2; c < 8; ++c)
 #pragma unroll
           for (int b = 0; b < 2; ++b)
-            tile_at<uint4>(S.p[b][lane >> 4], sizeof(S.p[0][0]), umma::sw128_off(16 * quarter + (lane & 15), 32 + 8 * c, 0)) =
+            tile_at<uint4>(S.p[b][lane >> 4], sizeof(S.p[0][0]), umma::sw128_off(16 * quarter + (lane & 15), 8 * c, 0)) =
                 make_uint4(0, 0, 0, 0);
-      }
       if (ok && (ok = wait_all(&S.g_full, 0))) {
         umma::fence_after();
         put_p(0);
@@ -600,34 +588,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
+#pragma unroll 1
+        for (int hc = 0; hc < 4; ++hc) {  // 16 channels x 32 tokens
           // matrices of 8 tokens x 8 channels: lane / 8 = 2 (token group) + channel group
-          const int c = 4 * quarter + 2 * half + (lane >> 3 & 1), r8 = lane & 7;
-          const uint32_t row = smem_addr(ot) + (c >> 3) * 8192u + (uint32_t)(8 * (lane >> 4) + r8) * 128u + (((c & 7) ^ r8) << 4);
+          const int half = hc >> 1, cols = hc & 1, c = 4 * quarter + 2 * half + (lane >> 3 & 1), r8 = lane & 7;
+          const uint32_t row = smem_addr(ot) + (c >> 3) * 8192u + (uint32_t)(32 * cols + 8 * (lane >> 4) + r8) * 128u +
+                               (((c & 7) ^ r8) << 4);
+          float o1[16], o2[16];
+          tmem_get_frag2(tlane + TM_O1 + 32 * cols, tlane + TM_O2 + 32 * cols, half, o1, o2);
+          const float* const f = &S.pt[32 * cols + pc];
 #pragma unroll
-          for (int cols = 0; cols < 2; ++cols) {
-            float o1[16], o2[16];
-            tmem_get_frag2(tlane + TM_O1 + 32 * cols, tlane + TM_O2 + 32 * cols, half, o1, o2);
-            if (half == 1 && cols == 1) {
-              umma::fence_before();
-              __syncwarp();
-              if (lane == 0) {
-                mbar_arrive(&S.o1_go);
-                mbar_arrive(&S.o2_go);
-              }
+          for (int m = 0; m < 4; m += 2) {
+            uint32_t r[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int e = 4 * m + 2 * k;
+              r[k] = bf16_pair(fma2(*reinterpret_cast<const float2*>(f + 8 * (m + k / 2)), make_float2(o1[e], o1[e + 1]),
+                                    make_float2(o2[e], o2[e + 1])));
             }
-#pragma unroll
-            for (int m = 0; m < 4; m += 2) {
-              uint32_t r[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int e = 4 * m + 2 * k;
-                r[k] = bf16_pair(fma2(f[4 * cols + m + k / 2], make_float2(o1[e], o1[e + 1]), make_float2(o2[e], o2[e + 1])));
-              }
-              stmatrix4_t(row + (4 * cols + m) * 1024u, r);
-            }
+            stmatrix4_t(row + m * 1024u, r);
           }
+        }
+        umma::fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&S.o1_go);
+          mbar_arrive(&S.o2_go);
         }
         const int64_t t0 = S.seg.t0 + from(i);
         if (L == kC) {
@@ -742,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
     for (int i = 0; i < nit && ok; ++i) {
       const int L = count(i);
-      const float dec = S.pw[L];
+      const float dec = S.dec[L];
       if (!(ok = wait_all(&S.ds_full, i & 1))) break;
       umma::fence_after();
 #pragma unroll
