@@ -341,16 +341,23 @@ cudaError_t recurrent_dispatch(const PrefillArgs& a, cudaStream_t s) {
   return cudaErrorInvalidValue;
 }
 
-// Blocks per segment; 2^30 where sequences stay whole: enough chains for the
-// SMs, or few blocks.  Else as many segments as fill the SMs, at most kMaxSegs
-// per sequence of the mean length (a segment reads all its predecessors'
-// states), and not below kMinSeg blocks.
-constexpr int64_t kMinSeg = 8, kMaxSegs = 16;
+// Blocks per segment; 2^30 where sequences stay whole.  The lengths are on the
+// device: the rule sees their number and sum.
+//  * Few blocks in all (16, or 24 of several sequences) stay whole.
+//  * Fewer chains than half the SMs: as many segments per sequence as fit on
+//    them in one wave, of the mean length, not below kMinSeg blocks and at most
+//    kMaxSegs of them (a segment reads all its predecessors' states).
+//  * Else, up to kMaxSkew sequences: those longer than twice the mean are cut,
+//    so that a batch does not wait for its longest one.  (Where none is, the
+//    first launch finds nothing to do.)
+constexpr int64_t kMinSeg = 8, kMaxSegs = 16, kMaxSkew = 32;
 int64_t seg_chunks(const gdn_dims& d, int32_t n_seq, int64_t total) {
-  const int64_t chunks = (total + kC - 1) / kC, mean = (chunks + n_seq - 1) / n_seq;
-  if ((int64_t)d.hv * n_seq >= 96 || chunks <= (n_seq > 1 ? 24 : 16)) return 1 << 30;
-  const int64_t fill = (d.hv * chunks + sm_count() - 1) / sm_count();
-  return std::max(std::max(fill + 1, kMinSeg), (mean + kMaxSegs - 1) / kMaxSegs);
+  const int64_t whole = 1 << 30, chunks = (total + kC - 1) / kC, mean = (chunks + n_seq - 1) / n_seq;
+  if (chunks <= (n_seq > 1 ? 24 : 16)) return whole;
+  const int64_t per_seq = sm_count() / d.hv / n_seq;
+  if (per_seq > 1)
+    return std::max(std::max((mean + per_seq) / per_seq, kMinSeg), (mean + kMaxSegs - 1) / kMaxSegs);
+  return n_seq > 1 && n_seq <= kMaxSkew ? 2 * std::max(mean, kMinSeg) : whole;
 }
 int64_t seg_slots(int64_t sc, int32_t n_seq, int64_t total) { return first_slot(total, n_seq) / sc + n_seq; }
 

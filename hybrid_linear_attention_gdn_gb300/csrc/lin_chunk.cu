@@ -28,9 +28,9 @@
 // shared memory take all its bandwidth: two parts of V w therefore go through
 // registers to TMEM, whose 512 columns are all in use.
 //
-// 18 warps by role (of 20): 8 hold S (2 per 32 V channels, 64 dk columns each), 4
-// make P from G and write outputs (one of them issues the copies), 4 scale and
-// split V, and two issue the products: dS and O1, and G and O2.  The tensor core
+// 19 warps by role (of 20): 8 hold S (2 per 32 V channels, 64 dk columns each), 4
+// make P from G and write outputs, 4 scale and split V (all 8 where there are no
+// outputs), one issues the copies and two the products: dS and O1, and G and O2.  The tensor core
 // takes a product about when the one before it is done, so that one issuer's
 // waits for the other warps left it idle a third of the time.
 #include "lin.cuh"
@@ -46,12 +46,12 @@ namespace {
 
 constexpr int kD = 128;  // dk = dv
 constexpr int kStages = 3;
-constexpr int kStateWarps = 8, kOutWarp = 8, kSplitWarp = 12, kIssuer = 16;  // 16: dS, O1; 17: G, O2
+constexpr int kStateWarps = 8, kOutWarp = 8, kSplitWarp = 12, kIssuer = 16, kLoader = 18;  // 16: dS, O1; 17: G, O2
 constexpr int kThreads = 20 * 32;
 constexpr int kStateThreads = kStateWarps * 32;
 // Registers per thread, by warpgroup (state, state, output, split, issuer);
 // 640 x 96 at launch is what there is.
-constexpr int kStateRegs = 136, kOutRegs = 72, kSplitRegs = 72, kRestRegs = 64;
+constexpr int kStateRegs = 136, kOutRegs = 96, kSplitRegs = 64, kRestRegs = 48;
 static_assert(2 * kStateRegs + kOutRegs + kSplitRegs + kRestRegs <= 5 * 96, "the launch's registers");
 
 // TMEM columns.  G (M = 64) is in the first 16 lanes of each warp's 32; S^T and
@@ -145,25 +145,22 @@ __device__ __forceinline__ void tmem_get_frag(uint32_t taddr, float (&v)[8], int
       : "r"(taddr)
       : "memory");
 }
-// 16 lanes x 32 columns of two regions: register 4 m + 2 g + e of a thread is
+// 16 lanes x 64 columns of two regions: register 4 m + 2 g + e of a thread is
 // lane lane / 4 + 8 g, column 8 m + 2 (lane % 4) + e
-__device__ __forceinline__ void tmem_get_frag2(uint32_t ta, uint32_t tb, int half, float (&va)[16], float (&vb)[16],
+__device__ __forceinline__ void tmem_get_frag2(uint32_t ta, uint32_t tb, int half, float (&va)[32], float (&vb)[32],
                                                int line = __builtin_LINE()) {
-  if (!umma::tmem_ok(ta, 32, true, line) || !umma::tmem_ok(tb, 32, true, line)) {
+  if (!umma::tmem_ok(ta, 64, true, line) || !umma::tmem_ok(tb, 64, true, line)) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) va[i] = vb[i] = 0.f;
+    for (int i = 0; i < 32; ++i) va[i] = vb[i] = 0.f;
     return;
   }
   const uint32_t off = (uint32_t)(16 * half) << 16;
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n"
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, "
-      "[%33];\n"
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n"
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n"
       "tcgen05.wait::ld.sync.aligned;\n"
-      : "=f"(va[0]), "=f"(va[1]), "=f"(va[2]), "=f"(va[3]), "=f"(va[4]), "=f"(va[5]), "=f"(va[6]), "=f"(va[7]),
-        "=f"(va[8]), "=f"(va[9]), "=f"(va[10]), "=f"(va[11]), "=f"(va[12]), "=f"(va[13]), "=f"(va[14]), "=f"(va[15]),
-        "=f"(vb[0]), "=f"(vb[1]), "=f"(vb[2]), "=f"(vb[3]), "=f"(vb[4]), "=f"(vb[5]), "=f"(vb[6]), "=f"(vb[7]),
-        "=f"(vb[8]), "=f"(vb[9]), "=f"(vb[10]), "=f"(vb[11]), "=f"(vb[12]), "=f"(vb[13]), "=f"(vb[14]), "=f"(vb[15])
+      : "=f"(va[0]), "=f"(va[1]), "=f"(va[2]), "=f"(va[3]), "=f"(va[4]), "=f"(va[5]), "=f"(va[6]), "=f"(va[7]), "=f"(va[8]), "=f"(va[9]), "=f"(va[10]), "=f"(va[11]), "=f"(va[12]), "=f"(va[13]), "=f"(va[14]), "=f"(va[15]), "=f"(va[16]), "=f"(va[17]), "=f"(va[18]), "=f"(va[19]), "=f"(va[20]), "=f"(va[21]), "=f"(va[22]), "=f"(va[23]), "=f"(va[24]), "=f"(va[25]), "=f"(va[26]), "=f"(va[27]), "=f"(va[28]), "=f"(va[29]), "=f"(va[30]), "=f"(va[31]),
+        "=f"(vb[0]), "=f"(vb[1]), "=f"(vb[2]), "=f"(vb[3]), "=f"(vb[4]), "=f"(vb[5]), "=f"(vb[6]), "=f"(vb[7]), "=f"(vb[8]), "=f"(vb[9]), "=f"(vb[10]), "=f"(vb[11]), "=f"(vb[12]), "=f"(vb[13]), "=f"(vb[14]), "=f"(vb[15]), "=f"(vb[16]), "=f"(vb[17]), "=f"(vb[18]), "=f"(vb[19]), "=f"(vb[20]), "=f"(vb[21]), "=f"(vb[22]), "=f"(vb[23]), "=f"(vb[24]), "=f"(vb[25]), "=f"(vb[26]), "=f"(vb[27]), "=f"(vb[28]), "=f"(vb[29]), "=f"(vb[30]), "=f"(vb[31])
       : "r"(ta + off), "r"(tb + off)
       : "memory");
 }
@@ -224,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&S.full[i], 1);
-      mbar_init(&S.empty[i], 1);
+      mbar_init(&S.empty[i], STATE ? 1 : 4);  // the products; the warps that see them done
     }
     mbar_init(&S.g_full, 1);
     mbar_init(&S.p_full, 4 + 4);
@@ -278,6 +275,95 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nit = (int)((m1 - m0 + head + kC - 1) / kC);
   auto from = [&](int i) { return i ? m0 - head + (int64_t)i * kC : m0; };
   auto count = [&](int i) { return (int)(min(m1, m0 - head + (int64_t)(i + 1) * kC) - from(i)); };
+
+  // V w, split: V channels 32 quarter .. + 31 of the chunks' tokens 32 th0 .. 32 th1 - 1,
+  // transposed on the way to TMEM, by `threads` threads' warps in all.  A
+  // thread's tokens are 8 m + 2 (lane % 4), + 1.
+  auto split = [&](const int th0, const int th1, const int threads) {
+    const int quarter = warp & 3, j0 = 2 * (lane & 3);
+    const uint32_t tlane = tmem + ((uint32_t)(32 * quarter) << 16);
+    bool ok = true;
+    for (int i = 0; i < nit && ok; ++i) {
+      Stage& st = S.st[i % kStages];
+      const int L = count(i);
+      ok = wait_all(&S.full[i % kStages], (i / kStages) & 1);
+      if (L < kC) {
+        if (named_sync_or(2, threads, !ok)) ok = false;
+        if (!ok) break;
+        // rows behind the chunk are others' values: zeros, or a NaN among them
+        // would reach this chunk's products
+#pragma unroll 1
+        for (int e = tid & (threads - 1); e < (kC - L) * 8; e += threads) {
+          const uint32_t at = (uint32_t)(L + e / 8) * 128u + (e % 8) * 16u;
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            tile_at<uint4>(st.v[b], sizeof(st.v[b]), at) = make_uint4(0, 0, 0, 0);
+            tile_at<uint4>(st.qk[b], sizeof(st.qk[b]), 8192 + at) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        umma::fence_proxy_async();
+        named_sync(2, threads);
+      }
+      if (!ok) break;
+      const float* const wl = &S.w[kC - L + j0];  // of tokens j0, ..
+#pragma unroll 1
+      for (int th = th0; th < th1; ++th) {  // 32 tokens
+        // the operand was read by the last chunk's products
+        if (i > 0 && !(ok = wait_all(th ? &S.ds_full : &S.dsa_done, (i - 1) & 1))) break;
+        umma::fence_after();
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          // matrices of 8 tokens x 8 channels: lane / 8 = 2 (token group) + channel group
+          const int c = 4 * quarter + 2 * half + (lane >> 3 & 1);  // 16-byte piece of the 128 channels
+          const int r8 = lane & 7;
+          const uint32_t off = (c >> 3) * 8192u + (uint32_t)(32 * th + 8 * (lane >> 4) + r8) * 128u + (((c & 7) ^ r8) << 4);
+          const uint32_t row = smem_addr(st.v[0]) + off, to = smem_addr(S.vw[0]) + off;
+          float2 x[8];
+#pragma unroll
+          for (int m = 0; m < 4; m += 2) {
+            uint32_t r[4];
+            ldmatrix4_t(row + m * 1024u, r);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              x[2 * m + k] = make_float2(__uint_as_float(r[k] << 16), __uint_as_float(r[k] & 0xffff0000u));
+          }
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const float2 w = make_float2(wl[32 * th + 8 * m], wl[32 * th + 8 * m + 1]);
+            x[2 * m] = mul2(x[2 * m], w);
+            x[2 * m + 1] = mul2(x[2 * m + 1], w);
+          }
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            uint32_t r[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) r[k] = take_bf16(x[k]);
+            tmem_put_frag(tlane + TM_VW + 32 * part + 16 * th, half, r);
+          }
+#pragma unroll
+          for (int m = 0; m < 4; m += 2) {
+            uint32_t r[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) r[k] = take_bf16(x[2 * m + k]);
+            stmatrix4_t(to + m * 1024u, r);
+          }
+        }
+        umma::fence_proxy_async();
+        tmem_wait_st();
+        umma::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(th ? &S.dsb_go : &S.dsa_go);
+      }
+      if (!ok) break;
+      if (!STATE) {
+        // after G(i), so that p_full's phases do not mix: G(i) is issued once
+        // P(i - 1) is there
+        if (!(ok = wait_all(&S.g_full, i & 1))) break;
+        if (lane == 0) mbar_arrive(&S.p_full);
+      }
+    }
+    if (!ok && lane == 0) report(a.err, GDN_DEV_ERR_TIMEOUT);
+  };
 
   if (warp >= kIssuer) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRestRegs));
@@ -387,112 +473,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
-    if (warp == kIssuer || (!STATE && warp == kIssuer + 1)) {
-      if (!ok && lane == 0) report(a.err, GDN_DEV_ERR_TIMEOUT);
-      // the products in flight end before their memory is used otherwise
-      if (lane == 0) umma::commit(&S.drained);
-      __syncwarp();
-      wait_all(&S.drained, 0);
-    }
-  } else if (warp >= kSplitWarp) {
-    // --------------------------------------------------------------- V w, split
-    // V channels 32 quarter .. + 31 of every token, transposed on the way to
-    // TMEM.  A thread's tokens are 8 m + 2 (lane % 4), + 1 (m = 0 .. 7).
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kSplitRegs));
-    const int quarter = warp & 3, j0 = 2 * (lane & 3);
-    const uint32_t tlane = tmem + ((uint32_t)(32 * quarter) << 16);
-    bool ok = true;
-    for (int i = 0; i < nit && ok; ++i) {
-      Stage& st = S.st[i % kStages];
-      const int L = count(i);
-      ok = wait_all(&S.full[i % kStages], (i / kStages) & 1);
-      if (L < kC) {
-        if (named_sync_or(2, 128, !ok)) ok = false;
+    if (warp == kLoader && lane == 0) {
+      // ---------------------------------------------------------------- loader
+      const int64_t kd = (int64_t)a.hk * kD;
+      int n_load = 0;
+      for (; n_load < nit; ++n_load) {
+        // the state tile has passed through the last stage; chunk n_load -
+        // kStages' products are done (and its V split, which dS waited for)
+        if (n_load == kStages - 1) ok = mbar_wait(&S.init, 0);
+        if (n_load >= kStages) ok = mbar_wait(&S.empty[s], s_par ^ 1);
         if (!ok) break;
-        // rows behind the chunk are others' values: zeros, or a NaN among them
-        // would reach this chunk's products
-#pragma unroll 1
-        for (int e = tid - kSplitWarp * 32; e < (kC - L) * 8; e += 128) {
-          const uint32_t at = (uint32_t)(L + e / 8) * 128u + (e % 8) * 16u;
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            tile_at<uint4>(st.v[b], sizeof(st.v[b]), at) = make_uint4(0, 0, 0, 0);
-            tile_at<uint4>(st.qk[b], sizeof(st.qk[b]), 8192 + at) = make_uint4(0, 0, 0, 0);
-          }
-        }
-        umma::fence_proxy_async();
-        named_sync(2, 128);
-      }
-      if (!ok) break;
-      const float* const wl = &S.w[kC - L + j0];  // of tokens j0, ..
-#pragma unroll 1
-      for (int th = 0; th < 2; ++th) {  // 32 tokens
-        // the operand was read by the last chunk's products
-        if (i > 0 && !(ok = wait_all(th ? &S.ds_full : &S.dsa_done, (i - 1) & 1))) break;
-        umma::fence_after();
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          // matrices of 8 tokens x 8 channels: lane / 8 = 2 (token group) + channel group
-          const int c = 4 * quarter + 2 * half + (lane >> 3 & 1);  // 16-byte piece of the 128 channels
-          const int r8 = lane & 7;
-          const uint32_t off = (c >> 3) * 8192u + (uint32_t)(32 * th + 8 * (lane >> 4) + r8) * 128u + (((c & 7) ^ r8) << 4);
-          const uint32_t row = smem_addr(st.v[0]) + off, to = smem_addr(S.vw[0]) + off;
-          float2 x[8];
-#pragma unroll
-          for (int m = 0; m < 4; m += 2) {
-            uint32_t r[4];
-            ldmatrix4_t(row + m * 1024u, r);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              x[2 * m + k] = make_float2(__uint_as_float(r[k] << 16), __uint_as_float(r[k] & 0xffff0000u));
-          }
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const float2 w = make_float2(wl[32 * th + 8 * m], wl[32 * th + 8 * m + 1]);
-            x[2 * m] = mul2(x[2 * m], w);
-            x[2 * m + 1] = mul2(x[2 * m + 1], w);
-          }
-#pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            uint32_t r[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) r[k] = take_bf16(x[k]);
-            tmem_put_frag(tlane + TM_VW + 32 * part + 16 * th, half, r);
-          }
-#pragma unroll
-          for (int m = 0; m < 4; m += 2) {
-            uint32_t r[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) r[k] = take_bf16(x[2 * m + k]);
-            stmatrix4_t(to + m * 1024u, r);
-          }
-        }
-        umma::fence_proxy_async();
-        tmem_wait_st();
-        umma::fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(th ? &S.dsb_go : &S.dsa_go);
-      }
-      if (!ok) break;
-      if (!STATE) {
-        // after G(i), so that p_full's phases do not mix: G(i) is issued once
-        // P(i - 1) is there
-        if (!(ok = wait_all(&S.g_full, i & 1))) break;
-        if (lane == 0) mbar_arrive(&S.p_full);
-      }
-    }
-    if (!ok && lane == 0) report(a.err, GDN_DEV_ERR_TIMEOUT);
-  } else if (warp >= kOutWarp) {
-    // ------------------------------------------------------------------ outputs
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOutRegs));
-    // Warp kOutWarp also issues the copies: chunk i + kStages once chunk i's
-    // products are done (and its V split, which dS waited for).
-    const int64_t kd = (int64_t)a.hk * kD;
-    const bool loader = warp == kOutWarp;
-    int n_load = 0;
-    auto load = [&]() {  // chunk n_load
-      const int s = n_load % kStages;
-      if (lane == 0) {
         Stage& st = S.st[s];
         const int32_t row = (int32_t)(S.seg.t0 + from(n_load));
         mbar_arrive_expect_tx(&S.full[s], (STATE ? 4 : 6) * 8192);
@@ -503,25 +493,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (GDN_SPAN_G(xk, 64, a.C)) tma_load_2d(st.qk[b] + 8192, &xmap, (int32_t)xk, row, &S.full[s]);
           if (GDN_SPAN_G(xv, 64, a.C)) tma_load_2d(st.v[b], &xmap, (int32_t)xv, row, &S.full[s]);
         }
+        next();
       }
-      __syncwarp();
-      ++n_load;
-    };
-    bool ok = true;
-    if (loader) {
-      while (n_load < min(nit, kStages - 1)) load();
-      // the state tile has passed through the last stage
-      if (nit >= kStages && (ok = wait_all(&S.init, 0))) load();
+      if (!ok) report(a.err, GDN_DEV_ERR_TIMEOUT);
+      // what is in flight lands before the memory goes (at once, unless a wait expired)
+      for (int k = max(0, n_load - kStages); k < n_load; ++k) mbar_wait(&S.full[k % kStages], (k / kStages) & 1);
     }
+    __syncwarp();
+    if (warp == kIssuer || (!STATE && warp == kIssuer + 1)) {
+      if (!ok && lane == 0) report(a.err, GDN_DEV_ERR_TIMEOUT);
+      // the products in flight end before their memory is used otherwise
+      if (lane == 0) umma::commit(&S.drained);
+      __syncwarp();
+      wait_all(&S.drained, 0);
+    }
+  } else if (warp >= kSplitWarp) {
+    // --------------------------------------------------------------- V w, split
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kSplitRegs));
+    split(0, STATE ? 1 : 2, STATE ? 256 : 128);
+  } else if (warp >= kOutWarp) {
+    // ------------------------------------------------------------------ outputs
+    static_assert(kOutRegs == 96, "as at launch");
     if (STATE) {
-      if (loader)
-        for (int i = 0; n_load < nit && ok; ++i)
-          if ((ok = wait_all(&S.empty[i % kStages], (i / kStages) & 1))) load();
+      split(1, 2, 256);
     } else {
+      bool ok = true;
       // V channels 32 quarter .. + 31, transposed on the way to shared memory; a
       // thread's tokens are 8 m + 2 (lane % 4), + 1
       const int quarter = warp & 3;
       const uint32_t tlane = tmem + ((uint32_t)(32 * quarter) << 16);
+      const bool storer = warp == kOutWarp;
       const auto out = GDN_GV(reinterpret_cast<uint4*>(a.out), a.total * ld / 8);
       // P: rows 16 quarter .. + 15 (G's first 16 lanes of the quarter); a thread's
       // rows are lane / 4, + 8 and its columns 8 m + 2 (lane % 4), + 1
@@ -580,25 +581,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ok = ok && wait_all(&S.o_full, i & 1);
         umma::fence_after();
-        if (loader && ok) {
-          if (n_load < nit) load();
-          if (lane == 0) bulk_wait_read();  // the last chunk's outputs have left their buffer
+        if (lane == 0 && ok) {
+          mbar_arrive(&S.empty[i % kStages]);
+          if (storer) bulk_wait_read();  // the last chunk's outputs have left their buffer
         }
         if (named_sync_or(3, 128, !ok)) {
           ok = false;
           break;
         }
 #pragma unroll 1
-        for (int hc = 0; hc < 4; ++hc) {  // 16 channels x 32 tokens
+        for (int half = 0; half < 2; ++half) {  // 16 channels
           // matrices of 8 tokens x 8 channels: lane / 8 = 2 (token group) + channel group
-          const int half = hc >> 1, cols = hc & 1, c = 4 * quarter + 2 * half + (lane >> 3 & 1), r8 = lane & 7;
-          const uint32_t row = smem_addr(ot) + (c >> 3) * 8192u + (uint32_t)(32 * cols + 8 * (lane >> 4) + r8) * 128u +
-                               (((c & 7) ^ r8) << 4);
-          float o1[16], o2[16];
-          tmem_get_frag2(tlane + TM_O1 + 32 * cols, tlane + TM_O2 + 32 * cols, half, o1, o2);
-          const float* const f = &S.pt[32 * cols + pc];
+          const int c = 4 * quarter + 2 * half + (lane >> 3 & 1), r8 = lane & 7;
+          const uint32_t row = smem_addr(ot) + (c >> 3) * 8192u + (uint32_t)(8 * (lane >> 4) + r8) * 128u + (((c & 7) ^ r8) << 4);
+          float o1[32], o2[32];
+          tmem_get_frag2(tlane + TM_O1, tlane + TM_O2, half, o1, o2);
+          if (half == 1) {
+            umma::fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&S.o1_go);
+              mbar_arrive(&S.o2_go);
+            }
+          }
+          const float* const f = &S.pt[pc];
 #pragma unroll
-          for (int m = 0; m < 4; m += 2) {
+          for (int m = 0; m < 8; m += 2) {
             uint32_t r[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -609,17 +617,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             stmatrix4_t(row + m * 1024u, r);
           }
         }
-        umma::fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&S.o1_go);
-          mbar_arrive(&S.o2_go);
-        }
         const int64_t t0 = S.seg.t0 + from(i);
         if (L == kC) {
           umma::fence_proxy_async();
           named_sync(3, 128);
-          if (loader && lane == 0) {
+          if (storer && lane == 0) {
 #pragma unroll
             for (int b = 0; b < 2; ++b)
               if (GDN_SPAN_G((int64_t)h * kD + 64 * b, 64, ld) && GDN_SPAN_G(t0, kC, a.total))
@@ -634,15 +636,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tile_at<uint4>(ot, sizeof(S.o), (c >> 3) * 8192u + t * 128u + (((c & 7) ^ (t & 7)) << 4));
           }
         }
-        if (loader && lane == 0) bulk_commit();
+        if (storer && lane == 0) bulk_commit();
         __syncwarp();
       }
-      if (loader && lane == 0) bulk_wait_all();
+      if (storer && lane == 0) bulk_wait_all();
       __syncwarp();
+      if (!ok && lane == 0) report(a.err, GDN_DEV_ERR_TIMEOUT);
     }
-    if (!ok && lane == 0) report(a.err, GDN_DEV_ERR_TIMEOUT);
-    if (loader)  // what is in flight lands before the memory goes (at once, unless a wait expired)
-      for (int k = max(0, n_load - kStages); k < n_load; ++k) wait_all(&S.full[k % kStages], (k / kStages) & 1);
   } else {
     // -------------------------------------------------------------------- state
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kStateRegs));
