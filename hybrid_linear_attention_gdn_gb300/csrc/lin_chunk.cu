@@ -28,8 +28,8 @@
 // shared memory take all its bandwidth: two parts of V w therefore go through
 // registers to TMEM, whose 512 columns are all in use.
 //
-// 19 warps by role (of 20): 8 hold S (2 per 32 V channels, 64 dk columns each), 4
-// make P from G and write outputs, 4 scale and split V (all 8 where there are no
+// 19 warps by role (of 20): 8 hold S (2 per 32 V channels, 64 dk columns each) and
+// make P from G, 4 write outputs, 4 scale and split V (all 8 where there are no
 // outputs), one issues the copies and two the products: dS and O1, and G and O2.  The tensor core
 // takes a product about when the one before it is done, so that one issuer's
 // waits for the other warps left it idle a third of the time.
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.empty[i], STATE ? 1 : 4);  // the products; the warps that see them done
     }
     mbar_init(&S.g_full, 1);
-    mbar_init(&S.p_full, 4 + 4);
+    mbar_init(&S.p_full, kStateWarps + 4);
     mbar_init(&S.dsa_go, 4 + kStateWarps);
     mbar_init(&S.dsb_go, 4);
     mbar_init(&S.dsa_done, 1);
@@ -524,62 +524,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tlane = tmem + ((uint32_t)(32 * quarter) << 16);
       const bool storer = warp == kOutWarp;
       const auto out = GDN_GV(reinterpret_cast<uint4*>(a.out), a.total * ld / 8);
-      // P: rows 16 quarter .. + 15 (G's first 16 lanes of the quarter); a thread's
-      // rows are lane / 4, + 8 and its columns 8 m + 2 (lane % 4), + 1
-      const int pr = 16 * quarter + (lane >> 2), pc = 2 * (lane & 3);
-      // matrices of 8 rows x 8 columns: lane / 8 = 2 (column group) + row group
-      const uint32_t prow = (uint32_t)(16 * quarter + (lane & 15)) * 128u, pc8 = lane >> 4;
-      auto put_p = [&](int i) {
-        // G(i)'s commit covers the products before it, O2(i - 2) among them: P's
-        // buffer is free
-        const uint32_t pt = smem_addr(S.p[i & 1][0]) + prow;
-#pragma unroll 1
-        for (int c = 0; c <= quarter; ++c) {  // 16 columns; those behind lie above the diagonal
-          float g[8];
-          tmem_get_frag(tlane + TM_G + 16 * c, g);
-          const int d0 = pr - pc - 16 * c;  // t - j
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {  // column group k / 2, row group k % 2
-            const int d = d0 + 8 * (k & 1) - 8 * (k >> 1), e = 4 * (k >> 1) + 2 * (k & 1);
-            float2 x = make_float2(d >= 0 ? g[e] * S.ps[max(d, 0)] : 0.f, d >= 1 ? g[e + 1] * S.ps[max(d - 1, 0)] : 0.f);
-            hi[k] = take_bf16(x);
-            lo[k] = bf16_pair(x);
-          }
-          const uint32_t to = pt + (((2 * c + pc8) ^ (lane & 7)) << 4);
-          stmatrix4(to, hi);
-          stmatrix4(to + 8192u, lo);
-        }
-        umma::fence_proxy_async();
-        umma::fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.p_full);
-      };
       if (lane == 0) {  // nothing to read yet
         mbar_arrive(&S.o1_go);
         mbar_arrive(&S.o2_go);
       }
-      if (ok) ok = wait_all(&S.init, 0);  // the state tile has left p
-      if (ok)  // columns 16 (quarter + 1) .. of its rows: zeros, once
-        for (int c = 2 * quarter + 2; c < 8; ++c)
-#pragma unroll
-          for (int b = 0; b < 2; ++b)
-            tile_at<uint4>(S.p[b][lane >> 4], sizeof(S.p[0][0]), umma::sw128_off(16 * quarter + (lane & 15), 8 * c, 0)) =
-                make_uint4(0, 0, 0, 0);
-      if (ok && (ok = wait_all(&S.g_full, 0))) {
-        umma::fence_after();
-        put_p(0);
-      }
       for (int i = 0; i < nit && ok; ++i) {
         const int L = count(i);
         uint8_t* const ot = S.o[0];
-        if (i + 1 < nit) {
-          if ((ok = wait_all(&S.g_full, (i + 1) & 1))) {
-            umma::fence_after();
-            put_p(i + 1);
-          }
-        }
-        ok = ok && wait_all(&S.o_full, i & 1);
+        ok = wait_all(&S.o_full, i & 1);
         umma::fence_after();
         if (lane == 0 && ok) {
           mbar_arrive(&S.empty[i % kStages]);
@@ -604,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mbar_arrive(&S.o2_go);
             }
           }
-          const float* const f = &S.pt[pc];
+          const float* const f = &S.pt[2 * (lane & 3)];
 #pragma unroll
           for (int m = 0; m < 8; m += 2) {
             uint32_t r[4];
@@ -700,6 +652,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         st[2 * e] = lo2(x);
         st[2 * e + 1] = hi2(x);
       }
+      named_sync(1, kStateThreads);
+      if (!STATE && half == 0)  // P above the diagonal blocks: zeros, once
+        for (int c = 2 * (warp & 3) + 2; c < 8; ++c)
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+            tile_at<uint4>(S.p[b][lane >> 4], sizeof(S.p[0][0]), umma::sw128_off(16 * (warp & 3) + (lane & 15), 8 * c, 0)) =
+                make_uint4(0, 0, 0, 0);
       umma::fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.init);
@@ -722,9 +681,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.o1_go);
     };
+          // P: rows 16 quarter .. + 15 (G's first 16 lanes of the quarter); a thread's
+          // rows are lane / 4, + 8 and its columns 8 m + 2 (lane % 4), + 1; the quarter's
+          // two warps take the blocks of 16 columns in turn
+          const int pr = 16 * (warp & 3) + (lane >> 2), pc = 2 * (lane & 3);
+          // matrices of 8 rows x 8 columns: lane / 8 = 2 (column group) + row group
+          const uint32_t prow = (uint32_t)(16 * (warp & 3) + (lane & 15)) * 128u, pc8 = lane >> 4;
+          auto put_p = [&](int i) {
+            // G(i)'s commit covers the products before it, O2(i - 2) among them: P's
+            // buffer is free
+            const uint32_t pt = smem_addr(S.p[i & 1][0]) + prow;
+    #pragma unroll 1
+            for (int c = half; c <= (warp & 3); c += 2) {  // 16 columns; those behind lie above the diagonal
+              float g[8];
+              tmem_get_frag(tlane + TM_G + 16 * c, g);
+              const int d0 = pr - pc - 16 * c;  // t - j
+              uint32_t hi[4], lo[4];
+    #pragma unroll
+              for (int k = 0; k < 4; ++k) {  // column group k / 2, row group k % 2
+                const int d = d0 + 8 * (k & 1) - 8 * (k >> 1), e = 4 * (k >> 1) + 2 * (k & 1);
+                float2 x = make_float2(d >= 0 ? g[e] * S.ps[max(d, 0)] : 0.f, d >= 1 ? g[e + 1] * S.ps[max(d - 1, 0)] : 0.f);
+                hi[k] = take_bf16(x);
+                lo[k] = bf16_pair(x);
+              }
+              const uint32_t to = pt + (((2 * c + pc8) ^ (lane & 7)) << 4);
+              stmatrix4(to, hi);
+              stmatrix4(to + 8192u, lo);
+            }
+            umma::fence_proxy_async();
+            umma::fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.p_full);
+          };
     if (!STATE) put_s();
     if (lane == 0) mbar_arrive(&S.dsa_go);  // no dS to read yet
     bool ok = true;
+    if (!STATE && (ok = wait_all(&S.g_full, 0))) {
+      umma::fence_after();
+      put_p(0);
+    }
 #pragma unroll 1
     for (int i = 0; i < nit && ok; ++i) {
       const int L = count(i);
@@ -744,6 +739,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&S.dsa_go);
       if (!STATE) {
         if (i + 1 < nit) {
+          if (!(ok = wait_all(&S.g_full, (i + 1) & 1))) break;
+          umma::fence_after();
+          put_p(i + 1);
           if (!(ok = wait_all(&S.o_full, i & 1))) break;  // the operand was read
           umma::fence_after();
           put_s();
