@@ -28,7 +28,7 @@
 // shared memory take all its bandwidth: two parts of V w therefore go through
 // registers to TMEM, whose 512 columns are all in use.
 //
-// 19 warps by role (of 20): 8 hold S (2 per 32 V channels, 64 dk columns each) and
+// 27 warps by role (of 28): 16 hold S (4 per 32 V channels, 32 dk columns each) and
 // make P from G, 4 write outputs, 4 scale and split V (all 8 where there are no
 // outputs), one issues the copies and two the products: dS and O1, and G and O2.  The tensor core
 // takes a product about when the one before it is done, so that one issuer's
@@ -46,13 +46,13 @@ namespace {
 
 constexpr int kD = 128;  // dk = dv
 constexpr int kStages = 3;
-constexpr int kStateWarps = 8, kOutWarp = 8, kSplitWarp = 12, kIssuer = 16, kLoader = 18;  // 16: dS, O1; 17: G, O2
-constexpr int kThreads = 20 * 32;
+constexpr int kStateWarps = 16, kOutWarp = 16, kSplitWarp = 20, kIssuer = 24, kLoader = 26;  // 24: dS, O1; 25: G, O2
+constexpr int kThreads = 28 * 32;
 constexpr int kStateThreads = kStateWarps * 32;
-// Registers per thread, by warpgroup (state, state, output, split, issuer);
-// 640 x 96 at launch is what there is.
-constexpr int kStateRegs = 136, kOutRegs = 96, kSplitRegs = 64, kRestRegs = 48;
-static_assert(2 * kStateRegs + kOutRegs + kSplitRegs + kRestRegs <= 5 * 96, "the launch's registers");
+// Registers per thread, by warpgroup (four of state, output, split, issuers);
+// 896 x 72 at launch is what there is.
+constexpr int kLaunchRegs = 72, kStateRegs = 80, kOutRegs = 72, kSplitRegs = 64, kRestRegs = 48;
+static_assert(4 * kStateRegs + kOutRegs + kSplitRegs + kRestRegs <= 7 * kLaunchRegs, "the launch's registers");
 
 // TMEM columns.  G (M = 64) is in the first 16 lanes of each warp's 32; S^T and
 // V w are two parts each.
@@ -68,7 +68,7 @@ struct __align__(1024) ChunkSmem {
   uint8_t p[2][2][64 * 128];    // P [t][j], by the chunk's parity: its two parts
   uint8_t o[2][64 * 128];       // outputs [t][dv], 64-column blocks
   uint8_t vw[2][64 * 128];      // V w's third part [j][dv], 64-column blocks
-  uint8_t ck[kStateWarps][32 * 64];  // a state warp's rows on their way to a checkpoint, 16 columns
+  uint8_t ck[kStateWarps][32 * 32];  // a state warp's rows on their way to a checkpoint, 8 columns
   __align__(16) float w[2 * kC];  // lambda^(63 - j), zeros from 64 on
   float ps[kC];                 // scale lambda^n
   float pt[kC];                 // scale lambda^(n + 1)
@@ -145,22 +145,23 @@ __device__ __forceinline__ void tmem_get_frag(uint32_t taddr, float (&v)[8], int
       : "r"(taddr)
       : "memory");
 }
-// 16 lanes x 64 columns of two regions: register 4 m + 2 g + e of a thread is
+// 16 lanes x 32 columns of two regions: register 4 m + 2 g + e of a thread is
 // lane lane / 4 + 8 g, column 8 m + 2 (lane % 4) + e
-__device__ __forceinline__ void tmem_get_frag2(uint32_t ta, uint32_t tb, int half, float (&va)[32], float (&vb)[32],
+__device__ __forceinline__ void tmem_get_frag2(uint32_t ta, uint32_t tb, int half, float (&va)[16], float (&vb)[16],
                                                int line = __builtin_LINE()) {
-  if (!umma::tmem_ok(ta, 64, true, line) || !umma::tmem_ok(tb, 64, true, line)) {
+  if (!umma::tmem_ok(ta, 32, true, line) || !umma::tmem_ok(tb, 32, true, line)) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) va[i] = vb[i] = 0.f;
+    for (int i = 0; i < 16; ++i) va[i] = vb[i] = 0.f;
     return;
   }
   const uint32_t off = (uint32_t)(16 * half) << 16;
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n"
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, "
+      "[%33];\n"
       "tcgen05.wait::ld.sync.aligned;\n"
-      : "=f"(va[0]), "=f"(va[1]), "=f"(va[2]), "=f"(va[3]), "=f"(va[4]), "=f"(va[5]), "=f"(va[6]), "=f"(va[7]), "=f"(va[8]), "=f"(va[9]), "=f"(va[10]), "=f"(va[11]), "=f"(va[12]), "=f"(va[13]), "=f"(va[14]), "=f"(va[15]), "=f"(va[16]), "=f"(va[17]), "=f"(va[18]), "=f"(va[19]), "=f"(va[20]), "=f"(va[21]), "=f"(va[22]), "=f"(va[23]), "=f"(va[24]), "=f"(va[25]), "=f"(va[26]), "=f"(va[27]), "=f"(va[28]), "=f"(va[29]), "=f"(va[30]), "=f"(va[31]),
-        "=f"(vb[0]), "=f"(vb[1]), "=f"(vb[2]), "=f"(vb[3]), "=f"(vb[4]), "=f"(vb[5]), "=f"(vb[6]), "=f"(vb[7]), "=f"(vb[8]), "=f"(vb[9]), "=f"(vb[10]), "=f"(vb[11]), "=f"(vb[12]), "=f"(vb[13]), "=f"(vb[14]), "=f"(vb[15]), "=f"(vb[16]), "=f"(vb[17]), "=f"(vb[18]), "=f"(vb[19]), "=f"(vb[20]), "=f"(vb[21]), "=f"(vb[22]), "=f"(vb[23]), "=f"(vb[24]), "=f"(vb[25]), "=f"(vb[26]), "=f"(vb[27]), "=f"(vb[28]), "=f"(vb[29]), "=f"(vb[30]), "=f"(vb[31])
+      : "=f"(va[0]), "=f"(va[1]), "=f"(va[2]), "=f"(va[3]), "=f"(va[4]), "=f"(va[5]), "=f"(va[6]), "=f"(va[7]), "=f"(va[8]), "=f"(va[9]), "=f"(va[10]), "=f"(va[11]), "=f"(va[12]), "=f"(va[13]), "=f"(va[14]), "=f"(va[15]),
+        "=f"(vb[0]), "=f"(vb[1]), "=f"(vb[2]), "=f"(vb[3]), "=f"(vb[4]), "=f"(vb[5]), "=f"(vb[6]), "=f"(vb[7]), "=f"(vb[8]), "=f"(vb[9]), "=f"(vb[10]), "=f"(vb[11]), "=f"(vb[12]), "=f"(vb[13]), "=f"(vb[14]), "=f"(vb[15])
       : "r"(ta + off), "r"(tb + off)
       : "memory");
 }
@@ -513,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     split(0, STATE ? 1 : 2, STATE ? 256 : 128);
   } else if (warp >= kOutWarp) {
     // ------------------------------------------------------------------ outputs
-    static_assert(kOutRegs == 96, "as at launch");
+    static_assert(kOutRegs == kLaunchRegs, "as at launch");
     if (STATE) {
       split(1, 2, 256);
     } else {
@@ -542,13 +543,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {  // 16 channels
+        for (int hc = 0; hc < 4; ++hc) {  // 16 channels x 32 tokens
           // matrices of 8 tokens x 8 channels: lane / 8 = 2 (token group) + channel group
-          const int c = 4 * quarter + 2 * half + (lane >> 3 & 1), r8 = lane & 7;
-          const uint32_t row = smem_addr(ot) + (c >> 3) * 8192u + (uint32_t)(8 * (lane >> 4) + r8) * 128u + (((c & 7) ^ r8) << 4);
-          float o1[32], o2[32];
-          tmem_get_frag2(tlane + TM_O1, tlane + TM_O2, half, o1, o2);
-          if (half == 1) {
+          const int half = hc >> 1, cols = hc & 1, c = 4 * quarter + 2 * half + (lane >> 3 & 1), r8 = lane & 7;
+          const uint32_t row = smem_addr(ot) + (c >> 3) * 8192u + (uint32_t)(32 * cols + 8 * (lane >> 4) + r8) * 128u +
+                               (((c & 7) ^ r8) << 4);
+          float o1[16], o2[16];
+          tmem_get_frag2(tlane + TM_O1 + 32 * cols, tlane + TM_O2 + 32 * cols, half, o1, o2);
+          if (hc == 3) {
             umma::fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -556,9 +558,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               mbar_arrive(&S.o2_go);
             }
           }
-          const float* const f = &S.pt[2 * (lane & 3)];
+          const float* const f = &S.pt[32 * cols + 2 * (lane & 3)];
 #pragma unroll
-          for (int m = 0; m < 8; m += 2) {
+          for (int m = 0; m < 4; m += 2) {
             uint32_t r[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -598,127 +600,125 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // -------------------------------------------------------------------- state
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kStateRegs));
-    const int row = 32 * (warp & 3) + lane, half = warp >> 2;  // V channel; dk columns 64 half ..
-    const uint32_t tlane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const int quarter = warp & 3, part = warp >> 2;  // V channels 32 quarter .., dk columns 32 part ..
+    const int row = 32 * quarter + lane;
+    const uint32_t tlane = tmem + ((uint32_t)(32 * quarter) << 16);
     const int64_t slot_n = ld * kD, own = (int64_t)h * kD * kD;
-    const auto pool = GDN_GV(a.ssm, a.num_slots * slot_n);
     const auto segs = GDN_GV(a.seg_state, a.n_segs * slot_n);
     // A tile moves in whole rows (512 bytes per warp access) and through shared
     // memory: piece p of row r at p ^ (r & 7).
     uint8_t* const tile = reinterpret_cast<uint8_t*>(&S.st[kStages - 1]);
     auto piece = [](int r, int p) { return (uint32_t)r * 512u + (uint32_t)((p ^ (r & 7)) << 4); };
-    float2 st[32];
+    float2 st[16];
     {
       const int seg = S.seg.seg, n_seg = S.seg.n_seg;
-      const float dec = power(GDN_GV(a.log_decay, a.hv)[h], (int64_t)a.seg_chunks * kC);
-#pragma unroll 1
-      for (int part = 0; part < 2; ++part) {
-        float4 v[8];  // piece `lane` of rows warp + 64 part, + 8, ..
-        auto place = [&](int j) { return own + ((warp + 8 * j + 64 * part) * 32 + lane) * 4; };
+      float4 v[8];  // piece `lane` of rows warp, warp + 16, ..
+      auto place = [&](int j) { return own + ((warp + 16 * j) * 32 + lane) * 4; };
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (seg == 0) {
-          const bool kept = !STATE && n_seg > 1;
-          const auto src = kept ? GDN_GV((const float*)a.seg_state, a.n_segs * slot_n) + (S.seg.seg0 + n_seg - 1) * slot_n
-                                : GDN_GV((const float*)a.ssm, a.num_slots * slot_n) + S.seg.slot * slot_n;
+      for (int j = 0; j < 8; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (seg == 0) {
+        const bool kept = !STATE && n_seg > 1;
+        const auto src = kept ? GDN_GV((const float*)a.seg_state, a.n_segs * slot_n) + (S.seg.seg0 + n_seg - 1) * slot_n
+                              : GDN_GV((const float*)a.ssm, a.num_slots * slot_n) + S.seg.slot * slot_n;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = vec_at<const float4>(src, place(j));
-          if (STATE) {
-            const auto keep = segs + (S.seg.seg0 + n_seg - 1) * slot_n;
+        for (int j = 0; j < 8; ++j) v[j] = vec_at<const float4>(src, place(j));
+        if (STATE) {
+          const auto keep = segs + (S.seg.seg0 + n_seg - 1) * slot_n;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) vec_at<float4>(keep, place(j)) = v[j];
-          }
-        } else if (!STATE) {
-          for (int k = 0; k < seg; ++k) {
-            const float d = k ? dec : 0.f;  // the first segment's state holds the slot's already
-            const auto from_seg = segs + (S.seg.seg0 + k) * slot_n;
+          for (int j = 0; j < 8; ++j) vec_at<float4>(keep, place(j)) = v[j];
+        }
+      } else if (!STATE) {
+        const float dec = power(GDN_GV(a.log_decay, a.hv)[h], (int64_t)a.seg_chunks * kC);
+        for (int k = 0; k < seg; ++k) {
+          const float d = k ? dec : 0.f;  // the first segment's state holds the slot's already
+          const auto from_seg = segs + (S.seg.seg0 + k) * slot_n;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float4 x = vec_at<const float4>(from_seg, place(j));
-              v[j].x = fmaf(d, v[j].x, x.x);
-              v[j].y = fmaf(d, v[j].y, x.y);
-              v[j].z = fmaf(d, v[j].z, x.z);
-              v[j].w = fmaf(d, v[j].w, x.w);
-            }
+          for (int j = 0; j < 8; ++j) {
+            const float4 x = vec_at<const float4>(from_seg, place(j));
+            v[j].x = fmaf(d, v[j].x, x.x);
+            v[j].y = fmaf(d, v[j].y, x.y);
+            v[j].z = fmaf(d, v[j].z, x.z);
+            v[j].w = fmaf(d, v[j].w, x.w);
           }
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) tile_at<float4>(tile, kTile, piece(warp + 8 * j + 64 * part, lane)) = v[j];
       }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) tile_at<float4>(tile, kTile, piece(warp + 16 * j, lane)) = v[j];
       named_sync(1, kStateThreads);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float4 x = tile_at<float4>(tile, kTile, piece(row, 16 * half + e));
+      for (int e = 0; e < 8; ++e) {
+        const float4 x = tile_at<float4>(tile, kTile, piece(row, 8 * part + e));
         st[2 * e] = lo2(x);
         st[2 * e + 1] = hi2(x);
       }
       named_sync(1, kStateThreads);
-      if (!STATE && half == 0)  // P above the diagonal blocks: zeros, once
-        for (int c = 2 * (warp & 3) + 2; c < 8; ++c)
+      if (!STATE && part == 0)  // P above the diagonal blocks: zeros, once
+        for (int c = 2 * quarter + 2; c < 8; ++c)
 #pragma unroll
           for (int b = 0; b < 2; ++b)
-            tile_at<uint4>(S.p[b][lane >> 4], sizeof(S.p[0][0]), umma::sw128_off(16 * (warp & 3) + (lane & 15), 8 * c, 0)) =
+            tile_at<uint4>(S.p[b][lane >> 4], sizeof(S.p[0][0]), umma::sw128_off(16 * quarter + (lane & 15), 8 * c, 0)) =
                 make_uint4(0, 0, 0, 0);
       umma::fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.init);
     }
     auto put_s = [&]() {  // the O1 operand
+      uint32_t r[16], lo[16];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t hi[16], lo[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float2 x = st[16 * q + e];
-          hi[e] = take_bf16(x);
-          lo[e] = bf16_pair(x);
-        }
-        tmem_put16(tlane + TM_S + 32 * half + 16 * q, hi);
-        tmem_put16(tlane + TM_S + 64 + 32 * half + 16 * q, lo);
+      for (int e = 0; e < 16; ++e) {
+        float2 x = st[e];
+        r[e] = take_bf16(x);
+        lo[e] = bf16_pair(x);
       }
+      tmem_put16(tlane + TM_S + 16 * part, r);
+      tmem_put16(tlane + TM_S + 64 + 16 * part, lo);
       tmem_wait_st();
       umma::fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.o1_go);
     };
-          // P: rows 16 quarter .. + 15 (G's first 16 lanes of the quarter); a thread's
-          // rows are lane / 4, + 8 and its columns 8 m + 2 (lane % 4), + 1; the quarter's
-          // two warps take the blocks of 16 columns in turn
-          const int pr = 16 * (warp & 3) + (lane >> 2), pc = 2 * (lane & 3);
-          // matrices of 8 rows x 8 columns: lane / 8 = 2 (column group) + row group
-          const uint32_t prow = (uint32_t)(16 * (warp & 3) + (lane & 15)) * 128u, pc8 = lane >> 4;
-          auto put_p = [&](int i) {
-            // G(i)'s commit covers the products before it, O2(i - 2) among them: P's
-            // buffer is free
-            const uint32_t pt = smem_addr(S.p[i & 1][0]) + prow;
-    #pragma unroll 1
-            for (int c = half; c <= (warp & 3); c += 2) {  // 16 columns; those behind lie above the diagonal
-              float g[8];
-              tmem_get_frag(tlane + TM_G + 16 * c, g);
-              const int d0 = pr - pc - 16 * c;  // t - j
-              uint32_t hi[4], lo[4];
-    #pragma unroll
-              for (int k = 0; k < 4; ++k) {  // column group k / 2, row group k % 2
-                const int d = d0 + 8 * (k & 1) - 8 * (k >> 1), e = 4 * (k >> 1) + 2 * (k & 1);
-                float2 x = make_float2(d >= 0 ? g[e] * S.ps[max(d, 0)] : 0.f, d >= 1 ? g[e + 1] * S.ps[max(d - 1, 0)] : 0.f);
-                hi[k] = take_bf16(x);
-                lo[k] = bf16_pair(x);
-              }
-              const uint32_t to = pt + (((2 * c + pc8) ^ (lane & 7)) << 4);
-              stmatrix4(to, hi);
-              stmatrix4(to + 8192u, lo);
-            }
-            umma::fence_proxy_async();
-            umma::fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&S.p_full);
-          };
+    // P: rows 16 quarter .. + 15 (G's first 16 lanes of the quarter), of them
+    // the columns 16 part .. + 15, unless they lie above the diagonal; a
+    // thread's rows are lane / 4, + 8 and its columns 8 m + 2 (lane % 4), + 1
+    auto put_p = [&](int i) {
+      if (part <= quarter) {
+        float g[8];
+        umma::fence_after();
+        tmem_get_frag(tlane + TM_G + 16 * part, g);
+        const int d0 = 16 * (quarter - part) + (lane >> 2) - 2 * (lane & 3);  // t - j
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // column group k / 2, row group k % 2
+          const int d = d0 + 8 * (k & 1) - 8 * (k >> 1), e = 4 * (k >> 1) + 2 * (k & 1);
+          float2 x = make_float2(d >= 0 ? g[e] * S.ps[max(d, 0)] : 0.f, d >= 1 ? g[e + 1] * S.ps[max(d - 1, 0)] : 0.f);
+          hi[k] = take_bf16(x);
+          lo[k] = bf16_pair(x);
+        }
+        // matrices of 8 rows x 8 columns: lane / 8 = 2 (column group) + row group.
+        // G(i)'s commit covers the products before it, O2(i - 2) among them: P's
+        // buffer is free
+        const uint32_t to = smem_addr(S.p[i & 1][0]) + (uint32_t)(16 * quarter + (lane & 15)) * 128u +
+                            (((2 * part + (lane >> 4)) ^ (lane & 7)) << 4);
+        stmatrix4(to, hi);
+        stmatrix4(to + 8192u, lo);
+        umma::fence_proxy_async();
+        umma::fence_before();
+        __syncwarp();
+      }
+      if (lane == 0) mbar_arrive(&S.p_full);
+    };
     if (!STATE) put_s();
     if (lane == 0) mbar_arrive(&S.dsa_go);  // no dS to read yet
     bool ok = true;
-    if (!STATE && (ok = wait_all(&S.g_full, 0))) {
-      umma::fence_after();
-      put_p(0);
+    if (!STATE && (ok = wait_all(&S.g_full, 0))) put_p(0);
+    // the chunk that ends at the next block boundary, and the boundary's place
+    const int kpc = a.ckpt_block / kC;
+    int to_ckpt = nit;
+    int64_t ck_idx = 0;
+    if (!STATE && a.max_ckpt > 0) {
+      const int64_t c0 = (S.seg.p0 + m0) / kC;  // the first chunk's absolute number
+      to_ckpt = kpc - 1 - (int)(c0 % kpc);
+      ck_idx = c0 / kpc - S.seg.p0 / a.ckpt_block;
     }
 #pragma unroll 1
     for (int i = 0; i < nit && ok; ++i) {
@@ -727,9 +727,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = wait_all(&S.ds_full, i & 1))) break;
       umma::fence_after();
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < 2; ++q) {
         float d[16];
-        umma::tmem_ld16(tlane + TM_DS + 64 * half + 16 * q, d);
+        umma::tmem_ld16(tlane + TM_DS + 32 * part + 16 * q, d);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           st[8 * q + e] = fma2(st[8 * q + e], make_float2(dec, dec), make_float2(d[2 * e], d[2 * e + 1]));
@@ -740,42 +740,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!STATE) {
         if (i + 1 < nit) {
           if (!(ok = wait_all(&S.g_full, (i + 1) & 1))) break;
-          umma::fence_after();
           put_p(i + 1);
           if (!(ok = wait_all(&S.o_full, i & 1))) break;  // the operand was read
           umma::fence_after();
           put_s();
         }
-        // a block boundary at the chunk's end
-        const int64_t P = S.seg.p0 + from(i) + L;
-        if (a.max_ckpt > 0 && P % a.ckpt_block == 0) {
-          const int64_t idx = P / a.ckpt_block - S.seg.p0 / a.ckpt_block - 1;
-          if (idx < a.max_ckpt) {
-            const int32_t id = GDN_GV(a.ckpt_ids, (long long)a.n_seq * a.max_ckpt)[(int64_t)S.seg.n * a.max_ckpt + idx];
+        // a block boundary at the chunk's end (a sequence that ends inside the
+        // chunk does not reach it)
+        if (i == to_ckpt) {
+          to_ckpt += kpc;
+          const bool whole = i + 1 < nit || (S.seg.p0 + m1) % kC == 0;
+          if (whole && ck_idx < a.max_ckpt) {
+            const int32_t id =
+                GDN_GV(a.ckpt_ids, (long long)a.n_seq * a.max_ckpt)[(int64_t)S.seg.n * a.max_ckpt + ck_idx];
             const int cls = slot_class(id, a.ck_num_slots);
             if (cls == 2 && tid == 0) report(a.err, GDN_DEV_ERR_SLOT_OOB);
             if (cls == 0) {
-              // 16 columns at a time through the warp's 2 KB, so that 64 bytes
-              // of a row leave together (32 bytes from each lane's own row
-              // took 5,000 cycles)
-              const auto to = GDN_GV(a.ck_ssm, a.ck_num_slots * slot_n) + (id * slot_n + own + (row - lane) * kD + 64 * half);
+              // 8 columns at a time through the warp's 1 KB: 32-byte runs of 16
+              // rows per access
+              const auto to = GDN_GV(a.ck_ssm, a.ck_num_slots * slot_n) + (id * slot_n + own + (row - lane) * kD + 32 * part);
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  tile_at<float4>(S.ck[warp], sizeof(S.ck[0]), (uint32_t)lane * 64u + ((e ^ (lane >> 1 & 3)) << 4)) =
-                      join4(st[8 * q + 2 * e], st[8 * q + 2 * e + 1]);
+                for (int e = 0; e < 2; ++e)
+                  tile_at<float4>(S.ck[warp], sizeof(S.ck[0]), (uint32_t)lane * 32u + ((e ^ (lane >> 2 & 1)) << 4)) =
+                      join4(st[4 * q + 2 * e], st[4 * q + 2 * e + 1]);
                 __syncwarp();
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const int r = 8 * j + lane / 4;
-                  vec_at<float4>(to, r * kD + 16 * q + 4 * (lane & 3)) =
-                      tile_at<float4>(S.ck[warp], sizeof(S.ck[0]), (uint32_t)r * 64u + (((lane & 3) ^ (r >> 1 & 3)) << 4));
+                for (int j = 0; j < 2; ++j) {
+                  const int r = 16 * j + lane / 2;
+                  vec_at<float4>(to, r * kD + 8 * q + 4 * (lane & 1)) =
+                      tile_at<float4>(S.ck[warp], sizeof(S.ck[0]), (uint32_t)r * 32u + (((lane & 1) ^ (r >> 2 & 1)) << 4));
                 }
                 __syncwarp();
               }
             }
           }
+          ++ck_idx;
         }
       }
     }
@@ -784,13 +785,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (tid == 0) report(a.err, GDN_DEV_ERR_TIMEOUT);
     } else if (STATE || S.seg.seg == S.seg.n_seg - 1) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        tile_at<float4>(tile, kTile, piece(row, 16 * half + e)) = join4(st[2 * e], st[2 * e + 1]);
+      for (int e = 0; e < 8; ++e)
+        tile_at<float4>(tile, kTile, piece(row, 8 * part + e)) = join4(st[2 * e], st[2 * e + 1]);
       named_sync(1, kStateThreads);
-      const auto to = STATE ? segs + (S.seg.seg0 + S.seg.seg) * slot_n : pool + S.seg.slot * slot_n;
+      const auto to = STATE ? segs + (S.seg.seg0 + S.seg.seg) * slot_n
+                            : GDN_GV(a.ssm, a.num_slots * slot_n) + S.seg.slot * slot_n;
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        vec_at<float4>(to, own + ((warp + 8 * j) * 32 + lane) * 4) = tile_at<float4>(tile, kTile, piece(warp + 8 * j, lane));
+      for (int j = 0; j < 8; ++j)
+        vec_at<float4>(to, own + ((warp + 16 * j) * 32 + lane) * 4) = tile_at<float4>(tile, kTile, piece(warp + 16 * j, lane));
     }
   }
   umma::fence_before();
