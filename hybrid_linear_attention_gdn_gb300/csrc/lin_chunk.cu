@@ -201,9 +201,19 @@ __device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_
                : "memory");
 }
 
-// wait of a whole warp
+// Wait of a whole warp, at most kWaitLimitNs as mbar_wait(), in few
+// instructions: the roles' loops share the instruction caches, and a wait's code
+// is in all of them.
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+  uint32_t t0 = 0;
+  while (!__all_sync(0xffffffffu, mbar_test(bar, parity))) {
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;\n" : "=r"(t));
+    t |= 1;
+    if (t0 == 0) t0 = t;
+    if (__any_sync(0xffffffffu, t - t0 > (uint32_t)kWaitLimitNs)) return false;
+  }
+  return true;
 }
 
 // grid (V heads, segment slots).  STATE: the segment's own state alone (every
