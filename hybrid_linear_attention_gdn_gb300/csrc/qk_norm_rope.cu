@@ -9,6 +9,12 @@
 // map of gdn_batch_maps says where a row's k and v go.
 //
 // HBM bound: each value is read and written once.
+//
+// qk_rope_kernel (head sizes 8 to 256, powers of two): a warp walks heads of one
+// row, whose cosines and sines it holds in registers, four heads' (or groups of
+// small heads') loads in flight.  A lane has 8 values of a head, in two runs of
+// 4 that are each other's partners, so that nothing but the sum of squares goes
+// between lanes.  qk_rope_any_kernel: every other shape, a warp per head.
 #include "ssm.cuh"  // allow_smem
 #include "decode_tma.cuh"  // sm_count
 
@@ -139,6 +145,199 @@ __global__ void __launch_bounds__(kThreads) qk_rope_any_kernel(const RopeArgs a)
   }
 }
 
+// 4 consecutive values
+template <typename T> struct Four;
+template <> struct Four<__nv_bfloat16> {
+  uint2 u;
+  __device__ __forceinline__ void get(float* f) const {
+    f[0] = __uint_as_float(u.x << 16);
+    f[1] = __uint_as_float(u.x & 0xffff0000u);
+    f[2] = __uint_as_float(u.y << 16);
+    f[3] = __uint_as_float(u.y & 0xffff0000u);
+  }
+  __device__ __forceinline__ void set(const float* f) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+    u.x = *reinterpret_cast<const uint32_t*>(&a);
+    u.y = *reinterpret_cast<const uint32_t*>(&b);
+  }
+};
+template <> struct Four<float> {
+  float4 u;
+  __device__ __forceinline__ void get(float* f) const { f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w; }
+  __device__ __forceinline__ void set(const float* f) { u = make_float4(f[0], f[1], f[2], f[3]); }
+};
+
+// grid x: rows x parts of their heads, a warp each.  LPH = d / 8 lanes per head.
+constexpr int kAhead = 4;  // head groups whose loads are in flight
+template <typename T, int LPH, bool INTER>
+__global__ void __launch_bounds__(kThreads) qk_rope_kernel(const RopeArgs a, const int parts) {
+  using F = Four<T>;
+  constexpr int HPW = 32 / LPH, D = 8 * LPH;
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, l = lane % LPH, hsub = lane / LPH;
+  const int64_t wi = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int64_t r = wi / parts;
+  const int part = (int)(wi % parts);
+  if (r >= a.n_rows) return;
+  const RowInfo ri = row_info(a, r, part == 0 && lane == 0);
+  // the lane's two runs of 4 values
+  const int half = a.rot / 2;
+  const bool turns = 8 * l < a.rot;  // (rot is a multiple of 8)
+  const int ea = INTER || !turns ? 8 * l : 4 * l, eb = INTER || !turns ? 8 * l + 4 : half + 4 * l;
+  float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
+  if (turns) {
+    const auto tab = GDN_GV(a.cos_sin, a.max_pos * a.rot) + ri.pos * a.rot;
+    const float4 c4 = vec_at<const float4>(tab, 4 * l), s4 = vec_at<const float4>(tab, half + 4 * l);
+    c[0] = c4.x, c[1] = c4.y, c[2] = c4.z, c[3] = c4.w;
+    s[0] = s4.x, s[1] = s4.y, s[2] = s4.z, s[3] = s4.w;
+  }
+  const int nq = (a.hq + HPW - 1) / HPW, nk = (a.hk + HPW - 1) / HPW;
+  auto walk = [&](const bool isq, const int i0, const int i1) {  // head groups i0, i0 + parts, ..
+    const gdn_rows& in = isq ? a.q : a.k;
+    const gdn_rows& out = isq ? a.q_out : a.k_out;
+    const int nh = isq ? a.hq : a.hk;
+    const float* const wp = isq ? a.q_weight : a.k_weight;
+    const auto src = GDN_GV((const T*)in.data, extent(a.n_rows, in.row, nh, in.head, D)) + r * in.row;
+    const bool to_out = isq || a.k_to_out, to_cache = !isq && ri.slot >= 0;
+    float w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = 1.f;
+    if (wp) {
+      const auto wv = GDN_GV(wp, D);
+      const float4 wa = vec_at<const float4>(wv, ea), wb = vec_at<const float4>(wv, eb);
+      w[0] = wa.x, w[1] = wa.y, w[2] = wa.z, w[3] = wa.w, w[4] = wb.x, w[5] = wb.y, w[6] = wb.z, w[7] = wb.w;
+    }
+    for (int i = i0; i < i1; i += kAhead * parts) {
+      F xa[kAhead], xb[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int h = (i + k * parts) * HPW + hsub;
+        if (i + k * parts < i1 && h < nh) {
+          xa[k] = vec_at<const F>(src, h * in.head + ea);
+          xb[k] = vec_at<const F>(src, h * in.head + eb);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (i + k * parts >= i1) break;  // the whole warp
+        const int h = (i + k * parts) * HPW + hsub;
+        float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (h < nh) {
+          xa[k].get(y);
+          xb[k].get(y + 4);
+        }
+        if (wp) {
+          float ss = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
+#pragma unroll
+          for (int o = LPH / 2; o; o /= 2) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          const float rn = 1.f / sqrtf(ss * (1.f / D) + a.eps);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] *= rn * w[e];
+        }
+        if (turns) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float& u = y[INTER ? 2 * e : e];
+            float& t = y[INTER ? 2 * e + 1 : e + 4];
+            const float p = u * c[e] - t * s[e];
+            t = t * c[e] + u * s[e];
+            u = p;
+          }
+        }
+        if (ri.bad)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = 0.f;
+        if (h < nh) {
+          F oa, ob;
+          oa.set(y);
+          ob.set(y + 4);
+          if (to_out) {
+            const auto dst = GDN_GV((T*)out.data, extent(a.n_rows, out.row, nh, out.head, D)) + (r * out.row + h * out.head);
+            vec_at<F>(dst, ea) = oa;
+            vec_at<F>(dst, eb) = ob;
+          }
+          if (to_cache) {
+            const auto dst = GDN_GV((T*)a.k_cache.data, page_extent(a, a.k_cache, a.hk, D)) + page_off(a, a.k_cache, ri.slot, h);
+            vec_at<F>(dst, ea) = oa;
+            vec_at<F>(dst, eb) = ob;
+          }
+        }
+      }
+    }
+  };
+  // queries first, then keys: group i of both in turn to part i % parts
+  walk(true, part, nq);
+  const int k0 = ((part - nq) % parts + parts) % parts;
+  walk(false, k0, nk);
+  if (a.to_cache && ri.slot >= 0 && a.hv > 0) {  // values: 4 at a time
+    const int n4 = a.dv / 4, n = a.hv * n4;
+    const auto src = GDN_GV((const T*)a.v.data, extent(a.n_rows, a.v.row, a.hv, a.v.head, a.dv)) + r * a.v.row;
+    const auto dst = GDN_GV((T*)a.v_cache.data, page_extent(a, a.v_cache, a.hv, a.dv));
+    for (int e0 = part * 32 + lane; e0 < n; e0 += kAhead * parts * 32) {
+      F x[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int e = e0 + k * parts * 32;
+        if (e < n) x[k] = vec_at<const F>(src, e / n4 * a.v.head + e % n4 * 4);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int e = e0 + k * parts * 32;
+        if (e < n) vec_at<F>(dst, page_off(a, a.v_cache, ri.slot, e / n4) + e % n4 * 4) = x[k];
+      }
+    }
+  }
+}
+
+// whether the vectorised kernel takes these tensors: 4 values are one access everywhere
+bool vec_rows(const gdn_rows& r, int heads, size_t esz) {
+  return heads == 0 || !r.data || (aligned(r.data, 4 * esz) && r.row % 4 == 0 && r.head % 4 == 0);
+}
+bool vec_pages(const gdn_pages& r, int heads, size_t esz) {
+  return heads == 0 || !r.data || (aligned(r.data, 4 * esz) && r.page % 4 == 0 && r.row % 4 == 0 && r.head % 4 == 0);
+}
+bool vec_shape(const RopeArgs& a, size_t esz) {
+  if (a.d < 8 || a.d > 256 || (a.d & (a.d - 1)) || a.rot % 8 || !aligned(a.cos_sin, 16) || !aligned(a.q_weight, 16) ||
+      !aligned(a.k_weight, 16))
+    return false;
+  if (!vec_rows(a.q, a.hq, esz) || !vec_rows(a.q_out, a.hq, esz) || !vec_rows(a.k, a.hk, esz) ||
+      !vec_rows(a.k_out, a.hk, esz))
+    return false;
+  return !a.to_cache || (vec_pages(a.k_cache, a.hk, esz) &&
+                         (a.hv == 0 || (a.dv % 4 == 0 && vec_rows(a.v, a.hv, esz) && vec_pages(a.v_cache, a.hv, esz))));
+}
+
+template <typename T, int LPH>
+cudaError_t rope_vec(const RopeArgs& a, cudaStream_t s) {
+  constexpr int HPW = 32 / LPH;
+  // A row's heads in so many parts that there are 8 warps per SM, each with
+  // kAhead head groups at least.
+  const int64_t groups = (a.hq + HPW - 1) / HPW + (a.hk + HPW - 1) / HPW;
+  const int64_t want = (8LL * sm_count() + a.n_rows - 1) / a.n_rows, most = (groups + kAhead - 1) / kAhead;
+  const int parts = (int)std::max<int64_t>(1, std::min(want, most));
+  const int64_t ctas = (a.n_rows * parts + kThreads / 32 - 1) / (kThreads / 32);
+  if (ctas > 2147483647LL) return cudaErrorInvalidValue;
+  return a.interleaved ? launch_pdl(qk_rope_kernel<T, LPH, true>, dim3((unsigned)ctas), dim3(kThreads), 0, s, dim3(1), a, parts)
+                       : launch_pdl(qk_rope_kernel<T, LPH, false>, dim3((unsigned)ctas), dim3(kThreads), 0, s, dim3(1), a, parts);
+}
+template <typename T>
+cudaError_t rope_any(const RopeArgs& a, cudaStream_t s);
+template <typename T>
+cudaError_t rope_dispatch(const RopeArgs& a, cudaStream_t s) {
+  if (vec_shape(a, sizeof(T))) switch (a.d) {
+      case 8: return rope_vec<T, 1>(a, s);
+      case 16: return rope_vec<T, 2>(a, s);
+      case 32: return rope_vec<T, 4>(a, s);
+      case 64: return rope_vec<T, 8>(a, s);
+      case 128: return rope_vec<T, 16>(a, s);
+      case 256: return rope_vec<T, 32>(a, s);
+    }
+  return rope_any<T>(a, s);
+}
+
 template <typename T>
 cudaError_t rope_any(const RopeArgs& a, cudaStream_t s) {
   const int64_t items = a.n_rows * (a.hq + a.hk + (a.to_cache ? a.hv : 0));
@@ -211,7 +410,7 @@ extern "C" gdn_status gdn_qk_norm_rope(int32_t act_dtype, int32_t hq, int32_t hk
   }
   a.err = dev_err;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = act_dtype == GDN_BF16 ? rope_any<__nv_bfloat16>(a, s) : rope_any<float>(a, s);
+  const cudaError_t e = act_dtype == GDN_BF16 ? rope_dispatch<__nv_bfloat16>(a, s) : rope_dispatch<float>(a, s);
   if (e != cudaSuccess) return GDN_ERR_CUDA;
   count_launch(GDN_K_QK_NORM_ROPE);
   return GDN_OK;
