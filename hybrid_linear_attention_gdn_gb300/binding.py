@@ -809,26 +809,48 @@ def lin_prefill(dims: Dims, pool: StatePool, ckpt: StatePool | None, log_decay, 
     _check(fn, st)
 
 
-def _rows(fn: str, what: str, t, dtype, shape, device: int) -> CRows:
-    """t [rows][heads][width] as gdn_rows: any strides, a head's values consecutive."""
+_NO_ROWS, _NO_PAGES = CRows(None, 0, 0), CPages(None, 0, 0, 0)
+
+
+def _bad_view(fn: str, what: str, t, dtype, shape, why: str):
+    raise GdnError(fn, ERR_INVALID_ARG, f"{what} must be a {dtype} tensor of shape {tuple(shape)} on the current CUDA "
+                                        f"device{why}, got {t.dtype} {tuple(t.shape)}, strides {t.stride()} on {t.device}")
+
+
+def _rows(fn: str, what: str, t, dtype, shape, device: int, out: bool = False) -> CRows:
+    """t [rows][heads][width] as gdn_rows: any strides, a head's values
+    consecutive; an output's rows and heads one behind the other."""
     if t is None:
-        return CRows(None, 0, 0)
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or (t.shape[2] > 1 and t.stride(2) != 1):
-        raise GdnError(fn, ERR_INVALID_ARG, f"{what} must be a {dtype} tensor of shape {tuple(shape)} with consecutive "
-                                            f"head values, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}")
-    if t.get_device() != device:
-        raise GdnError(fn, ERR_INVALID_ARG, f"{what} is on {t.device}, not on the current CUDA device")
-    return CRows(t.data_ptr(), t.stride(0), t.stride(1))
+        return _NO_ROWS
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
+        _bad_view(fn, what, t, dtype, shape, "")
+    row, head, one = t.stride()
+    n, heads, width = shape
+    if (one != 1 and width > 1) or (out and ((head < width and heads > 1) or (row < (heads - 1) * head + width and n > 1))):
+        _bad_view(fn, what, t, dtype, shape, " with consecutive head values" + (" and separate rows" if out else ""))
+    return CRows(t.data_ptr(), row, head)
 
 
-def _overlap(t) -> bool:
-    """Whether different elements of t may share memory."""
+def _separate(sizes, strides) -> bool:
+    """Whether the elements of a tensor of these sizes and strides lie apart."""
     need = 1
-    for size, stride in sorted(((n, s) for n, s in zip(t.shape, t.stride()) if n > 1), key=lambda p: p[1]):
+    for size, stride in sorted(((n, s) for n, s in zip(sizes, strides) if n > 1), key=lambda p: p[1]):
         if stride < need:
-            return True
+            return False
         need = stride * size
-    return False
+    return True
+
+
+def _pages(fn: str, what: str, t, dtype, shape, device: int) -> CPages:
+    """t [pages][block][heads][width] as gdn_pages: any strides, a head's values consecutive."""
+    if t is None:
+        return _NO_PAGES
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
+        _bad_view(fn, what, t, dtype, shape, "")
+    strides = t.stride()
+    if (strides[3] != 1 and shape[3] > 1) or not (t.is_contiguous() or _separate(shape, strides)):
+        _bad_view(fn, what, t, dtype, shape, " with consecutive head values and separate rows")
+    return CPages(t.data_ptr(), *strides[:3])
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float = 1e-6, interleaved: bool = False,
@@ -846,53 +868,42 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float = 1e-6
     if x is None or x.dim() != 3 or x.dtype not in _DT_CODE or (k is not None and k.dim() != 3):
         raise GdnError(fn, ERR_INVALID_ARG, "q and k must be float32 or bfloat16 tensors [rows][heads][d]")
     act, dev, (rows, _, d) = x.dtype, _device(), x.shape
-    hq, hk = (0 if t is None else int(t.shape[1]) for t in (q, k))
-    if cos_sin.dim() != 2:
-        raise GdnError(fn, ERR_INVALID_ARG, f"cos_sin must be of shape (max_pos, rot), got {tuple(cos_sin.shape)}")
+    hq, hk = 0 if q is None else q.shape[1], 0 if k is None else k.shape[1]
     if q_out is None:
         q_out = q
     if k_out is None and slot_map is None:
         k_out = k
-    a = [_rows(fn, "q", q, act, (rows, hq, d), dev), _rows(fn, "k", k, act, (rows, hk, d), dev)]
-    o = [_rows(fn, "q_out", q_out, act, (rows, hq, d), dev), _rows(fn, "k_out", k_out, act, (rows, hk, d), dev)]
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _require(fn, name, w, torch.float32, (d,), dev)
-    _require(fn, "cos_sin", cos_sin, torch.float32, cos_sin.shape, dev)
+    qs, ks = (rows, hq, d), (rows, hk, d)
+    cq, ck = _rows(fn, "q", q, act, qs, dev), _rows(fn, "k", k, act, ks, dev)
+    cqo, cko = _rows(fn, "q_out", q_out, act, qs, dev, True), _rows(fn, "k_out", k_out, act, ks, dev, True)
+    if q_weight is not None:
+        _require(fn, "q_weight", q_weight, torch.float32, (d,), dev)
+    if k_weight is not None:
+        _require(fn, "k_weight", k_weight, torch.float32, (d,), dev)
+    if cos_sin.dim() != 2:
+        raise GdnError(fn, ERR_INVALID_ARG, f"cos_sin must be of shape (max_pos, rot), got {tuple(cos_sin.shape)}")
+    max_pos, rot = cos_sin.shape
+    _require(fn, "cos_sin", cos_sin, torch.float32, (max_pos, rot), dev)
     _require(fn, "positions", positions, torch.int64, (rows,), dev)
-    cv, pages, pages_n, block, hv, dv = CRows(None, 0, 0), [CPages(None, 0, 0, 0)] * 2, 0, 1, 0, 0
+    cv, ckc, cvc, pages, block, hv, dv = _NO_ROWS, _NO_PAGES, _NO_PAGES, 0, 1, 0, 0
     if slot_map is not None:
         _require(fn, "slot_map", slot_map, torch.int64, (rows,), dev)
-        if k is None or k_cache is None or (v is None) != (v_cache is None):
-            raise GdnError(fn, ERR_INVALID_ARG, "a slot_map needs k and k_cache, and v with v_cache")
+        if k is None or k_cache is None or k_cache.dim() != 4 or (v is None) != (v_cache is None):
+            raise GdnError(fn, ERR_INVALID_ARG, "a slot_map needs k and k_cache [pages][block][hk][d], and v with v_cache")
+        pages, block = k_cache.shape[:2]
+        ckc = _pages(fn, "k_cache", k_cache, act, (pages, block, hk, d), dev)
         if v is not None:
             if v.dim() != 3:
                 raise GdnError(fn, ERR_INVALID_ARG, f"v must be of shape (rows, hv, dv), got {tuple(v.shape)}")
-            hv, dv = int(v.shape[1]), int(v.shape[2])
+            _, hv, dv = v.shape
             cv = _rows(fn, "v", v, act, (rows, hv, dv), dev)
-        pages = []
-        for name, t, h, w in (("k_cache", k_cache, hk, d), ("v_cache", v_cache, hv, dv)):
-            if t is None:
-                pages.append(CPages(None, 0, 0, 0))
-                continue
-            want = (k_cache.shape[0], k_cache.shape[1], h, w)
-            if t.dtype != act or t.dim() != 4 or tuple(t.shape) != want or (w > 1 and t.stride(3) != 1) or _overlap(t):
-                raise GdnError(fn, ERR_INVALID_ARG, f"{name} must be a {act} tensor of shape {want} with consecutive "
-                                                    f"head values, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}")
-            if t.get_device() != dev:
-                raise GdnError(fn, ERR_INVALID_ARG, f"{name} is on {t.device}, not on the current CUDA device")
-            pages.append(CPages(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2)))
-        pages_n, block = int(k_cache.shape[0]), int(k_cache.shape[1])
+            cvc = _pages(fn, "v_cache", v_cache, act, (pages, block, hv, dv), dev)
     elif k_cache is not None or v_cache is not None:
         raise GdnError(fn, ERR_INVALID_ARG, "a cache without a slot_map")
-    for name, t in (("q_out", q_out), ("k_out", k_out)):
-        if t is not None and _overlap(t):
-            raise GdnError(fn, ERR_INVALID_ARG, f"{name}'s rows overlap: strides {t.stride()}")
     _require_err(fn, dev_err, dev)
-    st = L.gdn_qk_norm_rope(_DT_CODE[act], hq, hk, int(d), hv, dv, int(rows), a[0], a[1], cv, _ptr(q_weight),
-                            _ptr(k_weight), float(eps), _ptr(cos_sin), int(cos_sin.shape[0]), int(cos_sin.shape[1]),
-                            int(bool(interleaved)), _ptr(positions), o[0], o[1], pages[0], pages[1], pages_n, block,
-                            _ptr(slot_map), _ptr(dev_err), _stream(stream, dev))
+    st = L.gdn_qk_norm_rope(_DT_CODE[act], hq, hk, d, hv, dv, rows, cq, ck, cv, _ptr(q_weight), _ptr(k_weight),
+                            float(eps), _ptr(cos_sin), max_pos, rot, 1 if interleaved else 0, _ptr(positions), cqo, cko,
+                            ckc, cvc, pages, block, _ptr(slot_map), _ptr(dev_err), _stream(stream, dev))
     _check(fn, st)
     return q_out, k_out
 

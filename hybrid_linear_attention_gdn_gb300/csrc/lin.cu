@@ -134,7 +134,7 @@ cudaError_t decode_dispatch(const DecodeArgs& a, int dk, cudaStream_t s) {
   switch (dk) {
     case 16: return decode_launch<16, 4, 1, T>(a, s);
     case 64: return decode_launch<64, 8, 2, T>(a, s);
-    case 128: return decode_launch<128, 16, 4, T>(a, s);
+    case 128: return decode_launch<128, 8, 4, T>(a, s);
   }
   return cudaErrorInvalidValue;
 }

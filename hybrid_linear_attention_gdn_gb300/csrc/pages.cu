@@ -19,10 +19,10 @@ namespace {
 // ---------------------------------------------------------------------------
 // page copy
 // ---------------------------------------------------------------------------
-// A CTA walks the pairs y, y + gridDim.y, ... of one piece of one plane: it
-// reads its pairs' ids 256 at a time, keeps the usable ones, and moves 32 KB
-// per pair with eight 16-byte accesses in flight per thread.
-constexpr int kCopyThreads = 256, kCopyVec = 8;
+// A CTA walks the pairs y, y + gridDim.y, ... of one piece (16 KB) of one plane:
+// it reads its pairs' ids 256 at a time, keeps the usable ones, and moves two
+// pairs' pieces at once with eight 16-byte accesses in flight per thread.
+constexpr int kCopyThreads = 256, kCopyVec = 4, kCopyPairs = 2;
 constexpr int64_t kPiece = (int64_t)kCopyThreads * kCopyVec * 16;
 
 struct CopyArgs {
@@ -60,19 +60,22 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const CopyArgs 
     }
     __syncthreads();
     const int np = n_pair;
-    for (int p = 0; p < np; ++p) {
-      const int64_t src = pair[p].x * a.page_stride, dst = pair[p].y * a.page_stride;
-      uint4 v[kCopyVec];
+    for (int p = 0; p < np; p += kCopyPairs) {
+      uint4 v[kCopyPairs][kCopyVec];
 #pragma unroll
-      for (int i = 0; i < kCopyVec; ++i) {
-        const int64_t off = begin + ((int64_t)i * kCopyThreads + tid) * 16;
-        if (off < end) v[i] = __ldcs(&vec_at<const uint4>(pages, src + off));
-      }
+      for (int k = 0; k < kCopyPairs; ++k)
 #pragma unroll
-      for (int i = 0; i < kCopyVec; ++i) {
-        const int64_t off = begin + ((int64_t)i * kCopyThreads + tid) * 16;
-        if (off < end) __stcs(&vec_at<uint4>(pages, dst + off), v[i]);
-      }
+        for (int i = 0; i < kCopyVec; ++i) {
+          const int64_t off = begin + ((int64_t)i * kCopyThreads + tid) * 16;
+          if (p + k < np && off < end) v[k][i] = __ldcs(&vec_at<const uint4>(pages, pair[p + k].x * a.page_stride + off));
+        }
+#pragma unroll
+      for (int k = 0; k < kCopyPairs; ++k)
+#pragma unroll
+        for (int i = 0; i < kCopyVec; ++i) {
+          const int64_t off = begin + ((int64_t)i * kCopyThreads + tid) * 16;
+          if (p + k < np && off < end) __stcs(&vec_at<uint4>(pages, pair[p + k].y * a.page_stride + off), v[k][i]);
+        }
     }
     __syncthreads();  // pair and n_pair may be replaced
   }
@@ -148,10 +151,7 @@ __device__ __forceinline__ bool load_fork(const ForkArgs& a, int i, Fork& f, uin
 }
 
 // one CTA: the new blocks, in the forks' order, and the pairs to copy
-__global__ void __launch_bounds__(kThreads) fork_alloc_kernel(const ForkArgs a) {
-  __shared__ int warp_sums[32];
-  pdl_wait();
-  pdl_trigger();
+__device__ __forceinline__ void fork_alloc(const ForkArgs& a, int* warp_sums) {
   const int tid = threadIdx.x;
   const int32_t n_free = min(max(*a.n_free, 0), a.free_cap);
   uint32_t bad = 0;
@@ -193,17 +193,15 @@ __global__ void __launch_bounds__(kThreads) fork_alloc_kernel(const ForkArgs a) 
   if (tid == 0) *a.n_free_out = max(n_free - carry, 0);
 }
 
-// a CTA per fork: its row of the table, and one more holder per shared block
-constexpr int kRowThreads = 256;
-__global__ void __launch_bounds__(kRowThreads) fork_rows_kernel(const ForkArgs a) {
-  pdl_wait();
-  pdl_trigger();
+// forks first, first + step, ..: their rows of the table, by `threads` threads of
+// which this is number t, and one more holder per shared block
+__device__ __forceinline__ void fork_rows(const ForkArgs& a, int64_t first, int64_t step, int t, int threads) {
   const auto table = GDN_GV(a.table, (long long)a.n_rows * a.max_blocks);
-  for (int i = blockIdx.x; i < a.n; i += gridDim.x) {
+  for (int64_t i = first; i < a.n; i += step) {
     Fork f;
     uint32_t bad = 0;
-    if (!load_fork(a, i, f, bad)) continue;  // reported by the first launch
-    for (int64_t j = threadIdx.x; j < f.full + f.part; j += kRowThreads) {
+    if (!load_fork(a, (int)i, f, bad)) continue;  // reported by fork_alloc
+    for (int64_t j = t; j < f.full + f.part; j += threads) {
       int32_t id;
       if (j < f.full) {
         id = table[(int64_t)f.src * a.max_blocks + j];
@@ -221,6 +219,35 @@ __global__ void __launch_bounds__(kRowThreads) fork_rows_kernel(const ForkArgs a
     if (bad) report(a.err, bad);
   }
 }
+
+// Small batches: one cluster, a warp per fork.  Larger ones in two launches, the
+// second with a CTA per fork on the whole GPU.
+constexpr int kCluster = 8;
+constexpr int kRowThreads = 256;
+__global__ void __launch_bounds__(kThreads) fork_small_kernel(const ForkArgs a) {
+  __shared__ int warp_sums[32];
+  pdl_wait();
+  pdl_trigger();
+  const int rank = (int)cluster_ctarank();
+  if (rank == 0) fork_alloc(a, warp_sums);
+  cluster_arrive_release();
+  cluster_wait_acquire();  // copy_dst complete
+  fork_rows(a, rank * (kThreads / 32) + (threadIdx.x >> 5), kCluster * (kThreads / 32), threadIdx.x & 31, 32);
+}
+__global__ void __launch_bounds__(kThreads) fork_alloc_kernel(const ForkArgs a) {
+  __shared__ int warp_sums[32];
+  pdl_wait();
+  pdl_trigger();
+  fork_alloc(a, warp_sums);
+}
+__global__ void __launch_bounds__(kRowThreads) fork_rows_kernel(const ForkArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  fork_rows(a, blockIdx.x, gridDim.x, threadIdx.x, kRowThreads);
+}
+// Whether one cluster does a call over n rows of max_blocks entries: up to one
+// entry per thread of it (256 rows of 128 in a graph: fork, copy and release 26 us so, 21 with the GPU).
+bool one_cluster(int64_t n, int64_t max_blocks) { return n * max_blocks <= (int64_t)kCluster * kThreads; }
 
 // ---------------------------------------------------------------------------
 // release
@@ -241,22 +268,20 @@ struct ReleaseArgs {
   uint32_t* err;
 };
 
-// A CTA per request: one holder less for every block behind its new length.
-// A block that nobody holds any more ends at -1 for the second launch.
-__global__ void __launch_bounds__(kRowThreads) release_rows_kernel(const ReleaseArgs a) {
-  pdl_wait();
-  pdl_trigger();
+// Requests first, first + step, ..: one holder less for every block behind a
+// request's new length.  A block that nobody holds any more ends at -1.
+__device__ __forceinline__ void release_rows(const ReleaseArgs& a, int64_t first, int64_t step, int t, int threads) {
   const auto table = GDN_GV(a.table, (long long)a.n_rows * a.max_blocks);
   const auto refs = GDN_GV(a.refs, a.num_blocks);
   const int64_t up = ((int64_t)1 << a.shift) - 1;
-  for (int i = blockIdx.x; i < a.n; i += gridDim.x) {
+  for (int64_t i = first; i < a.n; i += step) {
     const int32_t row = GDN_GV(a.rows, a.n)[i];
     const int cls = slot_class(row, a.n_rows);
     uint32_t bad = cls == 2 ? GDN_DEV_ERR_SLOT_OOB : 0;
     const int64_t from = GDN_GV(a.new_lens, a.n)[i], to = GDN_GV(a.old_lens, a.n)[i];
     if (!cls && (from < 0 || to < from || to > ((int64_t)a.max_blocks << a.shift))) bad |= GDN_DEV_ERR_SEQLENS;
     if (!cls && !bad)
-      for (int64_t j = ((from + up) >> a.shift) + threadIdx.x; j < (to + up) >> a.shift; j += kRowThreads) {
+      for (int64_t j = ((from + up) >> a.shift) + t; j < (to + up) >> a.shift; j += threads) {
         const int64_t at = (int64_t)row * a.max_blocks + j;
         const int32_t id = table[at];
         table[at] = -1;
@@ -266,10 +291,16 @@ __global__ void __launch_bounds__(kRowThreads) release_rows_kernel(const Release
     if (bad) report(a.err, bad);
   }
 }
+__global__ void __launch_bounds__(kRowThreads) release_rows_kernel(const ReleaseArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  release_rows(a, blockIdx.x, gridDim.x, threadIdx.x, kRowThreads);
+}
 
-// One cluster: the blocks at -1, in ascending order, onto the stack.
-constexpr int kCluster = 8;
+// One cluster: the blocks at -1, in ascending order, onto the stack; ROWS: the
+// requests' rows before that, a warp each.
 constexpr int kPer = 4;  // consecutive blocks per thread and pass
+template <bool ROWS>
 __global__ void __launch_bounds__(kThreads) release_push_kernel(const ReleaseArgs a) {
   __shared__ int warp_sums[32];
   __shared__ int counts[kCluster];  // in CTA 0: every CTA's
@@ -282,6 +313,10 @@ __global__ void __launch_bounds__(kThreads) release_push_kernel(const ReleaseArg
   constexpr int kTile = kThreads * kPer;
   const int64_t tiles = ((int64_t)a.num_blocks + kTile - 1) / kTile, per = (tiles + kCluster - 1) / kCluster;
   const int64_t b0 = rank * per * kTile, b1 = min((int64_t)a.num_blocks, b0 + per * kTile);
+  if (ROWS) {
+    release_rows(a, rank * (kThreads / 32) + (tid >> 5), kCluster * (kThreads / 32), tid & 31, 32);
+    cluster.sync();  // the counts are final
+  }
   int mine = 0;
   for (int64_t b = b0 + tid; b < b1; b += kThreads) mine += refs[b] < 0;
   int total;
@@ -344,8 +379,20 @@ struct CompactArgs {
   uint32_t* err;
 };
 
+// the tables' entries, by `step` threads of which this is number `first`
+__device__ __forceinline__ void remap_entries(const CompactArgs& a, int64_t first, int64_t step) {
+  const auto table = GDN_GV(a.table, a.n_entries);
+  const auto out = GDN_GV(a.table_out, a.n_entries);
+  const auto remap = GDN_GV(a.remap, a.num_blocks);
+  for (int64_t i = first; i < a.n_entries; i += step) {
+    const int32_t id = table[i];
+    out[i] = slot_class(id, a.num_blocks) ? id : remap[id];
+  }
+}
+
 // One cluster.  `live` blocks are in use; the k-th highest of those at or
 // above `live` goes to the k-th lowest free one below it.
+template <bool REMAP>
 __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) {
   __shared__ int warp_sums[32];
   __shared__ int counts[2][kCluster];
@@ -463,10 +510,12 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) 
   if (skip) {
     if (a.free_out != a.free_ids)
       for (int64_t i = gt; i < a.free_cap; i += gn) free_out[i] = free_ids[i];
+    if (REMAP) remap_entries(a, gt, gn);  // the identity
     return;
   }
   if (a.free_out != a.free_ids)
     for (int64_t i = n_free + gt; i < a.free_cap; i += gn) free_out[i] = free_ids[i];
+  if (REMAP) remap_entries(a, gt, gn);  // remap has been final since the last barrier
   int nf = 0;
   for (int p = 0; p < passes; ++p) {
     const int64_t w = w0 + p * kThreads + tid;
@@ -488,17 +537,11 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) 
   }
 }
 
-// the tables' entries
+// the tables' entries where they are too many for the cluster
 __global__ void __launch_bounds__(kRowThreads) remap_kernel(const CompactArgs a) {
   pdl_wait();
   pdl_trigger();
-  const auto table = GDN_GV(a.table, a.n_entries);
-  const auto out = GDN_GV(a.table_out, a.n_entries);
-  const auto remap = GDN_GV(a.remap, a.num_blocks);
-  for (int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x; i < a.n_entries; i += (int64_t)gridDim.x * kRowThreads) {
-    const int32_t id = table[i];
-    out[i] = slot_class(id, a.num_blocks) ? id : remap[id];
-  }
+  remap_entries(a, (int64_t)blockIdx.x * kRowThreads + threadIdx.x, (int64_t)gridDim.x * kRowThreads);
 }
 
 int shift_of(int32_t block) {
@@ -546,10 +589,15 @@ extern "C" gdn_status gdn_block_fork(const int32_t* src_rows, const int32_t* dst
   ForkArgs a = {src_rows, dst_rows, lens,     n,        shift_of(block), block_table, n_rows,   max_blocks, refs,
                 num_blocks, free_ids, free_cap, n_free, n_free_out,      copy_src,    copy_dst, dev_err};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_pdl(fork_alloc_kernel, dim3(1), dim3(kThreads), 0, s, dim3(1), a);
-  if (e == cudaSuccess && n > 0)
-    e = launch_pdl(fork_rows_kernel, dim3((unsigned)std::min<int64_t>(n, 8LL * sm_count())), dim3(kRowThreads), 0, s,
-                   dim3(1), a);
+  cudaError_t e;
+  if (one_cluster(n, max_blocks)) {
+    e = launch_pdl(fork_small_kernel, dim3(kCluster), dim3(kThreads), 0, s, dim3(kCluster), a);
+  } else {
+    e = launch_pdl(fork_alloc_kernel, dim3(1), dim3(kThreads), 0, s, dim3(1), a);
+    if (e == cudaSuccess)
+      e = launch_pdl(fork_rows_kernel, dim3((unsigned)std::min<int64_t>(n, 8LL * sm_count())), dim3(kRowThreads), 0, s,
+                     dim3(1), a);
+  }
   if (e != cudaSuccess) return GDN_ERR_CUDA;
   count_launch(GDN_K_BLOCK_FORK);
   return GDN_OK;
@@ -567,11 +615,15 @@ extern "C" gdn_status gdn_block_release(const int32_t* rows, const int64_t* old_
   ReleaseArgs a = {rows, old_lens, new_lens, n, shift_of(block), block_table, n_rows, max_blocks, refs, num_blocks,
                    free_ids, free_cap, n_free, n_free_out, dev_err};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaSuccess;
-  if (n > 0)
+  cudaError_t e;
+  if (one_cluster(n, max_blocks)) {
+    e = launch_pdl(release_push_kernel<true>, dim3(kCluster), dim3(kThreads), 0, s, dim3(kCluster), a);
+  } else {
     e = launch_pdl(release_rows_kernel, dim3((unsigned)std::min<int64_t>(n, 8LL * sm_count())), dim3(kRowThreads), 0, s,
                    dim3(1), a);
-  if (e == cudaSuccess) e = launch_pdl(release_push_kernel, dim3(kCluster), dim3(kThreads), 0, s, dim3(kCluster), a);
+    if (e == cudaSuccess)
+      e = launch_pdl(release_push_kernel<false>, dim3(kCluster), dim3(kThreads), 0, s, dim3(kCluster), a);
+  }
   if (e != cudaSuccess) return GDN_ERR_CUDA;
   count_launch(GDN_K_BLOCK_RELEASE);
   return GDN_OK;
@@ -619,11 +671,14 @@ extern "C" gdn_status gdn_block_compact(const int32_t* block_table, int32_t* tab
   a.wrong = reinterpret_cast<int32_t*>(ws + up16(4LL * num_blocks) + up16(4LL * a.words));
   a.err = dev_err;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_pdl(compact_kernel, dim3(kCluster), dim3(kThreads), 0, s, dim3(kCluster), a);
-  if (e == cudaSuccess && n_entries > 0)
-    e = launch_pdl(remap_kernel,
-                   dim3((unsigned)std::min<int64_t>((n_entries + kRowThreads - 1) / kRowThreads, 4LL * sm_count())),
-                   dim3(kRowThreads), 0, s, dim3(1), a);
+  cudaError_t e;
+  if (one_cluster(1, n_entries)) {
+    e = launch_pdl(compact_kernel<true>, dim3(kCluster), dim3(kThreads), 0, s, dim3(kCluster), a);
+  } else {
+    e = launch_pdl(compact_kernel<false>, dim3(kCluster), dim3(kThreads), 0, s, dim3(kCluster), a);
+    if (e == cudaSuccess)
+      e = launch_pdl(remap_kernel, dim3(4u * (unsigned)sm_count()), dim3(kRowThreads), 0, s, dim3(1), a);
+  }
   if (e != cudaSuccess) return GDN_ERR_CUDA;
   count_launch(GDN_K_BLOCK_COMPACT);
   return GDN_OK;
