@@ -11,8 +11,8 @@
 // HBM bound: each value is read and written once.
 //
 // qk_rope_kernel (head sizes 8 to 256, powers of two): a warp walks heads of one
-// row, whose cosines and sines it holds in registers, four heads' (or groups of
-// small heads') loads in flight.  A lane has 8 values of a head, in two runs of
+// row, whose cosines and sines it holds in registers, four heads' (or
+// groups of small heads') loads in flight.  A lane has 8 values of a head, in two runs of
 // 4 that are each other's partners, so that nothing but the sum of squares goes
 // between lanes.  qk_rope_any_kernel: every other shape, a warp per head.
 #include "ssm.cuh"  // allow_smem
@@ -170,7 +170,7 @@ template <> struct Four<float> {
 // grid x: rows x parts of their heads, a warp each.  LPH = d / 8 lanes per head.
 constexpr int kAhead = 4;  // head groups whose loads are in flight
 template <typename T, int LPH, bool INTER>
-__global__ void __launch_bounds__(kThreads) qk_rope_kernel(const RopeArgs a, const int parts) {
+__global__ void __launch_bounds__(kThreads, 4) qk_rope_kernel(const RopeArgs a, const int parts) {
   using F = Four<T>;
   constexpr int HPW = 32 / LPH, D = 8 * LPH;
   pdl_wait();
@@ -192,14 +192,10 @@ __global__ void __launch_bounds__(kThreads) qk_rope_kernel(const RopeArgs a, con
     c[0] = c4.x, c[1] = c4.y, c[2] = c4.z, c[3] = c4.w;
     s[0] = s4.x, s[1] = s4.y, s[2] = s4.z, s[3] = s4.w;
   }
-  const int nq = (a.hq + HPW - 1) / HPW, nk = (a.hk + HPW - 1) / HPW;
-  auto walk = [&](const bool isq, const int i0, const int i1) {  // head groups i0, i0 + parts, ..
-    const gdn_rows& in = isq ? a.q : a.k;
-    const gdn_rows& out = isq ? a.q_out : a.k_out;
-    const int nh = isq ? a.hq : a.hk;
-    const float* const wp = isq ? a.q_weight : a.k_weight;
-    const auto src = GDN_GV((const T*)in.data, extent(a.n_rows, in.row, nh, in.head, D)) + r * in.row;
-    const bool to_out = isq || a.k_to_out, to_cache = !isq && ri.slot >= 0;
+  // Head groups i0, i0 + parts, .. of nh heads from src to out and cache (which
+  // may be null), all at the row; strides of heads in 32 bits.
+  auto walk = [&](const auto src, const auto out, const auto cache, const bool to_out, const bool to_cache, const int nh,
+                  const int in_head, const int out_head, const int c_head, const float* const wp, const int i0) {
     float w[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[e] = 1.f;
@@ -208,34 +204,39 @@ __global__ void __launch_bounds__(kThreads) qk_rope_kernel(const RopeArgs a, con
       const float4 wa = vec_at<const float4>(wv, ea), wb = vec_at<const float4>(wv, eb);
       w[0] = wa.x, w[1] = wa.y, w[2] = wa.z, w[3] = wa.w, w[4] = wb.x, w[5] = wb.y, w[6] = wb.z, w[7] = wb.w;
     }
-    for (int i = i0; i < i1; i += kAhead * parts) {
+    const int step = HPW * parts;
+    for (int h0 = i0 * HPW + hsub; h0 - hsub < nh; h0 += kAhead * step) {
       F xa[kAhead], xb[kAhead];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int h = (i + k * parts) * HPW + hsub;
-        if (i + k * parts < i1 && h < nh) {
-          xa[k] = vec_at<const F>(src, h * in.head + ea);
-          xb[k] = vec_at<const F>(src, h * in.head + eb);
+      for (int k = 0; k < kAhead; ++k)
+        if (h0 + k * step < nh) {
+          xa[k] = vec_at<const F>(src, (h0 + k * step) * in_head + ea);
+          xb[k] = vec_at<const F>(src, (h0 + k * step) * in_head + eb);
         }
-      }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        if (i + k * parts >= i1) break;  // the whole warp
-        const int h = (i + k * parts) * HPW + hsub;
-        float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (h < nh) {
-          xa[k].get(y);
-          xb[k].get(y + 4);
-        }
+        const int h = h0 + k * step;
+        if (h - hsub >= nh) break;  // the whole warp
+        float y[8];
+        xa[k].get(y);  // (a head beyond the last one: whatever, and not stored)
+        xb[k].get(y + 4);
         if (wp) {
-          float ss = 0.f;
+          float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
+          for (int e = 0; e < 8; e += 2) {
+            const float2 v = make_float2(y[e], y[e + 1]);
+            sq = fma2(v, v, sq);
+          }
+          float ss = sq.x + sq.y;
 #pragma unroll
           for (int o = LPH / 2; o; o /= 2) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          const float rn = 1.f / sqrtf(ss * (1.f / D) + a.eps);
+          const float rn = rsqrtf(ss * (1.f / D) + a.eps);  // 2 units in the last place
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] *= rn * w[e];
+          for (int e = 0; e < 8; e += 2) {
+            const float2 v = mul2(make_float2(y[e], y[e + 1]), mul2(make_float2(w[e], w[e + 1]), make_float2(rn, rn)));
+            y[e] = v.x;
+            y[e + 1] = v.y;
+          }
         }
         if (turns) {
 #pragma unroll
@@ -250,28 +251,38 @@ __global__ void __launch_bounds__(kThreads) qk_rope_kernel(const RopeArgs a, con
         if (ri.bad)
 #pragma unroll
           for (int e = 0; e < 8; ++e) y[e] = 0.f;
-        if (h < nh) {
-          F oa, ob;
-          oa.set(y);
-          ob.set(y + 4);
-          if (to_out) {
-            const auto dst = GDN_GV((T*)out.data, extent(a.n_rows, out.row, nh, out.head, D)) + (r * out.row + h * out.head);
-            vec_at<F>(dst, ea) = oa;
-            vec_at<F>(dst, eb) = ob;
-          }
-          if (to_cache) {
-            const auto dst = GDN_GV((T*)a.k_cache.data, page_extent(a, a.k_cache, a.hk, D)) + page_off(a, a.k_cache, ri.slot, h);
-            vec_at<F>(dst, ea) = oa;
-            vec_at<F>(dst, eb) = ob;
-          }
+        F oa, ob;
+        oa.set(y);
+        ob.set(y + 4);
+        if (to_out && h < nh) {
+          vec_at<F>(out, h * out_head + ea) = oa;
+          vec_at<F>(out, h * out_head + eb) = ob;
+        }
+        if (to_cache && h < nh) {
+          vec_at<F>(cache, h * c_head + ea) = oa;
+          vec_at<F>(cache, h * c_head + eb) = ob;
         }
       }
     }
   };
   // queries first, then keys: group i of both in turn to part i % parts
-  walk(true, part, nq);
-  const int k0 = ((part - nq) % parts + parts) % parts;
-  walk(false, k0, nk);
+  const int nq = (a.hq + HPW - 1) / HPW;
+  {
+    const auto src = GDN_GV((const T*)a.q.data, extent(a.n_rows, a.q.row, a.hq, a.q.head, D)) + (a.hq ? r * a.q.row : 0);
+    const auto out = GDN_GV((T*)a.q_out.data, extent(a.n_rows, a.q_out.row, a.hq, a.q_out.head, D)) +
+                     (a.hq ? r * a.q_out.row : 0);
+    walk(src, out, out, true, false, a.hq, (int)a.q.head, (int)a.q_out.head, 0, a.q_weight, part);
+  }
+  {
+    const bool to_out = a.k_to_out, to_cache = ri.slot >= 0;
+    const auto src = GDN_GV((const T*)a.k.data, extent(a.n_rows, a.k.row, a.hk, a.k.head, D)) + (a.hk ? r * a.k.row : 0);
+    const auto out = GDN_GV((T*)a.k_out.data, to_out ? extent(a.n_rows, a.k_out.row, a.hk, a.k_out.head, D) : 0) +
+                     (to_out && a.hk ? r * a.k_out.row : 0);
+    const auto cache = GDN_GV((T*)a.k_cache.data, to_cache ? page_extent(a, a.k_cache, a.hk, D) : 0) +
+                       (to_cache ? page_off(a, a.k_cache, ri.slot, 0) : 0);
+    walk(src, out, cache, to_out, to_cache, a.hk, (int)a.k.head, (int)a.k_out.head, (int)a.k_cache.head, a.k_weight,
+         ((part - nq) % parts + parts) % parts);
+  }
   if (a.to_cache && ri.slot >= 0 && a.hv > 0) {  // values: 4 at a time
     const int n4 = a.dv / 4, n = a.hv * n4;
     const auto src = GDN_GV((const T*)a.v.data, extent(a.n_rows, a.v.row, a.hv, a.v.head, a.dv)) + r * a.v.row;
@@ -293,11 +304,14 @@ __global__ void __launch_bounds__(kThreads) qk_rope_kernel(const RopeArgs a, con
 }
 
 // whether the vectorised kernel takes these tensors: 4 values are one access everywhere
+// and a head's place in its row is a 32-bit offset
+bool small(int64_t head, int heads) { return head * heads < (1LL << 30); }
 bool vec_rows(const gdn_rows& r, int heads, size_t esz) {
-  return heads == 0 || !r.data || (aligned(r.data, 4 * esz) && r.row % 4 == 0 && r.head % 4 == 0);
+  return heads == 0 || !r.data || (aligned(r.data, 4 * esz) && r.row % 4 == 0 && r.head % 4 == 0 && small(r.head, heads));
 }
 bool vec_pages(const gdn_pages& r, int heads, size_t esz) {
-  return heads == 0 || !r.data || (aligned(r.data, 4 * esz) && r.page % 4 == 0 && r.row % 4 == 0 && r.head % 4 == 0);
+  return heads == 0 || !r.data ||
+         (aligned(r.data, 4 * esz) && r.page % 4 == 0 && r.row % 4 == 0 && r.head % 4 == 0 && small(r.head, heads));
 }
 bool vec_shape(const RopeArgs& a, size_t esz) {
   if (a.d < 8 || a.d > 256 || (a.d & (a.d - 1)) || a.rot % 8 || !aligned(a.cos_sin, 16) || !aligned(a.q_weight, 16) ||
@@ -313,11 +327,13 @@ bool vec_shape(const RopeArgs& a, size_t esz) {
 template <typename T, int LPH>
 cudaError_t rope_vec(const RopeArgs& a, cudaStream_t s) {
   constexpr int HPW = 32 / LPH;
-  // A row's heads in so many parts that there are 8 warps per SM, each with
-  // kAhead head groups at least.
+  // A row's heads in so many parts that there are 8 warps per SM: a warp's
+  // start (position, table, weights) costs as much as several heads, so that
+  // more than one part per row is for few rows only (32768 rows of 32 + 4 heads
+  // 117 us in one part, 148 in two; 64 rows 3 us in 18 parts, 4 in 5).
   const int64_t groups = (a.hq + HPW - 1) / HPW + (a.hk + HPW - 1) / HPW;
-  const int64_t want = (8LL * sm_count() + a.n_rows - 1) / a.n_rows, most = (groups + kAhead - 1) / kAhead;
-  const int parts = (int)std::max<int64_t>(1, std::min(want, most));
+  const int64_t want = (8LL * sm_count() + a.n_rows - 1) / a.n_rows;
+  const int parts = (int)std::max<int64_t>(1, std::min(want, groups));
   const int64_t ctas = (a.n_rows * parts + kThreads / 32 - 1) / (kThreads / 32);
   if (ctas > 2147483647LL) return cudaErrorInvalidValue;
   return a.interleaved ? launch_pdl(qk_rope_kernel<T, LPH, true>, dim3((unsigned)ctas), dim3(kThreads), 0, s, dim3(1), a, parts)
