@@ -142,23 +142,29 @@ cudaError_t decode_dispatch(const DecodeArgs& a, int dk, cudaStream_t s) {
 // ---------------------------------------------------------------------------
 // prefill, one token after another (every shape and type)
 // ---------------------------------------------------------------------------
-// A state row lies across DK / 16 lanes, 16 columns each, in registers; tokens
+// A state row lies across DK / 16 lanes, 16 columns each (in runs of 4, so that
+// the lanes' shared-memory accesses lie side by side), in registers; tokens
 // come through shared memory in windows of up to 16, the next window's inputs
 // requested a window ahead.  A window ends at a checkpoint.
 constexpr int kWin = 16;
 
-template <int DK>
-__host__ __device__ constexpr int rec_min_threads() { return DK == 128 ? 128 : DK == 64 ? 64 : 32; }
+__host__ __device__ constexpr int rec_min_threads(int dk) { return dk == 128 ? 128 : dk == 64 ? 64 : 32; }
+// a thread per 16 columns of a row, a power of two of them, at most 256
+int rec_threads(int dk, int dv) {
+  int n = rec_min_threads(dk);
+  while (n < 256 && n < dv * (dk / 16)) n *= 2;
+  return n;
+}
 
 template <int DK, typename T, bool STATE>
 __global__ void __launch_bounds__(256) lin_recurrent_kernel(const PrefillArgs a) {
   constexpr int LPR = DK / 16;
   // window elements per thread, at most (fewest threads)
-  constexpr int PF = kWin * (2 * DK / rec_min_threads<DK>()) + (kWin + LPR - 1) / LPR;
+  constexpr int QK = kWin * DK / rec_min_threads(DK), VV = kWin / LPR;
   extern __shared__ __align__(16) float smem[];
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, nt = blockDim.x, R = nt / LPR;
+  const int tid = threadIdx.x, nt = blockDim.x, R = nt / LPR, rsh = 31 - __clz(R);  // rows of a CTA: a power of two
   const int h = blockIdx.y;
   Segment s;
   if (!find_segment(a, blockIdx.z, s, tid == 0 && blockIdx.x == 0 && h == 0 && (!STATE))) return;
@@ -175,7 +181,7 @@ __global__ void __launch_bounds__(256) lin_recurrent_kernel(const PrefillArgs a)
   const auto sv = GDN_SV(smem + 2 * kWin * DK, kWin * R), so = GDN_SV(smem + 2 * kWin * DK + kWin * R, kWin * R);
   const auto x = GDN_GV(reinterpret_cast<const T*>(a.qkv), a.total * a.C);
   const int64_t kd = (int64_t)a.hk * DK, hq = h / a.G;
-  const int row = tid / LPR, c0 = tid % LPR * 16;
+  const int row = tid / LPR, c0 = tid % LPR * 4;  // columns c0 + 4 LPR e, .. + 3 (e = 0 .. 3)
   const bool active = row < rows;
   const float ld_h = GDN_GV(a.log_decay, a.hv)[h];
   const Decay dec = decay_of(ld_h);
@@ -190,7 +196,7 @@ __global__ void __launch_bounds__(256) lin_recurrent_kernel(const PrefillArgs a)
     auto load = [&](const auto& from, float keep) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float4 u = vec_at<const float4>(from, own + 4 * e);
+        const float4 u = vec_at<const float4>(from, own + 4 * LPR * e);
         st[4 * e] = fmaf(keep, st[4 * e], u.x);
         st[4 * e + 1] = fmaf(keep, st[4 * e + 1], u.y);
         st[4 * e + 2] = fmaf(keep, st[4 * e + 2], u.z);
@@ -205,7 +211,7 @@ __global__ void __launch_bounds__(256) lin_recurrent_kernel(const PrefillArgs a)
         const auto keep = segs + (s.seg0 + s.n_seg - 1) * slot_n;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          vec_at<float4>(keep, own + 4 * e) = make_float4(st[4 * e], st[4 * e + 1], st[4 * e + 2], st[4 * e + 3]);
+          vec_at<float4>(keep, own + 4 * LPR * e) = make_float4(st[4 * e], st[4 * e + 1], st[4 * e + 2], st[4 * e + 3]);
       }
     } else if (!STATE) {
       // the first segment's state holds the slot's already
@@ -217,36 +223,41 @@ __global__ void __launch_bounds__(256) lin_recurrent_kernel(const PrefillArgs a)
   const int64_t blk = a.ckpt_block;
   int64_t bound = ((s.p0 + s.m0) / blk + 1) * blk - s.p0;  // tokens of the sequence up to it
   auto window = [&](int64_t m, int64_t bnd) { return (int)max((int64_t)0, min((int64_t)kWin, min(s.m1, bnd) - m)); };
-  float pf[PF];
+  // A window's inputs as they are (a conversion beside its load would wait for
+  // it, one load after another): of q and k this thread's column of every
+  // (nt / DK)-th token, of v its row of every LPR-th.
+  const int qc = tid % DK, qt = tid / DK, qstep = nt / DK, vr = tid & (R - 1), vt = tid >> rsh;
+  T pq[QK], pk[QK], pv[VV];
   auto request = [&](int64_t m, int n) {
     const int64_t at = (s.t0 + m) * a.C;
-    const int nq = n * DK, all = 2 * nq + n * rows;
+    const auto xq = x + (at + hq * DK + qc), xv = x + (at + 2 * kd + (int64_t)h * a.dv + r0);
 #pragma unroll
-    for (int j = 0; j < PF; ++j) {
-      const int e = tid + j * nt;
-      if (e < all) {
-        int64_t src;
-        if (e < 2 * nq) {
-          const int f = e < nq ? e : e - nq;
-          src = at + (f / DK) * a.C + (e < nq ? 0 : kd) + hq * DK + f % DK;
-        } else {
-          const int f = e - 2 * nq;
-          src = at + (f / rows) * a.C + 2 * kd + (int64_t)h * a.dv + r0 + f % rows;
-        }
-        pf[j] = to_f32(x[src]);
+    for (int j = 0; j < QK; ++j) {
+      const int t = qt + j * qstep;
+      if (t < n) {
+        if (!STATE) pq[j] = xq[t * a.C];
+        pk[j] = xq[t * a.C + kd];
       }
+    }
+#pragma unroll
+    for (int j = 0; j < VV; ++j) {
+      const int t = vt + j * LPR;
+      if (t < n && vr < rows) pv[j] = xv[t * a.C + vr];
     }
   };
   auto deposit = [&](int n) {
-    const int nq = n * DK, all = 2 * nq + n * rows;
 #pragma unroll
-    for (int j = 0; j < PF; ++j) {
-      const int e = tid + j * nt;
-      if (e < all) {
-        if (e < nq) sq[e] = pf[j];
-        else if (e < 2 * nq) sk[e - nq] = pf[j];
-        else sv[(e - 2 * nq) / rows * R + (e - 2 * nq) % rows] = pf[j];
+    for (int j = 0; j < QK; ++j) {
+      const int t = qt + j * qstep;
+      if (t < n) {
+        if (!STATE) sq[t * DK + qc] = to_f32(pq[j]);
+        sk[t * DK + qc] = to_f32(pk[j]);
       }
+    }
+#pragma unroll
+    for (int j = 0; j < VV; ++j) {
+      const int t = vt + j * LPR;
+      if (t < n) sv[(t << rsh) + vr] = vr < rows ? to_f32(pv[j]) : 0.f;
     }
   };
   int64_t m = s.m0;
@@ -261,17 +272,17 @@ __global__ void __launch_bounds__(256) lin_recurrent_kernel(const PrefillArgs a)
     if (nn > 0) request(m + n, nn);
 #pragma unroll 4
     for (int t = 0; t < n; ++t) {
-      const float v = active ? sv[t * R + row] : 0.f;
+      const float v = sv[(t << rsh) + row];
       float p[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float4 k4 = vec_at<const float4>(sk, t * DK + c0 + 4 * e);
+        const float4 k4 = vec_at<const float4>(sk, t * DK + c0 + 4 * LPR * e);
         st[4 * e] = step(dec, st[4 * e], v, k4.x);
         st[4 * e + 1] = step(dec, st[4 * e + 1], v, k4.y);
         st[4 * e + 2] = step(dec, st[4 * e + 2], v, k4.z);
         st[4 * e + 3] = step(dec, st[4 * e + 3], v, k4.w);
         if (!STATE) {
-          const float4 q4 = vec_at<const float4>(sq, t * DK + c0 + 4 * e);
+          const float4 q4 = vec_at<const float4>(sq, t * DK + c0 + 4 * LPR * e);
           p[0] = fmaf(st[4 * e], q4.x, p[0]);
           p[1] = fmaf(st[4 * e + 1], q4.y, p[1]);
           p[2] = fmaf(st[4 * e + 2], q4.z, p[2]);
@@ -282,13 +293,13 @@ __global__ void __launch_bounds__(256) lin_recurrent_kernel(const PrefillArgs a)
         float o = (p[0] + p[1]) + (p[2] + p[3]);
 #pragma unroll
         for (int w = LPR / 2; w; w /= 2) o += __shfl_xor_sync(0xffffffffu, o, w);
-        if (active && tid % LPR == 0) so[t * R + row] = o * a.scale;
+        if (active && tid % LPR == 0) so[(t << rsh) + row] = o * a.scale;
       }
     }
     auto store = [&](const auto& to) {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        vec_at<float4>(to, own + 4 * e) = make_float4(st[4 * e], st[4 * e + 1], st[4 * e + 2], st[4 * e + 3]);
+        vec_at<float4>(to, own + 4 * LPR * e) = make_float4(st[4 * e], st[4 * e + 1], st[4 * e + 2], st[4 * e + 3]);
     };
     if (!STATE && at_bound && active) {
       const int64_t idx = bound + s.p0;  // the boundary's position
@@ -302,8 +313,9 @@ __global__ void __launch_bounds__(256) lin_recurrent_kernel(const PrefillArgs a)
     }
     __syncthreads();  // so complete; q, k, v may be replaced
     if (!STATE)
-      for (int e = tid; e < n * rows; e += nt)
-        out[(s.t0 + m + e / rows) * ld + (int64_t)h * a.dv + r0 + e % rows] = from_f32<T>(so[e / rows * R + e % rows]);
+      for (int e = tid; e < n << rsh; e += nt)
+        if ((e & (R - 1)) < rows)
+          out[(s.t0 + m + (e >> rsh)) * ld + (int64_t)h * a.dv + r0 + (e & (R - 1))] = from_f32<T>(so[e]);
     m += n;
     n = nn;
     bound = mb;
@@ -320,8 +332,7 @@ __global__ void __launch_bounds__(256) lin_recurrent_kernel(const PrefillArgs a)
 template <int DK, typename T>
 cudaError_t recurrent_launch(const PrefillArgs& a, cudaStream_t s) {
   constexpr int LPR = DK / 16;
-  const int nt = std::max(rec_min_threads<DK>(), std::min(256, (a.dv * LPR + 31) / 32 * 32));
-  const int R = nt / LPR;
+  const int nt = rec_threads(DK, a.dv), R = nt / LPR;
   const size_t smem = sizeof(float) * (2 * kWin * DK + 2 * kWin * (size_t)R);
   const dim3 grid((a.dv + R - 1) / R, a.hv, a.n_segs);
   if (a.seg_state) {
@@ -343,6 +354,7 @@ cudaError_t recurrent_dispatch(const PrefillArgs& a, cudaStream_t s) {
 
 // Blocks per segment; 2^30 where sequences stay whole.  The lengths are on the
 // device: the rule sees their number and sum.
+// Chunk form, one CTA per head and segment on an SM:
 //  * Few blocks in all (16, or 24 of several sequences) stay whole.
 //  * Fewer chains than half the SMs: as many segments per sequence as fit on
 //    them in one wave, of the mean length, not below kMinSeg blocks and at most
@@ -350,14 +362,26 @@ cudaError_t recurrent_dispatch(const PrefillArgs& a, cudaStream_t s) {
 //  * Else, up to kMaxSkew sequences: those longer than twice the mean are cut,
 //    so that a batch does not wait for its longest one.  (Where none is, the
 //    first launch finds nothing to do.)
-constexpr int64_t kMinSeg = 8, kMaxSegs = 16, kMaxSkew = 32;
-int64_t seg_chunks(const gdn_dims& d, int32_t n_seq, int64_t total) {
-  const int64_t whole = 1 << 30, chunks = (total + kC - 1) / kC, mean = (chunks + n_seq - 1) / n_seq;
-  if (chunks <= (n_seq > 1 ? 24 : 16)) return whole;
+// Recurrence, a block in some 4 us: segments of 2 blocks or more until there
+// are 4 CTAs per SM.
+constexpr int64_t kWhole = 1 << 30, kMinSeg = 8, kMaxSegs = 16, kMaxSkew = 32, kMinRecSeg = 2;
+int64_t chunk_seg(const gdn_dims& d, int32_t n_seq, int64_t total) {
+  const int64_t chunks = (total + kC - 1) / kC, mean = (chunks + n_seq - 1) / n_seq;
+  if (chunks <= (n_seq > 1 ? 24 : 16)) return kWhole;
   const int64_t per_seq = sm_count() / d.hv / n_seq;
   if (per_seq > 1)
     return std::max(std::max((mean + per_seq) / per_seq, kMinSeg), (mean + kMaxSegs - 1) / kMaxSegs);
-  return n_seq > 1 && n_seq <= kMaxSkew ? 2 * std::max(mean, kMinSeg) : whole;
+  return n_seq > 1 && n_seq <= kMaxSkew ? 2 * std::max(mean, kMinSeg) : kWhole;
+}
+int64_t rec_seg(const gdn_dims& d, int32_t n_seq, int64_t total) {
+  const int64_t chunks = (total + kC - 1) / kC, mean = (chunks + n_seq - 1) / n_seq;
+  const int64_t rows = rec_threads(d.dk, d.dv) / (d.dk / 16), ctas = d.hv * ((d.dv + rows - 1) / rows);
+  const int64_t per_seq = std::min<int64_t>(4LL * sm_count() / ctas / n_seq, kMaxSegs);
+  if (per_seq <= 1 || mean <= kMinRecSeg) return kWhole;
+  return std::max((mean + per_seq) / per_seq, kMinRecSeg);
+}
+int64_t seg_chunks(const gdn_dims& d, int32_t n_seq, int64_t total, bool chunked) {
+  return chunked ? chunk_seg(d, n_seq, total) : rec_seg(d, n_seq, total);
 }
 int64_t seg_slots(int64_t sc, int32_t n_seq, int64_t total) { return first_slot(total, n_seq) / sc + n_seq; }
 
@@ -410,9 +434,14 @@ extern "C" gdn_status gdn_lin_decode_step(const gdn_dims* dims, gdn_pool pool, c
 extern "C" size_t gdn_lin_prefill_workspace_size(const gdn_dims* dims, int32_t n_seq, int64_t total_tokens) {
   using namespace gdn;
   if (check_lin(dims) != GDN_OK || n_seq <= 0 || total_tokens <= 0) return 0;
-  const int64_t sc = seg_chunks(*dims, n_seq, total_tokens);
-  if (sc >= lin::first_slot(total_tokens, n_seq)) return 0;
-  return (size_t)seg_slots(sc, n_seq, total_tokens) * ssm_slot_bytes(*dims);
+  // (which form runs depends on the tensors' alignment, too)
+  size_t most = 0;
+  for (int chunked = 0; chunked <= (lin::chunk_shape(*dims) ? 1 : 0); ++chunked) {
+    const int64_t sc = seg_chunks(*dims, n_seq, total_tokens, chunked);
+    if (sc < lin::first_slot(total_tokens, n_seq))
+      most = std::max(most, (size_t)seg_slots(sc, n_seq, total_tokens) * ssm_slot_bytes(*dims));
+  }
+  return most;
 }
 
 extern "C" gdn_status gdn_lin_prefill(const gdn_dims* dims, gdn_pool pool, gdn_pool ckpt, const float* log_decay,
@@ -458,19 +487,18 @@ extern "C" gdn_status gdn_lin_prefill(const gdn_dims* dims, gdn_pool pool, gdn_p
   a.dv = dims->dv;
   a.G = dims->hv / dims->hk;
   a.C = channels(*dims);
-  const int64_t sc = seg_chunks(*dims, n_seq, total_tokens), segs = seg_slots(sc, n_seq, total_tokens);
+  // GDN_LIN_PREFILL_PATH=recurrent (read on every call) forces the recurrence
+  const char* path = std::getenv("GDN_LIN_PREFILL_PATH");
+  const bool chunked = lin::chunk_supported(*dims, total_tokens, qkv, out) && !(path && !std::strcmp(path, "recurrent"));
+  const int64_t sc = seg_chunks(*dims, n_seq, total_tokens, chunked), segs = seg_slots(sc, n_seq, total_tokens);
   if (segs > 65535) return GDN_ERR_UNSUPPORTED;
   a.seg_chunks = (int32_t)sc;
   a.n_segs = (int32_t)segs;
-  a.seg_state = need > 0 ? reinterpret_cast<float*>(workspace) : nullptr;
+  a.seg_state = sc < lin::first_slot(total_tokens, n_seq) ? reinterpret_cast<float*>(workspace) : nullptr;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  // GDN_LIN_PREFILL_PATH=recurrent (read on every call) forces the recurrence
-  const char* path = std::getenv("GDN_LIN_PREFILL_PATH");
-  if (lin::chunk_supported(*dims, total_tokens, qkv, out) && !(path && !std::strcmp(path, "recurrent")))
-    e = lin::chunk_launch(a, s);
-  else
-    e = dims->act_dtype == GDN_BF16 ? recurrent_dispatch<__nv_bfloat16>(a, s) : recurrent_dispatch<float>(a, s);
+  const cudaError_t e = chunked                          ? lin::chunk_launch(a, s)
+                        : dims->act_dtype == GDN_BF16 ? recurrent_dispatch<__nv_bfloat16>(a, s)
+                                                      : recurrent_dispatch<float>(a, s);
   if (e != cudaSuccess) return GDN_ERR_CUDA;
   count_launch(GDN_K_LIN_PREFILL);
   return GDN_OK;
