@@ -276,7 +276,7 @@ extern "C" gdn_status gdn_gated_rmsnorm(const gdn_dims* dims, const void* o, con
                                         const float* weight, float eps, int64_t n_tokens, void* y,
                                         void* stream) {
   using namespace gdn;
-  const gdn_status st = check_dims(dims);
+  const gdn_status st = check_dims_state(dims);
   if (st != GDN_OK) return st;
   if (n_tokens < 0 || !(eps >= 0.f)) return GDN_ERR_INVALID_ARG;
   if (n_tokens == 0) return GDN_OK;

@@ -76,7 +76,8 @@ typedef struct {
   int32_t dk;         /* key/query head dim: 16, 64 or 128          */
   int32_t dv;         /* value head dim: 1..256                     */
   int32_t conv_width; /* conv1d width W: 2..8; 1: no conv history
-                         (gdn_lin_*, slot and record calls only)    */
+                         (gdn_lin_*, gdn_gated_rmsnorm, slot and
+                         record calls only)                         */
   int32_t act_dtype;  /* GDN_F32 or GDN_BF16: qkv, a, b and outputs */
   int32_t conv_dtype; /* GDN_F32 or GDN_BF16: the conv history      */
 } gdn_dims;
@@ -555,8 +556,8 @@ gdn_status gdn_batch_maps(const int32_t* new_lens, const int64_t* start_pos, int
  *   S <- lambda S + k v^T;  o = scale S^T q  (updated S);  lambda = exp(log_decay)
  * There is no conv, gate or normalisation: dims->conv_width is 1 and the
  * pools hold no conv history (pool.conv may be NULL).  gdn_slot_copy,
- * gdn_slot_zero, gdn_spec_commit, gdn_state_pack and gdn_state_unpack take
- * such dims and pools as well.
+ * gdn_slot_zero, gdn_spec_commit, gdn_state_pack, gdn_state_unpack and
+ * gdn_gated_rmsnorm take such dims and pools as well.
  *   log_decay [hv] float: natural logarithm of each head's decay, <= 0
  *   (-INFINITY: nothing is kept from one token to the next)
  *
