@@ -45,7 +45,6 @@ namespace lin {
 namespace {
 
 constexpr int kD = 128;  // dk = dv
-constexpr int kStages = 3;
 constexpr int kStateWarps = 16, kOutWarp = 16, kSplitWarp = 20, kIssuer = 24, kLoader = 26;  // 24: dS, O1; 25: G, O2
 constexpr int kThreads = 28 * 32;
 constexpr int kStateThreads = kStateWarps * 32;
@@ -58,13 +57,18 @@ static_assert(4 * kStateRegs + kOutRegs + kSplitRegs + kRestRegs <= 7 * kLaunchR
 // V w are two parts each.
 constexpr uint32_t TM_G = 0, TM_DS = 64, TM_O1 = 192, TM_O2 = 256, TM_S = 320, TM_VW = 448, TM_COLS = 512;
 
-// 64-column blocks of 128-byte rows, 16-byte piece c of row r at c ^ (r & 7)
-struct __align__(1024) Stage {
-  uint8_t qk[2][128 * 128];  // rows 0..63 q, 64..127 k
-  uint8_t v[2][64 * 128];
+// Stages of a chunk's inputs, 64-column blocks of 128-byte rows (16-byte piece c
+// of row r at c ^ (r & 7)): blocks of q and k rows, then v's; without q smaller
+// and more of them: the state pass takes 1,200 cycles a chunk and a copy some
+// 2,400, so that three stages had it wait for the copies (1,800).
+template <bool STATE>
+struct Stages {
+  static constexpr int N = STATE ? 5 : 3;
+  static constexpr uint32_t K = STATE ? 0 : 8192, BLOCK = 8192 + K, V = 2 * BLOCK, BYTES = V + 2 * 8192;
+  static constexpr int BEFORE_TILE = STATE ? 3 : 2;  // that the state tile leaves free
 };
 struct __align__(1024) ChunkSmem {
-  Stage st[kStages];
+  uint8_t st[Stages<false>::N * Stages<false>::BYTES];
   uint8_t p[2][2][64 * 128];    // P [t][j], by the chunk's parity: its two parts
   uint8_t o[2][64 * 128];       // outputs [t][dv], 64-column blocks
   uint8_t vw[2][64 * 128];      // V w's third part [j][dv], 64-column blocks
@@ -75,19 +79,22 @@ struct __align__(1024) ChunkSmem {
   float dec[kC + 1];            // lambda^n
   Segment seg;
   int some;
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[Stages<true>::N], empty[Stages<true>::N];
   // dsa_go: V w of the chunk's first 32 tokens is there, the last dS has been
   // read; dsb_go: that of its last 32; dsa_done: the former's products are done;
   // o1_go: S is there, the last outputs have been read; o2_go: the latter
-  uint64_t g_full, p_full, dsa_go, dsb_go, dsa_done, ds_full, o1_go, o2_go, o_full, init, drained;
+  uint64_t dsa_go[2], dsb_go[2], dsa_done[2], ds_full[2];  // by buffer of V w and dS
+  uint64_t g_full, p_full, o1_go, o2_go, o_full, init, drained;
   uint32_t tmem_base;
 };
 // The state tile's way between global memory and the threads' rows: 64 KB from
-// the last stage on, free before chunk kStages - 1 is loaded and P first
-// written, and after the last product (which no output has left by then).
-constexpr unsigned kTile = kD * kD * 4;
+// kTileAt on, free before the first stage there is loaded and P first written,
+// and after the last product (which no output has left by then).
+constexpr unsigned kTile = kD * kD * 4, kTileAt = 2 * Stages<false>::BYTES;
+static_assert(kTileAt == Stages<true>::BEFORE_TILE * Stages<true>::BYTES, "of whole stages");
+static_assert(Stages<true>::N * Stages<true>::BYTES <= offsetof(ChunkSmem, o), "stages without q: P's place, too");
 static_assert(sizeof(ChunkSmem) + 1024 <= 232448, "shared memory of a CTA");
-static_assert(offsetof(ChunkSmem, vw) - offsetof(ChunkSmem, st) - (kStages - 1) * sizeof(Stage) >= kTile, "state tile");
+static_assert(kTileAt + kTile <= offsetof(ChunkSmem, vw), "state tile");
 
 // The leading 8 bits of both values as bf16, packed in pairs; x: what is left
 // of it, exactly.  Three parts hold all of an fp32 value's 24 bits.
@@ -230,21 +237,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) umma::tmem_alloc(&S.tmem_base, TM_COLS);
   if (tid == 64) {
 #pragma unroll
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < Stages<STATE>::N; ++i) {
       mbar_init(&S.full[i], 1);
       mbar_init(&S.empty[i], STATE ? 1 : 4);  // the products; the warps that see them done
     }
     mbar_init(&S.g_full, 1);
     mbar_init(&S.p_full, kStateWarps + 4);
-    mbar_init(&S.dsa_go, 4 + kStateWarps);
-    mbar_init(&S.dsb_go, 4);
-    mbar_init(&S.dsa_done, 1);
-    mbar_init(&S.ds_full, 1);
+#pragma unroll
+    for (int i = 0; i < (STATE ? 2 : 1); ++i) {
+      mbar_init(&S.dsa_go[i], 4 + kStateWarps);
+      mbar_init(&S.dsb_go[i], 4);
+      mbar_init(&S.dsa_done[i], 1);
+      mbar_init(&S.ds_full[i], 1);
+    }
     mbar_init(&S.o1_go, kStateWarps + 4);
     mbar_init(&S.o2_go, 4);
     mbar_init(&S.o_full, 2);
     mbar_init(&S.init, kStateWarps);
-    mbar_init(&S.drained, STATE ? 1 : 2);
+    mbar_init(&S.drained, 2);
     fence_mbar_init();
   }
   pdl_wait();
@@ -269,6 +279,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   umma::fence_after();
   const uint32_t tmem = S.tmem_base;
+  // Buffers of V w and dS: one, or two where G, S and the outputs leave their
+  // places to the second; chunk i's is buf(i), used for the use(i)-th time.
+  auto buf = [](int i) { return STATE ? i & 1 : 0; };
+  auto use = [](int i) { return STATE ? i >> 1 : i; };
+  auto ds_at = [&](int i) { return tmem + (buf(i) ? TM_O1 : TM_DS); };
+  auto vw_at = [&](int i) { return tmem + (buf(i) ? TM_S : TM_VW); };
+  using St = Stages<STATE>;
   const int64_t ld = (int64_t)a.hv * kD;
   if (!S.some || S.seg.padded) {
     if (S.some) {  // outputs of an unusable slot: zeros
@@ -292,12 +309,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   // thread's tokens are 8 m + 2 (lane % 4), + 1.
   auto split = [&](const int th0, const int th1, const int threads) {
     const int quarter = warp & 3, j0 = 2 * (lane & 3);
-    const uint32_t tlane = tmem + ((uint32_t)(32 * quarter) << 16);
     bool ok = true;
-    for (int i = 0; i < nit && ok; ++i) {
-      Stage& st = S.st[i % kStages];
+    int i = 0;
+    for (; i < nit && ok; ++i) {
+      uint8_t* const st = S.st + i % St::N * St::BYTES;
       const int L = count(i);
-      ok = wait_all(&S.full[i % kStages], (i / kStages) & 1);
+      ok = wait_all(&S.full[i % St::N], (i / St::N) & 1);
       if (L < kC) {
         if (named_sync_or(2, threads, !ok)) ok = false;
         if (!ok) break;
@@ -308,19 +325,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t at = (uint32_t)(L + e / 8) * 128u + (e % 8) * 16u;
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            tile_at<uint4>(st.v[b], sizeof(st.v[b]), at) = make_uint4(0, 0, 0, 0);
-            tile_at<uint4>(st.qk[b], sizeof(st.qk[b]), 8192 + at) = make_uint4(0, 0, 0, 0);
+            tile_at<uint4>(st + St::V + 8192 * b, 8192, at) = make_uint4(0, 0, 0, 0);
+            tile_at<uint4>(st + St::K + St::BLOCK * b, 8192, at) = make_uint4(0, 0, 0, 0);
           }
         }
         umma::fence_proxy_async();
         named_sync(2, threads);
       }
       if (!ok) break;
+      const uint32_t vw_t = vw_at(i) + ((uint32_t)(32 * quarter) << 16);
       const float* const wl = &S.w[kC - L + j0];  // of tokens j0, ..
 #pragma unroll 1
       for (int th = th0; th < th1; ++th) {  // 32 tokens
-        // the operand was read by the last chunk's products
-        if (i > 0 && !(ok = wait_all(th ? &S.ds_full : &S.dsa_done, (i - 1) & 1))) break;
+        // the operand was read by the products of the chunk before (STATE: two before)
+        if (use(i) > 0 && !(ok = wait_all(th ? &S.ds_full[buf(i)] : &S.dsa_done[buf(i)], (use(i) - 1) & 1))) break;
         umma::fence_after();
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
@@ -328,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int c = 4 * quarter + 2 * half + (lane >> 3 & 1);  // 16-byte piece of the 128 channels
           const int r8 = lane & 7;
           const uint32_t off = (c >> 3) * 8192u + (uint32_t)(32 * th + 8 * (lane >> 4) + r8) * 128u + (((c & 7) ^ r8) << 4);
-          const uint32_t row = smem_addr(st.v[0]) + off, to = smem_addr(S.vw[0]) + off;
+          const uint32_t row = smem_addr(st + St::V) + off, to = smem_addr(buf(i) ? S.o[0] : S.vw[0]) + off;
           float2 x[8];
 #pragma unroll
           for (int m = 0; m < 4; m += 2) {
@@ -349,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t r[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) r[k] = take_bf16(x[k]);
-            tmem_put_frag(tlane + TM_VW + 32 * part + 16 * th, half, r);
+            tmem_put_frag(vw_t + 32 * part + 16 * th, half, r);
           }
 #pragma unroll
           for (int m = 0; m < 4; m += 2) {
@@ -363,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_st();
         umma::fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(th ? &S.dsb_go : &S.dsa_go);
+        if (lane == 0) mbar_arrive(th ? &S.dsb_go[buf(i)] : &S.dsa_go[buf(i)]);
       }
       if (!ok) break;
       if (!STATE) {
@@ -373,50 +391,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&S.p_full);
       }
     }
-    if (!ok && lane == 0) report(a.err, GDN_DEV_ERR_TIMEOUT);
+    if (!ok) {
+      if (lane == 0) report(a.err, GDN_DEV_ERR_TIMEOUT);
+      // a warp whose wait ended just in time may have gone on to a last chunk
+      // that is not full: it is not left alone at the barrier there
+      if (i < nit - 1 && count(nit - 1) < kC) named_sync_or(2, threads, true);
+    }
   };
 
   if (warp >= kIssuer) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRestRegs));
-    const uint64_t dq0 = umma::desc(smem_addr(S.st[0].qk[0]), 16, 1024);  // q as rows, k 8 KB on
+    const uint64_t dq0 = umma::desc(smem_addr(S.st), 16, 1024);  // q as rows, k 8 KB on
     bool ok = true;
     int s = 0, s_par = 0;  // a chunk's stage and its phase
     auto next = [&]() {
-      if (++s == kStages) {
+      if (++s == St::N) {
         s = 0;
         s_par ^= 1;
       }
     };
-    if (warp == kIssuer) {
-      // ------------------------------------------------------- issuer of dS, O1
+    if (warp == kIssuer || (STATE && warp == kIssuer + 1)) {
+      // -------------- issuer of dS, O1 (STATE: both, of every other chunk's dS)
       constexpr uint32_t ID_DS = umma::idesc_bf16(128, kD, false, true);   // V w in TMEM
       constexpr uint32_t ID_DS3 = umma::idesc_bf16(128, kD, true, true);  // in shared memory
       constexpr uint32_t ID_O1 = umma::idesc_bf16(128, kC, false, false);
-      const uint64_t dk0 = umma::desc(smem_addr(S.st[0].qk[0]) + 8192, 16384, 1024);  // k as columns
-      const uint64_t dvw = umma::desc(smem_addr(S.vw[0]), 8192, 1024);
+      const uint64_t dk0 = umma::desc(smem_addr(S.st) + St::K, St::BLOCK, 1024);  // k as columns
+      const uint64_t dvw0 = umma::desc(smem_addr(S.vw[0]), 8192, 1024), dvw1 = umma::desc(smem_addr(S.o[0]), 8192, 1024);
 #pragma unroll 1
-      for (int i = 0; i < nit; ++i, next()) {
-        const uint32_t at = s * (uint32_t)sizeof(Stage);
+      for (int i = STATE ? warp - kIssuer : 0; i < nit; i += STATE ? 2 : 1) {
+        const uint32_t at = i % St::N * St::BYTES;
         // dS^T = (V w)^T K, the small parts first (whoever split V has seen the
         // chunk's copies land)
-        const uint64_t dk = umma::adv(dk0, at);
+        const uint64_t dk = umma::adv(dk0, at), dvw = buf(i) ? dvw1 : dvw0;
+        const uint32_t ds = ds_at(i), vw = vw_at(i);
 #pragma unroll
         for (int th = 0; th < 2; ++th) {  // 32 tokens, whose V w may be replaced under the others' products
-          if (!(ok = wait_all(th ? &S.dsb_go : &S.dsa_go, i & 1))) break;
+          if (!(ok = wait_all(th ? &S.dsb_go[buf(i)] : &S.dsa_go[buf(i)], use(i) & 1))) break;
           umma::fence_after();
           if (lane == 0) {
 #pragma unroll
             for (int k = 2 * th; k < 2 * th + 2; ++k) {
-              if (k == 0) mma_ss<false>(tmem + TM_DS, dvw, dk, ID_DS3);
-              else mma_ss<true>(tmem + TM_DS, umma::adv(dvw, 2048 * k), umma::adv(dk, 2048 * k), ID_DS3);
+              if (k == 0) mma_ss<false>(ds, dvw, dk, ID_DS3);
+              else mma_ss<true>(ds, umma::adv(dvw, 2048 * k), umma::adv(dk, 2048 * k), ID_DS3);
             }
 #pragma unroll
             for (int part = 1; part >= 0; --part)
 #pragma unroll
               for (int k = 2 * th; k < 2 * th + 2; ++k)
-                mma_ts<true>(tmem + TM_DS, tmem + TM_VW + 32 * part + 8 * k, umma::adv(dk, 2048 * k), ID_DS);
-            umma::commit(th ? &S.ds_full : &S.dsa_done);
-            if (STATE && th) umma::commit(&S.empty[s]);
+                mma_ts<true>(ds, vw + 32 * part + 8 * k, umma::adv(dk, 2048 * k), ID_DS);
+            umma::commit(th ? &S.ds_full[buf(i)] : &S.dsa_done[buf(i)]);
+            if (STATE && th) umma::commit(&S.empty[i % St::N]);
           }
           __syncwarp();
         }
@@ -441,13 +465,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // -------------------------------------------------------- issuer of G, O2
       constexpr uint32_t ID_G = umma::idesc_bf16(64, kC, false, false);
       constexpr uint32_t ID_O2 = umma::idesc_bf16(128, kC, true, false);
-      const uint64_t dv0 = umma::desc(smem_addr(S.st[0].v[0]), 8192, 1024);
+      const uint64_t dv0 = umma::desc(smem_addr(S.st) + St::V, 8192, 1024);
       const uint64_t dp0 = umma::desc(smem_addr(S.p[0][0]), 16, 1024);
       uint32_t at = 0;  // the stage of the chunk whose G is next
       auto issue_g = [&]() -> bool {
         if (!wait_all(&S.full[s], s_par)) return false;
         umma::fence_after();
-        at = s * (uint32_t)sizeof(Stage);
+        at = s * St::BYTES;
         if (lane == 0) {
           const uint64_t d = umma::adv(dq0, at);
           mma_ss<false>(tmem + TM_G, d, umma::adv(d, 8192), ID_G);
@@ -489,29 +513,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t kd = (int64_t)a.hk * kD;
       int n_load = 0;
       for (; n_load < nit; ++n_load) {
-        // the state tile has passed through the last stage; chunk n_load -
-        // kStages' products are done (and its V split, which dS waited for)
-        if (n_load == kStages - 1) ok = mbar_wait(&S.init, 0);
-        if (n_load >= kStages) ok = mbar_wait(&S.empty[s], s_par ^ 1);
+        // the state tile has passed through; the products of the stage's last
+        // chunk are done (and its V split, which dS waited for)
+        if (n_load == St::BEFORE_TILE) ok = mbar_wait(&S.init, 0);
+        if (ok && n_load >= St::N) ok = mbar_wait(&S.empty[s], s_par ^ 1);
         if (!ok) break;
-        Stage& st = S.st[s];
+        uint8_t* const st = S.st + s * St::BYTES;
         const int32_t row = (int32_t)(S.seg.t0 + from(n_load));
         mbar_arrive_expect_tx(&S.full[s], (STATE ? 4 : 6) * 8192);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const int64_t xq = hq * kD + 64 * b, xk = kd + xq, xv = 2 * kd + (int64_t)h * kD + 64 * b;
-          if (!STATE && GDN_SPAN_G(xq, 64, a.C)) tma_load_2d(st.qk[b], &xmap, (int32_t)xq, row, &S.full[s]);
-          if (GDN_SPAN_G(xk, 64, a.C)) tma_load_2d(st.qk[b] + 8192, &xmap, (int32_t)xk, row, &S.full[s]);
-          if (GDN_SPAN_G(xv, 64, a.C)) tma_load_2d(st.v[b], &xmap, (int32_t)xv, row, &S.full[s]);
+          if (!STATE && GDN_SPAN_G(xq, 64, a.C)) tma_load_2d(st + St::BLOCK * b, &xmap, (int32_t)xq, row, &S.full[s]);
+          if (GDN_SPAN_G(xk, 64, a.C)) tma_load_2d(st + St::K + St::BLOCK * b, &xmap, (int32_t)xk, row, &S.full[s]);
+          if (GDN_SPAN_G(xv, 64, a.C)) tma_load_2d(st + St::V + 8192 * b, &xmap, (int32_t)xv, row, &S.full[s]);
         }
         next();
       }
       if (!ok) report(a.err, GDN_DEV_ERR_TIMEOUT);
       // what is in flight lands before the memory goes (at once, unless a wait expired)
-      for (int k = max(0, n_load - kStages); k < n_load; ++k) mbar_wait(&S.full[k % kStages], (k / kStages) & 1);
+      for (int k = max(0, n_load - St::N); k < n_load; ++k) mbar_wait(&S.full[k % St::N], (k / St::N) & 1);
     }
     __syncwarp();
-    if (warp == kIssuer || (!STATE && warp == kIssuer + 1)) {
+    if (warp <= kIssuer + 1) {
       if (!ok && lane == 0) report(a.err, GDN_DEV_ERR_TIMEOUT);
       // the products in flight end before their memory is used otherwise
       if (lane == 0) umma::commit(&S.drained);
@@ -545,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait_all(&S.o_full, i & 1);
         umma::fence_after();
         if (lane == 0 && ok) {
-          mbar_arrive(&S.empty[i % kStages]);
+          mbar_arrive(&S.empty[i % St::N]);
           if (storer) bulk_wait_read();  // the last chunk's outputs have left their buffer
         }
         if (named_sync_or(3, 128, !ok)) {
@@ -617,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const auto segs = GDN_GV(a.seg_state, a.n_segs * slot_n);
     // A tile moves in whole rows (512 bytes per warp access) and through shared
     // memory: piece p of row r at p ^ (r & 7).
-    uint8_t* const tile = reinterpret_cast<uint8_t*>(&S.st[kStages - 1]);
+    uint8_t* const tile = S.st + kTileAt;
     auto piece = [](int r, int p) { return (uint32_t)r * 512u + (uint32_t)((p ^ (r & 7)) << 4); };
     float2 st[16];
     {
@@ -718,7 +742,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&S.p_full);
     };
     if (!STATE) put_s();
-    if (lane == 0) mbar_arrive(&S.dsa_go);  // no dS to read yet
+    if (lane == 0) {  // no dS to read yet
+      mbar_arrive(&S.dsa_go[0]);
+      if (STATE) mbar_arrive(&S.dsa_go[1]);
+    }
     bool ok = true;
     if (!STATE && (ok = wait_all(&S.g_full, 0))) put_p(0);
     // the chunk that ends at the next block boundary, and the boundary's place
@@ -734,19 +761,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < nit && ok; ++i) {
       const int L = count(i);
       const float dec = S.dec[L];
-      if (!(ok = wait_all(&S.ds_full, i & 1))) break;
+      if (!(ok = wait_all(&S.ds_full[buf(i)], use(i) & 1))) break;
       umma::fence_after();
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         float d[16];
-        umma::tmem_ld16(tlane + TM_DS + 32 * part + 16 * q, d);
+        umma::tmem_ld16(ds_at(i) + ((uint32_t)(32 * quarter) << 16) + 32 * part + 16 * q, d);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           st[8 * q + e] = fma2(st[8 * q + e], make_float2(dec, dec), make_float2(d[2 * e], d[2 * e + 1]));
       }
       umma::fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.dsa_go);
+      if (lane == 0) mbar_arrive(&S.dsa_go[buf(i)]);
       if (!STATE) {
         if (i + 1 < nit) {
           if (!(ok = wait_all(&S.g_full, (i + 1) & 1))) break;
