@@ -390,8 +390,119 @@ __device__ __forceinline__ void remap_entries(const CompactArgs& a, int64_t firs
   }
 }
 
-// One cluster.  `live` blocks are in use; the k-th highest of those at or
-// above `live` goes to the k-th lowest free one below it.
+// `live` blocks are in use; the k-th highest of those at or above `live` goes to
+// the k-th lowest free one below it.
+//
+// One CTA with everything but the tensors in its shared memory, 8 blocks and 8
+// table entries per thread: a few dependent global accesses and eight
+// barriers.
+constexpr int kSmallBlocks = 8 * kThreads, kSmallEntries = 8 * kThreads;
+template <bool REMAP>
+__global__ void __launch_bounds__(kThreads) compact_small_kernel(const CompactArgs a) {
+  constexpr int kWords = kSmallBlocks / 32, kPer = 8;
+  __shared__ uint32_t bits_s[kWords], was_s[kWords];                // the free blocks: now, before the moves
+  __shared__ uint16_t to_s[kSmallBlocks];                           // where a block goes
+  __shared__ uint16_t src_s[kSmallBlocks / 2], dst_s[kSmallBlocks / 2];  // (as many movers as holes)
+  __shared__ int warp_sums[32];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, N = a.num_blocks;
+  const auto bits = GDN_SV(bits_s, kWords), was = GDN_SV(was_s, kWords);
+  const auto to = GDN_SV(to_s, kSmallBlocks), src = GDN_SV(src_s, kSmallBlocks / 2), dst = GDN_SV(dst_s, kSmallBlocks / 2);
+  const auto free_ids = GDN_GV(a.free_ids, a.free_cap);
+  const auto free_out = GDN_GV(a.free_out, a.free_cap);
+  const auto refs = GDN_GV(a.refs, N);
+  const auto refs_out = GDN_GV(a.refs_out, N);
+  const auto table = GDN_GV(a.table, a.n_entries);
+  const auto table_out = GDN_GV(a.table_out, a.n_entries);
+  const auto move_src = GDN_GV(a.move_src, a.max_moves), move_dst = GDN_GV(a.move_dst, a.max_moves);
+  const int32_t nf0 = *a.n_free;
+  int32_t entry[kPer];
+  if (REMAP) {
+#pragma unroll
+    for (int e = 0; e < kPer; ++e)
+      if (e * kThreads + tid < a.n_entries) entry[e] = table[e * kThreads + tid];
+  }
+  if (tid < kWords) bits[tid] = 0;
+  for (int b = tid; b < N; b += kThreads) to[b] = (uint16_t)b;
+  __syncthreads();
+  const bool bad_count = nf0 < 0 || nf0 > a.free_cap || nf0 > N;
+  const int32_t n_free = bad_count ? 0 : nf0;
+  bool wrong = false;
+  for (int i = tid; i < n_free; i += kThreads) {
+    const int32_t id = free_ids[i];
+    if (id < 0 || id >= N) wrong = true;
+    else if (atomicOr(&bits[id >> 5], 1u << (id & 31)) >> (id & 31) & 1) wrong = true;  // twice on the stack
+  }
+  if (wrong) report(a.err, GDN_DEV_ERR_SLOT_OOB);
+  if (bad_count && tid == 0) report(a.err, GDN_DEV_ERR_BLOCKS);
+  const bool skip = __syncthreads_or(wrong || bad_count) != 0;
+  // this thread's blocks 8 tid .. 8 tid + 7
+  const int b0 = kPer * tid, live = N - n_free;
+  auto first = [&](int n) { return (1u << min(max(n - b0, 0), kPer)) - 1; };  // those below n
+  auto mine = [&]() { return bits[tid / 4] >> (kPer * (tid % 4)) & 0xffu; };
+  int moves = 0;
+  if (!skip) {
+    uint32_t h = mine() & first(live), m = ~mine() & first(N) & ~first(live);
+    const int nh = __popc(h), nm = __popc(m);
+    int total;
+    const int upto = scan_cta(nh | nm << 16, warp_sums, total), all = total >> 16;
+    moves = min(all, a.max_moves);
+    int k = (upto & 0xffff) - nh;
+    for (; h; h &= h - 1, ++k)
+      if (k < moves) dst[k] = (uint16_t)(b0 + __ffs(h) - 1);
+    k = all - (upto >> 16);  // movers above this thread's
+    for (; m; ++k) {
+      const int b = 31 - __clz(m);
+      if (k < moves) src[k] = (uint16_t)(b0 + b);
+      m &= ~(1u << b);
+    }
+    if (tid < kWords) was[tid] = bits[tid];
+    __syncthreads();
+  }
+  for (int64_t k = tid; k < a.max_moves; k += kThreads) {
+    if (k < moves) {
+      const int s = src[k], d = dst[k];
+      const int32_t c = refs[s];
+      move_src[k] = s;
+      move_dst[k] = d;
+      to[s] = (uint16_t)d;
+      atomicOr(&bits[s >> 5], 1u << (s & 31));
+      atomicAnd(&bits[d >> 5], ~(1u << (d & 31)));
+      refs_out[d] = c;  // a moved block's count goes along
+      refs_out[s] = 0;
+    } else {
+      move_src[k] = move_dst[k] = -1;
+    }
+  }
+  if (tid == 0) *a.n_moves = moves;
+  __syncthreads();
+  if (a.refs_out != a.refs)  // the others; a free block has none
+    for (int b = tid; b < N; b += kThreads) {
+      const uint32_t now = bits[b >> 5] >> (b & 31) & 1;
+      if (skip) refs_out[b] = refs[b];
+      else if (now == (was[b >> 5] >> (b & 31) & 1)) refs_out[b] = now ? 0 : refs[b];
+    }
+  if (a.free_out != a.free_ids)
+    for (int64_t i = (skip ? 0 : n_free) + tid; i < a.free_cap; i += kThreads) free_out[i] = free_ids[i];
+  if (REMAP) {
+#pragma unroll
+    for (int e = 0; e < kPer; ++e)
+      if (e * kThreads + tid < a.n_entries)
+        table_out[e * kThreads + tid] = slot_class(entry[e], N) ? entry[e] : (int32_t)to[entry[e]];
+  } else {
+    const auto remap = GDN_GV(a.remap, N);
+    for (int b = tid; b < N; b += kThreads) remap[b] = to[b];
+  }
+  if (skip) return;
+  // the stack: the free blocks, the lowest on top
+  uint32_t f = mine();
+  int all;
+  int k = scan_cta(__popc(f), warp_sums, all) - __popc(f);
+  for (; f; f &= f - 1, ++k) free_out[n_free - 1 - k] = (int32_t)(b0 + __ffs(f) - 1);
+}
+
+// The same by one cluster, for pools beyond a CTA's shared memory.
 template <bool REMAP>
 __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) {
   __shared__ int warp_sums[32];
@@ -414,7 +525,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) 
   for (int w = gt; w < a.words; w += gn) bitmap[w] = 0;
   if (gt == 0) *a.wrong = bad_count;
   for (int64_t b = gt; b < a.num_blocks; b += gn) remap[b] = (int32_t)b;
-  for (int k = gt; k < a.max_moves; k += gn) move_src[k] = move_dst[k] = -1;
+  for (int64_t k = gt; k < a.max_moves; k += gn) move_src[k] = move_dst[k] = -1;
   cluster.sync();
   bool wrong = false;
   for (int i = gt; i < n_free; i += gn) {
@@ -672,10 +783,14 @@ extern "C" gdn_status gdn_block_compact(const int32_t* block_table, int32_t* tab
   a.err = dev_err;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (one_cluster(1, n_entries)) {
-    e = launch_pdl(compact_kernel<true>, dim3(kCluster), dim3(kThreads), 0, s, dim3(kCluster), a);
+  const bool small = num_blocks <= kSmallBlocks, whole = n_entries <= kSmallEntries;
+  const unsigned ctas = small ? 1 : kCluster;
+  if (whole) {
+    e = launch_pdl(small ? compact_small_kernel<true> : compact_kernel<true>, dim3(ctas), dim3(kThreads), 0, s,
+                   dim3(ctas), a);
   } else {
-    e = launch_pdl(compact_kernel<false>, dim3(kCluster), dim3(kThreads), 0, s, dim3(kCluster), a);
+    e = launch_pdl(small ? compact_small_kernel<false> : compact_kernel<false>, dim3(ctas), dim3(kThreads), 0, s,
+                   dim3(ctas), a);
     if (e == cudaSuccess)
       e = launch_pdl(remap_kernel, dim3(4u * (unsigned)sm_count()), dim3(kRowThreads), 0, s, dim3(1), a);
   }

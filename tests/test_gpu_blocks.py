@@ -245,6 +245,31 @@ def test_compact(cuda, N, used, max_moves, in_place):
     assert int(nm) == len(movers) and src.tolist() == movers + pad and dst.tolist() == holes + pad and int(err) == 0
 
 
+@pytest.mark.parametrize("N,used,rows,max_blocks,max_moves", [
+    (8192, 0.5, 64, 128, 8192), (8192, 0.5, 64, 129, 5000), (8191, 0.9, 3, 3000, 8191), (8193, 0.5, 64, 128, 8193),
+    (40, 0.5, 90, 100, 40), (9000, 0.7, 100, 100, 100), (1024, 1.0, 8, 128, 5), (1025, 0.001, 8, 200, 1025),
+])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_compact_at_the_limits_of_one_cta(cuda, N, used, rows, max_blocks, max_moves, in_place):
+    p = Pool(N + rows, N, rows, max_blocks, 16)
+    for i in range(min(int(N * used), rows * max_blocks)):
+        p.table[i % rows, i // rows] = p.free.pop()
+        p.refs[p.table[i % rows, i // rows]] = int(p.rng.integers(3))
+    p.table[-1, -1] = p.table[0, 0]  # shared
+    p.device()
+    err, nm, src, dst = _word(), _word(), _i32([5] * max_moves), _i32([5] * max_moves)
+    ws = torch.full((gdn.block_compact_workspace_size(N),), 255, dtype=torch.uint8, device="cuda")
+    outs = {} if in_place else dict(table_out=torch.full_like(p.d_table, 3), refs_out=torch.full_like(p.d_refs, 3),
+                                    free_out=torch.full_like(p.d_free, 3))
+    gdn.block_compact(p.d_table, p.d_refs, p.d_free, p.d_n, src, dst, nm, ws, dev_err=err, **outs)
+    if not in_place:
+        p.d_table, p.d_refs, p.d_free = outs.values()
+    movers, holes = compact(p, max_moves)
+    p.check()
+    pad = [-1] * (max_moves - len(movers))
+    assert int(nm) == len(movers) and src.tolist() == movers + pad and dst.tolist() == holes + pad and int(err) == 0
+
+
 @pytest.mark.parametrize("wrong,bit", [("twice", binding.DEV_ERR_SLOT_OOB), ("outside", binding.DEV_ERR_SLOT_OOB),
                                        ("count", binding.DEV_ERR_BLOCKS), ("negative", binding.DEV_ERR_BLOCKS)])
 @pytest.mark.parametrize("in_place", [True, False])
