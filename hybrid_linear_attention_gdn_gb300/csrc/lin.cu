@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(256) lin_recurrent_kernel(const PrefillArgs a)
       }
     } else if (!STATE) {
       // the first segment's state holds the slot's already
-      const float keep = power(ld_h, (int64_t)a.seg_chunks * kC);
+      const float keep = power(ld_h, (int64_t)s.chunks * kC);
       for (int k = 0; k < s.seg; ++k) load(segs + (s.seg0 + k) * slot_n, k ? keep : 0.f);
     }
   }
@@ -352,27 +352,28 @@ cudaError_t recurrent_dispatch(const PrefillArgs& a, cudaStream_t s) {
   return cudaErrorInvalidValue;
 }
 
-// Blocks per segment; 2^30 where sequences stay whole.  The lengths are on the
+// Blocks per segment (kWhole: sequences stay whole).  The lengths are on the
 // device: the rule sees their number and sum.
-// Chunk form, one CTA per head and segment on an SM:
-//  * Few blocks in all (16, or 24 of several sequences) stay whole.
-//  * Fewer chains than half the SMs: as many segments per sequence as fit on
-//    them in one wave, of the mean length, not below kMinSeg blocks and at most
-//    kMaxSegs of them (a segment reads all its predecessors' states).
-//  * Else, up to kMaxSkew sequences: those longer than twice the mean are cut,
-//    so that a batch does not wait for its longest one.  (Where none is, the
-//    first launch finds nothing to do.)
-// Recurrence, a block in some 4 us: segments of 2 blocks or more until there
-// are 4 CTAs per SM.
-constexpr int64_t kWhole = 1 << 30, kMinSeg = 8, kMaxSegs = 16, kMaxSkew = 32, kMinRecSeg = 2;
+// Chunk form, one CTA per head and segment on an SM, some 1.75 us a block, and
+// 0.72 us in the state pass before it: segments of the length at which all of
+// them are one wave on the SMs, not below kMinSeg blocks.  They cost a second
+// launch and joining the states (a segment reads all its predecessors'), some
+// 6 us: worth it if the longest sequence takes longer whole,
+//   1.75 longest > (1.75 + 0.72) segment + 6,
+// which the device decides for itself where it is not known here.  Measured with 32
+// heads, cut and whole: 8192 tokens 93 and 212 us, 5000 + 1000 + 1000 92 and 132,
+// 2 x 2048 55 and 59; 3 x 2700 115 and 76 (two waves), 2 x 1024 36 and 33.
+constexpr int64_t kMinSeg = 8, kMaxSegs = 16, kMinRecSeg = 2;
+int64_t cut_from(int64_t seg) { return (10 * seg + 24) / 7 + 1; }
 int64_t chunk_seg(const gdn_dims& d, int32_t n_seq, int64_t total) {
-  const int64_t chunks = (total + kC - 1) / kC, mean = (chunks + n_seq - 1) / n_seq;
-  if (chunks <= (n_seq > 1 ? 24 : 16)) return kWhole;
-  const int64_t per_seq = sm_count() / d.hv / n_seq;
-  if (per_seq > 1)
-    return std::max(std::max((mean + per_seq) / per_seq, kMinSeg), (mean + kMaxSegs - 1) / kMaxSegs);
-  return n_seq > 1 && n_seq <= kMaxSkew ? 2 * std::max(mean, kMinSeg) : kWhole;
+  const int64_t chunks = (total + kC - 1) / kC, mean = (chunks + n_seq - 1) / n_seq, wave = sm_count() / d.hv;
+  if (wave < 2 || n_seq > kMaxCut) return kWhole;
+  // (a sequence's blocks may be one more than its length says)
+  const int64_t seg = std::max(std::max((chunks + n_seq) / wave + 1, kMinSeg), (mean + kMaxSegs - 1) / kMaxSegs);
+  return chunks < cut_from(seg) ? kWhole : seg;
 }
+// Recurrence, a block in some 16 us: segments of 2 blocks or more until there
+// are 4 CTAs per SM.
 int64_t rec_seg(const gdn_dims& d, int32_t n_seq, int64_t total) {
   const int64_t chunks = (total + kC - 1) / kC, mean = (chunks + n_seq - 1) / n_seq;
   const int64_t rows = rec_threads(d.dk, d.dv) / (d.dk / 16), ctas = d.hv * ((d.dv + rows - 1) / rows);
@@ -493,6 +494,7 @@ extern "C" gdn_status gdn_lin_prefill(const gdn_dims* dims, gdn_pool pool, gdn_p
   const int64_t sc = seg_chunks(*dims, n_seq, total_tokens, chunked), segs = seg_slots(sc, n_seq, total_tokens);
   if (segs > 65535) return GDN_ERR_UNSUPPORTED;
   a.seg_chunks = (int32_t)sc;
+  a.cut_from = chunked && sc < lin::kWhole ? (int32_t)std::min<int64_t>(cut_from(sc), INT32_MAX) : 0;
   a.n_segs = (int32_t)segs;
   a.seg_state = sc < lin::first_slot(total_tokens, n_seq) ? reinterpret_cast<float*>(workspace) : nullptr;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

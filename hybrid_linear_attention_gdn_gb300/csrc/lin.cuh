@@ -34,7 +34,13 @@ struct PrefillArgs {
   // from its predecessors' states.
   float* seg_state;  // [n_segs][hv][dv][dk]
   int32_t n_segs, seg_chunks;
+  // > 0 (at most kMaxCut sequences): they stay whole unless one has this many
+  // blocks, which only the device knows
+  int32_t cut_from;
 };
+
+constexpr int64_t kWhole = 1 << 30;  // blocks of a segment where sequences stay whole
+constexpr int kMaxCut = 32;
 
 // Sequence n's blocks occupy the slots from first_slot(cu[n], n) on, its
 // segments those from that / seg_chunks + n on.  A sequence of len tokens
@@ -54,6 +60,7 @@ struct Segment {
   int64_t seg0;     // its first segment's slot
   int32_t slot, n;  // state slot, sequence
   int32_t seg, n_seg;
+  int32_t chunks;   // blocks per segment
   int64_t m0, m1;   // the segment's tokens [m0, m1)
   bool padded;      // no usable slot: outputs are zeros
 };
@@ -63,42 +70,74 @@ __device__ __forceinline__ bool bad_rows(const PrefillArgs& a, int64_t t0, int64
   return t0 < 0 || len < 0 || t0 + len > a.total || p0 < 0 || p0 > INT64_MAX - len - kC;
 }
 
+// blocks of absolute positions that len tokens from position p0 on touch
+__device__ __forceinline__ int64_t blocks_of(int64_t len, int64_t p0) { return len ? (p0 % kC + len + kC - 1) / kC : 0; }
+
 // The segment of segment slot `at`, by one warp or more (every lane gets it).
 // false: no such segment.  The leader of segment slot n reports what is wrong
 // with sequence n (there are at least as many slots as sequences).
 __device__ __forceinline__ bool find_segment(const PrefillArgs& a, const int64_t at, Segment& s, bool leader) {
-  const auto cu = GDN_GV(a.cu_seqlens, a.n_seq + 1);
+  const auto cu = GDN_GV(a.cu_seqlens, a.n_seq + 1), ids = GDN_GV(a.slot_ids, a.n_seq);
+  const auto start = GDN_GV(a.start_pos, a.n_seq);
   const int lane = threadIdx.x & 31;
-  if (leader && at < a.n_seq) {
-    if (bad_rows(a, cu[at], (int64_t)cu[at + 1] - cu[at], GDN_GV(a.start_pos, a.n_seq)[at]))
-      report(a.err, GDN_DEV_ERR_SEQLENS);
-    else if (slot_class(GDN_GV(a.slot_ids, a.n_seq)[at], a.num_slots) == 2)
-      report(a.err, GDN_DEV_ERR_SLOT_OOB);
+  s.chunks = a.seg_chunks;
+  bool bad;
+  if (a.n_seq <= 32) {  // a sequence per lane: one round of loads
+    const bool mine = lane < a.n_seq;
+    const int i = mine ? lane : 0;
+    const int64_t t0 = cu[i], len = (int64_t)cu[i + 1] - t0, p0 = start[i];
+    const int32_t slot = ids[i];
+    bad = bad_rows(a, t0, len, p0);
+    const bool oob = slot_class(slot, a.num_slots) == 2;
+    if (a.cut_from > 0) {
+      // (a sequence has at most 2^25 + 2 blocks)
+      const int longest = __reduce_max_sync(0xffffffffu, mine && !bad ? (int)blocks_of(len, p0) : 0);
+      if (longest < a.cut_from) s.chunks = (int32_t)kWhole;
+    }
+    const uint32_t bad_set = __ballot_sync(0xffffffffu, mine && bad), oob_set = __ballot_sync(0xffffffffu, mine && oob);
+    if (leader && at < a.n_seq) {
+      if (bad_set >> at & 1) report(a.err, GDN_DEV_ERR_SEQLENS);
+      else if (oob_set >> at & 1) report(a.err, GDN_DEV_ERR_SLOT_OOB);
+    }
+    s.seg0 = first_slot(t0, i) / s.chunks + i;
+    const uint32_t le = __ballot_sync(0xffffffffu, mine && s.seg0 <= at);
+    s.n = le ? 31 - __clz(le) : 0;
+    bad = bad_set >> s.n & 1;
+    s.t0 = __shfl_sync(0xffffffffu, t0, s.n);
+    s.len = __shfl_sync(0xffffffffu, len, s.n);
+    s.p0 = __shfl_sync(0xffffffffu, p0, s.n);
+    s.slot = __shfl_sync(0xffffffffu, slot, s.n);
+    s.seg0 = __shfl_sync(0xffffffffu, s.seg0, s.n);
+  } else {
+    if (leader && at < a.n_seq) {
+      if (bad_rows(a, cu[at], (int64_t)cu[at + 1] - cu[at], start[at])) report(a.err, GDN_DEV_ERR_SEQLENS);
+      else if (slot_class(ids[at], a.num_slots) == 2) report(a.err, GDN_DEV_ERR_SLOT_OOB);
+    }
+    int lo = 0, n = a.n_seq;  // the answer is in [lo, lo + n)
+    while (n > 1) {           // offsets outside [0, total] end this early, never outside the array
+      const int step = (n + 31) / 32, i = lane * step;
+      const bool le = i < n && first_slot(cu[lo + (i < n ? i : 0)], lo + i) / s.chunks + (lo + i) <= at;
+      const uint32_t m = __ballot_sync(0xffffffffu, le);
+      const int last = m ? 31 - __clz(m) : 0;
+      lo += last * step;
+      n = min(step, n - last * step);
+    }
+    s.n = lo;
+    s.t0 = cu[lo];
+    s.len = (int64_t)cu[lo + 1] - s.t0;
+    s.p0 = start[lo];
+    s.slot = ids[lo];
+    bad = bad_rows(a, s.t0, s.len, s.p0);
+    s.seg0 = first_slot(s.t0, lo) / s.chunks + lo;
   }
-  int lo = 0, n = a.n_seq;  // the answer is in [lo, lo + n)
-  while (n > 1) {           // offsets outside [0, total] end this early, never outside the array
-    const int step = (n + 31) / 32, i = lane * step;
-    const bool le = i < n && first_slot(cu[lo + (i < n ? i : 0)], lo + i) / a.seg_chunks + (lo + i) <= at;
-    const uint32_t m = __ballot_sync(0xffffffffu, le);
-    const int last = m ? 31 - __clz(m) : 0;
-    lo += last * step;
-    n = min(step, n - last * step);
-  }
-  s.n = lo;
-  s.t0 = cu[lo];
-  s.len = (int64_t)cu[lo + 1] - s.t0;
-  s.p0 = GDN_GV(a.start_pos, a.n_seq)[lo];
-  s.slot = GDN_GV(a.slot_ids, a.n_seq)[lo];
-  if (bad_rows(a, s.t0, s.len, s.p0)) return false;
+  if (bad) return false;
   s.padded = slot_class(s.slot, a.num_slots) != 0;
-  s.seg0 = first_slot(s.t0, lo) / a.seg_chunks + lo;
-  const int64_t seg = at - s.seg0;
-  const int64_t head = s.p0 % kC, nch = s.len ? (head + s.len + kC - 1) / kC : 0;
-  s.n_seg = (int32_t)((nch + a.seg_chunks - 1) / a.seg_chunks);
+  const int64_t seg = at - s.seg0, head = s.p0 % kC;
+  s.n_seg = (int32_t)((blocks_of(s.len, s.p0) + s.chunks - 1) / s.chunks);
   if (seg < 0 || seg >= s.n_seg) return false;
   s.seg = (int32_t)seg;
-  s.m0 = seg ? seg * a.seg_chunks * kC - head : 0;
-  s.m1 = min(s.len, (seg + 1) * (int64_t)a.seg_chunks * kC - head);
+  s.m0 = seg ? seg * s.chunks * kC - head : 0;
+  s.m1 = min(s.len, (seg + 1) * (int64_t)s.chunks * kC - head);
   return true;
 }
 

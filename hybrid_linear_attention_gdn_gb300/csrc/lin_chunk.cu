@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 8; ++j) vec_at<float4>(keep, place(j)) = v[j];
         }
       } else if (!STATE) {
-        const float dec = power(GDN_GV(a.log_decay, a.hv)[h], (int64_t)a.seg_chunks * kC);
+        const float dec = power(GDN_GV(a.log_decay, a.hv)[h], (int64_t)S.seg.chunks * kC);
         for (int k = 0; k < seg; ++k) {
           const float d = k ? dec : 0.f;  // the first segment's state holds the slot's already
           const auto from_seg = segs + (S.seg.seg0 + k) * slot_n;

@@ -246,3 +246,30 @@ def test_slots_and_rows_beyond_32_bits(cuda):
     want = run(st.pool, [1, 2], 0, x, st.out(90))
     got = run(far, [slots - 1, slots - 2], rows - 90, big, big_o)
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("name", ["square", "own_keys"])
+@pytest.mark.parametrize("lens,starts", [
+    ([2100, 5, 64], [0, 3, 0]),           # one long sequence: cut
+    ([5, 900, 5, 1], [62, 127, 0, 9]),
+    ([720] * 3, [0, 64, 1]),              # of one length: whole
+    ([0, 3000, 0], [5, 70, 64]),
+    ([2000] + [7] * 31, [1] * 32),        # the most that are cut
+    ([2000] + [7] * 32, [1] * 33),        # one more: whole
+])
+def test_cut_or_whole_by_the_longest(cuda, name, lens, starts):
+    run_prefill(LinSetup(name, 33, num_slots=len(lens) + 3), lens, starts, block=256, gaps=(1, 2))
+
+
+def test_bad_offsets_beside_a_cut_sequence(cuda):
+    """A sequence whose rows are inconsistent is left out, the others run."""
+    st = LinSetup("square", 34)
+    x = st.tokens(2300)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = st.out(2300)
+    _call(st, st.pool, _i32([1, 2, 5]), _i32([0, 2000, 2300, 2200]), _i64([0, 0, 0]), x.cuda(), out, err=err)
+    ref = linear.prefill(st.od, st.opool, None, st.old, st.scale, [1, 2], [0, 2000, 2300], [0, 0], np.zeros((2, 0), int),
+                         64, f64(x))
+    assert_out_close(out, ref, 128)
+    _state_close(st.pool, st.opool)
+    assert int(err) == gdn.binding.DEV_ERR_SEQLENS
