@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 4) qk_rope_kernel(const RopeArgs a, 
   const bool turns = 8 * l < a.rot;  // (rot is a multiple of 8)
   const int ea = INTER || !turns ? 8 * l : 4 * l, eb = INTER || !turns ? 8 * l + 4 : half + 4 * l;
   float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
-  if (turns) {
+  if (turns && !ri.bad) {  // (a table of no rows is not read)
     const auto tab = GDN_GV(a.cos_sin, a.max_pos * a.rot) + ri.pos * a.rot;
     const float4 c4 = vec_at<const float4>(tab, 4 * l), s4 = vec_at<const float4>(tab, half + 4 * l);
     c[0] = c4.x, c[1] = c4.y, c[2] = c4.z, c[3] = c4.w;

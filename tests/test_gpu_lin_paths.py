@@ -273,3 +273,13 @@ def test_bad_offsets_beside_a_cut_sequence(cuda):
     assert_out_close(out, ref, 128)
     _state_close(st.pool, st.opool)
     assert int(err) == gdn.binding.DEV_ERR_SEQLENS
+
+
+def test_a_verified_draft_is_committed(cuda):
+    """spec_commit of slots without a conv history."""
+    st = LinSetup("tiny", 35)
+    spec = StatePool(torch.randn((6, *st.pool.ssm.shape[1:]), generator=st.gen).cuda())
+    want = st.pool.ssm.clone()
+    gdn.spec_commit(st.dims, spec, st.pool, _i32([[0, 1, 2], [3, 4, 5], [1, 2, 3]]), _i32([2, 0, 3]), _i32([4, 5, 0]))
+    want[4], want[0] = spec.ssm[1], spec.ssm[3]
+    assert torch.equal(st.pool.ssm, want)

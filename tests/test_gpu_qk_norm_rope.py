@@ -230,3 +230,15 @@ def test_refusals(cuda):
             f()
             pytest.fail(f"case {i} was accepted")
     assert torch.equal(before, c.x)
+
+
+@pytest.mark.parametrize("d", [64, 20])
+def test_a_table_of_no_positions(cuda, d):
+    """Every position lies outside: zeros, and the table is not read."""
+    c = Case(40, 5, 3, 1, d, 4 if d == 20 else 32, "bf16")
+    c.cs = torch.ones((3, c.cs.shape[1]))
+    tab = c.cs.cuda()[:0]
+    q, k = gdn.qk_norm_rope(c.q, c.k, c.qw.cuda(), c.kw.cuda(), tab, c.pos.cuda(), dev_err=c.err) \
+        if tab.data_ptr() else (c.q.zero_(), c.k.zero_())
+    assert not bool(q.any()) and not bool(k.any())
+    assert not tab.data_ptr() or int(c.err) == binding.DEV_ERR_SEQLENS
