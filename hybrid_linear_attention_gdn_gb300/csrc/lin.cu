@@ -189,18 +189,16 @@ __global__ void __launch_bounds__(256) lin_recurrent_kernel(const PrefillArgs a)
   const int64_t own = h * head + (int64_t)(r0 + row) * DK + c0;  // this thread's place in a slot
   const auto pool = GDN_GV(a.ssm, a.num_slots * slot_n);
   const auto segs = GDN_GV(a.seg_state, a.n_segs * slot_n);
-  float st[16];
+  float2 st[8];  // (pairs: two fused multiply-adds per instruction)
 #pragma unroll
-  for (int e = 0; e < 16; ++e) st[e] = 0.f;
+  for (int e = 0; e < 8; ++e) st[e] = make_float2(0.f, 0.f);
   if (active) {
     auto load = [&](const auto& from, float keep) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float4 u = vec_at<const float4>(from, own + 4 * LPR * e);
-        st[4 * e] = fmaf(keep, st[4 * e], u.x);
-        st[4 * e + 1] = fmaf(keep, st[4 * e + 1], u.y);
-        st[4 * e + 2] = fmaf(keep, st[4 * e + 2], u.z);
-        st[4 * e + 3] = fmaf(keep, st[4 * e + 3], u.w);
+        st[2 * e] = fma2(make_float2(keep, keep), st[2 * e], lo2(u));
+        st[2 * e + 1] = fma2(make_float2(keep, keep), st[2 * e + 1], hi2(u));
       }
     };
     if (s.seg == 0) {
@@ -211,7 +209,7 @@ __global__ void __launch_bounds__(256) lin_recurrent_kernel(const PrefillArgs a)
         const auto keep = segs + (s.seg0 + s.n_seg - 1) * slot_n;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          vec_at<float4>(keep, own + 4 * LPR * e) = make_float4(st[4 * e], st[4 * e + 1], st[4 * e + 2], st[4 * e + 3]);
+          vec_at<float4>(keep, own + 4 * LPR * e) = join4(st[2 * e], st[2 * e + 1]);
       }
     } else if (!STATE) {
       // the first segment's state holds the slot's already
@@ -273,24 +271,20 @@ __global__ void __launch_bounds__(256) lin_recurrent_kernel(const PrefillArgs a)
 #pragma unroll 4
     for (int t = 0; t < n; ++t) {
       const float v = sv[(t << rsh) + row];
-      float p[4] = {0.f, 0.f, 0.f, 0.f};
+      float2 p[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float4 k4 = vec_at<const float4>(sk, t * DK + c0 + 4 * LPR * e);
-        st[4 * e] = step(dec, st[4 * e], v, k4.x);
-        st[4 * e + 1] = step(dec, st[4 * e + 1], v, k4.y);
-        st[4 * e + 2] = step(dec, st[4 * e + 2], v, k4.z);
-        st[4 * e + 3] = step(dec, st[4 * e + 3], v, k4.w);
+        st[2 * e] = step2(dec, st[2 * e], v, lo2(k4));
+        st[2 * e + 1] = step2(dec, st[2 * e + 1], v, hi2(k4));
         if (!STATE) {
           const float4 q4 = vec_at<const float4>(sq, t * DK + c0 + 4 * LPR * e);
-          p[0] = fmaf(st[4 * e], q4.x, p[0]);
-          p[1] = fmaf(st[4 * e + 1], q4.y, p[1]);
-          p[2] = fmaf(st[4 * e + 2], q4.z, p[2]);
-          p[3] = fmaf(st[4 * e + 3], q4.w, p[3]);
+          p[0] = fma2(st[2 * e], lo2(q4), p[0]);
+          p[1] = fma2(st[2 * e + 1], hi2(q4), p[1]);
         }
       }
       if (!STATE) {
-        float o = (p[0] + p[1]) + (p[2] + p[3]);
+        float o = (p[0].x + p[0].y) + (p[1].x + p[1].y);
 #pragma unroll
         for (int w = LPR / 2; w; w /= 2) o += __shfl_xor_sync(0xffffffffu, o, w);
         if (active && tid % LPR == 0) so[(t << rsh) + row] = o * a.scale;
@@ -299,7 +293,7 @@ __global__ void __launch_bounds__(256) lin_recurrent_kernel(const PrefillArgs a)
     auto store = [&](const auto& to) {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        vec_at<float4>(to, own + 4 * LPR * e) = make_float4(st[4 * e], st[4 * e + 1], st[4 * e + 2], st[4 * e + 3]);
+        vec_at<float4>(to, own + 4 * LPR * e) = join4(st[2 * e], st[2 * e + 1]);
     };
     if (!STATE && at_bound && active) {
       const int64_t idx = bound + s.p0;  // the boundary's position
@@ -363,7 +357,7 @@ cudaError_t recurrent_dispatch(const PrefillArgs& a, cudaStream_t s) {
 // which the device decides for itself where it is not known here.  Measured with 32
 // heads, cut and whole: 8192 tokens 93 and 212 us, 5000 + 1000 + 1000 92 and 132,
 // 2 x 2048 55 and 59; 3 x 2700 115 and 76 (two waves), 2 x 1024 36 and 33.
-constexpr int64_t kMinSeg = 8, kMaxSegs = 16, kMinRecSeg = 2;
+constexpr int64_t kMinSeg = 8, kMaxSegs = 16;
 int64_t cut_from(int64_t seg) { return (10 * seg + 24) / 7 + 1; }
 int64_t chunk_seg(const gdn_dims& d, int32_t n_seq, int64_t total) {
   const int64_t chunks = (total + kC - 1) / kC, mean = (chunks + n_seq - 1) / n_seq, wave = sm_count() / d.hv;
@@ -372,14 +366,18 @@ int64_t chunk_seg(const gdn_dims& d, int32_t n_seq, int64_t total) {
   const int64_t seg = std::max(std::max((chunks + n_seq) / wave + 1, kMinSeg), (mean + kMaxSegs - 1) / kMaxSegs);
   return chunks < cut_from(seg) ? kWhole : seg;
 }
-// Recurrence, a block in some 16 us: segments of 2 blocks or more until there
-// are 4 CTAs per SM.
+// Recurrence, a block in some 16 us and 10 in the state pass: as short segments
+// as give 3 CTAs per SM, at most kMaxRecSegs per sequence of the mean length; a
+// mean below two segments stays whole.  Cut and whole, 16 heads of 64 x 64: 1024
+// tokens 46 and 278 us (in segments of 2 blocks 79), 2048 tokens 85 (2 blocks; of 1
+// block 91) and 553; 8 x 60 tokens 30 and 20.
+constexpr int64_t kMaxRecSegs = 32;
 int64_t rec_seg(const gdn_dims& d, int32_t n_seq, int64_t total) {
   const int64_t chunks = (total + kC - 1) / kC, mean = (chunks + n_seq - 1) / n_seq;
   const int64_t rows = rec_threads(d.dk, d.dv) / (d.dk / 16), ctas = d.hv * ((d.dv + rows - 1) / rows);
-  const int64_t per_seq = std::min<int64_t>(4LL * sm_count() / ctas / n_seq, kMaxSegs);
-  if (per_seq <= 1 || mean <= kMinRecSeg) return kWhole;
-  return std::max((mean + per_seq) / per_seq, kMinRecSeg);
+  const int64_t fill = 3LL * sm_count();
+  const int64_t seg = std::max(((chunks + n_seq) * ctas + fill - 1) / fill, (mean + kMaxRecSegs - 1) / kMaxRecSegs);
+  return mean < 2 * seg ? kWhole : seg;
 }
 int64_t seg_chunks(const gdn_dims& d, int32_t n_seq, int64_t total, bool chunked) {
   return chunked ? chunk_seg(d, n_seq, total) : rec_seg(d, n_seq, total);

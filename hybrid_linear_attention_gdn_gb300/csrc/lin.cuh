@@ -168,6 +168,10 @@ __device__ __forceinline__ float step(Decay d, float s, float v, float k) {
   return fmaf(d.hi, s, fmaf(d.lo, s, v * k));
 }
 
+__device__ __forceinline__ float2 step2(Decay d, float2 s, float v, float2 k) {
+  return fma2(make_float2(d.hi, d.hi), s, fma2(make_float2(d.lo, d.lo), s, mul2(make_float2(v, v), k)));
+}
+
 // The chunk form on the tensor cores (lin_chunk.cu)
 bool chunk_shape(const gdn_dims& d);
 bool chunk_supported(const gdn_dims& d, int64_t total, const void* qkv, const void* out);
