@@ -19,7 +19,10 @@ using namespace lin;
 // ---------------------------------------------------------------------------
 // A state row of dk floats lies across LPR = dk / 4 lanes, a float4 each; a
 // thread holds NR of its warp's rows at once, all requested before the first
-// is used.  HBM bound: 8 dk bytes per row against 4 dk flops.
+// is used.  HBM bound: 8 dk bytes per row against 4 dk flops; 249 requests of 32
+// heads of 128 x 128 153 us, a copy's rate, one request 2.0 us.  NR 4 of dk 128, 32
+// rows per CTA: with 8 as fast from 64 requests on, but 2.5 us for one and 9.3
+// for 16 of them (7.8); with 16 192 us for 249, as half the warps fit.
 struct DecodeArgs {
   float* ssm;
   int32_t num_slots;
@@ -116,25 +119,18 @@ __global__ void __launch_bounds__(kDT) lin_decode_kernel(const DecodeArgs a) {
   if ((writer == 0 || (lane & (2 * writer - 1)) == 0) && at < a.dv) out[at] = from_f32<T>(p[0] * a.scale);
 }
 
-template <int DK, int BIG, int SMALL, typename T>
+template <int DK, int NR, typename T>
 cudaError_t decode_launch(const DecodeArgs& a, cudaStream_t s) {
-  constexpr int per = kDT / 32 * (32 / (DK / 4));
-  const int64_t big = (int64_t)((a.dv + per * BIG - 1) / (per * BIG)) * a.hv * a.B;
-  // Whole heads per CTA once that fills the SMs twice over, else fewer rows
-  // per thread and more CTAs.
-  if (big >= 2LL * sm_count())
-    return launch_pdl(lin_decode_kernel<DK, BIG, T>, dim3((a.dv + per * BIG - 1) / (per * BIG), a.hv, a.B), dim3(kDT),
-                      0, s, dim3(1), a);
-  return launch_pdl(lin_decode_kernel<DK, SMALL, T>, dim3((a.dv + per * SMALL - 1) / (per * SMALL), a.hv, a.B),
-                    dim3(kDT), 0, s, dim3(1), a);
+  constexpr int per = kDT / 32 * (32 / (DK / 4)) * NR;
+  return launch_pdl(lin_decode_kernel<DK, NR, T>, dim3((a.dv + per - 1) / per, a.hv, a.B), dim3(kDT), 0, s, dim3(1), a);
 }
 
 template <typename T>
 cudaError_t decode_dispatch(const DecodeArgs& a, int dk, cudaStream_t s) {
   switch (dk) {
-    case 16: return decode_launch<16, 4, 1, T>(a, s);
-    case 64: return decode_launch<64, 8, 2, T>(a, s);
-    case 128: return decode_launch<128, 8, 4, T>(a, s);
+    case 16: return decode_launch<16, 1, T>(a, s);
+    case 64: return decode_launch<64, 2, T>(a, s);
+    case 128: return decode_launch<128, 4, T>(a, s);
   }
   return cudaErrorInvalidValue;
 }
@@ -145,7 +141,10 @@ cudaError_t decode_dispatch(const DecodeArgs& a, int dk, cudaStream_t s) {
 // A state row lies across DK / 16 lanes, 16 columns each (in runs of 4, so that
 // the lanes' shared-memory accesses lie side by side), in registers; tokens
 // come through shared memory in windows of up to 16, the next window's inputs
-// requested a window ahead.  A window ends at a checkpoint.
+// requested a window ahead.  A window ends at a checkpoint.  Bound by issue: a
+// token costs a warp 40 paired multiply-adds and 9 shared-memory reads for its 32
+// x 16 values, 0.25 us with a CTA or two per SM; sequences are cut into segments
+// to fill the SMs.
 constexpr int kWin = 16;
 
 __host__ __device__ constexpr int rec_min_threads(int dk) { return dk == 128 ? 128 : dk == 64 ? 64 : 32; }

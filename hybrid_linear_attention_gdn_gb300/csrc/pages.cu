@@ -395,7 +395,7 @@ __device__ __forceinline__ void remap_entries(const CompactArgs& a, int64_t firs
 //
 // One CTA with everything but the tensors in its shared memory, 8 blocks and 8
 // table entries per thread: a few dependent global accesses and eight
-// barriers.
+// barriers.  512 blocks 4.8 us (by one cluster 13.4), 8192 blocks 11.9 (19.2).
 constexpr int kSmallBlocks = 8 * kThreads, kSmallEntries = 8 * kThreads;
 template <bool REMAP>
 __global__ void __launch_bounds__(kThreads) compact_small_kernel(const CompactArgs a) {
