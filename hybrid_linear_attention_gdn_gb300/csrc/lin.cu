@@ -349,20 +349,24 @@ cudaError_t recurrent_dispatch(const PrefillArgs& a, cudaStream_t s) {
 // device: the rule sees their number and sum.
 // Chunk form, one CTA per head and segment on an SM, some 1.75 us a block, and
 // 0.72 us in the state pass before it: segments of the length at which all of
-// them are one wave on the SMs, not below kMinSeg blocks.  They cost a second
-// launch and joining the states (a segment reads all its predecessors'), some
-// 6 us: worth it if the longest sequence takes longer whole,
+// them are one wave on the SMs, not below kMinSeg blocks.  Flags, another launch
+// and joining the states (a segment reads all its predecessors') cost some 6 us:
+// worth it if the longest sequence takes longer whole,
 //   1.75 longest > (1.75 + 0.72) segment + 6,
-// which the device decides for itself where it is not known here.  Measured with 32
-// heads, cut and whole: 8192 tokens 93 and 212 us, 5000 + 1000 + 1000 92 and 132,
-// 2 x 2048 55 and 59; 3 x 2700 115 and 76 (two waves), 2 x 1024 36 and 33.
+// which the device decides where it is not known here.  Measured with 32 heads, cut
+// and whole: 8192 tokens 91 and 217 us, 5000 + 1000 + 1000 87 and 136, 2 x 2048 50
+// and 60; 3 x 2700 90 and 78 (two waves), 2 x 1024 36 and 34.
 constexpr int64_t kMinSeg = 8, kMaxSegs = 16;
 int64_t cut_from(int64_t seg) { return (10 * seg + 24) / 7 + 1; }
 int64_t chunk_seg(const gdn_dims& d, int32_t n_seq, int64_t total) {
   const int64_t chunks = (total + kC - 1) / kC, mean = (chunks + n_seq - 1) / n_seq, wave = sm_count() / d.hv;
   if (wave < 2 || n_seq > kMaxCut) return kWhole;
-  // (a sequence's blocks may be one more than its length says)
-  const int64_t seg = std::max(std::max((chunks + n_seq) / wave + 1, kMinSeg), (mean + kMaxSegs - 1) / kMaxSegs);
+  // (a sequence's blocks may be one more than its length says.)  First segments run
+  // beside the state pass on the SMs that it leaves free; where those are half
+  // a wave of heads or more, a shorter one per sequence is for nothing.
+  const int64_t spare = 2 * (sm_count() - wave * d.hv) >= d.hv ? 45 : 0, all = 100 * (chunks + n_seq - 1);
+  const int64_t seg = std::max(std::max((all + 100 * wave + spare - 1) / (100 * wave + spare) + 1, kMinSeg),
+                               (mean + kMaxSegs - 1) / kMaxSegs);
   return chunks < cut_from(seg) ? kWhole : seg;
 }
 // Recurrence, a block in some 16 us and 10 in the state pass: as short segments
@@ -435,9 +439,9 @@ extern "C" size_t gdn_lin_prefill_workspace_size(const gdn_dims* dims, int32_t n
   // (which form runs depends on the tensors' alignment, too)
   size_t most = 0;
   for (int chunked = 0; chunked <= (lin::chunk_shape(*dims) ? 1 : 0); ++chunked) {
-    const int64_t sc = seg_chunks(*dims, n_seq, total_tokens, chunked);
+    const int64_t sc = seg_chunks(*dims, n_seq, total_tokens, chunked), segs = seg_slots(sc, n_seq, total_tokens);
     if (sc < lin::first_slot(total_tokens, n_seq))
-      most = std::max(most, (size_t)seg_slots(sc, n_seq, total_tokens) * ssm_slot_bytes(*dims));
+      most = std::max(most, (size_t)segs * ssm_slot_bytes(*dims) + (chunked ? 4 * lin::sync_words(segs, dims->hv) : 0));
   }
   return most;
 }
@@ -491,9 +495,15 @@ extern "C" gdn_status gdn_lin_prefill(const gdn_dims* dims, gdn_pool pool, gdn_p
   const int64_t sc = seg_chunks(*dims, n_seq, total_tokens, chunked), segs = seg_slots(sc, n_seq, total_tokens);
   if (segs > 65535) return GDN_ERR_UNSUPPORTED;
   a.seg_chunks = (int32_t)sc;
-  a.cut_from = chunked && sc < lin::kWhole ? (int32_t)std::min<int64_t>(cut_from(sc), INT32_MAX) : 0;
   a.n_segs = (int32_t)segs;
   a.seg_state = sc < lin::first_slot(total_tokens, n_seq) ? reinterpret_cast<float*>(workspace) : nullptr;
+  if (chunked && a.seg_state) {
+    a.sync = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + (size_t)segs * ssm_slot_bytes(*dims));
+    a.cut_from = (int32_t)std::min<int64_t>(cut_from(sc), INT32_MAX);
+    // a sequence of b blocks has (b - 1) / sc segments beyond its first one, and all
+    // have at most total / 64 + 2 n_seq blocks
+    a.max_extra = (int32_t)((total_tokens / lin::kC + n_seq) / sc);
+  }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = chunked                          ? lin::chunk_launch(a, s)
                         : dims->act_dtype == GDN_BF16 ? recurrent_dispatch<__nv_bfloat16>(a, s)

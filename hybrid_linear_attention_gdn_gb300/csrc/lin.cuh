@@ -28,12 +28,16 @@ struct PrefillArgs {
   int32_t hk, hv, dk, dv, G;
   int64_t C;
   // Segments of seg_chunks blocks; slots n_segs.  Where a sequence has
-  // several, a first launch leaves each segment's own state (from zero, the
+  // several, a state pass leaves each segment's own state (from zero, the
   // first one from the slot's) in seg_state, the slot's own state at the last
-  // segment's otherwise unused place, and a second launch starts each segment
-  // from its predecessors' states.
+  // segment's otherwise unused place, and each segment starts from its
+  // predecessors' states.
   float* seg_state;  // [n_segs][hv][dv][dk]
   int32_t n_segs, seg_chunks;
+  // Chunk form: what is in seg_state, and the work's order.  [0]: pieces of work
+  // taken; [1 + segment slot hv + head]: whether that place's state is there.
+  uint32_t* sync;
+  int32_t max_extra;  // most segments beyond the sequences' first ones
   // > 0 (at most kMaxCut sequences): they stay whole unless one has this many
   // blocks, which only the device knows
   int32_t cut_from;
@@ -50,6 +54,12 @@ constexpr int kMaxCut = 32;
 __host__ __device__ __forceinline__ int64_t first_slot(int64_t tokens, int64_t n) {
   const int64_t by_chunk = tokens / kC + 2 * n;
   return by_chunk < tokens ? by_chunk : tokens;
+}
+
+// sequence n's first segment slot, in 32 bits (a 64-bit division costs as much as
+// a load); offsets that are none come out as any number
+__device__ __forceinline__ int64_t first_segment(int64_t tokens, int64_t n, int chunks) {
+  return (uint32_t)first_slot(tokens, n) / (uint32_t)chunks + n;
 }
 
 // One segment of one sequence.
@@ -73,71 +83,140 @@ __device__ __forceinline__ bool bad_rows(const PrefillArgs& a, int64_t t0, int64
 // blocks of absolute positions that len tokens from position p0 on touch
 __device__ __forceinline__ int64_t blocks_of(int64_t len, int64_t p0) { return len ? (p0 % kC + len + kC - 1) / kC : 0; }
 
+// One sequence as a lane holds it.
+struct Sequence {
+  int64_t t0, len, p0;
+  int32_t slot;
+  bool bad, oob;
+};
+__device__ __forceinline__ Sequence load_sequence(const PrefillArgs& a, int i) {
+  const auto cu = GDN_GV(a.cu_seqlens, a.n_seq + 1);
+  Sequence q;
+  q.t0 = cu[i];
+  q.len = (int64_t)cu[i + 1] - q.t0;
+  q.p0 = GDN_GV(a.start_pos, a.n_seq)[i];
+  q.slot = GDN_GV(a.slot_ids, a.n_seq)[i];
+  q.bad = bad_rows(a, q.t0, q.len, q.p0);
+  q.oob = slot_class(q.slot, a.num_slots) == 2;
+  return q;
+}
+__device__ __forceinline__ void report_sequence(const PrefillArgs& a, const Sequence& q) {
+  if (q.bad) report(a.err, GDN_DEV_ERR_SEQLENS);
+  else if (q.oob) report(a.err, GDN_DEV_ERR_SLOT_OOB);
+}
+// The first one of a sequence's n_seg segments has what is left of whole ones: it
+// waits for no other.  Where the state pass runs beside the others (a.sync), it
+// has 7/10 of two segments: the second one waits for a pass over the first.
+__device__ __forceinline__ int64_t first_blocks(const PrefillArgs& a, int64_t blocks, int n_seg, int chunks) {
+  const int64_t rest = blocks - (n_seg - 1) * (int64_t)chunks;
+  return a.sync && n_seg == 2 ? max(rest, (7 * blocks + 9) / 10) : rest;
+}
+// segment `seg` of sequence n in segments of `chunks` blocks
+__device__ __forceinline__ Segment segment_of(const PrefillArgs& a, const Sequence& q, int n, int64_t seg, int chunks) {
+  Segment s;
+  const int64_t head = q.p0 % kC;
+  s.t0 = q.t0;
+  s.p0 = q.p0;
+  s.len = q.len;
+  s.slot = q.slot;
+  s.n = n;
+  s.chunks = chunks;
+  s.seg0 = first_segment(q.t0, n, chunks);
+  s.padded = slot_class(q.slot, a.num_slots) != 0;
+  const int64_t blocks = blocks_of(q.len, q.p0);
+  s.n_seg = ((uint32_t)blocks + chunks - 1) / (uint32_t)chunks;  // (at most 2^25 + 2 blocks)
+  s.seg = (int32_t)seg;
+  const int64_t first = first_blocks(a, blocks, s.n_seg, chunks);
+  s.m0 = seg ? (first + (seg - 1) * chunks) * kC - head : 0;
+  s.m1 = min(q.len, (first + seg * chunks) * kC - head);
+  return s;
+}
+
 // The segment of segment slot `at`, by one warp or more (every lane gets it).
 // false: no such segment.  The leader of segment slot n reports what is wrong
 // with sequence n (there are at least as many slots as sequences).
 __device__ __forceinline__ bool find_segment(const PrefillArgs& a, const int64_t at, Segment& s, bool leader) {
-  const auto cu = GDN_GV(a.cu_seqlens, a.n_seq + 1), ids = GDN_GV(a.slot_ids, a.n_seq);
-  const auto start = GDN_GV(a.start_pos, a.n_seq);
+  const auto cu = GDN_GV(a.cu_seqlens, a.n_seq + 1);
   const int lane = threadIdx.x & 31;
-  s.chunks = a.seg_chunks;
-  bool bad;
+  Sequence q;
+  int n;
   if (a.n_seq <= 32) {  // a sequence per lane: one round of loads
     const bool mine = lane < a.n_seq;
-    const int i = mine ? lane : 0;
-    const int64_t t0 = cu[i], len = (int64_t)cu[i + 1] - t0, p0 = start[i];
-    const int32_t slot = ids[i];
-    bad = bad_rows(a, t0, len, p0);
-    const bool oob = slot_class(slot, a.num_slots) == 2;
-    if (a.cut_from > 0) {
-      // (a sequence has at most 2^25 + 2 blocks)
-      const int longest = __reduce_max_sync(0xffffffffu, mine && !bad ? (int)blocks_of(len, p0) : 0);
-      if (longest < a.cut_from) s.chunks = (int32_t)kWhole;
-    }
-    const uint32_t bad_set = __ballot_sync(0xffffffffu, mine && bad), oob_set = __ballot_sync(0xffffffffu, mine && oob);
-    if (leader && at < a.n_seq) {
-      if (bad_set >> at & 1) report(a.err, GDN_DEV_ERR_SEQLENS);
-      else if (oob_set >> at & 1) report(a.err, GDN_DEV_ERR_SLOT_OOB);
-    }
-    s.seg0 = first_slot(t0, i) / s.chunks + i;
-    const uint32_t le = __ballot_sync(0xffffffffu, mine && s.seg0 <= at);
-    s.n = le ? 31 - __clz(le) : 0;
-    bad = bad_set >> s.n & 1;
-    s.t0 = __shfl_sync(0xffffffffu, t0, s.n);
-    s.len = __shfl_sync(0xffffffffu, len, s.n);
-    s.p0 = __shfl_sync(0xffffffffu, p0, s.n);
-    s.slot = __shfl_sync(0xffffffffu, slot, s.n);
-    s.seg0 = __shfl_sync(0xffffffffu, s.seg0, s.n);
+    q = load_sequence(a, mine ? lane : 0);
+    if (leader && lane == 0 && at < a.n_seq) report_sequence(a, at ? load_sequence(a, (int)at) : q);
+    const uint32_t le = __ballot_sync(0xffffffffu, mine && first_segment(q.t0, lane, a.seg_chunks) <= at);
+    n = le ? 31 - __clz(le) : 0;
+    q.t0 = __shfl_sync(0xffffffffu, q.t0, n);
+    q.len = __shfl_sync(0xffffffffu, q.len, n);
+    q.p0 = __shfl_sync(0xffffffffu, q.p0, n);
+    q.slot = __shfl_sync(0xffffffffu, q.slot, n);
+    q.bad = bad_rows(a, q.t0, q.len, q.p0);
   } else {
-    if (leader && at < a.n_seq) {
-      if (bad_rows(a, cu[at], (int64_t)cu[at + 1] - cu[at], start[at])) report(a.err, GDN_DEV_ERR_SEQLENS);
-      else if (slot_class(ids[at], a.num_slots) == 2) report(a.err, GDN_DEV_ERR_SLOT_OOB);
-    }
-    int lo = 0, n = a.n_seq;  // the answer is in [lo, lo + n)
-    while (n > 1) {           // offsets outside [0, total] end this early, never outside the array
-      const int step = (n + 31) / 32, i = lane * step;
-      const bool le = i < n && first_slot(cu[lo + (i < n ? i : 0)], lo + i) / s.chunks + (lo + i) <= at;
-      const uint32_t m = __ballot_sync(0xffffffffu, le);
-      const int last = m ? 31 - __clz(m) : 0;
+    if (leader && lane == 0 && at < a.n_seq) report_sequence(a, load_sequence(a, (int)at));
+    int lo = 0, m = a.n_seq;  // the answer is in [lo, lo + m)
+    while (m > 1) {           // offsets outside [0, total] end this early, never outside the array
+      const int step = (m + 31) / 32, i = lane * step;
+      const bool le = i < m && first_segment(cu[lo + (i < m ? i : 0)], lo + i, a.seg_chunks) <= at;
+      const uint32_t set = __ballot_sync(0xffffffffu, le);
+      const int last = set ? 31 - __clz(set) : 0;
       lo += last * step;
-      n = min(step, n - last * step);
+      m = min(step, m - last * step);
     }
-    s.n = lo;
-    s.t0 = cu[lo];
-    s.len = (int64_t)cu[lo + 1] - s.t0;
-    s.p0 = start[lo];
-    s.slot = ids[lo];
-    bad = bad_rows(a, s.t0, s.len, s.p0);
-    s.seg0 = first_slot(s.t0, lo) / s.chunks + lo;
+    n = lo;
+    q = load_sequence(a, n);
   }
-  if (bad) return false;
-  s.padded = slot_class(s.slot, a.num_slots) != 0;
-  const int64_t seg = at - s.seg0, head = s.p0 % kC;
-  s.n_seg = (int32_t)((blocks_of(s.len, s.p0) + s.chunks - 1) / s.chunks);
-  if (seg < 0 || seg >= s.n_seg) return false;
-  s.seg = (int32_t)seg;
-  s.m0 = seg ? seg * s.chunks * kC - head : 0;
-  s.m1 = min(s.len, (seg + 1) * (int64_t)s.chunks * kC - head);
+  if (q.bad) return false;
+  const int64_t seg = at - first_segment(q.t0, n, a.seg_chunks);
+  s = segment_of(a, q, n, seg, a.seg_chunks);
+  return seg >= 0 && seg < s.n_seg;
+}
+
+// Piece `item` of the work of at most kMaxCut sequences, by one warp: first the
+// state passes of all segments but the last ones, then every sequence's first
+// segment, the longest first, then the other segments.  A piece waits for
+// earlier ones at most.  Sequences stay whole unless one has cut_from blocks.
+// false: there is no such piece.
+__device__ __forceinline__ bool find_item(const PrefillArgs& a, int64_t item, Segment& s, bool& state, bool leader) {
+  const int lane = threadIdx.x & 31;
+  const bool mine = lane < a.n_seq;
+  Sequence q = load_sequence(a, mine ? lane : 0);
+  if (leader && mine) report_sequence(a, q);
+  const int blocks = mine && !q.bad ? (int)blocks_of(q.len, q.p0) : 0;  // (at most 2^25 + 2)
+  const int longest = __reduce_max_sync(0xffffffffu, blocks);
+  // a sequence without a usable slot has nothing to hand on
+  const int chunks = longest < a.cut_from || slot_class(q.slot, a.num_slots) ? (int)kWhole : a.seg_chunks;
+  const int n_seg = (blocks + chunks - 1) / chunks, extra = max(n_seg - 1, 0);
+  int upto = extra;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += u;
+  }
+  const int extras = __shfl_sync(0xffffffffu, upto, 31), firsts = __popc(__ballot_sync(0xffffffffu, n_seg > 0));
+  state = item < extras;
+  const bool first = !state && item < extras + firsts;
+  const int64_t rest = state ? item : item - extras - firsts;  // among those behind the first ones
+  uint32_t who;
+  if (first) {
+    const int key = n_seg ? (int)first_blocks(a, blocks, n_seg, chunks) : 0;
+    int rank = 0;
+    for (int i = 0; i < a.n_seq; ++i) {
+      const int k = __shfl_sync(0xffffffffu, key, i);
+      rank += k > key || (k == key && i < lane);
+    }
+    who = __ballot_sync(0xffffffffu, n_seg > 0 && rank == item - extras);
+  } else {
+    who = __ballot_sync(0xffffffffu, upto > rest);
+  }
+  if (!who) return false;
+  const int n = __ffs(who) - 1;
+  const int before = __shfl_sync(0xffffffffu, upto - extra, n);
+  const int64_t seg = first ? 0 : rest - before + (state ? 0 : 1);
+  q.t0 = __shfl_sync(0xffffffffu, q.t0, n);
+  q.len = __shfl_sync(0xffffffffu, q.len, n);
+  q.p0 = __shfl_sync(0xffffffffu, q.p0, n);
+  q.slot = __shfl_sync(0xffffffffu, q.slot, n);
+  s = segment_of(a, q, n, seg, __shfl_sync(0xffffffffu, chunks, n));
   return true;
 }
 
@@ -171,6 +250,9 @@ __device__ __forceinline__ float step(Decay d, float s, float v, float k) {
 __device__ __forceinline__ float2 step2(Decay d, float2 s, float v, float2 k) {
   return fma2(make_float2(d.hi, d.hi), s, fma2(make_float2(d.lo, d.lo), s, mul2(make_float2(v, v), k)));
 }
+
+// words of PrefillArgs::sync
+inline int64_t sync_words(int64_t n_segs, int64_t hv) { return 1 + n_segs * hv; }
 
 // The chunk form on the tensor cores (lin_chunk.cu)
 bool chunk_shape(const gdn_dims& d);

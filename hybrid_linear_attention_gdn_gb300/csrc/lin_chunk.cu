@@ -35,10 +35,17 @@
 // issuer's waits for the other warps left it idle a third of the time.
 //
 // Bound by the products: 2,630 of some 3,100 cycles a chunk.  4 x 8192 tokens of 32
-// heads 225 us (128 CTAs; 0.76 of a copy of the same bytes), 1 x 8192 93 us (four
-// segments: state pass 30, then 62), 37 tokens 8.0 us.  The roles' loops share the
+// heads 223 us (128 CTAs; 0.76 of a copy of the same bytes), 1 x 8192 91 us (five
+// segments), 37 tokens 8.3 us.  The roles' loops share the
 // instruction caches: rolled, and with short waits, their hit rate went from 73 to 94
 // % and 4 x 8192 tokens from 260 to 241 us.
+//
+// Sequences that may be cut into segments are one launch behind a small one that
+// clears the flags: state passes and segments are pieces of work that CTAs take
+// in an order in which whatever a piece waits for was taken before it, so that first
+// segments and whole sequences run beside the state pass (as two launches: seven
+// ragged prompts of 3,968 tokens 71 us, now 63; 2 x 2048 54 and 50; 1 x 8192 93 and 91;
+// 2048 alone 36 and 38, the price of the order).
 #include "lin.cuh"
 
 #include "decode_tma.cuh"  // sm_count
@@ -85,7 +92,8 @@ struct __align__(1024) ChunkSmem {
   float pt[kC];                 // scale lambda^(n + 1)
   float dec[kC + 1];            // lambda^n
   Segment seg;
-  int some;
+  int work, head;
+  float log_decay;
   uint64_t full[Stages<true>::N], empty[Stages<true>::N];
   // dsa_go: V w of the chunk's first 32 tokens is there, the last dS has been
   // read; dsb_go: that of its last 32; dsa_done: the former's products are done;
@@ -230,19 +238,29 @@ __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity) {
   return true;
 }
 
-// grid (V heads, segment slots).  STATE: the segment's own state alone (every
-// segment but a sequence's last).
+// Marks the state at segment slot `at` as there; the writers have met at a barrier.
+__device__ __forceinline__ void set_flag(const PrefillArgs& a, int64_t at, int h) {
+  __threadfence();
+  atomicExch(&GDN_GV(a.sync, 1 + (int64_t)a.n_segs * a.hv)[1 + at * a.hv + h], 1u);
+}
+// Waits for it, at most kWaitLimitNs; the pieces that set flags wait for none.
+__device__ __forceinline__ bool wait_flag(const PrefillArgs& a, int64_t at, int h) {
+  const uint32_t* const p = &GDN_GV(a.sync, 1 + (int64_t)a.n_segs * a.hv)[1 + at * a.hv + h];
+  uint64_t t0 = 0;
+  for (;;) {
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];\n" : "=r"(v) : "l"(p) : "memory");
+    if (v) return true;
+    const uint64_t t = globaltimer_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kWaitLimitNs) return false;
+  }
+}
+
+// Barriers, before the CTA's own.
 template <bool STATE>
-__global__ void __launch_bounds__(kThreads, 1)
-    lin_chunk_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap xmap,
-                     const __grid_constant__ CUtensorMap omap) {
-  extern __shared__ __align__(1024) unsigned char smem_raw[];
-  ChunkSmem& S = *reinterpret_cast<ChunkSmem*>(smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023));
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be one value per warp
-  const int h = blockIdx.x, hq = h / a.G;
-  if (warp == 1) umma::tmem_alloc(&S.tmem_base, TM_COLS);
-  if (tid == 64) {
+__device__ __forceinline__ void init_barriers(ChunkSmem& S) {
+  if (threadIdx.x == 64) {
 #pragma unroll
     for (int i = 0; i < Stages<STATE>::N; ++i) {
       mbar_init(&S.full[i], 1);
@@ -264,27 +282,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&S.drained, 2);
     fence_mbar_init();
   }
-  pdl_wait();
-  pdl_trigger();
-  if (warp == 0) {
-    Segment s;
-    const bool some = find_segment(a, blockIdx.y, s, !STATE && lane == 0 && h == 0);
-    if (lane == 0) {
-      S.seg = s;
-      S.some = some && !(STATE && (s.seg == s.n_seg - 1 || s.padded));
-    }
-  }
-  if (tid >= 96 && tid < 96 + 2 * kC) {
-    const int n = tid - 96;
-    const float ld_h = GDN_GV(a.log_decay, a.hv)[h], x = n <= kC ? power(ld_h, n) : 0.f;
+}
+// A head's factors, before it, too.
+__device__ __forceinline__ void init_factors(ChunkSmem& S, const float scale, const float log_decay) {
+  const int n = (int)threadIdx.x - 96;
+  if (n >= 0 && n < 2 * kC) {
+    const float x = n <= kC ? power(log_decay, n) : 0.f;
     if (n <= kC) S.dec[n] = x;
     S.w[n < kC ? kC - 1 - n : n] = n < kC ? x : 0.f;
-    if (n < kC) S.ps[n] = x * a.scale;
-    if (n >= 1 && n <= kC) S.pt[n - 1] = x * a.scale;
+    if (n < kC) S.ps[n] = x * scale;
+    if (n >= 1 && n <= kC) S.pt[n - 1] = x * scale;
   }
-  umma::fence_before();
-  __syncthreads();
-  umma::fence_after();
+}
+
+// The chunks of segment S.seg of V head h.  STATE: the segment's own state alone.
+template <bool STATE>
+__device__ __forceinline__ void run(const PrefillArgs& a, const CUtensorMap& xmap, const CUtensorMap& omap, ChunkSmem& S,
+                                    const int h, const int warp) {
+  const int tid = threadIdx.x, lane = tid & 31, hq = h / a.G;
   const uint32_t tmem = S.tmem_base;
   // Buffers of V w and dS: one, or two where G, S and the outputs leave their
   // places to the second; chunk i's is buf(i), used for the use(i)-th time.
@@ -294,16 +309,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto vw_at = [&](int i) { return tmem + (buf(i) ? TM_S : TM_VW); };
   using St = Stages<STATE>;
   const int64_t ld = (int64_t)a.hv * kD;
-  if (!S.some || S.seg.padded) {
-    if (S.some) {  // outputs of an unusable slot: zeros
-      const auto out = GDN_GV(reinterpret_cast<uint4*>(a.out), a.total * ld / 8);
-      const int64_t n = (S.seg.m1 - S.seg.m0) * (kD / 8);
-      for (int64_t e = tid; e < n; e += kThreads)
-        out[((S.seg.t0 + S.seg.m0 + e / (kD / 8)) * ld + (int64_t)h * kD) / 8 + e % (kD / 8)] = make_uint4(0, 0, 0, 0);
-    }
-    if (warp == 1) umma::tmem_dealloc(tmem, TM_COLS);
-    return;
-  }
   // chunk i holds the segment's tokens [from(i), from(i) + count(i))
   const int64_t m0 = S.seg.m0, m1 = S.seg.m1;
   const int head = (int)((S.seg.p0 + m0) % kC);  // 0 but for a sequence's first chunk
@@ -653,6 +658,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     float2 st[16];
     {
       const int seg = S.seg.seg, n_seg = S.seg.n_seg;
+      if (!STATE && n_seg > 1) {  // the slot's own state, or the predecessors' passes
+        bool there = true;
+        if (seg == 0) there = wait_flag(a, S.seg.seg0 + n_seg - 1, h);
+        else
+          for (int k = lane; k < seg; k += 32) there &= wait_flag(a, S.seg.seg0 + k, h);
+        if (!there) report(a.err, GDN_DEV_ERR_TIMEOUT);
+        __syncwarp();
+      }
       float4 v[8];  // piece `lane` of rows warp, warp + 16, ..
       auto place = [&](int j) { return own + ((warp + 16 * j) * 32 + lane) * 4; };
 #pragma unroll
@@ -669,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 8; ++j) vec_at<float4>(keep, place(j)) = v[j];
         }
       } else if (!STATE) {
-        const float dec = power(GDN_GV(a.log_decay, a.hv)[h], (int64_t)S.seg.chunks * kC);
+        const float dec = power(S.log_decay, (int64_t)S.seg.chunks * kC);
         for (int k = 0; k < seg; ++k) {
           const float d = k ? dec : 0.f;  // the first segment's state holds the slot's already
           const auto from_seg = segs + (S.seg.seg0 + k) * slot_n;
@@ -686,6 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int j = 0; j < 8; ++j) tile_at<float4>(tile, kTile, piece(warp + 16 * j, lane)) = v[j];
       named_sync(1, kStateThreads);
+      if (STATE && seg == 0 && tid == 0) set_flag(a, S.seg.seg0 + n_seg - 1, h);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float4 x = tile_at<float4>(tile, kTile, piece(row, 8 * part + e));
@@ -838,10 +852,86 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < 8; ++j)
         vec_at<float4>(to, own + ((warp + 16 * j) * 32 + lane) * 4) = tile_at<float4>(tile, kTile, piece(warp + 16 * j, lane));
     }
+    if (STATE) {
+      named_sync(1, kStateThreads);
+      if (tid == 0) set_flag(a, S.seg.seg0 + S.seg.seg, h);  // (after a timeout, too: nobody waits for long)
+    }
+  }
+}
+
+// CUT: some sequences may be cut into segments.  A CTA takes the next piece of
+// work, state passes before the segments that wait for them, so that whatever is
+// waited for has begun.  Else grid (V heads, sequences).
+template <bool CUT>
+__global__ void __launch_bounds__(kThreads, 1)
+    lin_chunk_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap xmap,
+                     const __grid_constant__ CUtensorMap omap) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  ChunkSmem& S = *reinterpret_cast<ChunkSmem*>(smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023));
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be one value per warp
+  if (warp == 1) umma::tmem_alloc(&S.tmem_base, TM_COLS);
+  if (!CUT) init_barriers<false>(S);
+  pdl_wait();
+  pdl_trigger();
+  if (!CUT && tid >= 96 && tid < 96 + 2 * kC) init_factors(S, a.scale, GDN_GV(a.log_decay, a.hv)[blockIdx.x]);
+  if (warp == 0) {
+    Segment s;
+    bool some, state = false;
+    int h = blockIdx.x;
+    float log_decay;
+    if (CUT) {
+      uint32_t ticket = 0;
+      if (lane == 0) ticket = atomicAdd(&GDN_GV(a.sync, 1)[0], 1u);
+      ticket = __shfl_sync(0xffffffffu, ticket, 0);
+      h = (int)(ticket % a.hv);
+      log_decay = GDN_GV(a.log_decay, a.hv)[h];
+      some = find_item(a, ticket / a.hv, s, state, ticket == 0);
+    } else {
+      log_decay = GDN_GV(a.log_decay, a.hv)[h];
+      some = find_segment(a, blockIdx.y, s, lane == 0 && h == 0);
+    }
+    if (lane == 0) {
+      S.seg = s;
+      S.head = h;
+      S.work = !some ? 0 : state ? 1 : s.padded ? 2 : 3;
+      S.log_decay = log_decay;
+    }
   }
   umma::fence_before();
   __syncthreads();
-  if (warp == 1) umma::tmem_dealloc(tmem, TM_COLS);
+  umma::fence_after();
+  const int work = S.work, h = CUT ? S.head : (int)blockIdx.x;
+  if (work == 3) {
+    if (CUT) {
+      init_barriers<false>(S);
+      init_factors(S, a.scale, S.log_decay);
+      __syncthreads();
+    }
+    run<false>(a, xmap, omap, S, h, warp);
+  } else if (CUT && work == 1) {
+    init_barriers<true>(S);
+    init_factors(S, a.scale, S.log_decay);
+    __syncthreads();
+    run<true>(a, xmap, omap, S, h, warp);
+  } else if (work == 2) {  // outputs of an unusable slot: zeros
+    const int64_t ld = (int64_t)a.hv * kD;
+    const auto out = GDN_GV(reinterpret_cast<uint4*>(a.out), a.total * ld / 8);
+    const int64_t n = (S.seg.m1 - S.seg.m0) * (kD / 8);
+    for (int64_t e = tid; e < n; e += kThreads)
+      out[((S.seg.t0 + S.seg.m0 + e / (kD / 8)) * ld + (int64_t)h * kD) / 8 + e % (kD / 8)] = make_uint4(0, 0, 0, 0);
+  }
+  umma::fence_before();
+  __syncthreads();
+  if (warp == 1) umma::tmem_dealloc(S.tmem_base, TM_COLS);
+}
+
+// no piece taken, no state there
+__global__ void __launch_bounds__(256) lin_clear_kernel(uint32_t* sync, int64_t words) {
+  pdl_wait();
+  pdl_trigger();
+  const auto w = GDN_GV(sync, words);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < words; i += (int64_t)gridDim.x * 256) w[i] = 0;
 }
 
 }  // namespace
@@ -859,15 +949,19 @@ cudaError_t chunk_launch(const PrefillArgs& a, cudaStream_t s) {
   if ((e = tensor_map_2d(&omap, a.out, a.total, (int64_t)a.hv * kD, 2, 64, kC, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess)
     return e;
   const size_t smem = sizeof(ChunkSmem) + 1024;
-  const dim3 grid(a.hv, a.n_segs);
   if (a.seg_state) {
+    const int64_t words = sync_words(a.n_segs, a.hv);
+    const int64_t pieces = (2LL * a.max_extra + a.n_seq) * a.hv;  // state passes, segments behind the first ones, those
+    if ((e = launch_pdl(lin_clear_kernel, dim3((unsigned)std::min<int64_t>((words + 255) / 256, 64)), dim3(256), 0, s,
+                        dim3(1), a.sync, words)) != cudaSuccess)
+      return e;
     constexpr auto k = lin_chunk_kernel<true>;
     if ((e = ssm::allow_smem<k>(smem)) != cudaSuccess) return e;
-    if ((e = launch_pdl(k, grid, dim3(kThreads), smem, s, dim3(1), a, xmap, omap)) != cudaSuccess) return e;
+    return launch_pdl(k, dim3((unsigned)pieces), dim3(kThreads), smem, s, dim3(1), a, xmap, omap);
   }
   constexpr auto k = lin_chunk_kernel<false>;
   if ((e = ssm::allow_smem<k>(smem)) != cudaSuccess) return e;
-  return launch_pdl(k, grid, dim3(kThreads), smem, s, dim3(1), a, xmap, omap);
+  return launch_pdl(k, dim3(a.hv, a.n_segs), dim3(kThreads), smem, s, dim3(1), a, xmap, omap);
 }
 
 }  // namespace lin
