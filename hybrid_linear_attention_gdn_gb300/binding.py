@@ -31,6 +31,7 @@ _DT_CODE = {torch.float32: F32, torch.bfloat16: BF16}
 
 _lock = threading.Lock()
 _lib = None
+_checked = False  # whether that is the bounds-checked library
 
 
 class GdnError(RuntimeError):
@@ -139,7 +140,9 @@ def library_path() -> str:
 
 def load(build_if_missing: bool = False) -> ctypes.CDLL:
     """Load libgdn.so (optionally building it first).  Raises if absent."""
-    global _lib
+    global _lib, _checked
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = library_path()
@@ -154,6 +157,7 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
                 fn = getattr(lib, name)
                 fn.argtypes = argtypes
                 fn.restype = restype
+            _checked = debug_bounds()
             _lib = lib
     return _lib
 
@@ -182,7 +186,7 @@ def _check(fn: str, status: int):
         raise GdnError(fn, status, msg)
     # the checked library: every call is followed by a read of the bounds
     # words (not while a CUDA graph is being captured)
-    if debug_bounds() and not torch.cuda.is_current_stream_capturing():
+    if _checked and not torch.cuda.is_current_stream_capturing():
         bad = debug_bounds_take()
         if bad is not None:
             raise BoundsError(f"{fn}: {bad[0]} index check(s) failed, first at {bad[1]}: "
@@ -238,13 +242,12 @@ class Dims:
         return 2 * self.hk * self.dk + self.hv * self.dv
 
     def c(self) -> CDims:
-        key = (self.hk, self.hv, self.dk, self.dv, self.conv_width, self.act_dtype, self.conv_dtype)
-        cached = self.__dict__.get("_c")
-        if cached is None or cached[0] != key:
-            cached = (key, CDims(self.hk, self.hv, self.dk, self.dv, self.conv_width,
-                                 _DT_CODE[self.act_dtype], _DT_CODE[self.conv_dtype]))
+        cached = self.__dict__.get("_c")  # (frozen: made once)
+        if cached is None:
+            cached = CDims(self.hk, self.hv, self.dk, self.dv, self.conv_width, _DT_CODE[self.act_dtype],
+                           _DT_CODE[self.conv_dtype])
             self.__dict__["_c"] = cached
-        return cached[1]
+        return cached
 
 
 @dataclass
