@@ -175,16 +175,18 @@ def test_captured_calls(cuda, name):
             assert all(torch.equal(a, b) for a, b in zip((out, tok, st.pool.ssm, ck.ssm), want))
 
 
-def test_threads_on_their_own_streams(cuda):
+@pytest.mark.parametrize("total", [900, 2600])
+def test_threads_on_their_own_streams(cuda, total):
+    """Whole sequences, and one that is cut (pieces of one call wait for others of it)."""
     base = LinSetup("square", 28)
-    x = base.tokens(900).cuda()
+    x = base.tokens(total).cuda()
     first = base.pool.ssm.clone()
-    cu, sp, ids = _i32([0, 700, 900]), _i64([0, 70]), _i32([2, 5])
+    cu, sp, ids = _i32([0, total - 200, total]), _i64([0, 70]), _i32([2, 5])
 
     def work(stream, res):
         with torch.cuda.stream(stream):
-            pool, out = StatePool(first.clone()), base.out(900)
-            tok, ws = base.out(2), _ws(base, 2, 900)
+            pool, out = StatePool(first.clone()), base.out(total)
+            tok, ws = base.out(2), _ws(base, 2, total)
             for _ in range(20):
                 _call(base, pool, ids, cu, sp, x, out, ws=ws)
                 gdn.lin_decode_step(base.dims, pool, base.ld, ids, x[:2], tok, scale=base.scale)
