@@ -24,7 +24,7 @@
 // bf16 parts keep fp32's range, so no scaling is needed.
 //
 // A product of K = 16 takes some 59 cycles with N = 64 and 67 to 73 with N = 128
-// (measured; M = 64 no less than M = 128), 2,800 a chunk, and both operands from
+// (measured; M = 64 no less than M = 128), 2,630 a chunk, and both operands from
 // shared memory take all its bandwidth: two parts of V w therefore go through
 // registers to TMEM, whose 512 columns are all in use.
 //
@@ -35,10 +35,10 @@
 // issuer's waits for the other warps left it idle a third of the time.
 //
 // Bound by the products: 2,630 of some 3,100 cycles a chunk.  4 x 8192 tokens of 32
-// heads 223 us (128 CTAs; 0.76 of a copy of the same bytes), 1 x 8192 91 us (five
-// segments), 37 tokens 8.3 us.  The roles' loops share the
-// instruction caches: rolled, and with short waits, their hit rate went from 73 to 94
-// % and 4 x 8192 tokens from 260 to 241 us.
+// heads 223 us (128 CTAs; 0.76 of a copy's rate), 1 x 8192 91 us (five segments), 37
+// tokens 8.3 us.  The roles' loops share the instruction caches: rolled, and with
+// short waits, their hit rate went from 73 to 94 % and 4 x 8192 tokens from 260 to
+// 241 us.
 //
 // Sequences that may be cut into segments are one launch behind a small one that
 // clears the flags: state passes and segments are pieces of work that CTAs take
@@ -182,8 +182,10 @@ __device__ __forceinline__ void tmem_get_frag2(uint32_t ta, uint32_t tb, int hal
       "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, "
       "[%33];\n"
       "tcgen05.wait::ld.sync.aligned;\n"
-      : "=f"(va[0]), "=f"(va[1]), "=f"(va[2]), "=f"(va[3]), "=f"(va[4]), "=f"(va[5]), "=f"(va[6]), "=f"(va[7]), "=f"(va[8]), "=f"(va[9]), "=f"(va[10]), "=f"(va[11]), "=f"(va[12]), "=f"(va[13]), "=f"(va[14]), "=f"(va[15]),
-        "=f"(vb[0]), "=f"(vb[1]), "=f"(vb[2]), "=f"(vb[3]), "=f"(vb[4]), "=f"(vb[5]), "=f"(vb[6]), "=f"(vb[7]), "=f"(vb[8]), "=f"(vb[9]), "=f"(vb[10]), "=f"(vb[11]), "=f"(vb[12]), "=f"(vb[13]), "=f"(vb[14]), "=f"(vb[15])
+      : "=f"(va[0]), "=f"(va[1]), "=f"(va[2]), "=f"(va[3]), "=f"(va[4]), "=f"(va[5]), "=f"(va[6]), "=f"(va[7]),
+      "=f"(va[8]), "=f"(va[9]), "=f"(va[10]), "=f"(va[11]), "=f"(va[12]), "=f"(va[13]), "=f"(va[14]), "=f"(va[15]),
+        "=f"(vb[0]), "=f"(vb[1]), "=f"(vb[2]), "=f"(vb[3]), "=f"(vb[4]), "=f"(vb[5]), "=f"(vb[6]), "=f"(vb[7]),
+        "=f"(vb[8]), "=f"(vb[9]), "=f"(vb[10]), "=f"(vb[11]), "=f"(vb[12]), "=f"(vb[13]), "=f"(vb[14]), "=f"(vb[15])
       : "r"(ta + off), "r"(tb + off)
       : "memory");
 }
