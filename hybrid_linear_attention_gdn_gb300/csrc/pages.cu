@@ -313,10 +313,8 @@ __global__ void __launch_bounds__(kThreads) release_push_kernel(const ReleaseArg
   constexpr int kTile = kThreads * kPer;
   const int64_t tiles = ((int64_t)a.num_blocks + kTile - 1) / kTile, per = (tiles + kCluster - 1) / kCluster;
   const int64_t b0 = rank * per * kTile, b1 = min((int64_t)a.num_blocks, b0 + per * kTile);
-  if (ROWS) {
-    release_rows(a, rank * (kThreads / 32) + (tid >> 5), kCluster * (kThreads / 32), tid & 31, 32);
-    cluster.sync();  // the counts are final
-  }
+  if (ROWS) release_rows(a, rank * (kThreads / 32) + (tid >> 5), kCluster * (kThreads / 32), tid & 31, 32);
+  cluster.sync();  // the counts are final; every CTA has begun, so that its shared memory may be written
   int mine = 0;
   for (int64_t b = b0 + tid; b < b1; b += kThreads) mine += refs[b] < 0;
   int total;
@@ -526,7 +524,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) 
   if (gt == 0) *a.wrong = bad_count;
   for (int64_t b = gt; b < a.num_blocks; b += gn) remap[b] = (int32_t)b;
   for (int64_t k = gt; k < a.max_moves; k += gn) move_src[k] = move_dst[k] = -1;
-  cluster.sync();
+  cluster.sync();  // (every CTA has begun, too: see the stores to their shared memory below)
   bool wrong = false;
   for (int i = gt; i < n_free; i += gn) {
     const int32_t id = free_ids[i];
