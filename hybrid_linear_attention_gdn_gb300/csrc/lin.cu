@@ -192,18 +192,19 @@ __global__ void __launch_bounds__(256) lin_recurrent_kernel(const PrefillArgs a)
 #pragma unroll
   for (int e = 0; e < 8; ++e) st[e] = make_float2(0.f, 0.f);
   if (active) {
-    auto load = [&](const auto& from, float keep) {
+    auto load = [&](const auto& from, Decay keep) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float4 u = vec_at<const float4>(from, own + 4 * LPR * e);
-        st[2 * e] = fma2(make_float2(keep, keep), st[2 * e], lo2(u));
-        st[2 * e + 1] = fma2(make_float2(keep, keep), st[2 * e + 1], hi2(u));
+        st[2 * e] = add_decayed2(keep, st[2 * e], lo2(u));
+        st[2 * e + 1] = add_decayed2(keep, st[2 * e + 1], hi2(u));
       }
     };
+    const Decay none = {0.f, 0.f};
     if (s.seg == 0) {
       const bool kept = !STATE && s.n_seg > 1;
-      if (kept) load(segs + (s.seg0 + s.n_seg - 1) * slot_n, 0.f);
-      else load(pool + (int64_t)s.slot * slot_n, 0.f);
+      if (kept) load(segs + (s.seg0 + s.n_seg - 1) * slot_n, none);
+      else load(pool + (int64_t)s.slot * slot_n, none);
       if (STATE) {
         const auto keep = segs + (s.seg0 + s.n_seg - 1) * slot_n;
 #pragma unroll
@@ -212,8 +213,8 @@ __global__ void __launch_bounds__(256) lin_recurrent_kernel(const PrefillArgs a)
       }
     } else if (!STATE) {
       // the first segment's state holds the slot's already
-      const float keep = power(ld_h, (int64_t)s.chunks * kC);
-      for (int k = 0; k < s.seg; ++k) load(segs + (s.seg0 + k) * slot_n, k ? keep : 0.f);
+      const Decay keep = decay_of(ld_h, (int64_t)s.chunks * kC);
+      for (int k = 0; k < s.seg; ++k) load(segs + (s.seg0 + k) * slot_n, k ? keep : none);
     }
   }
   // the tokens until the next block boundary

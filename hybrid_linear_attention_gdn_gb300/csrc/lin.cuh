@@ -220,18 +220,18 @@ __device__ __forceinline__ bool find_item(const PrefillArgs& a, int64_t item, Se
   return true;
 }
 
-// lambda^n (n >= 0).  The rounding of the exponent (2^-24 of it) is the same
-// part of every power: what a state still remembers has exponents of a few
-// units in sum, however many powers were multiplied.  lambda^0 is 1 for every
-// decay, -inf too.
+// lambda^n (n >= 0) as one float, for a factor of a token's own terms: an
+// exponent that is rounded (2^-24 of it) hides in what remains of such a term.
+// lambda^0 is 1 for every decay, -inf too.
 __device__ __forceinline__ float power(float log_decay, int64_t n) {
   return n == 0 ? 1.f : expf(log_decay * (float)n);
 }
 
-// A decay as the sum of two floats.  A state that remembers 2,000 tokens has
-// been multiplied by lambda as often: its rounding to one float (2^-25) would
-// put it off by 6e-5.  As 1 + expm1(log_decay) the error is 2^-24 of the small
-// part; a decay that forgets within two tokens needs no second part.
+// A decay as the sum of two floats, for a state that is multiplied by it again
+// and again: a rounding to one float (2^-25) is the same every time and adds up,
+// over 2,000 remembered multiplications to 6e-5.  As 1 + expm1(log_decay) the
+// error is 2^-24 of the small part; a decay that forgets within two
+// multiplications needs no second part.
 struct Decay {
   float hi, lo;
 };
@@ -242,13 +242,19 @@ __device__ __forceinline__ Decay decay_of(float log_decay) {
   d.lo = slow ? expm1f(log_decay) : 0.f;
   return d;
 }
-// lambda s + v k
-__device__ __forceinline__ float step(Decay d, float s, float v, float k) {
-  return fmaf(d.hi, s, fmaf(d.lo, s, v * k));
+// lambda^n, n > 0: of a chunk (2^20 tokens of a memory as long are 16,384 of
+// them: with one float the state was 2.1e-4 off) or of a segment
+__device__ __forceinline__ Decay decay_of(float log_decay, int64_t n) { return decay_of(log_decay * (float)n); }
+// lambda s + x
+__device__ __forceinline__ float add_decayed(Decay d, float s, float x) { return fmaf(d.hi, s, fmaf(d.lo, s, x)); }
+__device__ __forceinline__ float2 add_decayed2(Decay d, float2 s, float2 x) {
+  return fma2(make_float2(d.hi, d.hi), s, fma2(make_float2(d.lo, d.lo), s, x));
 }
+// lambda s + v k
+__device__ __forceinline__ float step(Decay d, float s, float v, float k) { return add_decayed(d, s, v * k); }
 
 __device__ __forceinline__ float2 step2(Decay d, float2 s, float v, float2 k) {
-  return fma2(make_float2(d.hi, d.hi), s, fma2(make_float2(d.lo, d.lo), s, mul2(make_float2(v, v), k)));
+  return add_decayed2(d, s, mul2(make_float2(v, v), k));
 }
 
 // words of PrefillArgs::sync

@@ -90,7 +90,7 @@ struct __align__(1024) ChunkSmem {
   __align__(16) float w[2 * kC];  // lambda^(63 - j), zeros from 64 on
   float ps[kC];                 // scale lambda^n
   float pt[kC];                 // scale lambda^(n + 1)
-  float dec[kC + 1];            // lambda^n
+  Decay dec[kC + 1];            // lambda^n, n > 0
   Segment seg;
   int work, head;
   float log_decay;
@@ -290,7 +290,7 @@ __device__ __forceinline__ void init_factors(ChunkSmem& S, const float scale, co
   const int n = (int)threadIdx.x - 96;
   if (n >= 0 && n < 2 * kC) {
     const float x = n <= kC ? power(log_decay, n) : 0.f;
-    if (n <= kC) S.dec[n] = x;
+    if (n >= 1 && n <= kC) S.dec[n] = decay_of(log_decay, n);
     S.w[n < kC ? kC - 1 - n : n] = n < kC ? x : 0.f;
     if (n < kC) S.ps[n] = x * scale;
     if (n >= 1 && n <= kC) S.pt[n - 1] = x * scale;
@@ -684,17 +684,17 @@ __device__ __forceinline__ void run(const PrefillArgs& a, const CUtensorMap& xma
           for (int j = 0; j < 8; ++j) vec_at<float4>(keep, place(j)) = v[j];
         }
       } else if (!STATE) {
-        const float dec = power(S.log_decay, (int64_t)S.seg.chunks * kC);
+        const Decay dec = decay_of(S.log_decay, (int64_t)S.seg.chunks * kC);
         for (int k = 0; k < seg; ++k) {
-          const float d = k ? dec : 0.f;  // the first segment's state holds the slot's already
+          const Decay d = k ? dec : Decay{0.f, 0.f};  // the first segment's state holds the slot's already
           const auto from_seg = segs + (S.seg.seg0 + k) * slot_n;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float4 x = vec_at<const float4>(from_seg, place(j));
-            v[j].x = fmaf(d, v[j].x, x.x);
-            v[j].y = fmaf(d, v[j].y, x.y);
-            v[j].z = fmaf(d, v[j].z, x.z);
-            v[j].w = fmaf(d, v[j].w, x.w);
+            v[j].x = add_decayed(d, v[j].x, x.x);
+            v[j].y = add_decayed(d, v[j].y, x.y);
+            v[j].z = add_decayed(d, v[j].z, x.z);
+            v[j].w = add_decayed(d, v[j].w, x.w);
           }
         }
       }
@@ -783,7 +783,16 @@ __device__ __forceinline__ void run(const PrefillArgs& a, const CUtensorMap& xma
 #pragma unroll 1
     for (int i = 0; i < nit && ok; ++i) {
       const int L = count(i);
-      const float dec = S.dec[L];
+      const Decay dec = S.dec[L];
+      // the decay is applied under the wait for dS: 4 x 8192 tokens 224 us in a
+      // graph, with both of its factors behind the wait 227 (with one rounded factor 222)
+      if (dec.hi == 1.f) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) st[e] = fma2(make_float2(dec.lo, dec.lo), st[e], st[e]);
+      } else {  // (no second part)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) st[e] = mul2(make_float2(dec.hi, dec.hi), st[e]);
+      }
       if (!(ok = wait_all(&S.ds_full[buf(i)], use(i) & 1))) break;
       umma::fence_after();
 #pragma unroll
@@ -792,7 +801,7 @@ __device__ __forceinline__ void run(const PrefillArgs& a, const CUtensorMap& xma
         umma::tmem_ld16(ds_at(i) + ((uint32_t)(32 * quarter) << 16) + 32 * part + 16 * q, d);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          st[8 * q + e] = fma2(st[8 * q + e], make_float2(dec, dec), make_float2(d[2 * e], d[2 * e + 1]));
+          st[8 * q + e] = fma2(st[8 * q + e], make_float2(1.f, 1.f), make_float2(d[2 * e], d[2 * e + 1]));
       }
       umma::fence_before();
       __syncwarp();
