@@ -820,28 +820,30 @@ def _bad_view(fn: str, what: str, t, dtype, shape, why: str):
                                         f"device{why}, got {t.dtype} {tuple(t.shape)}, strides {t.stride()} on {t.device}")
 
 
+def _separate(sizes, strides) -> bool:
+    """Whether the elements of a tensor of these sizes and strides lie apart:
+    each dimension steps over all that the ones with smaller strides span."""
+    span = 1
+    for size, stride in sorted(((n, s) for n, s in zip(sizes, strides) if n > 1), key=lambda p: p[1]):
+        if stride < span:
+            return False
+        span += stride * (size - 1)
+    return True
+
+
 def _rows(fn: str, what: str, t, dtype, shape, device: int, out: bool = False) -> CRows:
     """t [rows][heads][width] as gdn_rows: any strides, a head's values
-    consecutive; an output's rows and heads one behind the other."""
+    consecutive; an output's elements apart, whether it is kept by rows or by heads."""
     if t is None:
         return _NO_ROWS
     if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
         _bad_view(fn, what, t, dtype, shape, "")
     row, head, one = t.stride()
     n, heads, width = shape
-    if (one != 1 and width > 1) or (out and ((head < width and heads > 1) or (row < (heads - 1) * head + width and n > 1))):
+    apart = not out or (head >= width > 0 and row >= head * heads) or _separate(shape, (row, head, one))
+    if (one != 1 and width > 1) or not apart:
         _bad_view(fn, what, t, dtype, shape, " with consecutive head values" + (" and separate rows" if out else ""))
     return CRows(t.data_ptr(), row, head)
-
-
-def _separate(sizes, strides) -> bool:
-    """Whether the elements of a tensor of these sizes and strides lie apart."""
-    need = 1
-    for size, stride in sorted(((n, s) for n, s in zip(sizes, strides) if n > 1), key=lambda p: p[1]):
-        if stride < need:
-            return False
-        need = stride * size
-    return True
 
 
 def _pages(fn: str, what: str, t, dtype, shape, device: int) -> CPages:
