@@ -388,7 +388,7 @@ extern "C" gdn_status gdn_qk_norm_rope(int32_t act_dtype, int32_t hq, int32_t hk
     return GDN_ERR_UNSUPPORTED;
   if (n_rows == 0) return GDN_OK;
   if (n_rows > 2147483647LL) return GDN_ERR_UNSUPPORTED;
-  if (!positions || (rot > 0 && !cos_sin) || !aligned(cos_sin, 4)) return GDN_ERR_INVALID_ARG;
+  if (!positions || (rot > 0 && max_pos > 0 && !cos_sin) || !aligned(cos_sin, 4)) return GDN_ERR_INVALID_ARG;
   if (hq > 0 && (bad_rows(q, esz) || bad_rows(q_out, esz))) return GDN_ERR_INVALID_ARG;
   if (hk > 0 && bad_rows(k, esz)) return GDN_ERR_INVALID_ARG;
   if (hk > 0 && !cache && bad_rows(k_out, esz)) return GDN_ERR_INVALID_ARG;

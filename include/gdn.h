@@ -617,6 +617,7 @@ gdn_status gdn_lin_prefill(const gdn_dims* dims, gdn_pool pool, gdn_pool ckpt, c
  *   q_out, k_out as q, k: each may be its input (same strides); any other
  *   overlap is undefined
  *   positions [n_rows] int64; cos_sin [max_pos][rot] float, its cosines first
+ *   (max_pos = 0: every position is outside; cos_sin may be NULL)
  *   slot_map [n_rows] int64 (see gdn_batch_maps) or NULL: row r's k and v also
  *   go to row slot % block of page slot / block of k_cache and v_cache
  *   [num_pages][block][...]; slot -1: they do not.  With a slot_map k_out may
