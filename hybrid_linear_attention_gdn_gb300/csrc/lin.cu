@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(256) lin_recurrent_kernel(const PrefillArgs a)
   }
   // the tokens until the next block boundary
   const int64_t blk = a.ckpt_block;
-  int64_t bound = ((s.p0 + s.m0) / blk + 1) * blk - s.p0;  // tokens of the sequence up to it
+  int64_t bound = s.m0 + blk - (s.p0 + s.m0) % blk;  // tokens of the sequence up to it
   auto window = [&](int64_t m, int64_t bnd) { return (int)max((int64_t)0, min((int64_t)kWin, min(s.m1, bnd) - m)); };
   // A window's inputs as they are (a conversion beside its load would wait for
   // it, one load after another): of q and k this thread's column of every

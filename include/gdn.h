@@ -575,7 +575,8 @@ gdn_status gdn_lin_decode_step(const gdn_dims* dims, gdn_pool pool, const float*
  * start position, block-aligned checkpoints of the state, final state into the
  * working slot, rows outside the sequences not written) with every token the
  * step above.  A checkpoint id outside the pool is skipped and sets
- * GDN_DEV_ERR_SLOT_OOB.  Above 16384 sequences, 2^31 - 1 tokens or 65535
+ * GDN_DEV_ERR_SLOT_OOB; a sequence that ends beyond position 2^63 - 65 counts as
+ * inconsistent (GDN_DEV_ERR_SEQLENS).  Above 16384 sequences, 2^31 - 1 tokens or 65535
  * segments: GDN_ERR_UNSUPPORTED.  dk = dv = 128 with bf16 activations and qkv
  * and out 16-byte aligned: 64-token blocks on the tensor cores, some 1.75 us a
  * block and head; everything else one token after another, some 0.25 us each.
