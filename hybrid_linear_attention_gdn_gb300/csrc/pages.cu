@@ -8,7 +8,7 @@
 // Whole numbers but for the page copies, which are HBM streams.  Every result
 // is the same whatever the order in which the threads run: new blocks go out
 // in the requests' order, given-up ones go back by id.
-#include "ssm.cuh"  // allow_smem
+#include "gdn_common.cuh"
 #include "decode_tma.cuh"  // sm_count
 
 #include <cooperative_groups.h>

@@ -15,7 +15,7 @@
 // groups of small heads') loads in flight.  A lane has 8 values of a head, in two runs of
 // 4 that are each other's partners, so that nothing but the sum of squares goes
 // between lanes.  qk_rope_any_kernel: every other shape, a warp per head.
-#include "ssm.cuh"  // allow_smem
+#include "gdn_common.cuh"
 #include "decode_tma.cuh"  // sm_count
 
 namespace gdn {
