@@ -355,7 +355,7 @@ cudaError_t recurrent_dispatch(const PrefillArgs& a, cudaStream_t s) {
 // worth it if the longest sequence takes longer whole,
 //   1.75 longest > (1.75 + 0.72) segment + 6,
 // which the device decides where it is not known here.  Measured with 32 heads, cut
-// and whole: 8192 tokens 91 and 217 us, 5000 + 1000 + 1000 87 and 136, 2 x 2048 50
+// and whole: 8192 tokens 92 and 217 us, 5000 + 1000 + 1000 87 and 136, 2 x 2048 51
 // and 60; 3 x 2700 90 and 78 (two waves), 2 x 1024 36 and 34.
 constexpr int64_t kMinSeg = 8, kMaxSegs = 16;
 int64_t cut_from(int64_t seg) { return (10 * seg + 24) / 7 + 1; }
@@ -363,8 +363,11 @@ int64_t chunk_seg(const gdn_dims& d, int32_t n_seq, int64_t total) {
   const int64_t chunks = (total + kC - 1) / kC, mean = (chunks + n_seq - 1) / n_seq, wave = sm_count() / d.hv;
   if (wave < 2 || n_seq > kMaxCut) return kWhole;
   // (a sequence's blocks may be one more than its length says.)  First segments run
-  // beside the state pass on the SMs that it leaves free; where those are half
-  // a wave of heads or more, a shorter one per sequence is for nothing.
+  // beside the state pass on the SMs that it leaves free.  Where those are half
+  // of the heads or more, the blocks are divided by 0.45 of a wave more: with 0, 0.25
+  // and 0.45 of one, 32 heads, 8192 tokens 98, 96 and 92 us, 6000 + 2000 95, 93 and 90,
+  // 5000 + 1000 + 1000 90, 88 and 87; 20 heads, 8192 tokens 70, 68 and 68; 16 heads 60,
+  // 59 and 59.  (48 and 64 heads leave too few; one 0.45 for all numbers of heads.)
   const int64_t spare = 2 * (sm_count() - wave * d.hv) >= d.hv ? 45 : 0, all = 100 * (chunks + n_seq - 1);
   const int64_t seg = std::max(std::max((all + 100 * wave + spare - 1) / (100 * wave + spare) + 1, kMinSeg),
                                (mean + kMaxSegs - 1) / kMaxSegs);

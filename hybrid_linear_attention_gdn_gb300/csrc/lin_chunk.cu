@@ -14,7 +14,8 @@
 //   O1^T = S^T Q^T                  A = S^T in TMEM, in parts
 //   O2^T = V^T P^T                  A = V; P = G with its decays, in parts
 // dS does not need S, so only an elementwise update per chunk is left of the
-// recurrence, and the tensor core always has another chunk's work.
+// recurrence, and the tensor core always has another chunk's work.  lambda^L of
+// S's update is two floats (see Decay).
 //
 // Roundings.  q, k and v are bf16 already and enter G, dS and O2 exactly.  V w
 // is split into three bf16 parts (24 bits: the fp32 product itself), so that
@@ -34,9 +35,10 @@
 // The tensor core takes a product about when the one before it is done, so that one
 // issuer's waits for the other warps left it idle a third of the time.
 //
-// Bound by the products: 2,630 of some 3,100 cycles a chunk.  4 x 8192 tokens of 32
-// heads 223 us (128 CTAs; 0.76 of a copy's rate), 1 x 8192 91 us (five segments), 37
-// tokens 8.3 us.  The roles' loops share the instruction caches: rolled, and with
+// Bound by the products: 2,630 of some 3,100 cycles a chunk, by the products'
+// times measured one by one.  In a graph of calls 4 x 8192 tokens of 32 heads 224 us
+// (128 CTAs; 0.76 of a copy's rate), 1 x 8192 92 us (five segments), 37 tokens 8.6 us;
+// called one by one some 230, 93 and 13.  The roles' loops share the instruction caches: rolled, and with
 // short waits, their hit rate went from 73 to 94 % and 4 x 8192 tokens from 260 to
 // 241 us.
 //
@@ -44,8 +46,9 @@
 // clears the flags: state passes and segments are pieces of work that CTAs take
 // in an order in which whatever a piece waits for was taken before it, so that first
 // segments and whole sequences run beside the state pass (as two launches: seven
-// ragged prompts of 3,968 tokens 71 us, now 63; 2 x 2048 54 and 50; 1 x 8192 93 and 91;
-// 2048 alone 36 and 38, the price of the order).
+// ragged prompts of 3,968 tokens 71 us, so 63; 2 x 2048 54 and 50; 1 x 8192 93 and 91;
+// 2048 alone 36 and 38, the price of the order; all with the decays in one float,
+// 1 us less).
 #include "lin.cuh"
 
 #include "decode_tma.cuh"  // sm_count

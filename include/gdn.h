@@ -580,9 +580,11 @@ gdn_status gdn_lin_decode_step(const gdn_dims* dims, gdn_pool pool, const float*
  * segments: GDN_ERR_UNSUPPORTED.  dk = dv = 128 with bf16 activations and qkv
  * and out 16-byte aligned: 64-token blocks on the tensor cores, some 1.75 us a
  * block and head; everything else one token after another, some 0.25 us each.
- * States and checkpoints have fp32's accuracy in both forms; outputs of the
- * first one are off by at most some 2^-16 of the sum of their terms' magnitudes
- * before they are rounded to bf16.  A NaN or an infinity among a sequence's
+ * States and checkpoints have fp32's accuracy in both forms: the roundings of
+ * blocks or tokens are independent, and no decay's own error adds up (within 2e-5 of
+ * a head's state after 2^20 remembered tokens in the first form, 2^17 in the
+ * other).  Outputs of the first one are off by at most some 2^-16 of the sum of
+ * their terms' magnitudes before they are rounded to bf16.  A NaN or an infinity among a sequence's
  * inputs reaches that sequence's outputs and states from its 64-token block of
  * positions on, nothing before it and no other sequence.
  *   workspace: >= gdn_lin_prefill_workspace_size(...) bytes, 256-aligned (may

@@ -5,8 +5,12 @@ matrix).  A token multiplies what is kept by lambda (its own error at most
 2^-23, the product's 2^-24) and adds v k^T (2^-24): at most 2^-22 of what a
 state remembers, and a state remembers at most some 80 tokens' worth here
 (rates from 1/8 to 1/80 a token, or at most 60 tokens without decay), in the
-worst case 80 * 2^-22 = 1.9e-5 <= 2e-5.  The chunk form rounds k lambda^n to 16
-bits (2^-17 of each term) beside chunk sums in fp32: below the same bound.
+worst case 80 * 2^-22 = 1.9e-5 <= 2e-5.  The chunk form takes the products of v
+and lambda^n exactly as their fp32 value (24 bits in three parts) and adds a
+chunk's terms in twelve products, each off by at most 2^-23 of the terms'
+magnitudes in sum, which for 64 independent terms are up to 8 times their sum:
+12 * 8 * 2^-23 = 1.1e-5; a state takes two roundings per chunk, with a decay of two
+floats, fewer than the recurrence's.  Together below the same bound.
 Outputs: 2e-3 (bf16) and 1e-4 (fp32), the bounds of the other steps, beyond the
 error of the exact values' own rounding: where a strong decay leaves
 o = (q.k) v, one factor times bf16 values, a row's rounding errors are not

@@ -1,5 +1,6 @@
 """Releases of more entries than one cluster walks (two launches): many calls
-behind one another, on several streams at once, captured and replayed."""
+behind one another, on several streams at once, captured and replayed.  Copies
+of pages that lie beyond 2^32 bytes."""
 import pytest
 import torch
 
@@ -64,3 +65,18 @@ def test_on_several_streams_and_replayed(cuda):
     torch.cuda.synchronize()
     for h in held:
         h.check()
+
+
+def test_pages_beyond_32_bits(cuda):
+    """Three pages of 6000 bytes and more, 2^31 bytes apart, in two planes."""
+    far, page = 2 ** 31 + 4096, 6016
+    buf = torch.zeros(2 * far + 2 * page + 64, dtype=torch.uint8, device="cuda")
+    planes = [buf[i * page:].as_strided((3, page), (far, 1)) for i in range(2)]
+    for i, p in enumerate(planes):
+        for j in range(3):
+            p[j] = 1 + 3 * i + j
+    err = _word()
+    gdn.page_copy(gdn.PagePlanes(planes), _i32([2, -1]), _i32([0, 1]), dev_err=err)
+    assert int(err) == 0
+    for i, p in enumerate(planes):
+        assert [sorted(set(p[j].tolist())) for j in range(3)] == [[3 + 3 * i], [2 + 3 * i], [3 + 3 * i]]
