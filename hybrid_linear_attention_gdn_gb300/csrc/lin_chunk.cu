@@ -20,9 +20,11 @@
 // Roundings.  q, k and v are bf16 already and enter G, dS and O2 exactly.  V w
 // is split into three bf16 parts (24 bits: the fp32 product itself), so that
 // states and checkpoints keep fp32's accuracy; P and S^T, which only outputs
-// see, into two (16 bits, off by at most 2^-16 of a term, against the output's
-// own 2^-8; with one part each the outputs were 2.4e-3 off instead of 1.7e-3).
-// bf16 parts keep fp32's range, so no scaling is needed.
+// see, into two (off by at most 2^-17 of a term, against the output's own 2^-8;
+// with one part each the outputs were 2.4e-3 off instead of 1.7e-3; a third one,
+// for which neither TMEM nor shared memory has room, would be 12 products more a
+// chunk).  bf16 parts keep fp32's range (a P or S beyond 3.39e38 is infinite), so
+// no scaling is needed.
 //
 // A product of K = 16 takes some 59 cycles with N = 64 and 67 to 73 with N = 128
 // (measured; M = 64 no less than M = 128), 2,630 a chunk, and both operands from
@@ -124,6 +126,14 @@ __device__ __forceinline__ uint32_t take_bf16(float2& x) {
 __device__ __forceinline__ uint32_t bf16_pair(float2 x) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Both values to the nearest bf16, packed in pairs; x: what is left, exactly.
+// Two parts (the second one by bf16_pair) are off by at most 2^-17 of the value;
+// with a first part by truncation 2^-16, at no less time.
+__device__ __forceinline__ uint32_t take_near(float2& x) {
+  const uint32_t p = bf16_pair(x);
+  x = fma2(make_float2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u)), make_float2(-1.f, -1.f), x);
+  return p;
 }
 
 // Four 8 x 8 matrices of 16-bit values, transposed: lane 8 i + r names row r of
@@ -727,7 +737,7 @@ __device__ __forceinline__ void run(const PrefillArgs& a, const CUtensorMap& xma
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         float2 x = st[e];
-        r[e] = take_bf16(x);
+        r[e] = take_near(x);
         lo[e] = bf16_pair(x);
       }
       tmem_put16(tlane + TM_S + 16 * part, r);
@@ -751,7 +761,7 @@ __device__ __forceinline__ void run(const PrefillArgs& a, const CUtensorMap& xma
         for (int k = 0; k < 4; ++k) {  // column group k / 2, row group k % 2
           const int d = d0 + 8 * (k & 1) - 8 * (k >> 1), e = 4 * (k >> 1) + 2 * (k & 1);
           float2 x = make_float2(d >= 0 ? g[e] * S.ps[max(d, 0)] : 0.f, d >= 1 ? g[e + 1] * S.ps[max(d - 1, 0)] : 0.f);
-          hi[k] = take_bf16(x);
+          hi[k] = take_near(x);
           lo[k] = bf16_pair(x);
         }
         // matrices of 8 rows x 8 columns: lane / 8 = 2 (column group) + row group.

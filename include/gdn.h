@@ -583,7 +583,7 @@ gdn_status gdn_lin_decode_step(const gdn_dims* dims, gdn_pool pool, const float*
  * States and checkpoints have fp32's accuracy in both forms: the roundings of
  * blocks or tokens are independent, and no decay's own error adds up (within 2e-5 of
  * a head's state after 2^20 remembered tokens in the first form, 2^17 in the
- * other).  Outputs of the first one are off by at most some 2^-16 of the sum of
+ * other).  Outputs of the first one are off by at most some 2^-17 of the sum of
  * their terms' magnitudes before they are rounded to bf16.  A NaN or an infinity among a sequence's
  * inputs reaches that sequence's outputs and states from its 64-token block of
  * positions on, nothing before it and no other sequence.
