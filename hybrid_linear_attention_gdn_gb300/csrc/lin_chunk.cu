@@ -38,9 +38,9 @@
 // issuer's waits for the other warps left it idle a third of the time.
 //
 // Bound by the products: 2,630 of some 3,100 cycles a chunk, by the products'
-// times measured one by one.  In a graph of calls 4 x 8192 tokens of 32 heads 224 us
-// (128 CTAs; 0.76 of a copy's rate), 1 x 8192 92 us (five segments), 37 tokens 8.6 us;
-// called one by one some 230, 93 and 13.  The roles' loops share the instruction caches: rolled, and with
+// times measured one by one.  In a graph of calls 4 x 8192 tokens of 32 heads 221 us
+// (128 CTAs; 0.77 of a copy's rate), 1 x 8192 91 us (five segments), 37 tokens 8.5 us;
+// called one by one 235, 91 and 13.  The roles' loops share the instruction caches: rolled, and with
 // short waits, their hit rate went from 73 to 94 % and 4 x 8192 tokens from 260 to
 // 241 us.
 //
