@@ -40,9 +40,9 @@
 // Bound by the products: 2,630 of some 3,100 cycles a chunk, by the products'
 // times measured one by one.  In a graph of calls 4 x 8192 tokens of 32 heads 221 us
 // (128 CTAs; 0.77 of a copy's rate), 1 x 8192 91 us (five segments), 37 tokens 8.5 us;
-// called one by one 235, 91 and 13.  The roles' loops share the instruction caches: rolled, and with
-// short waits, their hit rate went from 73 to 94 % and 4 x 8192 tokens from 260 to
-// 241 us.
+// called one by one 235, 91 and 13.  The roles' loops share the instruction
+// caches: rolled, and with short waits, their hit rate went from 73 to 94 % and 4 x
+// 8192 tokens from 260 to 241 us.
 //
 // Sequences that may be cut into segments are one launch behind a small one that
 // clears the flags: state passes and segments are pieces of work that CTAs take

@@ -584,9 +584,9 @@ gdn_status gdn_lin_decode_step(const gdn_dims* dims, gdn_pool pool, const float*
  * blocks or tokens are independent, and no decay's own error adds up (within 2e-5 of
  * a head's state after 2^20 remembered tokens in the first form, 2^17 in the
  * other).  Outputs of the first one are off by at most some 2^-17 of the sum of
- * their terms' magnitudes before they are rounded to bf16.  A NaN or an infinity among a sequence's
- * inputs reaches that sequence's outputs and states from its 64-token block of
- * positions on, nothing before it and no other sequence.
+ * their terms' magnitudes before they are rounded to bf16.  A NaN or an infinity
+ * among a sequence's inputs reaches that sequence's outputs and states from its
+ * 64-token block of positions on, nothing before it and no other sequence.
  *   workspace: >= gdn_lin_prefill_workspace_size(...) bytes, 256-aligned (may
  *   be NULL where that is 0); nothing in it needs to be zero, and nothing is
  *   kept in it between calls, but calls that run at once (on two streams, or
